@@ -80,6 +80,7 @@ typedef enum {
 #define MOE_DEV_NONFINITE 0x1u  /* a token's logits held NaN/inf (A2)       */
 #define MOE_DEV_BAD_EXPERT 0x2u /* an expert id >= num_experts was given    */
 #define MOE_DEV_TIMEOUT 0x4u    /* a bounded device-side wait gave up       */
+#define MOE_DEV_BAD_INDEX 0x8u  /* a sequence bound or state slot out of range */
 
 typedef struct {
   int32_t hidden;       /* H                                              */
@@ -278,6 +279,106 @@ moe_status moe_topk_candidates(const float *logits, int T, int ld, int N, int k,
 moe_status moe_topk_merge(const int32_t *ids, const float *values, int T, int n_lists,
                           int k, int32_t *ids_out, float *values_out,
                           void *workspace, size_t ws_bytes, void *stream);
+
+/* ---- The other half of a hybrid decoder layer: the gated delta rule (the
+ * token mixer in front of the block) and the norms around a block.
+ *
+ * Gated delta rule.  Per value head h (which reads query/key head
+ * h / (v_heads / qk_heads)) a state S [v_dim][qk_dim] in fp32 goes through
+ * the tokens of a sequence:
+ *   S <- exp(g_t) S;   u = beta_t (v_t - S k_t);   S <- S + u k_t^T;
+ *   o_t = S q_t * scale.
+ * With qk_norm != 0, q and k are first divided by sqrt(sum x^2 + qk_eps).
+ * g is the natural logarithm of the decay (g <= 0 in use; below -128, -inf
+ * included, it counts as -128: the state is forgotten).  Sums, states and
+ * gates are fp32 (or better); out is rounded to bf16 once. */
+typedef struct {
+  int32_t qk_heads; /* Hk                                                 */
+  int32_t v_heads;  /* Hv: a multiple of Hk, <= 256                       */
+  int32_t qk_dim;   /* 64 or 128                                          */
+  int32_t v_dim;    /* 64 or 128                                          */
+  int32_t qk_norm;  /* 0: q and k as they are, 1: divided by their 2-norm */
+  float qk_eps;     /* >= 0, finite; used when qk_norm != 0               */
+  float scale;      /* finite                                             */
+} moe_delta_dims;
+
+/* Rows of the tokens, device pointers.  Token t's q lies at q + t * q_ld as
+ * [Hk][qk_dim], k alike, v as [Hv][v_dim] (slices of one projected row are
+ * fine); g and beta at g + t * g_ld as [Hv].  q, k, v 16-byte aligned with
+ * strides that are multiples of 8; g and beta 4-byte aligned. */
+typedef struct {
+  const moe_bf16 *q, *k, *v;
+  const float *g, *beta;
+  int64_t q_ld, k_ld, v_ld, g_ld, beta_ld;
+} moe_delta_inputs;
+
+/* Bytes of workspace moe_delta_chunk needs for up to N tokens in up to B
+ * sequences (0 on bad dims or sizes).  moe_delta_step needs 256. */
+size_t moe_delta_workspace_bytes(const moe_delta_dims *dims, int N, int B);
+
+/* The rule over whole prompts: N token rows hold B sequences one after
+ * another, sequence b rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (device,
+ * int32 [B + 1]; NULL when B == 1: all N rows).  Sequences may be empty.
+ * State of sequence b: slot slots[b] of state_in / state_out (device, int32;
+ * NULL: slot b), each [n_slots][Hv][v_dim][qk_dim] fp32, 16-byte aligned.
+ * state_in NULL: all start from zero.  state_out NULL: not kept.  state_out
+ * may be state_in (updated in place) or disjoint from it.  Two sequences
+ * must not share a slot.  A sequence whose slot is negative is skipped, its
+ * out rows and state left as they were; so is one whose slot is >= n_slots
+ * or whose bounds are not 0 <= start <= end <= N, and that sets
+ * MOE_DEV_BAD_INDEX.  out row t lies at out + t * out_ld as [Hv][v_dim] bf16
+ * (16-byte aligned, out_ld a multiple of 8) and must not overlap the inputs.
+ * N <= 2^20, B <= 65536.  A value that is not finite makes its head's state,
+ * and that head's outputs within the same run of 64 tokens and after it,
+ * not finite; other heads and sequences do not see it. */
+moe_status moe_delta_chunk(const moe_delta_dims *dims, const moe_delta_inputs *in, int N,
+                           const int32_t *cu_seqlens, int B, const int32_t *slots, int n_slots,
+                           const float *state_in, float *state_out, moe_bf16 *out,
+                           int64_t out_ld, void *workspace, size_t ws_bytes, void *stream);
+
+/* The rule for decode and draft verification: B sequences of exactly T
+ * tokens (row b * T + i), one pass over each state.  Otherwise as
+ * moe_delta_chunk; the workspace holds only the status word. */
+moe_status moe_delta_step(const moe_delta_dims *dims, const moe_delta_inputs *in, int B, int T,
+                          const int32_t *slots, int n_slots, const float *state_in,
+                          float *state_out, moe_bf16 *out, int64_t out_ld, void *workspace,
+                          size_t ws_bytes, void *stream);
+
+/* The norm after a block, its gate, the scaled residual add and the norm
+ * before the next block, in one pass over each row:
+ *   y        = res_scale * act(gate) * post(x) + resid_in,
+ *   resid_out = bf16(y),   x_next = bf16(rms(resid_out) * gamma_pre)
+ * with post(x) = rms(x) * gamma_post (x itself when gamma_post is NULL),
+ * rms(r) = r / sqrt(mean(r^2) + eps), no gate factor when gate_kind is
+ * MOE_GATE_NONE and no residual when resid_in is NULL.  One of resid_out and
+ * x_next may be NULL; gamma_pre is NULL exactly when x_next is. */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1 /* gate [width], one factor per channel           */
+#define MOE_GATE_ELEMENT 2 /* gate laid out like the rows                     */
+#define MOE_GATE_ROW 3     /* one factor per row                              */
+#define MOE_ACT_IDENTITY 0
+#define MOE_ACT_SIGMOID 1
+#define MOE_ACT_SILU 2
+
+/* `rows` rows of `width` values; row r of a tensor with stride ld starts at
+ * (r / inner) * ld + (r % inner) * width (inner = 1: plain rows; inner =
+ * heads: one row per head of a token).  All bf16, 16-byte aligned.  Any
+ * width from 1 to 16384 and any ld >= inner * width is served (multiples of
+ * 8 by 16-byte accesses).  gate_ld: the row stride of an element gate; of a
+ * row gate the stride between groups of `inner` factors.  Outputs may be x
+ * or resid_in themselves (the same pointer and stride); any other overlap
+ * of an output is MOE_ERR_INVALID_ARG. */
+typedef struct {
+  int64_t rows;
+  int32_t width, inner;
+  const moe_bf16 *x, *gamma_post, *gate, *resid_in, *gamma_pre;
+  moe_bf16 *resid_out, *x_next;
+  int64_t x_ld, gate_ld, resid_in_ld, resid_out_ld, x_next_ld;
+  int32_t gate_kind, gate_act;
+  float res_scale, eps;
+} moe_norm_args;
+
+moe_status moe_norm_gate_residual(const moe_norm_args *args, void *stream);
 
 /* Copy the device status word to *bits (synchronises the stream). */
 moe_status moe_read_status(const void *workspace, void *stream, uint32_t *bits);

@@ -8,7 +8,10 @@ exception.  PyTorch is used for device memory and streams only.
 The entry points keep the C names: ``moe_router_logits``,
 ``moe_select_top8``, ``moe_build_expert_lists``, ``moe_expert_swiglu_w8``,
 ``moe_combine``, ``moe_block_forward``, ``moe_block_forward_host``,
-``moe_workspace_bytes``, ``moe_read_status``, ``moe_clear_status``.  Array
+``moe_workspace_bytes``, ``moe_read_status``, ``moe_clear_status``; the other
+half of a hybrid decoder layer in ``moe_delta_chunk``, ``moe_delta_step``
+(the gated delta rule; ``GatedDelta`` holds its workspace) and
+``moe_norm_gate_residual`` (``norm_gate_residual`` takes tensors).  Array
 arguments may be torch tensors (their ``data_ptr()`` is passed), raw integer
 addresses, or None where the C argument is nullable.
 
@@ -29,13 +32,17 @@ __all__ = [
     "moe_block_forward_profiled", "moe_block_kernel_count", "moe_block_kernel_name",
     "moe_block_forward_noalloc", "moe_topk_workspace_bytes", "moe_topk_candidates",
     "moe_topk_merge", "moe_block_forward_residual",
+    "DeltaDims", "moe_delta_workspace_bytes", "moe_delta_chunk", "moe_delta_step",
+    "moe_norm_gate_residual", "GatedDelta", "norm_gate_residual", "DEV_BAD_INDEX",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_gb300.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA = range(5)
-DEV_NONFINITE, DEV_BAD_EXPERT, DEV_TIMEOUT = 0x1, 0x2, 0x4
+DEV_NONFINITE, DEV_BAD_EXPERT, DEV_TIMEOUT, DEV_BAD_INDEX = 0x1, 0x2, 0x4, 0x8
+GATE_NONE, GATE_CHANNEL, GATE_ELEMENT, GATE_ROW = range(4)
+GATE_ACTS = {"identity": 0, "sigmoid": 1, "silu": 2}
 
 # every symbol include/moe_gb300.h declares
 EXPORTS = (
@@ -46,6 +53,7 @@ EXPORTS = (
     "moe_block_forward_profiled", "moe_block_kernel_count", "moe_block_kernel_name",
     "moe_block_forward_noalloc", "moe_topk_workspace_bytes", "moe_topk_candidates",
     "moe_topk_merge", "moe_block_forward_residual",
+    "moe_delta_workspace_bytes", "moe_delta_chunk", "moe_delta_step", "moe_norm_gate_residual",
 )
 
 
@@ -72,6 +80,28 @@ class Weights(ctypes.Structure):
         "ws13_q", "ws13_s", "ws2_q", "ws2_s")]
 
 
+class DeltaDims(ctypes.Structure):
+    _fields_ = [("qk_heads", ctypes.c_int32), ("v_heads", ctypes.c_int32),
+                ("qk_dim", ctypes.c_int32), ("v_dim", ctypes.c_int32),
+                ("qk_norm", ctypes.c_int32), ("qk_eps", ctypes.c_float),
+                ("scale", ctypes.c_float)]
+
+
+class DeltaInputs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "g", "beta")] +
+                [(n, ctypes.c_int64) for n in ("q_ld", "k_ld", "v_ld", "g_ld", "beta_ld")])
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = ([("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("inner", ctypes.c_int32)] +
+                [(n, ctypes.c_void_p) for n in ("x", "gamma_post", "gate", "resid_in",
+                                                "gamma_pre", "resid_out", "x_next")] +
+                [(n, ctypes.c_int64) for n in ("x_ld", "gate_ld", "resid_in_ld", "resid_out_ld",
+                                               "x_next_ld")] +
+                [("gate_kind", ctypes.c_int32), ("gate_act", ctypes.c_int32),
+                 ("res_scale", ctypes.c_float), ("eps", ctypes.c_float)])
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -89,6 +119,8 @@ def lib() -> ctypes.CDLL:
             P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
             DP = ctypes.POINTER(Dims)
             WP = ctypes.POINTER(Weights)
+            DDP, DIP = ctypes.POINTER(DeltaDims), ctypes.POINTER(DeltaInputs)
+            L64 = ctypes.c_int64
             sig = {
                 "moe_workspace_bytes": (Z, [DP, I]),
                 "moe_router_logits": (I, [DP, WP, P, I, P, P, P]),
@@ -112,6 +144,10 @@ def lib() -> ctypes.CDLL:
                 "moe_topk_merge": (I, [P, P, I, I, I, P, P, P, Z, P]),
                 "moe_block_forward_residual": (I, [DP, WP, P, I, P, P, ctypes.c_float, P, P,
                                                    P, Z, P]),
+                "moe_delta_workspace_bytes": (Z, [DDP, I, I]),
+                "moe_delta_chunk": (I, [DDP, DIP, I, P, I, P, I, P, P, P, L64, P, Z, P]),
+                "moe_delta_step": (I, [DDP, DIP, I, I, P, I, P, P, P, L64, P, Z, P]),
+                "moe_norm_gate_residual": (I, [ctypes.POINTER(NormArgs), P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -261,6 +297,31 @@ def moe_topk_merge(ids, values, T, n_lists, k, ids_out, values_out, workspace, w
            "moe_topk_merge")
 
 
+def moe_delta_workspace_bytes(dims: DeltaDims, N, B) -> int:
+    return int(lib().moe_delta_workspace_bytes(ctypes.byref(dims), int(N), int(B)))
+
+
+def moe_delta_chunk(dims: DeltaDims, inputs: DeltaInputs, N, cu_seqlens, B, slots, n_slots,
+                    state_in, state_out, out, out_ld, workspace, ws_bytes, stream=None):
+    _check(lib().moe_delta_chunk(ctypes.byref(dims), ctypes.byref(inputs), int(N),
+                                 _a(cu_seqlens), int(B), _a(slots), int(n_slots), _a(state_in),
+                                 _a(state_out), _a(out), int(out_ld), _a(workspace),
+                                 int(ws_bytes), _s(stream)), "moe_delta_chunk")
+
+
+def moe_delta_step(dims: DeltaDims, inputs: DeltaInputs, B, T, slots, n_slots, state_in,
+                   state_out, out, out_ld, workspace, ws_bytes, stream=None):
+    _check(lib().moe_delta_step(ctypes.byref(dims), ctypes.byref(inputs), int(B), int(T),
+                                _a(slots), int(n_slots), _a(state_in), _a(state_out), _a(out),
+                                int(out_ld), _a(workspace), int(ws_bytes), _s(stream)),
+           "moe_delta_step")
+
+
+def moe_norm_gate_residual(args: NormArgs, stream=None):
+    _check(lib().moe_norm_gate_residual(ctypes.byref(args), _s(stream)),
+           "moe_norm_gate_residual")
+
+
 def moe_read_status(workspace, stream=None) -> int:
     bits = ctypes.c_uint32(0)
     _check(lib().moe_read_status(_a(workspace), _s(stream), ctypes.byref(bits)), "moe_read_status")
@@ -308,3 +369,176 @@ class MoEBlock:
 
     def clear_status(self, stream=None):
         moe_clear_status(self.workspace, stream)
+
+
+def _require(ok, where):
+    if not ok:
+        raise MoEError(MOE_ERR_INVALID_ARG, where)
+
+
+class GatedDelta:
+    """The gated delta rule with its workspace, for up to ``max_tokens`` token
+    rows in up to ``max_seqs`` sequences per ``chunk`` call.
+
+    ``q``, ``k`` [N][qk_heads][qk_dim] and ``v`` [N][v_heads][v_dim] are bf16,
+    ``g`` (the decay's logarithm) and ``beta`` [N][v_heads] fp32; only their
+    first stride is free (slices of one projected row are fine).  States are
+    fp32 [n_slots][v_heads][v_dim][qk_dim].  ``state_out`` may be
+    ``state_in``.  The workspace belongs to one stream at a time.
+    """
+
+    def __init__(self, qk_heads, v_heads, qk_dim, v_dim, max_tokens, max_seqs=1, qk_norm=True,
+                 qk_eps=1e-6, scale=None, device="cuda"):
+        import torch
+        self.dims = DeltaDims(qk_heads, v_heads, qk_dim, v_dim, int(qk_norm), qk_eps,
+                              qk_dim ** -0.5 if scale is None else scale)
+        self.ws_bytes = moe_delta_workspace_bytes(self.dims, max_tokens, max_seqs)
+        if self.ws_bytes == 0:
+            raise MoEError(MOE_ERR_UNSUPPORTED, "moe_delta_workspace_bytes")
+        # only the status word must start at zero
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.workspace[:256].zero_()
+
+    def _inputs(self, q, k, v, g, beta, where):
+        import torch
+        d, n = self.dims, q.shape[0]
+        for x, dtype, shape in ((q, torch.bfloat16, (n, d.qk_heads, d.qk_dim)),
+                                (k, torch.bfloat16, (n, d.qk_heads, d.qk_dim)),
+                                (v, torch.bfloat16, (n, d.v_heads, d.v_dim)),
+                                (g, torch.float32, (n, d.v_heads)),
+                                (beta, torch.float32, (n, d.v_heads))):
+            _require(x.dtype == dtype and tuple(x.shape) == shape and x.is_cuda and
+                     (n == 0 or x[0].is_contiguous()), where)
+        # a single row has no stride of its own
+        ld = [x.stride(0) if n > 1 else x[:1].numel() for x in (q, k, v, g, beta)]
+        return n, DeltaInputs(_a(q), _a(k), _a(v), _a(g), _a(beta), *ld)
+
+    def _states(self, state_in, state_out, slots, B, where):
+        import torch
+        d, n_slots = self.dims, B
+        for x in (state_in, state_out):
+            if x is not None:
+                n_slots = x.shape[0]
+                _require(x.dtype == torch.float32 and x.is_cuda and x.is_contiguous() and
+                         tuple(x.shape[1:]) == (d.v_heads, d.v_dim, d.qk_dim), where)
+        _require(state_in is None or state_out is None or
+                 state_in.shape[0] == state_out.shape[0], where)
+        _require(slots is None or (slots.dtype == torch.int32 and slots.is_cuda and
+                                   slots.is_contiguous() and tuple(slots.shape) == (B,)), where)
+        if slots is not None and state_in is None and state_out is None:
+            n_slots = 1 << 30  # no state to be out of
+        return n_slots
+
+    def _out(self, out, n, where):
+        import torch
+        d = self.dims
+        if out is None:
+            out = torch.empty((n, d.v_heads, d.v_dim), dtype=torch.bfloat16,
+                              device=self.workspace.device)
+        _require(out.dtype == torch.bfloat16 and tuple(out.shape) == (n, d.v_heads, d.v_dim) and
+                 out.is_cuda and (n == 0 or out[0].is_contiguous()), where)
+        return out, out.stride(0) if n > 1 else d.v_heads * d.v_dim
+
+    def chunk(self, q, k, v, g, beta, cu_seqlens=None, state_in=None, state_out=None, slots=None,
+              out=None, stream=None):
+        """Whole prompts: the rows of len(cu_seqlens) - 1 sequences one after
+        another (one sequence without ``cu_seqlens``).  Returns out [N][v_heads][v_dim]."""
+        import torch
+        where = "GatedDelta.chunk"
+        n, inputs = self._inputs(q, k, v, g, beta, where)
+        B = 1
+        if cu_seqlens is not None:
+            _require(cu_seqlens.dtype == torch.int32 and cu_seqlens.is_cuda and
+                     cu_seqlens.is_contiguous() and cu_seqlens.dim() == 1 and
+                     cu_seqlens.shape[0] >= 1, where)
+            B = cu_seqlens.shape[0] - 1
+        n_slots = self._states(state_in, state_out, slots, B, where)
+        out, out_ld = self._out(out, n, where)
+        moe_delta_chunk(self.dims, inputs, n, cu_seqlens, B, slots, n_slots, state_in, state_out,
+                        out, out_ld, self.workspace, self.ws_bytes, stream)
+        return out
+
+    def step(self, q, k, v, g, beta, state_in=None, state_out=None, slots=None, tokens=None,
+             out=None, stream=None):
+        """Decode and verification: ``tokens`` consecutive rows for each
+        sequence (by default as many as make ``slots``, or else the states,
+        one per sequence).  Returns out [rows][v_heads][v_dim]."""
+        where = "GatedDelta.step"
+        n, inputs = self._inputs(q, k, v, g, beta, where)
+        if tokens is None:
+            lead = slots if slots is not None else state_in if state_in is not None else state_out
+            B = n if lead is None else lead.shape[0]
+            tokens = n // B if B else 0
+        else:
+            B = n // tokens if tokens else 0
+        _require(B * tokens == n, where)
+        n_slots = self._states(state_in, state_out, slots, B, where)
+        out, out_ld = self._out(out, n, where)
+        moe_delta_step(self.dims, inputs, B, tokens, slots, n_slots, state_in, state_out, out,
+                       out_ld, self.workspace, self.ws_bytes, stream)
+        return out
+
+    def status(self, stream=None) -> int:
+        return moe_read_status(self.workspace, stream)
+
+    def clear_status(self, stream=None):
+        moe_clear_status(self.workspace, stream)
+
+
+def _rows_of(t, shape, where):
+    """(inner, stride) of a bf16 tensor [rows][width] or [tokens][heads][width]
+    whose first stride alone is free."""
+    import torch
+    _require(t.dtype == torch.bfloat16 and t.is_cuda and tuple(t.shape) == tuple(shape) and
+             (t.shape[0] == 0 or t[0].is_contiguous()), where)
+    return t.stride(0) if t.shape[0] > 1 else t[:1].numel()
+
+
+def norm_gate_residual(x, gamma_post=None, gate=None, gate_act="sigmoid", resid=None,
+                       res_scale=1.0, gamma_pre=None, eps=1e-6, resid_out=None, x_next=None,
+                       stream=None):
+    """``resid_out = bf16(resid + res_scale * act(gate) * norm(x) * gamma_post)``
+    and ``x_next = bf16(norm(resid_out) * gamma_pre)`` in one kernel (see
+    ``moe_norm_gate_residual``).  ``x`` is bf16 [rows][width] or
+    [tokens][heads][width] (one norm per head); ``gate`` is [width] (per
+    channel), shaped like ``x``, or [.., 1] (per row).  Returns (resid_out,
+    x_next), x_next None without ``gamma_pre``; x is not changed unless it is
+    given as an output."""
+    import torch
+    where = "norm_gate_residual"
+    _require(x.dim() in (2, 3) and x.shape[-1] > 0 and gate_act in GATE_ACTS, where)
+    width = x.shape[-1]
+    inner = x.shape[1] if x.dim() == 3 else 1
+    _require(inner > 0, where)
+    a = NormArgs(rows=x.shape[0] * inner, width=width, inner=inner, res_scale=res_scale, eps=eps,
+                 gate_act=GATE_ACTS[gate_act], gate_kind=GATE_NONE)
+    a.x, a.x_ld = _a(x), _rows_of(x, x.shape, where)
+    for name, gamma in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
+        if gamma is not None:
+            _require(gamma.dtype == torch.bfloat16 and gamma.is_cuda and
+                     tuple(gamma.shape) == (width,) and gamma.is_contiguous(), where)
+            setattr(a, name, _a(gamma))
+    if gate is not None:
+        if gate.dim() == 1:
+            _require(gate.dtype == torch.bfloat16 and gate.is_cuda and
+                     tuple(gate.shape) == (width,) and gate.is_contiguous(), where)
+            a.gate_kind = GATE_CHANNEL
+        elif tuple(gate.shape) == tuple(x.shape):
+            a.gate_kind, a.gate_ld = GATE_ELEMENT, _rows_of(gate, x.shape, where)
+        else:
+            a.gate_kind = GATE_ROW
+            a.gate_ld = _rows_of(gate, tuple(x.shape[:-1]) + (1,), where)
+        a.gate = _a(gate)
+    if resid is not None:
+        a.resid_in, a.resid_in_ld = _a(resid), _rows_of(resid, x.shape, where)
+    if resid_out is None:
+        resid_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    a.resid_out, a.resid_out_ld = _a(resid_out), _rows_of(resid_out, x.shape, where)
+    if gamma_pre is not None:
+        if x_next is None:
+            x_next = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        a.x_next, a.x_next_ld = _a(x_next), _rows_of(x_next, x.shape, where)
+    else:
+        _require(x_next is None, where)
+    moe_norm_gate_residual(a, stream)
+    return resid_out, x_next

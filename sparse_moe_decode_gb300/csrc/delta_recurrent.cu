@@ -1,0 +1,175 @@
+// delta_recurrent.cu -- the gated delta rule token by token: decode, draft
+// verification, and sequences too short for the chunked form.
+//
+// Per token and value head, with S [dv][dk] (row r holds value r's memory):
+//   a = e^g,  u = beta (v - a S k),  S <- a S + u k^T,  o = scale S q
+//     = scale (a S_old q + u (k . q)).
+// Both products with the old state are formed together, so each token costs
+// one pass over the registers that hold the state and one reduction.
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "delta_seq.cuh"
+#include "mixer.h"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+
+// Sums N values over the 32 lanes at once: each round halves the values a
+// lane still carries (N + N/2 + ... shuffles in place of 5 N).  The total of
+// value i ends in every lane l with l / (32 / N) == i.
+template <int N>
+__device__ __forceinline__ float reduce_spread(float (&v)[N], int lane) {
+  int o = 16;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = up ? v[i] : v[i + n];
+      const float keep = up ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(kFull, send, o);
+    }
+  }
+  float r = v[0];
+  for (; o >= 1; o >>= 1) r += __shfl_xor_sync(kFull, r, o);
+  return r;
+}
+
+template <int V>
+struct Vec;
+template <>
+struct Vec<4> {
+  using F = float4;
+  using H = uint2;
+};
+template <>
+struct Vec<2> {
+  using F = float2;
+  using H = uint32_t;
+};
+
+__device__ __forceinline__ void unpack(uint2 w, float (&o)[4]) {
+  o[0] = bf16_lo(w.x), o[1] = bf16_hi(w.x), o[2] = bf16_lo(w.y), o[3] = bf16_hi(w.y);
+}
+__device__ __forceinline__ void unpack(uint32_t w, float (&o)[2]) {
+  o[0] = bf16_lo(w), o[1] = bf16_hi(w);
+}
+__device__ __forceinline__ void unpack(float4 w, float (&o)[4]) {
+  o[0] = w.x, o[1] = w.y, o[2] = w.z, o[3] = w.w;
+}
+__device__ __forceinline__ void unpack(float2 w, float (&o)[2]) { o[0] = w.x, o[1] = w.y; }
+__device__ __forceinline__ float4 pack(const float (&v)[4]) {
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ float2 pack(const float (&v)[2]) { return make_float2(v[0], v[1]); }
+
+constexpr int kWarps = 4;
+constexpr int kRows = 16;  // state rows per warp
+
+// One warp holds kRows rows of one head's state, lane l columns V l .. V l +
+// V - 1 of each (a row is one coalesced access).
+template <int DK>
+__global__ void __launch_bounds__(32 * kWarps)
+delta_recurrent_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, moe_bf16 *out,
+                       int64_t out_ld) {
+  constexpr int V = DK / 32;
+  using VF = typename Vec<V>::F;
+  using VH = typename Vec<V>::H;
+  const int lane = threadIdx.x & 31;
+  const int tiles = d.v_dim / kRows;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int tile = static_cast<int>(unit % tiles);
+  const int64_t bh = unit / tiles;
+  const int h = static_cast<int>(bh % d.v_heads);
+  const int64_t b64 = bh / d.v_heads;
+  if (b64 >= seq.B) return;
+  const int b = static_cast<int>(b64);
+  const DeltaSeqRange r = delta_seq_range(seq, b);
+  if (!r.ok) return;
+  const int hk = h / (d.v_heads / d.qk_heads);
+  const int64_t at =
+      ((static_cast<int64_t>(r.slot) * d.v_heads + h) * d.v_dim + tile * kRows) * DK + lane * V;
+  float s[kRows][V];
+  if (seq.state_in) {
+    const float *p = seq.state_in + at;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) unpack(*reinterpret_cast<const VF *>(p + i * DK), s[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[i][j] = 0.0f;
+  }
+  for (int t = 0; t < r.len; ++t) {
+    const int64_t row = static_cast<int64_t>(r.start) + t;
+    float k[V], q[V];
+    unpack(*reinterpret_cast<const VH *>(in.k + row * in.k_ld + hk * DK + lane * V), k);
+    unpack(*reinterpret_cast<const VH *>(in.q + row * in.q_ld + hk * DK + lane * V), q);
+    const float v =
+        bf16_to_f32(in.v[row * in.v_ld + h * d.v_dim + tile * kRows + (lane & (kRows - 1))]);
+    const float a = expf(delta_log_decay(in.g[row * in.g_ld + h]));
+    const float beta = in.beta[row * in.beta_ld + h];
+    float kk = 0.0f, qq = 0.0f, kq = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      kk = fmaf(k[j], k[j], kk);
+      qq = fmaf(q[j], q[j], qq);
+      kq = fmaf(k[j], q[j], kq);
+    }
+    kk = warp_sum(kk), qq = warp_sum(qq), kq = warp_sum(kq);
+    float kn = 1.0f, qn = d.scale;
+    if (d.qk_norm) {
+      kn = 1.0f / sqrtf(kk + d.qk_eps);
+      qn = d.scale / sqrtf(qq + d.qk_eps);
+    }
+    float part[2 * kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      float sk = 0.0f, sq = 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        sk = fmaf(s[i][j], k[j], sk);
+        sq = fmaf(s[i][j], q[j], sq);
+      }
+      part[i] = sk;
+      part[kRows + i] = sq;
+    }
+    // lane i < kRows: row i's S k; lane kRows + i: its S q
+    const float sum = reduce_spread(part, lane);
+    const float sq = __shfl_down_sync(kFull, sum, kRows);
+    const float u = beta * (v - a * kn * sum);  // lanes < kRows
+    if (lane < kRows)
+      out[row * out_ld + h * d.v_dim + tile * kRows + lane] =
+          f32_to_bf16(qn * (a * sq + u * kn * kq));
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const float ui = __shfl_sync(kFull, u, i) * kn;
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[i][j] = fmaf(a, s[i][j], ui * k[j]);
+    }
+  }
+  if (seq.state_out) {
+    float *p = seq.state_out + at;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) *reinterpret_cast<VF *>(p + i * DK) = pack(s[i]);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_delta_recurrent(const moe_delta_dims &d, const moe_delta_inputs &in,
+                                   const DeltaSeqs &seq, moe_bf16 *out, int64_t out_ld,
+                                   cudaStream_t s) {
+  const int64_t units = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / kRows);
+  const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
+  if (d.qk_dim == 128)
+    delta_recurrent_kernel<128><<<grid, 32 * kWarps, 0, s>>>(d, in, seq, out, out_ld);
+  else
+    delta_recurrent_kernel<64><<<grid, 32 * kWarps, 0, s>>>(d, in, seq, out, out_ld);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,33 @@
+// mixer.h -- host-side launchers of the gated delta rule and of the norms
+// around a block (internal).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe_gb300.h"
+
+namespace moe {
+
+// Which tokens and which state a sequence has: its rows come from cu_seqlens
+// (N rows in all) or, without them, are b * T .. b * T + T - 1.
+struct DeltaSeqs {
+  const int32_t *cu_seqlens;  // [B + 1] or nullptr
+  int N, B, T;
+  const int32_t *slots;  // [B] or nullptr
+  int n_slots;
+  const float *state_in;  // nullable
+  float *state_out;       // nullable
+  uint32_t *status;
+};
+
+// Token by token, the state in registers (any length).
+cudaError_t launch_delta_recurrent(const moe_delta_dims &d, const moe_delta_inputs &in,
+                                   const DeltaSeqs &seq, moe_bf16 *out, int64_t out_ld,
+                                   cudaStream_t s);
+
+// a.rows > 0; `vec8`: every row starts on a 16-byte boundary and width is a
+// multiple of 8.
+cudaError_t launch_norm_gate_residual(const moe_norm_args &a, bool vec8, cudaStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,343 @@
+"""The gated delta rule (moe_delta_chunk, moe_delta_step) against its fp64
+definition, token by token; the bounds stand in mixer_ref."""
+import numpy as np
+import pytest
+
+from mixer_ref import delta_rule, out_bound, state_bound
+from util import gpu_env
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module")
+def env():
+    return gpu_env()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def make(env, n, heads=(2, 4), dims=(128, 128), seed=0, k_std=1.0, v_std=1.0, guard=3):
+    """Token rows as slices of one projected buffer with `guard` NaN rows
+    before and after them."""
+    import torch
+    _, dev = env
+    (hk, hv), (dk, dv) = heads, dims
+    g = torch.Generator(device=dev).manual_seed(1000 * seed + n)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device=dev)
+
+    def guarded(t):
+        buf = torch.full((n + 2 * guard, t.shape[1]), float("nan"), dtype=t.dtype, device=dev)
+        buf[guard:guard + n] = t
+        return buf[guard:guard + n]
+
+    row = torch.cat([normal(n, hk * dk), k_std * normal(n, hk * dk), v_std * normal(n, hv * dv)], 1)
+    q, k, v = guarded(row.bfloat16()).split([hk * dk, hk * dk, hv * dv], 1)
+    gb = guarded(torch.cat([-torch.exp(1.5 * normal(n, hv) - 2.0), torch.sigmoid(normal(n, hv))], 1))
+    return dict(q=q.unflatten(1, (hk, dk)), k=k.unflatten(1, (hk, dk)),
+                v=v.unflatten(1, (hv, dv)), g=gb[:, :hv], beta=gb[:, hv:])
+
+
+def states(env, slots, heads, dims, seed=0):
+    import torch
+    _, dev = env
+    g = torch.Generator(device=dev).manual_seed(77 + seed)
+    return torch.randn((slots, heads[1], dims[1], dims[0]), generator=g, device=dev) * 0.2
+
+
+def mixer(env, heads, dims, n, b, qk_norm=True):
+    moe, dev = env
+    return moe.GatedDelta(*heads, *dims, max_tokens=n, max_seqs=b, qk_norm=qk_norm, qk_eps=EPS,
+                          device=dev)
+
+
+def cu_of(env, lens):
+    import torch
+    _, dev = env
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=dev)
+
+
+def check_seq(s, rows, S0, out, S1, dims, qk_norm=True):
+    """One sequence's rows (a slice) against the definition."""
+    c = {x: f64(s[x][rows]) for x in ("q", "k", "v", "g", "beta")}
+    want, S, oabs, A = delta_rule(**c, S0=f64(S0), scale=dims[0] ** -0.5, qk_norm=qk_norm, eps=EPS)
+    chunks = 1 + want.shape[0] // 64
+    err = np.abs(f64(out[rows]) - want)
+    assert not (err > out_bound(want, oabs, chunks)).any() and not np.isnan(err).any(), err.max()
+    if S1 is not None:
+        err = np.abs(f64(S1) - S)
+        assert not (err > state_bound(A, chunks)).any() and not np.isnan(err).any(), err.max()
+
+
+def run_chunk(env, s, lens, heads, dims, state=True, qk_norm=True, in_place=False, seed=0):
+    import torch
+    _, dev = env
+    n, b = sum(lens), len(lens)
+    m = mixer(env, heads, dims, n, b, qk_norm)
+    pool = states(env, b + 2, heads, dims, seed)
+    slots = torch.from_numpy(np.random.RandomState(seed).permutation(b + 2)[:b].astype(np.int32))
+    slots = slots.to(dev)
+    given = pool.clone()
+    S1 = pool if in_place else torch.full_like(pool, 7.0)
+    out = m.chunk(**s, cu_seqlens=cu_of(env, lens), slots=slots, state_in=pool if state else None,
+                  state_out=S1)
+    assert m.status() == 0
+    at = 0
+    for i, L in enumerate(lens):
+        S0 = given[slots[i]] if state else torch.zeros_like(given[0])
+        check_seq(s, slice(at, at + L), S0, out, S1[slots[i]], dims, qk_norm)
+        at += L
+    rest = [x for x in range(b + 2) if x not in slots.tolist()]
+    assert torch.equal(S1[rest], given[rest] if in_place else torch.full_like(given[rest], 7.0))
+    return out, S1
+
+
+@pytest.mark.parametrize("n", [1, 2, 7, 15, 16, 17, 31, 33, 63, 64, 65, 100, 128, 129, 200])
+def test_chunk_one_sequence(env, n):
+    s = make(env, n)
+    run_chunk(env, s, [n], (2, 4), (128, 128))
+    run_chunk(env, s, [n], (2, 4), (128, 128), state=False)
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("heads", [(1, 1), (1, 3), (2, 2), (3, 12)])
+def test_chunk_ragged(env, heads, dims):
+    lens = [70, 0, 1, 64, 130, 3]
+    run_chunk(env, make(env, sum(lens), heads, dims, seed=1), lens, heads, dims)
+
+
+def test_chunk_many_sequences_in_place(env):
+    lens = [int(x) for x in np.random.RandomState(3).randint(0, 90, 40)]
+    run_chunk(env, make(env, sum(lens), (1, 2), (64, 64)), lens, (1, 2), (64, 64), in_place=True)
+
+
+def test_chunk_long(env):
+    run_chunk(env, make(env, 1500, (1, 2)), [1500], (1, 2), (128, 128))
+
+
+@pytest.mark.parametrize("k_std", [0.05, 1e-6])
+def test_chunk_without_norm(env, k_std):
+    """k as it is (small enough for the rule to contract), tiny k too."""
+    lens = [150, 20]
+    run_chunk(env, make(env, 170, k_std=k_std, v_std=30.0), lens, (2, 4), (128, 128),
+              qk_norm=False)
+
+
+def test_chunk_without_norm_unit_keys_repeated(env):
+    """The same unit key for every token with beta 1: each token replaces
+    what the last one wrote, and the inverse's entries alternate."""
+    import torch
+    s = make(env, 130)
+    s["k"].zero_()
+    s["k"][:, :, 5] = 1.0
+    s["beta"].fill_(1.0)
+    run_chunk(env, s, [130], (2, 4), (128, 128), qk_norm=False)
+
+
+def test_chunk_gate_extremes(env):
+    """Resets (-inf, -1000), no decay at all, beta 0 and 1, zero keys and
+    queries, and infinite decay beside very slow ones."""
+    s = make(env, 200)
+    s["g"][10] = -float("inf")
+    s["g"][70:72] = -1000.0
+    s["g"][90] = -600.0
+    s["g"][91:140] = -1e-3
+    s["g"][140:180] = 0.0
+    s["beta"][20:30] = 0.0
+    s["beta"][40:50] = 1.0
+    s["k"][60:66] = 0.0
+    s["q"][66] = 0.0
+    run_chunk(env, s, [200], (2, 4), (128, 128))
+    run_chunk(env, s, [64, 136], (2, 4), (128, 128))
+
+
+def test_chunk_slow_decay_after_a_reset_keeps_its_bits(env):
+    """Sums of logarithms that reach -40000 within a run of 64 tokens do not
+    cost the later, slow decays their digits."""
+    s = make(env, 128)
+    s["g"][:] = -0.001
+    s["g"][::2] = -120.0
+    s["g"][40:] = -0.0123
+    run_chunk(env, s, [128], (2, 4), (128, 128))
+
+
+def test_sequences_do_not_see_one_another(env):
+    """A sequence's bits do not depend on its neighbours, NaN among them."""
+    import torch
+    moe, dev = env
+    lens = [80, 40, 200]
+    s = make(env, 320)
+    want, S = run_chunk(env, s, lens, (2, 4), (128, 128))
+    s["v"][85] = float("nan")
+    s["k"][90] = float("inf")
+    m = mixer(env, (2, 4), (128, 128), 320, 3)
+    pool = states(env, 5, (2, 4), (128, 128))
+    slots = torch.from_numpy(np.random.RandomState(0).permutation(5)[:3].astype(np.int32)).to(dev)
+    S1 = torch.full_like(pool, 7.0)
+    out = m.chunk(**s, cu_seqlens=cu_of(env, lens), slots=slots, state_in=pool, state_out=S1)
+    for rows, i in ((slice(0, 80), 0), (slice(120, 320), 2)):
+        assert torch.equal(out[rows], want[rows])
+        assert torch.equal(S1[slots[i]], S[slots[i]])
+    assert torch.isnan(out[119]).all()
+
+
+@pytest.mark.parametrize("api", ["chunk", "step"])
+def test_skipped_and_bad_sequences(env, api):
+    """A negative slot skips its sequence; a slot out of range does too and
+    sets the status bit; nothing of either is written."""
+    import torch
+    moe, dev = env
+    heads, dims = (2, 4), (128, 128)
+    T = 70 if api == "chunk" else 5
+    s = make(env, 4 * T, heads, dims)
+    for third, bit in ((-1, 0), (6, moe.DEV_BAD_INDEX)):
+        m = mixer(env, heads, dims, 4 * T, 4)
+        pool = states(env, 6, heads, dims)
+        slots = torch.tensor([4, -1, third, 0], dtype=torch.int32, device=dev)
+        out = torch.full((4 * T, 4, 128), 3.0, dtype=torch.bfloat16, device=dev)
+        S1 = torch.full_like(pool, 7.0)
+        kw = dict(state_in=pool, state_out=S1, slots=slots, out=out)
+        if api == "chunk":
+            m.chunk(**s, cu_seqlens=cu_of(env, [T] * 4), **kw)
+        else:
+            m.step(**s, **kw)
+        assert m.status() == bit
+        m.clear_status()
+        assert m.status() == 0
+        assert (out[T:3 * T] == 3.0).all() and (S1[[1, 2, 3, 5]] == 7.0).all()
+        for i in (0, 3):
+            check_seq(s, slice(i * T, i * T + T), pool[slots[i]], out, S1[slots[i]], dims)
+
+
+@pytest.mark.parametrize("cu", [[0, 100, 50, 120], [-5, 20, 60, 120], [0, 40, 80, 121],
+                                [0, 40, 1 << 30, 120]])
+def test_bad_bounds_are_skipped(env, cu):
+    """Bounds that are not 0 <= start <= end <= N set the status bit, and the
+    sequences that have them are not touched."""
+    import torch
+    moe, dev = env
+    heads, dims = (1, 2), (64, 64)
+    s = make(env, 120, heads, dims)
+    m = mixer(env, heads, dims, 120, 3)
+    S1 = torch.full((3, 2, 64, 64), 7.0, device=dev)
+    m.chunk(**s, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=dev), state_out=S1)
+    assert m.status() == moe.DEV_BAD_INDEX
+    for i in range(3):
+        if not 0 <= cu[i] <= cu[i + 1] <= 120:
+            assert (S1[i] == 7.0).all()
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("B,T", [(1, 1), (3, 1), (2, 2), (5, 5), (1, 17), (70, 1)])
+def test_step(env, B, T, dims):
+    import torch
+    _, dev = env
+    heads = (2, 4)
+    s = make(env, B * T, heads, dims, seed=2)
+    m = mixer(env, heads, dims, B * T, B)
+    pool = states(env, B + 1, heads, dims)
+    given = pool.clone()
+    slots = torch.arange(B, 0, -1, dtype=torch.int32, device=dev)
+    S1 = torch.full_like(pool, 7.0)
+    out = m.step(**s, state_in=pool, state_out=S1, slots=slots)
+    for i in range(B):
+        check_seq(s, slice(i * T, i * T + T), given[slots[i]], out, S1[slots[i]], dims)
+    assert (S1[0] == 7.0).all()
+    inp = m.step(**s, state_in=pool, state_out=pool, slots=slots)
+    assert torch.equal(inp, out) and torch.equal(pool[1:], S1[1:])
+    again = m.step(**s, state_in=given, slots=slots)  # the state is not kept
+    assert torch.equal(again, out)
+
+
+def test_step_zero_state_and_no_norm(env):
+    heads, dims = (4, 4), (128, 64)
+    s = make(env, 12, heads, dims, k_std=0.05)
+    m = mixer(env, heads, dims, 12, 3, qk_norm=False)
+    import torch
+    S1 = torch.empty((3, 4, 64, 128), device=env[1])
+    out = m.step(**s, state_out=S1, tokens=4)
+    for i in range(3):
+        check_seq(s, slice(4 * i, 4 * i + 4), torch.zeros_like(S1[0]), out, S1[i], dims, False)
+
+
+def test_prompt_then_steps(env):
+    """A prompt in one call, then tokens one at a time on its state, is the
+    whole sequence."""
+    import torch
+    heads, dims = (2, 4), (128, 128)
+    n = 140
+    s = make(env, n, heads, dims)
+    m = mixer(env, heads, dims, n, 1)
+    state = torch.zeros((1, 4, 128, 128), device=env[1])
+    cut = {k: v[:130] for k, v in s.items()}
+    outs = [m.chunk(**cut, state_in=state, state_out=state)]
+    for t in range(130, n):
+        outs.append(m.step(**{k: v[t:t + 1] for k, v in s.items()}, state_in=state,
+                           state_out=state))
+    check_seq(s, slice(0, n), torch.zeros_like(state[0]), torch.cat(outs), state[0], dims)
+
+
+def test_empty_calls(env):
+    import torch
+    moe, dev = env
+    s = make(env, 0, guard=1)
+    m = mixer(env, (2, 4), (128, 128), 8, 4)
+    pool = states(env, 2, (2, 4), (128, 128))
+    S1 = torch.full_like(pool, 7.0)
+    out = m.chunk(**s, cu_seqlens=cu_of(env, [0, 0]), state_in=pool, state_out=S1)
+    assert out.shape == (0, 4, 128) and torch.equal(S1, pool)  # no tokens: the state as it was
+    m.chunk(**s, cu_seqlens=cu_of(env, []), state_in=pool, state_out=S1)
+    m.step(**s, state_in=pool, state_out=S1, tokens=0)
+
+
+def test_streams_and_graphs(env):
+    import torch
+    heads, dims = (2, 4), (128, 128)
+    s = make(env, 150, heads, dims)
+    m = mixer(env, heads, dims, 150, 1)
+    state = states(env, 1, heads, dims)
+    S1, S2 = torch.empty_like(state), torch.empty_like(state)
+    want = m.chunk(**s, state_in=state, state_out=S1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = m.chunk(**s, state_in=state, state_out=S2)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.equal(want, got) and torch.equal(S1, S2)
+    out = torch.zeros_like(want)
+    tok = {k: v[:1] for k, v in s.items()}
+    tout = torch.zeros_like(want[:1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.chunk(**s, state_in=state, state_out=S2, out=out)
+        m.step(**tok, state_in=S2, state_out=S2, out=tout)
+    S2.zero_()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert torch.equal(tout, m.step(**tok, state_in=S1, state_out=S1))
+    assert torch.equal(S1, S2)
+
+
+def test_state_offsets_beyond_32_bits(env):
+    """A pool whose last slot starts past 2^31 values."""
+    import torch
+    _, dev = env
+    heads, dims = (2, 32), (128, 128)
+    pool = torch.empty((4200, 32, 128, 128), device=dev)
+    last = states(env, 1, heads, dims)[0]
+    slots = torch.tensor([4199], dtype=torch.int32, device=dev)
+    for n, api in ((3, "step"), (70, "chunk")):
+        s = make(env, n, heads, dims)
+        m = mixer(env, heads, dims, n, 1)
+        pool[4199] = last
+        out = getattr(m, api)(**s, state_in=pool, state_out=pool, slots=slots,
+                              **({"cu_seqlens": cu_of(env, [n])} if api == "chunk" else {}))
+        check_seq(s, slice(0, n), last, out, pool[4199], dims)
