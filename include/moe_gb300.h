@@ -324,9 +324,9 @@ size_t moe_delta_workspace_bytes(const moe_delta_dims *dims, int N, int B);
  * state_in NULL: all start from zero.  state_out NULL: not kept.  state_out
  * may be state_in (updated in place) or disjoint from it.  Two sequences
  * must not share a slot.  A sequence whose slot is negative is skipped, its
- * out rows and state left as they were; so is one whose slot is >= n_slots
- * or whose bounds are not 0 <= start <= end <= N, and that sets
- * MOE_DEV_BAD_INDEX.  out row t lies at out + t * out_ld as [Hv][v_dim] bf16
+ * out rows and state left as they were; so is one whose slot is >= n_slots,
+ * and that sets MOE_DEV_BAD_INDEX.  If any bounds are not 0 <= start <= end
+ * <= N, MOE_DEV_BAD_INDEX is set and no out row or state is written.  out row t lies at out + t * out_ld as [Hv][v_dim] bf16
  * (16-byte aligned, out_ld a multiple of 8) and must not overlap the inputs.
  * N <= 2^20, B <= 65536.  A value that is not finite makes its head's state,
  * and that head's outputs within the same run of 64 tokens and after it,

@@ -1,0 +1,802 @@
+// delta_chunk.cu -- the gated delta rule over prompts, 64 tokens at a time.
+//
+// Within a chunk that starts from state S (rows = value channels, columns =
+// key channels), with G the running sum of g, gamma_i = e^{G_i} and
+// Gamma_ij = e^{G_i - G_j}:
+//   u_i = beta_i (v_i - gamma_i S k_i) - sum_{j<i} beta_i Gamma_ij (k_i.k_j) u_j
+//   o_i = gamma_i S q_i + sum_{j<=i} Gamma_ij (q_i.k_j) u_j
+//   S' = gamma_64 S + sum_j Gamma_64,j u_j k_j^T.
+// The first line is a unit lower-triangular system: u = T x with T = (I + L)^-1.
+//
+// Two kernels.  delta_prep_kernel, one CTA per (chunk, value head), forms
+// what does not depend on the state: T, the masked q.k products P, the
+// decays, and k and q as fp16.  delta_chain_kernel walks a sequence's chunks
+// with the state in registers: a warp owns 16 state rows (all of their
+// columns), and the three products of its chain -- S k^T, T x, u k^T -- hand
+// their results on as the next one's A operand without leaving the warp's
+// registers (an accumulator fragment of mma.sync m16n8 is an A fragment of
+// the next k16 step), so that no barrier lies on the chain.  A second warp
+// per 16 rows forms the outputs from copies of the operands.  mma.sync
+// rather than tcgen05: the chain is bound by its dependent steps, and a
+// round trip of each through tensor memory costs more than the products.
+//
+// Precision.  k and q are bf16: scaled by a power of two per token they are
+// exact in fp16 (elements within 2^29 of the token's largest).  S, x, u and T
+// are fp32 and enter the products as two fp16 terms under a power-of-two
+// scale per row, 22 bits; products accumulate in fp32 and the state is summed
+// in fp32 registers.  The outputs, which are rounded to bf16 once, take P, S
+// and u as single fp16 terms (2^-11, an eighth of the rounding to come).
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "delta_mma.cuh"
+#include "delta_seq.cuh"
+#include "kernels.h"
+#include "mixer.h"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kC = 64;  // tokens per chunk
+constexpr int kTile = kC * kC * 2;  // bytes of a 64 x 64 fp16 tile
+// Per (chunk, value head): T's two terms, P, then vectors of 64 fp32.
+enum { kVecC, kVecBeta, kVecT, kVecD, kVecO, kVecP, kVecMisc, kVecs };
+constexpr int kHeadBlob = 3 * kTile + kVecs * kC * 4;
+constexpr int kHeader = 256;      // status word, flags
+constexpr int kFlagWord = 16;     // header word: some bound of the call is bad
+constexpr int kPrepThreads = 128;
+constexpr int kLd = kC + 1;       // row stride of the fp32 work matrix
+
+template <int DK>
+constexpr int kKeyBlob = 2 * kC * DK * 2;  // per (chunk, key head): k, then q, as fp16
+
+// Tiles of fp16 in 16-byte pieces, rows of COLS values; a row's pieces are
+// permuted within groups of eight by its number, so that eight rows' pieces of
+// one column lie in different banks.
+template <int COLS>
+__device__ __forceinline__ uint32_t tile_at(int row, int piece) {
+  return static_cast<uint32_t>(row * COLS * 2 + ((piece ^ (row & 7)) << 4));
+}
+
+// Sequence b's first chunk slot: chunks of different sequences never share
+// one, whatever the lengths.
+__device__ __forceinline__ int slot_base(const DeltaSeqs &s, int b) {
+  return (s.cu_seqlens ? s.cu_seqlens[b] : b * s.T) / kC + b;
+}
+
+// ------------------------------------------------------------------- prep
+
+template <int DK>
+struct PrepSmem {
+  alignas(128) uint8_t key[kKeyBlob<DK>];
+  alignas(128) uint8_t head[kHeadBlob];
+  float m[kC * kLd];  // below the diagonal L, above it T transposed
+  float kappa[kC], rho[kC], beta[kC], ghi[kC], glo[kC], half_max[2][kC];
+};
+
+// T(i, j) of the work matrix: stored transposed above the diagonal.
+__device__ __forceinline__ float t_at(const float *m, int i, int j) {
+  return i > j ? m[j * kLd + i] : (i == j ? 1.0f : 0.0f);
+}
+
+// acc (16 rows from r0, 16 columns from c0) = A B over k in [k0, k1), fp32
+// values in three tf32 products each.
+template <class FA, class FB>
+__device__ __forceinline__ void product16(float (&acc)[2][4], int r0, int c0, int k0, int k1,
+                                          FA a_of, FB b_of, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+  for (int k = k0; k < k1; k += 8) {
+    uint32_t ah[4], al[4];
+    split_tf32(a_of(r0 + g, k + t), ah[0], al[0]);
+    split_tf32(a_of(r0 + g + 8, k + t), ah[1], al[1]);
+    split_tf32(a_of(r0 + g, k + t + 4), ah[2], al[2]);
+    split_tf32(a_of(r0 + g + 8, k + t + 4), ah[3], al[3]);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      uint32_t bh[2], bl[2];
+      split_tf32(b_of(k + t, c0 + 8 * n + g), bh[0], bl[0]);
+      split_tf32(b_of(k + t + 4, c0 + 8 * n + g), bh[1], bl[1]);
+      mma8(acc[n], ah, bl[0], bl[1]);
+      mma8(acc[n], al, bh[0], bh[1]);
+      mma8(acc[n], ah, bh[0], bh[1]);
+    }
+  }
+}
+
+template <int DK>
+__global__ void __launch_bounds__(kPrepThreads)
+delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t *ws,
+                  uint8_t *ws_key, uint8_t *ws_head) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  PrepSmem<DK> &sm = *reinterpret_cast<PrepSmem<DK> *>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slot = blockIdx.x, h = blockIdx.y, ratio = d.v_heads / d.qk_heads, hk = h / ratio;
+
+  if (slot == 0 && h == 0) {
+    // one CTA looks at every bound: a call with a bad one does nothing
+    __shared__ int any_bad;
+    if (tid == 0) any_bad = 0;
+    __syncthreads();
+    if (seq.cu_seqlens)
+      for (int b = tid; b < seq.B; b += kPrepThreads) {
+        const int lo = seq.cu_seqlens[b], hi = seq.cu_seqlens[b + 1];
+        if (lo < 0 || lo > hi || hi > seq.N) any_bad = 1;
+      }
+    __syncthreads();
+    if (tid == 0) {
+      reinterpret_cast<uint32_t *>(ws)[kFlagWord] = any_bad;
+      if (any_bad) set_status(seq.status, MOE_DEV_BAD_INDEX);
+    }
+  }
+
+  // whose chunk this is: the last sequence whose slots start at or before it
+  int lo = 0, hi = seq.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (slot_base(seq, mid) <= slot) lo = mid;
+    else hi = mid;
+  }
+  const DeltaSeqRange r = delta_seq_range(seq, lo);
+  const int chunk = slot - slot_base(seq, lo);
+  if (!r.ok || chunk < 0 || chunk >= (r.len + kC - 1) / kC) return;
+  const int left = min(kC, r.len - chunk * kC);  // tokens of this chunk
+  const int64_t row0 = static_cast<int64_t>(r.start) + chunk * kC;
+
+  // k and q: scaled to fp16, their norms
+  constexpr int kLanes = DK / 8;  // threads of a row, 8 values each
+  constexpr int kRowsAt = kPrepThreads / kLanes;
+  const int piece = tid % kLanes;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    uint4 raw[kC / kRowsAt];
+#pragma unroll
+    for (int p = 0; p < kC / kRowsAt; ++p) {
+      const int i = p * kRowsAt + tid / kLanes;
+      const moe_bf16 *src = which ? in.q + (row0 + i) * in.q_ld : in.k + (row0 + i) * in.k_ld;
+      raw[p] = i < left ? *reinterpret_cast<const uint4 *>(src + hk * DK + piece * 8)
+                        : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int p = 0; p < kC / kRowsAt; ++p) {
+      const int i = p * kRowsAt + tid / kLanes;
+      const uint32_t w[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
+      float x[8], amax = 0.0f, ss = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] = (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+        amax = fmaxf(amax, fabsf(x[j]));
+        ss = fmaf(x[j], x[j], ss);
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) {
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+        ss += __shfl_xor_sync(kFull, ss, o);
+      }
+      float mult, inv;
+      pow2_scale(amax, mult, inv);
+      uint4 o;
+      o.x = h2_bits(__floats2half2_rn(x[0] * mult, x[1] * mult));
+      o.y = h2_bits(__floats2half2_rn(x[2] * mult, x[3] * mult));
+      o.z = h2_bits(__floats2half2_rn(x[4] * mult, x[5] * mult));
+      o.w = h2_bits(__floats2half2_rn(x[6] * mult, x[7] * mult));
+      *reinterpret_cast<uint4 *>(sm.key + which * (kKeyBlob<DK> / 2) + tile_at<DK>(i, piece)) = o;
+      if (piece == 0) {
+        if (d.qk_norm) inv = inv / sqrtf(ss + d.qk_eps);
+        if (which) inv *= d.scale;
+        (which ? sm.rho : sm.kappa)[i] = i < left ? inv : 0.0f;
+      }
+    }
+  }
+
+  // decays: sums of logarithms in fp64, kept as two fp32 terms each, so that
+  // differences of large sums keep their digits
+  float *vec = reinterpret_cast<float *>(sm.head + 3 * kTile);
+  if (warp == 0) {
+    const int i = 2 * lane;
+    double g0 = 0.0, g1 = 0.0;
+    if (i < left) g0 = delta_log_decay(in.g[(row0 + i) * in.g_ld + h]);
+    if (i + 1 < left) g1 = delta_log_decay(in.g[(row0 + i + 1) * in.g_ld + h]);
+    sm.beta[i] = i < left ? in.beta[(row0 + i) * in.beta_ld + h] : 0.0f;
+    sm.beta[i + 1] = i + 1 < left ? in.beta[(row0 + i + 1) * in.beta_ld + h] : 0.0f;
+    double sum = g0 + g1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double up = __shfl_up_sync(kFull, sum, o);
+      if (lane >= o) sum += up;
+    }
+    const double total = __shfl_sync(kFull, sum, 31);
+    const double first = sum - g1;
+    const double s[2] = {first, sum};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float hi32 = static_cast<float>(s[j]);
+      sm.ghi[i + j] = hi32;
+      sm.glo[i + j] = static_cast<float>(s[j] - hi32);
+      vec[kVecO * kC + i + j] = expf(hi32);                             // gamma_i
+      vec[kVecD * kC + i + j] = expf(static_cast<float>(total - s[j]));  // Gamma_64,i
+    }
+    if (lane == 0) vec[kVecMisc * kC] = expf(static_cast<float>(total));
+  }
+  __syncthreads();
+
+  // L and P: rows 16 warp .. + 15 of k k^T and q k^T, up to the diagonal block
+  {
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t kt = ptx::smem_u32(sm.key), qt = kt + kKeyBlob<DK> / 2;
+    float kk[8][4] = {}, qk[8][4] = {};
+#pragma unroll
+    for (int s = 0; s < DK / 16; ++s) {
+      uint32_t ka[4], qa[4];
+      const int ar = 16 * warp + (lane & 15), ap = 2 * s + (lane >> 4);
+      ldsm4(ka, kt + tile_at<DK>(ar, ap));
+      ldsm4(qa, qt + tile_at<DK>(ar, ap));
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        if (np <= warp) {
+          uint32_t b[4];
+          ldsm4(b, kt + tile_at<DK>(16 * np + (lane & 7) + ((lane >> 4) << 3),
+                                    2 * s + ((lane >> 3) & 1)));
+          mma16(kk[2 * np], ka, b[0], b[1]);
+          mma16(kk[2 * np + 1], ka, b[2], b[3]);
+          mma16(qk[2 * np], qa, b[0], b[1]);
+          mma16(qk[2 * np + 1], qa, b[2], b[3]);
+        }
+      }
+    }
+    float pmax[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 16 * warp + g + (e >> 1) * 8, j = 8 * n + 2 * t + (e & 1);
+        float p = 0.0f;
+        if (j <= i) {
+          const float decay = expf((sm.ghi[i] - sm.ghi[j]) + (sm.glo[i] - sm.glo[j]));
+          const float kj = decay * sm.kappa[j];
+          if (j < i) sm.m[i * kLd + j] = sm.beta[i] * sm.kappa[i] * kj * kk[n][e];
+          p = sm.rho[i] * kj * qk[n][e];
+        }
+        qk[n][e] = p;
+        pmax[e >> 1] = fmaxf(pmax[e >> 1], fabsf(p));
+      }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float mx = pmax[half];
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+      float mult, inv;
+      pow2_scale(mx, mult, inv);
+      const int i = 16 * warp + g + 8 * half;
+      if (t == 0) vec[kVecP * kC + i] = inv;
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+        *reinterpret_cast<__half2 *>(sm.head + 2 * kTile + tile_at<kC>(i, n) + 4 * t) =
+            __floats2half2_rn(qk[n][2 * half] * mult, qk[n][2 * half + 1] * mult);
+    }
+  }
+  if (tid < kC) {
+    vec[kVecBeta * kC + tid] = sm.beta[tid];
+    const float gamma = vec[kVecO * kC + tid];
+    vec[kVecC * kC + tid] = sm.beta[tid] * gamma * sm.kappa[tid];
+    vec[kVecO * kC + tid] = sm.rho[tid] * gamma;
+    vec[kVecD * kC + tid] *= sm.kappa[tid];
+  }
+  __syncwarp();
+
+  // T: the 16 x 16 diagonal blocks by substitution (a lane per column), ...
+  {
+    const int o = 16 * warp, c = lane & 15;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float v = i == c ? 1.0f : 0.0f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) v = fmaf(-sm.m[(o + i) * kLd + o + j], x[j], v);
+      x[i] = v;
+    }
+    __syncwarp();
+    if (lane < 16)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i > c) sm.m[(o + c) * kLd + o + i] = x[i];
+  }
+  __syncthreads();
+  // ... then [A 0; B C]^-1 = [A^-1 0; -C^-1 B A^-1 C^-1] for blocks of 16 and 32
+  const auto l_of = [&](int i, int j) { return sm.m[i * kLd + j]; };
+  const auto t_of = [&](int i, int j) { return t_at(sm.m, i, j); };
+  const auto up_of = [&](int i, int j) { return sm.m[j * kLd + i]; };  // B A^-1, kept above
+  const auto put = [&](const float(&acc)[2][4], int r0, int c0, float sign) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sm.m[(c0 + 8 * n + 2 * t + (e & 1)) * kLd + r0 + g + (e >> 1) * 8] = sign * acc[n][e];
+  };
+  {
+    float acc[2][4];
+    const int o = 32 * warp;
+    if (warp < 2) {
+      product16(acc, o + 16, o, o, o + 16, l_of, t_of, lane);
+      put(acc, o + 16, o, 1.0f);
+      __syncwarp();
+      product16(acc, o + 16, o, o + 16, o + 32, t_of, up_of, lane);
+      __syncwarp();
+      put(acc, o + 16, o, -1.0f);
+    }
+    __syncthreads();
+    const int r0 = 32 + 16 * (warp & 1), c0 = 16 * (warp >> 1);
+    product16(acc, r0, c0, c0, 32, l_of, t_of, lane);  // T(k, c) = 0 for k < c
+    put(acc, r0, c0, 1.0f);
+    __syncthreads();
+    product16(acc, r0, c0, 32, r0 + 16, t_of, up_of, lane);
+    __syncthreads();
+    put(acc, r0, c0, -1.0f);
+    __syncthreads();
+  }
+  // T's rows as two fp16 terms
+  {
+    const int i = tid & 63, j0 = (tid >> 6) * 32;
+    float mx = j0 <= i && i < j0 + 32 ? 1.0f : 0.0f;
+    for (int j = j0; j < min(i, j0 + 32); ++j) mx = fmaxf(mx, fabsf(sm.m[j * kLd + i]));
+    sm.half_max[tid >> 6][i] = mx;
+    __syncthreads();
+    mx = fmaxf(sm.half_max[0][i], sm.half_max[1][i]);
+    float mult, inv;
+    pow2_scale(mx, mult, inv);
+    if (tid < kC) vec[kVecT * kC + i] = inv;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      uint32_t hi32[4], lo32[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + 8 * p + 2 * e;
+        split_h2(t_at(sm.m, i, j), t_at(sm.m, i, j + 1), mult, hi32[e], lo32[e]);
+      }
+      const uint32_t at = tile_at<kC>(i, j0 / 8 + p);
+      *reinterpret_cast<uint4 *>(sm.head + at) = make_uint4(hi32[0], hi32[1], hi32[2], hi32[3]);
+      *reinterpret_cast<uint4 *>(sm.head + kTile + at) =
+          make_uint4(lo32[0], lo32[1], lo32[2], lo32[3]);
+    }
+  }
+  ptx::fence_proxy_async_smem();
+  __syncthreads();
+  if (tid == 0) {
+    bulk_store(ws_head + (static_cast<size_t>(slot) * d.v_heads + h) * kHeadBlob,
+               ptx::smem_u32(sm.head), kHeadBlob);
+    if (h % ratio == 0)
+      bulk_store(ws_key + (static_cast<size_t>(slot) * d.qk_heads + hk) * kKeyBlob<DK>,
+                 ptx::smem_u32(sm.key), kKeyBlob<DK>);
+    bulk_store_wait();
+  }
+}
+
+// ------------------------------------------------------------------ chain
+
+// Shared memory of one pair of warps (16 state rows): operands handed from
+// the chain warp to the output warp, the value rows, the output rows.
+template <int DK>
+struct PairSmem {
+  uint4 s_frag[DK / 16][32];  // S as A fragments, fp16
+  uint4 u_frag[2][4][32];     // u likewise, two chunks
+  float2 s_inv[32], u_inv[2][32];
+  alignas(16) uint8_t v[3][kC * 32];  // 16 value channels of the chunk's tokens
+  alignas(16) uint8_t o[kC * 32];
+};
+
+template <int DK, int PAIRS>
+struct ChainCfg {
+  // one CTA per SM: the ring takes what the pairs leave of its shared memory
+  static constexpr int kStageBytes = kKeyBlob<DK> + kHeadBlob;
+  static constexpr int kStages = PAIRS >= 4 && DK == 128 ? 2 : 3;
+  static constexpr int kThreads = 32 * (2 * PAIRS + 1);
+  static constexpr int kSmem =
+      kStages * kStageBytes + PAIRS * static_cast<int>(sizeof(PairSmem<DK>)) + 128;
+};
+
+// 16-byte pieces of the 32-byte token rows of v and o, permuted so that eight
+// rows' pieces of one column lie in different banks.
+__device__ __forceinline__ uint32_t row32_at(int row, int piece) {
+  return static_cast<uint32_t>(row * 32 + ((piece ^ ((row >> 2) & 1)) << 4));
+}
+
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(kFull, v, 1));
+  return fmaxf(v, __shfl_xor_sync(kFull, v, 2));
+}
+
+// A fragments (two terms) of columns 16 s .. + 15 of a 16-row accumulator.
+template <int N>
+__device__ __forceinline__ void split_frag(const float (&x)[N][4], int s, float m0, float m1,
+                                           uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  split_h2(x[2 * s][0], x[2 * s][1], m0, hi[0], lo[0]);
+  split_h2(x[2 * s][2], x[2 * s][3], m1, hi[1], lo[1]);
+  split_h2(x[2 * s + 1][0], x[2 * s + 1][1], m0, hi[2], lo[2]);
+  split_h2(x[2 * s + 1][2], x[2 * s + 1][3], m1, hi[3], lo[3]);
+}
+
+template <int N>
+__device__ __forceinline__ void row_max(const float (&x)[N][4], float &m0, float &m1) {
+  m0 = m1 = 0.0f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    m0 = fmaxf(m0, fmaxf(fabsf(x[n][0]), fabsf(x[n][1])));
+    m1 = fmaxf(m1, fmaxf(fabsf(x[n][2]), fabsf(x[n][3])));
+  }
+  m0 = quad_max(m0), m1 = quad_max(m1);
+}
+
+template <int DK, int PAIRS>
+__global__ void __launch_bounds__(ChainCfg<DK, PAIRS>::kThreads, 1)
+delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const uint8_t *ws,
+                   const uint8_t *ws_key, const uint8_t *ws_head, moe_bf16 *out, int64_t out_ld,
+                   unsigned long long budget_ns) {
+  using Cfg = ChainCfg<DK, PAIRS>;
+  constexpr int kStages = Cfg::kStages;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t *ring = smem_raw;
+  PairSmem<DK> *pairs = reinterpret_cast<PairSmem<DK> *>(ring + kStages * Cfg::kStageBytes);
+  uint64_t *full = reinterpret_cast<uint64_t *>(pairs + PAIRS), *empty = full + kStages;
+  __shared__ int abort_flag;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tiles = d.v_dim / (16 * PAIRS);
+  const int tile = blockIdx.x % tiles;
+  const int h = (blockIdx.x / tiles) % d.v_heads;
+  const int b = blockIdx.x / tiles / d.v_heads;
+  if (reinterpret_cast<const uint32_t *>(ws)[kFlagWord]) return;
+  const DeltaSeqRange r = delta_seq_range(seq, b);
+  if (!r.ok) return;
+  const int hk = h / (d.v_heads / d.qk_heads);
+  const int chunks = (r.len + kC - 1) / kC;
+  const int base = slot_base(seq, b);
+
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 2 * PAIRS);
+    }
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+
+  if (warp == 2 * PAIRS) {
+    // producer: one stage per chunk, keys and queries, then the head's part
+    if (lane == 0) {
+      int issued = 0;
+      for (; issued < chunks; ++issued) {
+        const int s = issued % kStages, use = issued / kStages;
+        if (use > 0 && !ptx::mbar_wait(&empty[s], (use - 1) & 1, &abort_flag, budget_ns)) break;
+        const uint32_t dst = ptx::smem_u32(ring + s * Cfg::kStageBytes);
+        const size_t at = static_cast<size_t>(base) + issued;
+        ptx::mbar_expect_tx(&full[s], Cfg::kStageBytes);
+        bulk_load(dst, ws_key + (at * d.qk_heads + hk) * kKeyBlob<DK>, kKeyBlob<DK>, &full[s]);
+        bulk_load(dst + kKeyBlob<DK>, ws_head + (at * d.v_heads + h) * kHeadBlob, kHeadBlob,
+                  &full[s]);
+      }
+      // copies in flight land before the CTA's shared memory is given up
+      int ignore = 0;
+      for (int c = max(0, issued - kStages); c < issued; ++c)
+        ptx::mbar_wait(&full[c % kStages], (c / kStages) & 1, &ignore, ptx::kDrainBudgetNs);
+      if (abort_flag) set_status(seq.status, MOE_DEV_TIMEOUT);
+    }
+    return;
+  }
+
+  const bool chain = warp < PAIRS;
+  const int pair = chain ? warp : warp - PAIRS;
+  PairSmem<DK> &ps = pairs[pair];
+  const int bar_s = 1 + 2 * pair, bar_u = 2 + 2 * pair;
+  const int dv0 = (tile * PAIRS + pair) * 16;
+  const int g = lane >> 2, t = lane & 3;
+  // a wait that gave up is not repeated: the loops below run to their end on
+  // whatever the ring holds, so that both warps of a pair pass every barrier
+  bool dead = false;
+  // B fragments of two n8 tiles from rows (plain) or columns (trans) of a tile
+  const int b_row = (lane & 7) + ((lane >> 4) << 3), b_piece = (lane >> 3) & 1;
+  const int bt_row = (lane & 7) + (((lane >> 3) & 1) << 3), bt_piece = lane >> 4;
+
+  if (chain) {
+    const int64_t at =
+        ((static_cast<int64_t>(r.slot) * d.v_heads + h) * d.v_dim + dv0 + g) * DK + 2 * t;
+    float S[DK / 8][4];
+    if (seq.state_in) {
+      const float *p = seq.state_in + at;
+#pragma unroll
+      for (int n = 0; n < DK / 8; ++n) {
+        const float2 a = *reinterpret_cast<const float2 *>(p + 8 * n);
+        const float2 c = *reinterpret_cast<const float2 *>(p + 8 * DK + 8 * n);
+        S[n][0] = a.x, S[n][1] = a.y, S[n][2] = c.x, S[n][3] = c.y;
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[n][e] = 0.0f;
+    }
+    const uint32_t v_smem = ptx::smem_u32(ps.v[0]);
+    const auto fetch_v = [&](int c) {  // this pair's 16 channels of chunk c, zeros past the end
+      if (c < chunks) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const int i = p * 16 + (lane >> 1), piece = lane & 1;
+          const bool live = c * kC + i < r.len;
+          const int64_t row = static_cast<int64_t>(r.start) + (live ? c * kC + i : 0);
+          cp_async16(v_smem + (c % 3) * kC * 32 + row32_at(i, piece),
+                     in.v + row * in.v_ld + h * d.v_dim + dv0 + piece * 8, live);
+        }
+      }
+      cp_async_commit();
+    };
+    fetch_v(0);
+    fetch_v(1);
+    for (int c = 0; c < chunks; ++c) {
+      const int st = c % kStages;
+      const uint32_t kt = ptx::smem_u32(ring + st * Cfg::kStageBytes);
+      const uint32_t tt = kt + kKeyBlob<DK>;
+      const float *vec =
+          reinterpret_cast<const float *>(ring + st * Cfg::kStageBytes + kKeyBlob<DK> + 3 * kTile);
+      fetch_v(c + 2);
+      float m0, m1, i0, i1, x0, x1;
+      row_max(S, x0, x1);
+      pow2_scale(x0, m0, i0);
+      pow2_scale(x1, m1, i1);
+      ps.s_inv[lane] = make_float2(i0, i1);
+      if (!dead)
+        dead = !ptx::mbar_wait(&full[st], (c / kStages) & 1, &abort_flag, budget_ns);
+      // X^T = S k^T (16 value channels x 64 tokens)
+      float X[8][4] = {};
+#pragma unroll
+      for (int s = 0; s < DK / 16; ++s) {
+        uint32_t hi[4], lo[4];
+        split_frag(S, s, m0, m1, hi, lo);
+        ps.s_frag[s][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          uint32_t bb[4];
+          ldsm4(bb, kt + tile_at<DK>(16 * np + b_row, 2 * s + b_piece));
+          mma16(X[2 * np], hi, bb[0], bb[1]);
+          mma16(X[2 * np + 1], hi, bb[2], bb[3]);
+          mma16(X[2 * np], lo, bb[0], bb[1]);
+          mma16(X[2 * np + 1], lo, bb[2], bb[3]);
+        }
+      }
+      bar_arrive(bar_s, 64);
+      // x_i = beta_i v_i - c_i (S k_i)
+      cp_async_wait<2>();
+      __syncwarp();
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t vv[4];
+        ldsm4_t(vv, v_smem + (c % 3) * kC * 32 +
+                        row32_at(16 * np + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int n = 2 * np + q;
+          const float2 be = *reinterpret_cast<const float2 *>(vec + kVecBeta * kC + 8 * n + 2 * t);
+          const float2 cc = *reinterpret_cast<const float2 *>(vec + kVecC * kC + 8 * n + 2 * t);
+          X[n][0] = be.x * bf16_lo(vv[2 * q]) - cc.x * (i0 * X[n][0]);
+          X[n][1] = be.y * bf16_hi(vv[2 * q]) - cc.y * (i0 * X[n][1]);
+          X[n][2] = be.x * bf16_lo(vv[2 * q + 1]) - cc.x * (i1 * X[n][2]);
+          X[n][3] = be.y * bf16_hi(vv[2 * q + 1]) - cc.y * (i1 * X[n][3]);
+        }
+      }
+      // u = T x: column tile n of u^T takes the tokens j up to its own
+      row_max(X, x0, x1);
+      pow2_scale(x0, m0, i0);
+      pow2_scale(x1, m1, i1);
+      float U[8][4] = {};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        uint32_t hi[4], lo[4];
+        split_frag(X, s, m0, m1, hi, lo);
+#pragma unroll
+        for (int np = s; np < 4; ++np) {
+          uint32_t th[4], tl[4];
+          const uint32_t a = tt + tile_at<kC>(16 * np + b_row, 2 * s + b_piece);
+          ldsm4(th, a);
+          ldsm4(tl, a + kTile);
+          mma16(U[2 * np], hi, tl[0], tl[1]);
+          mma16(U[2 * np + 1], hi, tl[2], tl[3]);
+          mma16(U[2 * np], lo, th[0], th[1]);
+          mma16(U[2 * np + 1], lo, th[2], th[3]);
+          mma16(U[2 * np], hi, th[0], th[1]);
+          mma16(U[2 * np + 1], hi, th[2], th[3]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const float2 ts = *reinterpret_cast<const float2 *>(vec + kVecT * kC + 8 * n + 2 * t);
+        U[n][0] *= i0 * ts.x, U[n][1] *= i0 * ts.y;
+        U[n][2] *= i1 * ts.x, U[n][3] *= i1 * ts.y;
+      }
+      // the output warp's copy
+      row_max(U, x0, x1);
+      pow2_scale(x0, m0, i0);
+      pow2_scale(x1, m1, i1);
+      ps.u_inv[c & 1][lane] = make_float2(i0, i1);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        ps.u_frag[c & 1][s][lane] = make_uint4(
+            h2_bits(__floats2half2_rn(U[2 * s][0] * m0, U[2 * s][1] * m0)),
+            h2_bits(__floats2half2_rn(U[2 * s][2] * m1, U[2 * s][3] * m1)),
+            h2_bits(__floats2half2_rn(U[2 * s + 1][0] * m0, U[2 * s + 1][1] * m0)),
+            h2_bits(__floats2half2_rn(U[2 * s + 1][2] * m1, U[2 * s + 1][3] * m1)));
+      // also says that the output warp has read this chunk's s_frag
+      bar_sync(bar_u, 64);
+      // S = gamma S + sum_j (Gamma_64,j u_j) k_j^T
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const float2 dd = *reinterpret_cast<const float2 *>(vec + kVecD * kC + 8 * n + 2 * t);
+        U[n][0] *= dd.x, U[n][1] *= dd.y, U[n][2] *= dd.x, U[n][3] *= dd.y;
+      }
+      row_max(U, x0, x1);
+      pow2_scale(x0, m0, i0);
+      pow2_scale(x1, m1, i1);
+      uint32_t wh[4][4], wl[4][4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) split_frag(U, s, m0, m1, wh[s], wl[s]);
+      const float gamma = vec[kVecMisc * kC];
+#pragma unroll
+      for (int np = 0; np < DK / 16; ++np) {
+        float acc[2][4] = {};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          uint32_t bb[4];
+          ldsm4_t(bb, kt + tile_at<DK>(16 * s + bt_row, 2 * np + bt_piece));
+          mma16(acc[0], wh[s], bb[0], bb[1]);
+          mma16(acc[1], wh[s], bb[2], bb[3]);
+          mma16(acc[0], wl[s], bb[0], bb[1]);
+          mma16(acc[1], wl[s], bb[2], bb[3]);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float(&a)[4] = S[2 * np + q];
+          a[0] = fmaf(gamma, a[0], i0 * acc[q][0]);
+          a[1] = fmaf(gamma, a[1], i0 * acc[q][1]);
+          a[2] = fmaf(gamma, a[2], i1 * acc[q][2]);
+          a[3] = fmaf(gamma, a[3], i1 * acc[q][3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&empty[st]);
+    }
+    cp_async_wait<0>();
+    if (seq.state_out) {
+      float *p = seq.state_out + at;
+#pragma unroll
+      for (int n = 0; n < DK / 8; ++n) {
+        *reinterpret_cast<float2 *>(p + 8 * n) = make_float2(S[n][0], S[n][1]);
+        *reinterpret_cast<float2 *>(p + 8 * DK + 8 * n) = make_float2(S[n][2], S[n][3]);
+      }
+    }
+    return;
+  }
+
+  // output warp: o_i = rho_i gamma_i (S q_i) + sum_j P_ij u_j
+  const uint32_t o_smem = ptx::smem_u32(ps.o);
+  for (int c = 0; c < chunks; ++c) {
+    const int st = c % kStages;
+    const uint32_t qt = ptx::smem_u32(ring + st * Cfg::kStageBytes) + kKeyBlob<DK> / 2;
+    const uint32_t pt = qt + kKeyBlob<DK> / 2 + 2 * kTile;
+    const float *vec =
+        reinterpret_cast<const float *>(ring + st * Cfg::kStageBytes + kKeyBlob<DK> + 3 * kTile);
+    if (!dead) dead = !ptx::mbar_wait(&full[st], (c / kStages) & 1, &abort_flag, budget_ns);
+    bar_sync(bar_s, 64);
+    const float2 si = ps.s_inv[lane];
+    float O[8][4] = {};
+#pragma unroll
+    for (int s = 0; s < DK / 16; ++s) {
+      const uint4 f = ps.s_frag[s][lane];
+      const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t bb[4];
+        ldsm4(bb, qt + tile_at<DK>(16 * np + b_row, 2 * s + b_piece));
+        mma16(O[2 * np], a, bb[0], bb[1]);
+        mma16(O[2 * np + 1], a, bb[2], bb[3]);
+      }
+    }
+    bar_sync(bar_u, 64);
+    const float2 ui = ps.u_inv[c & 1][lane];
+    float I[8][4] = {};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const uint4 f = ps.u_frag[c & 1][s][lane];
+      const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int np = s; np < 4; ++np) {
+        uint32_t bb[4];
+        ldsm4(bb, pt + tile_at<kC>(16 * np + b_row, 2 * s + b_piece));
+        mma16(I[2 * np], a, bb[0], bb[1]);
+        mma16(I[2 * np + 1], a, bb[2], bb[3]);
+      }
+    }
+#pragma unroll
+    for (int np = 0; np < 4; ++np) {
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int n = 2 * np + q;
+        const float2 oq = *reinterpret_cast<const float2 *>(vec + kVecO * kC + 8 * n + 2 * t);
+        const float2 pi = *reinterpret_cast<const float2 *>(vec + kVecP * kC + 8 * n + 2 * t);
+        w[2 * q] = pack_bf16x2((si.x * O[n][0]) * oq.x + (ui.x * I[n][0]) * pi.x,
+                               (si.x * O[n][1]) * oq.y + (ui.x * I[n][1]) * pi.y);
+        w[2 * q + 1] = pack_bf16x2((si.y * O[n][2]) * oq.x + (ui.y * I[n][2]) * pi.x,
+                                   (si.y * O[n][3]) * oq.y + (ui.y * I[n][3]) * pi.y);
+      }
+      // transposed back: token rows of 16 channels
+      stsm4_t(o_smem + row32_at(16 * np + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1), w[0],
+              w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&empty[st]);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int i = p * 16 + (lane >> 1), piece = lane & 1;
+      if (c * kC + i < r.len)
+        *reinterpret_cast<uint4 *>(
+            out + (static_cast<int64_t>(r.start) + c * kC + i) * out_ld + h * d.v_dim + dv0 +
+            piece * 8) = *reinterpret_cast<const uint4 *>(ps.o + row32_at(i, piece));
+    }
+    __syncwarp();
+  }
+}
+
+template <int DK, int PAIRS>
+cudaError_t launch_chain(const moe_delta_dims &d, const moe_delta_inputs &in, const DeltaSeqs &seq,
+                         const uint8_t *ws, const uint8_t *ws_key, const uint8_t *ws_head,
+                         moe_bf16 *out, int64_t out_ld, cudaStream_t s) {
+  using Cfg = ChainCfg<DK, PAIRS>;
+  static_assert(Cfg::kSmem <= 227 * 1024 - 16, "shared memory of one SM");
+  cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<DK, PAIRS>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / (16 * PAIRS));
+  delta_chain_kernel<DK, PAIRS><<<static_cast<unsigned>(grid), Cfg::kThreads, Cfg::kSmem, s>>>(
+      d, in, seq, ws, ws_key, ws_head, out, out_ld, tc_wait_budget_ns());
+  return cudaGetLastError();
+}
+
+template <int DK>
+cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const DeltaSeqs &seq,
+                   uint8_t *ws, moe_bf16 *out, int64_t out_ld, cudaStream_t s) {
+  const size_t slots = static_cast<size_t>(seq.N) / kC + seq.B;
+  uint8_t *ws_key = ws + kHeader;
+  uint8_t *ws_head = ws_key + slots * d.qk_heads * kKeyBlob<DK>;
+  constexpr int kSmem = sizeof(PrepSmem<DK>);
+  cudaError_t e = cudaFuncSetAttribute(delta_prep_kernel<DK>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(slots), d.v_heads);
+  delta_prep_kernel<DK><<<grid, kPrepThreads, kSmem, s>>>(d, in, seq, ws, ws_key, ws_head);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int64_t groups = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / 16);
+  if (groups <= 2 * 152)
+    return launch_chain<DK, 2>(d, in, seq, ws, ws_key, ws_head, out, out_ld, s);
+  return launch_chain<DK, 4>(d, in, seq, ws, ws_key, ws_head, out, out_ld, s);
+}
+
+}  // namespace
+
+size_t delta_chunk_workspace(const moe_delta_dims &d, int N, int B) {
+  const size_t slots = static_cast<size_t>(N) / kC + B;
+  const size_t key = d.qk_dim == 128 ? kKeyBlob<128> : kKeyBlob<64>;
+  return kHeader + slots * (d.qk_heads * key + static_cast<size_t>(d.v_heads) * kHeadBlob);
+}
+
+cudaError_t launch_delta_chunk(const moe_delta_dims &d, const moe_delta_inputs &in,
+                               const DeltaSeqs &seq, void *ws, moe_bf16 *out, int64_t out_ld,
+                               cudaStream_t s) {
+  return d.qk_dim == 128 ? launch<128>(d, in, seq, static_cast<uint8_t *>(ws), out, out_ld, s)
+                         : launch<64>(d, in, seq, static_cast<uint8_t *>(ws), out, out_ld, s);
+}
+
+}  // namespace moe

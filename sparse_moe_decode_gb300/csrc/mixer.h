@@ -26,6 +26,12 @@ cudaError_t launch_delta_recurrent(const moe_delta_dims &d, const moe_delta_inpu
                                    const DeltaSeqs &seq, moe_bf16 *out, int64_t out_ld,
                                    cudaStream_t s);
 
+// In chunks of 64 tokens; ws holds delta_chunk_workspace bytes.
+size_t delta_chunk_workspace(const moe_delta_dims &d, int N, int B);
+cudaError_t launch_delta_chunk(const moe_delta_dims &d, const moe_delta_inputs &in,
+                               const DeltaSeqs &seq, void *ws, moe_bf16 *out, int64_t out_ld,
+                               cudaStream_t s);
+
 // a.rows > 0; `vec8`: every row starts on a 16-byte boundary and width is a
 // multiple of 8.
 cudaError_t launch_norm_gate_residual(const moe_norm_args &a, bool vec8, cudaStream_t s);

@@ -118,7 +118,7 @@ size_t moe_delta_workspace_bytes(const moe_delta_dims *dims, int N, int B) {
   if (check_delta_dims(dims) != MOE_OK || N < 0 || N > kDeltaMaxTokens || B < 0 ||
       B > kDeltaMaxSeqs)
     return 0;
-  return 256;
+  return delta_chunk_workspace(*dims, N, B);
 }
 
 moe_status moe_delta_chunk(const moe_delta_dims *dims, const moe_delta_inputs *in, int N,
@@ -137,8 +137,8 @@ moe_status moe_delta_chunk(const moe_delta_dims *dims, const moe_delta_inputs *i
   if (B == 0) return MOE_OK;
   const DeltaSeqs seq = delta_seqs(cu_seqlens, N, B, N, slots, n_slots, state_in, state_out,
                                    workspace);
-  return cuda_status(launch_delta_recurrent(*dims, *in, seq, out, out_ld,
-                                            static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_delta_chunk(*dims, *in, seq, workspace, out, out_ld,
+                                        static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_delta_step(const moe_delta_dims *dims, const moe_delta_inputs *in, int B, int T,

@@ -217,19 +217,24 @@ def test_skipped_and_bad_sequences(env, api):
 @pytest.mark.parametrize("cu", [[0, 100, 50, 120], [-5, 20, 60, 120], [0, 40, 80, 121],
                                 [0, 40, 1 << 30, 120]])
 def test_bad_bounds_are_skipped(env, cu):
-    """Bounds that are not 0 <= start <= end <= N set the status bit, and the
-    sequences that have them are not touched."""
+    """Bounds that are not 0 <= start <= end <= N set the status bit, and
+    nothing is written."""
     import torch
     moe, dev = env
     heads, dims = (1, 2), (64, 64)
     s = make(env, 120, heads, dims)
     m = mixer(env, heads, dims, 120, 3)
     S1 = torch.full((3, 2, 64, 64), 7.0, device=dev)
-    m.chunk(**s, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=dev), state_out=S1)
+    out = torch.full((120, 2, 64), 3.0, dtype=torch.bfloat16, device=dev)
+    m.chunk(**s, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=dev), state_out=S1, out=out)
     assert m.status() == moe.DEV_BAD_INDEX
-    for i in range(3):
-        if not 0 <= cu[i] <= cu[i + 1] <= 120:
-            assert (S1[i] == 7.0).all()
+    assert (S1 == 7.0).all() and (out == 3.0).all()
+    # the next call is not affected
+    m.clear_status()
+    m.chunk(**s, cu_seqlens=cu_of(env, [50, 0, 70]), state_out=S1, out=out)
+    assert m.status() == 0
+    check_seq(s, slice(0, 50), torch.zeros_like(S1[0]), out, S1[0], dims)
+    check_seq(s, slice(50, 120), torch.zeros_like(S1[0]), out, S1[2], dims)
 
 
 @pytest.mark.parametrize("dims", [(64, 64), (64, 128), (128, 64), (128, 128)])
@@ -293,6 +298,14 @@ def test_empty_calls(env):
     assert out.shape == (0, 4, 128) and torch.equal(S1, pool)  # no tokens: the state as it was
     m.chunk(**s, cu_seqlens=cu_of(env, []), state_in=pool, state_out=S1)
     m.step(**s, state_in=pool, state_out=S1, tokens=0)
+
+
+def test_workspace_is_checked(env):
+    moe, _ = env
+    big = make(env, 4096)
+    m = mixer(env, (2, 4), (128, 128), 8, 1)
+    with pytest.raises(moe.MoEError):
+        m.chunk(**big, cu_seqlens=cu_of(env, [4096]))  # more rows than max_tokens
 
 
 def test_streams_and_graphs(env):
