@@ -371,9 +371,22 @@ class MoEBlock:
         moe_clear_status(self.workspace, stream)
 
 
-def _require(ok, where):
-    if not ok:
-        raise MoEError(MOE_ERR_INVALID_ARG, where)
+def _invalid(where):
+    raise MoEError(MOE_ERR_INVALID_ARG, where)
+
+
+_raw_stream = None
+
+
+def _stream_of(stream, device_index):
+    """The given stream, or the current one of the tensors' device."""
+    global _raw_stream
+    if stream is not None:
+        return _s(stream)
+    if _raw_stream is None:
+        import torch
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+    return _raw_stream(device_index)
 
 
 class GatedDelta:
@@ -398,65 +411,86 @@ class GatedDelta:
         # only the status word must start at zero
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         self.workspace[:256].zero_()
+        self._device = self.workspace.device
+        self._index = self.workspace.get_device()
+        self._ws = self.workspace.data_ptr()
+        self._dims_ref = ctypes.byref(self.dims)
+        # row shapes, and the strides inside a row that a call's tensors must have
+        k, v = (qk_heads, qk_dim), (v_heads, v_dim)
+        self._rows = tuple((torch.bfloat16, s, (s[1], 1)) for s in (k, k, v)) + tuple(
+            (torch.float32, (v_heads,), (1,)) for _ in range(2))
+        self._out_row = (torch.bfloat16, v, (v_dim, 1))
+        self._state = (v_heads, v_dim, qk_dim)
+        self._state_strides = (v_heads * v_dim * qk_dim, v_dim * qk_dim, qk_dim, 1)
+        self._f32, self._i32 = torch.float32, torch.int32
+        self._empty = torch.empty
 
-    def _inputs(self, q, k, v, g, beta, where):
-        import torch
-        d, n = self.dims, q.shape[0]
-        for x, dtype, shape in ((q, torch.bfloat16, (n, d.qk_heads, d.qk_dim)),
-                                (k, torch.bfloat16, (n, d.qk_heads, d.qk_dim)),
-                                (v, torch.bfloat16, (n, d.v_heads, d.v_dim)),
-                                (g, torch.float32, (n, d.v_heads)),
-                                (beta, torch.float32, (n, d.v_heads))):
-            _require(x.dtype == dtype and tuple(x.shape) == shape and x.is_cuda and
-                     (n == 0 or x[0].is_contiguous()), where)
+    def _row_ld(self, x, n, spec, where):
+        """The row stride of x, which must be [n, *row shape] on this device."""
+        dtype, row, inner = spec
+        shape, strides = x.shape, x.stride()
+        if (x.dtype is not dtype or x.get_device() != self._index or shape[0] != n or
+                shape[1:] != row):
+            _invalid(where)
+        if strides[1:] != inner and n and not x[0].is_contiguous():
+            _invalid(where)
         # a single row has no stride of its own
-        ld = [x.stride(0) if n > 1 else x[:1].numel() for x in (q, k, v, g, beta)]
-        return n, DeltaInputs(_a(q), _a(k), _a(v), _a(g), _a(beta), *ld)
+        return strides[0] if n > 1 else row[0] * inner[0]
 
-    def _states(self, state_in, state_out, slots, B, where):
-        import torch
-        d, n_slots = self.dims, B
+    def _call(self, fn, where, q, k, v, g, beta, lead, cu, B, slots, state_in, state_out, out,
+              stream):
+        n = q.shape[0]
+        if self._index < 0:  # not a CUDA device
+            _invalid(where)
+        rows = [self._row_ld(x, n, spec, where)
+                for x, spec in zip((q, k, v, g, beta), self._rows)]
+        inputs = DeltaInputs(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                             beta.data_ptr(), *rows)
+        n_slots = B
         for x in (state_in, state_out):
             if x is not None:
                 n_slots = x.shape[0]
-                _require(x.dtype == torch.float32 and x.is_cuda and x.is_contiguous() and
-                         tuple(x.shape[1:]) == (d.v_heads, d.v_dim, d.qk_dim), where)
-        _require(state_in is None or state_out is None or
-                 state_in.shape[0] == state_out.shape[0], where)
-        _require(slots is None or (slots.dtype == torch.int32 and slots.is_cuda and
-                                   slots.is_contiguous() and tuple(slots.shape) == (B,)), where)
-        if slots is not None and state_in is None and state_out is None:
-            n_slots = 1 << 30  # no state to be out of
-        return n_slots
-
-    def _out(self, out, n, where):
-        import torch
-        d = self.dims
+                if (x.dtype is not self._f32 or x.get_device() != self._index or
+                        x.shape[1:] != self._state or
+                        (x.stride() != self._state_strides and not x.is_contiguous())):
+                    _invalid(where)
+        if state_in is not None and state_out is not None and state_in.shape[0] != n_slots:
+            _invalid(where)
+        if slots is not None:
+            if (slots.dtype is not self._i32 or slots.get_device() != self._index or
+                    slots.shape != (B,) or not slots.is_contiguous()):
+                _invalid(where)
+            if state_in is None and state_out is None:
+                n_slots = 1 << 30  # no state to be out of
         if out is None:
-            out = torch.empty((n, d.v_heads, d.v_dim), dtype=torch.bfloat16,
-                              device=self.workspace.device)
-        _require(out.dtype == torch.bfloat16 and tuple(out.shape) == (n, d.v_heads, d.v_dim) and
-                 out.is_cuda and (n == 0 or out[0].is_contiguous()), where)
-        return out, out.stride(0) if n > 1 else d.v_heads * d.v_dim
+            out = self._empty((n,) + self._state[:2], dtype=self._out_row[0], device=self._device)
+            out_ld = self._state[0] * self._state[1]
+        else:
+            out_ld = self._row_ld(out, n, self._out_row, where)
+        st = fn(self._dims_ref, ctypes.byref(inputs), *lead,
+                None if cu is None else cu.data_ptr(), B,
+                None if slots is None else slots.data_ptr(), n_slots,
+                None if state_in is None else state_in.data_ptr(),
+                None if state_out is None else state_out.data_ptr(), out.data_ptr(), out_ld,
+                self._ws, self.ws_bytes, _stream_of(stream, self._index))
+        if st != MOE_OK:
+            raise MoEError(st, where)
+        return out
 
     def chunk(self, q, k, v, g, beta, cu_seqlens=None, state_in=None, state_out=None, slots=None,
               out=None, stream=None):
         """Whole prompts: the rows of len(cu_seqlens) - 1 sequences one after
         another (one sequence without ``cu_seqlens``).  Returns out [N][v_heads][v_dim]."""
-        import torch
         where = "GatedDelta.chunk"
-        n, inputs = self._inputs(q, k, v, g, beta, where)
         B = 1
         if cu_seqlens is not None:
-            _require(cu_seqlens.dtype == torch.int32 and cu_seqlens.is_cuda and
-                     cu_seqlens.is_contiguous() and cu_seqlens.dim() == 1 and
-                     cu_seqlens.shape[0] >= 1, where)
+            if (cu_seqlens.dtype is not self._i32 or cu_seqlens.get_device() != self._index or
+                    cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or
+                    not cu_seqlens.is_contiguous()):
+                _invalid(where)
             B = cu_seqlens.shape[0] - 1
-        n_slots = self._states(state_in, state_out, slots, B, where)
-        out, out_ld = self._out(out, n, where)
-        moe_delta_chunk(self.dims, inputs, n, cu_seqlens, B, slots, n_slots, state_in, state_out,
-                        out, out_ld, self.workspace, self.ws_bytes, stream)
-        return out
+        return self._call(_lib_fn("moe_delta_chunk"), where, q, k, v, g, beta, (q.shape[0],),
+                          cu_seqlens, B, slots, state_in, state_out, out, stream)
 
     def step(self, q, k, v, g, beta, state_in=None, state_out=None, slots=None, tokens=None,
              out=None, stream=None):
@@ -464,19 +498,17 @@ class GatedDelta:
         sequence (by default as many as make ``slots``, or else the states,
         one per sequence).  Returns out [rows][v_heads][v_dim]."""
         where = "GatedDelta.step"
-        n, inputs = self._inputs(q, k, v, g, beta, where)
+        n = q.shape[0]
         if tokens is None:
             lead = slots if slots is not None else state_in if state_in is not None else state_out
             B = n if lead is None else lead.shape[0]
             tokens = n // B if B else 0
         else:
-            B = n // tokens if tokens else 0
-        _require(B * tokens == n, where)
-        n_slots = self._states(state_in, state_out, slots, B, where)
-        out, out_ld = self._out(out, n, where)
-        moe_delta_step(self.dims, inputs, B, tokens, slots, n_slots, state_in, state_out, out,
-                       out_ld, self.workspace, self.ws_bytes, stream)
-        return out
+            B = n // tokens if tokens > 0 else 0
+        if B * tokens != n:
+            _invalid(where)
+        return self._call(_step_fn, where, q, k, v, g, beta, (tokens,), None, B, slots, state_in,
+                          state_out, out, stream)
 
     def status(self, stream=None) -> int:
         return moe_read_status(self.workspace, stream)
@@ -485,13 +517,27 @@ class GatedDelta:
         moe_clear_status(self.workspace, stream)
 
 
-def _rows_of(t, shape, where):
-    """(inner, stride) of a bf16 tensor [rows][width] or [tokens][heads][width]
-    whose first stride alone is free."""
-    import torch
-    _require(t.dtype == torch.bfloat16 and t.is_cuda and tuple(t.shape) == tuple(shape) and
-             (t.shape[0] == 0 or t[0].is_contiguous()), where)
-    return t.stride(0) if t.shape[0] > 1 else t[:1].numel()
+def _lib_fn(name):
+    return getattr(_lib if _lib is not None else lib(), name)
+
+
+def _step_fn(dims, inputs, T, _cu, B, *rest):
+    return _lib_fn("moe_delta_step")(dims, inputs, B, T, *rest)
+
+
+def _norm_ld(t, shape, bf16, index, where):
+    """The first stride of a bf16 tensor of this shape, whose rows are whole."""
+    if t.dtype is not bf16 or t.get_device() != index or t.shape != shape:
+        _invalid(where)
+    if shape[0] > 1:
+        strides = t.stride()
+        if (strides[-1] != 1 and shape[-1] > 1) or (len(shape) == 3 and shape[1] > 1 and
+                                                   strides[1] != shape[2]):
+            _invalid(where)
+        return strides[0]
+    if shape[0] and not t[0].is_contiguous():
+        _invalid(where)
+    return shape[-1] * (shape[1] if len(shape) == 3 else 1)
 
 
 def norm_gate_residual(x, gamma_post=None, gate=None, gate_act="sigmoid", resid=None,
@@ -506,39 +552,47 @@ def norm_gate_residual(x, gamma_post=None, gate=None, gate_act="sigmoid", resid=
     given as an output."""
     import torch
     where = "norm_gate_residual"
-    _require(x.dim() in (2, 3) and x.shape[-1] > 0 and gate_act in GATE_ACTS, where)
-    width = x.shape[-1]
-    inner = x.shape[1] if x.dim() == 3 else 1
-    _require(inner > 0, where)
-    a = NormArgs(rows=x.shape[0] * inner, width=width, inner=inner, res_scale=res_scale, eps=eps,
-                 gate_act=GATE_ACTS[gate_act], gate_kind=GATE_NONE)
-    a.x, a.x_ld = _a(x), _rows_of(x, x.shape, where)
-    for name, gamma in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
+    bf16, index, shape = torch.bfloat16, x.get_device(), x.shape
+    act = GATE_ACTS.get(gate_act)
+    if act is None or index < 0 or len(shape) not in (2, 3) or 0 in shape[1:]:
+        _invalid(where)
+    width = shape[-1]
+    inner = shape[1] if len(shape) == 3 else 1
+    x_ld = _norm_ld(x, shape, bf16, index, where)
+    gammas = [None, None]
+    for i, gamma in enumerate((gamma_post, gamma_pre)):
         if gamma is not None:
-            _require(gamma.dtype == torch.bfloat16 and gamma.is_cuda and
-                     tuple(gamma.shape) == (width,) and gamma.is_contiguous(), where)
-            setattr(a, name, _a(gamma))
+            if (gamma.dtype is not bf16 or gamma.get_device() != index or
+                    gamma.shape != (width,) or not gamma.is_contiguous()):
+                _invalid(where)
+            gammas[i] = gamma.data_ptr()
+    kind = gate_ld = 0
     if gate is not None:
         if gate.dim() == 1:
-            _require(gate.dtype == torch.bfloat16 and gate.is_cuda and
-                     tuple(gate.shape) == (width,) and gate.is_contiguous(), where)
-            a.gate_kind = GATE_CHANNEL
-        elif tuple(gate.shape) == tuple(x.shape):
-            a.gate_kind, a.gate_ld = GATE_ELEMENT, _rows_of(gate, x.shape, where)
+            kind = GATE_CHANNEL
+            if (gate.dtype is not bf16 or gate.get_device() != index or gate.shape != (width,) or
+                    not gate.is_contiguous()):
+                _invalid(where)
         else:
-            a.gate_kind = GATE_ROW
-            a.gate_ld = _rows_of(gate, tuple(x.shape[:-1]) + (1,), where)
-        a.gate = _a(gate)
-    if resid is not None:
-        a.resid_in, a.resid_in_ld = _a(resid), _rows_of(resid, x.shape, where)
+            kind = GATE_ELEMENT if gate.shape == shape else GATE_ROW
+            gate_ld = _norm_ld(gate, shape if kind == GATE_ELEMENT else shape[:-1] + (1,), bf16,
+                               index, where)
     if resid_out is None:
-        resid_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    a.resid_out, a.resid_out_ld = _a(resid_out), _rows_of(resid_out, x.shape, where)
-    if gamma_pre is not None:
-        if x_next is None:
-            x_next = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        a.x_next, a.x_next_ld = _a(x_next), _rows_of(x_next, x.shape, where)
-    else:
-        _require(x_next is None, where)
-    moe_norm_gate_residual(a, stream)
+        resid_out = torch.empty(shape, dtype=bf16, device=x.device)
+    if gamma_pre is None:
+        if x_next is not None:
+            _invalid(where)
+    elif x_next is None:
+        x_next = torch.empty(shape, dtype=bf16, device=x.device)
+    a = NormArgs(
+        shape[0] * inner, width, inner, x.data_ptr(), gammas[0],
+        None if gate is None else gate.data_ptr(), None if resid is None else resid.data_ptr(),
+        gammas[1], resid_out.data_ptr(), None if x_next is None else x_next.data_ptr(), x_ld,
+        gate_ld, 0 if resid is None else _norm_ld(resid, shape, bf16, index, where),
+        _norm_ld(resid_out, shape, bf16, index, where),
+        0 if x_next is None else _norm_ld(x_next, shape, bf16, index, where), kind, act,
+        res_scale, eps)
+    st = _lib_fn("moe_norm_gate_residual")(ctypes.byref(a), _stream_of(stream, index))
+    if st != MOE_OK:
+        raise MoEError(st, where)
     return resid_out, x_next

@@ -28,6 +28,8 @@
 // and u as single fp16 terms (2^-11, an eighth of the rounding to come).
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "delta_mma.cuh"
 #include "delta_seq.cuh"
@@ -72,7 +74,7 @@ struct PrepSmem {
   alignas(128) uint8_t key[kKeyBlob<DK>];
   alignas(128) uint8_t head[kHeadBlob];
   float m[kC * kLd];  // below the diagonal L, above it T transposed
-  float kappa[kC], rho[kC], beta[kC], ghi[kC], glo[kC], half_max[2][kC];
+  float kappa[kC], rho[kC], beta[kC], ghi[kC], glo[kC], half_max[2][kC], half_sum[2][kC];
 };
 
 // T(i, j) of the work matrix: stored transposed above the diagonal.
@@ -220,7 +222,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t 
       vec[kVecO * kC + i + j] = expf(hi32);                             // gamma_i
       vec[kVecD * kC + i + j] = expf(static_cast<float>(total - s[j]));  // Gamma_64,i
     }
-    if (lane == 0) vec[kVecMisc * kC] = expf(static_cast<float>(total));
+    if (lane == 0) vec[kVecMisc * kC] = expf(static_cast<float>(total));  // gamma_64
   }
   __syncthreads();
 
@@ -280,12 +282,25 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t 
             __floats2half2_rn(qk[n][2 * half] * mult, qk[n][2 * half + 1] * mult);
     }
   }
-  if (tid < kC) {
-    vec[kVecBeta * kC + tid] = sm.beta[tid];
-    const float gamma = vec[kVecO * kC + tid];
-    vec[kVecC * kC + tid] = sm.beta[tid] * gamma * sm.kappa[tid];
-    vec[kVecO * kC + tid] = sm.rho[tid] * gamma;
-    vec[kVecD * kC + tid] *= sm.kappa[tid];
+  if (warp == 0) {
+    // the factors of the tokens; the update's, Gamma_64,j kappa_j, over a
+    // power of two not below the largest
+    float dmax = 0.0f;
+#pragma unroll
+    for (int i = lane; i < kC; i += 32) {
+      const float gamma = vec[kVecO * kC + i];
+      vec[kVecBeta * kC + i] = sm.beta[i];
+      vec[kVecC * kC + i] = -sm.beta[i] * gamma * sm.kappa[i];
+      vec[kVecO * kC + i] = sm.rho[i] * gamma;
+      dmax = fmaxf(dmax, vec[kVecD * kC + i] *= sm.kappa[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dmax = fmaxf(dmax, __shfl_xor_sync(kFull, dmax, o));
+    float up, down;
+    pow2_above(dmax, up, down);
+    vec[kVecD * kC + lane] *= down;
+    vec[kVecD * kC + lane + 32] *= down;
+    if (lane == 0) vec[kVecMisc * kC + 2] = up;
   }
   __syncwarp();
 
@@ -340,24 +355,37 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t 
     put(acc, r0, c0, -1.0f);
     __syncthreads();
   }
-  // T's rows as two fp16 terms
+  // T's rows as two fp16 terms, and a power of two above every row's sum
   {
     const int i = tid & 63, j0 = (tid >> 6) * 32;
-    float mx = j0 <= i && i < j0 + 32 ? 1.0f : 0.0f;
-    for (int j = j0; j < min(i, j0 + 32); ++j) mx = fmaxf(mx, fabsf(sm.m[j * kLd + i]));
+    float mx = 0.0f, sum = 0.0f;
+#pragma unroll 8
+    for (int j = j0; j < j0 + 32; ++j) {
+      const float v = fabsf(t_at(sm.m, i, j));
+      mx = fmaxf(mx, v);
+      sum += v;
+    }
     sm.half_max[tid >> 6][i] = mx;
+    sm.half_sum[tid >> 6][i] = sum;
     __syncthreads();
     mx = fmaxf(sm.half_max[0][i], sm.half_max[1][i]);
-    float mult, inv;
+    sum = fmaxf(sm.half_sum[0][lane] + sm.half_sum[1][lane],
+                sm.half_sum[0][lane + 32] + sm.half_sum[1][lane + 32]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum = fmaxf(sum, __shfl_xor_sync(kFull, sum, o));
+    float mult, inv, up, down;
+    pow2_above(sum, up, down);
     pow2_scale(mx, mult, inv);
-    if (tid < kC) vec[kVecT * kC + i] = inv;
+    if (tid < kC) vec[kVecT * kC + i] = inv * down;
+    if (tid == 0) vec[kVecMisc * kC + 1] = up;
+    const float2 m2 = make_float2(mult, mult);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       uint32_t hi32[4], lo32[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int j = j0 + 8 * p + 2 * e;
-        split_h2(t_at(sm.m, i, j), t_at(sm.m, i, j + 1), mult, hi32[e], lo32[e]);
+        split_h2(mul2(make_float2(t_at(sm.m, i, j), t_at(sm.m, i, j + 1)), m2), hi32[e], lo32[e]);
       }
       const uint32_t at = tile_at<kC>(i, j0 / 8 + p);
       *reinterpret_cast<uint4 *>(sm.head + at) = make_uint4(hi32[0], hi32[1], hi32[2], hi32[3]);
@@ -379,25 +407,28 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t 
 
 // ------------------------------------------------------------------ chain
 
-// Shared memory of one pair of warps (16 state rows): operands handed from
-// the chain warp to the output warp, the value rows, the output rows.
+// Shared memory of one group of three warps (16 state rows): what the two
+// chain warps exchange, what they hand to the output warp, the value rows and
+// the output rows.
 template <int DK>
-struct PairSmem {
-  uint4 s_frag[DK / 16][32];  // S as A fragments, fp16
-  uint4 u_frag[2][4][32];     // u likewise, two chunks
-  float2 s_inv[32], u_inv[2][32];
+struct GroupSmem {
+  uint4 s_frag[DK / 16][32];    // S as A fragments, fp16
+  uint4 u_frag[4][32];          // u likewise
+  float4 x_part[2][8][32];      // each half's S k^T
+  uint4 w_frag[4][2][32];       // the update's A fragments, two terms
+  float2 s_inv[2][32], u_inv[32];
   alignas(16) uint8_t v[3][kC * 32];  // 16 value channels of the chunk's tokens
   alignas(16) uint8_t o[kC * 32];
 };
 
-template <int DK, int PAIRS>
+template <int DK, int GROUPS>
 struct ChainCfg {
-  // one CTA per SM: the ring takes what the pairs leave of its shared memory
+  // one CTA per SM: the ring takes what the groups leave of its shared memory
   static constexpr int kStageBytes = kKeyBlob<DK> + kHeadBlob;
-  static constexpr int kStages = PAIRS >= 4 && DK == 128 ? 2 : 3;
-  static constexpr int kThreads = 32 * (2 * PAIRS + 1);
+  static constexpr int kStages = GROUPS >= 4 && DK == 128 ? 2 : 3;
+  static constexpr int kThreads = 32 * (3 * GROUPS + 1);
   static constexpr int kSmem =
-      kStages * kStageBytes + PAIRS * static_cast<int>(sizeof(PairSmem<DK>)) + 128;
+      kStages * kStageBytes + GROUPS * static_cast<int>(sizeof(GroupSmem<DK>)) + 64;
 };
 
 // 16-byte pieces of the 32-byte token rows of v and o, permuted so that eight
@@ -411,42 +442,57 @@ __device__ __forceinline__ float quad_max(float v) {
   return fmaxf(v, __shfl_xor_sync(kFull, v, 2));
 }
 
-// A fragments (two terms) of columns 16 s .. + 15 of a 16-row accumulator.
-template <int N>
-__device__ __forceinline__ void split_frag(const float (&x)[N][4], int s, float m0, float m1,
-                                           uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-  split_h2(x[2 * s][0], x[2 * s][1], m0, hi[0], lo[0]);
-  split_h2(x[2 * s][2], x[2 * s][3], m1, hi[1], lo[1]);
-  split_h2(x[2 * s + 1][0], x[2 * s + 1][1], m0, hi[2], lo[2]);
-  split_h2(x[2 * s + 1][2], x[2 * s + 1][3], m1, hi[3], lo[3]);
+// An accumulator tile of 16 rows x 8 columns: rows lane / 4 (top) and
+// lane / 4 + 8 (low), columns 2 (lane % 4), + 1.
+struct Acc {
+  float2 top, low;
+};
+
+__device__ __forceinline__ void mma16(Acc &c, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  float f[4] = {c.top.x, c.top.y, c.low.x, c.low.y};
+  ::moe::mma16(f, a, b0, b1);
+  c.top = make_float2(f[0], f[1]), c.low = make_float2(f[2], f[3]);
 }
 
+// A fragments (two terms) of the 16 columns of tiles p and q, scaled by rows.
+__device__ __forceinline__ void split_frag(const Acc &p, const Acc &q, float2 m0, float2 m1,
+                                           uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  split_h2(mul2(p.top, m0), hi[0], lo[0]);
+  split_h2(mul2(p.low, m1), hi[1], lo[1]);
+  split_h2(mul2(q.top, m0), hi[2], lo[2]);
+  split_h2(mul2(q.low, m1), hi[3], lo[3]);
+}
+
+// Power-of-two scales of the two rows a lane holds, from N tiles.
 template <int N>
-__device__ __forceinline__ void row_max(const float (&x)[N][4], float &m0, float &m1) {
-  m0 = m1 = 0.0f;
+__device__ __forceinline__ void row_scales(const Acc (&x)[N], float &m0, float &m1, float &i0,
+                                           float &i1) {
+  float a = 0.0f, b = 0.0f;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    m0 = fmaxf(m0, fmaxf(fabsf(x[n][0]), fabsf(x[n][1])));
-    m1 = fmaxf(m1, fmaxf(fabsf(x[n][2]), fabsf(x[n][3])));
+    a = max3_abs(a, x[n].top.x, x[n].top.y);
+    b = max3_abs(b, x[n].low.x, x[n].low.y);
   }
-  m0 = quad_max(m0), m1 = quad_max(m1);
+  pow2_scale(quad_max(a), m0, i0);
+  pow2_scale(quad_max(b), m1, i1);
 }
 
-template <int DK, int PAIRS>
-__global__ void __launch_bounds__(ChainCfg<DK, PAIRS>::kThreads, 1)
+template <int DK, int GROUPS>
+__global__ void __launch_bounds__(ChainCfg<DK, GROUPS>::kThreads, 1)
 delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const uint8_t *ws,
                    const uint8_t *ws_key, const uint8_t *ws_head, moe_bf16 *out, int64_t out_ld,
                    unsigned long long budget_ns) {
-  using Cfg = ChainCfg<DK, PAIRS>;
+  using Cfg = ChainCfg<DK, GROUPS>;
   constexpr int kStages = Cfg::kStages;
+  constexpr int kHalf = DK / 2;  // key channels of a chain warp
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t *ring = smem_raw;
-  PairSmem<DK> *pairs = reinterpret_cast<PairSmem<DK> *>(ring + kStages * Cfg::kStageBytes);
-  uint64_t *full = reinterpret_cast<uint64_t *>(pairs + PAIRS), *empty = full + kStages;
-  __shared__ int abort_flag;
+  GroupSmem<DK> *groups = reinterpret_cast<GroupSmem<DK> *>(ring + kStages * Cfg::kStageBytes);
+  uint64_t *full = reinterpret_cast<uint64_t *>(groups + GROUPS), *empty = full + kStages;
+  int *abort_flag = reinterpret_cast<int *>(empty + kStages);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tiles = d.v_dim / (16 * PAIRS);
+  const int tiles = d.v_dim / (16 * GROUPS);
   const int tile = blockIdx.x % tiles;
   const int h = (blockIdx.x / tiles) % d.v_heads;
   const int b = blockIdx.x / tiles / d.v_heads;
@@ -458,22 +504,22 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   const int base = slot_base(seq, b);
 
   if (tid == 0) {
-    abort_flag = 0;
+    *abort_flag = 0;
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], 2 * PAIRS);
+      ptx::mbar_init(&empty[s], 3 * GROUPS);
     }
     ptx::fence_mbar_init();
   }
   __syncthreads();
 
-  if (warp == 2 * PAIRS) {
+  if (warp == 3 * GROUPS) {
     // producer: one stage per chunk, keys and queries, then the head's part
     if (lane == 0) {
       int issued = 0;
       for (; issued < chunks; ++issued) {
         const int s = issued % kStages, use = issued / kStages;
-        if (use > 0 && !ptx::mbar_wait(&empty[s], (use - 1) & 1, &abort_flag, budget_ns)) break;
+        if (use > 0 && !ptx::mbar_wait(&empty[s], (use - 1) & 1, abort_flag, budget_ns)) break;
         const uint32_t dst = ptx::smem_u32(ring + s * Cfg::kStageBytes);
         const size_t at = static_cast<size_t>(base) + issued;
         ptx::mbar_expect_tx(&full[s], Cfg::kStageBytes);
@@ -485,48 +531,48 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
       int ignore = 0;
       for (int c = max(0, issued - kStages); c < issued; ++c)
         ptx::mbar_wait(&full[c % kStages], (c / kStages) & 1, &ignore, ptx::kDrainBudgetNs);
-      if (abort_flag) set_status(seq.status, MOE_DEV_TIMEOUT);
+      if (*reinterpret_cast<volatile int *>(abort_flag)) set_status(seq.status, MOE_DEV_TIMEOUT);
     }
     return;
   }
 
-  const bool chain = warp < PAIRS;
-  const int pair = chain ? warp : warp - PAIRS;
-  PairSmem<DK> &ps = pairs[pair];
-  const int bar_s = 1 + 2 * pair, bar_u = 2 + 2 * pair;
-  const int dv0 = (tile * PAIRS + pair) * 16;
+  // Chain warps 2 g, 2 g + 1 (the halves of the key channels), output warp
+  // 2 GROUPS + g.  The three warps of a group meet twice per chunk: bar_x
+  // (both halves of S k^T and the copy of S are there), bar_w (u is there).
+  // Every buffer of the group is written before one of the two, read between
+  // it and the other, and so free again when its writer comes back to it.
+  const bool chain = warp < 2 * GROUPS;
+  const int group = chain ? warp >> 1 : warp - 2 * GROUPS, half = warp & 1;
+  GroupSmem<DK> &gs = groups[group];
+  const int bar_x = 1 + 2 * group, bar_w = 2 + 2 * group;
+  const int dv0 = (tile * GROUPS + group) * 16;
   const int g = lane >> 2, t = lane & 3;
   // a wait that gave up is not repeated: the loops below run to their end on
-  // whatever the ring holds, so that both warps of a pair pass every barrier
+  // whatever the ring holds, so that all warps of a group pass every barrier
   bool dead = false;
   // B fragments of two n8 tiles from rows (plain) or columns (trans) of a tile
   const int b_row = (lane & 7) + ((lane >> 4) << 3), b_piece = (lane >> 3) & 1;
   const int bt_row = (lane & 7) + (((lane >> 3) & 1) << 3), bt_piece = lane >> 4;
 
   if (chain) {
-    const int64_t at =
-        ((static_cast<int64_t>(r.slot) * d.v_heads + h) * d.v_dim + dv0 + g) * DK + 2 * t;
-    float S[DK / 8][4];
-    if (seq.state_in) {
-      const float *p = seq.state_in + at;
+    const int64_t at = ((static_cast<int64_t>(r.slot) * d.v_heads + h) * d.v_dim + dv0 + g) * DK +
+                       half * kHalf + 2 * t;
+    Acc S[kHalf / 8];
 #pragma unroll
-      for (int n = 0; n < DK / 8; ++n) {
-        const float2 a = *reinterpret_cast<const float2 *>(p + 8 * n);
-        const float2 c = *reinterpret_cast<const float2 *>(p + 8 * DK + 8 * n);
-        S[n][0] = a.x, S[n][1] = a.y, S[n][2] = c.x, S[n][3] = c.y;
+    for (int n = 0; n < kHalf / 8; ++n) {
+      S[n].top = S[n].low = make_float2(0.0f, 0.0f);
+      if (seq.state_in) {
+        S[n].top = *reinterpret_cast<const float2 *>(seq.state_in + at + 8 * n);
+        S[n].low = *reinterpret_cast<const float2 *>(seq.state_in + at + 8 * DK + 8 * n);
       }
-    } else {
-#pragma unroll
-      for (int n = 0; n < DK / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[n][e] = 0.0f;
     }
-    const uint32_t v_smem = ptx::smem_u32(ps.v[0]);
-    const auto fetch_v = [&](int c) {  // this pair's 16 channels of chunk c, zeros past the end
+    const uint32_t v_smem = ptx::smem_u32(gs.v[0]);
+    // this half's 32 tokens of the group's channels of chunk c, zeros past the end
+    const auto fetch_v = [&](int c) {
       if (c < chunks) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const int i = p * 16 + (lane >> 1), piece = lane & 1;
+        for (int p = 0; p < 2; ++p) {
+          const int i = half * 32 + p * 16 + (lane >> 1), piece = lane & 1;
           const bool live = c * kC + i < r.len;
           const int64_t row = static_cast<int64_t>(r.start) + (live ? c * kC + i : 0);
           cp_async16(v_smem + (c % 3) * kC * 32 + row32_at(i, piece),
@@ -544,34 +590,36 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
       const float *vec =
           reinterpret_cast<const float *>(ring + st * Cfg::kStageBytes + kKeyBlob<DK> + 3 * kTile);
       fetch_v(c + 2);
-      float m0, m1, i0, i1, x0, x1;
-      row_max(S, x0, x1);
-      pow2_scale(x0, m0, i0);
-      pow2_scale(x1, m1, i1);
-      ps.s_inv[lane] = make_float2(i0, i1);
-      if (!dead)
-        dead = !ptx::mbar_wait(&full[st], (c / kStages) & 1, &abort_flag, budget_ns);
-      // X^T = S k^T (16 value channels x 64 tokens)
-      float X[8][4] = {};
+      float m0, m1, i0, i1;
+      row_scales(S, m0, m1, i0, i1);
+      gs.s_inv[half][lane] = make_float2(i0, i1);
+      if (!dead) dead = !ptx::mbar_wait(&full[st], (c / kStages) & 1, abort_flag, budget_ns);
+      // this half's share of X^T = S k^T (16 value channels x 64 tokens)
+      Acc X[8] = {};
 #pragma unroll
-      for (int s = 0; s < DK / 16; ++s) {
+      for (int s = 0; s < kHalf / 16; ++s) {
         uint32_t hi[4], lo[4];
-        split_frag(S, s, m0, m1, hi, lo);
-        ps.s_frag[s][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        split_frag(S[2 * s], S[2 * s + 1], make_float2(m0, m0), make_float2(m1, m1), hi, lo);
+        gs.s_frag[half * (kHalf / 16) + s][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
           uint32_t bb[4];
-          ldsm4(bb, kt + tile_at<DK>(16 * np + b_row, 2 * s + b_piece));
+          ldsm4(bb, kt + tile_at<DK>(16 * np + b_row, half * (kHalf / 8) + 2 * s + b_piece));
           mma16(X[2 * np], hi, bb[0], bb[1]);
           mma16(X[2 * np + 1], hi, bb[2], bb[3]);
           mma16(X[2 * np], lo, bb[0], bb[1]);
           mma16(X[2 * np + 1], lo, bb[2], bb[3]);
         }
       }
-      bar_arrive(bar_s, 64);
-      // x_i = beta_i v_i - c_i (S k_i)
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        X[n].top = mul2(X[n].top, make_float2(i0, i0));
+        X[n].low = mul2(X[n].low, make_float2(i1, i1));
+        gs.x_part[half][n][lane] = make_float4(X[n].top.x, X[n].top.y, X[n].low.x, X[n].low.y);
+      }
       cp_async_wait<2>();
-      __syncwarp();
+      bar_sync(bar_x, 96);
+      // x_i = beta_i v_i - c_i (S k_i); vec holds -c_i
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
         uint32_t vv[4];
@@ -582,75 +630,84 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
           const int n = 2 * np + q;
           const float2 be = *reinterpret_cast<const float2 *>(vec + kVecBeta * kC + 8 * n + 2 * t);
           const float2 cc = *reinterpret_cast<const float2 *>(vec + kVecC * kC + 8 * n + 2 * t);
-          X[n][0] = be.x * bf16_lo(vv[2 * q]) - cc.x * (i0 * X[n][0]);
-          X[n][1] = be.y * bf16_hi(vv[2 * q]) - cc.y * (i0 * X[n][1]);
-          X[n][2] = be.x * bf16_lo(vv[2 * q + 1]) - cc.x * (i1 * X[n][2]);
-          X[n][3] = be.y * bf16_hi(vv[2 * q + 1]) - cc.y * (i1 * X[n][3]);
+          const float4 y = gs.x_part[half ^ 1][n][lane];
+          const float2 one = make_float2(1.0f, 1.0f);
+          X[n].top = fma2(X[n].top, one, make_float2(y.x, y.y));
+          X[n].low = fma2(X[n].low, one, make_float2(y.z, y.w));
+          X[n].top = fma2(cc, X[n].top,
+                          mul2(be, make_float2(bf16_lo(vv[2 * q]), bf16_hi(vv[2 * q]))));
+          X[n].low = fma2(cc, X[n].low,
+                          mul2(be, make_float2(bf16_lo(vv[2 * q + 1]), bf16_hi(vv[2 * q + 1]))));
         }
       }
-      // u = T x: column tile n of u^T takes the tokens j up to its own
-      row_max(X, x0, x1);
-      pow2_scale(x0, m0, i0);
-      pow2_scale(x1, m1, i1);
-      float U[8][4] = {};
+      // u = T x.  Column tiles 2 np, 2 np + 1 of u^T take the tokens of k16
+      // steps 0 .. np; the halves take np = 0 and 3, and np = 1 and 2: five
+      // steps each.
+      row_scales(X, m0, m1, i0, i1);
+      Acc U[2][2] = {};
+      const int np_of[2] = {half ? 1 : 0, half ? 2 : 3};
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         uint32_t hi[4], lo[4];
-        split_frag(X, s, m0, m1, hi, lo);
+        split_frag(X[2 * s], X[2 * s + 1], make_float2(m0, m0), make_float2(m1, m1), hi, lo);
 #pragma unroll
-        for (int np = s; np < 4; ++np) {
-          uint32_t th[4], tl[4];
-          const uint32_t a = tt + tile_at<kC>(16 * np + b_row, 2 * s + b_piece);
-          ldsm4(th, a);
-          ldsm4(tl, a + kTile);
-          mma16(U[2 * np], hi, tl[0], tl[1]);
-          mma16(U[2 * np + 1], hi, tl[2], tl[3]);
-          mma16(U[2 * np], lo, th[0], th[1]);
-          mma16(U[2 * np + 1], lo, th[2], th[3]);
-          mma16(U[2 * np], hi, th[0], th[1]);
-          mma16(U[2 * np + 1], hi, th[2], th[3]);
+        for (int j = 0; j < 2; ++j) {
+          if (s <= np_of[j]) {
+            uint32_t th[4], tl[4];
+            const uint32_t a = tt + tile_at<kC>(16 * np_of[j] + b_row, 2 * s + b_piece);
+            ldsm4(th, a);
+            ldsm4(tl, a + kTile);
+            mma16(U[j][0], hi, tl[0], tl[1]);
+            mma16(U[j][1], hi, tl[2], tl[3]);
+            mma16(U[j][0], lo, th[0], th[1]);
+            mma16(U[j][1], lo, th[2], th[3]);
+            mma16(U[j][0], hi, th[0], th[1]);
+            mma16(U[j][1], hi, th[2], th[3]);
+          }
         }
       }
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const float2 ts = *reinterpret_cast<const float2 *>(vec + kVecT * kC + 8 * n + 2 * t);
-        U[n][0] *= i0 * ts.x, U[n][1] *= i0 * ts.y;
-        U[n][2] *= i1 * ts.x, U[n][3] *= i1 * ts.y;
-      }
-      // the output warp's copy
-      row_max(U, x0, x1);
-      pow2_scale(x0, m0, i0);
-      pow2_scale(x1, m1, i1);
-      ps.u_inv[c & 1][lane] = make_float2(i0, i1);
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        ps.u_frag[c & 1][s][lane] = make_uint4(
-            h2_bits(__floats2half2_rn(U[2 * s][0] * m0, U[2 * s][1] * m0)),
-            h2_bits(__floats2half2_rn(U[2 * s][2] * m1, U[2 * s][3] * m1)),
-            h2_bits(__floats2half2_rn(U[2 * s + 1][0] * m0, U[2 * s + 1][1] * m0)),
-            h2_bits(__floats2half2_rn(U[2 * s + 1][2] * m1, U[2 * s + 1][3] * m1)));
-      // also says that the output warp has read this chunk's s_frag
-      bar_sync(bar_u, 64);
-      // S = gamma S + sum_j (Gamma_64,j u_j) k_j^T
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const float2 dd = *reinterpret_cast<const float2 *>(vec + kVecD * kC + 8 * n + 2 * t);
-        U[n][0] *= dd.x, U[n][1] *= dd.y, U[n][2] *= dd.x, U[n][3] *= dd.y;
-      }
-      row_max(U, x0, x1);
-      pow2_scale(x0, m0, i0);
-      pow2_scale(x1, m1, i1);
+      // Rescaled by T's row scales and down by a bound of its row sums, u
+      // stays below 2^15 (the scale of x), and so does w_j = Gamma_64,j
+      // kappa_j u_j over the largest such factor.
+      const float tau = vec[kVecMisc * kC + 1];
+      gs.u_inv[lane] = make_float2(i0 * tau, i1 * tau);
       uint32_t wh[4][4], wl[4][4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) split_frag(U, s, m0, m1, wh[s], wl[s]);
-      const float gamma = vec[kVecMisc * kC];
+      for (int j = 0; j < 2; ++j) {
+        uint32_t f[4], hi[4], lo[4];
 #pragma unroll
-      for (int np = 0; np < DK / 16; ++np) {
-        float acc[2][4] = {};
+        for (int q = 0; q < 2; ++q) {
+          const int n = 2 * np_of[j] + q;
+          const float2 ts = *reinterpret_cast<const float2 *>(vec + kVecT * kC + 8 * n + 2 * t);
+          const float2 dd = *reinterpret_cast<const float2 *>(vec + kVecD * kC + 8 * n + 2 * t);
+          const float2 top = mul2(U[j][q].top, ts), low = mul2(U[j][q].low, ts);
+          f[2 * q] = h2_bits(__float22half2_rn(top));
+          f[2 * q + 1] = h2_bits(__float22half2_rn(low));
+          split_h2(mul2(top, dd), hi[2 * q], lo[2 * q]);
+          split_h2(mul2(low, dd), hi[2 * q + 1], lo[2 * q + 1]);
+        }
+        gs.u_frag[np_of[j]][lane] = make_uint4(f[0], f[1], f[2], f[3]);
+        gs.w_frag[np_of[j]][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        gs.w_frag[np_of[j]][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      bar_sync(bar_w, 96);
+      // S = gamma S + sum_j w_j k_j^T
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const uint4 a = gs.w_frag[s][0][lane], e = gs.w_frag[s][1][lane];
+        wh[s][0] = a.x, wh[s][1] = a.y, wh[s][2] = a.z, wh[s][3] = a.w;
+        wl[s][0] = e.x, wl[s][1] = e.y, wl[s][2] = e.z, wl[s][3] = e.w;
+      }
+      const float gamma = vec[kVecMisc * kC], back = tau * vec[kVecMisc * kC + 2];
+      const float2 gamma2 = make_float2(gamma, gamma);
+      const float2 b0 = make_float2(i0 * back, i0 * back), b1 = make_float2(i1 * back, i1 * back);
+#pragma unroll
+      for (int np = 0; np < kHalf / 16; ++np) {
+        Acc acc[2] = {};
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           uint32_t bb[4];
-          ldsm4_t(bb, kt + tile_at<DK>(16 * s + bt_row, 2 * np + bt_piece));
+          ldsm4_t(bb, kt + tile_at<DK>(16 * s + bt_row, half * (kHalf / 8) + 2 * np + bt_piece));
           mma16(acc[0], wh[s], bb[0], bb[1]);
           mma16(acc[1], wh[s], bb[2], bb[3]);
           mma16(acc[0], wl[s], bb[0], bb[1]);
@@ -658,11 +715,9 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          float(&a)[4] = S[2 * np + q];
-          a[0] = fmaf(gamma, a[0], i0 * acc[q][0]);
-          a[1] = fmaf(gamma, a[1], i0 * acc[q][1]);
-          a[2] = fmaf(gamma, a[2], i1 * acc[q][2]);
-          a[3] = fmaf(gamma, a[3], i1 * acc[q][3]);
+          Acc &a = S[2 * np + q];
+          a.top = fma2(acc[q].top, b0, mul2(gamma2, a.top));
+          a.low = fma2(acc[q].low, b1, mul2(gamma2, a.low));
         }
       }
       __syncwarp();
@@ -670,46 +725,55 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
     }
     cp_async_wait<0>();
     if (seq.state_out) {
-      float *p = seq.state_out + at;
 #pragma unroll
-      for (int n = 0; n < DK / 8; ++n) {
-        *reinterpret_cast<float2 *>(p + 8 * n) = make_float2(S[n][0], S[n][1]);
-        *reinterpret_cast<float2 *>(p + 8 * DK + 8 * n) = make_float2(S[n][2], S[n][3]);
+      for (int n = 0; n < kHalf / 8; ++n) {
+        *reinterpret_cast<float2 *>(seq.state_out + at + 8 * n) = S[n].top;
+        *reinterpret_cast<float2 *>(seq.state_out + at + 8 * DK + 8 * n) = S[n].low;
       }
     }
     return;
   }
 
   // output warp: o_i = rho_i gamma_i (S q_i) + sum_j P_ij u_j
-  const uint32_t o_smem = ptx::smem_u32(ps.o);
+  const uint32_t o_smem = ptx::smem_u32(gs.o);
   for (int c = 0; c < chunks; ++c) {
     const int st = c % kStages;
     const uint32_t qt = ptx::smem_u32(ring + st * Cfg::kStageBytes) + kKeyBlob<DK> / 2;
     const uint32_t pt = qt + kKeyBlob<DK> / 2 + 2 * kTile;
     const float *vec =
         reinterpret_cast<const float *>(ring + st * Cfg::kStageBytes + kKeyBlob<DK> + 3 * kTile);
-    if (!dead) dead = !ptx::mbar_wait(&full[st], (c / kStages) & 1, &abort_flag, budget_ns);
-    bar_sync(bar_s, 64);
-    const float2 si = ps.s_inv[lane];
-    float O[8][4] = {};
+    if (!dead) dead = !ptx::mbar_wait(&full[st], (c / kStages) & 1, abort_flag, budget_ns);
+    bar_sync(bar_x, 96);
+    Acc O[8] = {};
 #pragma unroll
-    for (int s = 0; s < DK / 16; ++s) {
-      const uint4 f = ps.s_frag[s][lane];
-      const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+    for (int side = 0; side < 2; ++side) {
+      // the halves of S have scales of their own
+      Acc acc[8] = {};
 #pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t bb[4];
-        ldsm4(bb, qt + tile_at<DK>(16 * np + b_row, 2 * s + b_piece));
-        mma16(O[2 * np], a, bb[0], bb[1]);
-        mma16(O[2 * np + 1], a, bb[2], bb[3]);
+      for (int s = 0; s < kHalf / 16; ++s) {
+        const uint4 f = gs.s_frag[side * (kHalf / 16) + s][lane];
+        const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          uint32_t bb[4];
+          ldsm4(bb, qt + tile_at<DK>(16 * np + b_row, side * (kHalf / 8) + 2 * s + b_piece));
+          mma16(acc[2 * np], a, bb[0], bb[1]);
+          mma16(acc[2 * np + 1], a, bb[2], bb[3]);
+        }
+      }
+      const float2 si = gs.s_inv[side][lane];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        O[n].top = fma2(acc[n].top, make_float2(si.x, si.x), O[n].top);
+        O[n].low = fma2(acc[n].low, make_float2(si.y, si.y), O[n].low);
       }
     }
-    bar_sync(bar_u, 64);
-    const float2 ui = ps.u_inv[c & 1][lane];
-    float I[8][4] = {};
+    bar_sync(bar_w, 96);
+    const float2 ui = gs.u_inv[lane];
+    Acc I[8] = {};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const uint4 f = ps.u_frag[c & 1][s][lane];
+      const uint4 f = gs.u_frag[s][lane];
       const uint32_t a[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
       for (int np = s; np < 4; ++np) {
@@ -727,10 +791,10 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
         const int n = 2 * np + q;
         const float2 oq = *reinterpret_cast<const float2 *>(vec + kVecO * kC + 8 * n + 2 * t);
         const float2 pi = *reinterpret_cast<const float2 *>(vec + kVecP * kC + 8 * n + 2 * t);
-        w[2 * q] = pack_bf16x2((si.x * O[n][0]) * oq.x + (ui.x * I[n][0]) * pi.x,
-                               (si.x * O[n][1]) * oq.y + (ui.x * I[n][1]) * pi.y);
-        w[2 * q + 1] = pack_bf16x2((si.y * O[n][2]) * oq.x + (ui.y * I[n][2]) * pi.x,
-                                   (si.y * O[n][3]) * oq.y + (ui.y * I[n][3]) * pi.y);
+        const float2 top = fma2(mul2(I[n].top, make_float2(ui.x, ui.x)), pi, mul2(O[n].top, oq));
+        const float2 low = fma2(mul2(I[n].low, make_float2(ui.y, ui.y)), pi, mul2(O[n].low, oq));
+        w[2 * q] = pack_bf16(top.x, top.y);
+        w[2 * q + 1] = pack_bf16(low.x, low.y);
       }
       // transposed back: token rows of 16 channels
       stsm4_t(o_smem + row32_at(16 * np + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1), w[0],
@@ -744,23 +808,36 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
       if (c * kC + i < r.len)
         *reinterpret_cast<uint4 *>(
             out + (static_cast<int64_t>(r.start) + c * kC + i) * out_ld + h * d.v_dim + dv0 +
-            piece * 8) = *reinterpret_cast<const uint4 *>(ps.o + row32_at(i, piece));
+            piece * 8) = *reinterpret_cast<const uint4 *>(gs.o + row32_at(i, piece));
     }
     __syncwarp();
   }
 }
 
-template <int DK, int PAIRS>
+// Sets a kernel's shared-memory limit once per device.
+template <class F>
+cudaError_t allow_smem(F kernel, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <int DK, int GROUPS>
 cudaError_t launch_chain(const moe_delta_dims &d, const moe_delta_inputs &in, const DeltaSeqs &seq,
                          const uint8_t *ws, const uint8_t *ws_key, const uint8_t *ws_head,
                          moe_bf16 *out, int64_t out_ld, cudaStream_t s) {
-  using Cfg = ChainCfg<DK, PAIRS>;
-  static_assert(Cfg::kSmem <= 227 * 1024 - 16, "shared memory of one SM");
-  cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<DK, PAIRS>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+  using Cfg = ChainCfg<DK, GROUPS>;
+  static_assert(Cfg::kSmem <= 227 * 1024, "shared memory of one SM");
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(delta_chain_kernel<DK, GROUPS>, Cfg::kSmem, done);
   if (e != cudaSuccess) return e;
-  const int64_t grid = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / (16 * PAIRS));
-  delta_chain_kernel<DK, PAIRS><<<static_cast<unsigned>(grid), Cfg::kThreads, Cfg::kSmem, s>>>(
+  const int64_t grid = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / (16 * GROUPS));
+  delta_chain_kernel<DK, GROUPS><<<static_cast<unsigned>(grid), Cfg::kThreads, Cfg::kSmem, s>>>(
       d, in, seq, ws, ws_key, ws_head, out, out_ld, tc_wait_budget_ns());
   return cudaGetLastError();
 }
@@ -772,8 +849,8 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
   uint8_t *ws_key = ws + kHeader;
   uint8_t *ws_head = ws_key + slots * d.qk_heads * kKeyBlob<DK>;
   constexpr int kSmem = sizeof(PrepSmem<DK>);
-  cudaError_t e = cudaFuncSetAttribute(delta_prep_kernel<DK>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(delta_prep_kernel<DK>, kSmem, done);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(slots), d.v_heads);
   delta_prep_kernel<DK><<<grid, kPrepThreads, kSmem, s>>>(d, in, seq, ws, ws_key, ws_head);

@@ -69,18 +69,63 @@ __device__ __forceinline__ void pow2_scale(float amax, float &mult, float &inv) 
   inv = __uint_as_float(static_cast<uint32_t>(254 - m) << 23);
 }
 
+// The power of two above x >= 0 (x < up <= 2 x for normal x) and its inverse.
+__device__ __forceinline__ void pow2_above(float x, float &up, float &down) {
+  const int e = static_cast<int>((__float_as_uint(x) >> 23) & 255u);
+  const int m = min(max(e + 1, 1), 253);
+  up = __uint_as_float(static_cast<uint32_t>(m) << 23);
+  down = __uint_as_float(static_cast<uint32_t>(254 - m) << 23);
+}
+
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// (a, b) scaled -> fp16 pairs hi and lo with hi + lo = 22 bits of each.
-__device__ __forceinline__ void split_h2(float a, float b, float mult, uint32_t &hi,
-                                         uint32_t &lo) {
-  a *= mult, b *= mult;
-  const __half2 h = __floats2half2_rn(a, b);
-  const float2 back = __half22float2(h);
+// d = a b + c on two fp32 at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// max(|a|, |b|, |c|), NaN ignored.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// fp16 pairs hi = fp16(x) and lo = fp16(x - hi): 22 bits of x, which is
+// scaled already (the subtraction is exact).
+__device__ __forceinline__ void split_h2(float2 x, uint32_t &hi, uint32_t &lo) {
+  const __half2 h = __float22half2_rn(x);
   hi = h2_bits(h);
-  lo = h2_bits(__floats2half2_rn(a - back.x, b - back.y));
+  float a, b;
+  asm("{\n\t.reg .b16 l, h, m;\n\t"
+      "mov.b32 {l, h}, %2;\n\tmov.b16 m, 0xBC00;\n\t"  // -1
+      "fma.rn.f32.f16 %0, l, m, %3;\n\tfma.rn.f32.f16 %1, h, m, %4;\n\t}"
+      : "=f"(a), "=f"(b)
+      : "r"(hi), "f"(x.x), "f"(x.y));
+  lo = h2_bits(__floats2half2_rn(a, b));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {

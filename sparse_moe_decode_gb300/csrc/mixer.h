@@ -32,8 +32,8 @@ cudaError_t launch_delta_chunk(const moe_delta_dims &d, const moe_delta_inputs &
                                const DeltaSeqs &seq, void *ws, moe_bf16 *out, int64_t out_ld,
                                cudaStream_t s);
 
-// a.rows > 0; `vec8`: every row starts on a 16-byte boundary and width is a
-// multiple of 8.
-cudaError_t launch_norm_gate_residual(const moe_norm_args &a, bool vec8, cudaStream_t s);
+// a.rows > 0; vec = 8 or 2: width and every stride are multiples of it (the
+// rows start on 16- or 4-byte boundaries), otherwise 1.
+cudaError_t launch_norm_gate_residual(const moe_norm_args &a, int vec, cudaStream_t s);
 
 }  // namespace moe

@@ -200,11 +200,14 @@ moe_status moe_norm_gate_residual(const moe_norm_args *args, void *stream) {
       const bool in_place = i < 2 && o.p == ins[i].p && o.ld == ins[i].ld;
       if (!in_place && overlap(o, ins[i])) return MOE_ERR_INVALID_ARG;
     }
-  const bool vec8 = a.width % 8 == 0 && a.x_ld % 8 == 0 &&
-                    (!a.resid_in || a.resid_in_ld % 8 == 0) &&
-                    (!a.resid_out || a.resid_out_ld % 8 == 0) &&
-                    (!a.x_next || a.x_next_ld % 8 == 0) && (!element || a.gate_ld % 8 == 0);
-  return cuda_status(launch_norm_gate_residual(a, vec8, static_cast<cudaStream_t>(stream)));
+  // common divisors of everything that places a row
+  int64_t by = a.width | a.x_ld;
+  if (a.resid_in) by |= a.resid_in_ld;
+  if (a.resid_out) by |= a.resid_out_ld;
+  if (a.x_next) by |= a.x_next_ld;
+  if (element) by |= a.gate_ld;
+  const int vec = by % 8 == 0 ? 8 : by % 2 == 0 ? 2 : 1;
+  return cuda_status(launch_norm_gate_residual(a, vec, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
