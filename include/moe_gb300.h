@@ -289,8 +289,9 @@ moe_status moe_topk_merge(const int32_t *ids, const float *values, int T, int n_
  *   S <- exp(g_t) S;   u = beta_t (v_t - S k_t);   S <- S + u k_t^T;
  *   o_t = S q_t * scale.
  * With qk_norm != 0, q and k are first divided by sqrt(sum x^2 + qk_eps).
- * g is the natural logarithm of the decay (g <= 0 in use; below -128, -inf
- * included, it counts as -128: the state is forgotten).  Sums, states and
+ * g is the natural logarithm of the decay, g <= 0 (below -128, -inf included,
+ * it counts as -128: the state is forgotten; growth is served as long as no
+ * 64 consecutive g sum to more than 3).  Sums, states and
  * gates are fp32 (or better); out is rounded to bf16 once. */
 typedef struct {
   int32_t qk_heads; /* Hk                                                 */

@@ -47,8 +47,7 @@ enum { kVecC, kVecBeta, kVecT, kVecD, kVecO, kVecP, kVecMisc, kVecs };
 constexpr int kHeadBlob = 3 * kTile + kVecs * kC * 4;
 constexpr int kHeader = 256;      // status word, flags
 constexpr int kFlagWord = 16;     // header word: some bound of the call is bad
-constexpr int kPrepThreads = 128;
-constexpr int kLd = kC + 1;       // row stride of the fp32 work matrix
+constexpr int kPrepThreads = 256;
 
 template <int DK>
 constexpr int kKeyBlob = 2 * kC * DK * 2;  // per (chunk, key head): k, then q, as fp16
@@ -69,70 +68,82 @@ __device__ __forceinline__ int slot_base(const DeltaSeqs &s, int b) {
 
 // ------------------------------------------------------------------- prep
 
+constexpr int kTLd = kC + 4;  // row stride of T
+
+// T's rows have room for four values beside them: the tokens' factors.
+enum { kGLo = kC, kKappa, kRho };
+
 template <int DK>
 struct PrepSmem {
   alignas(128) uint8_t key[kKeyBlob<DK>];
+  // L (fp32, permuted) until T's two terms replace it; P; the vectors, of
+  // which kVecT holds the sums of g until T's scales replace them
   alignas(128) uint8_t head[kHeadBlob];
-  float m[kC * kLd];  // below the diagonal L, above it T transposed
-  float kappa[kC], rho[kC], beta[kC], ghi[kC], glo[kC], half_max[2][kC], half_sum[2][kC];
+  float t[kC * kTLd];  // T; blocks of 16 above the diagonal are never touched
 };
 
-// T(i, j) of the work matrix: stored transposed above the diagonal.
-__device__ __forceinline__ float t_at(const float *m, int i, int j) {
-  return i > j ? m[j * kLd + i] : (i == j ? 1.0f : 0.0f);
+// Where L(i, j) lies: pieces of four columns permuted by the row, so that
+// eight rows' pieces of one column lie in different banks.
+__device__ __forceinline__ int l_at(int i, int j) { return i * kC + (j ^ ((i & 7) << 2)); }
+
+// The power of two that brings a token's values below 2^15 (bounded by their
+// 2-norm), and its inverse: their bf16 digits are exact in fp16 down to 2^-25
+// of the norm and off by 2^-39 of it below that.
+__device__ __forceinline__ void token_scale(float ss, float &mult, float &inv) {
+  const int e = static_cast<int>((__float_as_uint(ss) >> 23) & 255u);
+  const int m = 142 - ((e - 125) >> 1);  // 127 + 15 - ceil((e - 126) / 2)
+  mult = __uint_as_float(static_cast<uint32_t>(m) << 23);
+  inv = __uint_as_float(static_cast<uint32_t>(254 - m) << 23);
 }
 
-// acc (16 rows from r0, 16 columns from c0) = A B over k in [k0, k1), fp32
-// values in three tf32 products each.
+// A 16 x 8 tile (rows r0, columns c0) of A B over k in [k0, k1): fp32 values
+// as two tf32 terms each, three products.
 template <class FA, class FB>
-__device__ __forceinline__ void product16(float (&acc)[2][4], int r0, int c0, int k0, int k1,
-                                          FA a_of, FB b_of, int lane) {
+__device__ __forceinline__ void product(float (&acc)[4], int r0, int c0, int k0, int k1, FA a_of,
+                                        FB b_of, int lane) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int n = 0; n < 2; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+  for (int i = 0; i < 4; ++i) acc[i] = 0.0f;
   for (int k = k0; k < k1; k += 8) {
-    uint32_t ah[4], al[4];
+    uint32_t ah[4], al[4], bh[2], bl[2];
     split_tf32(a_of(r0 + g, k + t), ah[0], al[0]);
     split_tf32(a_of(r0 + g + 8, k + t), ah[1], al[1]);
     split_tf32(a_of(r0 + g, k + t + 4), ah[2], al[2]);
     split_tf32(a_of(r0 + g + 8, k + t + 4), ah[3], al[3]);
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      uint32_t bh[2], bl[2];
-      split_tf32(b_of(k + t, c0 + 8 * n + g), bh[0], bl[0]);
-      split_tf32(b_of(k + t + 4, c0 + 8 * n + g), bh[1], bl[1]);
-      mma8(acc[n], ah, bl[0], bl[1]);
-      mma8(acc[n], al, bh[0], bh[1]);
-      mma8(acc[n], ah, bh[0], bh[1]);
-    }
+    split_tf32(b_of(k + t, c0 + g), bh[0], bl[0]);
+    split_tf32(b_of(k + t + 4, c0 + g), bh[1], bl[1]);
+    mma8(acc, ah, bl[0], bl[1]);
+    mma8(acc, al, bh[0], bh[1]);
+    mma8(acc, ah, bh[0], bh[1]);
   }
 }
 
+// One CTA per chunk and key head, for `heads` of the value heads that read
+// it.  Warps 0..3 take k (k k^T, L, T's diagonal blocks), warps 4..7 take q
+// (q k^T, P), 16 tokens each.
 template <int DK>
-__global__ void __launch_bounds__(kPrepThreads)
-delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t *ws,
+__global__ void __launch_bounds__(kPrepThreads, 3)
+delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int heads, uint8_t *ws,
                   uint8_t *ws_key, uint8_t *ws_head) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   PrepSmem<DK> &sm = *reinterpret_cast<PrepSmem<DK> *>(smem_raw);
+  __shared__ float red[kPrepThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int slot = blockIdx.x, h = blockIdx.y, ratio = d.v_heads / d.qk_heads, hk = h / ratio;
+  const int ratio = d.v_heads / d.qk_heads;
+  const int slot = blockIdx.x, h0 = blockIdx.y * heads, hk = h0 / ratio;
 
-  if (slot == 0 && h == 0) {
+  if (slot == 0 && h0 == 0) {
     // one CTA looks at every bound: a call with a bad one does nothing
-    __shared__ int any_bad;
-    if (tid == 0) any_bad = 0;
-    __syncthreads();
+    bool bad = false;
     if (seq.cu_seqlens)
       for (int b = tid; b < seq.B; b += kPrepThreads) {
         const int lo = seq.cu_seqlens[b], hi = seq.cu_seqlens[b + 1];
-        if (lo < 0 || lo > hi || hi > seq.N) any_bad = 1;
+        bad |= lo < 0 || lo > hi || hi > seq.N;
       }
-    __syncthreads();
+    bad = __syncthreads_or(bad);
     if (tid == 0) {
-      reinterpret_cast<uint32_t *>(ws)[kFlagWord] = any_bad;
-      if (any_bad) set_status(seq.status, MOE_DEV_BAD_INDEX);
+      reinterpret_cast<uint32_t *>(ws)[kFlagWord] = bad;
+      if (bad) set_status(seq.status, MOE_DEV_BAD_INDEX);
     }
   }
 
@@ -149,259 +160,333 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t 
   const int left = min(kC, r.len - chunk * kC);  // tokens of this chunk
   const int64_t row0 = static_cast<int64_t>(r.start) + chunk * kC;
 
-  // k and q: scaled to fp16, their norms
-  constexpr int kLanes = DK / 8;  // threads of a row, 8 values each
-  constexpr int kRowsAt = kPrepThreads / kLanes;
-  const int piece = tid % kLanes;
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    uint4 raw[kC / kRowsAt];
-#pragma unroll
-    for (int p = 0; p < kC / kRowsAt; ++p) {
-      const int i = p * kRowsAt + tid / kLanes;
-      const moe_bf16 *src = which ? in.q + (row0 + i) * in.q_ld : in.k + (row0 + i) * in.k_ld;
-      raw[p] = i < left ? *reinterpret_cast<const uint4 *>(src + hk * DK + piece * 8)
-                        : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int p = 0; p < kC / kRowsAt; ++p) {
-      const int i = p * kRowsAt + tid / kLanes;
-      const uint32_t w[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
-      float x[8], amax = 0.0f, ss = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[j] = (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
-        amax = fmaxf(amax, fabsf(x[j]));
-        ss = fmaf(x[j], x[j], ss);
-      }
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) {
-        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-        ss += __shfl_xor_sync(kFull, ss, o);
-      }
-      float mult, inv;
-      pow2_scale(amax, mult, inv);
-      uint4 o;
-      o.x = h2_bits(__floats2half2_rn(x[0] * mult, x[1] * mult));
-      o.y = h2_bits(__floats2half2_rn(x[2] * mult, x[3] * mult));
-      o.z = h2_bits(__floats2half2_rn(x[4] * mult, x[5] * mult));
-      o.w = h2_bits(__floats2half2_rn(x[6] * mult, x[7] * mult));
-      *reinterpret_cast<uint4 *>(sm.key + which * (kKeyBlob<DK> / 2) + tile_at<DK>(i, piece)) = o;
-      if (piece == 0) {
-        if (d.qk_norm) inv = inv / sqrtf(ss + d.qk_eps);
-        if (which) inv *= d.scale;
-        (which ? sm.rho : sm.kappa)[i] = i < left ? inv : 0.0f;
-      }
-    }
-  }
+  const int w = warp & 3;          // this warp's 16 tokens
+  const bool is_q = warp >= 4;
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t kt = ptx::smem_u32(sm.key);
 
-  // decays: sums of logarithms in fp64, kept as two fp32 terms each, so that
-  // differences of large sums keep their digits
-  float *vec = reinterpret_cast<float *>(sm.head + 3 * kTile);
-  if (warp == 0) {
-    const int i = 2 * lane;
-    double g0 = 0.0, g1 = 0.0;
-    if (i < left) g0 = delta_log_decay(in.g[(row0 + i) * in.g_ld + h]);
-    if (i + 1 < left) g1 = delta_log_decay(in.g[(row0 + i + 1) * in.g_ld + h]);
-    sm.beta[i] = i < left ? in.beta[(row0 + i) * in.beta_ld + h] : 0.0f;
-    sm.beta[i + 1] = i + 1 < left ? in.beta[(row0 + i + 1) * in.beta_ld + h] : 0.0f;
-    double sum = g0 + g1;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double up = __shfl_up_sync(kFull, sum, o);
-      if (lane >= o) sum += up;
-    }
-    const double total = __shfl_sync(kFull, sum, 31);
-    const double first = sum - g1;
-    const double s[2] = {first, sum};
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float hi32 = static_cast<float>(s[j]);
-      sm.ghi[i + j] = hi32;
-      sm.glo[i + j] = static_cast<float>(s[j] - hi32);
-      vec[kVecO * kC + i + j] = expf(hi32);                             // gamma_i
-      vec[kVecD * kC + i + j] = expf(static_cast<float>(total - s[j]));  // Gamma_64,i
-    }
-    if (lane == 0) vec[kVecMisc * kC] = expf(static_cast<float>(total));  // gamma_64
-  }
-  __syncthreads();
-
-  // L and P: rows 16 warp .. + 15 of k k^T and q k^T, up to the diagonal block
+  // k and q: scaled to fp16, and the tokens' factors.  Eight lanes a row.
   {
-    const int g = lane >> 2, t = lane & 3;
-    const uint32_t kt = ptx::smem_u32(sm.key), qt = kt + kKeyBlob<DK> / 2;
-    float kk[8][4] = {}, qk[8][4] = {};
-#pragma unroll
-    for (int s = 0; s < DK / 16; ++s) {
-      uint32_t ka[4], qa[4];
-      const int ar = 16 * warp + (lane & 15), ap = 2 * s + (lane >> 4);
-      ldsm4(ka, kt + tile_at<DK>(ar, ap));
-      ldsm4(qa, qt + tile_at<DK>(ar, ap));
-#pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        if (np <= warp) {
-          uint32_t b[4];
-          ldsm4(b, kt + tile_at<DK>(16 * np + (lane & 7) + ((lane >> 4) << 3),
-                                    2 * s + ((lane >> 3) & 1)));
-          mma16(kk[2 * np], ka, b[0], b[1]);
-          mma16(kk[2 * np + 1], ka, b[2], b[3]);
-          mma16(qk[2 * np], qa, b[0], b[1]);
-          mma16(qk[2 * np + 1], qa, b[2], b[3]);
-        }
-      }
-    }
-    float pmax[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 16 * warp + g + (e >> 1) * 8, j = 8 * n + 2 * t + (e & 1);
-        float p = 0.0f;
-        if (j <= i) {
-          const float decay = expf((sm.ghi[i] - sm.ghi[j]) + (sm.glo[i] - sm.glo[j]));
-          const float kj = decay * sm.kappa[j];
-          if (j < i) sm.m[i * kLd + j] = sm.beta[i] * sm.kappa[i] * kj * kk[n][e];
-          p = sm.rho[i] * kj * qk[n][e];
-        }
-        qk[n][e] = p;
-        pmax[e >> 1] = fmaxf(pmax[e >> 1], fabsf(p));
-      }
-    }
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float mx = pmax[half];
-      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-      float mult, inv;
-      pow2_scale(mx, mult, inv);
-      const int i = 16 * warp + g + 8 * half;
-      if (t == 0) vec[kVecP * kC + i] = inv;
-#pragma unroll
-      for (int n = 0; n < 8; ++n)
-        *reinterpret_cast<__half2 *>(sm.head + 2 * kTile + tile_at<kC>(i, n) + 4 * t) =
-            __floats2half2_rn(qk[n][2 * half] * mult, qk[n][2 * half + 1] * mult);
-    }
-  }
-  if (warp == 0) {
-    // the factors of the tokens; the update's, Gamma_64,j kappa_j, over a
-    // power of two not below the largest
-    float dmax = 0.0f;
-#pragma unroll
-    for (int i = lane; i < kC; i += 32) {
-      const float gamma = vec[kVecO * kC + i];
-      vec[kVecBeta * kC + i] = sm.beta[i];
-      vec[kVecC * kC + i] = -sm.beta[i] * gamma * sm.kappa[i];
-      vec[kVecO * kC + i] = sm.rho[i] * gamma;
-      dmax = fmaxf(dmax, vec[kVecD * kC + i] *= sm.kappa[i]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dmax = fmaxf(dmax, __shfl_xor_sync(kFull, dmax, o));
-    float up, down;
-    pow2_above(dmax, up, down);
-    vec[kVecD * kC + lane] *= down;
-    vec[kVecD * kC + lane + 32] *= down;
-    if (lane == 0) vec[kVecMisc * kC + 2] = up;
-  }
-  __syncwarp();
-
-  // T: the 16 x 16 diagonal blocks by substitution (a lane per column), ...
-  {
-    const int o = 16 * warp, c = lane & 15;
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float v = i == c ? 1.0f : 0.0f;
-#pragma unroll
-      for (int j = 0; j < i; ++j) v = fmaf(-sm.m[(o + i) * kLd + o + j], x[j], v);
-      x[i] = v;
-    }
-    __syncwarp();
-    if (lane < 16)
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i > c) sm.m[(o + c) * kLd + o + i] = x[i];
-  }
-  __syncthreads();
-  // ... then [A 0; B C]^-1 = [A^-1 0; -C^-1 B A^-1 C^-1] for blocks of 16 and 32
-  const auto l_of = [&](int i, int j) { return sm.m[i * kLd + j]; };
-  const auto t_of = [&](int i, int j) { return t_at(sm.m, i, j); };
-  const auto up_of = [&](int i, int j) { return sm.m[j * kLd + i]; };  // B A^-1, kept above
-  const auto put = [&](const float(&acc)[2][4], int r0, int c0, float sign) {
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        sm.m[(c0 + 8 * n + 2 * t + (e & 1)) * kLd + r0 + g + (e >> 1) * 8] = sign * acc[n][e];
-  };
-  {
-    float acc[2][4];
-    const int o = 32 * warp;
-    if (warp < 2) {
-      product16(acc, o + 16, o, o, o + 16, l_of, t_of, lane);
-      put(acc, o + 16, o, 1.0f);
-      __syncwarp();
-      product16(acc, o + 16, o, o + 16, o + 32, t_of, up_of, lane);
-      __syncwarp();
-      put(acc, o + 16, o, -1.0f);
-    }
-    __syncthreads();
-    const int r0 = 32 + 16 * (warp & 1), c0 = 16 * (warp >> 1);
-    product16(acc, r0, c0, c0, 32, l_of, t_of, lane);  // T(k, c) = 0 for k < c
-    put(acc, r0, c0, 1.0f);
-    __syncthreads();
-    product16(acc, r0, c0, 32, r0 + 16, t_of, up_of, lane);
-    __syncthreads();
-    put(acc, r0, c0, -1.0f);
-    __syncthreads();
-  }
-  // T's rows as two fp16 terms, and a power of two above every row's sum
-  {
-    const int i = tid & 63, j0 = (tid >> 6) * 32;
-    float mx = 0.0f, sum = 0.0f;
-#pragma unroll 8
-    for (int j = j0; j < j0 + 32; ++j) {
-      const float v = fabsf(t_at(sm.m, i, j));
-      mx = fmaxf(mx, v);
-      sum += v;
-    }
-    sm.half_max[tid >> 6][i] = mx;
-    sm.half_sum[tid >> 6][i] = sum;
-    __syncthreads();
-    mx = fmaxf(sm.half_max[0][i], sm.half_max[1][i]);
-    sum = fmaxf(sm.half_sum[0][lane] + sm.half_sum[1][lane],
-                sm.half_sum[0][lane + 32] + sm.half_sum[1][lane + 32]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum = fmaxf(sum, __shfl_xor_sync(kFull, sum, o));
-    float mult, inv, up, down;
-    pow2_above(sum, up, down);
-    pow2_scale(mx, mult, inv);
-    if (tid < kC) vec[kVecT * kC + i] = inv * down;
-    if (tid == 0) vec[kVecMisc * kC + 1] = up;
-    const float2 m2 = make_float2(mult, mult);
+    constexpr int kPieces = DK / 64;  // 16-byte pieces of a lane
+    const moe_bf16 *src = is_q ? in.q : in.k;
+    const int64_t ld = is_q ? in.q_ld : in.k_ld;
+    const int piece = lane & 7;
+    uint4 raw[4][kPieces];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      uint32_t hi32[4], lo32[4];
+      const int i = 16 * w + 4 * p + (lane >> 3);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = j0 + 8 * p + 2 * e;
-        split_h2(mul2(make_float2(t_at(sm.m, i, j), t_at(sm.m, i, j + 1)), m2), hi32[e], lo32[e]);
+      for (int e = 0; e < kPieces; ++e)
+        raw[p][e] = i < left ? *reinterpret_cast<const uint4 *>(src + (row0 + i) * ld + hk * DK +
+                                                                (piece + 8 * e) * 8)
+                             : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int i = 16 * w + 4 * p + (lane >> 3);
+      float2 x[kPieces][4], sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e) {
+        const uint32_t u[4] = {raw[p][e].x, raw[p][e].y, raw[p][e].z, raw[p][e].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[e][j] = make_float2(bf16_lo(u[j]), bf16_hi(u[j]));
+          sum = fma2(x[e][j], x[e][j], sum);
+        }
       }
-      const uint32_t at = tile_at<kC>(i, j0 / 8 + p);
-      *reinterpret_cast<uint4 *>(sm.head + at) = make_uint4(hi32[0], hi32[1], hi32[2], hi32[3]);
-      *reinterpret_cast<uint4 *>(sm.head + kTile + at) =
-          make_uint4(lo32[0], lo32[1], lo32[2], lo32[3]);
+      float ss = sum.x + sum.y;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+      float mult, inv;
+      token_scale(ss, mult, inv);
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e) {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[j] = h2_bits(__float22half2_rn(mul2(x[e][j], make_float2(mult, mult))));
+        *reinterpret_cast<uint4 *>(sm.key + (is_q ? kKeyBlob<DK> / 2 : 0) +
+                                   tile_at<DK>(i, piece + 8 * e)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      if (d.qk_norm) inv = inv / sqrtf(ss + d.qk_eps);
+      if (is_q) inv *= d.scale;
+      if (piece == 0) sm.t[i * kTLd + (is_q ? kRho : kKappa)] = i < left ? inv : 0.0f;
     }
   }
-  ptx::fence_proxy_async_smem();
   __syncthreads();
-  if (tid == 0) {
-    bulk_store(ws_head + (static_cast<size_t>(slot) * d.v_heads + h) * kHeadBlob,
-               ptx::smem_u32(sm.head), kHeadBlob);
-    if (h % ratio == 0)
-      bulk_store(ws_key + (static_cast<size_t>(slot) * d.qk_heads + hk) * kKeyBlob<DK>,
-                 ptx::smem_u32(sm.key), kKeyBlob<DK>);
-    bulk_store_wait();
+
+  // rows of k k^T or q k^T: the tiles left of the diagonal block, and its two
+  float off[6][4] = {}, dia[2][4] = {};
+  {
+    const uint32_t at = kt + (is_q ? kKeyBlob<DK> / 2 : 0);
+    const int b_row = (lane & 7) + ((lane >> 4) << 3), b_piece = (lane >> 3) & 1;
+#pragma unroll
+    for (int s = 0; s < DK / 16; ++s) {
+      uint32_t a[4], b[4];
+      ldsm4(a, at + tile_at<DK>(16 * w + (lane & 15), 2 * s + (lane >> 4)));
+      ldsm4(b, kt + tile_at<DK>(16 * w + b_row, 2 * s + b_piece));
+      mma16(dia[0], a, b[0], b[1]);
+      mma16(dia[1], a, b[2], b[3]);
+#pragma unroll
+      for (int np = 0; np < 3; ++np)
+        if (np < w) {
+          ldsm4(b, kt + tile_at<DK>(16 * np + b_row, 2 * s + b_piece));
+          mma16(off[2 * np], a, b[0], b[1]);
+          mma16(off[2 * np + 1], a, b[2], b[3]);
+        }
+    }
+  }
+
+  float *vec = reinterpret_cast<float *>(sm.head + 3 * kTile);
+  float *ghi = vec + kVecT * kC;
+  float *L = reinterpret_cast<float *>(sm.head);
+  float *T = sm.t;
+  for (int hh = 0; hh < heads; ++hh) {
+    const int h = h0 + hh;
+    // Decays: sums of g in fp64, in units of log 2, kept as two fp32 terms, so
+    // that differences of large sums keep their digits.
+    if (warp == 4) {
+      const int i = 2 * lane;
+      double g0 = 0.0, g1 = 0.0;
+      float be0 = 0.0f, be1 = 0.0f;
+      if (i < left) {
+        g0 = delta_log_decay(in.g[(row0 + i) * in.g_ld + h]);
+        be0 = in.beta[(row0 + i) * in.beta_ld + h];
+      }
+      if (i + 1 < left) {
+        g1 = delta_log_decay(in.g[(row0 + i + 1) * in.g_ld + h]);
+        be1 = in.beta[(row0 + i + 1) * in.beta_ld + h];
+      }
+      double sum = g0 + g1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double up = __shfl_up_sync(kFull, sum, o);
+        if (lane >= o) sum += up;
+      }
+      const double kLog2E = 1.4426950408889634;
+      const double second = sum * kLog2E, first = (sum - g1) * kLog2E;
+      const double total = __shfl_sync(kFull, second, 31);
+      const float2 sh = make_float2(static_cast<float>(first), static_cast<float>(second));
+      const float2 kap = make_float2(T[i * kTLd + kKappa], T[(i + 1) * kTLd + kKappa]);
+      const float2 rho = make_float2(T[i * kTLd + kRho], T[(i + 1) * kTLd + kRho]);
+      const float2 gamma = make_float2(exp2f(sh.x), exp2f(sh.y));
+      *reinterpret_cast<float2 *>(ghi + i) = sh;
+      T[i * kTLd + kGLo] = static_cast<float>(first - sh.x);
+      T[(i + 1) * kTLd + kGLo] = static_cast<float>(second - sh.y);
+      *reinterpret_cast<float2 *>(vec + kVecBeta * kC + i) = make_float2(be0, be1);
+      *reinterpret_cast<float2 *>(vec + kVecC * kC + i) =
+          make_float2(-be0 * gamma.x * kap.x, -be1 * gamma.y * kap.y);
+      *reinterpret_cast<float2 *>(vec + kVecO * kC + i) =
+          make_float2(rho.x * gamma.x, rho.y * gamma.y);
+      // the update's factors, Gamma_64,j kappa_j, over a power of two above
+      // the largest
+      float2 dd = make_float2(exp2f(static_cast<float>(total - first)) * kap.x,
+                              exp2f(static_cast<float>(total - second)) * kap.y);
+      float dmax = fmaxf(dd.x, dd.y);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dmax = fmaxf(dmax, __shfl_xor_sync(kFull, dmax, o));
+      float up, down;
+      pow2_above(dmax, up, down);
+      *reinterpret_cast<float2 *>(vec + kVecD * kC + i) = make_float2(dd.x * down, dd.y * down);
+      if (lane == 0) {
+        vec[kVecMisc * kC] = exp2f(static_cast<float>(total));  // gamma_64
+        vec[kVecMisc * kC + 2] = up;
+      }
+    }
+    __syncthreads();
+
+    // L = beta_i kappa_i Gamma_ij kappa_j k_i.k_j below the diagonal, P =
+    // rho_i Gamma_ij kappa_j q_i.k_j up to it.  Left of the diagonal block
+    // Gamma_ij = e^{G_i - G_r} e^{G_r - G_j} about the block's first token r:
+    // both factors are decays, and the product underflows only where Gamma does.
+    {
+      const int ref = 16 * w, i0 = ref + g, i1 = i0 + 8;
+      const float rh = ghi[ref], rl = T[ref * kTLd + kGLo];
+      const float h0r = ghi[i0], l0r = T[i0 * kTLd + kGLo], h1r = ghi[i1],
+                  l1r = T[i1 * kTLd + kGLo];
+      float f0, f1;
+      if (is_q) {
+        f0 = T[i0 * kTLd + kRho], f1 = T[i1 * kTLd + kRho];
+      } else {
+        f0 = vec[kVecBeta * kC + i0] * T[i0 * kTLd + kKappa];
+        f1 = vec[kVecBeta * kC + i1] * T[i1 * kTLd + kKappa];
+      }
+      const float a0 = f0 * exp2f((h0r - rh) + (l0r - rl));
+      const float a1 = f1 * exp2f((h1r - rh) + (l1r - rl));
+      // P's row scale from norms: by their scales k and q stay below 2^15, so
+      // |P_ij| <= rho_i max kappa 2^30, which goes to 2^11 or less (room for
+      // decays that grow by up to 2^5).
+      float s0 = 1.0f, s1 = 1.0f;
+      if (is_q) {
+        float kmax = fmaxf(T[lane * kTLd + kKappa], T[(lane + 32) * kTLd + kKappa]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) kmax = fmaxf(kmax, __shfl_xor_sync(kFull, kmax, o));
+        float up0, up1;
+        pow2_above(fabsf(f0) * kmax, up0, s0);
+        pow2_above(fabsf(f1) * kmax, up1, s1);
+        s0 *= 0x1p-19f, s1 *= 0x1p-19f;
+        if (t == 0) vec[kVecP * kC + i0] = up0 * 0x1p19f, vec[kVecP * kC + i1] = up1 * 0x1p19f;
+      }
+      uint8_t *P = sm.head + 2 * kTile + 4 * t;
+      // one tile: eight columns from `col` of this warp's rows
+      const auto put_tile = [&](int col, float2 top, float2 low) {
+        if (is_q) {
+          *reinterpret_cast<__half2 *>(P + tile_at<kC>(i0, col / 8)) =
+              __float22half2_rn(mul2(top, make_float2(s0, s0)));
+          *reinterpret_cast<__half2 *>(P + tile_at<kC>(i1, col / 8)) =
+              __float22half2_rn(mul2(low, make_float2(s1, s1)));
+        } else {
+          *reinterpret_cast<float2 *>(L + l_at(i0, col + 2 * t)) = top;
+          *reinterpret_cast<float2 *>(L + l_at(i1, col + 2 * t)) = low;
+        }
+      };
+#pragma unroll
+      for (int n = 0; n < 6; ++n) {
+        if (n < 2 * w) {
+          const int j = 8 * n + 2 * t;
+          const float2 gj = *reinterpret_cast<const float2 *>(ghi + j);
+          const float *tj = T + j * kTLd;
+          const float2 col =
+              make_float2(tj[kKappa] * exp2f((rh - gj.x) + (rl - tj[kGLo])),
+                          tj[kTLd + kKappa] * exp2f((rh - gj.y) + (rl - tj[kTLd + kGLo])));
+          put_tile(8 * n, mul2(make_float2(off[n][0], off[n][1]), mul2(col, make_float2(a0, a0))),
+                   mul2(make_float2(off[n][2], off[n][3]), mul2(col, make_float2(a1, a1))));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = (e >> 1) ? i1 : i0, j = ref + 8 * q + 2 * t + (e & 1);
+          const float *tj = T + j * kTLd;
+          const float diff = (((e >> 1) ? h1r : h0r) - ghi[j]) + (((e >> 1) ? l1r : l0r) - tj[kGLo]);
+          const bool on = is_q ? j <= i : j < i;
+          v[e] = on ? ((e >> 1) ? f1 : f0) * exp2f(diff) * tj[kKappa] * dia[q][e] : 0.0f;
+        }
+        put_tile(ref + 8 * q, make_float2(v[0], v[1]), make_float2(v[2], v[3]));
+      }
+      if (!is_q) {
+        __syncwarp();
+        // T's 16 x 16 diagonal block by substitution, a lane per column
+        const int c = lane & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float v = i == c ? 1.0f : 0.0f;
+#pragma unroll
+          for (int j = 0; j < i; j += 4) {
+            const float4 l = *reinterpret_cast<const float4 *>(L + l_at(ref + i, ref + j));
+            v = fmaf(-l.x, x[j], v);
+            if (j + 1 < i) v = fmaf(-l.y, x[j + 1], v);
+            if (j + 2 < i) v = fmaf(-l.z, x[j + 2], v);
+            if (j + 3 < i) v = fmaf(-l.w, x[j + 3], v);
+          }
+          x[i] = v;
+        }
+        if (lane < 16)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) T[(ref + i) * kTLd + ref + c] = x[i];
+      }
+    }
+    __syncthreads();
+
+    // [A 0; B C]^-1 = [A^-1 0; -C^-1 B A^-1 C^-1] for blocks of 16, then 32.
+    // B A^-1 waits in the block's own place.
+    const auto l_of = [&](int i, int j) { return L[l_at(i, j)]; };
+    const auto t_of = [&](int i, int j) { return T[i * kTLd + j]; };
+    const auto put = [&](const float(&acc)[4], int r0, int c0, float sign) {
+      float *p = T + (r0 + g) * kTLd + c0 + 2 * t;
+      *reinterpret_cast<float2 *>(p) = make_float2(sign * acc[0], sign * acc[1]);
+      *reinterpret_cast<float2 *>(p + 8 * kTLd) = make_float2(sign * acc[2], sign * acc[3]);
+    };
+    float acc[4];
+    if (warp < 4) {
+      // a warp's eight columns of B A^-1 are all that it reads of it
+      const int o = 32 * (warp >> 1), c0 = o + 8 * (warp & 1);
+      product(acc, o + 16, c0, c0, o + 16, l_of, t_of, lane);
+      put(acc, o + 16, c0, 1.0f);
+      __syncwarp();
+      product(acc, o + 16, c0, o + 16, o + 32, t_of, t_of, lane);
+      __syncwarp();
+      put(acc, o + 16, c0, -1.0f);
+    }
+    __syncthreads();
+    {
+      const int r0 = 32 + 16 * (warp >> 2), c0 = 8 * (warp & 3);
+      product(acc, r0, c0, c0, 32, l_of, t_of, lane);  // T(k, c) = 0 for k < c
+      put(acc, r0, c0, 1.0f);
+      __syncthreads();
+      product(acc, r0, c0, 32, r0 + 16, t_of, t_of, lane);
+      __syncthreads();
+      put(acc, r0, c0, -1.0f);
+    }
+    __syncthreads();
+
+    // T's rows as two fp16 terms in L's place, four threads a row, and a power
+    // of two above every row's sum
+    {
+      const int i = tid >> 2, q = tid & 3;
+      float2 v[2][4];
+      float mx = 0.0f, sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int p = q + 4 * e;
+        if (p / 2 <= i / 16) {
+          const float4 a = *reinterpret_cast<const float4 *>(T + i * kTLd + 8 * p);
+          const float4 b = *reinterpret_cast<const float4 *>(T + i * kTLd + 8 * p + 4);
+          v[e][0] = make_float2(a.x, a.y), v[e][1] = make_float2(a.z, a.w);
+          v[e][2] = make_float2(b.x, b.y), v[e][3] = make_float2(b.z, b.w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            mx = max3_abs(mx, v[e][j].x, v[e][j].y);
+            sum += fabsf(v[e][j].x) + fabsf(v[e][j].y);
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+        sum += __shfl_xor_sync(kFull, sum, o);
+      }
+      float most = sum;
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
+      if (lane == 0) red[warp] = most;
+      __syncthreads();
+      most = red[0];
+#pragma unroll
+      for (int o = 1; o < kPrepThreads / 32; ++o) most = fmaxf(most, red[o]);
+      float mult, inv, up, down;
+      pow2_above(most, up, down);
+      pow2_scale(mx, mult, inv);
+      if (q == 0) vec[kVecT * kC + i] = inv * down;
+      if (tid == 0) vec[kVecMisc * kC + 1] = up;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int p = q + 4 * e;
+        if (p / 2 <= i / 16) {
+          uint32_t hw[4], lw[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) split_h2(mul2(v[e][j], make_float2(mult, mult)), hw[j], lw[j]);
+          const uint32_t at = tile_at<kC>(i, p);
+          *reinterpret_cast<uint4 *>(sm.head + at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+          *reinterpret_cast<uint4 *>(sm.head + kTile + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+        }
+      }
+    }
+    ptx::fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      bulk_store(ws_head + (static_cast<size_t>(slot) * d.v_heads + h) * kHeadBlob,
+                 ptx::smem_u32(sm.head), kHeadBlob);
+      if (h % ratio == 0)
+        bulk_store(ws_key + (static_cast<size_t>(slot) * d.qk_heads + hk) * kKeyBlob<DK>,
+                   ptx::smem_u32(sm.key), kKeyBlob<DK>);
+      bulk_store_wait();
+    }
+    if (hh + 1 < heads) __syncthreads();  // the copy has left the head's place
   }
 }
 
@@ -842,6 +927,10 @@ cudaError_t launch_chain(const moe_delta_dims &d, const moe_delta_inputs &in, co
   return cudaGetLastError();
 }
 
+// Chunks times key heads from which a CTA of the first kernel serves all the
+// value heads of its key head.
+constexpr size_t kPrepShare = 1000;
+
 template <int DK>
 cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const DeltaSeqs &seq,
                    uint8_t *ws, moe_bf16 *out, int64_t out_ld, cudaStream_t s) {
@@ -852,8 +941,10 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(delta_prep_kernel<DK>, kSmem, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(slots), d.v_heads);
-  delta_prep_kernel<DK><<<grid, kPrepThreads, kSmem, s>>>(d, in, seq, ws, ws_key, ws_head);
+  const int ratio = d.v_heads / d.qk_heads;
+  const int heads = slots * d.qk_heads >= kPrepShare ? ratio : 1;
+  const dim3 grid(static_cast<unsigned>(slots), d.v_heads / heads);
+  delta_prep_kernel<DK><<<grid, kPrepThreads, kSmem, s>>>(d, in, seq, heads, ws, ws_key, ws_head);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t groups = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / 16);
   if (groups <= 2 * 152)
