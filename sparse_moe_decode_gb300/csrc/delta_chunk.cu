@@ -511,7 +511,11 @@ struct ChainCfg {
   // one CTA per SM: the ring takes what the groups leave of its shared memory
   static constexpr int kStageBytes = kKeyBlob<DK> + kHeadBlob;
   static constexpr int kStages = GROUPS >= 4 && DK == 128 ? 2 : 3;
-  static constexpr int kThreads = 32 * (3 * GROUPS + 1);
+  // With stages to spare the output warp waits for a chunk's operands half a
+  // chunk ahead and the group's barrier passes them on; otherwise the chain
+  // warps wait for them where they need them.
+  static constexpr bool kAhead = kStages >= 3;
+  static constexpr int kThreads = 32 * 3 * GROUPS;
   static constexpr int kSmem =
       kStages * kStageBytes + GROUPS * static_cast<int>(sizeof(GroupSmem<DK>)) + 64;
 };
@@ -598,34 +602,12 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   }
   __syncthreads();
 
-  if (warp == 3 * GROUPS) {
-    // producer: one stage per chunk, keys and queries, then the head's part
-    if (lane == 0) {
-      int issued = 0;
-      for (; issued < chunks; ++issued) {
-        const int s = issued % kStages, use = issued / kStages;
-        if (use > 0 && !ptx::mbar_wait(&empty[s], (use - 1) & 1, abort_flag, budget_ns)) break;
-        const uint32_t dst = ptx::smem_u32(ring + s * Cfg::kStageBytes);
-        const size_t at = static_cast<size_t>(base) + issued;
-        ptx::mbar_expect_tx(&full[s], Cfg::kStageBytes);
-        bulk_load(dst, ws_key + (at * d.qk_heads + hk) * kKeyBlob<DK>, kKeyBlob<DK>, &full[s]);
-        bulk_load(dst + kKeyBlob<DK>, ws_head + (at * d.v_heads + h) * kHeadBlob, kHeadBlob,
-                  &full[s]);
-      }
-      // copies in flight land before the CTA's shared memory is given up
-      int ignore = 0;
-      for (int c = max(0, issued - kStages); c < issued; ++c)
-        ptx::mbar_wait(&full[c % kStages], (c / kStages) & 1, &ignore, ptx::kDrainBudgetNs);
-      if (*reinterpret_cast<volatile int *>(abort_flag)) set_status(seq.status, MOE_DEV_TIMEOUT);
-    }
-    return;
-  }
-
   // Chain warps 2 g, 2 g + 1 (the halves of the key channels), output warp
   // 2 GROUPS + g.  The three warps of a group meet twice per chunk: bar_x
-  // (both halves of S k^T and the copy of S are there), bar_w (u is there).
-  // Every buffer of the group is written before one of the two, read between
-  // it and the other, and so free again when its writer comes back to it.
+  // (both halves of S k^T and the copy of S are there), bar_w (u is there, and
+  // the next chunk's values).  Every buffer of the group is written before one
+  // of the two, read between it and the other, and so free again when its
+  // writer comes back to it.
   const bool chain = warp < 2 * GROUPS;
   const int group = chain ? warp >> 1 : warp - 2 * GROUPS, half = warp & 1;
   GroupSmem<DK> &gs = groups[group];
@@ -640,6 +622,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   const int bt_row = (lane & 7) + (((lane >> 3) & 1) << 3), bt_piece = lane >> 4;
 
   if (chain) {
+    constexpr int kSteps = kHalf / 16;
     const int64_t at = ((static_cast<int64_t>(r.slot) * d.v_heads + h) * d.v_dim + dv0 + g) * DK +
                        half * kHalf + 2 * t;
     Acc S[kHalf / 8];
@@ -651,49 +634,57 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
         S[n].low = *reinterpret_cast<const float2 *>(seq.state_in + at + 8 * DK + 8 * n);
       }
     }
-    const uint32_t v_smem = ptx::smem_u32(gs.v[0]);
-    // this half's 32 tokens of the group's channels of chunk c, zeros past the end
-    const auto fetch_v = [&](int c) {
-      if (c < chunks) {
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int i = half * 32 + p * 16 + (lane >> 1), piece = lane & 1;
-          const bool live = c * kC + i < r.len;
-          const int64_t row = static_cast<int64_t>(r.start) + (live ? c * kC + i : 0);
-          cp_async16(v_smem + (c % 3) * kC * 32 + row32_at(i, piece),
-                     in.v + row * in.v_ld + h * d.v_dim + dv0 + piece * 8, live);
-        }
-      }
-      cp_async_commit();
-    };
-    fetch_v(0);
-    fetch_v(1);
+    const uint32_t v_at =
+        ptx::smem_u32(gs.v[0]) + row32_at((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+    // T's fragments that this half needs (below)
+    const int np_of[2] = {half ? 1 : 0, half ? 2 : 3};
+    if (chunks) bar_sync(bar_w, 96);
+    float m0, m1, i0, i1;
+    row_scales(S, m0, m1, i0, i1);
     for (int c = 0; c < chunks; ++c) {
       const int st = c % kStages;
       const uint32_t kt = ptx::smem_u32(ring + st * Cfg::kStageBytes);
       const uint32_t tt = kt + kKeyBlob<DK>;
       const float *vec =
           reinterpret_cast<const float *>(ring + st * Cfg::kStageBytes + kKeyBlob<DK> + 3 * kTile);
-      fetch_v(c + 2);
-      float m0, m1, i0, i1;
-      row_scales(S, m0, m1, i0, i1);
+      if (!Cfg::kAhead && !dead)
+        dead = !ptx::mbar_wait(&full[st], (c / kStages) & 1, abort_flag, budget_ns);
       gs.s_inv[half][lane] = make_float2(i0, i1);
-      if (!dead) dead = !ptx::mbar_wait(&full[st], (c / kStages) & 1, abort_flag, budget_ns);
       // this half's share of X^T = S k^T (16 value channels x 64 tokens)
       Acc X[8] = {};
 #pragma unroll
-      for (int s = 0; s < kHalf / 16; ++s) {
-        uint32_t hi[4], lo[4];
+      for (int s = 0; s < kSteps; ++s) {
+        uint32_t hi[4], lo[4], bb[4][4];
+#pragma unroll
+        for (int np = 0; np < 4; ++np)
+          ldsm4(bb[np], kt + tile_at<DK>(16 * np + b_row, half * (kHalf / 8) + 2 * s + b_piece));
         split_frag(S[2 * s], S[2 * s + 1], make_float2(m0, m0), make_float2(m1, m1), hi, lo);
-        gs.s_frag[half * (kHalf / 16) + s][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        gs.s_frag[half * kSteps + s][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
-          uint32_t bb[4];
-          ldsm4(bb, kt + tile_at<DK>(16 * np + b_row, half * (kHalf / 8) + 2 * s + b_piece));
-          mma16(X[2 * np], hi, bb[0], bb[1]);
-          mma16(X[2 * np + 1], hi, bb[2], bb[3]);
-          mma16(X[2 * np], lo, bb[0], bb[1]);
-          mma16(X[2 * np + 1], lo, bb[2], bb[3]);
+          mma16(X[2 * np], hi, bb[np][0], bb[np][1]);
+          mma16(X[2 * np + 1], hi, bb[np][2], bb[np][3]);
+        }
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          mma16(X[2 * np], lo, bb[np][0], bb[np][1]);
+          mma16(X[2 * np + 1], lo, bb[np][2], bb[np][3]);
+        }
+      }
+      // beta_i v_i
+      Acc Y[8];
+      float2 cc[8];
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t vv[4];
+        ldsm4_t(vv, v_at + (c % 3) * kC * 32 + np * 16 * 32);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int n = 2 * np + q;
+          const float2 be = *reinterpret_cast<const float2 *>(vec + kVecBeta * kC + 8 * n + 2 * t);
+          cc[n] = *reinterpret_cast<const float2 *>(vec + kVecC * kC + 8 * n + 2 * t);
+          Y[n].top = mul2(be, make_float2(bf16_lo(vv[2 * q]), bf16_hi(vv[2 * q])));
+          Y[n].low = mul2(be, make_float2(bf16_lo(vv[2 * q + 1]), bf16_hi(vv[2 * q + 1])));
         }
       }
 #pragma unroll
@@ -701,62 +692,56 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
         X[n].top = mul2(X[n].top, make_float2(i0, i0));
         X[n].low = mul2(X[n].low, make_float2(i1, i1));
         gs.x_part[half][n][lane] = make_float4(X[n].top.x, X[n].top.y, X[n].low.x, X[n].low.y);
+        Y[n].top = fma2(cc[n], X[n].top, Y[n].top);
+        Y[n].low = fma2(cc[n], X[n].low, Y[n].low);
       }
-      cp_async_wait<2>();
       bar_sync(bar_x, 96);
-      // x_i = beta_i v_i - c_i (S k_i); vec holds -c_i
+      // x_i = beta_i v_i - c_i (S k_i), with the other half's share; vec holds -c_i
+      {
+        float4 y[8];
 #pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t vv[4];
-        ldsm4_t(vv, v_smem + (c % 3) * kC * 32 +
-                        row32_at(16 * np + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1));
+        for (int n = 0; n < 8; ++n) y[n] = gs.x_part[half ^ 1][n][lane];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int n = 2 * np + q;
-          const float2 be = *reinterpret_cast<const float2 *>(vec + kVecBeta * kC + 8 * n + 2 * t);
-          const float2 cc = *reinterpret_cast<const float2 *>(vec + kVecC * kC + 8 * n + 2 * t);
-          const float4 y = gs.x_part[half ^ 1][n][lane];
-          const float2 one = make_float2(1.0f, 1.0f);
-          X[n].top = fma2(X[n].top, one, make_float2(y.x, y.y));
-          X[n].low = fma2(X[n].low, one, make_float2(y.z, y.w));
-          X[n].top = fma2(cc, X[n].top,
-                          mul2(be, make_float2(bf16_lo(vv[2 * q]), bf16_hi(vv[2 * q]))));
-          X[n].low = fma2(cc, X[n].low,
-                          mul2(be, make_float2(bf16_lo(vv[2 * q + 1]), bf16_hi(vv[2 * q + 1]))));
+        for (int n = 0; n < 8; ++n) {
+          X[n].top = fma2(cc[n], make_float2(y[n].x, y[n].y), Y[n].top);
+          X[n].low = fma2(cc[n], make_float2(y[n].z, y[n].w), Y[n].low);
         }
       }
       // u = T x.  Column tiles 2 np, 2 np + 1 of u^T take the tokens of k16
       // steps 0 .. np; the halves take np = 0 and 3, and np = 1 and 2: five
       // steps each.
+      uint32_t th[4][2][4], tl[4][2][4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (s <= np_of[j]) {
+            const uint32_t a = tt + tile_at<kC>(16 * np_of[j] + b_row, 2 * s + b_piece);
+            ldsm4(th[s][j], a);
+            ldsm4(tl[s][j], a + kTile);
+          }
       row_scales(X, m0, m1, i0, i1);
-      Acc U[2][2] = {};
-      const int np_of[2] = {half ? 1 : 0, half ? 2 : 3};
+      Acc U[2][2] = {}, V[2][2] = {}, W[2][2] = {};
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         uint32_t hi[4], lo[4];
         split_frag(X[2 * s], X[2 * s + 1], make_float2(m0, m0), make_float2(m1, m1), hi, lo);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (s <= np_of[j]) {
-            uint32_t th[4], tl[4];
-            const uint32_t a = tt + tile_at<kC>(16 * np_of[j] + b_row, 2 * s + b_piece);
-            ldsm4(th, a);
-            ldsm4(tl, a + kTile);
-            mma16(U[j][0], hi, tl[0], tl[1]);
-            mma16(U[j][1], hi, tl[2], tl[3]);
-            mma16(U[j][0], lo, th[0], th[1]);
-            mma16(U[j][1], lo, th[2], th[3]);
-            mma16(U[j][0], hi, th[0], th[1]);
-            mma16(U[j][1], hi, th[2], th[3]);
-          }
-        }
+        for (int j = 0; j < 2; ++j)
+          if (s <= np_of[j])
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              mma16(U[j][q], hi, th[s][j][2 * q], th[s][j][2 * q + 1]);
+              mma16(V[j][q], hi, tl[s][j][2 * q], tl[s][j][2 * q + 1]);
+              mma16(W[j][q], lo, th[s][j][2 * q], th[s][j][2 * q + 1]);
+            }
       }
       // Rescaled by T's row scales and down by a bound of its row sums, u
       // stays below 2^15 (the scale of x), and so does w_j = Gamma_64,j
       // kappa_j u_j over the largest such factor.
-      const float tau = vec[kVecMisc * kC + 1];
+      const float gamma = vec[kVecMisc * kC], tau = vec[kVecMisc * kC + 1];
+      const float back = tau * vec[kVecMisc * kC + 2];
       gs.u_inv[lane] = make_float2(i0 * tau, i1 * tau);
-      uint32_t wh[4][4], wl[4][4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         uint32_t f[4], hi[4], lo[4];
@@ -765,50 +750,67 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
           const int n = 2 * np_of[j] + q;
           const float2 ts = *reinterpret_cast<const float2 *>(vec + kVecT * kC + 8 * n + 2 * t);
           const float2 dd = *reinterpret_cast<const float2 *>(vec + kVecD * kC + 8 * n + 2 * t);
-          const float2 top = mul2(U[j][q].top, ts), low = mul2(U[j][q].low, ts);
+          const float2 one = make_float2(1.0f, 1.0f);
+          const float2 top =
+              mul2(fma2(U[j][q].top, one, fma2(V[j][q].top, one, W[j][q].top)), ts);
+          const float2 low =
+              mul2(fma2(U[j][q].low, one, fma2(V[j][q].low, one, W[j][q].low)), ts);
           f[2 * q] = h2_bits(__float22half2_rn(top));
           f[2 * q + 1] = h2_bits(__float22half2_rn(low));
           split_h2(mul2(top, dd), hi[2 * q], lo[2 * q]);
           split_h2(mul2(low, dd), hi[2 * q + 1], lo[2 * q + 1]);
         }
-        gs.u_frag[np_of[j]][lane] = make_uint4(f[0], f[1], f[2], f[3]);
         gs.w_frag[np_of[j]][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         gs.w_frag[np_of[j]][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        gs.u_frag[np_of[j]][lane] = make_uint4(f[0], f[1], f[2], f[3]);
       }
       bar_sync(bar_w, 96);
-      // S = gamma S + sum_j w_j k_j^T
+      // S = gamma S + sum_j w_j k_j^T, 32 key channels at a time
+      uint32_t wh[4][4], wl[4][4];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const uint4 a = gs.w_frag[s][0][lane], e = gs.w_frag[s][1][lane];
         wh[s][0] = a.x, wh[s][1] = a.y, wh[s][2] = a.z, wh[s][3] = a.w;
         wl[s][0] = e.x, wl[s][1] = e.y, wl[s][2] = e.z, wl[s][3] = e.w;
       }
-      const float gamma = vec[kVecMisc * kC], back = tau * vec[kVecMisc * kC + 2];
       const float2 gamma2 = make_float2(gamma, gamma);
       const float2 b0 = make_float2(i0 * back, i0 * back), b1 = make_float2(i1 * back, i1 * back);
+      float a0 = 0.0f, a1 = 0.0f;
 #pragma unroll
-      for (int np = 0; np < kHalf / 16; ++np) {
-        Acc acc[2] = {};
+      for (int np = 0; np < kSteps; np += 2) {
+        Acc acc[4] = {};
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          uint32_t bb[4];
-          ldsm4_t(bb, kt + tile_at<DK>(16 * s + bt_row, half * (kHalf / 8) + 2 * np + bt_piece));
-          mma16(acc[0], wh[s], bb[0], bb[1]);
-          mma16(acc[1], wh[s], bb[2], bb[3]);
-          mma16(acc[0], wl[s], bb[0], bb[1]);
-          mma16(acc[1], wl[s], bb[2], bb[3]);
+          uint32_t bb[2][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            ldsm4_t(bb[j], kt + tile_at<DK>(16 * s + bt_row,
+                                            half * (kHalf / 8) + 2 * (np + j) + bt_piece));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            mma16(acc[2 * j], wh[s], bb[j][0], bb[j][1]);
+            mma16(acc[2 * j + 1], wh[s], bb[j][2], bb[j][3]);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            mma16(acc[2 * j], wl[s], bb[j][0], bb[j][1]);
+            mma16(acc[2 * j + 1], wl[s], bb[j][2], bb[j][3]);
+          }
         }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < 4; ++q) {
           Acc &a = S[2 * np + q];
           a.top = fma2(acc[q].top, b0, mul2(gamma2, a.top));
           a.low = fma2(acc[q].low, b1, mul2(gamma2, a.low));
+          a0 = max3_abs(a0, a.top.x, a.top.y);
+          a1 = max3_abs(a1, a.low.x, a.low.y);
         }
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&empty[st]);
+      pow2_scale(quad_max(a0), m0, i0);
+      pow2_scale(quad_max(a1), m1, i1);
     }
-    cp_async_wait<0>();
     if (seq.state_out) {
 #pragma unroll
       for (int n = 0; n < kHalf / 8; ++n) {
@@ -819,15 +821,62 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
     return;
   }
 
-  // output warp: o_i = rho_i gamma_i (S q_i) + sum_j P_ij u_j
-  const uint32_t o_smem = ptx::smem_u32(gs.o);
+  // Output warp: o_i = rho_i gamma_i (S q_i) + sum_j P_ij u_j.  It also brings
+  // in the group's values, and the first one the ring's stages.
+  const bool producer = group == 0 && lane == 0;
+  int issued = 0;
+  const auto issue = [&](int c) {  // the operands of chunk c: keys and queries, the head's part
+    const int s = c % kStages;
+    const uint32_t dst = ptx::smem_u32(ring + s * Cfg::kStageBytes);
+    const size_t at = static_cast<size_t>(base) + c;
+    ptx::mbar_expect_tx(&full[s], Cfg::kStageBytes);
+    bulk_load(dst, ws_key + (at * d.qk_heads + hk) * kKeyBlob<DK>, kKeyBlob<DK>, &full[s]);
+    bulk_load(dst + kKeyBlob<DK>, ws_head + (at * d.v_heads + h) * kHeadBlob, kHeadBlob, &full[s]);
+    issued = c + 1;
+  };
+  const uint32_t v_smem = ptx::smem_u32(gs.v[0]);
+  const moe_bf16 *v_src = in.v + static_cast<int64_t>(r.start) * in.v_ld + h * d.v_dim + dv0;
+  const auto fetch_v = [&](int c) {  // the group's channels of chunk c, zeros past the end
+    if (c < chunks) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int i = p * 16 + (lane >> 1), piece = lane & 1, row = c * kC + i;
+        const bool live = row < r.len;
+        cp_async16(v_smem + (c % 3) * kC * 32 + row32_at(i, piece),
+                   v_src + (live ? row * in.v_ld : 0) + piece * 8, live);
+      }
+    }
+    cp_async_commit();
+  };
+  const auto wait_full = [&](int c) {
+    if (!dead) dead = !ptx::mbar_wait(&full[c % kStages], (c / kStages) & 1, abort_flag, budget_ns);
+  };
+  if (chunks) {
+    if (producer)
+      for (int c = 0; c < min(chunks, kStages); ++c) issue(c);
+    fetch_v(0);
+    fetch_v(1);
+    wait_full(0);
+    cp_async_wait<1>();
+    bar_sync(bar_w, 96);
+  }
+  const uint32_t o_at = ptx::smem_u32(gs.o) + row32_at((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+  moe_bf16 *o_dst = out + static_cast<int64_t>(r.start) * out_ld + h * d.v_dim + dv0;
   for (int c = 0; c < chunks; ++c) {
     const int st = c % kStages;
     const uint32_t qt = ptx::smem_u32(ring + st * Cfg::kStageBytes) + kKeyBlob<DK> / 2;
     const uint32_t pt = qt + kKeyBlob<DK> / 2 + 2 * kTile;
     const float *vec =
         reinterpret_cast<const float *>(ring + st * Cfg::kStageBytes + kKeyBlob<DK> + 3 * kTile);
-    if (!dead) dead = !ptx::mbar_wait(&full[st], (c / kStages) & 1, abort_flag, budget_ns);
+    if (producer && c > 0 && c - 1 + kStages < chunks && !dead) {
+      // the stage that chunk c - 1 has left
+      dead = !ptx::mbar_wait(&empty[(c - 1) % kStages], ((c - 1) / kStages) & 1, abort_flag,
+                             budget_ns);
+      if (!dead) issue(c - 1 + kStages);
+    }
+    __syncwarp();
+    fetch_v(c + 2);
+    if (!Cfg::kAhead) wait_full(c);
     bar_sync(bar_x, 96);
     Acc O[8] = {};
 #pragma unroll
@@ -853,6 +902,9 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
         O[n].low = fma2(acc[n].low, make_float2(si.y, si.y), O[n].low);
       }
     }
+    if (Cfg::kAhead && c + 1 < chunks) wait_full(c + 1);
+    cp_async_wait<1>();
+    __syncwarp();
     bar_sync(bar_w, 96);
     const float2 ui = gs.u_inv[lane];
     Acc I[8] = {};
@@ -882,20 +934,26 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
         w[2 * q + 1] = pack_bf16(low.x, low.y);
       }
       // transposed back: token rows of 16 channels
-      stsm4_t(o_smem + row32_at(16 * np + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1), w[0],
-              w[1], w[2], w[3]);
+      stsm4_t(o_at + np * 16 * 32, w[0], w[1], w[2], w[3]);
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&empty[st]);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      const int i = p * 16 + (lane >> 1), piece = lane & 1;
-      if (c * kC + i < r.len)
-        *reinterpret_cast<uint4 *>(
-            out + (static_cast<int64_t>(r.start) + c * kC + i) * out_ld + h * d.v_dim + dv0 +
-            piece * 8) = *reinterpret_cast<const uint4 *>(gs.o + row32_at(i, piece));
+      const int i = p * 16 + (lane >> 1), piece = lane & 1, row = c * kC + i;
+      if (row < r.len)
+        *reinterpret_cast<uint4 *>(o_dst + row * out_ld + piece * 8) =
+            *reinterpret_cast<const uint4 *>(gs.o + row32_at(i, piece));
     }
     __syncwarp();
+  }
+  cp_async_wait<0>();
+  if (producer) {
+    // copies in flight land before the CTA's shared memory is given up
+    int ignore = 0;
+    for (int c = max(0, issued - kStages); c < issued; ++c)
+      ptx::mbar_wait(&full[c % kStages], (c / kStages) & 1, &ignore, ptx::kDrainBudgetNs);
+    if (*reinterpret_cast<volatile int *>(abort_flag)) set_status(seq.status, MOE_DEV_TIMEOUT);
   }
 }
 
