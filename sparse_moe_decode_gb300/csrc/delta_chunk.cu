@@ -515,7 +515,11 @@ struct ChainCfg {
   // chunk ahead and the group's barrier passes them on; otherwise the chain
   // warps wait for them where they need them.
   static constexpr bool kAhead = kStages >= 3;
-  static constexpr int kThreads = 32 * 3 * GROUPS;
+  // A warp of its own for the ring where that leaves the others registers
+  // enough (four warps share a quarter of the SM's); else the first output
+  // warp brings the stages in.
+  static constexpr bool kProducer = GROUPS < 4;
+  static constexpr int kThreads = 32 * (3 * GROUPS + kProducer);
   static constexpr int kSmem =
       kStages * kStageBytes + GROUPS * static_cast<int>(sizeof(GroupSmem<DK>)) + 64;
 };
@@ -602,6 +606,35 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   }
   __syncthreads();
 
+  const auto issue = [&](int c) {  // the operands of chunk c: keys and queries, the head's part
+    const int s = c % kStages;
+    const uint32_t dst = ptx::smem_u32(ring + s * Cfg::kStageBytes);
+    const size_t at = static_cast<size_t>(base) + c;
+    ptx::mbar_expect_tx(&full[s], Cfg::kStageBytes);
+    bulk_load(dst, ws_key + (at * d.qk_heads + hk) * kKeyBlob<DK>, kKeyBlob<DK>, &full[s]);
+    bulk_load(dst + kKeyBlob<DK>, ws_head + (at * d.v_heads + h) * kHeadBlob, kHeadBlob, &full[s]);
+  };
+  // Waits for the stage that chunk c - kStages has left; false if it gave up.
+  const auto wait_empty = [&](int c) {
+    return c < kStages || ptx::mbar_wait(&empty[c % kStages], (c / kStages - 1) & 1, abort_flag,
+                                         budget_ns);
+  };
+  // Copies in flight land before the CTA's shared memory is given up.
+  const auto drain = [&](int issued) {
+    int ignore = 0;
+    for (int c = max(0, issued - kStages); c < issued; ++c)
+      ptx::mbar_wait(&full[c % kStages], (c / kStages) & 1, &ignore, ptx::kDrainBudgetNs);
+    if (*reinterpret_cast<volatile int *>(abort_flag)) set_status(seq.status, MOE_DEV_TIMEOUT);
+  };
+  if (Cfg::kProducer && warp == 3 * GROUPS) {
+    if (lane == 0) {
+      int c = 0;
+      for (; c < chunks && wait_empty(c); ++c) issue(c);
+      drain(c);
+    }
+    return;
+  }
+
   // Chain warps 2 g, 2 g + 1 (the halves of the key channels), output warp
   // 2 GROUPS + g.  The three warps of a group meet twice per chunk: bar_x
   // (both halves of S k^T and the copy of S are there), bar_w (u is there, and
@@ -651,7 +684,8 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
         dead = !ptx::mbar_wait(&full[st], (c / kStages) & 1, abort_flag, budget_ns);
       gs.s_inv[half][lane] = make_float2(i0, i1);
       // this half's share of X^T = S k^T (16 value channels x 64 tokens)
-      Acc X[8] = {};
+      Acc X[8] = {}, Y[8];
+      float2 cc[8];
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         uint32_t hi[4], lo[4], bb[4][4];
@@ -670,21 +704,20 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
           mma16(X[2 * np], lo, bb[np][0], bb[np][1]);
           mma16(X[2 * np + 1], lo, bb[np][2], bb[np][3]);
         }
-      }
-      // beta_i v_i
-      Acc Y[8];
-      float2 cc[8];
+        if (s > 0) continue;
+        // beta_i v_i, in the shadow of the products
 #pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t vv[4];
-        ldsm4_t(vv, v_at + (c % 3) * kC * 32 + np * 16 * 32);
+        for (int np = 0; np < 4; ++np) {
+          uint32_t vv[4];
+          ldsm4_t(vv, v_at + (c % 3) * kC * 32 + np * 16 * 32);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int n = 2 * np + q;
-          const float2 be = *reinterpret_cast<const float2 *>(vec + kVecBeta * kC + 8 * n + 2 * t);
-          cc[n] = *reinterpret_cast<const float2 *>(vec + kVecC * kC + 8 * n + 2 * t);
-          Y[n].top = mul2(be, make_float2(bf16_lo(vv[2 * q]), bf16_hi(vv[2 * q])));
-          Y[n].low = mul2(be, make_float2(bf16_lo(vv[2 * q + 1]), bf16_hi(vv[2 * q + 1])));
+          for (int q = 0; q < 2; ++q) {
+            const int n = 2 * np + q;
+            const float2 be = *reinterpret_cast<const float2 *>(vec + kVecBeta * kC + 8 * n + 2 * t);
+            cc[n] = *reinterpret_cast<const float2 *>(vec + kVecC * kC + 8 * n + 2 * t);
+            Y[n].top = mul2(be, make_float2(bf16_lo(vv[2 * q]), bf16_hi(vv[2 * q])));
+            Y[n].low = mul2(be, make_float2(bf16_lo(vv[2 * q + 1]), bf16_hi(vv[2 * q + 1])));
+          }
         }
       }
 #pragma unroll
@@ -720,6 +753,17 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
             ldsm4(th[s][j], a);
             ldsm4(tl[s][j], a + kTile);
           }
+      const float gamma = vec[kVecMisc * kC], tau = vec[kVecMisc * kC + 1];
+      const float back = tau * vec[kVecMisc * kC + 2];
+      float2 ts[2][2], dd[2][2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int at_n = 8 * (2 * np_of[j] + q) + 2 * t;
+          ts[j][q] = *reinterpret_cast<const float2 *>(vec + kVecT * kC + at_n);
+          dd[j][q] = *reinterpret_cast<const float2 *>(vec + kVecD * kC + at_n);
+        }
       row_scales(X, m0, m1, i0, i1);
       Acc U[2][2] = {}, V[2][2] = {}, W[2][2] = {};
 #pragma unroll
@@ -739,26 +783,21 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
       // Rescaled by T's row scales and down by a bound of its row sums, u
       // stays below 2^15 (the scale of x), and so does w_j = Gamma_64,j
       // kappa_j u_j over the largest such factor.
-      const float gamma = vec[kVecMisc * kC], tau = vec[kVecMisc * kC + 1];
-      const float back = tau * vec[kVecMisc * kC + 2];
       gs.u_inv[lane] = make_float2(i0 * tau, i1 * tau);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         uint32_t f[4], hi[4], lo[4];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const int n = 2 * np_of[j] + q;
-          const float2 ts = *reinterpret_cast<const float2 *>(vec + kVecT * kC + 8 * n + 2 * t);
-          const float2 dd = *reinterpret_cast<const float2 *>(vec + kVecD * kC + 8 * n + 2 * t);
           const float2 one = make_float2(1.0f, 1.0f);
           const float2 top =
-              mul2(fma2(U[j][q].top, one, fma2(V[j][q].top, one, W[j][q].top)), ts);
+              mul2(fma2(U[j][q].top, one, fma2(V[j][q].top, one, W[j][q].top)), ts[j][q]);
           const float2 low =
-              mul2(fma2(U[j][q].low, one, fma2(V[j][q].low, one, W[j][q].low)), ts);
+              mul2(fma2(U[j][q].low, one, fma2(V[j][q].low, one, W[j][q].low)), ts[j][q]);
           f[2 * q] = h2_bits(__float22half2_rn(top));
           f[2 * q + 1] = h2_bits(__float22half2_rn(low));
-          split_h2(mul2(top, dd), hi[2 * q], lo[2 * q]);
-          split_h2(mul2(low, dd), hi[2 * q + 1], lo[2 * q + 1]);
+          split_h2(mul2(top, dd[j][q]), hi[2 * q], lo[2 * q]);
+          split_h2(mul2(low, dd[j][q]), hi[2 * q + 1], lo[2 * q + 1]);
         }
         gs.w_frag[np_of[j]][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         gs.w_frag[np_of[j]][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -822,18 +861,9 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   }
 
   // Output warp: o_i = rho_i gamma_i (S q_i) + sum_j P_ij u_j.  It also brings
-  // in the group's values, and the first one the ring's stages.
-  const bool producer = group == 0 && lane == 0;
+  // in the group's values.
+  const bool producer = !Cfg::kProducer && group == 0 && lane == 0;
   int issued = 0;
-  const auto issue = [&](int c) {  // the operands of chunk c: keys and queries, the head's part
-    const int s = c % kStages;
-    const uint32_t dst = ptx::smem_u32(ring + s * Cfg::kStageBytes);
-    const size_t at = static_cast<size_t>(base) + c;
-    ptx::mbar_expect_tx(&full[s], Cfg::kStageBytes);
-    bulk_load(dst, ws_key + (at * d.qk_heads + hk) * kKeyBlob<DK>, kKeyBlob<DK>, &full[s]);
-    bulk_load(dst + kKeyBlob<DK>, ws_head + (at * d.v_heads + h) * kHeadBlob, kHeadBlob, &full[s]);
-    issued = c + 1;
-  };
   const uint32_t v_smem = ptx::smem_u32(gs.v[0]);
   const moe_bf16 *v_src = in.v + static_cast<int64_t>(r.start) * in.v_ld + h * d.v_dim + dv0;
   const auto fetch_v = [&](int c) {  // the group's channels of chunk c, zeros past the end
@@ -853,7 +883,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   };
   if (chunks) {
     if (producer)
-      for (int c = 0; c < min(chunks, kStages); ++c) issue(c);
+      for (; issued < min(chunks, kStages); ++issued) issue(issued);
     fetch_v(0);
     fetch_v(1);
     wait_full(0);
@@ -868,13 +898,11 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
     const uint32_t pt = qt + kKeyBlob<DK> / 2 + 2 * kTile;
     const float *vec =
         reinterpret_cast<const float *>(ring + st * Cfg::kStageBytes + kKeyBlob<DK> + 3 * kTile);
-    if (producer && c > 0 && c - 1 + kStages < chunks && !dead) {
-      // the stage that chunk c - 1 has left
-      dead = !ptx::mbar_wait(&empty[(c - 1) % kStages], ((c - 1) / kStages) & 1, abort_flag,
-                             budget_ns);
-      if (!dead) issue(c - 1 + kStages);
+    if (producer && c > 0 && issued < chunks && !dead) {
+      dead = !wait_empty(issued);
+      if (!dead) issue(issued++);
     }
-    __syncwarp();
+    if (!Cfg::kProducer) __syncwarp();
     fetch_v(c + 2);
     if (!Cfg::kAhead) wait_full(c);
     bar_sync(bar_x, 96);
@@ -887,12 +915,14 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
       for (int s = 0; s < kHalf / 16; ++s) {
         const uint4 f = gs.s_frag[side * (kHalf / 16) + s][lane];
         const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+        uint32_t bb[4][4];
+#pragma unroll
+        for (int np = 0; np < 4; ++np)
+          ldsm4(bb[np], qt + tile_at<DK>(16 * np + b_row, side * (kHalf / 8) + 2 * s + b_piece));
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
-          uint32_t bb[4];
-          ldsm4(bb, qt + tile_at<DK>(16 * np + b_row, side * (kHalf / 8) + 2 * s + b_piece));
-          mma16(acc[2 * np], a, bb[0], bb[1]);
-          mma16(acc[2 * np + 1], a, bb[2], bb[3]);
+          mma16(acc[2 * np], a, bb[np][0], bb[np][1]);
+          mma16(acc[2 * np + 1], a, bb[np][2], bb[np][3]);
         }
       }
       const float2 si = gs.s_inv[side][lane];
@@ -912,12 +942,14 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
     for (int s = 0; s < 4; ++s) {
       const uint4 f = gs.u_frag[s][lane];
       const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+      uint32_t bb[4][4];
+#pragma unroll
+      for (int np = s; np < 4; ++np)
+        ldsm4(bb[np], pt + tile_at<kC>(16 * np + b_row, 2 * s + b_piece));
 #pragma unroll
       for (int np = s; np < 4; ++np) {
-        uint32_t bb[4];
-        ldsm4(bb, pt + tile_at<kC>(16 * np + b_row, 2 * s + b_piece));
-        mma16(I[2 * np], a, bb[0], bb[1]);
-        mma16(I[2 * np + 1], a, bb[2], bb[3]);
+        mma16(I[2 * np], a, bb[np][0], bb[np][1]);
+        mma16(I[2 * np + 1], a, bb[np][2], bb[np][3]);
       }
     }
 #pragma unroll
@@ -948,13 +980,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
     __syncwarp();
   }
   cp_async_wait<0>();
-  if (producer) {
-    // copies in flight land before the CTA's shared memory is given up
-    int ignore = 0;
-    for (int c = max(0, issued - kStages); c < issued; ++c)
-      ptx::mbar_wait(&full[c % kStages], (c / kStages) & 1, &ignore, ptx::kDrainBudgetNs);
-    if (*reinterpret_cast<volatile int *>(abort_flag)) set_status(seq.status, MOE_DEV_TIMEOUT);
-  }
+  if (producer) drain(issued);
 }
 
 // Sets a kernel's shared-memory limit once per device.
