@@ -20,6 +20,7 @@ There is no CPU fallback: if the library is missing, ``lib()`` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -411,86 +412,102 @@ class GatedDelta:
         # only the status word must start at zero
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         self.workspace[:256].zero_()
-        self._device = self.workspace.device
         self._index = self.workspace.get_device()
+        self._new = functools.partial(torch.empty, dtype=torch.bfloat16,
+                                      device=self.workspace.device)
         self._ws = self.workspace.data_ptr()
         self._dims_ref = ctypes.byref(self.dims)
-        # row shapes, and the strides inside a row that a call's tensors must have
-        k, v = (qk_heads, qk_dim), (v_heads, v_dim)
-        self._rows = tuple((torch.bfloat16, s, (s[1], 1)) for s in (k, k, v)) + tuple(
-            (torch.float32, (v_heads,), (1,)) for _ in range(2))
-        self._out_row = (torch.bfloat16, v, (v_dim, 1))
-        self._state = (v_heads, v_dim, qk_dim)
-        self._state_strides = (v_heads * v_dim * qk_dim, v_dim * qk_dim, qk_dim, 1)
-        self._f32, self._i32 = torch.float32, torch.int32
-        self._empty = torch.empty
+        self._chunk_fn, self._step_fn = lib().moe_delta_chunk, lib().moe_delta_step
+        self._heads = (qk_heads, v_heads, qk_dim, v_dim)
+        self._state_shape = (v_heads, v_dim, qk_dim)
+        self._types = (torch.bfloat16, torch.float32, torch.int32)
 
-    def _row_ld(self, x, n, spec, where):
-        """The row stride of x, which must be [n, *row shape] on this device."""
-        dtype, row, inner = spec
-        shape, strides = x.shape, x.stride()
-        if (x.dtype is not dtype or x.get_device() != self._index or shape[0] != n or
-                shape[1:] != row):
+    def _inputs(self, n, q, k, v, g, beta, where):
+        """The call's moe_delta_inputs.  q, k, v: [n][heads][dim], g, beta: [n][v_heads]."""
+        hk, hv, dk, dv = self._heads
+        bf16, f32, _ = self._types
+        index = self._index
+        try:
+            ql, q1, q2 = q.stride()
+            kl, k1, k2 = k.stride()
+            vl, v1, v2 = v.stride()
+            gl, g1 = g.stride()
+            bl, b1 = beta.stride()
+        except ValueError:  # another number of dimensions
             _invalid(where)
-        if strides[1:] != inner and n and not x[0].is_contiguous():
+        if (index < 0 or q.shape != (n, hk, dk) or k.shape != (n, hk, dk) or
+                v.shape != (n, hv, dv) or g.shape != (n, hv) or beta.shape != (n, hv) or
+                q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16 or
+                g.dtype is not f32 or beta.dtype is not f32 or q.get_device() != index or
+                k.get_device() != index or v.get_device() != index or g.get_device() != index or
+                beta.get_device() != index):
             _invalid(where)
-        # a single row has no stride of its own
-        return strides[0] if n > 1 else row[0] * inner[0]
+        if (not (q1 == k1 == dk and v1 == dv and q2 == k2 == v2 == g1 == b1 == 1) and n and
+                not all(x[0].is_contiguous() for x in (q, k, v, g, beta))):
+            _invalid(where)
+        if n < 2:  # a single row has no stride of its own
+            ql = kl = hk * dk
+            vl, gl, bl = hv * dv, hv, hv
+        return DeltaInputs(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                           beta.data_ptr(), ql, kl, vl, gl, bl)
 
-    def _call(self, fn, where, q, k, v, g, beta, lead, cu, B, slots, state_in, state_out, out,
-              stream):
-        n = q.shape[0]
-        if self._index < 0:  # not a CUDA device
-            _invalid(where)
-        rows = [self._row_ld(x, n, spec, where)
-                for x, spec in zip((q, k, v, g, beta), self._rows)]
-        inputs = DeltaInputs(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                             beta.data_ptr(), *rows)
+    def _states(self, B, state_in, state_out, slots, where):
+        """The addresses of slots, state_in and state_out and the number of slots."""
+        p_in = p_out = p_slots = None
         n_slots = B
-        for x in (state_in, state_out):
-            if x is not None:
-                n_slots = x.shape[0]
-                if (x.dtype is not self._f32 or x.get_device() != self._index or
-                        x.shape[1:] != self._state or
-                        (x.stride() != self._state_strides and not x.is_contiguous())):
-                    _invalid(where)
-        if state_in is not None and state_out is not None and state_in.shape[0] != n_slots:
-            _invalid(where)
+        if state_in is not None:
+            n_slots, p_in = state_in.shape[0], self._state(state_in, where)
+        if state_out is not None:
+            if state_in is not None and state_out.shape[0] != n_slots:
+                _invalid(where)
+            n_slots, p_out = state_out.shape[0], self._state(state_out, where)
         if slots is not None:
-            if (slots.dtype is not self._i32 or slots.get_device() != self._index or
+            if (slots.dtype is not self._types[2] or slots.get_device() != self._index or
                     slots.shape != (B,) or not slots.is_contiguous()):
                 _invalid(where)
-            if state_in is None and state_out is None:
+            p_slots = slots.data_ptr()
+            if p_in is None and p_out is None:
                 n_slots = 1 << 30  # no state to be out of
+        return p_slots, n_slots, p_in, p_out
+
+    def _state(self, x, where):
+        if (x.dtype is not self._types[1] or x.get_device() != self._index or
+                x.shape[1:] != self._state_shape or not x.is_contiguous()):
+            _invalid(where)
+        return x.data_ptr()
+
+    def _output(self, n, out, where):
+        """The output tensor and its row stride."""
+        _, hv, _, dv = self._heads
         if out is None:
-            out = self._empty((n,) + self._state[:2], dtype=self._out_row[0], device=self._device)
-            out_ld = self._state[0] * self._state[1]
-        else:
-            out_ld = self._row_ld(out, n, self._out_row, where)
-        st = fn(self._dims_ref, ctypes.byref(inputs), *lead,
-                None if cu is None else cu.data_ptr(), B,
-                None if slots is None else slots.data_ptr(), n_slots,
-                None if state_in is None else state_in.data_ptr(),
-                None if state_out is None else state_out.data_ptr(), out.data_ptr(), out_ld,
-                self._ws, self.ws_bytes, _stream_of(stream, self._index))
-        if st != MOE_OK:
-            raise MoEError(st, where)
-        return out
+            return self._new((n, hv, dv)), hv * dv
+        if (out.dtype is not self._types[0] or out.get_device() != self._index or
+                out.shape != (n, hv, dv) or (n and not out[0].is_contiguous())):
+            _invalid(where)
+        return out, out.stride(0) if n > 1 else hv * dv
 
     def chunk(self, q, k, v, g, beta, cu_seqlens=None, state_in=None, state_out=None, slots=None,
               out=None, stream=None):
         """Whole prompts: the rows of len(cu_seqlens) - 1 sequences one after
         another (one sequence without ``cu_seqlens``).  Returns out [N][v_heads][v_dim]."""
         where = "GatedDelta.chunk"
-        B = 1
+        n = q.shape[0]
+        inputs = self._inputs(n, q, k, v, g, beta, where)
+        B, cu = 1, None
         if cu_seqlens is not None:
-            if (cu_seqlens.dtype is not self._i32 or cu_seqlens.get_device() != self._index or
+            if (cu_seqlens.dtype is not self._types[2] or cu_seqlens.get_device() != self._index or
                     cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or
                     not cu_seqlens.is_contiguous()):
                 _invalid(where)
-            B = cu_seqlens.shape[0] - 1
-        return self._call(_lib_fn("moe_delta_chunk"), where, q, k, v, g, beta, (q.shape[0],),
-                          cu_seqlens, B, slots, state_in, state_out, out, stream)
+            B, cu = cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr()
+        p_slots, n_slots, p_in, p_out = self._states(B, state_in, state_out, slots, where)
+        out, out_ld = self._output(n, out, where)
+        st = self._chunk_fn(self._dims_ref, ctypes.byref(inputs), n, cu, B, p_slots, n_slots, p_in,
+                            p_out, out.data_ptr(), out_ld, self._ws, self.ws_bytes,
+                            _stream_of(stream, self._index))
+        if st:
+            raise MoEError(st, where)
+        return out
 
     def step(self, q, k, v, g, beta, state_in=None, state_out=None, slots=None, tokens=None,
              out=None, stream=None):
@@ -499,6 +516,7 @@ class GatedDelta:
         one per sequence).  Returns out [rows][v_heads][v_dim]."""
         where = "GatedDelta.step"
         n = q.shape[0]
+        inputs = self._inputs(n, q, k, v, g, beta, where)
         if tokens is None:
             lead = slots if slots is not None else state_in if state_in is not None else state_out
             B = n if lead is None else lead.shape[0]
@@ -507,8 +525,14 @@ class GatedDelta:
             B = n // tokens if tokens > 0 else 0
         if B * tokens != n:
             _invalid(where)
-        return self._call(_step_fn, where, q, k, v, g, beta, (tokens,), None, B, slots, state_in,
-                          state_out, out, stream)
+        p_slots, n_slots, p_in, p_out = self._states(B, state_in, state_out, slots, where)
+        out, out_ld = self._output(n, out, where)
+        st = self._step_fn(self._dims_ref, ctypes.byref(inputs), B, tokens, p_slots, n_slots, p_in,
+                           p_out, out.data_ptr(), out_ld, self._ws, self.ws_bytes,
+                           _stream_of(stream, self._index))
+        if st:
+            raise MoEError(st, where)
+        return out
 
     def status(self, stream=None) -> int:
         return moe_read_status(self.workspace, stream)
@@ -517,27 +541,18 @@ class GatedDelta:
         moe_clear_status(self.workspace, stream)
 
 
-def _lib_fn(name):
-    return getattr(_lib if _lib is not None else lib(), name)
-
-
-def _step_fn(dims, inputs, T, _cu, B, *rest):
-    return _lib_fn("moe_delta_step")(dims, inputs, B, T, *rest)
-
-
 def _norm_ld(t, shape, bf16, index, where):
     """The first stride of a bf16 tensor of this shape, whose rows are whole."""
     if t.dtype is not bf16 or t.get_device() != index or t.shape != shape:
         _invalid(where)
-    if shape[0] > 1:
-        strides = t.stride()
-        if (strides[-1] != 1 and shape[-1] > 1) or (len(shape) == 3 and shape[1] > 1 and
-                                                   strides[1] != shape[2]):
-            _invalid(where)
-        return strides[0]
-    if shape[0] and not t[0].is_contiguous():
+    if t.is_contiguous():
+        return shape[-1] * (shape[1] if len(shape) == 3 else 1)
+    if len(shape) == 1 or shape[0] < 2 or not t[0].is_contiguous():
         _invalid(where)
-    return shape[-1] * (shape[1] if len(shape) == 3 else 1)
+    return t.stride(0)
+
+
+_norm_fn = None
 
 
 def norm_gate_residual(x, gamma_post=None, gate=None, gate_act="sigmoid", resid=None,
@@ -550,49 +565,56 @@ def norm_gate_residual(x, gamma_post=None, gate=None, gate_act="sigmoid", resid=
     channel), shaped like ``x``, or [.., 1] (per row).  Returns (resid_out,
     x_next), x_next None without ``gamma_pre``; x is not changed unless it is
     given as an output."""
-    import torch
+    global _norm_fn
     where = "norm_gate_residual"
-    bf16, index, shape = torch.bfloat16, x.get_device(), x.shape
+    if _norm_fn is None:
+        import torch
+        _norm_fn = (lib().moe_norm_gate_residual, torch.bfloat16, torch.empty)
+    fn, bf16, empty = _norm_fn
+    index, shape = x.get_device(), x.shape
     act = GATE_ACTS.get(gate_act)
     if act is None or index < 0 or len(shape) not in (2, 3) or 0 in shape[1:]:
         _invalid(where)
     width = shape[-1]
     inner = shape[1] if len(shape) == 3 else 1
+    per_channel = (width,)
+    p_post = p_pre = p_gate = p_resid = p_next = None
+    kind = gate_ld = resid_ld = next_ld = 0
     x_ld = _norm_ld(x, shape, bf16, index, where)
-    gammas = [None, None]
-    for i, gamma in enumerate((gamma_post, gamma_pre)):
-        if gamma is not None:
-            if (gamma.dtype is not bf16 or gamma.get_device() != index or
-                    gamma.shape != (width,) or not gamma.is_contiguous()):
-                _invalid(where)
-            gammas[i] = gamma.data_ptr()
-    kind = gate_ld = 0
+    if gamma_post is not None:
+        _norm_ld(gamma_post, per_channel, bf16, index, where)
+        p_post = gamma_post.data_ptr()
     if gate is not None:
-        if gate.dim() == 1:
+        p_gate = gate.data_ptr()
+        if gate.shape == per_channel:
             kind = GATE_CHANNEL
-            if (gate.dtype is not bf16 or gate.get_device() != index or gate.shape != (width,) or
-                    not gate.is_contiguous()):
-                _invalid(where)
+            _norm_ld(gate, per_channel, bf16, index, where)
+        elif gate.shape == shape:
+            kind, gate_ld = GATE_ELEMENT, _norm_ld(gate, shape, bf16, index, where)
         else:
-            kind = GATE_ELEMENT if gate.shape == shape else GATE_ROW
-            gate_ld = _norm_ld(gate, shape if kind == GATE_ELEMENT else shape[:-1] + (1,), bf16,
-                               index, where)
+            kind, gate_ld = GATE_ROW, _norm_ld(gate, shape[:-1] + (1,), bf16, index, where)
+    if resid is not None:
+        p_resid, resid_ld = resid.data_ptr(), _norm_ld(resid, shape, bf16, index, where)
     if resid_out is None:
-        resid_out = torch.empty(shape, dtype=bf16, device=x.device)
-    if gamma_pre is None:
-        if x_next is not None:
-            _invalid(where)
-    elif x_next is None:
-        x_next = torch.empty(shape, dtype=bf16, device=x.device)
-    a = NormArgs(
-        shape[0] * inner, width, inner, x.data_ptr(), gammas[0],
-        None if gate is None else gate.data_ptr(), None if resid is None else resid.data_ptr(),
-        gammas[1], resid_out.data_ptr(), None if x_next is None else x_next.data_ptr(), x_ld,
-        gate_ld, 0 if resid is None else _norm_ld(resid, shape, bf16, index, where),
-        _norm_ld(resid_out, shape, bf16, index, where),
-        0 if x_next is None else _norm_ld(x_next, shape, bf16, index, where), kind, act,
-        res_scale, eps)
-    st = _lib_fn("moe_norm_gate_residual")(ctypes.byref(a), _stream_of(stream, index))
-    if st != MOE_OK:
+        resid_out = empty(shape, dtype=bf16, device=x.device)
+        out_ld = inner * width
+    else:
+        out_ld = _norm_ld(resid_out, shape, bf16, index, where)
+    if gamma_pre is not None:
+        _norm_ld(gamma_pre, per_channel, bf16, index, where)
+        p_pre = gamma_pre.data_ptr()
+        if x_next is None:
+            x_next = empty(shape, dtype=bf16, device=x.device)
+            next_ld = inner * width
+        else:
+            next_ld = _norm_ld(x_next, shape, bf16, index, where)
+        p_next = x_next.data_ptr()
+    elif x_next is not None:
+        _invalid(where)
+    a = NormArgs(shape[0] * inner, width, inner, x.data_ptr(), p_post, p_gate, p_resid, p_pre,
+                 resid_out.data_ptr(), p_next, x_ld, gate_ld, resid_ld, out_ld, next_ld, kind, act,
+                 res_scale, eps)
+    st = fn(ctypes.byref(a), _stream_of(stream, index))
+    if st:
         raise MoEError(st, where)
     return resid_out, x_next

@@ -300,6 +300,30 @@ def test_empty_calls(env):
     m.step(**s, state_in=pool, state_out=S1, tokens=0)
 
 
+def test_tensors_are_checked(env):
+    import torch
+    moe, dev = env
+    s = make(env, 12)
+    m = mixer(env, (2, 4), (128, 128), 12, 3)
+    st = states(env, 3, (2, 4), (128, 128))
+    slots = torch.arange(3, dtype=torch.int32, device=dev)
+    bad = [dict(q=s["q"][:11]), dict(k=s["k"].float()), dict(v=s["v"].transpose(1, 2)),
+           dict(v=s["v"].cpu()), dict(g=s["g"].double()), dict(beta=s["beta"][:, :2]),
+           dict(q=s["q"][:, 0]), dict(state_in=st[:2]), dict(state_in=st.transpose(2, 3)),
+           dict(state_in=st.bfloat16()), dict(slots=slots.long()),
+           dict(out=torch.empty(12, 4, 64, dtype=torch.bfloat16, device=dev))]
+    for kw in bad:
+        with pytest.raises(moe.MoEError):
+            m.step(**{**s, "state_in": st, "state_out": st, "slots": slots, **kw})
+    for kw in bad + [dict(slots=slots[:2])]:
+        with pytest.raises(moe.MoEError):
+            m.chunk(**{**s, "cu_seqlens": cu_of(env, [4, 4, 4]), "state_in": st, "state_out": st,
+                       "slots": slots, **kw})
+    with pytest.raises(moe.MoEError):
+        m.chunk(**s, cu_seqlens=cu_of(env, [12]).long())
+    m.step(**s, state_in=st, state_out=st, slots=slots)
+
+
 def test_workspace_is_checked(env):
     moe, _ = env
     big = make(env, 4096)

@@ -136,6 +136,23 @@ def test_rows_do_not_see_one_another(env, width):
     assert torch.equal(r[keep], r2) and torch.equal(n[keep], n2)
 
 
+def test_tensors_are_checked(env):
+    import torch
+    moe, dev = env
+    s = make(env, 6, 64)
+    x, w = s["x"], s["post"]
+    wide = torch.zeros(128, dtype=torch.bfloat16, device=dev)
+    for kw in (dict(gamma_post=w.float()), dict(gamma_post=wide[::2]), dict(gamma_pre=wide),
+               dict(gate=x[:5]), dict(gate=x.t().contiguous().t()), dict(resid=x.float()),
+               dict(resid=x.cpu()), dict(x_next=torch.empty_like(x)), dict(resid_out=x[:, :32]),
+               dict(gate=wide)):
+        with pytest.raises(moe.MoEError):
+            moe.norm_gate_residual(x, **kw)
+    for y in (x.float(), x[0], x.t(), x[None, None]):
+        with pytest.raises(moe.MoEError):
+            moe.norm_gate_residual(y)
+
+
 def test_no_rows_and_stream(env):
     import torch
     moe, dev = env

@@ -125,3 +125,5 @@ def test_python_entries_check_their_tensors(moe):
     g = torch.zeros(4, 4)
     with pytest.raises(moe.MoEError):
         m.chunk(q, q, v, g, g)
+    with pytest.raises(moe.MoEError):
+        m.step(q[0], q, v, g, g)
