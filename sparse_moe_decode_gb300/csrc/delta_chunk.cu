@@ -41,10 +41,18 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kC = 64;  // tokens per chunk
-constexpr int kTile = kC * kC * 2;  // bytes of a 64 x 64 fp16 tile
-// Per (chunk, value head): T's two terms, P, then vectors of 64 fp32.
-enum { kVecC, kVecBeta, kVecT, kVecD, kVecO, kVecP, kVecMisc, kVecs };
-constexpr int kHeadBlob = 3 * kTile + kVecs * kC * 4;
+// A lower triangle of 64 x 64 fp16: ten blocks of 16 x 16, (np, s) for rows 16
+// np .., columns 16 s .., one after another.
+constexpr int kBlock = 16 * 16 * 2;
+constexpr int kTri = 10 * kBlock;
+// Per (chunk, value head): what the chain warps read -- T's two terms and
+// vectors of 64 fp32 --, then what the output warps read, P and two vectors.
+enum { kVecC, kVecBeta, kVecT, kVecD, kVecMisc, kVecsA };
+enum { kVecO, kVecP, kVecsB };
+enum { kGamma, kTau, kDUp, kCMax };  // of kVecMisc
+constexpr int kPartA = 2 * kTri + kVecsA * kC * 4;
+constexpr int kPartB = kTri + kVecsB * kC * 4;
+constexpr int kHeadBlob = kPartA + kPartB;
 constexpr int kHeader = 256;      // status word, flags
 constexpr int kFlagWord = 16;     // header word: some bound of the call is bad
 constexpr int kPrepThreads = 256;
@@ -58,6 +66,17 @@ constexpr int kKeyBlob = 2 * kC * DK * 2;  // per (chunk, key head): k, then q, 
 template <int COLS>
 __device__ __forceinline__ uint32_t tile_at(int row, int piece) {
   return static_cast<uint32_t>(row * COLS * 2 + ((piece ^ (row & 7)) << 4));
+}
+
+// 16-byte pieces of 32-byte rows (blocks of a triangle, rows of v and o),
+// permuted so that eight rows' pieces of one column lie in different banks.
+__device__ __forceinline__ uint32_t row32_at(int row, int piece) {
+  return static_cast<uint32_t>(row * 32 + ((piece ^ ((row >> 2) & 1)) << 4));
+}
+__device__ __forceinline__ int block_of(int np, int s) { return np * (np + 1) / 2 + s; }
+// Piece `piece` (of eight columns) of row i of a triangle.
+__device__ __forceinline__ uint32_t tri_at(int i, int piece) {
+  return static_cast<uint32_t>(block_of(i >> 4, piece >> 1) * kBlock) + row32_at(i & 15, piece & 1);
 }
 
 // Sequence b's first chunk slot: chunks of different sequences never share
@@ -82,9 +101,11 @@ struct PrepSmem {
   float t[kC * kTLd];  // T; blocks of 16 above the diagonal are never touched
 };
 
-// Where L(i, j) lies: pieces of four columns permuted by the row, so that
-// eight rows' pieces of one column lie in different banks.
-__device__ __forceinline__ int l_at(int i, int j) { return i * kC + (j ^ ((i & 7) << 2)); }
+// Where L(i, j) lies, in the same blocks: pieces of four columns permuted by
+// the row, so that eight rows' pieces of one column lie in different banks.
+__device__ __forceinline__ int l_at(int i, int j) {
+  return block_of(i >> 4, j >> 4) * 256 + (i & 15) * 16 + ((j & 15) ^ (((i >> 1) & 3) << 2));
+}
 
 // The power of two that brings a token's values below 2^15 (bounded by their
 // 2-norm), and its inverse: their bf16 digits are exact in fp16 down to 2^-25
@@ -238,7 +259,8 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
     }
   }
 
-  float *vec = reinterpret_cast<float *>(sm.head + 3 * kTile);
+  float *vec = reinterpret_cast<float *>(sm.head + 2 * kTri);
+  float *vec_b = reinterpret_cast<float *>(sm.head + kPartA + kTri);
   float *ghi = vec + kVecT * kC;
   float *L = reinterpret_cast<float *>(sm.head);
   float *T = sm.t;
@@ -275,23 +297,27 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
       T[i * kTLd + kGLo] = static_cast<float>(first - sh.x);
       T[(i + 1) * kTLd + kGLo] = static_cast<float>(second - sh.y);
       *reinterpret_cast<float2 *>(vec + kVecBeta * kC + i) = make_float2(be0, be1);
-      *reinterpret_cast<float2 *>(vec + kVecC * kC + i) =
-          make_float2(-be0 * gamma.x * kap.x, -be1 * gamma.y * kap.y);
-      *reinterpret_cast<float2 *>(vec + kVecO * kC + i) =
+      const float2 cc = make_float2(-be0 * gamma.x * kap.x, -be1 * gamma.y * kap.y);
+      *reinterpret_cast<float2 *>(vec + kVecC * kC + i) = cc;
+      *reinterpret_cast<float2 *>(vec_b + kVecO * kC + i) =
           make_float2(rho.x * gamma.x, rho.y * gamma.y);
       // the update's factors, Gamma_64,j kappa_j, over a power of two above
       // the largest
       float2 dd = make_float2(exp2f(static_cast<float>(total - first)) * kap.x,
                               exp2f(static_cast<float>(total - second)) * kap.y);
-      float dmax = fmaxf(dd.x, dd.y);
+      float dmax = fmaxf(dd.x, dd.y), cmax = fmaxf(fabsf(cc.x), fabsf(cc.y));
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dmax = fmaxf(dmax, __shfl_xor_sync(kFull, dmax, o));
+      for (int o = 16; o > 0; o >>= 1) {
+        dmax = fmaxf(dmax, __shfl_xor_sync(kFull, dmax, o));
+        cmax = fmaxf(cmax, __shfl_xor_sync(kFull, cmax, o));
+      }
       float up, down;
       pow2_above(dmax, up, down);
       *reinterpret_cast<float2 *>(vec + kVecD * kC + i) = make_float2(dd.x * down, dd.y * down);
       if (lane == 0) {
-        vec[kVecMisc * kC] = exp2f(static_cast<float>(total));  // gamma_64
-        vec[kVecMisc * kC + 2] = up;
+        vec[kVecMisc * kC + kGamma] = exp2f(static_cast<float>(total));
+        vec[kVecMisc * kC + kDUp] = up;
+        vec[kVecMisc * kC + kCMax] = cmax;
       }
     }
     __syncthreads();
@@ -326,15 +352,15 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
         pow2_above(fabsf(f0) * kmax, up0, s0);
         pow2_above(fabsf(f1) * kmax, up1, s1);
         s0 *= 0x1p-19f, s1 *= 0x1p-19f;
-        if (t == 0) vec[kVecP * kC + i0] = up0 * 0x1p19f, vec[kVecP * kC + i1] = up1 * 0x1p19f;
+        if (t == 0) vec_b[kVecP * kC + i0] = up0 * 0x1p19f, vec_b[kVecP * kC + i1] = up1 * 0x1p19f;
       }
-      uint8_t *P = sm.head + 2 * kTile + 4 * t;
+      uint8_t *P = sm.head + kPartA + 4 * t;
       // one tile: eight columns from `col` of this warp's rows
       const auto put_tile = [&](int col, float2 top, float2 low) {
         if (is_q) {
-          *reinterpret_cast<__half2 *>(P + tile_at<kC>(i0, col / 8)) =
+          *reinterpret_cast<__half2 *>(P + tri_at(i0, col / 8)) =
               __float22half2_rn(mul2(top, make_float2(s0, s0)));
-          *reinterpret_cast<__half2 *>(P + tile_at<kC>(i1, col / 8)) =
+          *reinterpret_cast<__half2 *>(P + tri_at(i1, col / 8)) =
               __float22half2_rn(mul2(low, make_float2(s1, s1)));
         } else {
           *reinterpret_cast<float2 *>(L + l_at(i0, col + 2 * t)) = top;
@@ -462,7 +488,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
       pow2_above(most, up, down);
       pow2_scale(mx, mult, inv);
       if (q == 0) vec[kVecT * kC + i] = inv * down;
-      if (tid == 0) vec[kVecMisc * kC + 1] = up;
+      if (tid == 0) vec[kVecMisc * kC + kTau] = up;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int p = q + 4 * e;
@@ -470,9 +496,9 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
           uint32_t hw[4], lw[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) split_h2(mul2(v[e][j], make_float2(mult, mult)), hw[j], lw[j]);
-          const uint32_t at = tile_at<kC>(i, p);
+          const uint32_t at = tri_at(i, p);
           *reinterpret_cast<uint4 *>(sm.head + at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-          *reinterpret_cast<uint4 *>(sm.head + kTile + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+          *reinterpret_cast<uint4 *>(sm.head + kTri + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
         }
       }
     }
@@ -492,43 +518,39 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
 
 // ------------------------------------------------------------------ chain
 
-// Shared memory of one group of three warps (16 state rows): what the two
-// chain warps exchange, what they hand to the output warp, the value rows and
-// the output rows.
-template <int DK>
-struct GroupSmem {
-  uint4 s_frag[DK / 16][32];    // S as A fragments, fp16
-  uint4 u_frag[4][32];          // u likewise
-  float4 x_part[2][8][32];      // each half's S k^T
-  uint4 w_frag[4][2][32];       // the update's A fragments, two terms
-  float2 s_inv[2][32], u_inv[32];
-  alignas(16) uint8_t v[3][kC * 32];  // 16 value channels of the chunk's tokens
-  alignas(16) uint8_t o[kC * 32];
-};
+// How the chain runs: WARPS chain warps and two output warps per group of 16
+// state rows, GROUPS groups per CTA, one CTA per SM.
+template <int DK, int WARPS, int GROUPS>
+struct Chain {
+  static constexpr int kCols = DK / WARPS;   // key channels of a chain warp
+  static constexpr int kSteps = kCols / 16;  // k16 steps of its share of S k^T
+  static constexpr int kOwn = 4 / WARPS;     // 16-token blocks of u it forms
+  // Ring stages: for the chain warps k, T and their vectors; for the output
+  // warps q, P and theirs.
+  static constexpr int kStageA = kKeyBlob<DK> / 2 + kPartA;
+  static constexpr int kStageB = kKeyBlob<DK> / 2 + kPartB;
+  static constexpr int kStages = 3;
+  // Eight warps, two to a quarter of the SM, may have 255 registers each; a
+  // ninth would cost every one of them a third.  So the four output warps
+  // bring in the rings' stages, one of a chunk's four copies each (issuing a
+  // bulk copy holds its thread for some 500 cycles).
+  static constexpr int kThreads = 32 * (WARPS + 2) * GROUPS;
 
-template <int DK, int GROUPS>
-struct ChainCfg {
-  // one CTA per SM: the ring takes what the groups leave of its shared memory
-  static constexpr int kStageBytes = kKeyBlob<DK> + kHeadBlob;
-  static constexpr int kStages = GROUPS >= 4 && DK == 128 ? 2 : 3;
-  // With stages to spare the output warp waits for a chunk's operands half a
-  // chunk ahead and the group's barrier passes them on; otherwise the chain
-  // warps wait for them where they need them.
-  static constexpr bool kAhead = kStages >= 3;
-  // A warp of its own for the ring where that leaves the others registers
-  // enough (four warps share a quarter of the SM's); else the first output
-  // warp brings the stages in.
-  static constexpr bool kProducer = GROUPS < 4;
-  static constexpr int kThreads = 32 * (3 * GROUPS + kProducer);
-  static constexpr int kSmem =
-      kStages * kStageBytes + GROUPS * static_cast<int>(sizeof(GroupSmem<DK>)) + 64;
+  // What the warps of a group hand one another.
+  struct Group {
+    uint4 s_frag[DK / 16][32];           // S as A fragments, fp16
+    uint4 u_frag[4][32];                 // u likewise
+    float4 x_part[4][WARPS - 1][2][32];  // shares of S k^T for the block's owner
+    float4 y[4][2][32];                  // beta v
+    uint4 x_frag[4][2][32];              // x as A fragments, two terms
+    uint4 w_frag[4][2][32];              // the update's, two terms
+    float2 s_inv[WARPS][32], v_max[2][32], u_inv[32];
+    alignas(16) uint8_t v[3][kC * 32];   // 16 value channels of the chunk's tokens
+    alignas(16) uint8_t o[kC * 32];      // output rows on their way out
+  };
+  static constexpr int kSmem = kStages * (kStageA + kStageB) +
+                               GROUPS * static_cast<int>(sizeof(Group)) + 256;
 };
-
-// 16-byte pieces of the 32-byte token rows of v and o, permuted so that eight
-// rows' pieces of one column lie in different banks.
-__device__ __forceinline__ uint32_t row32_at(int row, int piece) {
-  return static_cast<uint32_t>(row * 32 + ((piece ^ ((row >> 2) & 1)) << 4));
-}
 
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(kFull, v, 1));
@@ -547,42 +569,39 @@ __device__ __forceinline__ void mma16(Acc &c, const uint32_t (&a)[4], uint32_t b
   c.top = make_float2(f[0], f[1]), c.low = make_float2(f[2], f[3]);
 }
 
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return fma2(a, both(1.0f), b); }
+
 // A fragments (two terms) of the 16 columns of tiles p and q, scaled by rows.
-__device__ __forceinline__ void split_frag(const Acc &p, const Acc &q, float2 m0, float2 m1,
+__device__ __forceinline__ void split_frag(const Acc &p, const Acc &q, float m0, float m1,
                                            uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-  split_h2(mul2(p.top, m0), hi[0], lo[0]);
-  split_h2(mul2(p.low, m1), hi[1], lo[1]);
-  split_h2(mul2(q.top, m0), hi[2], lo[2]);
-  split_h2(mul2(q.low, m1), hi[3], lo[3]);
+  split_h2(mul2(p.top, both(m0)), hi[0], lo[0]);
+  split_h2(mul2(p.low, both(m1)), hi[1], lo[1]);
+  split_h2(mul2(q.top, both(m0)), hi[2], lo[2]);
+  split_h2(mul2(q.low, both(m1)), hi[3], lo[3]);
 }
 
-// Power-of-two scales of the two rows a lane holds, from N tiles.
-template <int N>
-__device__ __forceinline__ void row_scales(const Acc (&x)[N], float &m0, float &m1, float &i0,
-                                           float &i1) {
-  float a = 0.0f, b = 0.0f;
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    a = max3_abs(a, x[n].top.x, x[n].top.y);
-    b = max3_abs(b, x[n].low.x, x[n].low.y);
-  }
-  pow2_scale(quad_max(a), m0, i0);
-  pow2_scale(quad_max(b), m1, i1);
+__device__ __forceinline__ void put4(uint4 *p, const uint32_t (&v)[4]) {
+  *p = make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void get4(const uint4 *p, uint32_t (&v)[4]) {
+  const uint4 w = *p;
+  v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
 }
 
-template <int DK, int GROUPS>
-__global__ void __launch_bounds__(ChainCfg<DK, GROUPS>::kThreads, 1)
+template <int DK, int WARPS, int GROUPS>
+__global__ void __launch_bounds__(Chain<DK, WARPS, GROUPS>::kThreads, 1)
 delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const uint8_t *ws,
                    const uint8_t *ws_key, const uint8_t *ws_head, moe_bf16 *out, int64_t out_ld,
                    unsigned long long budget_ns) {
-  using Cfg = ChainCfg<DK, GROUPS>;
-  constexpr int kStages = Cfg::kStages;
-  constexpr int kHalf = DK / 2;  // key channels of a chain warp
+  using C = Chain<DK, WARPS, GROUPS>;
+  using Group = typename C::Group;
+  constexpr int kKeyTile = kKeyBlob<DK> / 2, kStages = C::kStages;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  uint8_t *ring = smem_raw;
-  GroupSmem<DK> *groups = reinterpret_cast<GroupSmem<DK> *>(ring + kStages * Cfg::kStageBytes);
-  uint64_t *full = reinterpret_cast<uint64_t *>(groups + GROUPS), *empty = full + kStages;
-  int *abort_flag = reinterpret_cast<int *>(empty + kStages);
+  uint8_t *ring_a = smem_raw, *ring_b = ring_a + kStages * C::kStageA;
+  Group *groups = reinterpret_cast<Group *>(ring_b + kStages * C::kStageB);
+  uint64_t *full = reinterpret_cast<uint64_t *>(groups + GROUPS);
+  int *abort_flag = reinterpret_cast<int *>(full + kStages);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tiles = d.v_dim / (16 * GROUPS);
@@ -594,106 +613,82 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   if (!r.ok) return;
   const int hk = h / (d.v_heads / d.qk_heads);
   const int chunks = (r.len + kC - 1) / kC;
-  const int base = slot_base(seq, b);
 
   if (tid == 0) {
     *abort_flag = 0;
-    for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], 3 * GROUPS);
-    }
+    for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s], 4);
     ptx::fence_mbar_init();
   }
   __syncthreads();
 
-  const auto issue = [&](int c) {  // the operands of chunk c: keys and queries, the head's part
-    const int s = c % kStages;
-    const uint32_t dst = ptx::smem_u32(ring + s * Cfg::kStageBytes);
-    const size_t at = static_cast<size_t>(base) + c;
-    ptx::mbar_expect_tx(&full[s], Cfg::kStageBytes);
-    bulk_load(dst, ws_key + (at * d.qk_heads + hk) * kKeyBlob<DK>, kKeyBlob<DK>, &full[s]);
-    bulk_load(dst + kKeyBlob<DK>, ws_head + (at * d.v_heads + h) * kHeadBlob, kHeadBlob, &full[s]);
-  };
-  // Waits for the stage that chunk c - kStages has left; false if it gave up.
-  const auto wait_empty = [&](int c) {
-    return c < kStages || ptx::mbar_wait(&empty[c % kStages], (c / kStages - 1) & 1, abort_flag,
-                                         budget_ns);
-  };
-  // Copies in flight land before the CTA's shared memory is given up.
-  const auto drain = [&](int issued) {
-    int ignore = 0;
-    for (int c = max(0, issued - kStages); c < issued; ++c)
-      ptx::mbar_wait(&full[c % kStages], (c / kStages) & 1, &ignore, ptx::kDrainBudgetNs);
-    if (*reinterpret_cast<volatile int *>(abort_flag)) set_status(seq.status, MOE_DEV_TIMEOUT);
-  };
-  if (Cfg::kProducer && warp == 3 * GROUPS) {
-    if (lane == 0) {
-      int c = 0;
-      for (; c < chunks && wait_empty(c); ++c) issue(c);
-      drain(c);
-    }
-    return;
-  }
-
-  // Chain warps 2 g, 2 g + 1 (the halves of the key channels), output warp
-  // 2 GROUPS + g.  The three warps of a group meet twice per chunk: bar_x
-  // (both halves of S k^T and the copy of S are there), bar_w (u is there, and
-  // the next chunk's values).  Every buffer of the group is written before one
-  // of the two, read between it and the other, and so free again when its
-  // writer comes back to it.
-  const bool chain = warp < 2 * GROUPS;
-  const int group = chain ? warp >> 1 : warp - 2 * GROUPS, half = warp & 1;
-  GroupSmem<DK> &gs = groups[group];
-  const int bar_x = 1 + 2 * group, bar_w = 2 + 2 * group;
+  // Chain warps WARPS g .. WARPS g + WARPS - 1 (a share of the key channels
+  // each), output warps WARPS GROUPS + 2 g, + 1 (half of the tokens each).  The
+  // warps meet three times per chunk: all of the CTA at bar_x (the shares of S
+  // k^T, the copy of S and beta v are there; nobody reads the previous chunk's
+  // stage any more), a group's chain warps at bar_y (x is there), a group at
+  // bar_w (u is there, and the next chunk's operands).  Every buffer of the
+  // group is written before one of them, read after it, and free again when
+  // its writer comes back to it: x_part, y and v_max x|y, s_frag x|w, x_frag
+  // y|w, w_frag and u_frag w|next x.
+  const bool chain = warp < WARPS * GROUPS;
+  const int group = chain ? warp / WARPS : (warp - WARPS * GROUPS) / 2, part = warp % WARPS;
+  Group &gs = groups[group];
+  const int bar_x = 0, bar_y = 1 + 2 * group, bar_w = bar_y + 1;
+  constexpr int kAll = C::kThreads, kGroup = 32 * (WARPS + 2);
   const int dv0 = (tile * GROUPS + group) * 16;
   const int g = lane >> 2, t = lane & 3;
-  // a wait that gave up is not repeated: the loops below run to their end on
-  // whatever the ring holds, so that all warps of a group pass every barrier
-  bool dead = false;
   // B fragments of two n8 tiles from rows (plain) or columns (trans) of a tile
   const int b_row = (lane & 7) + ((lane >> 4) << 3), b_piece = (lane >> 3) & 1;
   const int bt_row = (lane & 7) + (((lane >> 3) & 1) << 3), bt_piece = lane >> 4;
 
   if (chain) {
-    constexpr int kSteps = kHalf / 16;
     const int64_t at = ((static_cast<int64_t>(r.slot) * d.v_heads + h) * d.v_dim + dv0 + g) * DK +
-                       half * kHalf + 2 * t;
-    Acc S[kHalf / 8];
+                       part * C::kCols + 2 * t;
+    Acc S[2 * C::kSteps];
 #pragma unroll
-    for (int n = 0; n < kHalf / 8; ++n) {
-      S[n].top = S[n].low = make_float2(0.0f, 0.0f);
+    for (int n = 0; n < 2 * C::kSteps; ++n) {
+      S[n].top = S[n].low = both(0.0f);
       if (seq.state_in) {
         S[n].top = *reinterpret_cast<const float2 *>(seq.state_in + at + 8 * n);
         S[n].low = *reinterpret_cast<const float2 *>(seq.state_in + at + 8 * DK + 8 * n);
       }
     }
-    const uint32_t v_at =
-        ptx::smem_u32(gs.v[0]) + row32_at((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
-    // T's fragments that this half needs (below)
-    const int np_of[2] = {half ? 1 : 0, half ? 2 : 3};
-    if (chunks) bar_sync(bar_w, 96);
+    // The 16-token blocks whose x and u this warp forms.  u's block np takes
+    // np + 1 steps: blocks 0 and 3, and 1 and 2, make equal pairs.
+    int own[C::kOwn];
+    if constexpr (WARPS == 4) own[0] = part;
+    else own[0] = part, own[1] = 3 - part;
+    // the warp that owns block np, and where this warp's share for it goes
+    const auto owner = [](int np) { return WARPS == 4 ? np : min(np, 3 - np); };
+    const auto place = [&](int np) { return (part - owner(np) - 1 + WARPS) % WARPS; };
     float m0, m1, i0, i1;
-    row_scales(S, m0, m1, i0, i1);
-    for (int c = 0; c < chunks; ++c) {
-      const int st = c % kStages;
-      const uint32_t kt = ptx::smem_u32(ring + st * Cfg::kStageBytes);
-      const uint32_t tt = kt + kKeyBlob<DK>;
-      const float *vec =
-          reinterpret_cast<const float *>(ring + st * Cfg::kStageBytes + kKeyBlob<DK> + 3 * kTile);
-      if (!Cfg::kAhead && !dead)
-        dead = !ptx::mbar_wait(&full[st], (c / kStages) & 1, abort_flag, budget_ns);
-      gs.s_inv[half][lane] = make_float2(i0, i1);
-      // this half's share of X^T = S k^T (16 value channels x 64 tokens)
-      Acc X[8] = {}, Y[8];
-      float2 cc[8];
+    {
+      float a0 = 0.0f, a1 = 0.0f;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
+      for (int n = 0; n < 2 * C::kSteps; ++n) {
+        a0 = max3_abs(a0, S[n].top.x, S[n].top.y);
+        a1 = max3_abs(a1, S[n].low.x, S[n].low.y);
+      }
+      pow2_scale(quad_max(a0), m0, i0);
+      pow2_scale(quad_max(a1), m1, i1);
+    }
+    if (chunks) bar_sync(bar_w, kGroup);
+    int st = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t kt = ptx::smem_u32(ring_a + st * C::kStageA), tt = kt + kKeyTile;
+      const float *vec =
+          reinterpret_cast<const float *>(ring_a + st * C::kStageA + kKeyTile + 2 * kTri);
+      gs.s_inv[part][lane] = make_float2(i0, i1);
+      // this warp's share of X^T = S k^T (16 value channels x 64 tokens)
+      Acc X[8] = {};
+#pragma unroll
+      for (int s = 0; s < C::kSteps; ++s) {
         uint32_t hi[4], lo[4], bb[4][4];
 #pragma unroll
         for (int np = 0; np < 4; ++np)
-          ldsm4(bb[np], kt + tile_at<DK>(16 * np + b_row, half * (kHalf / 8) + 2 * s + b_piece));
-        split_frag(S[2 * s], S[2 * s + 1], make_float2(m0, m0), make_float2(m1, m1), hi, lo);
-        gs.s_frag[half * kSteps + s][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          ldsm4(bb[np], kt + tile_at<DK>(16 * np + b_row, part * (C::kCols / 8) + 2 * s + b_piece));
+        split_frag(S[2 * s], S[2 * s + 1], m0, m1, hi, lo);
+        put4(&gs.s_frag[part * C::kSteps + s][lane], hi);
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
           mma16(X[2 * np], hi, bb[np][0], bb[np][1]);
@@ -704,155 +699,180 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
           mma16(X[2 * np], lo, bb[np][0], bb[np][1]);
           mma16(X[2 * np + 1], lo, bb[np][2], bb[np][3]);
         }
-        if (s > 0) continue;
-        // beta_i v_i, in the shadow of the products
-#pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          uint32_t vv[4];
-          ldsm4_t(vv, v_at + (c % 3) * kC * 32 + np * 16 * 32);
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int n = 2 * np + q;
-            const float2 be = *reinterpret_cast<const float2 *>(vec + kVecBeta * kC + 8 * n + 2 * t);
-            cc[n] = *reinterpret_cast<const float2 *>(vec + kVecC * kC + 8 * n + 2 * t);
-            Y[n].top = mul2(be, make_float2(bf16_lo(vv[2 * q]), bf16_hi(vv[2 * q])));
-            Y[n].low = mul2(be, make_float2(bf16_lo(vv[2 * q + 1]), bf16_hi(vv[2 * q + 1])));
-          }
-        }
       }
+      Acc mine[C::kOwn][2];
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        X[n].top = mul2(X[n].top, make_float2(i0, i0));
-        X[n].low = mul2(X[n].low, make_float2(i1, i1));
-        gs.x_part[half][n][lane] = make_float4(X[n].top.x, X[n].top.y, X[n].low.x, X[n].low.y);
-        Y[n].top = fma2(cc[n], X[n].top, Y[n].top);
-        Y[n].low = fma2(cc[n], X[n].low, Y[n].low);
-      }
-      bar_sync(bar_x, 96);
-      // x_i = beta_i v_i - c_i (S k_i), with the other half's share; vec holds -c_i
-      {
-        float4 y[8];
-#pragma unroll
-        for (int n = 0; n < 8; ++n) y[n] = gs.x_part[half ^ 1][n][lane];
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          X[n].top = fma2(cc[n], make_float2(y[n].x, y[n].y), Y[n].top);
-          X[n].low = fma2(cc[n], make_float2(y[n].z, y[n].w), Y[n].low);
-        }
-      }
-      // u = T x.  Column tiles 2 np, 2 np + 1 of u^T take the tokens of k16
-      // steps 0 .. np; the halves take np = 0 and 3, and np = 1 and 2: five
-      // steps each.
-      uint32_t th[4][2][4], tl[4][2][4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (s <= np_of[j]) {
-            const uint32_t a = tt + tile_at<kC>(16 * np_of[j] + b_row, 2 * s + b_piece);
-            ldsm4(th[s][j], a);
-            ldsm4(tl[s][j], a + kTile);
-          }
-      const float gamma = vec[kVecMisc * kC], tau = vec[kVecMisc * kC + 1];
-      const float back = tau * vec[kVecMisc * kC + 2];
-      float2 ts[2][2], dd[2][2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int np = 0; np < 4; ++np)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const int at_n = 8 * (2 * np_of[j] + q) + 2 * t;
-          ts[j][q] = *reinterpret_cast<const float2 *>(vec + kVecT * kC + at_n);
-          dd[j][q] = *reinterpret_cast<const float2 *>(vec + kVecD * kC + at_n);
+          Acc &x = X[2 * np + q];
+          x.top = mul2(x.top, both(i0)), x.low = mul2(x.low, both(i1));
+          if (owner(np) != part)
+            gs.x_part[np][place(np)][q][lane] = make_float4(x.top.x, x.top.y, x.low.x, x.low.y);
+#pragma unroll
+          for (int j = 0; j < C::kOwn; ++j)
+            if (np == own[j]) mine[j][q] = x;
         }
-      row_scales(X, m0, m1, i0, i1);
-      Acc U[2][2] = {}, V[2][2] = {}, W[2][2] = {};
+      // T's fragments of the own blocks, a step ahead of their use
+      uint32_t th[2][C::kOwn][4], tl[2][C::kOwn][4];
+      const auto load_t = [&](int s) {
+#pragma unroll
+        for (int j = 0; j < C::kOwn; ++j)
+          if (s <= own[j]) {
+            const uint32_t a = tt + block_of(own[j], s) * kBlock + row32_at(b_row, b_piece);
+            ldsm4(th[s & 1][j], a);
+            ldsm4(tl[s & 1][j], a + kTri);
+          }
+      };
+      load_t(0);
+      float2 cc[C::kOwn][2];
+#pragma unroll
+      for (int j = 0; j < C::kOwn; ++j)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          cc[j][q] =
+              *reinterpret_cast<const float2 *>(vec + kVecC * kC + 16 * own[j] + 8 * q + 2 * t);
+      const float4 misc = *reinterpret_cast<const float4 *>(vec + kVecMisc * kC);
+      bar_sync(bar_x, kAll);
+      // x_i = beta_i v_i - c_i (S k_i); vec holds -c_i.  Its scale comes from
+      // norms, so that the warps agree on it without another exchange:
+      // |S k_i| <= |S| |k_i|, where k_i (scaled) stays below 2^15 and each
+      // share of S below 2^15 i0 per element.
+      float2 si = gs.s_inv[0][lane];
+#pragma unroll
+      for (int p = 1; p < WARPS; ++p) si = add2(si, gs.s_inv[p][lane]);
+      const float2 va = gs.v_max[0][lane], vb = gs.v_max[1][lane];
+      const float2 vm = make_float2(fmaxf(va.x, vb.x), fmaxf(va.y, vb.y));
+      const float gamma = misc.x, tau = misc.y, back = misc.y * misc.z;
+      const float reach = misc.w * (0x1p30f * (C::kCols == 16   ? 4.0f
+                                               : C::kCols == 32 ? 5.66f
+                                                                : 8.0f));
+      float n0, n1, j0, j1;
+      pow2_above(fmaf(reach, si.x, vm.x), j0, n0);
+      pow2_above(fmaf(reach, si.y, vm.y), j1, n1);
+      n0 *= 0x1p15f, n1 *= 0x1p15f, j0 *= 0x1p-15f, j1 *= 0x1p-15f;
+#pragma unroll
+      for (int j = 0; j < C::kOwn; ++j) {
+        float4 y[WARPS - 1][2];
+#pragma unroll
+        for (int p = 0; p < WARPS - 1; ++p)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) y[p][q] = gs.x_part[own[j]][p][q][lane];
+        const float4 z[2] = {gs.y[own[j]][0][lane], gs.y[own[j]][1][lane]};
+        Acc x[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          x[q] = mine[j][q];
+#pragma unroll
+          for (int p = 0; p < WARPS - 1; ++p) {
+            x[q].top = add2(x[q].top, make_float2(y[p][q].x, y[p][q].y));
+            x[q].low = add2(x[q].low, make_float2(y[p][q].z, y[p][q].w));
+          }
+          x[q].top = fma2(cc[j][q], x[q].top, make_float2(z[q].x, z[q].y));
+          x[q].low = fma2(cc[j][q], x[q].low, make_float2(z[q].z, z[q].w));
+        }
+        uint32_t hi[4], lo[4];
+        split_frag(x[0], x[1], n0, n1, hi, lo);
+        put4(&gs.x_frag[own[j]][0][lane], hi);
+        put4(&gs.x_frag[own[j]][1][lane], lo);
+      }
+      float2 ts[C::kOwn][2], dd[C::kOwn][2];
+#pragma unroll
+      for (int j = 0; j < C::kOwn; ++j)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int col = 16 * own[j] + 8 * q + 2 * t;
+          ts[j][q] = *reinterpret_cast<const float2 *>(vec + kVecT * kC + col);
+          dd[j][q] = *reinterpret_cast<const float2 *>(vec + kVecD * kC + col);
+        }
+      bar_sync(bar_y, 32 * WARPS);
+      // u = T x
+      Acc U[C::kOwn][2] = {}, V[C::kOwn][2] = {}, W[C::kOwn][2] = {};
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
+        if (s > own[C::kOwn - 1]) continue;  // the last is the largest
         uint32_t hi[4], lo[4];
-        split_frag(X[2 * s], X[2 * s + 1], make_float2(m0, m0), make_float2(m1, m1), hi, lo);
+        get4(&gs.x_frag[s][0][lane], hi);
+        get4(&gs.x_frag[s][1][lane], lo);
+        if (s < 3) load_t(s + 1);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (s <= np_of[j])
+        for (int j = 0; j < C::kOwn; ++j)
+          if (s <= own[j])
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              mma16(U[j][q], hi, th[s][j][2 * q], th[s][j][2 * q + 1]);
-              mma16(V[j][q], hi, tl[s][j][2 * q], tl[s][j][2 * q + 1]);
-              mma16(W[j][q], lo, th[s][j][2 * q], th[s][j][2 * q + 1]);
+              mma16(U[j][q], hi, th[s & 1][j][2 * q], th[s & 1][j][2 * q + 1]);
+              mma16(V[j][q], hi, tl[s & 1][j][2 * q], tl[s & 1][j][2 * q + 1]);
+              mma16(W[j][q], lo, th[s & 1][j][2 * q], th[s & 1][j][2 * q + 1]);
             }
       }
       // Rescaled by T's row scales and down by a bound of its row sums, u
       // stays below 2^15 (the scale of x), and so does w_j = Gamma_64,j
       // kappa_j u_j over the largest such factor.
-      gs.u_inv[lane] = make_float2(i0 * tau, i1 * tau);
+      if (part == 0) gs.u_inv[lane] = make_float2(j0 * tau, j1 * tau);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < C::kOwn; ++j) {
         uint32_t f[4], hi[4], lo[4];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const float2 one = make_float2(1.0f, 1.0f);
-          const float2 top =
-              mul2(fma2(U[j][q].top, one, fma2(V[j][q].top, one, W[j][q].top)), ts[j][q]);
-          const float2 low =
-              mul2(fma2(U[j][q].low, one, fma2(V[j][q].low, one, W[j][q].low)), ts[j][q]);
+          const float2 top = mul2(add2(U[j][q].top, add2(V[j][q].top, W[j][q].top)), ts[j][q]);
+          const float2 low = mul2(add2(U[j][q].low, add2(V[j][q].low, W[j][q].low)), ts[j][q]);
           f[2 * q] = h2_bits(__float22half2_rn(top));
           f[2 * q + 1] = h2_bits(__float22half2_rn(low));
           split_h2(mul2(top, dd[j][q]), hi[2 * q], lo[2 * q]);
           split_h2(mul2(low, dd[j][q]), hi[2 * q + 1], lo[2 * q + 1]);
         }
-        gs.w_frag[np_of[j]][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        gs.w_frag[np_of[j]][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        gs.u_frag[np_of[j]][lane] = make_uint4(f[0], f[1], f[2], f[3]);
+        put4(&gs.w_frag[own[j]][0][lane], hi);
+        put4(&gs.w_frag[own[j]][1][lane], lo);
+        put4(&gs.u_frag[own[j]][lane], f);
       }
-      bar_sync(bar_w, 96);
-      // S = gamma S + sum_j w_j k_j^T, 32 key channels at a time
+      bar_sync(bar_w, kGroup);
+      // S = gamma S + sum_j w_j k_j^T, up to 32 key channels at a time
       uint32_t wh[4][4], wl[4][4];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const uint4 a = gs.w_frag[s][0][lane], e = gs.w_frag[s][1][lane];
-        wh[s][0] = a.x, wh[s][1] = a.y, wh[s][2] = a.z, wh[s][3] = a.w;
-        wl[s][0] = e.x, wl[s][1] = e.y, wl[s][2] = e.z, wl[s][3] = e.w;
+        get4(&gs.w_frag[s][0][lane], wh[s]);
+        get4(&gs.w_frag[s][1][lane], wl[s]);
       }
-      const float2 gamma2 = make_float2(gamma, gamma);
-      const float2 b0 = make_float2(i0 * back, i0 * back), b1 = make_float2(i1 * back, i1 * back);
+      const float2 b0 = both(j0 * back), b1 = both(j1 * back);
+      constexpr int kAt = C::kSteps >= 2 ? 2 : 1;  // 16-channel blocks at a time
       float a0 = 0.0f, a1 = 0.0f;
 #pragma unroll
-      for (int np = 0; np < kSteps; np += 2) {
-        Acc acc[4] = {};
+      for (int np = 0; np < C::kSteps; np += kAt) {
+        Acc acc[2 * kAt] = {};
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          uint32_t bb[2][4];
+          uint32_t bb[kAt][4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < kAt; ++j)
             ldsm4_t(bb[j], kt + tile_at<DK>(16 * s + bt_row,
-                                            half * (kHalf / 8) + 2 * (np + j) + bt_piece));
+                                            part * (C::kCols / 8) + 2 * (np + j) + bt_piece));
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < kAt; ++j) {
             mma16(acc[2 * j], wh[s], bb[j][0], bb[j][1]);
             mma16(acc[2 * j + 1], wh[s], bb[j][2], bb[j][3]);
           }
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < kAt; ++j) {
             mma16(acc[2 * j], wl[s], bb[j][0], bb[j][1]);
             mma16(acc[2 * j + 1], wl[s], bb[j][2], bb[j][3]);
           }
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2 * kAt; ++q) {
           Acc &a = S[2 * np + q];
-          a.top = fma2(acc[q].top, b0, mul2(gamma2, a.top));
-          a.low = fma2(acc[q].low, b1, mul2(gamma2, a.low));
+          a.top = fma2(acc[q].top, b0, mul2(both(gamma), a.top));
+          a.low = fma2(acc[q].low, b1, mul2(both(gamma), a.low));
           a0 = max3_abs(a0, a.top.x, a.top.y);
           a1 = max3_abs(a1, a.low.x, a.low.y);
         }
       }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&empty[st]);
+      if (++st == kStages) st = 0;
       pow2_scale(quad_max(a0), m0, i0);
       pow2_scale(quad_max(a1), m1, i1);
     }
     if (seq.state_out) {
 #pragma unroll
-      for (int n = 0; n < kHalf / 8; ++n) {
+      for (int n = 0; n < 2 * C::kSteps; ++n) {
         *reinterpret_cast<float2 *>(seq.state_out + at + 8 * n) = S[n].top;
         *reinterpret_cast<float2 *>(seq.state_out + at + 8 * DK + 8 * n) = S[n].low;
       }
@@ -860,127 +880,204 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
     return;
   }
 
-  // Output warp: o_i = rho_i gamma_i (S q_i) + sum_j P_ij u_j.  It also brings
-  // in the group's values.
-  const bool producer = !Cfg::kProducer && group == 0 && lane == 0;
-  int issued = 0;
-  const uint32_t v_smem = ptx::smem_u32(gs.v[0]);
-  const moe_bf16 *v_src = in.v + static_cast<int64_t>(r.start) * in.v_ld + h * d.v_dim + dv0;
-  const auto fetch_v = [&](int c) {  // the group's channels of chunk c, zeros past the end
+  // Output warps: o_i = rho_i gamma_i (S q_i) + sum_j P_ij u_j.  They also bring
+  // in the group's values, as beta v in the chain's accumulator layout.  Each
+  // has two of the four 16-token blocks, an equal share of P's triangle.
+  const int side = (warp - WARPS * GROUPS) & 1;
+  const int own[2] = {side, 3 - side};
+  const int my_row = lane >> 1;  // of a block, and the half row this lane copies
+  const int64_t row0 = r.start + my_row;
+  const uint32_t v_smem = ptx::smem_u32(gs.v[0]), v_to = v_smem + row32_at(my_row, lane & 1);
+  const uint32_t v_at = v_smem + row32_at(b_row, b_piece);
+  const moe_bf16 *v_src = in.v + row0 * in.v_ld + h * d.v_dim + dv0 + (lane & 1) * 8;
+  const auto fetch_v = [&](int c) {  // the own blocks of chunk c, zeros past the end
     if (c < chunks) {
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int i = p * 16 + (lane >> 1), piece = lane & 1, row = c * kC + i;
-        const bool live = row < r.len;
-        cp_async16(v_smem + (c % 3) * kC * 32 + row32_at(i, piece),
-                   v_src + (live ? row * in.v_ld : 0) + piece * 8, live);
+      for (int j = 0; j < 2; ++j) {
+        const bool live = c * kC + 16 * own[j] + my_row < r.len;
+        cp_async16(v_to + (c % 3) * kC * 32 + own[j] * 16 * 32,
+                   live ? v_src + 16 * own[j] * in.v_ld : in.v, live);
       }
+      v_src += kC * in.v_ld;
     }
     cp_async_commit();
   };
-  const auto wait_full = [&](int c) {
-    if (!dead) dead = !ptx::mbar_wait(&full[c % kStages], (c / kStages) & 1, abort_flag, budget_ns);
+  // The only wait for a chunk's operands: bar_w passes it on.  One that gave
+  // up is not repeated; the loops run to their end on whatever the ring holds,
+  // so that all warps pass every barrier.
+  bool dead = false;
+  const auto wait_full = [&](int stage, uint32_t parity) {
+    if (!dead) dead = !ptx::mbar_wait(&full[stage], parity, abort_flag, budget_ns);
   };
+  // beta v of chunk c (the last copy but two) and its largest per row
+  const auto values = [&](int c, int stage) {
+    cp_async_wait<2>();
+    __syncwarp();
+    const float *vec =
+        reinterpret_cast<const float *>(ring_a + stage * C::kStageA + kKeyTile + 2 * kTri);
+    float top = 0.0f, low = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t vv[4];
+      ldsm4_t(vv, v_at + (c % 3) * kC * 32 + own[j] * 16 * 32);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float2 be =
+            *reinterpret_cast<const float2 *>(vec + kVecBeta * kC + 16 * own[j] + 8 * q + 2 * t);
+        const float2 y0 = mul2(be, make_float2(bf16_lo(vv[2 * q]), bf16_hi(vv[2 * q])));
+        const float2 y1 = mul2(be, make_float2(bf16_lo(vv[2 * q + 1]), bf16_hi(vv[2 * q + 1])));
+        gs.y[own[j]][q][lane] = make_float4(y0.x, y0.y, y1.x, y1.y);
+        top = max3_abs(top, y0.x, y0.y);
+        low = max3_abs(low, y1.x, y1.y);
+      }
+    }
+    gs.v_max[side][lane] = make_float2(quad_max(top), quad_max(low));
+  };
+  // This warp's copy of every chunk: k or T's part into ring a, q or P's into
+  // ring b.
+  static_assert(2 * GROUPS == 4, "an output warp for each copy of a chunk");
+  const int copy = warp - WARPS * GROUPS;
+  const bool into_b = copy & 2, of_head = copy & 1;
+  const size_t base = slot_base(seq, b);
+  const uint8_t *from = of_head ? ws_head + (base * d.v_heads + h) * kHeadBlob + (into_b ? kPartA : 0)
+                                : ws_key + (base * d.qk_heads + hk) * kKeyBlob<DK> + (into_b ? kKeyTile : 0);
+  const size_t from_step = of_head ? static_cast<size_t>(d.v_heads) * kHeadBlob
+                                   : static_cast<size_t>(d.qk_heads) * kKeyBlob<DK>;
+  const uint32_t copy_bytes = !of_head ? kKeyTile : into_b ? kPartB : kPartA;
+  const uint32_t to_step = into_b ? C::kStageB : C::kStageA;
+  const uint32_t to = ptx::smem_u32(into_b ? ring_b : ring_a) + (of_head ? kKeyTile : 0);
+  int fed = 0;  // chunks under way
+  const auto feed = [&](int stage) {
+    if (lane == 0) {
+      mbar_expect(&full[stage], copy_bytes);
+      bulk_load(to + stage * to_step, from, copy_bytes, &full[stage]);
+    }
+    from += from_step;
+    ++fed;
+  };
+  int st = 0;
+  uint32_t parity = 0;
   if (chunks) {
-    if (producer)
-      for (; issued < min(chunks, kStages); ++issued) issue(issued);
+    for (int c = 0; c < min(chunks, kStages - 1); ++c) feed(c);
     fetch_v(0);
     fetch_v(1);
-    wait_full(0);
-    cp_async_wait<1>();
-    bar_sync(bar_w, 96);
+    wait_full(0, 0);
+    bar_sync(bar_w, kGroup);
   }
-  const uint32_t o_at = ptx::smem_u32(gs.o) + row32_at((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
-  moe_bf16 *o_dst = out + static_cast<int64_t>(r.start) * out_ld + h * d.v_dim + dv0;
+  const uint32_t o_at = ptx::smem_u32(gs.o) + row32_at(b_row, b_piece);
+  const uint8_t *o_from = gs.o + row32_at(my_row, lane & 1);
+  moe_bf16 *o_dst = out + row0 * out_ld + h * d.v_dim + dv0 + (lane & 1) * 8;
   for (int c = 0; c < chunks; ++c) {
-    const int st = c % kStages;
-    const uint32_t qt = ptx::smem_u32(ring + st * Cfg::kStageBytes) + kKeyBlob<DK> / 2;
-    const uint32_t pt = qt + kKeyBlob<DK> / 2 + 2 * kTile;
-    const float *vec =
-        reinterpret_cast<const float *>(ring + st * Cfg::kStageBytes + kKeyBlob<DK> + 3 * kTile);
-    if (producer && c > 0 && issued < chunks && !dead) {
-      dead = !wait_empty(issued);
-      if (!dead) issue(issued++);
-    }
-    if (!Cfg::kProducer) __syncwarp();
+    const uint32_t qt = ptx::smem_u32(ring_b + st * C::kStageB), pt = qt + kKeyTile;
+    const float *vec = reinterpret_cast<const float *>(ring_b + st * C::kStageB + kKeyTile + kTri);
     fetch_v(c + 2);
-    if (!Cfg::kAhead) wait_full(c);
-    bar_sync(bar_x, 96);
-    Acc O[8] = {};
+    values(c, st);
+    uint32_t bb[2][2][4];
+    const auto load_q = [&](int s) {
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      // the halves of S have scales of their own
-      Acc acc[8] = {};
+      for (int j = 0; j < 2; ++j)
+        ldsm4(bb[s & 1][j], qt + tile_at<DK>(16 * own[j] + b_row, 2 * s + b_piece));
+    };
+    load_q(0);
+    bar_sync(bar_x, kAll);
+    // The shares of S have scales of their own: brought to the largest.
+    uint32_t a[DK / 16][4];
 #pragma unroll
-      for (int s = 0; s < kHalf / 16; ++s) {
-        const uint4 f = gs.s_frag[side * (kHalf / 16) + s][lane];
-        const uint32_t a[4] = {f.x, f.y, f.z, f.w};
-        uint32_t bb[4][4];
+    for (int s = 0; s < DK / 16; ++s) get4(&gs.s_frag[s][lane], a[s]);
+    float2 si[WARPS], most = both(0.0f);
 #pragma unroll
-        for (int np = 0; np < 4; ++np)
-          ldsm4(bb[np], qt + tile_at<DK>(16 * np + b_row, side * (kHalf / 8) + 2 * s + b_piece));
+    for (int p = 0; p < WARPS; ++p) {
+      si[p] = gs.s_inv[p][lane];
+      most = make_float2(fmaxf(most.x, si[p].x), fmaxf(most.y, si[p].y));
+    }
+    float down0, down1, unused;
+    pow2_above(most.x * 0.5f, unused, down0);  // 1 / most, a power of two
+    pow2_above(most.y * 0.5f, unused, down1);
+    Acc O[2][2] = {};
 #pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          mma16(acc[2 * np], a, bb[np][0], bb[np][1]);
-          mma16(acc[2 * np + 1], a, bb[np][2], bb[np][3]);
-        }
-      }
-      const float2 si = gs.s_inv[side][lane];
+    for (int s = 0; s < DK / 16; ++s) {
+      const float2 f = si[s / C::kSteps];
+      const __half2 f0 = __float2half2_rn(f.x * down0), f1 = __float2half2_rn(f.y * down1);
+      if (s + 1 < DK / 16) load_q(s + 1);
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        O[n].top = fma2(acc[n].top, make_float2(si.x, si.x), O[n].top);
-        O[n].low = fma2(acc[n].low, make_float2(si.y, si.y), O[n].low);
+      for (int e = 0; e < 4; ++e)
+        a[s][e] = h2_bits(__hmul2(*reinterpret_cast<const __half2 *>(&a[s][e]), (e & 1) ? f1 : f0));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        mma16(O[j][0], a[s], bb[s & 1][j][0], bb[s & 1][j][1]);
+        mma16(O[j][1], a[s], bb[s & 1][j][2], bb[s & 1][j][3]);
       }
     }
-    if (Cfg::kAhead && c + 1 < chunks) wait_full(c + 1);
-    cp_async_wait<1>();
-    __syncwarp();
-    bar_sync(bar_w, 96);
+    // what the second product needs, and the first one's factors, ahead of it
+    uint32_t pf[4][2][4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (s <= own[j])
+          ldsm4(pf[s][j], pt + block_of(own[j], s) * kBlock + row32_at(b_row, b_piece));
+    float2 pi[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int col = 16 * own[j] + 8 * q + 2 * t;
+        const float2 oq = *reinterpret_cast<const float2 *>(vec + kVecO * kC + col);
+        pi[j][q] = *reinterpret_cast<const float2 *>(vec + kVecP * kC + col);
+        O[j][q].top = mul2(mul2(O[j][q].top, both(most.x)), oq);
+        O[j][q].low = mul2(mul2(O[j][q].low, both(most.y)), oq);
+      }
+    const int next = st + 1 == kStages ? 0 : st + 1;
+    const uint32_t next_parity = next ? parity : parity ^ 1;
+    if (c + 1 < chunks) wait_full(next, next_parity);
+    bar_sync(bar_w, kGroup);
+    // chunk c - 1's stage is free (bar_x)
+    if (c + 2 < chunks && !*reinterpret_cast<volatile int *>(abort_flag))
+      feed(st == 0 ? kStages - 1 : st - 1);
     const float2 ui = gs.u_inv[lane];
-    Acc I[8] = {};
+    Acc I[2][2] = {};
+    uint32_t uf[4][4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const uint4 f = gs.u_frag[s][lane];
-      const uint32_t a[4] = {f.x, f.y, f.z, f.w};
-      uint32_t bb[4][4];
+    for (int s = 0; s < 4; ++s) get4(&gs.u_frag[s][lane], uf[s]);
 #pragma unroll
-      for (int np = s; np < 4; ++np)
-        ldsm4(bb[np], pt + tile_at<kC>(16 * np + b_row, 2 * s + b_piece));
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int np = s; np < 4; ++np) {
-        mma16(I[2 * np], a, bb[np][0], bb[np][1]);
-        mma16(I[2 * np + 1], a, bb[np][2], bb[np][3]);
-      }
-    }
+      for (int j = 0; j < 2; ++j)
+        if (s <= own[j]) {
+          mma16(I[j][0], uf[s], pf[s][j][0], pf[s][j][1]);
+          mma16(I[j][1], uf[s], pf[s][j][2], pf[s][j][3]);
+        }
 #pragma unroll
-    for (int np = 0; np < 4; ++np) {
+    for (int j = 0; j < 2; ++j) {
       uint32_t w[4];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const int n = 2 * np + q;
-        const float2 oq = *reinterpret_cast<const float2 *>(vec + kVecO * kC + 8 * n + 2 * t);
-        const float2 pi = *reinterpret_cast<const float2 *>(vec + kVecP * kC + 8 * n + 2 * t);
-        const float2 top = fma2(mul2(I[n].top, make_float2(ui.x, ui.x)), pi, mul2(O[n].top, oq));
-        const float2 low = fma2(mul2(I[n].low, make_float2(ui.y, ui.y)), pi, mul2(O[n].low, oq));
+        const float2 top = fma2(mul2(I[j][q].top, both(ui.x)), pi[j][q], O[j][q].top);
+        const float2 low = fma2(mul2(I[j][q].low, both(ui.y)), pi[j][q], O[j][q].low);
         w[2 * q] = pack_bf16(top.x, top.y);
         w[2 * q + 1] = pack_bf16(low.x, low.y);
       }
       // transposed back: token rows of 16 channels
-      stsm4_t(o_at + np * 16 * 32, w[0], w[1], w[2], w[3]);
+      stsm4_t(o_at + own[j] * 16 * 32, w[0], w[1], w[2], w[3]);
     }
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&empty[st]);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int i = p * 16 + (lane >> 1), piece = lane & 1, row = c * kC + i;
-      if (row < r.len)
-        *reinterpret_cast<uint4 *>(o_dst + row * out_ld + piece * 8) =
-            *reinterpret_cast<const uint4 *>(gs.o + row32_at(i, piece));
-    }
+    for (int j = 0; j < 2; ++j)
+      if (c * kC + 16 * own[j] + my_row < r.len)
+        *reinterpret_cast<uint4 *>(o_dst + 16 * own[j] * out_ld) =
+            *reinterpret_cast<const uint4 *>(o_from + own[j] * 16 * 32);
+    o_dst += kC * out_ld;
+    st = next, parity = next_parity;
     __syncwarp();
   }
   cp_async_wait<0>();
-  if (producer) drain(issued);
+  if (lane == 0) {
+    // copies in flight land before the CTA's shared memory is given up
+    int ignore = 0;
+    for (int c = max(0, fed - kStages); c < fed; ++c)
+      ptx::mbar_wait(&full[c % kStages], (c / kStages) & 1, &ignore, ptx::kDrainBudgetNs);
+    if (*reinterpret_cast<volatile int *>(abort_flag)) set_status(seq.status, MOE_DEV_TIMEOUT);
+  }
 }
 
 // Sets a kernel's shared-memory limit once per device.
@@ -996,17 +1093,17 @@ cudaError_t allow_smem(F kernel, int bytes, std::atomic<uint64_t> &done) {
   return e;
 }
 
-template <int DK, int GROUPS>
+template <int DK, int WARPS, int GROUPS>
 cudaError_t launch_chain(const moe_delta_dims &d, const moe_delta_inputs &in, const DeltaSeqs &seq,
                          const uint8_t *ws, const uint8_t *ws_key, const uint8_t *ws_head,
                          moe_bf16 *out, int64_t out_ld, cudaStream_t s) {
-  using Cfg = ChainCfg<DK, GROUPS>;
-  static_assert(Cfg::kSmem <= 227 * 1024, "shared memory of one SM");
+  using C = Chain<DK, WARPS, GROUPS>;
+  static_assert(C::kSmem <= 227 * 1024, "shared memory of one SM");
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(delta_chain_kernel<DK, GROUPS>, Cfg::kSmem, done);
+  cudaError_t e = allow_smem(delta_chain_kernel<DK, WARPS, GROUPS>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   const int64_t grid = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / (16 * GROUPS));
-  delta_chain_kernel<DK, GROUPS><<<static_cast<unsigned>(grid), Cfg::kThreads, Cfg::kSmem, s>>>(
+  delta_chain_kernel<DK, WARPS, GROUPS><<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, s>>>(
       d, in, seq, ws, ws_key, ws_head, out, out_ld, tc_wait_budget_ns());
   return cudaGetLastError();
 }
@@ -1030,10 +1127,7 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
   const dim3 grid(static_cast<unsigned>(slots), d.v_heads / heads);
   delta_prep_kernel<DK><<<grid, kPrepThreads, kSmem, s>>>(d, in, seq, heads, ws, ws_key, ws_head);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int64_t groups = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / 16);
-  if (groups <= 2 * 152)
-    return launch_chain<DK, 2>(d, in, seq, ws, ws_key, ws_head, out, out_ld, s);
-  return launch_chain<DK, 4>(d, in, seq, ws, ws_key, ws_head, out, out_ld, s);
+  return launch_chain<DK, 2, 2>(d, in, seq, ws, ws_key, ws_head, out, out_ld, s);
 }
 
 }  // namespace

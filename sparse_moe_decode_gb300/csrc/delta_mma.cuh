@@ -158,6 +158,15 @@ __device__ __forceinline__ void bulk_store_wait() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// Announces `bytes` of copies on a barrier.  Relaxed: it publishes nothing of
+// this thread's, so it need not wait for its stores in flight.
+__device__ __forceinline__ void mbar_expect(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cta.shared::cta.b64 _, [%0], %1;" ::"r"(
+                   ptx::smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+
 // Hardware barrier `id` of `threads` threads: sync waits, arrive does not.
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
