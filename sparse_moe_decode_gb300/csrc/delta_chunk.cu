@@ -87,18 +87,21 @@ __device__ __forceinline__ int slot_base(const DeltaSeqs &s, int b) {
 
 // ------------------------------------------------------------------- prep
 
-constexpr int kTLd = kC + 4;  // row stride of T
-
-// T's rows have room for four values beside them: the tokens' factors.
-enum { kGLo = kC, kKappa, kRho };
+constexpr int kTLd = kC + 4;     // row stride of T
+constexpr int kPrepHeads = 4;    // value heads of one CTA at most
 
 template <int DK>
 struct PrepSmem {
   alignas(128) uint8_t key[kKeyBlob<DK>];
-  // L (fp32, permuted) until T's two terms replace it; P; the vectors, of
-  // which kVecT holds the sums of g until T's scales replace them
+  // L (fp32) until T's two terms replace it; P; the vectors
   alignas(128) uint8_t head[kHeadBlob];
   float t[kC * kTLd];  // T; blocks of 16 above the diagonal are never touched
+  // the tokens' factors; per head the sums of g in units of log 2 (two terms)
+  // and beta
+  float kappa[kC], rho[kC], ghi[kPrepHeads][kC], glo[kPrepHeads][kC], beta[kPrepHeads][kC];
+  // Gamma's factors about the first token r of each block of rows:
+  // kappa_j e^{G_r - G_j} for the columns left of it, e^{G_i - G_r}
+  float col[4][kC], row[kC];
 };
 
 // Where L(i, j) lies, in the same blocks: pieces of four columns permuted by
@@ -117,26 +120,34 @@ __device__ __forceinline__ void token_scale(float ss, float &mult, float &inv) {
   inv = __uint_as_float(static_cast<uint32_t>(254 - m) << 23);
 }
 
-// A 16 x 8 tile (rows r0, columns c0) of A B over k in [k0, k1): fp32 values
-// as two tf32 terms each, three products.
-template <class FA, class FB>
-__device__ __forceinline__ void product(float (&acc)[4], int r0, int c0, int k0, int k1, FA a_of,
-                                        FB b_of, int lane) {
+// A 16 x 8 tile (rows r0, columns c0) of A B over STEPS steps of eight from
+// k0: fp32 values as two tf32 terms each, three products.
+template <int STEPS, class FA, class FB>
+__device__ __forceinline__ void product(float (&acc)[4], int r0, int c0, int k0, FA a_of, FB b_of,
+                                        int lane) {
   const int g = lane >> 2, t = lane & 3;
+  float a[STEPS][4], b[STEPS][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = 0.0f;
-  for (int k = k0; k < k1; k += 8) {
-    uint32_t ah[4], al[4], bh[2], bl[2];
-    split_tf32(a_of(r0 + g, k + t), ah[0], al[0]);
-    split_tf32(a_of(r0 + g + 8, k + t), ah[1], al[1]);
-    split_tf32(a_of(r0 + g, k + t + 4), ah[2], al[2]);
-    split_tf32(a_of(r0 + g + 8, k + t + 4), ah[3], al[3]);
-    split_tf32(b_of(k + t, c0 + g), bh[0], bl[0]);
-    split_tf32(b_of(k + t + 4, c0 + g), bh[1], bl[1]);
-    mma8(acc, ah, bl[0], bl[1]);
-    mma8(acc, al, bh[0], bh[1]);
-    mma8(acc, ah, bh[0], bh[1]);
+  for (int s = 0; s < STEPS; ++s) {
+    const int k = k0 + 8 * s;
+    a[s][0] = a_of(r0 + g, k + t), a[s][1] = a_of(r0 + g + 8, k + t);
+    a[s][2] = a_of(r0 + g, k + t + 4), a[s][3] = a_of(r0 + g + 8, k + t + 4);
+    b[s][0] = b_of(k + t, c0 + g), b[s][1] = b_of(k + t + 4, c0 + g);
   }
+  float part[3][4] = {};
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    uint32_t ah[4], al[4], bh[2], bl[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_tf32(a[s][i], ah[i], al[i]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) split_tf32(b[s][i], bh[i], bl[i]);
+    mma8(part[0], ah, bl[0], bl[1]);
+    mma8(part[1], al, bh[0], bh[1]);
+    mma8(part[2], ah, bh[0], bh[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = part[2][i] + (part[0][i] + part[1][i]);
 }
 
 // One CTA per chunk and key head, for `heads` of the value heads that read
@@ -186,12 +197,21 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
   const int g = lane >> 2, t = lane & 3;
   const uint32_t kt = ptx::smem_u32(sm.key);
 
-  // k and q: scaled to fp16, and the tokens' factors.  Eight lanes a row.
+  // k and q: scaled to fp16, and the tokens' factors.  Eight lanes a row.  While
+  // they come in, warp w sums head w's decays: in fp64, in units of log 2, kept
+  // as two fp32 terms, so that differences of large sums keep their digits.
   {
     constexpr int kPieces = DK / 64;  // 16-byte pieces of a lane
     const moe_bf16 *src = is_q ? in.q : in.k;
     const int64_t ld = is_q ? in.q_ld : in.k_ld;
     const int piece = lane & 7;
+    float g0 = 0.0f, g1 = 0.0f, be0 = 0.0f, be1 = 0.0f;
+    if (warp < heads) {
+      const int64_t i = row0 + 2 * lane;
+      if (2 * lane < left) g0 = in.g[i * in.g_ld + h0 + warp], be0 = in.beta[i * in.beta_ld + h0 + warp];
+      if (2 * lane + 1 < left)
+        g1 = in.g[(i + 1) * in.g_ld + h0 + warp], be1 = in.beta[(i + 1) * in.beta_ld + h0 + warp];
+    }
     uint4 raw[4][kPieces];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
@@ -201,6 +221,22 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
         raw[p][e] = i < left ? *reinterpret_cast<const uint4 *>(src + (row0 + i) * ld + hk * DK +
                                                                 (piece + 8 * e) * 8)
                              : make_uint4(0, 0, 0, 0);
+    }
+    if (warp < heads) {
+      const double d1 = delta_log_decay(g1);
+      double sum = delta_log_decay(g0) + d1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double up = __shfl_up_sync(kFull, sum, o);
+        if (lane >= o) sum += up;
+      }
+      const double kLog2E = 1.4426950408889634;
+      const double second = sum * kLog2E, first = (sum - d1) * kLog2E;
+      const float2 hi2 = make_float2(static_cast<float>(first), static_cast<float>(second));
+      *reinterpret_cast<float2 *>(&sm.ghi[warp][2 * lane]) = hi2;
+      *reinterpret_cast<float2 *>(&sm.glo[warp][2 * lane]) =
+          make_float2(static_cast<float>(first - hi2.x), static_cast<float>(second - hi2.y));
+      *reinterpret_cast<float2 *>(&sm.beta[warp][2 * lane]) = make_float2(be0, be1);
     }
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
@@ -232,7 +268,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
       }
       if (d.qk_norm) inv = inv / sqrtf(ss + d.qk_eps);
       if (is_q) inv *= d.scale;
-      if (piece == 0) sm.t[i * kTLd + (is_q ? kRho : kKappa)] = i < left ? inv : 0.0f;
+      if (piece == 0) (is_q ? sm.rho : sm.kappa)[i] = i < left ? inv : 0.0f;
     }
   }
   __syncthreads();
@@ -244,67 +280,54 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
     const int b_row = (lane & 7) + ((lane >> 4) << 3), b_piece = (lane >> 3) & 1;
 #pragma unroll
     for (int s = 0; s < DK / 16; ++s) {
-      uint32_t a[4], b[4];
+      uint32_t a[4], bd[4], b[3][4];
       ldsm4(a, at + tile_at<DK>(16 * w + (lane & 15), 2 * s + (lane >> 4)));
-      ldsm4(b, kt + tile_at<DK>(16 * w + b_row, 2 * s + b_piece));
-      mma16(dia[0], a, b[0], b[1]);
-      mma16(dia[1], a, b[2], b[3]);
+      ldsm4(bd, kt + tile_at<DK>(16 * w + b_row, 2 * s + b_piece));
+#pragma unroll
+      for (int np = 0; np < 3; ++np)
+        if (np < w) ldsm4(b[np], kt + tile_at<DK>(16 * np + b_row, 2 * s + b_piece));
+      mma16(dia[0], a, bd[0], bd[1]);
+      mma16(dia[1], a, bd[2], bd[3]);
 #pragma unroll
       for (int np = 0; np < 3; ++np)
         if (np < w) {
-          ldsm4(b, kt + tile_at<DK>(16 * np + b_row, 2 * s + b_piece));
-          mma16(off[2 * np], a, b[0], b[1]);
-          mma16(off[2 * np + 1], a, b[2], b[3]);
+          mma16(off[2 * np], a, b[np][0], b[np][1]);
+          mma16(off[2 * np + 1], a, b[np][2], b[np][3]);
         }
     }
   }
 
   float *vec = reinterpret_cast<float *>(sm.head + 2 * kTri);
   float *vec_b = reinterpret_cast<float *>(sm.head + kPartA + kTri);
-  float *ghi = vec + kVecT * kC;
   float *L = reinterpret_cast<float *>(sm.head);
   float *T = sm.t;
   for (int hh = 0; hh < heads; ++hh) {
     const int h = h0 + hh;
-    // Decays: sums of g in fp64, in units of log 2, kept as two fp32 terms, so
-    // that differences of large sums keep their digits.
+    const float *ghi = sm.ghi[hh], *glo = sm.glo[hh];
+    // Left of the diagonal block Gamma_ij = e^{G_i - G_r} e^{G_r - G_j} about
+    // the block's first token r: both factors are decays, and the product
+    // underflows only where Gamma does.
+    {
+      const int j = tid & 63, rb = tid >> 6;
+      if (j < 16 * rb)
+        sm.col[rb][j] = sm.kappa[j] * exp2f((ghi[16 * rb] - ghi[j]) + (glo[16 * rb] - glo[j]));
+      else if (j < 16 * rb + 16)
+        sm.row[j] = exp2f((ghi[j] - ghi[16 * rb]) + (glo[j] - glo[16 * rb]));
+    }
     if (warp == 4) {
+      // the chain's and the outputs' factors of the tokens; the update's,
+      // Gamma_64,j kappa_j, over a power of two above the largest
       const int i = 2 * lane;
-      double g0 = 0.0, g1 = 0.0;
-      float be0 = 0.0f, be1 = 0.0f;
-      if (i < left) {
-        g0 = delta_log_decay(in.g[(row0 + i) * in.g_ld + h]);
-        be0 = in.beta[(row0 + i) * in.beta_ld + h];
-      }
-      if (i + 1 < left) {
-        g1 = delta_log_decay(in.g[(row0 + i + 1) * in.g_ld + h]);
-        be1 = in.beta[(row0 + i + 1) * in.beta_ld + h];
-      }
-      double sum = g0 + g1;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_up_sync(kFull, sum, o);
-        if (lane >= o) sum += up;
-      }
-      const double kLog2E = 1.4426950408889634;
-      const double second = sum * kLog2E, first = (sum - g1) * kLog2E;
-      const double total = __shfl_sync(kFull, second, 31);
-      const float2 sh = make_float2(static_cast<float>(first), static_cast<float>(second));
-      const float2 kap = make_float2(T[i * kTLd + kKappa], T[(i + 1) * kTLd + kKappa]);
-      const float2 rho = make_float2(T[i * kTLd + kRho], T[(i + 1) * kTLd + kRho]);
+      const float2 sh = *reinterpret_cast<const float2 *>(ghi + i);
+      const float2 sl = *reinterpret_cast<const float2 *>(glo + i);
+      const float2 be = *reinterpret_cast<const float2 *>(sm.beta[hh] + i);
+      const float2 kap = *reinterpret_cast<const float2 *>(sm.kappa + i);
+      const float2 rho = *reinterpret_cast<const float2 *>(sm.rho + i);
+      const float th = ghi[kC - 1], tl = glo[kC - 1];
       const float2 gamma = make_float2(exp2f(sh.x), exp2f(sh.y));
-      *reinterpret_cast<float2 *>(ghi + i) = sh;
-      T[i * kTLd + kGLo] = static_cast<float>(first - sh.x);
-      T[(i + 1) * kTLd + kGLo] = static_cast<float>(second - sh.y);
-      *reinterpret_cast<float2 *>(vec + kVecBeta * kC + i) = make_float2(be0, be1);
-      const float2 cc = make_float2(-be0 * gamma.x * kap.x, -be1 * gamma.y * kap.y);
-      *reinterpret_cast<float2 *>(vec + kVecC * kC + i) = cc;
-      *reinterpret_cast<float2 *>(vec_b + kVecO * kC + i) =
-          make_float2(rho.x * gamma.x, rho.y * gamma.y);
-      // the update's factors, Gamma_64,j kappa_j, over a power of two above
-      // the largest
-      float2 dd = make_float2(exp2f(static_cast<float>(total - first)) * kap.x,
-                              exp2f(static_cast<float>(total - second)) * kap.y);
+      const float2 cc = make_float2(-be.x * gamma.x * kap.x, -be.y * gamma.y * kap.y);
+      const float2 dd = make_float2(exp2f((th - sh.x) + (tl - sl.x)) * kap.x,
+                                    exp2f((th - sh.y) + (tl - sl.y)) * kap.y);
       float dmax = fmaxf(dd.x, dd.y), cmax = fmaxf(fabsf(cc.x), fabsf(cc.y));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -313,9 +336,13 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
       }
       float up, down;
       pow2_above(dmax, up, down);
+      *reinterpret_cast<float2 *>(vec + kVecBeta * kC + i) = be;
+      *reinterpret_cast<float2 *>(vec + kVecC * kC + i) = cc;
       *reinterpret_cast<float2 *>(vec + kVecD * kC + i) = make_float2(dd.x * down, dd.y * down);
-      if (lane == 0) {
-        vec[kVecMisc * kC + kGamma] = exp2f(static_cast<float>(total));
+      *reinterpret_cast<float2 *>(vec_b + kVecO * kC + i) =
+          make_float2(rho.x * gamma.x, rho.y * gamma.y);
+      if (lane == 31) {
+        vec[kVecMisc * kC + kGamma] = gamma.y;
         vec[kVecMisc * kC + kDUp] = up;
         vec[kVecMisc * kC + kCMax] = cmax;
       }
@@ -323,29 +350,23 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
     __syncthreads();
 
     // L = beta_i kappa_i Gamma_ij kappa_j k_i.k_j below the diagonal, P =
-    // rho_i Gamma_ij kappa_j q_i.k_j up to it.  Left of the diagonal block
-    // Gamma_ij = e^{G_i - G_r} e^{G_r - G_j} about the block's first token r:
-    // both factors are decays, and the product underflows only where Gamma does.
+    // rho_i Gamma_ij kappa_j q_i.k_j up to it
     {
       const int ref = 16 * w, i0 = ref + g, i1 = i0 + 8;
-      const float rh = ghi[ref], rl = T[ref * kTLd + kGLo];
-      const float h0r = ghi[i0], l0r = T[i0 * kTLd + kGLo], h1r = ghi[i1],
-                  l1r = T[i1 * kTLd + kGLo];
+      const float h0r = ghi[i0], l0r = glo[i0], h1r = ghi[i1], l1r = glo[i1];
       float f0, f1;
       if (is_q) {
-        f0 = T[i0 * kTLd + kRho], f1 = T[i1 * kTLd + kRho];
+        f0 = sm.rho[i0], f1 = sm.rho[i1];
       } else {
-        f0 = vec[kVecBeta * kC + i0] * T[i0 * kTLd + kKappa];
-        f1 = vec[kVecBeta * kC + i1] * T[i1 * kTLd + kKappa];
+        f0 = sm.beta[hh][i0] * sm.kappa[i0];
+        f1 = sm.beta[hh][i1] * sm.kappa[i1];
       }
-      const float a0 = f0 * exp2f((h0r - rh) + (l0r - rl));
-      const float a1 = f1 * exp2f((h1r - rh) + (l1r - rl));
       // P's row scale from norms: by their scales k and q stay below 2^15, so
       // |P_ij| <= rho_i max kappa 2^30, which goes to 2^11 or less (room for
       // decays that grow by up to 2^5).
       float s0 = 1.0f, s1 = 1.0f;
       if (is_q) {
-        float kmax = fmaxf(T[lane * kTLd + kKappa], T[(lane + 32) * kTLd + kKappa]);
+        float kmax = fmaxf(sm.kappa[lane], sm.kappa[lane + 32]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) kmax = fmaxf(kmax, __shfl_xor_sync(kFull, kmax, o));
         float up0, up1;
@@ -354,42 +375,40 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
         s0 *= 0x1p-19f, s1 *= 0x1p-19f;
         if (t == 0) vec_b[kVecP * kC + i0] = up0 * 0x1p19f, vec_b[kVecP * kC + i1] = up1 * 0x1p19f;
       }
+      f0 *= s0, f1 *= s1;
+      const float a0 = f0 * sm.row[i0], a1 = f1 * sm.row[i1];
       uint8_t *P = sm.head + kPartA + 4 * t;
       // one tile: eight columns from `col` of this warp's rows
       const auto put_tile = [&](int col, float2 top, float2 low) {
         if (is_q) {
-          *reinterpret_cast<__half2 *>(P + tri_at(i0, col / 8)) =
-              __float22half2_rn(mul2(top, make_float2(s0, s0)));
-          *reinterpret_cast<__half2 *>(P + tri_at(i1, col / 8)) =
-              __float22half2_rn(mul2(low, make_float2(s1, s1)));
+          *reinterpret_cast<__half2 *>(P + tri_at(i0, col / 8)) = __float22half2_rn(top);
+          *reinterpret_cast<__half2 *>(P + tri_at(i1, col / 8)) = __float22half2_rn(low);
         } else {
           *reinterpret_cast<float2 *>(L + l_at(i0, col + 2 * t)) = top;
           *reinterpret_cast<float2 *>(L + l_at(i1, col + 2 * t)) = low;
         }
       };
 #pragma unroll
-      for (int n = 0; n < 6; ++n) {
+      for (int n = 0; n < 6; ++n)
         if (n < 2 * w) {
-          const int j = 8 * n + 2 * t;
-          const float2 gj = *reinterpret_cast<const float2 *>(ghi + j);
-          const float *tj = T + j * kTLd;
-          const float2 col =
-              make_float2(tj[kKappa] * exp2f((rh - gj.x) + (rl - tj[kGLo])),
-                          tj[kTLd + kKappa] * exp2f((rh - gj.y) + (rl - tj[kTLd + kGLo])));
+          const float2 col = *reinterpret_cast<const float2 *>(&sm.col[w][8 * n + 2 * t]);
           put_tile(8 * n, mul2(make_float2(off[n][0], off[n][1]), mul2(col, make_float2(a0, a0))),
                    mul2(make_float2(off[n][2], off[n][3]), mul2(col, make_float2(a1, a1))));
         }
-      }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
+        const int j = ref + 8 * q + 2 * t;
+        const float2 gj = *reinterpret_cast<const float2 *>(ghi + j);
+        const float2 lj = *reinterpret_cast<const float2 *>(glo + j);
+        const float2 kj = *reinterpret_cast<const float2 *>(sm.kappa + j);
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int i = (e >> 1) ? i1 : i0, j = ref + 8 * q + 2 * t + (e & 1);
-          const float *tj = T + j * kTLd;
-          const float diff = (((e >> 1) ? h1r : h0r) - ghi[j]) + (((e >> 1) ? l1r : l0r) - tj[kGLo]);
-          const bool on = is_q ? j <= i : j < i;
-          v[e] = on ? ((e >> 1) ? f1 : f0) * exp2f(diff) * tj[kKappa] * dia[q][e] : 0.0f;
+          const int i = (e >> 1) ? i1 : i0, jj = j + (e & 1);
+          const float diff = (((e >> 1) ? h1r : h0r) - ((e & 1) ? gj.y : gj.x)) +
+                             (((e >> 1) ? l1r : l0r) - ((e & 1) ? lj.y : lj.x));
+          const bool on = is_q ? jj <= i : jj < i;
+          v[e] = on ? ((e >> 1) ? f1 : f0) * exp2f(diff) * ((e & 1) ? kj.y : kj.x) * dia[q][e] : 0.0f;
         }
         put_tile(ref + 8 * q, make_float2(v[0], v[1]), make_float2(v[2], v[3]));
       }
@@ -431,20 +450,23 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
     if (warp < 4) {
       // a warp's eight columns of B A^-1 are all that it reads of it
       const int o = 32 * (warp >> 1), c0 = o + 8 * (warp & 1);
-      product(acc, o + 16, c0, c0, o + 16, l_of, t_of, lane);
+      product<2>(acc, o + 16, c0, o, l_of, t_of, lane);
       put(acc, o + 16, c0, 1.0f);
       __syncwarp();
-      product(acc, o + 16, c0, o + 16, o + 32, t_of, t_of, lane);
+      product<2>(acc, o + 16, c0, o + 16, t_of, t_of, lane);
       __syncwarp();
       put(acc, o + 16, c0, -1.0f);
     }
     __syncthreads();
     {
       const int r0 = 32 + 16 * (warp >> 2), c0 = 8 * (warp & 3);
-      product(acc, r0, c0, c0, 32, l_of, t_of, lane);  // T(k, c) = 0 for k < c
+      // T(k, c) = 0 for k < c, and its blocks above the diagonal do not exist
+      if ((warp & 3) < 2) product<4>(acc, r0, c0, 0, l_of, t_of, lane);
+      else product<2>(acc, r0, c0, 16, l_of, t_of, lane);
       put(acc, r0, c0, 1.0f);
       __syncthreads();
-      product(acc, r0, c0, 32, r0 + 16, t_of, t_of, lane);
+      if (warp < 4) product<2>(acc, r0, c0, 32, t_of, t_of, lane);
+      else product<4>(acc, r0, c0, 32, t_of, t_of, lane);
       __syncthreads();
       put(acc, r0, c0, -1.0f);
     }
@@ -510,7 +532,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
       if (h % ratio == 0)
         bulk_store(ws_key + (static_cast<size_t>(slot) * d.qk_heads + hk) * kKeyBlob<DK>,
                    ptx::smem_u32(sm.key), kKeyBlob<DK>);
-      bulk_store_wait();
+      bulk_store_wait(hh + 1 == heads);
     }
     if (hh + 1 < heads) __syncthreads();  // the copy has left the head's place
   }
@@ -1108,8 +1130,8 @@ cudaError_t launch_chain(const moe_delta_dims &d, const moe_delta_inputs &in, co
   return cudaGetLastError();
 }
 
-// Chunks times key heads from which a CTA of the first kernel serves all the
-// value heads of its key head.
+// Chunks times key heads from which a CTA of the first kernel serves several of
+// the value heads of its key head.
 constexpr size_t kPrepShare = 1000;
 
 template <int DK>
@@ -1123,7 +1145,10 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
   cudaError_t e = allow_smem(delta_prep_kernel<DK>, kSmem, done);
   if (e != cudaSuccess) return e;
   const int ratio = d.v_heads / d.qk_heads;
-  const int heads = slots * d.qk_heads >= kPrepShare ? ratio : 1;
+  int heads = 1;
+  if (slots * d.qk_heads >= kPrepShare)
+    for (int n = 2; n <= kPrepHeads; ++n)
+      if (ratio % n == 0) heads = n;
   const dim3 grid(static_cast<unsigned>(slots), d.v_heads / heads);
   delta_prep_kernel<DK><<<grid, kPrepThreads, kSmem, s>>>(d, in, seq, heads, ws, ws_key, ws_head);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

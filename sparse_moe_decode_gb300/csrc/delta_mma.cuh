@@ -153,9 +153,12 @@ __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t byt
                "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void bulk_store_wait() {
+// Waits for this thread's bulk stores: until shared memory has been read, or
+// (`written`) until they are complete.
+__device__ __forceinline__ void bulk_store_wait(bool written) {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if (written) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // Announces `bytes` of copies on a barrier.  Relaxed: it publishes nothing of
