@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "pair.cuh"
 #include "sm100_ptx.cuh"
 
 namespace moe {
@@ -79,26 +80,6 @@ __device__ __forceinline__ uint32_t h2_bits(__half2 h) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// d = a b + c on two fp32 at once.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
 // max(|a|, |b|, |c|), NaN ignored.
 __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   float d;
@@ -118,12 +99,6 @@ __device__ __forceinline__ void split_h2(float2 x, uint32_t &hi, uint32_t &lo) {
       : "=f"(a), "=f"(b)
       : "r"(hi), "f"(x.x), "f"(x.y));
   lo = h2_bits(__floats2half2_rn(a, b));
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {

@@ -6,20 +6,15 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "kernels.h"
 #include "mixer.h"
+#include "pair.cuh"
 
 namespace moe {
 namespace {
 
-// exp's argument is rounded once: a relative error of the sigmoid of 2^-21 up
-// to |z| = 8 and of |z| 2^-24 beyond, far below the one rounding to bf16.
-__device__ __forceinline__ float act(float z, int kind) {
-  if (kind == MOE_ACT_IDENTITY) return z;
-  const float s = __fdividef(1.0f, 1.0f + __expf(-z));
-  return kind == MOE_ACT_SILU ? z * s : s;
-}
-
-// VEC consecutive bf16.
+// VEC consecutive bf16, held in VALUES as pairs of fp32 (VEC = 1: a pair whose
+// second value is 0).
 template <int VEC>
 struct Bits;
 template <>
@@ -35,27 +30,49 @@ struct Bits<1> {
   using T = uint16_t;
 };
 
-__device__ __forceinline__ void unpack(uint4 w, float (&v)[8]) {
+__device__ __forceinline__ void unpack(uint4 w, float2 (&v)[4]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(u[i]), v[2 * i + 1] = bf16_hi(u[i]);
+  for (int i = 0; i < 4; ++i) v[i] = make_float2(bf16_lo(u[i]), bf16_hi(u[i]));
 }
-__device__ __forceinline__ void unpack(uint32_t w, float (&v)[2]) {
-  v[0] = bf16_lo(w), v[1] = bf16_hi(w);
+__device__ __forceinline__ void unpack(uint32_t w, float2 (&v)[1]) {
+  v[0] = make_float2(bf16_lo(w), bf16_hi(w));
 }
-__device__ __forceinline__ void unpack(uint16_t w, float (&v)[1]) { v[0] = bf16_to_f32(w); }
+__device__ __forceinline__ void unpack(uint16_t w, float2 (&v)[1]) {
+  v[0] = make_float2(bf16_to_f32(w), 0.0f);
+}
 
-__device__ __forceinline__ uint32_t pair(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
+__device__ __forceinline__ uint4 pack(const float2 (&v)[4]) {
+  return make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y),
+                    pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
 }
-__device__ __forceinline__ uint4 pack(const float (&v)[8]) {
-  return make_uint4(pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7]));
+__device__ __forceinline__ void pack(const float2 (&v)[1], uint32_t &w) {
+  w = pack_bf16(v[0].x, v[0].y);
 }
-__device__ __forceinline__ uint32_t pack(const float (&v)[2]) { return pair(v[0], v[1]); }
-__device__ __forceinline__ uint16_t pack(const float (&v)[1]) {
-  return static_cast<uint16_t>(pair(v[0], 0.0f));
+__device__ __forceinline__ void pack(const float2 (&v)[1], uint16_t &w) {
+  w = static_cast<uint16_t>(pack_bf16(v[0].x, 0.0f));
+}
+__device__ __forceinline__ void pack(const float2 (&v)[4], uint4 &w) { w = pack(v); }
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// exp's argument is rounded once: a relative error of the sigmoid of 2^-21 up
+// to |z| = 8 and of |z| 2^-24 beyond, far below the one rounding to bf16.
+__device__ __forceinline__ float sigmoid(float z) {
+  return __fdividef(1.0f, 1.0f + __expf(-z));
+}
+
+// z -> act(z); the kind is looked at once for all values.
+template <int N>
+__device__ __forceinline__ void activate(float2 (&z)[N], int kind) {
+  if (kind == MOE_ACT_SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = make_float2(sigmoid(z[i].x), sigmoid(z[i].y));
+  } else if (kind == MOE_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      z[i] = mul2(z[i], make_float2(sigmoid(z[i].x), sigmoid(z[i].y)));
+  }
 }
 
 // Sum over the `lanes` threads of a row: a power of two up to 32 (groups of
@@ -77,105 +94,165 @@ __device__ __forceinline__ float row_sum(float v, int lanes, float *tmp) {
 
 constexpr int kRowThreads = 256;  // of a block whose rows have up to 32 threads each
 
+// Threads of an SM that the rows are spread over: what the registers allow
+// (75 a thread with 16-byte groups, 64 in blocks of up to 1024, 32 to 40 with
+// narrower groups).  One block more than fit costs a second round: 16384 rows
+// of 2048 took 58 us at 768, 72 us at 1024.
+template <int VEC, int NV, int MOST>
+constexpr int kSmThreads = NV > 1 || (VEC == 8 && MOST > 256) ? 1024 : VEC == 8 ? 768 : 1536;
+
 // `1 << shift` threads of a warp (or, CTA, the whole block) share a row,
 // thread l the groups of VEC values l, l + lanes, ... (NV of them at most).
-// Everything a thread reads is asked for before the first sum needs it.
-template <int VEC, int NV, bool CTA>
-__global__ void __launch_bounds__(CTA ? 1024 : kRowThreads)
+// Blocks stay and take row after row; with one group per thread (NV = 1) the
+// next row's values are on their way while a row's sums are formed.
+// MOST: threads of a block at most.
+template <int VEC, int NV, bool CTA, int MOST>
+__global__ void __launch_bounds__(MOST)
 norm_gate_kernel(moe_norm_args a, int shift) {
   using W = typename Bits<VEC>::T;
-  __shared__ float tmp[2][32];
-  const uint32_t r = CTA ? blockIdx.x : (blockIdx.x * (kRowThreads >> shift)) + (threadIdx.x >> shift);
+  __shared__ float tmp[2][2][32];
   const int l = CTA ? threadIdx.x : threadIdx.x & ((1 << shift) - 1);
   const int lanes = CTA ? blockDim.x : 1 << shift;
-  const bool live = r < a.rows;  // a row's threads leave its work together
-  uint32_t outer = 0, head = 0;
-  if (live) {
-    outer = r;
-    if (a.inner > 1) outer = r / static_cast<uint32_t>(a.inner), head = r - outer * a.inner;
-  }
-  const int64_t in_row = static_cast<int64_t>(head) * a.width + l * VEC;
-  const int n = live ? a.width - l * VEC : 0;  // values from this thread's first on
+  const uint32_t per = CTA ? 1 : kRowThreads >> shift;  // rows of a block at a time
   const int step = lanes * VEC;
-  const moe_bf16 *x = a.x + outer * a.x_ld + in_row;
+  const int n = a.width - l * VEC;  // values from this thread's first on
   const bool element = a.gate_kind == MOE_GATE_ELEMENT;
-  const moe_bf16 *gate = nullptr;
-  if (element) gate = a.gate + outer * a.gate_ld + in_row;
-  if (a.gate_kind == MOE_GATE_CHANNEL) gate = a.gate + l * VEC;
-  const moe_bf16 *resid = a.resid_in ? a.resid_in + outer * a.resid_in_ld + in_row : nullptr;
-  W xw[NV], zw[NV] = {}, rw[NV] = {};
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = i * step;
-    if (c < n) {
-      xw[i] = *reinterpret_cast<const W *>(x + c);
-      if (gate) zw[i] = *reinterpret_cast<const W *>(gate + c);
-      if (resid) rw[i] = *reinterpret_cast<const W *>(resid + c);
+
+  constexpr int kP = (VEC + 1) / 2;  // pairs of a group
+  struct Row {
+    uint32_t outer, in_row;
+    W x[NV], z[NV], r[NV];
+    float factor;
+  };
+  // where a tensor's row lies (strides are below 2^32)
+  const auto at = [&](const Row &w, int64_t ld) {
+    return static_cast<uint64_t>(w.outer) * static_cast<uint32_t>(ld) + w.in_row;
+  };
+  const auto fetch = [&](Row &w, uint32_t r, bool live) {
+    uint32_t outer = live ? r : 0, head = 0;
+    if (a.inner > 1) {
+      const uint32_t whole = outer / static_cast<uint32_t>(a.inner);
+      head = outer - whole * a.inner, outer = whole;
     }
-  }
-  float factor = a.res_scale;
-  if (a.gate_kind == MOE_GATE_ROW && live)
-    factor *= act(bf16_to_f32(a.gate[outer * a.gate_ld + head]), a.gate_act);
-  float y[NV][VEC];
-  float ss = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (i * step < n) {
-      unpack(xw[i], y[i]);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) ss = fmaf(y[i][j], y[i][j], ss);
+    w.outer = outer;
+    w.in_row = head * static_cast<uint32_t>(a.width) + l * VEC;
+    w.factor = a.res_scale;
+    if (a.gate_kind == MOE_GATE_ROW && live) {
+      float2 z[1] = {make_float2(bf16_to_f32(a.gate[outer * a.gate_ld + head]), 0.0f)};
+      activate(z, a.gate_act);
+      w.factor *= z[0].x;
     }
-  }
-  float inv = 1.0f;
-  if (a.gamma_post) inv = 1.0f / sqrtf(row_sum<CTA>(ss, lanes, tmp[0]) / a.width + a.eps);
-  ss = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = i * step;
-    if (c < n) {
-      float w[VEC];
-      if (a.gamma_post) {
-        unpack(*reinterpret_cast<const W *>(a.gamma_post + l * VEC + c), w);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) y[i][j] *= inv * w[j];
-      }
-      if (gate) {
-        unpack(zw[i], w);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) y[i][j] *= act(w[j], a.gate_act);
-      }
-      unpack(rw[i], w);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) y[i][j] = resid ? fmaf(factor, y[i][j], w[j]) : factor * y[i][j];
-      // one rounding to bf16; the next norm reads the rounded residual
-      const W out = pack(y[i]);
-      if (a.resid_out) *reinterpret_cast<W *>(a.resid_out + outer * a.resid_out_ld + in_row + c) = out;
-      unpack(out, y[i]);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) ss = fmaf(y[i][j], y[i][j], ss);
-    }
-  }
-  if (a.x_next) {
-    inv = 1.0f / sqrtf(row_sum<CTA>(ss, lanes, tmp[1]) / a.width + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = i * step;
-      if (c < n) {
-        float w[VEC];
-        unpack(*reinterpret_cast<const W *>(a.gamma_pre + l * VEC + c), w);
+      w.x[i] = w.z[i] = w.r[i] = W{};
+      if (live && c < n) {  // a row's threads leave its work together
+        w.x[i] = *reinterpret_cast<const W *>(a.x + at(w, a.x_ld) + c);
+        if (element) w.z[i] = *reinterpret_cast<const W *>(a.gate + at(w, a.gate_ld) + c);
+        if (a.resid_in) w.r[i] = *reinterpret_cast<const W *>(a.resid_in + at(w, a.resid_in_ld) + c);
+      }
+    }
+  };
+  // a channel's factors: the same for every row
+  const auto channel = [&](const moe_bf16 *p, int i) {
+    W w{};
+    if (p && i * step < n) w = *reinterpret_cast<const W *>(p + l * VEC + i * step);
+    return w;
+  };
+  const bool by_channel = a.gate_kind == MOE_GATE_CHANNEL;
+  W post[NV], pre[NV], gate[NV];
+  constexpr bool kKeep = NV == 1;
+  if constexpr (kKeep) {
+    post[0] = channel(a.gamma_post, 0), pre[0] = channel(a.gamma_pre, 0);
+    gate[0] = channel(by_channel ? a.gate : nullptr, 0);
+  }
+  const float mean = 1.0f / static_cast<float>(a.width);
+
+  const uint32_t rows = static_cast<uint32_t>(a.rows), stride = gridDim.x * per;
+  // whole blocks go on together (the sums are formed by all their threads)
+  uint32_t first = blockIdx.x * per;
+  const uint32_t mine = CTA ? 0 : threadIdx.x >> shift;
+  Row row;
+  if (kKeep) fetch(row, first + mine, first + mine < rows);
+  for (int turn = 0; first < rows; turn ^= 1) {
+    if (!kKeep) fetch(row, first + mine, first + mine < rows);
+    const Row cur = row;
+    const int left = first + mine < rows ? n : 0;
+    // (row counts and strides stay below 2^31, so this sum does not wrap)
+    first += stride;
+    if (kKeep && first < rows) fetch(row, first + mine, first + mine < rows);
+    float2 y[NV][kP], ss = both(0.0f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) w[j] = y[i][j] * inv * w[j];
-        *reinterpret_cast<W *>(a.x_next + outer * a.x_next_ld + in_row + c) = pack(w);
+    for (int i = 0; i < NV; ++i) {
+      unpack(cur.x[i], y[i]);
+#pragma unroll
+      for (int j = 0; j < kP; ++j) ss = fma2(y[i][j], y[i][j], ss);
+    }
+    float inv = 1.0f;
+    if (a.gamma_post) inv = rsqrtf(fmaf(row_sum<CTA>(ss.x + ss.y, lanes, tmp[turn][0]), mean, a.eps));
+    ss = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * step;
+      if (c < left) {
+        float2 w[kP];
+        if (a.gamma_post) {
+          if constexpr (!kKeep) post[i] = channel(a.gamma_post, i);
+          unpack(post[i], w);
+#pragma unroll
+          for (int j = 0; j < kP; ++j) y[i][j] = mul2(y[i][j], mul2(w[j], both(inv)));
+        }
+        if (element || by_channel) {
+          if constexpr (!kKeep) gate[i] = channel(by_channel ? a.gate : nullptr, i);
+          unpack(element ? cur.z[i] : gate[i], w);
+          activate(w, a.gate_act);
+#pragma unroll
+          for (int j = 0; j < kP; ++j) y[i][j] = mul2(y[i][j], w[j]);
+        }
+        if (a.resid_in) {
+          unpack(cur.r[i], w);
+#pragma unroll
+          for (int j = 0; j < kP; ++j) y[i][j] = fma2(both(cur.factor), y[i][j], w[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kP; ++j) y[i][j] = mul2(both(cur.factor), y[i][j]);
+        }
+        // one rounding to bf16; the next norm reads the rounded residual
+        W out;
+        pack(y[i], out);
+        if (a.resid_out) *reinterpret_cast<W *>(a.resid_out + at(cur, a.resid_out_ld) + c) = out;
+        unpack(out, y[i]);
+#pragma unroll
+        for (int j = 0; j < kP; ++j) ss = fma2(y[i][j], y[i][j], ss);
+      }
+    }
+    if (a.x_next) {
+      inv = rsqrtf(fmaf(row_sum<CTA>(ss.x + ss.y, lanes, tmp[turn][1]), mean, a.eps));
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = i * step;
+        if (c < left) {
+          float2 w[kP];
+          if constexpr (!kKeep) pre[i] = channel(a.gamma_pre, i);
+          unpack(pre[i], w);
+#pragma unroll
+          for (int j = 0; j < kP; ++j) w[j] = mul2(y[i][j], mul2(w[j], both(inv)));
+          W out;
+          pack(w, out);
+          *reinterpret_cast<W *>(a.x_next + at(cur, a.x_next_ld) + c) = out;
+        }
       }
     }
   }
 }
 
-template <int VEC, int NV, bool CTA>
+template <int VEC, int NV, bool CTA, int MOST>
 cudaError_t launch(const moe_norm_args &a, int threads, int shift, cudaStream_t s) {
-  const int64_t per = CTA ? 1 : threads >> shift;  // rows of a block
-  norm_gate_kernel<VEC, NV, CTA>
-      <<<static_cast<unsigned>((a.rows + per - 1) / per), threads, 0, s>>>(a, shift);
+  const int64_t per = CTA ? 1 : threads >> shift;  // rows of a block at a time
+  const int64_t most = static_cast<int64_t>(tc_sm_count()) * (kSmThreads<VEC, NV, MOST> / threads);
+  const int64_t blocks = (a.rows + per - 1) / per;
+  norm_gate_kernel<VEC, NV, CTA, MOST>
+      <<<static_cast<unsigned>(blocks < most ? blocks : most), threads, 0, s>>>(a, shift);
   return cudaGetLastError();
 }
 
@@ -187,19 +264,31 @@ cudaError_t route(const moe_norm_args &a, cudaStream_t s) {
   if (groups <= 32) {
     int shift = 0;
     while ((1 << shift) < groups) ++shift;
-    return launch<VEC, 1, false>(a, kRowThreads, shift, s);
+    return launch<VEC, 1, false, kRowThreads>(a, kRowThreads, shift, s);
   }
-  if (groups <= 1024) return launch<VEC, 1, true>(a, (groups + 31) / 32 * 32, 0, s);
-  if (groups <= 2048) return launch<VEC, 2, true>(a, ((groups + 1) / 2 + 31) / 32 * 32, 0, s);
+  if (groups <= 256) return launch<VEC, 1, true, 256>(a, (groups + 31) / 32 * 32, 0, s);
+  if (groups <= 1024) return launch<VEC, 1, true, 1024>(a, (groups + 31) / 32 * 32, 0, s);
+  if (groups <= 2048) return launch<VEC, 2, true, 1024>(a, ((groups + 1) / 2 + 31) / 32 * 32, 0, s);
   if constexpr (VEC <= 2)
-    if (groups <= 8192) return launch<VEC, 8, true>(a, 1024, 0, s);
-  if constexpr (VEC == 1) return launch<VEC, 16, true>(a, 1024, 0, s);
+    if (groups <= 8192) return launch<VEC, 8, true, 1024>(a, 1024, 0, s);
+  if constexpr (VEC == 1) return launch<VEC, 16, true, 1024>(a, 1024, 0, s);
   return cudaErrorInvalidValue;  // not reached: width <= 16384
 }
 
 }  // namespace
 
-cudaError_t launch_norm_gate_residual(const moe_norm_args &a, int vec, cudaStream_t s) {
+cudaError_t launch_norm_gate_residual(const moe_norm_args &args, int vec, cudaStream_t s) {
+  moe_norm_args a = args;
+  // heads of whole rows one after another are plain rows
+  const int64_t w = int64_t(a.inner) * a.width;
+  if (a.inner > 1 && a.x_ld == w && (!a.resid_in || a.resid_in_ld == w) &&
+      (!a.resid_out || a.resid_out_ld == w) && (!a.x_next || a.x_next_ld == w) &&
+      (a.gate_kind != MOE_GATE_ELEMENT || a.gate_ld == w) &&
+      (a.gate_kind != MOE_GATE_ROW || a.gate_ld == a.inner)) {
+    a.inner = 1;
+    a.x_ld = a.resid_in_ld = a.resid_out_ld = a.x_next_ld = a.width;
+    a.gate_ld = a.gate_kind == MOE_GATE_ROW ? 1 : a.width;
+  }
   return vec == 8 ? route<8>(a, s) : vec == 2 ? route<2>(a, s) : route<1>(a, s);
 }
 
