@@ -33,6 +33,7 @@
 #include "common.cuh"
 #include "delta_mma.cuh"
 #include "delta_seq.cuh"
+#include "early.cuh"
 #include "kernels.h"
 #include "mixer.h"
 
@@ -164,6 +165,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
   const int ratio = d.v_heads / d.qk_heads;
   const int slot = blockIdx.x, h0 = blockIdx.y * heads, hk = h0 / ratio;
 
+  early_begin();
   if (slot == 0 && h0 == 0) {
     // one CTA looks at every bound: a call with a bad one does nothing
     bool bad = false;
@@ -630,6 +632,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   const int tile = blockIdx.x % tiles;
   const int h = (blockIdx.x / tiles) % d.v_heads;
   const int b = blockIdx.x / tiles / d.v_heads;
+  early_begin();
   if (reinterpret_cast<const uint32_t *>(ws)[kFlagWord]) return;
   const DeltaSeqRange r = delta_seq_range(seq, b);
   if (!r.ok) return;
@@ -1125,9 +1128,9 @@ cudaError_t launch_chain(const moe_delta_dims &d, const moe_delta_inputs &in, co
   cudaError_t e = allow_smem(delta_chain_kernel<DK, WARPS, GROUPS>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   const int64_t grid = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / (16 * GROUPS));
-  delta_chain_kernel<DK, WARPS, GROUPS><<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, s>>>(
-      d, in, seq, ws, ws_key, ws_head, out, out_ld, tc_wait_budget_ns());
-  return cudaGetLastError();
+  return launch_early(delta_chain_kernel<DK, WARPS, GROUPS>, dim3(static_cast<unsigned>(grid)),
+                      C::kThreads, C::kSmem, s, d, in, seq, ws, ws_key, ws_head, out, out_ld,
+                      tc_wait_budget_ns());
 }
 
 // Chunks times key heads from which a CTA of the first kernel serves several of
@@ -1150,8 +1153,9 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
     for (int n = 2; n <= kPrepHeads; ++n)
       if (ratio % n == 0) heads = n;
   const dim3 grid(static_cast<unsigned>(slots), d.v_heads / heads);
-  delta_prep_kernel<DK><<<grid, kPrepThreads, kSmem, s>>>(d, in, seq, heads, ws, ws_key, ws_head);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_early(delta_prep_kernel<DK>, grid, kPrepThreads, kSmem, s, d, in, seq, heads, ws,
+                   ws_key, ws_head);
+  if (e != cudaSuccess) return e;
   return launch_chain<DK, 2, 2>(d, in, seq, ws, ws_key, ws_head, out, out_ld, s);
 }
 

@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "delta_seq.cuh"
+#include "early.cuh"
 #include "mixer.h"
 
 namespace moe {
@@ -87,6 +88,7 @@ delta_recurrent_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, moe
   const int64_t b64 = bh / d.v_heads;
   if (b64 >= seq.B) return;
   const int b = static_cast<int>(b64);
+  early_begin();
   const DeltaSeqRange r = delta_seq_range(seq, b);
   if (!r.ok) return;
   const int hk = h / (d.v_heads / d.qk_heads);
@@ -165,11 +167,8 @@ cudaError_t launch_delta_recurrent(const moe_delta_dims &d, const moe_delta_inpu
                                    cudaStream_t s) {
   const int64_t units = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / kRows);
   const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
-  if (d.qk_dim == 128)
-    delta_recurrent_kernel<128><<<grid, 32 * kWarps, 0, s>>>(d, in, seq, out, out_ld);
-  else
-    delta_recurrent_kernel<64><<<grid, 32 * kWarps, 0, s>>>(d, in, seq, out, out_ld);
-  return cudaGetLastError();
+  return launch_early(d.qk_dim == 128 ? delta_recurrent_kernel<128> : delta_recurrent_kernel<64>,
+                      dim3(grid), 32 * kWarps, 0, s, d, in, seq, out, out_ld);
 }
 
 }  // namespace moe

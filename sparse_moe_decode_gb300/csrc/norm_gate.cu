@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "early.cuh"
 #include "kernels.h"
 #include "mixer.h"
 #include "pair.cuh"
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(MOST)
 norm_gate_kernel(moe_norm_args a, int shift) {
   using W = typename Bits<VEC>::T;
   __shared__ float tmp[2][2][32];
+  early_begin();
   const int l = CTA ? threadIdx.x : threadIdx.x & ((1 << shift) - 1);
   const int lanes = CTA ? blockDim.x : 1 << shift;
   const uint32_t per = CTA ? 1 : kRowThreads >> shift;  // rows of a block at a time
@@ -251,9 +253,9 @@ cudaError_t launch(const moe_norm_args &a, int threads, int shift, cudaStream_t 
   const int64_t per = CTA ? 1 : threads >> shift;  // rows of a block at a time
   const int64_t most = static_cast<int64_t>(tc_sm_count()) * (kSmThreads<VEC, NV, MOST> / threads);
   const int64_t blocks = (a.rows + per - 1) / per;
-  norm_gate_kernel<VEC, NV, CTA, MOST>
-      <<<static_cast<unsigned>(blocks < most ? blocks : most), threads, 0, s>>>(a, shift);
-  return cudaGetLastError();
+  return launch_early(norm_gate_kernel<VEC, NV, CTA, MOST>,
+                      dim3(static_cast<unsigned>(blocks < most ? blocks : most)), threads, 0, s, a,
+                      shift);
 }
 
 // Up to 32 groups of VEC values: part of a warp per row; more: a block per
