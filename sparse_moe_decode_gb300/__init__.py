@@ -20,7 +20,7 @@ There is no CPU fallback: if the library is missing, ``lib()`` raises.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib
 import os
 import threading
 
@@ -372,22 +372,34 @@ class MoEBlock:
         moe_clear_status(self.workspace, stream)
 
 
-def _invalid(where):
-    raise MoEError(MOE_ERR_INVALID_ARG, where)
+def _refuse(status, where):
+    raise MoEError(status, where)
 
 
+_binding = None
 _raw_stream = None
+
+
+def _tensor_calls():
+    """The extension module of the tensor-level calls (raises if it is not built)."""
+    global _binding, _raw_stream
+    if _binding is None:
+        import torch
+        L = lib()
+        if not os.path.exists(os.path.join(_PKG, "_binding.so")):
+            raise RuntimeError("_binding.so is not built; run `python -c \"import "
+                               "__graft_entry__ as g; g.build()\"`")
+        module = importlib.import_module("._binding", __name__)
+        module.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "moe_delta_chunk", "moe_delta_step", "moe_norm_gate_residual")))
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+        _binding = module
+    return _binding
 
 
 def _stream_of(stream, device_index):
     """The given stream, or the current one of the tensors' device."""
-    global _raw_stream
-    if stream is not None:
-        return _s(stream)
-    if _raw_stream is None:
-        import torch
-        _raw_stream = torch._C._cuda_getCurrentRawStream
-    return _raw_stream(device_index)
+    return _raw_stream(device_index) if stream is None else _s(stream)
 
 
 class GatedDelta:
@@ -413,146 +425,33 @@ class GatedDelta:
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         self.workspace[:256].zero_()
         self._index = self.workspace.get_device()
-        self._new = functools.partial(torch.empty, dtype=torch.bfloat16,
-                                      device=self.workspace.device)
-        self._ws = self.workspace.data_ptr()
-        self._dims_ref = ctypes.byref(self.dims)
-        self._chunk_fn, self._step_fn = lib().moe_delta_chunk, lib().moe_delta_step
-        self._heads = (qk_heads, v_heads, qk_dim, v_dim)
-        self._state_shape = (v_heads, v_dim, qk_dim)
-        self._types = (torch.bfloat16, torch.float32, torch.int32)
-
-    def _inputs(self, n, q, k, v, g, beta, where):
-        """The call's moe_delta_inputs.  q, k, v: [n][heads][dim], g, beta: [n][v_heads]."""
-        hk, hv, dk, dv = self._heads
-        bf16, f32, _ = self._types
-        index = self._index
-        try:
-            ql, q1, q2 = q.stride()
-            kl, k1, k2 = k.stride()
-            vl, v1, v2 = v.stride()
-            gl, g1 = g.stride()
-            bl, b1 = beta.stride()
-        except ValueError:  # another number of dimensions
-            _invalid(where)
-        if (index < 0 or q.shape != (n, hk, dk) or k.shape != (n, hk, dk) or
-                v.shape != (n, hv, dv) or g.shape != (n, hv) or beta.shape != (n, hv) or
-                q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16 or
-                g.dtype is not f32 or beta.dtype is not f32 or q.get_device() != index or
-                k.get_device() != index or v.get_device() != index or g.get_device() != index or
-                beta.get_device() != index):
-            _invalid(where)
-        if (not (q1 == k1 == dk and v1 == dv and q2 == k2 == v2 == g1 == b1 == 1) and n and
-                not all(x[0].is_contiguous() for x in (q, k, v, g, beta))):
-            _invalid(where)
-        if n < 2:  # a single row has no stride of its own
-            ql = kl = hk * dk
-            vl, gl, bl = hv * dv, hv, hv
-        return DeltaInputs(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                           beta.data_ptr(), ql, kl, vl, gl, bl)
-
-    def _states(self, B, state_in, state_out, slots, where):
-        """The addresses of slots, state_in and state_out and the number of slots."""
-        p_in = p_out = p_slots = None
-        n_slots = B
-        if state_in is not None:
-            n_slots, p_in = state_in.shape[0], self._state(state_in, where)
-        if state_out is not None:
-            if state_in is not None and state_out.shape[0] != n_slots:
-                _invalid(where)
-            n_slots, p_out = state_out.shape[0], self._state(state_out, where)
-        if slots is not None:
-            if (slots.dtype is not self._types[2] or slots.get_device() != self._index or
-                    slots.shape != (B,) or not slots.is_contiguous()):
-                _invalid(where)
-            p_slots = slots.data_ptr()
-            if p_in is None and p_out is None:
-                n_slots = 1 << 30  # no state to be out of
-        return p_slots, n_slots, p_in, p_out
-
-    def _state(self, x, where):
-        if (x.dtype is not self._types[1] or x.get_device() != self._index or
-                x.shape[1:] != self._state_shape or not x.is_contiguous()):
-            _invalid(where)
-        return x.data_ptr()
-
-    def _output(self, n, out, where):
-        """The output tensor and its row stride."""
-        _, hv, _, dv = self._heads
-        if out is None:
-            return self._new((n, hv, dv)), hv * dv
-        if (out.dtype is not self._types[0] or out.get_device() != self._index or
-                out.shape != (n, hv, dv) or (n and not out[0].is_contiguous())):
-            _invalid(where)
-        return out, out.stride(0) if n > 1 else hv * dv
+        calls = _tensor_calls()
+        self._chunk, self._step = calls.delta_chunk, calls.delta_step
+        self._handle = calls.delta(ctypes.addressof(self.dims), self.workspace.data_ptr(),
+                                   self.ws_bytes, self._index)
 
     def chunk(self, q, k, v, g, beta, cu_seqlens=None, state_in=None, state_out=None, slots=None,
               out=None, stream=None):
         """Whole prompts: the rows of len(cu_seqlens) - 1 sequences one after
         another (one sequence without ``cu_seqlens``).  Returns out [N][v_heads][v_dim]."""
-        where = "GatedDelta.chunk"
-        n = q.shape[0]
-        inputs = self._inputs(n, q, k, v, g, beta, where)
-        B, cu = 1, None
-        if cu_seqlens is not None:
-            if (cu_seqlens.dtype is not self._types[2] or cu_seqlens.get_device() != self._index or
-                    cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or
-                    not cu_seqlens.is_contiguous()):
-                _invalid(where)
-            B, cu = cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr()
-        p_slots, n_slots, p_in, p_out = self._states(B, state_in, state_out, slots, where)
-        out, out_ld = self._output(n, out, where)
-        st = self._chunk_fn(self._dims_ref, ctypes.byref(inputs), n, cu, B, p_slots, n_slots, p_in,
-                            p_out, out.data_ptr(), out_ld, self._ws, self.ws_bytes,
-                            _stream_of(stream, self._index))
-        if st:
-            raise MoEError(st, where)
-        return out
+        r = self._chunk(self._handle, q, k, v, g, beta, state_in, state_out, slots, out,
+                        cu_seqlens, _stream_of(stream, self._index) if self._index >= 0 else 0)
+        return r if type(r) is not int else _refuse(r, "GatedDelta.chunk")
 
     def step(self, q, k, v, g, beta, state_in=None, state_out=None, slots=None, tokens=None,
              out=None, stream=None):
         """Decode and verification: ``tokens`` consecutive rows for each
         sequence (by default as many as make ``slots``, or else the states,
         one per sequence).  Returns out [rows][v_heads][v_dim]."""
-        where = "GatedDelta.step"
-        n = q.shape[0]
-        inputs = self._inputs(n, q, k, v, g, beta, where)
-        if tokens is None:
-            lead = slots if slots is not None else state_in if state_in is not None else state_out
-            B = n if lead is None else lead.shape[0]
-            tokens = n // B if B else 0
-        else:
-            B = n // tokens if tokens > 0 else 0
-        if B * tokens != n:
-            _invalid(where)
-        p_slots, n_slots, p_in, p_out = self._states(B, state_in, state_out, slots, where)
-        out, out_ld = self._output(n, out, where)
-        st = self._step_fn(self._dims_ref, ctypes.byref(inputs), B, tokens, p_slots, n_slots, p_in,
-                           p_out, out.data_ptr(), out_ld, self._ws, self.ws_bytes,
-                           _stream_of(stream, self._index))
-        if st:
-            raise MoEError(st, where)
-        return out
+        r = self._step(self._handle, q, k, v, g, beta, state_in, state_out, slots, out, tokens,
+                       _stream_of(stream, self._index) if self._index >= 0 else 0)
+        return r if type(r) is not int else _refuse(r, "GatedDelta.step")
 
     def status(self, stream=None) -> int:
         return moe_read_status(self.workspace, stream)
 
     def clear_status(self, stream=None):
         moe_clear_status(self.workspace, stream)
-
-
-def _norm_ld(t, shape, bf16, index, where):
-    """The first stride of a bf16 tensor of this shape, whose rows are whole."""
-    if t.dtype is not bf16 or t.get_device() != index or t.shape != shape:
-        _invalid(where)
-    if t.is_contiguous():
-        return shape[-1] * (shape[1] if len(shape) == 3 else 1)
-    if len(shape) == 1 or shape[0] < 2 or not t[0].is_contiguous():
-        _invalid(where)
-    return t.stride(0)
-
-
-_norm_fn = None
 
 
 def norm_gate_residual(x, gamma_post=None, gate=None, gate_act="sigmoid", resid=None,
@@ -565,56 +464,10 @@ def norm_gate_residual(x, gamma_post=None, gate=None, gate_act="sigmoid", resid=
     channel), shaped like ``x``, or [.., 1] (per row).  Returns (resid_out,
     x_next), x_next None without ``gamma_pre``; x is not changed unless it is
     given as an output."""
-    global _norm_fn
-    where = "norm_gate_residual"
-    if _norm_fn is None:
-        import torch
-        _norm_fn = (lib().moe_norm_gate_residual, torch.bfloat16, torch.empty)
-    fn, bf16, empty = _norm_fn
-    index, shape = x.get_device(), x.shape
-    act = GATE_ACTS.get(gate_act)
-    if act is None or index < 0 or len(shape) not in (2, 3) or 0 in shape[1:]:
-        _invalid(where)
-    width = shape[-1]
-    inner = shape[1] if len(shape) == 3 else 1
-    per_channel = (width,)
-    p_post = p_pre = p_gate = p_resid = p_next = None
-    kind = gate_ld = resid_ld = next_ld = 0
-    x_ld = _norm_ld(x, shape, bf16, index, where)
-    if gamma_post is not None:
-        _norm_ld(gamma_post, per_channel, bf16, index, where)
-        p_post = gamma_post.data_ptr()
-    if gate is not None:
-        p_gate = gate.data_ptr()
-        if gate.shape == per_channel:
-            kind = GATE_CHANNEL
-            _norm_ld(gate, per_channel, bf16, index, where)
-        elif gate.shape == shape:
-            kind, gate_ld = GATE_ELEMENT, _norm_ld(gate, shape, bf16, index, where)
-        else:
-            kind, gate_ld = GATE_ROW, _norm_ld(gate, shape[:-1] + (1,), bf16, index, where)
-    if resid is not None:
-        p_resid, resid_ld = resid.data_ptr(), _norm_ld(resid, shape, bf16, index, where)
-    if resid_out is None:
-        resid_out = empty(shape, dtype=bf16, device=x.device)
-        out_ld = inner * width
-    else:
-        out_ld = _norm_ld(resid_out, shape, bf16, index, where)
-    if gamma_pre is not None:
-        _norm_ld(gamma_pre, per_channel, bf16, index, where)
-        p_pre = gamma_pre.data_ptr()
-        if x_next is None:
-            x_next = empty(shape, dtype=bf16, device=x.device)
-            next_ld = inner * width
-        else:
-            next_ld = _norm_ld(x_next, shape, bf16, index, where)
-        p_next = x_next.data_ptr()
-    elif x_next is not None:
-        _invalid(where)
-    a = NormArgs(shape[0] * inner, width, inner, x.data_ptr(), p_post, p_gate, p_resid, p_pre,
-                 resid_out.data_ptr(), p_next, x_ld, gate_ld, resid_ld, out_ld, next_ld, kind, act,
-                 res_scale, eps)
-    st = fn(ctypes.byref(a), _stream_of(stream, index))
-    if st:
-        raise MoEError(st, where)
-    return resid_out, x_next
+    act, index = GATE_ACTS.get(gate_act), x.get_device()
+    if act is None or index < 0:
+        _refuse(MOE_ERR_INVALID_ARG, "norm_gate_residual")
+    calls = _binding or _tensor_calls()
+    r = calls.norm(x, gamma_post, gate, act, resid, res_scale, gamma_pre, eps, resid_out, x_next,
+                   _stream_of(stream, index))
+    return r if type(r) is not int else _refuse(r, "norm_gate_residual")

@@ -1,8 +1,9 @@
 """Build libmoe_gb300.so for sm_103a with nvcc (in-tree, no torch extension).
 
 Each .cu is compiled to an object in parallel, then linked into a shared
-library next to this file.  Rebuilds only when a source or header is newer
-than the library.
+library next to this file; beside it the extension module ``_binding`` (the
+tensor-level calls) is compiled with g++ against the installed torch.  Each is
+rebuilt only when a source or header is newer.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Werror=implicit-fallthrough", "-Xcompiler", "-Wall",
@@ -49,9 +53,35 @@ def stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and not stale():
-        return LIB
-    return _build(BUILD, LIB, [], verbose, ptxas_info)
+    with concurrent.futures.ThreadPoolExecutor(1) as ex:
+        binding = ex.submit(build_binding, force)
+        if force or stale():
+            _build(BUILD, LIB, [], verbose, ptxas_info)
+        binding.result()
+    return LIB
+
+
+def build_binding(force: bool = False) -> str:
+    """The extension module of the tensor-level calls, against this torch."""
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "moe_gb300.h"), os.path.abspath(__file__)]
+    if (not force and os.path.exists(BINDING) and
+            all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps)):
+        return BINDING
+    import torch
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    tmp = BINDING + ".%d.tmp" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", INCLUDE, "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           BINDING_SRC, "-o", tmp, "-L", os.path.join(home, "lib"),
+           "-Wl,-rpath," + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on %s:\n%s%s" % (BINDING_SRC, r.stdout, r.stderr))
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build_variant(name: str, defines: dict) -> str:
