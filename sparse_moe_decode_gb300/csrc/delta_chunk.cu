@@ -88,13 +88,16 @@ __device__ __forceinline__ int slot_base(const DeltaSeqs &s, int b) {
 
 // ------------------------------------------------------------------- prep
 
-constexpr int kTLd = kC + 4;     // row stride of T
+constexpr int kTLd = kC + 4;     // row stride of L and T
 constexpr int kPrepHeads = 4;    // value heads of one CTA at most
 
 template <int DK>
 struct PrepSmem {
-  alignas(128) uint8_t key[kKeyBlob<DK>];
-  // L (fp32) until T's two terms replace it; P; the vectors
+  // k and q until their products are formed; then L
+  union {
+    alignas(128) uint8_t key[kKeyBlob<DK>];
+    float l[kC * kTLd];
+  };
   alignas(128) uint8_t head[kHeadBlob];
   float t[kC * kTLd];  // T; blocks of 16 above the diagonal are never touched
   // the tokens' factors; per head the sums of g in units of log 2 (two terms)
@@ -104,12 +107,6 @@ struct PrepSmem {
   // kappa_j e^{G_r - G_j} for the columns left of it, e^{G_i - G_r}
   float col[4][kC], row[kC];
 };
-
-// Where L(i, j) lies, in the same blocks: pieces of four columns permuted by
-// the row, so that eight rows' pieces of one column lie in different banks.
-__device__ __forceinline__ int l_at(int i, int j) {
-  return block_of(i >> 4, j >> 4) * 256 + (i & 15) * 16 + ((j & 15) ^ (((i >> 1) & 3) << 2));
-}
 
 // The power of two that brings a token's values below 2^15 (bounded by their
 // 2-norm), and its inverse: their bf16 digits are exact in fp16 down to 2^-25
@@ -121,34 +118,48 @@ __device__ __forceinline__ void token_scale(float ss, float &mult, float &inv) {
   inv = __uint_as_float(static_cast<uint32_t>(254 - m) << 23);
 }
 
-// A 16 x 8 tile (rows r0, columns c0) of A B over STEPS steps of eight from
-// k0: fp32 values as two tf32 terms each, three products.
-template <int STEPS, class FA, class FB>
-__device__ __forceinline__ void product(float (&acc)[4], int r0, int c0, int k0, FA a_of, FB b_of,
-                                        int lane) {
-  const int g = lane >> 2, t = lane & 3;
-  float a[STEPS][4], b[STEPS][2];
-#pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    const int k = k0 + 8 * s;
-    a[s][0] = a_of(r0 + g, k + t), a[s][1] = a_of(r0 + g + 8, k + t);
-    a[s][2] = a_of(r0 + g, k + t + 4), a[s][3] = a_of(r0 + g + 8, k + t + 4);
-    b[s][0] = b_of(k + t, c0 + g), b[s][1] = b_of(k + t + 4, c0 + g);
-  }
+// A 16 x 8 tile of A B over `pairs` pairs of k8 steps; a and b point at this
+// lane's elements (row g, column t of A's tile; row t, column g of B's).  fp32
+// values as two tf32 terms each, three products.
+__device__ __forceinline__ void product(float (&acc)[4], const float *a, const float *b,
+                                        int pairs) {
   float part[3][4] = {};
+#pragma unroll 1
+  for (; pairs > 0; --pairs, a += 16, b += 16 * kTLd) {
+    float x[2][4], y[2][2];
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    uint32_t ah[4], al[4], bh[2], bl[2];
+    for (int s = 0; s < 2; ++s) {
+      x[s][0] = a[8 * s], x[s][1] = a[8 * s + 8 * kTLd];
+      x[s][2] = a[8 * s + 4], x[s][3] = a[8 * s + 8 * kTLd + 4];
+      y[s][0] = b[8 * s * kTLd], y[s][1] = b[(8 * s + 4) * kTLd];
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split_tf32(a[s][i], ah[i], al[i]);
+    for (int s = 0; s < 2; ++s) {
+      uint32_t ah[4], al[4], bh[2], bl[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) split_tf32(b[s][i], bh[i], bl[i]);
-    mma8(part[0], ah, bl[0], bl[1]);
-    mma8(part[1], al, bh[0], bh[1]);
-    mma8(part[2], ah, bh[0], bh[1]);
+      for (int i = 0; i < 4; ++i) split_tf32(x[s][i], ah[i], al[i]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) split_tf32(y[s][i], bh[i], bl[i]);
+      mma8(part[0], ah, bl[0], bl[1]);
+      mma8(part[1], al, bh[0], bh[1]);
+      mma8(part[2], ah, bh[0], bh[1]);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i] = part[2][i] + (part[0][i] + part[1][i]);
+}
+
+// (hi, lo) += (h, l), pairs whose sum is the value: no digit of the larger
+// terms is lost.
+__device__ __forceinline__ void add_exact(float &hi, float &lo, float h, float l) {
+  const float s = __fadd_rn(hi, h), t = __fsub_rn(s, hi);
+  const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(h, t));
+  hi = s, lo = __fadd_rn(__fadd_rn(lo, l), e);
+}
+
+// The largest of 32 values >= 0 (their bits order like the values).
+__device__ __forceinline__ float warp_max_pos(float v) {
+  return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(v)));
 }
 
 // One CTA per chunk and key head, for `heads` of the value heads that read
@@ -199,54 +210,62 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
   const int g = lane >> 2, t = lane & 3;
   const uint32_t kt = ptx::smem_u32(sm.key);
 
-  // k and q: scaled to fp16, and the tokens' factors.  Eight lanes a row.  While
-  // they come in, warp w sums head w's decays: in fp64, in units of log 2, kept
-  // as two fp32 terms, so that differences of large sums keep their digits.
+  // k and q come in as they are, each piece to the place of its fp16 form; eight
+  // lanes a row.  Meanwhile warp w sums head w's decays, in units of log 2 as
+  // two fp32 terms each, so that differences of large sums keep their digits.
   {
     constexpr int kPieces = DK / 64;  // 16-byte pieces of a lane
+    const int piece = lane & 7, row = 16 * w + (lane >> 3);
     const moe_bf16 *src = is_q ? in.q : in.k;
     const int64_t ld = is_q ? in.q_ld : in.k_ld;
-    const int piece = lane & 7;
-    float g0 = 0.0f, g1 = 0.0f, be0 = 0.0f, be1 = 0.0f;
-    if (warp < heads) {
-      const int64_t i = row0 + 2 * lane;
-      if (2 * lane < left) g0 = in.g[i * in.g_ld + h0 + warp], be0 = in.beta[i * in.beta_ld + h0 + warp];
-      if (2 * lane + 1 < left)
-        g1 = in.g[(i + 1) * in.g_ld + h0 + warp], be1 = in.beta[(i + 1) * in.beta_ld + h0 + warp];
-    }
-    uint4 raw[4][kPieces];
+    uint8_t *tile = sm.key + (is_q ? kKeyBlob<DK> / 2 : 0);
+    src += row0 * ld + hk * DK + piece * 8;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      const int i = 16 * w + 4 * p + (lane >> 3);
+      const int i = row + 4 * p;
 #pragma unroll
       for (int e = 0; e < kPieces; ++e)
-        raw[p][e] = i < left ? *reinterpret_cast<const uint4 *>(src + (row0 + i) * ld + hk * DK +
-                                                                (piece + 8 * e) * 8)
-                             : make_uint4(0, 0, 0, 0);
+        cp_async16(kt + (is_q ? kKeyBlob<DK> / 2 : 0) + tile_at<DK>(i, piece + 8 * e),
+                   src + (i < left ? i * ld : 0) + 64 * e, i < left);
     }
+    cp_async_commit();
     if (warp < heads) {
-      const double d1 = delta_log_decay(g1);
-      double sum = delta_log_decay(g0) + d1;
+      const int64_t i = row0 + 2 * lane;
+      float g0 = 0.0f, g1 = 0.0f, be0 = 0.0f, be1 = 0.0f;
+      if (2 * lane < left)
+        g0 = in.g[i * in.g_ld + h0 + warp], be0 = in.beta[i * in.beta_ld + h0 + warp];
+      if (2 * lane + 1 < left)
+        g1 = in.g[(i + 1) * in.g_ld + h0 + warp], be1 = in.beta[(i + 1) * in.beta_ld + h0 + warp];
+      g0 = delta_log_decay(g0), g1 = delta_log_decay(g1);
+      float hi1 = g0, lo1 = 0.0f;
+      add_exact(hi1, lo1, g1, 0.0f);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_up_sync(kFull, sum, o);
-        if (lane >= o) sum += up;
+        const float h = __shfl_up_sync(kFull, hi1, o), l = __shfl_up_sync(kFull, lo1, o);
+        if (lane >= o) add_exact(hi1, lo1, h, l);
       }
-      const double kLog2E = 1.4426950408889634;
-      const double second = sum * kLog2E, first = (sum - d1) * kLog2E;
-      const float2 hi2 = make_float2(static_cast<float>(first), static_cast<float>(second));
-      *reinterpret_cast<float2 *>(&sm.ghi[warp][2 * lane]) = hi2;
+      float hi0 = hi1, lo0 = lo1;  // without this lane's second token
+      add_exact(hi0, lo0, -g1, 0.0f);
+      // times log2 e, as two terms too
+      constexpr double kLog2E = 1.4426950408889634;
+      constexpr float kHi = static_cast<float>(kLog2E);
+      constexpr float kLo = static_cast<float>(kLog2E - static_cast<double>(kHi));
+      const float p0 = hi0 * kHi, p1 = hi1 * kHi;
+      *reinterpret_cast<float2 *>(&sm.ghi[warp][2 * lane]) = make_float2(p0, p1);
       *reinterpret_cast<float2 *>(&sm.glo[warp][2 * lane]) =
-          make_float2(static_cast<float>(first - hi2.x), static_cast<float>(second - hi2.y));
+          make_float2(fmaf(hi0, kHi, -p0) + fmaf(hi0, kLo, lo0 * kHi),
+                      fmaf(hi1, kHi, -p1) + fmaf(hi1, kLo, lo1 * kHi));
       *reinterpret_cast<float2 *>(&sm.beta[warp][2 * lane]) = make_float2(be0, be1);
     }
-#pragma unroll
+    cp_async_wait<0>();  // each lane converts what it brought in
+#pragma unroll 1
     for (int p = 0; p < 4; ++p) {
-      const int i = 16 * w + 4 * p + (lane >> 3);
+      const int i = row + 4 * p;
       float2 x[kPieces][4], sum = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int e = 0; e < kPieces; ++e) {
-        const uint32_t u[4] = {raw[p][e].x, raw[p][e].y, raw[p][e].z, raw[p][e].w};
+        const uint4 raw = *reinterpret_cast<const uint4 *>(tile + tile_at<DK>(i, piece + 8 * e));
+        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           x[e][j] = make_float2(bf16_lo(u[j]), bf16_hi(u[j]));
@@ -264,8 +283,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           o[j] = h2_bits(__float22half2_rn(mul2(x[e][j], make_float2(mult, mult))));
-        *reinterpret_cast<uint4 *>(sm.key + (is_q ? kKeyBlob<DK> / 2 : 0) +
-                                   tile_at<DK>(i, piece + 8 * e)) =
+        *reinterpret_cast<uint4 *>(tile + tile_at<DK>(i, piece + 8 * e)) =
             make_uint4(o[0], o[1], o[2], o[3]);
       }
       if (d.qk_norm) inv = inv / sqrtf(ss + d.qk_eps);
@@ -273,14 +291,19 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
       if (piece == 0) (is_q ? sm.rho : sm.kappa)[i] = i < left ? inv : 0.0f;
     }
   }
+  ptx::fence_proxy_async_smem();
   __syncthreads();
+  const bool keeps_key = tid == 0 && h0 % ratio == 0;
+  if (keeps_key)
+    bulk_store(ws_key + (static_cast<size_t>(slot) * d.qk_heads + hk) * kKeyBlob<DK>,
+               ptx::smem_u32(sm.key), kKeyBlob<DK>);
 
   // rows of k k^T or q k^T: the tiles left of the diagonal block, and its two
   float off[6][4] = {}, dia[2][4] = {};
   {
     const uint32_t at = kt + (is_q ? kKeyBlob<DK> / 2 : 0);
     const int b_row = (lane & 7) + ((lane >> 4) << 3), b_piece = (lane >> 3) & 1;
-#pragma unroll
+#pragma unroll 2
     for (int s = 0; s < DK / 16; ++s) {
       uint32_t a[4], bd[4], b[3][4];
       ldsm4(a, at + tile_at<DK>(16 * w + (lane & 15), 2 * s + (lane >> 4)));
@@ -301,8 +324,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
 
   float *vec = reinterpret_cast<float *>(sm.head + 2 * kTri);
   float *vec_b = reinterpret_cast<float *>(sm.head + kPartA + kTri);
-  float *L = reinterpret_cast<float *>(sm.head);
-  float *T = sm.t;
+  float *L = sm.l, *T = sm.t;
   for (int hh = 0; hh < heads; ++hh) {
     const int h = h0 + hh;
     const float *ghi = sm.ghi[hh], *glo = sm.glo[hh];
@@ -330,12 +352,8 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
       const float2 cc = make_float2(-be.x * gamma.x * kap.x, -be.y * gamma.y * kap.y);
       const float2 dd = make_float2(exp2f((th - sh.x) + (tl - sl.x)) * kap.x,
                                     exp2f((th - sh.y) + (tl - sl.y)) * kap.y);
-      float dmax = fmaxf(dd.x, dd.y), cmax = fmaxf(fabsf(cc.x), fabsf(cc.y));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        dmax = fmaxf(dmax, __shfl_xor_sync(kFull, dmax, o));
-        cmax = fmaxf(cmax, __shfl_xor_sync(kFull, cmax, o));
-      }
+      const float dmax = warp_max_pos(fmaxf(dd.x, dd.y));
+      const float cmax = warp_max_pos(fmaxf(fabsf(cc.x), fabsf(cc.y)));
       float up, down;
       pow2_above(dmax, up, down);
       *reinterpret_cast<float2 *>(vec + kVecBeta * kC + i) = be;
@@ -349,6 +367,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
         vec[kVecMisc * kC + kCMax] = cmax;
       }
     }
+    if (hh == 0 && keeps_key) bulk_store_wait(false);  // L takes k's and q's place
     __syncthreads();
 
     // L = beta_i kappa_i Gamma_ij kappa_j k_i.k_j below the diagonal, P =
@@ -368,9 +387,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
       // decays that grow by up to 2^5).
       float s0 = 1.0f, s1 = 1.0f;
       if (is_q) {
-        float kmax = fmaxf(sm.kappa[lane], sm.kappa[lane + 32]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) kmax = fmaxf(kmax, __shfl_xor_sync(kFull, kmax, o));
+        const float kmax = warp_max_pos(fmaxf(sm.kappa[lane], sm.kappa[lane + 32]));
         float up0, up1;
         pow2_above(fabsf(f0) * kmax, up0, s0);
         pow2_above(fabsf(f1) * kmax, up1, s1);
@@ -386,8 +403,8 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
           *reinterpret_cast<__half2 *>(P + tri_at(i0, col / 8)) = __float22half2_rn(top);
           *reinterpret_cast<__half2 *>(P + tri_at(i1, col / 8)) = __float22half2_rn(low);
         } else {
-          *reinterpret_cast<float2 *>(L + l_at(i0, col + 2 * t)) = top;
-          *reinterpret_cast<float2 *>(L + l_at(i1, col + 2 * t)) = low;
+          *reinterpret_cast<float2 *>(L + i0 * kTLd + col + 2 * t) = top;
+          *reinterpret_cast<float2 *>(L + i1 * kTLd + col + 2 * t) = low;
         }
       };
 #pragma unroll
@@ -424,7 +441,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
           float v = i == c ? 1.0f : 0.0f;
 #pragma unroll
           for (int j = 0; j < i; j += 4) {
-            const float4 l = *reinterpret_cast<const float4 *>(L + l_at(ref + i, ref + j));
+            const float4 l = *reinterpret_cast<const float4 *>(L + (ref + i) * kTLd + ref + j);
             v = fmaf(-l.x, x[j], v);
             if (j + 1 < i) v = fmaf(-l.y, x[j + 1], v);
             if (j + 2 < i) v = fmaf(-l.z, x[j + 2], v);
@@ -439,42 +456,34 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
     }
     __syncthreads();
 
-    // [A 0; B C]^-1 = [A^-1 0; -C^-1 B A^-1 C^-1] for blocks of 16, then 32.
-    // B A^-1 waits in the block's own place.
-    const auto l_of = [&](int i, int j) { return L[l_at(i, j)]; };
-    const auto t_of = [&](int i, int j) { return T[i * kTLd + j]; };
-    const auto put = [&](const float(&acc)[4], int r0, int c0, float sign) {
-      float *p = T + (r0 + g) * kTLd + c0 + 2 * t;
-      *reinterpret_cast<float2 *>(p) = make_float2(sign * acc[0], sign * acc[1]);
-      *reinterpret_cast<float2 *>(p + 8 * kTLd) = make_float2(sign * acc[2], sign * acc[3]);
-    };
-    float acc[4];
-    if (warp < 4) {
-      // a warp's eight columns of B A^-1 are all that it reads of it
-      const int o = 32 * (warp >> 1), c0 = o + 8 * (warp & 1);
-      product<2>(acc, o + 16, c0, o, l_of, t_of, lane);
-      put(acc, o + 16, c0, 1.0f);
-      __syncwarp();
-      product<2>(acc, o + 16, c0, o + 16, t_of, t_of, lane);
-      __syncwarp();
-      put(acc, o + 16, c0, -1.0f);
-    }
-    __syncthreads();
-    {
-      const int r0 = 32 + 16 * (warp >> 2), c0 = 8 * (warp & 3);
-      // T(k, c) = 0 for k < c, and its blocks above the diagonal do not exist
-      if ((warp & 3) < 2) product<4>(acc, r0, c0, 0, l_of, t_of, lane);
-      else product<2>(acc, r0, c0, 16, l_of, t_of, lane);
-      put(acc, r0, c0, 1.0f);
+    // [A 0; B C]^-1 = [A^-1 0; -C^-1 B A^-1 C^-1] for blocks of 16 (two pairs,
+    // four warps), then of 32 (all warps; a warp has 16 x 8).  B A^-1 waits in
+    // the block's own place.  T(k, c) = 0 for k < c, and its blocks above the
+    // diagonal do not exist.
+#pragma unroll 1
+    for (int round = 0; round < 4; ++round) {
+      const bool wide = round >= 2, second = round & 1;
+      const bool on = wide || warp < 4;
+      const int o = wide ? 0 : 32 * (warp >> 1);
+      const int r0 = wide ? 32 + 16 * (warp >> 2) : o + 16;
+      const int c0 = wide ? 8 * (warp & 3) : o + 8 * (warp & 1);
+      int k0 = wide ? (second ? 32 : 16 * ((warp & 3) >> 1)) : (second ? o + 16 : o);
+      const int pairs = !wide ? 1 : second ? 1 + (warp >> 2) : 2 - ((warp & 3) >> 1);
+      float acc[4];
+      if (on)
+        product(acc, (second ? T : L) + (r0 + g) * kTLd + k0 + t, T + (k0 + t) * kTLd + c0 + g,
+                pairs);
+      if (second) __syncthreads();
+      if (on) {
+        const float sign = second ? -1.0f : 1.0f;
+        float *p = T + (r0 + g) * kTLd + c0 + 2 * t;
+        *reinterpret_cast<float2 *>(p) = make_float2(sign * acc[0], sign * acc[1]);
+        *reinterpret_cast<float2 *>(p + 8 * kTLd) = make_float2(sign * acc[2], sign * acc[3]);
+      }
       __syncthreads();
-      if (warp < 4) product<2>(acc, r0, c0, 32, t_of, t_of, lane);
-      else product<4>(acc, r0, c0, 32, t_of, t_of, lane);
-      __syncthreads();
-      put(acc, r0, c0, -1.0f);
     }
-    __syncthreads();
 
-    // T's rows as two fp16 terms in L's place, four threads a row, and a power
+    // T's rows as two fp16 terms, four threads a row, and a power
     // of two above every row's sum
     {
       const int i = tid >> 2, q = tid & 3;
@@ -531,9 +540,6 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
     if (tid == 0) {
       bulk_store(ws_head + (static_cast<size_t>(slot) * d.v_heads + h) * kHeadBlob,
                  ptx::smem_u32(sm.head), kHeadBlob);
-      if (h % ratio == 0)
-        bulk_store(ws_key + (static_cast<size_t>(slot) * d.qk_heads + hk) * kKeyBlob<DK>,
-                   ptx::smem_u32(sm.key), kKeyBlob<DK>);
       bulk_store_wait(hh + 1 == heads);
     }
     if (hh + 1 < heads) __syncthreads();  // the copy has left the head's place
