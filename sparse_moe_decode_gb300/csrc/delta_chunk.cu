@@ -88,15 +88,19 @@ __device__ __forceinline__ int slot_base(const DeltaSeqs &s, int b) {
 
 // ------------------------------------------------------------------- prep
 
-constexpr int kTLd = kC + 4;     // row stride of L and T
+constexpr int kTLd = kC + 4;     // row stride of T
 constexpr int kPrepHeads = 4;    // value heads of one CTA at most
 
 template <int DK>
 struct PrepSmem {
-  // k and q until their products are formed; then L
+  // k and q until their products are formed; then those (tiles of 16 x 8 in the
+  // order of the accumulators, 2 w + 2 of warp w) and L (blocks of 16 x 16)
   union {
     alignas(128) uint8_t key[kKeyBlob<DK>];
-    float l[kC * kTLd];
+    struct {
+      float4 kk[20][32], qk[20][32];
+      float l[10 * 256];
+    };
   };
   alignas(128) uint8_t head[kHeadBlob];
   float t[kC * kTLd];  // T; blocks of 16 above the diagonal are never touched
@@ -118,19 +122,27 @@ __device__ __forceinline__ void token_scale(float ss, float &mult, float &inv) {
   inv = __uint_as_float(static_cast<uint32_t>(254 - m) << 23);
 }
 
-// A 16 x 8 tile of A B over `pairs` pairs of k8 steps; a and b point at this
-// lane's elements (row g, column t of A's tile; row t, column g of B's).  fp32
+// Where L(i, j) lies: blocks of 16 x 16, their pieces of four columns permuted
+// by the row, so that eight rows' pieces of one column lie in different banks.
+__device__ __forceinline__ int l_at(int i, int j) {
+  return block_of(i >> 4, j >> 4) * 256 + (i & 15) * 16 + ((j & 15) ^ (((i >> 1) & 3) << 2));
+}
+
+// A 16 x 8 tile of A B over `pairs` pairs of k8 steps; a points at this lane's
+// row g and column t of A (rows `a_ld` apart, its four pieces of a pair permuted
+// by `a_x`, pairs `a_step` apart), b at row t, column g of B (rows of T).  fp32
 // values as two tf32 terms each, three products.
-__device__ __forceinline__ void product(float (&acc)[4], const float *a, const float *b,
-                                        int pairs) {
+__device__ __forceinline__ void product(float (&acc)[4], const float *a, int a_ld, int a_x,
+                                        int a_step, const float *b, int pairs) {
   float part[3][4] = {};
 #pragma unroll 1
-  for (; pairs > 0; --pairs, a += 16, b += 16 * kTLd) {
+  for (; pairs > 0; --pairs, a += a_step, b += 16 * kTLd) {
     float x[2][4], y[2][2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      x[s][0] = a[8 * s], x[s][1] = a[8 * s + 8 * kTLd];
-      x[s][2] = a[8 * s + 4], x[s][3] = a[8 * s + 8 * kTLd + 4];
+      const float *left = a + (((2 * s) ^ a_x) << 2), *right = a + (((2 * s + 1) ^ a_x) << 2);
+      x[s][0] = left[0], x[s][1] = left[8 * a_ld];
+      x[s][2] = right[0], x[s][3] = right[8 * a_ld];
       y[s][0] = b[8 * s * kTLd], y[s][1] = b[(8 * s + 4) * kTLd];
     }
 #pragma unroll
@@ -298,28 +310,36 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
     bulk_store(ws_key + (static_cast<size_t>(slot) * d.qk_heads + hk) * kKeyBlob<DK>,
                ptx::smem_u32(sm.key), kKeyBlob<DK>);
 
-  // rows of k k^T or q k^T: the tiles left of the diagonal block, and its two
-  float off[6][4] = {}, dia[2][4] = {};
+  // Rows of k k^T or q k^T, up to the diagonal block; then, once nobody reads k
+  // and q any more, into their place.
+  float4(*prod)[32] = (is_q ? sm.qk : sm.kk) + w * (w + 1);
   {
-    const uint32_t at = kt + (is_q ? kKeyBlob<DK> / 2 : 0);
-    const int b_row = (lane & 7) + ((lane >> 4) << 3), b_piece = (lane >> 3) & 1;
+    float acc[8][4] = {};
+    // a row's pieces are permuted by its number mod 8, which is lane % 8 for
+    // every row that a lane addresses
+    constexpr uint32_t kRow = DK * 2;
+    const uint32_t a_at = kt + (is_q ? kKeyBlob<DK> / 2 : 0) + (16 * w + (lane & 15)) * kRow;
+    const uint32_t b_at = kt + ((lane & 7) + ((lane >> 4) << 3)) * kRow;
 #pragma unroll 2
     for (int s = 0; s < DK / 16; ++s) {
-      uint32_t a[4], bd[4], b[3][4];
-      ldsm4(a, at + tile_at<DK>(16 * w + (lane & 15), 2 * s + (lane >> 4)));
-      ldsm4(bd, kt + tile_at<DK>(16 * w + b_row, 2 * s + b_piece));
+      uint32_t a[4], b[4][4];
+      const uint32_t bc = ((2 * s + ((lane >> 3) & 1)) ^ (lane & 7)) << 4;
+      ldsm4(a, a_at + (((2 * s + (lane >> 4)) ^ (lane & 7)) << 4));
 #pragma unroll
-      for (int np = 0; np < 3; ++np)
-        if (np < w) ldsm4(b[np], kt + tile_at<DK>(16 * np + b_row, 2 * s + b_piece));
-      mma16(dia[0], a, bd[0], bd[1]);
-      mma16(dia[1], a, bd[2], bd[3]);
+      for (int np = 0; np < 4; ++np)
+        if (np <= w) ldsm4(b[np], b_at + np * 16 * kRow + bc);
 #pragma unroll
-      for (int np = 0; np < 3; ++np)
-        if (np < w) {
-          mma16(off[2 * np], a, b[np][0], b[np][1]);
-          mma16(off[2 * np + 1], a, b[np][2], b[np][3]);
+      for (int np = 0; np < 4; ++np)
+        if (np <= w) {
+          mma16(acc[2 * np], a, b[np][0], b[np][1]);
+          mma16(acc[2 * np + 1], a, b[np][2], b[np][3]);
         }
     }
+    if (keeps_key) bulk_store_wait(false);
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+      if (n < 2 * w + 2) prod[n][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
   }
 
   float *vec = reinterpret_cast<float *>(sm.head + 2 * kTri);
@@ -367,7 +387,6 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
         vec[kVecMisc * kC + kCMax] = cmax;
       }
     }
-    if (hh == 0 && keeps_key) bulk_store_wait(false);  // L takes k's and q's place
     __syncthreads();
 
     // L = beta_i kappa_i Gamma_ij kappa_j k_i.k_j below the diagonal, P =
@@ -403,31 +422,32 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
           *reinterpret_cast<__half2 *>(P + tri_at(i0, col / 8)) = __float22half2_rn(top);
           *reinterpret_cast<__half2 *>(P + tri_at(i1, col / 8)) = __float22half2_rn(low);
         } else {
-          *reinterpret_cast<float2 *>(L + i0 * kTLd + col + 2 * t) = top;
-          *reinterpret_cast<float2 *>(L + i1 * kTLd + col + 2 * t) = low;
+          *reinterpret_cast<float2 *>(L + l_at(i0, col + 2 * t)) = top;
+          *reinterpret_cast<float2 *>(L + l_at(i1, col + 2 * t)) = low;
         }
       };
-#pragma unroll
-      for (int n = 0; n < 6; ++n)
-        if (n < 2 * w) {
-          const float2 col = *reinterpret_cast<const float2 *>(&sm.col[w][8 * n + 2 * t]);
-          put_tile(8 * n, mul2(make_float2(off[n][0], off[n][1]), mul2(col, make_float2(a0, a0))),
-                   mul2(make_float2(off[n][2], off[n][3]), mul2(col, make_float2(a1, a1))));
-        }
+#pragma unroll 1
+      for (int n = 0; n < 2 * w; ++n) {
+        const float4 y = prod[n][lane];
+        const float2 col = *reinterpret_cast<const float2 *>(&sm.col[w][8 * n + 2 * t]);
+        put_tile(8 * n, mul2(make_float2(y.x, y.y), mul2(col, make_float2(a0, a0))),
+                 mul2(make_float2(y.z, y.w), mul2(col, make_float2(a1, a1))));
+      }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int j = ref + 8 * q + 2 * t;
         const float2 gj = *reinterpret_cast<const float2 *>(ghi + j);
         const float2 lj = *reinterpret_cast<const float2 *>(glo + j);
         const float2 kj = *reinterpret_cast<const float2 *>(sm.kappa + j);
-        float v[4];
+        const float4 y = prod[2 * w + q][lane];
+        float v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = (e >> 1) ? i1 : i0, jj = j + (e & 1);
           const float diff = (((e >> 1) ? h1r : h0r) - ((e & 1) ? gj.y : gj.x)) +
                              (((e >> 1) ? l1r : l0r) - ((e & 1) ? lj.y : lj.x));
           const bool on = is_q ? jj <= i : jj < i;
-          v[e] = on ? ((e >> 1) ? f1 : f0) * exp2f(diff) * ((e & 1) ? kj.y : kj.x) * dia[q][e] : 0.0f;
+          v[e] = on ? ((e >> 1) ? f1 : f0) * exp2f(diff) * ((e & 1) ? kj.y : kj.x) * v[e] : 0.0f;
         }
         put_tile(ref + 8 * q, make_float2(v[0], v[1]), make_float2(v[2], v[3]));
       }
@@ -441,7 +461,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
           float v = i == c ? 1.0f : 0.0f;
 #pragma unroll
           for (int j = 0; j < i; j += 4) {
-            const float4 l = *reinterpret_cast<const float4 *>(L + (ref + i) * kTLd + ref + j);
+            const float4 l = *reinterpret_cast<const float4 *>(L + l_at(ref + i, ref + j));
             v = fmaf(-l.x, x[j], v);
             if (j + 1 < i) v = fmaf(-l.y, x[j + 1], v);
             if (j + 2 < i) v = fmaf(-l.z, x[j + 2], v);
@@ -471,8 +491,10 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
       const int pairs = !wide ? 1 : second ? 1 + (warp >> 2) : 2 - ((warp & 3) >> 1);
       float acc[4];
       if (on)
-        product(acc, (second ? T : L) + (r0 + g) * kTLd + k0 + t, T + (k0 + t) * kTLd + c0 + g,
-                pairs);
+        product(acc, second ? T + (r0 + g) * kTLd + k0 + t
+                            : L + block_of(r0 >> 4, k0 >> 4) * 256 + g * 16 + t,
+                second ? kTLd : 16, second ? 0 : (g >> 1) & 3, second ? 16 : 256,
+                T + (k0 + t) * kTLd + c0 + g, pairs);
       if (second) __syncthreads();
       if (on) {
         const float sign = second ? -1.0f : 1.0f;
