@@ -128,22 +128,22 @@ __device__ __forceinline__ int l_at(int i, int j) {
   return block_of(i >> 4, j >> 4) * 256 + (i & 15) * 16 + ((j & 15) ^ (((i >> 1) & 3) << 2));
 }
 
-// A 16 x 8 tile of A B over `pairs` pairs of k8 steps; a points at this lane's
-// row g and column t of A (rows `a_ld` apart, its four pieces of a pair permuted
-// by `a_x`, pairs `a_step` apart), b at row t, column g of B (rows of T).  fp32
-// values as two tf32 terms each, three products.
-__device__ __forceinline__ void product(float (&acc)[4], const float *a, int a_ld, int a_x,
-                                        int a_step, const float *b, int pairs) {
+// A 16 x 8 tile of A B over `pairs` pairs of k8 steps; a is the shared address of
+// this lane's row g and column t of A (rows `a_ld` bytes apart, its four pieces
+// of a pair permuted by `a_x`, pairs `a_step` apart), b that of row t, column g
+// of B (rows of T).  fp32 values as two tf32 terms each, three products.
+__device__ __forceinline__ void product(float (&acc)[4], uint32_t a, uint32_t a_ld, uint32_t a_x,
+                                        uint32_t a_step, uint32_t b, int pairs) {
   float part[3][4] = {};
 #pragma unroll 1
-  for (; pairs > 0; --pairs, a += a_step, b += 16 * kTLd) {
+  for (; pairs > 0; --pairs, a += a_step, b += 16 * kTLd * 4) {
     float x[2][4], y[2][2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const float *left = a + (((2 * s) ^ a_x) << 2), *right = a + (((2 * s + 1) ^ a_x) << 2);
-      x[s][0] = left[0], x[s][1] = left[8 * a_ld];
-      x[s][2] = right[0], x[s][3] = right[8 * a_ld];
-      y[s][0] = b[8 * s * kTLd], y[s][1] = b[(8 * s + 4) * kTLd];
+      const uint32_t left = a + (((2 * s) ^ a_x) << 4), right = a + (((2 * s + 1) ^ a_x) << 4);
+      x[s][0] = lds(left), x[s][1] = lds(left + 8 * a_ld);
+      x[s][2] = lds(right), x[s][3] = lds(right + 8 * a_ld);
+      y[s][0] = lds(b + 8 * s * kTLd * 4), y[s][1] = lds(b + (8 * s + 4) * kTLd * 4);
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -270,7 +270,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
       *reinterpret_cast<float2 *>(&sm.beta[warp][2 * lane]) = make_float2(be0, be1);
     }
     cp_async_wait<0>();  // each lane converts what it brought in
-#pragma unroll 1
+#pragma unroll 2
     for (int p = 0; p < 4; ++p) {
       const int i = row + 4 * p;
       float2 x[kPieces][4], sum = make_float2(0.0f, 0.0f);
@@ -298,7 +298,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
         *reinterpret_cast<uint4 *>(tile + tile_at<DK>(i, piece + 8 * e)) =
             make_uint4(o[0], o[1], o[2], o[3]);
       }
-      if (d.qk_norm) inv = inv / sqrtf(ss + d.qk_eps);
+      if (d.qk_norm) inv *= rsqrtf(ss + d.qk_eps);
       if (is_q) inv *= d.scale;
       if (piece == 0) (is_q ? sm.rho : sm.kappa)[i] = i < left ? inv : 0.0f;
     }
@@ -345,6 +345,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
   float *vec = reinterpret_cast<float *>(sm.head + 2 * kTri);
   float *vec_b = reinterpret_cast<float *>(sm.head + kPartA + kTri);
   float *L = sm.l, *T = sm.t;
+  const uint32_t l_base = ptx::smem_u32(L), t_at = ptx::smem_u32(T);
   for (int hh = 0; hh < heads; ++hh) {
     const int h = h0 + hh;
     const float *ghi = sm.ghi[hh], *glo = sm.glo[hh];
@@ -491,10 +492,10 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
       const int pairs = !wide ? 1 : second ? 1 + (warp >> 2) : 2 - ((warp & 3) >> 1);
       float acc[4];
       if (on)
-        product(acc, second ? T + (r0 + g) * kTLd + k0 + t
-                            : L + block_of(r0 >> 4, k0 >> 4) * 256 + g * 16 + t,
-                second ? kTLd : 16, second ? 0 : (g >> 1) & 3, second ? 16 : 256,
-                T + (k0 + t) * kTLd + c0 + g, pairs);
+        product(acc, second ? t_at + ((r0 + g) * kTLd + k0 + t) * 4
+                            : l_base + (block_of(r0 >> 4, k0 >> 4) * 256 + g * 16 + t) * 4,
+                4 * (second ? kTLd : 16), second ? 0 : (g >> 1) & 3, 4 * (second ? 16 : 256),
+                t_at + ((k0 + t) * kTLd + c0 + g) * 4, pairs);
       if (second) __syncthreads();
       if (on) {
         const float sign = second ? -1.0f : 1.0f;

@@ -103,6 +103,12 @@ __device__ __forceinline__ void split_h2(float2 x, uint32_t &hi, uint32_t &lo) {
   lo = h2_bits(__floats2half2_rn(a, b));
 }
 
+__device__ __forceinline__ float lds(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(live ? 16 : 0)
