@@ -11,6 +11,7 @@
 #include "common.cuh"
 #include "delta_seq.cuh"
 #include "early.cuh"
+#include "kernels.h"
 #include "mixer.h"
 
 namespace moe {
@@ -72,28 +73,56 @@ constexpr int kRows = 16;  // state rows per warp
 
 // One warp holds kRows rows of one head's state, lane l columns V l .. V l +
 // V - 1 of each (a row is one coalesced access).
-template <int DK>
-__global__ void __launch_bounds__(32 * kWarps)
+// BLOCKS: blocks of an SM that the registers leave room for.
+template <int DK, int BLOCKS>
+__global__ void __launch_bounds__(32 * kWarps, BLOCKS)
 delta_recurrent_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, moe_bf16 *out,
                        int64_t out_ld) {
   constexpr int V = DK / 32;
   using VF = typename Vec<V>::F;
   using VH = typename Vec<V>::H;
   const int lane = threadIdx.x & 31;
-  const int tiles = d.v_dim / kRows;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const uint32_t tiles = d.v_dim / kRows;
+  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int tile = static_cast<int>(unit % tiles);
-  const int64_t bh = unit / tiles;
-  const int h = static_cast<int>(bh % d.v_heads);
-  const int64_t b64 = bh / d.v_heads;
-  if (b64 >= seq.B) return;
-  const int b = static_cast<int>(b64);
+  const int h = static_cast<int>(unit / tiles % d.v_heads);
+  const int b = static_cast<int>(unit / tiles / d.v_heads);
+  if (b >= seq.B) return;
   early_begin();
+  if (seq.cu_seqlens) {
+    // a call with a bad bound does nothing (launched for few sequences only)
+    bool bad = false;
+    for (int i = lane; i < seq.B; i += 32) {
+      const int lo = seq.cu_seqlens[i], hi = seq.cu_seqlens[i + 1];
+      bad |= lo < 0 || lo > hi || hi > seq.N;
+    }
+    if (__any_sync(kFull, bad)) {
+      if (lane == 0) set_status(seq.status, MOE_DEV_BAD_INDEX);
+      return;
+    }
+  }
   const DeltaSeqRange r = delta_seq_range(seq, b);
   if (!r.ok) return;
   const int hk = h / (d.v_heads / d.qk_heads);
   const int64_t at =
       ((static_cast<int64_t>(r.slot) * d.v_heads + h) * d.v_dim + tile * kRows) * DK + lane * V;
+  // A token's values are asked for one token ahead.
+  const int64_t row0 = r.start;
+  const moe_bf16 *kp = in.k + row0 * in.k_ld + hk * DK + lane * V;
+  const moe_bf16 *qp = in.q + row0 * in.q_ld + hk * DK + lane * V;
+  const moe_bf16 *vp =
+      in.v + row0 * in.v_ld + h * d.v_dim + tile * kRows + (lane & (kRows - 1));
+  const float *gp = in.g + row0 * in.g_ld + h, *bp = in.beta + row0 * in.beta_ld + h;
+  moe_bf16 *op = out + row0 * out_ld + h * d.v_dim + tile * kRows + lane;
+  VH kw{}, qw{};
+  uint16_t vw = 0;
+  float gw = 0.0f, bw = 0.0f;
+  const auto fetch = [&] {
+    kw = *reinterpret_cast<const VH *>(kp), qw = *reinterpret_cast<const VH *>(qp);
+    vw = *vp, gw = *gp, bw = *bp;
+    kp += in.k_ld, qp += in.q_ld, vp += in.v_ld, gp += in.g_ld, bp += in.beta_ld;
+  };
+  if (r.len > 0) fetch();
   float s[kRows][V];
   if (seq.state_in) {
     const float *p = seq.state_in + at;
@@ -105,15 +134,12 @@ delta_recurrent_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, moe
 #pragma unroll
       for (int j = 0; j < V; ++j) s[i][j] = 0.0f;
   }
-  for (int t = 0; t < r.len; ++t) {
-    const int64_t row = static_cast<int64_t>(r.start) + t;
+  for (int t = 0; t < r.len; ++t, op += out_ld) {
     float k[V], q[V];
-    unpack(*reinterpret_cast<const VH *>(in.k + row * in.k_ld + hk * DK + lane * V), k);
-    unpack(*reinterpret_cast<const VH *>(in.q + row * in.q_ld + hk * DK + lane * V), q);
-    const float v =
-        bf16_to_f32(in.v[row * in.v_ld + h * d.v_dim + tile * kRows + (lane & (kRows - 1))]);
-    const float a = expf(delta_log_decay(in.g[row * in.g_ld + h]));
-    const float beta = in.beta[row * in.beta_ld + h];
+    unpack(kw, k);
+    unpack(qw, q);
+    const float v = bf16_to_f32(vw), a = expf(delta_log_decay(gw)), beta = bw;
+    if (t + 1 < r.len) fetch();
     float kk = 0.0f, qq = 0.0f, kq = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -124,8 +150,8 @@ delta_recurrent_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, moe
     kk = warp_sum(kk), qq = warp_sum(qq), kq = warp_sum(kq);
     float kn = 1.0f, qn = d.scale;
     if (d.qk_norm) {
-      kn = 1.0f / sqrtf(kk + d.qk_eps);
-      qn = d.scale / sqrtf(qq + d.qk_eps);
+      kn = rsqrtf(kk + d.qk_eps);
+      qn = d.scale * rsqrtf(qq + d.qk_eps);
     }
     float part[2 * kRows];
 #pragma unroll
@@ -144,8 +170,7 @@ delta_recurrent_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, moe
     const float sq = __shfl_down_sync(kFull, sum, kRows);
     const float u = beta * (v - a * kn * sum);  // lanes < kRows
     if (lane < kRows)
-      out[row * out_ld + h * d.v_dim + tile * kRows + lane] =
-          f32_to_bf16(qn * (a * sq + u * kn * kq));
+      *op = f32_to_bf16(qn * (a * sq + u * kn * kq));
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const float ui = __shfl_sync(kFull, u, i) * kn;
@@ -167,8 +192,16 @@ cudaError_t launch_delta_recurrent(const moe_delta_dims &d, const moe_delta_inpu
                                    cudaStream_t s) {
   const int64_t units = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / kRows);
   const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
-  return launch_early(d.qk_dim == 128 ? delta_recurrent_kernel<128> : delta_recurrent_kernel<64>,
-                      dim3(grid), 32 * kWarps, 0, s, d, in, seq, out, out_ld);
+  // Three blocks an SM keep a token's values in registers ahead of their use:
+  // 22.4 against 23.3 us for 32 sequences of one token (32 heads of 128), 12.3
+  // against 13.2 us for 4 of 8.  More blocks than that at once, with several
+  // tokens each to work on, go faster four to an SM: 8 of 8 tokens in 15.7
+  // against 17.9 us.
+  const bool four = seq.T > 1 && grid > 3u * static_cast<unsigned>(tc_sm_count());
+  const auto kernel = d.qk_dim == 128
+                          ? (four ? delta_recurrent_kernel<128, 4> : delta_recurrent_kernel<128, 3>)
+                          : (four ? delta_recurrent_kernel<64, 4> : delta_recurrent_kernel<64, 3>);
+  return launch_early(kernel, dim3(grid), 32 * kWarps, 0, s, d, in, seq, out, out_ld);
 }
 
 }  // namespace moe

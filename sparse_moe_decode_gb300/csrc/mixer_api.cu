@@ -14,6 +14,11 @@ namespace {
 constexpr int kDeltaMaxTokens = 1 << 20;
 constexpr int kDeltaMaxSeqs = 65536;
 constexpr int kDeltaMaxHeads = 256;
+// Calls of so few token rows run token by token: one sequence (32 value heads
+// of 128) takes 14.6 us in the chunked form whatever its length up to 64, and
+// 3.8 us and 0.65 us for each further token in the recurrent one (13.6 us at 16).
+constexpr int kRecurrentTokens = 16;
+constexpr int kRecurrentSeqs = 64;
 constexpr int kNormMaxWidth = 16384;
 constexpr int64_t kNormMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxStride = int64_t(1) << 31;  // elements: offsets stay far inside 63 bits
@@ -137,6 +142,9 @@ moe_status moe_delta_chunk(const moe_delta_dims *dims, const moe_delta_inputs *i
   if (B == 0) return MOE_OK;
   const DeltaSeqs seq = delta_seqs(cu_seqlens, N, B, N, slots, n_slots, state_in, state_out,
                                    workspace);
+  if (N <= kRecurrentTokens && B <= kRecurrentSeqs)
+    return cuda_status(launch_delta_recurrent(*dims, *in, seq, out, out_ld,
+                                              static_cast<cudaStream_t>(stream)));
   return cuda_status(launch_delta_chunk(*dims, *in, seq, workspace, out, out_ld,
                                         static_cast<cudaStream_t>(stream)));
 }
