@@ -8,24 +8,35 @@
 //   S' = gamma_64 S + sum_j Gamma_64,j u_j k_j^T.
 // The first line is a unit lower-triangular system: u = T x with T = (I + L)^-1.
 //
-// Two kernels.  delta_prep_kernel, one CTA per (chunk, value head), forms
-// what does not depend on the state: T, the masked q.k products P, the
-// decays, and k and q as fp16.  delta_chain_kernel walks a sequence's chunks
-// with the state in registers: a warp owns 16 state rows (all of their
-// columns), and the three products of its chain -- S k^T, T x, u k^T -- hand
-// their results on as the next one's A operand without leaving the warp's
-// registers (an accumulator fragment of mma.sync m16n8 is an A fragment of
-// the next k16 step), so that no barrier lies on the chain.  A second warp
-// per 16 rows forms the outputs from copies of the operands.  mma.sync
-// rather than tcgen05: the chain is bound by its dependent steps, and a
-// round trip of each through tensor memory costs more than the products.
+// Two kernels.  delta_prep_kernel, a CTA per chunk and key head, forms what
+// does not depend on the state: T, the masked q.k products P, the decays, and k
+// and q as fp16.  delta_chain_kernel walks a sequence's chunks with the state in
+// registers, 16 of its rows to a group of four warps.  Two of them are the
+// chain, each with half of the key channels: S k^T, T x and u k^T follow one
+// another there, and the two exchange shares through shared memory.  The other
+// two form the outputs from copies of the operands, a phase behind, and bring in
+// the next chunks.  mma.sync rather than tcgen05: the chain is bound by the
+// latency of its dependent steps, and a round trip of each through tensor
+// memory costs more than its few products.
 //
 // Precision.  k and q are bf16: scaled by a power of two per token they are
-// exact in fp16 (elements within 2^29 of the token's largest).  S, x, u and T
-// are fp32 and enter the products as two fp16 terms under a power-of-two
-// scale per row, 22 bits; products accumulate in fp32 and the state is summed
-// in fp32 registers.  The outputs, which are rounded to bf16 once, take P, S
-// and u as single fp16 terms (2^-11, an eighth of the rounding to come).
+// exact in fp16 down to 2^-25 of the token's norm.  S, x, u and T are fp32 and
+// enter the products as two fp16 terms under a power-of-two scale per row, 22
+// bits; products accumulate in fp32 and the state is summed in fp32 registers.
+// The scales are of the largest value where one warp holds a row (S) and of a
+// bound from norms where two would have to agree (x, u).  The outputs, which
+// are rounded to bf16 once, take P, S and u as single fp16 terms (2^-11, an
+// eighth of the rounding to come).
+//
+// What bounds it (GB300, 32 value heads of 128 x 128 on 16 key heads).  A chunk
+// of the chain takes 1.76 us on whatever SM it runs, so one prompt of 8192
+// tokens takes 225 us there and 84 us in the preparation, of 31 us for the
+// bytes; 13 sequences of 6007 tokens in all, 177 us on 152 SMs, against 170 us
+// if every SM had work to the end.  Measured and slower: four chain warps a group
+// with a quarter of the channels each (393 against 338 us for 8192 tokens then),
+// one output warp a group (369), a ninth warp for the copies (446: 168 registers
+// a thread), and CTAs that stay and take one piece of the work after the other
+// (321 against 313 us, and 263 against 246 for the 13 sequences).
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -571,13 +582,16 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
 
 // ------------------------------------------------------------------ chain
 
-// How the chain runs: WARPS chain warps and two output warps per group of 16
-// state rows, GROUPS groups per CTA, one CTA per SM.
-template <int DK, int WARPS, int GROUPS>
+// How the chain runs: kHalves chain warps and two output warps per group of 16
+// state rows, kGroups groups per CTA, one CTA per SM.
+constexpr int kHalves = 2;
+constexpr int kGroups = 2;
+constexpr int kRows = 16 * kGroups;  // state rows of a CTA
+
+template <int DK>
 struct Chain {
-  static constexpr int kCols = DK / WARPS;   // key channels of a chain warp
-  static constexpr int kSteps = kCols / 16;  // k16 steps of its share of S k^T
-  static constexpr int kOwn = 4 / WARPS;     // 16-token blocks of u it forms
+  static constexpr int kCols = DK / kHalves;  // key channels of a chain warp
+  static constexpr int kSteps = kCols / 16;   // k16 steps of its share of S k^T
   // Ring stages: for the chain warps k, T and their vectors; for the output
   // warps q, P and theirs.
   static constexpr int kStageA = kKeyBlob<DK> / 2 + kPartA;
@@ -587,22 +601,22 @@ struct Chain {
   // ninth would cost every one of them a third.  So the four output warps
   // bring in the rings' stages, one of a chunk's four copies each (issuing a
   // bulk copy holds its thread for some 500 cycles).
-  static constexpr int kThreads = 32 * (WARPS + 2) * GROUPS;
+  static constexpr int kThreads = 32 * (kHalves + 2) * kGroups;
 
   // What the warps of a group hand one another.
   struct Group {
     uint4 s_frag[DK / 16][32];           // S as A fragments, fp16
     uint4 u_frag[4][32];                 // u likewise
-    float4 x_part[4][WARPS - 1][2][32];  // shares of S k^T for the block's owner
+    float4 x_part[4][2][32];             // shares of S k^T for the block's owner
     float4 y[4][2][32];                  // beta v
     uint4 x_frag[4][2][32];              // x as A fragments, two terms
     uint4 w_frag[4][2][32];              // the update's, two terms
-    float2 s_inv[WARPS][32], v_max[2][32], u_inv[32];
+    float2 s_inv[kHalves][32], v_max[2][32], u_inv[32];
     alignas(16) uint8_t v[3][kC * 32];   // 16 value channels of the chunk's tokens
     alignas(16) uint8_t o[kC * 32];      // output rows on their way out
   };
   static constexpr int kSmem = kStages * (kStageA + kStageB) +
-                               GROUPS * static_cast<int>(sizeof(Group)) + 256;
+                               kGroups * static_cast<int>(sizeof(Group)) + 256;
 };
 
 __device__ __forceinline__ float quad_max(float v) {
@@ -642,22 +656,22 @@ __device__ __forceinline__ void get4(const uint4 *p, uint32_t (&v)[4]) {
   v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
 }
 
-template <int DK, int WARPS, int GROUPS>
-__global__ void __launch_bounds__(Chain<DK, WARPS, GROUPS>::kThreads, 1)
+template <int DK>
+__global__ void __launch_bounds__(Chain<DK>::kThreads, 1)
 delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const uint8_t *ws,
                    const uint8_t *ws_key, const uint8_t *ws_head, moe_bf16 *out, int64_t out_ld,
                    unsigned long long budget_ns) {
-  using C = Chain<DK, WARPS, GROUPS>;
+  using C = Chain<DK>;
   using Group = typename C::Group;
   constexpr int kKeyTile = kKeyBlob<DK> / 2, kStages = C::kStages;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t *ring_a = smem_raw, *ring_b = ring_a + kStages * C::kStageA;
   Group *groups = reinterpret_cast<Group *>(ring_b + kStages * C::kStageB);
-  uint64_t *full = reinterpret_cast<uint64_t *>(groups + GROUPS);
-  int *abort_flag = reinterpret_cast<int *>(full + kStages);
+  uint64_t *full = reinterpret_cast<uint64_t *>(groups + kGroups);
+  int *abort_flag = reinterpret_cast<int *>(full + kStages), *fed_by = abort_flag + 1;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tiles = d.v_dim / (16 * GROUPS);
+  const int tiles = d.v_dim / kRows;
   const int tile = blockIdx.x % tiles;
   const int h = (blockIdx.x / tiles) % d.v_heads;
   const int b = blockIdx.x / tiles / d.v_heads;
@@ -675,8 +689,8 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   }
   __syncthreads();
 
-  // Chain warps WARPS g .. WARPS g + WARPS - 1 (a share of the key channels
-  // each), output warps WARPS GROUPS + 2 g, + 1 (half of the tokens each).  The
+  // Chain warps 2 g, 2 g + 1 (half of the key channels each), output warps
+  // kHalves kGroups + 2 g, + 1 (half of the tokens each).  The
   // warps meet three times per chunk: all of the CTA at bar_x (the shares of S
   // k^T, the copy of S and beta v are there; nobody reads the previous chunk's
   // stage any more), a group's chain warps at bar_y (x is there), a group at
@@ -684,12 +698,13 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   // group is written before one of them, read after it, and free again when
   // its writer comes back to it: x_part, y and v_max x|y, s_frag x|w, x_frag
   // y|w, w_frag and u_frag w|next x.
-  const bool chain = warp < WARPS * GROUPS;
-  const int group = chain ? warp / WARPS : (warp - WARPS * GROUPS) / 2, part = warp % WARPS;
+  const bool chain = warp < kHalves * kGroups;
+  const int group = chain ? warp / kHalves : (warp - kHalves * kGroups) / 2;
+  const int part = warp % kHalves;
   Group &gs = groups[group];
-  const int bar_x = 0, bar_y = 1 + 2 * group, bar_w = bar_y + 1;
-  constexpr int kAll = C::kThreads, kGroup = 32 * (WARPS + 2);
-  const int dv0 = (tile * GROUPS + group) * 16;
+  const int bar_x = 0, bar_y = 1 + 2 * group, bar_w = bar_y + 1, bar_out = 1 + 2 * kGroups;
+  constexpr int kAll = C::kThreads, kGroup = 32 * (kHalves + 2);
+  const int dv0 = (tile * kGroups + group) * 16;
   const int g = lane >> 2, t = lane & 3;
   // B fragments of two n8 tiles from rows (plain) or columns (trans) of a tile
   const int b_row = (lane & 7) + ((lane >> 4) << 3), b_piece = (lane >> 3) & 1;
@@ -709,12 +724,8 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
     }
     // The 16-token blocks whose x and u this warp forms.  u's block np takes
     // np + 1 steps: blocks 0 and 3, and 1 and 2, make equal pairs.
-    int own[C::kOwn];
-    if constexpr (WARPS == 4) own[0] = part;
-    else own[0] = part, own[1] = 3 - part;
-    // the warp that owns block np, and where this warp's share for it goes
-    const auto owner = [](int np) { return WARPS == 4 ? np : min(np, 3 - np); };
-    const auto place = [&](int np) { return (part - owner(np) - 1 + WARPS) % WARPS; };
+    const int own[2] = {part, 3 - part};
+    const auto owner = [](int np) { return min(np, 3 - np); };
     float m0, m1, i0, i1;
     {
       float a0 = 0.0f, a1 = 0.0f;
@@ -754,7 +765,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
           mma16(X[2 * np + 1], lo, bb[np][2], bb[np][3]);
         }
       }
-      Acc mine[C::kOwn][2];
+      Acc mine[2][2];
 #pragma unroll
       for (int np = 0; np < 4; ++np)
 #pragma unroll
@@ -762,16 +773,16 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
           Acc &x = X[2 * np + q];
           x.top = mul2(x.top, both(i0)), x.low = mul2(x.low, both(i1));
           if (owner(np) != part)
-            gs.x_part[np][place(np)][q][lane] = make_float4(x.top.x, x.top.y, x.low.x, x.low.y);
+            gs.x_part[np][q][lane] = make_float4(x.top.x, x.top.y, x.low.x, x.low.y);
 #pragma unroll
-          for (int j = 0; j < C::kOwn; ++j)
+          for (int j = 0; j < 2; ++j)
             if (np == own[j]) mine[j][q] = x;
         }
       // T's fragments of the own blocks, a step ahead of their use
-      uint32_t th[2][C::kOwn][4], tl[2][C::kOwn][4];
+      uint32_t th[2][2][4], tl[2][2][4];
       const auto load_t = [&](int s) {
 #pragma unroll
-        for (int j = 0; j < C::kOwn; ++j)
+        for (int j = 0; j < 2; ++j)
           if (s <= own[j]) {
             const uint32_t a = tt + block_of(own[j], s) * kBlock + row32_at(b_row, b_piece);
             ldsm4(th[s & 1][j], a);
@@ -779,9 +790,9 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
           }
       };
       load_t(0);
-      float2 cc[C::kOwn][2];
+      float2 cc[2][2];
 #pragma unroll
-      for (int j = 0; j < C::kOwn; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int q = 0; q < 2; ++q)
           cc[j][q] =
@@ -792,36 +803,24 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
       // norms, so that the warps agree on it without another exchange:
       // |S k_i| <= |S| |k_i|, where k_i (scaled) stays below 2^15 and each
       // share of S below 2^15 i0 per element.
-      float2 si = gs.s_inv[0][lane];
-#pragma unroll
-      for (int p = 1; p < WARPS; ++p) si = add2(si, gs.s_inv[p][lane]);
+      const float2 si = add2(gs.s_inv[0][lane], gs.s_inv[1][lane]);
       const float2 va = gs.v_max[0][lane], vb = gs.v_max[1][lane];
       const float2 vm = make_float2(fmaxf(va.x, vb.x), fmaxf(va.y, vb.y));
       const float gamma = misc.x, tau = misc.y, back = misc.y * misc.z;
-      const float reach = misc.w * (0x1p30f * (C::kCols == 16   ? 4.0f
-                                               : C::kCols == 32 ? 5.66f
-                                                                : 8.0f));
+      const float reach = misc.w * (0x1p30f * (C::kCols == 32 ? 5.66f : 8.0f));  // sqrt
       float n0, n1, j0, j1;
       pow2_above(fmaf(reach, si.x, vm.x), j0, n0);
       pow2_above(fmaf(reach, si.y, vm.y), j1, n1);
       n0 *= 0x1p15f, n1 *= 0x1p15f, j0 *= 0x1p-15f, j1 *= 0x1p-15f;
 #pragma unroll
-      for (int j = 0; j < C::kOwn; ++j) {
-        float4 y[WARPS - 1][2];
-#pragma unroll
-        for (int p = 0; p < WARPS - 1; ++p)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) y[p][q] = gs.x_part[own[j]][p][q][lane];
+      for (int j = 0; j < 2; ++j) {
+        const float4 y[2] = {gs.x_part[own[j]][0][lane], gs.x_part[own[j]][1][lane]};
         const float4 z[2] = {gs.y[own[j]][0][lane], gs.y[own[j]][1][lane]};
         Acc x[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          x[q] = mine[j][q];
-#pragma unroll
-          for (int p = 0; p < WARPS - 1; ++p) {
-            x[q].top = add2(x[q].top, make_float2(y[p][q].x, y[p][q].y));
-            x[q].low = add2(x[q].low, make_float2(y[p][q].z, y[p][q].w));
-          }
+          x[q].top = add2(mine[j][q].top, make_float2(y[q].x, y[q].y));
+          x[q].low = add2(mine[j][q].low, make_float2(y[q].z, y[q].w));
           x[q].top = fma2(cc[j][q], x[q].top, make_float2(z[q].x, z[q].y));
           x[q].low = fma2(cc[j][q], x[q].low, make_float2(z[q].z, z[q].w));
         }
@@ -830,27 +829,27 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
         put4(&gs.x_frag[own[j]][0][lane], hi);
         put4(&gs.x_frag[own[j]][1][lane], lo);
       }
-      float2 ts[C::kOwn][2], dd[C::kOwn][2];
+      float2 ts[2][2], dd[2][2];
 #pragma unroll
-      for (int j = 0; j < C::kOwn; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int col = 16 * own[j] + 8 * q + 2 * t;
           ts[j][q] = *reinterpret_cast<const float2 *>(vec + kVecT * kC + col);
           dd[j][q] = *reinterpret_cast<const float2 *>(vec + kVecD * kC + col);
         }
-      bar_sync(bar_y, 32 * WARPS);
+      bar_sync(bar_y, 32 * kHalves);
       // u = T x
-      Acc U[C::kOwn][2] = {}, V[C::kOwn][2] = {}, W[C::kOwn][2] = {};
+      Acc U[2][2] = {}, V[2][2] = {}, W[2][2] = {};
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        if (s > own[C::kOwn - 1]) continue;  // the last is the largest
+        if (s > own[1]) continue;  // the larger one
         uint32_t hi[4], lo[4];
         get4(&gs.x_frag[s][0][lane], hi);
         get4(&gs.x_frag[s][1][lane], lo);
         if (s < 3) load_t(s + 1);
 #pragma unroll
-        for (int j = 0; j < C::kOwn; ++j)
+        for (int j = 0; j < 2; ++j)
           if (s <= own[j])
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -864,7 +863,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
       // kappa_j u_j over the largest such factor.
       if (part == 0) gs.u_inv[lane] = make_float2(j0 * tau, j1 * tau);
 #pragma unroll
-      for (int j = 0; j < C::kOwn; ++j) {
+      for (int j = 0; j < 2; ++j) {
         uint32_t f[4], hi[4], lo[4];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -888,7 +887,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
         get4(&gs.w_frag[s][1][lane], wl[s]);
       }
       const float2 b0 = both(j0 * back), b1 = both(j1 * back);
-      constexpr int kAt = C::kSteps >= 2 ? 2 : 1;  // 16-channel blocks at a time
+      constexpr int kAt = 2;  // 16-channel blocks at a time
       float a0 = 0.0f, a1 = 0.0f;
 #pragma unroll
       for (int np = 0; np < C::kSteps; np += kAt) {
@@ -937,7 +936,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   // Output warps: o_i = rho_i gamma_i (S q_i) + sum_j P_ij u_j.  They also bring
   // in the group's values, as beta v in the chain's accumulator layout.  Each
   // has two of the four 16-token blocks, an equal share of P's triangle.
-  const int side = (warp - WARPS * GROUPS) & 1;
+  const int side = (warp - kHalves * kGroups) & 1;
   const int own[2] = {side, 3 - side};
   const int my_row = lane >> 1;  // of a block, and the half row this lane copies
   const int64_t row0 = r.start + my_row;
@@ -989,8 +988,8 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   };
   // This warp's copy of every chunk: k or T's part into ring a, q or P's into
   // ring b.
-  static_assert(2 * GROUPS == 4, "an output warp for each copy of a chunk");
-  const int copy = warp - WARPS * GROUPS;
+  static_assert(2 * kGroups == 4, "an output warp for each copy of a chunk");
+  const int copy = warp - kHalves * kGroups;
   const bool into_b = copy & 2, of_head = copy & 1;
   const size_t base = slot_base(seq, b);
   const uint8_t *from = of_head ? ws_head + (base * d.v_heads + h) * kHeadBlob + (into_b ? kPartA : 0)
@@ -1038,12 +1037,8 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
     uint32_t a[DK / 16][4];
 #pragma unroll
     for (int s = 0; s < DK / 16; ++s) get4(&gs.s_frag[s][lane], a[s]);
-    float2 si[WARPS], most = both(0.0f);
-#pragma unroll
-    for (int p = 0; p < WARPS; ++p) {
-      si[p] = gs.s_inv[p][lane];
-      most = make_float2(fmaxf(most.x, si[p].x), fmaxf(most.y, si[p].y));
-    }
+    const float2 si[2] = {gs.s_inv[0][lane], gs.s_inv[1][lane]};
+    const float2 most = make_float2(fmaxf(si[0].x, si[1].x), fmaxf(si[0].y, si[1].y));
     float down0, down1, unused;
     pow2_above(most.x * 0.5f, unused, down0);  // 1 / most, a power of two
     pow2_above(most.y * 0.5f, unused, down1);
@@ -1125,8 +1120,14 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
     __syncwarp();
   }
   cp_async_wait<0>();
+  // Copies in flight land before the CTA's shared memory is given up.  After a
+  // wait that gave up, some of the four may have issued one more than the
+  // others, whose arrivals its barrier then still waits for.
+  if (lane == 0) fed_by[copy] = fed;
+  bar_sync(bar_out, 4 * 32);
   if (lane == 0) {
-    // copies in flight land before the CTA's shared memory is given up
+    const int all = max(max(fed_by[0], fed_by[1]), max(fed_by[2], fed_by[3]));
+    for (; fed < all; ++fed) ptx::mbar_arrive(&full[fed % kStages]);
     int ignore = 0;
     for (int c = max(0, fed - kStages); c < fed; ++c)
       ptx::mbar_wait(&full[c % kStages], (c / kStages) & 1, &ignore, ptx::kDrainBudgetNs);
@@ -1147,17 +1148,17 @@ cudaError_t allow_smem(F kernel, int bytes, std::atomic<uint64_t> &done) {
   return e;
 }
 
-template <int DK, int WARPS, int GROUPS>
+template <int DK>
 cudaError_t launch_chain(const moe_delta_dims &d, const moe_delta_inputs &in, const DeltaSeqs &seq,
                          const uint8_t *ws, const uint8_t *ws_key, const uint8_t *ws_head,
                          moe_bf16 *out, int64_t out_ld, cudaStream_t s) {
-  using C = Chain<DK, WARPS, GROUPS>;
+  using C = Chain<DK>;
   static_assert(C::kSmem <= 227 * 1024, "shared memory of one SM");
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(delta_chain_kernel<DK, WARPS, GROUPS>, C::kSmem, done);
+  cudaError_t e = allow_smem(delta_chain_kernel<DK>, C::kSmem, done);
   if (e != cudaSuccess) return e;
-  const int64_t grid = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / (16 * GROUPS));
-  return launch_early(delta_chain_kernel<DK, WARPS, GROUPS>, dim3(static_cast<unsigned>(grid)),
+  const int64_t grid = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / kRows);
+  return launch_early(delta_chain_kernel<DK>, dim3(static_cast<unsigned>(grid)),
                       C::kThreads, C::kSmem, s, d, in, seq, ws, ws_key, ws_head, out, out_ld,
                       tc_wait_budget_ns());
 }
@@ -1185,7 +1186,7 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
   e = launch_early(delta_prep_kernel<DK>, grid, kPrepThreads, kSmem, s, d, in, seq, heads, ws,
                    ws_key, ws_head);
   if (e != cudaSuccess) return e;
-  return launch_chain<DK, 2, 2>(d, in, seq, ws, ws_key, ws_head, out, out_ld, s);
+  return launch_chain<DK>(d, in, seq, ws, ws_key, ws_head, out, out_ld, s);
 }
 
 }  // namespace

@@ -10,9 +10,10 @@
 
 namespace moe {
 
-// Four 8x8 blocks of 16-bit values, ordered by barriers like any volatile asm; lane l gives the address of row l % 8 of
+// Four 8x8 blocks of 16-bit values; lane l gives the address of row l % 8 of
 // block l / 8.  Plain: lane holds row lane / 4, columns 2 (lane % 4), + 1 of
-// each block; trans: the same of the transposed block.
+// each block; trans: the same of the transposed block.  Barriers order them
+// like any volatile asm.
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -153,12 +154,9 @@ __device__ __forceinline__ void mbar_expect(uint64_t *bar, uint32_t bytes) {
                : "memory");
 }
 
-// Hardware barrier `id` of `threads` threads: sync waits, arrive does not.
+// Hardware barrier `id` of `threads` threads.
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(int id, int threads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 }  // namespace moe

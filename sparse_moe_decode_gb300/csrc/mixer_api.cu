@@ -16,7 +16,7 @@ constexpr int kDeltaMaxSeqs = 65536;
 constexpr int kDeltaMaxHeads = 256;
 // Calls of so few token rows run token by token: one sequence (32 value heads
 // of 128) takes 14.6 us in the chunked form whatever its length up to 64, and
-// 3.8 us and 0.65 us for each further token in the recurrent one (13.6 us at 16).
+// 3.8 us and 0.65 us for each further token in the recurrent one (11.6 us at 16).
 constexpr int kRecurrentTokens = 16;
 constexpr int kRecurrentSeqs = 64;
 constexpr int kNormMaxWidth = 16384;

@@ -120,6 +120,24 @@ def test_chunk_long(env):
     run_chunk(env, make(env, 1500, (1, 2)), [1500], (1, 2), (128, 128))
 
 
+@pytest.mark.parametrize("heads", [(128, 256), (84, 252), (64, 256), (51, 255)])
+def test_chunk_shared_preparation(env, heads):
+    """Enough chunks and key heads for a block of the first kernel to serve two,
+    three or four value heads; one where their ratio has none of these."""
+    lens = [130, 0, 1, 64, 65, 3] + [0] * 13 + [2]
+    run_chunk(env, make(env, sum(lens), heads, (64, 64), seed=4), lens, heads, (64, 64))
+
+
+@pytest.mark.parametrize("dims", [(64, 128), (128, 64)])
+@pytest.mark.parametrize("lens", [[16], [1, 0, 3], [0, 5, 11, 0], [1] * 16, [0] * 63 + [9],
+                                  [0] * 64 + [9], [17], [8, 9]])
+def test_chunk_few_rows(env, lens, dims):
+    """Both sides of the rule that sends calls of few rows token by token."""
+    run_chunk(env, make(env, sum(lens), (2, 6), dims, seed=5), lens, (2, 6), dims, seed=2)
+    run_chunk(env, make(env, sum(lens), (2, 6), dims, seed=6), lens, (2, 6), dims, state=False,
+              in_place=True)
+
+
 @pytest.mark.parametrize("k_std", [0.05, 1e-6])
 def test_chunk_without_norm(env, k_std):
     """k as it is (small enough for the rule to contract), tiny k too."""
@@ -235,6 +253,27 @@ def test_bad_bounds_are_skipped(env, cu):
     assert m.status() == 0
     check_seq(s, slice(0, 50), torch.zeros_like(S1[0]), out, S1[0], dims)
     check_seq(s, slice(50, 120), torch.zeros_like(S1[0]), out, S1[2], dims)
+
+
+@pytest.mark.parametrize("cu", [[0, 8, 4, 12], [-1, 4, 6, 12], [0, 4, 8, 13], [0, 4, 1 << 30, 12]])
+def test_bad_bounds_of_few_rows_are_skipped(env, cu):
+    import torch
+    moe, dev = env
+    heads, dims = (1, 2), (64, 64)
+    s = make(env, 12, heads, dims)
+    m = mixer(env, heads, dims, 12, 3)
+    S1 = torch.full((3, 2, 64, 64), 7.0, device=dev)
+    out = torch.full((12, 2, 64), 3.0, dtype=torch.bfloat16, device=dev)
+    m.chunk(**s, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=dev), state_out=S1, out=out)
+    assert m.status() == moe.DEV_BAD_INDEX
+    assert (S1 == 7.0).all() and (out == 3.0).all()
+    m.clear_status()
+    # a slot out of range, and one that skips
+    slots = torch.tensor([2, 3, -1], dtype=torch.int32, device=dev)
+    m.chunk(**s, cu_seqlens=cu_of(env, [5, 4, 3]), slots=slots, state_out=S1, out=out)
+    assert m.status() == moe.DEV_BAD_INDEX
+    assert (S1[:2] == 7.0).all() and (out[5:] == 3.0).all()
+    check_seq(s, slice(0, 5), torch.zeros_like(S1[0]), out, S1[2], dims)
 
 
 @pytest.mark.parametrize("dims", [(64, 64), (64, 128), (128, 64), (128, 128)])
