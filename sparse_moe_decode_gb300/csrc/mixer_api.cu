@@ -14,11 +14,20 @@ namespace {
 constexpr int kDeltaMaxTokens = 1 << 20;
 constexpr int kDeltaMaxSeqs = 65536;
 constexpr int kDeltaMaxHeads = 256;
-// Calls of so few token rows run token by token: one sequence (32 value heads
-// of 128) takes 14.6 us in the chunked form whatever its length up to 64, and
-// 3.8 us and 0.65 us for each further token in the recurrent one (11.6 us at 16).
-constexpr int kRecurrentTokens = 16;
-constexpr int kRecurrentSeqs = 64;
+// Calls of few token rows run token by token: one sequence (32 value heads of
+// 128) takes 14.7 us in the chunked form whatever its length up to 64, and 4 to
+// 5 us and 0.5 us for each further token in the recurrent one (11.1 us at 16, 15.5
+// at 24).  Further sequences add 3.4 us each to the chunked form, where 4096
+// state rows take the SMs, and next to nothing to the recurrent one: 4 of 7
+// tokens 10.6 against 25.3 us, 12 of 4 15.2 against 51.5 us.  The lengths are
+// not known here; where one sequence has all of the rows and the others none,
+// the rule loses (28 rows 24.9 against 18.2 us, 48 rows 49.8 against 30.0 us).
+bool few_rows(const moe_delta_dims &d, int N, int B) {
+  constexpr int kMostSeqs = 64;  // each warp looks at all of their bounds
+  if (B > kMostSeqs) return false;
+  const int more = 4 * (B - 1) * d.v_heads * d.v_dim / 4096;
+  return N <= 16 + (more < 32 ? more : 32);
+}
 constexpr int kNormMaxWidth = 16384;
 constexpr int64_t kNormMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxStride = int64_t(1) << 31;  // elements: offsets stay far inside 63 bits
@@ -142,7 +151,7 @@ moe_status moe_delta_chunk(const moe_delta_dims *dims, const moe_delta_inputs *i
   if (B == 0) return MOE_OK;
   const DeltaSeqs seq = delta_seqs(cu_seqlens, N, B, N, slots, n_slots, state_in, state_out,
                                    workspace);
-  if (N <= kRecurrentTokens && B <= kRecurrentSeqs)
+  if (few_rows(*dims, N, B))
     return cuda_status(launch_delta_recurrent(*dims, *in, seq, out, out_ld,
                                               static_cast<cudaStream_t>(stream)));
   return cuda_status(launch_delta_chunk(*dims, *in, seq, workspace, out, out_ld,
