@@ -97,6 +97,8 @@ __device__ __forceinline__ int slot_base(const DeltaSeqs &s, int b) {
   return (s.cu_seqlens ? s.cu_seqlens[b] : b * s.T) / kC + b;
 }
 
+__device__ __forceinline__ int first_slot(const DeltaSeqRange &r, int b) { return r.start / kC + b; }
+
 // ------------------------------------------------------------------- prep
 
 constexpr int kTLd = kC + 4;     // row stride of T
@@ -215,15 +217,17 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
     }
   }
 
-  // whose chunk this is: the last sequence whose slots start at or before it
-  int lo = 0, hi = seq.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (slot_base(seq, mid) <= slot) lo = mid;
-    else hi = mid;
+  // whose chunk this is: the last sequence whose slots start at or before it,
+  // a 32nd of those left per round of loads
+  int b = 0, hi = seq.B;
+  while (hi - b > 1) {
+    const int step = (hi - b + 31) >> 5, at = b + lane * step;
+    const bool before = at < hi && slot_base(seq, at) <= slot;
+    b += step * (31 - __clz(__ballot_sync(kFull, before) | 1u));
+    hi = min(hi, b + step);
   }
-  const DeltaSeqRange r = delta_seq_range(seq, lo);
-  const int chunk = slot - slot_base(seq, lo);
+  const DeltaSeqRange r = delta_seq_range(seq, b);
+  const int chunk = slot - first_slot(r, b);
   if (!r.ok || chunk < 0 || chunk >= (r.len + kC - 1) / kC) return;
   const int left = min(kC, r.len - chunk * kC);  // tokens of this chunk
   const int64_t row0 = static_cast<int64_t>(r.start) + chunk * kC;
@@ -675,18 +679,18 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   const int tile = blockIdx.x % tiles;
   const int h = (blockIdx.x / tiles) % d.v_heads;
   const int b = blockIdx.x / tiles / d.v_heads;
-  early_begin();
-  if (reinterpret_cast<const uint32_t *>(ws)[kFlagWord]) return;
-  const DeltaSeqRange r = delta_seq_range(seq, b);
-  if (!r.ok) return;
-  const int hk = h / (d.v_heads / d.qk_heads);
-  const int chunks = (r.len + kC - 1) / kC;
-
   if (tid == 0) {
     *abort_flag = 0;
     for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s], 4);
     ptx::fence_mbar_init();
   }
+  early_begin();
+  // (all of these loads are under way before the first is looked at)
+  const uint32_t bad = reinterpret_cast<const uint32_t *>(ws)[kFlagWord];
+  const DeltaSeqRange r = delta_seq_range(seq, b);
+  if (bad || !r.ok) return;
+  const int hk = h / (d.v_heads / d.qk_heads);
+  const int chunks = (r.len + kC - 1) / kC;
   __syncthreads();
 
   // Chain warps 2 g, 2 g + 1 (half of the key channels each), output warps
@@ -991,7 +995,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   static_assert(2 * kGroups == 4, "an output warp for each copy of a chunk");
   const int copy = warp - kHalves * kGroups;
   const bool into_b = copy & 2, of_head = copy & 1;
-  const size_t base = slot_base(seq, b);
+  const size_t base = first_slot(r, b);
   const uint8_t *from = of_head ? ws_head + (base * d.v_heads + h) * kHeadBlob + (into_b ? kPartA : 0)
                                 : ws_key + (base * d.qk_heads + hk) * kKeyBlob<DK> + (into_b ? kKeyTile : 0);
   const size_t from_step = of_head ? static_cast<size_t>(d.v_heads) * kHeadBlob

@@ -16,6 +16,7 @@ struct DeltaSeqRange {
 // sets MOE_DEV_BAD_INDEX.
 __device__ __forceinline__ DeltaSeqRange delta_seq_range(const DeltaSeqs &s, int b) {
   DeltaSeqRange r;
+  r.slot = s.slots ? s.slots[b] : b;
   if (s.cu_seqlens) {
     const int lo = s.cu_seqlens[b], hi = s.cu_seqlens[b + 1];
     r.ok = lo >= 0 && lo <= hi && hi <= s.N;
@@ -26,7 +27,6 @@ __device__ __forceinline__ DeltaSeqRange delta_seq_range(const DeltaSeqs &s, int
     r.start = b * s.T;
     r.len = s.T;
   }
-  r.slot = s.slots ? s.slots[b] : b;
   if (!r.ok || r.slot >= s.n_slots) {
     r.ok = false;
     set_status(s.status, MOE_DEV_BAD_INDEX);
