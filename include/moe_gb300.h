@@ -327,9 +327,11 @@ size_t moe_delta_workspace_bytes(const moe_delta_dims *dims, int N, int B);
  * must not share a slot.  A sequence whose slot is negative is skipped, its
  * out rows and state left as they were; so is one whose slot is >= n_slots,
  * and that sets MOE_DEV_BAD_INDEX.  If any bounds are not 0 <= start <= end
- * <= N, MOE_DEV_BAD_INDEX is set and no out row or state is written.  out row t lies at out + t * out_ld as [Hv][v_dim] bf16
- * (16-byte aligned, out_ld a multiple of 8) and must not overlap the inputs.
- * N <= 2^20, B <= 65536.  A value that is not finite makes its head's state,
+ * <= N, MOE_DEV_BAD_INDEX is set and no out row or state is written.  out row
+ * t lies at out + t * out_ld as [Hv][v_dim] bf16 (16-byte aligned, out_ld a
+ * multiple of 8) and must not overlap the inputs.  N <= 2^20, B <= 65536.
+ * Calls of few rows are worked on token by token, so that a sequence's last
+ * digits can depend on the size of the call it is part of.  A value that is not finite makes its head's state,
  * and that head's outputs within the same run of 64 tokens and after it,
  * not finite; other heads and sequences do not see it. */
 moe_status moe_delta_chunk(const moe_delta_dims *dims, const moe_delta_inputs *in, int N,

@@ -68,6 +68,7 @@ constexpr int kHeadBlob = kPartA + kPartB;
 constexpr int kHeader = 256;      // status word, flags
 constexpr int kFlagWord = 16;     // header word: some bound of the call is bad
 constexpr int kPrepThreads = 256;
+constexpr int kPrepCtas = 3;      // of the first kernel on an SM
 
 template <int DK>
 constexpr int kKeyBlob = 2 * kC * DK * 2;  // per (chunk, key head): k, then q, as fp16
@@ -190,8 +191,16 @@ __device__ __forceinline__ float warp_max_pos(float v) {
 // One CTA per chunk and key head, for `heads` of the value heads that read
 // it.  Warps 0..3 take k (k k^T, L, T's diagonal blocks), warps 4..7 take q
 // (q k^T, P), 16 tokens each.
+//
+// Bound by the instructions it issues (0.6 per cycle and scheduler, 84 us for
+// the 4096 chunks and heads of 8192 tokens, where it moves 1.8 TB/s): the tensor
+// pipe is active for 16 % of the time; the inverse, the decays of the triangles
+// and the conversions are the rest.  80 registers leave three CTAs an SM, which wait for
+// barriers in turn; two CTAs with 128 took the same time.  The products wait
+// in shared memory, in the place of k and q: kept in registers they spilled
+// (2048 tokens 97 against 93 us).
 template <int DK>
-__global__ void __launch_bounds__(kPrepThreads, 3)
+__global__ void __launch_bounds__(kPrepThreads, kPrepCtas)
 delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int heads, uint8_t *ws,
                   uint8_t *ws_key, uint8_t *ws_head) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -1167,10 +1176,6 @@ cudaError_t launch_chain(const moe_delta_dims &d, const moe_delta_inputs &in, co
                       tc_wait_budget_ns());
 }
 
-// Chunks times key heads from which a CTA of the first kernel serves several of
-// the value heads of its key head.
-constexpr size_t kPrepShare = 1000;
-
 template <int DK>
 cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const DeltaSeqs &seq,
                    uint8_t *ws, moe_bf16 *out, int64_t out_ld, cudaStream_t s) {
@@ -1182,8 +1187,13 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
   cudaError_t e = allow_smem(delta_prep_kernel<DK>, kSmem, done);
   if (e != cudaSuccess) return e;
   const int ratio = d.v_heads / d.qk_heads;
+  // A CTA serves several of the value heads of its key head (and forms k k^T
+  // and q k^T once for them) when there are enough to fill the SMs so: 8192
+  // tokens take 314 us with two heads of 32 to a CTA, 330 with one, 13 sequences
+  // of 6007 tokens 244 and 259, 2048 tokens 89.5 and 90.3; of 67 tokens,
+  // 20.6 and 18.6.
   int heads = 1;
-  if (slots * d.qk_heads >= kPrepShare)
+  if (slots * d.qk_heads >= static_cast<size_t>(kPrepCtas * tc_sm_count()))
     for (int n = 2; n <= kPrepHeads; ++n)
       if (ratio % n == 0) heads = n;
   const dim3 grid(static_cast<unsigned>(slots), d.v_heads / heads);
