@@ -65,8 +65,13 @@ enum { kGamma, kTau, kDUp, kCMax };  // of kVecMisc
 constexpr int kPartA = 2 * kTri + kVecsA * kC * 4;
 constexpr int kPartB = kTri + kVecsB * kC * 4;
 constexpr int kHeadBlob = kPartA + kPartB;
-constexpr int kHeader = 256;      // status word, flags
-constexpr int kFlagWord = 16;     // header word: some bound of the call is bad
+constexpr int kHeader = 256;      // status word, and these words
+enum {
+  kFlagWord = 16,  // some bound of the call is bad: it does nothing
+  kCountWord,      // sequences that have tokens, the first records of the list
+  kEmptyWord,      // sequences without, the last ones
+  kNextWord,       // pieces of work that the chain's CTAs have asked for
+};
 constexpr int kPrepThreads = 256;
 constexpr int kPrepCtas = 3;      // of the first kernel on an SM
 
@@ -188,6 +193,48 @@ __device__ __forceinline__ float warp_max_pos(float v) {
   return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(v)));
 }
 
+// What the second kernel has to do, by one CTA: a record {first row, tokens,
+// state slot, first chunk slot} per sequence, those with tokens from the front
+// (of 256 at a time the longest first), those without from the back.  A call
+// with a bad bound does nothing.
+__device__ void list_sequences(const DeltaSeqs &seq, uint32_t *head, int4 *list, int *lens) {
+  const int tid = threadIdx.x;
+  int count = 0, empty = 0;
+  bool bad = false;
+  for (int b0 = 0; b0 < seq.B; b0 += kPrepThreads) {
+    const int b = b0 + tid;
+    DeltaSeqRange r{};
+    int len = -1;
+    if (b < seq.B) {
+      if (seq.cu_seqlens) {
+        const int lo = seq.cu_seqlens[b], hi = seq.cu_seqlens[b + 1];
+        bad |= lo < 0 || lo > hi || hi > seq.N;
+      }
+      r = delta_seq_range(seq, b);
+      if (r.ok) len = r.len;
+    }
+    lens[tid] = len;
+    const int full = __syncthreads_count(len > 0), none = __syncthreads_count(len == 0);
+    if (len >= 0) {
+      int rank = 0;
+      for (int i = 0; i < min(kPrepThreads, seq.B - b0); ++i) {
+        const int other = lens[i];
+        rank += (len > 0 && other > len) || (other == len && i < tid);
+      }
+      list[len > 0 ? count + rank : seq.B - 1 - empty - rank] =
+          make_int4(r.start, len, r.slot, first_slot(r, b));
+    }
+    count += full, empty += none;
+    __syncthreads();
+  }
+  bad = __syncthreads_or(bad);
+  if (tid == 0) {
+    head[kFlagWord] = bad, head[kCountWord] = count, head[kEmptyWord] = empty;
+    head[kNextWord] = 0;
+    if (bad) set_status(seq.status, MOE_DEV_BAD_INDEX);
+  }
+}
+
 // One CTA per chunk and key head, for `heads` of the value heads that read
 // it.  Warps 0..3 take k (k k^T, L, T's diagonal blocks), warps 4..7 take q
 // (q k^T, P), 16 tokens each.
@@ -202,28 +249,19 @@ __device__ __forceinline__ float warp_max_pos(float v) {
 template <int DK>
 __global__ void __launch_bounds__(kPrepThreads, kPrepCtas)
 delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int heads, uint8_t *ws,
-                  uint8_t *ws_key, uint8_t *ws_head) {
+                  int4 *list, uint8_t *ws_key, uint8_t *ws_head) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   PrepSmem<DK> &sm = *reinterpret_cast<PrepSmem<DK> *>(smem_raw);
   __shared__ float red[kPrepThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ratio = d.v_heads / d.qk_heads;
-  const int slot = blockIdx.x, h0 = blockIdx.y * heads, hk = h0 / ratio;
+  const int slot = static_cast<int>(blockIdx.x) - 1, h0 = blockIdx.y * heads, hk = h0 / ratio;
 
   early_begin();
-  if (slot == 0 && h0 == 0) {
-    // one CTA looks at every bound: a call with a bad one does nothing
-    bool bad = false;
-    if (seq.cu_seqlens)
-      for (int b = tid; b < seq.B; b += kPrepThreads) {
-        const int lo = seq.cu_seqlens[b], hi = seq.cu_seqlens[b + 1];
-        bad |= lo < 0 || lo > hi || hi > seq.N;
-      }
-    bad = __syncthreads_or(bad);
-    if (tid == 0) {
-      reinterpret_cast<uint32_t *>(ws)[kFlagWord] = bad;
-      if (bad) set_status(seq.status, MOE_DEV_BAD_INDEX);
-    }
+  if (slot < 0) {  // the first CTAs have no chunk
+    if (blockIdx.y == 0)
+      list_sequences(seq, reinterpret_cast<uint32_t *>(ws), list, reinterpret_cast<int *>(smem_raw));
+    return;
   }
 
   // whose chunk this is: the last sequence whose slots start at or before it,
@@ -614,6 +652,7 @@ struct Chain {
   // ninth would cost every one of them a third.  So the four output warps
   // bring in the rings' stages, one of a chunk's four copies each (issuing a
   // bulk copy holds its thread for some 500 cycles).
+  static constexpr int kQueue = 8;
   static constexpr int kThreads = 32 * (kHalves + 2) * kGroups;
 
   // What the warps of a group hand one another.
@@ -671,8 +710,8 @@ __device__ __forceinline__ void get4(const uint4 *p, uint32_t (&v)[4]) {
 
 template <int DK>
 __global__ void __launch_bounds__(Chain<DK>::kThreads, 1)
-delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const uint8_t *ws,
-                   const uint8_t *ws_key, const uint8_t *ws_head, moe_bf16 *out, int64_t out_ld,
+delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t *ws,
+                   const int4 *list, const uint8_t *ws_key, const uint8_t *ws_head, moe_bf16 *out, int64_t out_ld,
                    unsigned long long budget_ns) {
   using C = Chain<DK>;
   using Group = typename C::Group;
@@ -682,24 +721,34 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   Group *groups = reinterpret_cast<Group *>(ring_b + kStages * C::kStageB);
   uint64_t *full = reinterpret_cast<uint64_t *>(groups + kGroups);
   int *abort_flag = reinterpret_cast<int *>(full + kStages), *fed_by = abort_flag + 1;
+  volatile int *queue = fed_by + 4;  // [kQueue]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tiles = d.v_dim / kRows;
-  const int tile = blockIdx.x % tiles;
-  const int h = (blockIdx.x / tiles) % d.v_heads;
-  const int b = blockIdx.x / tiles / d.v_heads;
   if (tid == 0) {
     *abort_flag = 0;
     for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s], 4);
     ptx::fence_mbar_init();
   }
+  // (all divisions by sizes are done before the wait, or a piece ahead)
+  const int tiles = d.v_dim / kRows, per = d.v_heads * tiles, ratio = d.v_heads / d.qk_heads;
+  const int seq_of = blockIdx.x / per;
+  int h = blockIdx.x / tiles % d.v_heads, row = blockIdx.x % tiles * kRows;
+  int key_head = h / ratio;
   early_begin();
-  // (all of these loads are under way before the first is looked at)
-  const uint32_t bad = reinterpret_cast<const uint32_t *>(ws)[kFlagWord];
-  const DeltaSeqRange r = delta_seq_range(seq, b);
-  if (bad || !r.ok) return;
-  const int hk = h / (d.v_heads / d.qk_heads);
-  const int chunks = (r.len + kC - 1) / kC;
+  // The work: kRows state rows of one head of one sequence are a piece, index
+  // (sequence of the list, head, rows).  A CTA's pieces number 0, 1 and 2 are
+  // given; for those after it asks, through output warp 0, which of them is
+  // next.  That warp publishes number k + 3 when it begins number k, so that
+  // all know it after that chunk's bar_x.
+  uint32_t *head = reinterpret_cast<uint32_t *>(ws);
+  const uint32_t bad = head[kFlagWord];
+  const int total = static_cast<int>(head[kCountWord]) * per;
+  const int4 first = list[seq_of];  // (meaningless past the total)
+  if (bad) return;
+  const int grid = static_cast<int>(gridDim.x);
+  const auto piece_at = [&](int k) {
+    return k < 3 ? static_cast<int>(blockIdx.x) + k * grid : queue[k % C::kQueue];
+  };
   __syncthreads();
 
   // Chain warps 2 g, 2 g + 1 (half of the key channels each), output warps
@@ -717,15 +766,28 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   Group &gs = groups[group];
   const int bar_x = 0, bar_y = 1 + 2 * group, bar_w = bar_y + 1, bar_out = 1 + 2 * kGroups;
   constexpr int kAll = C::kThreads, kGroup = 32 * (kHalves + 2);
-  const int dv0 = (tile * kGroups + group) * 16;
   const int g = lane >> 2, t = lane & 3;
   // B fragments of two n8 tiles from rows (plain) or columns (trans) of a tile
   const int b_row = (lane & 7) + ((lane >> 4) << 3), b_piece = (lane >> 3) & 1;
   const int bt_row = (lane & 7) + (((lane >> 3) & 1) << 3), bt_piece = lane >> 4;
 
   if (chain) {
-    const int64_t at = ((static_cast<int64_t>(r.slot) * d.v_heads + h) * d.v_dim + dv0 + g) * DK +
-                       part * C::kCols + 2 * t;
+    // The 16-token blocks whose x and u this warp forms.  u's block np takes
+    // np + 1 steps: blocks 0 and 3, and 1 and 2, make equal pairs.
+    const int own[2] = {part, 3 - part};
+    const auto owner = [](int np) { return min(np, 3 - np); };
+    int st = 0, index = piece_at(0);
+    int4 record = first;
+    if (index < total) bar_sync(bar_w, kGroup);  // the first chunk's operands are there
+    for (int k = 0; index < total; ++k) {
+    const int chunks = (record.y + kC - 1) / kC;
+    const int64_t at = ((static_cast<int64_t>(record.z) * d.v_heads + h) * d.v_dim + row + group * 16 + g) *
+                           DK + part * C::kCols + 2 * t;
+    index = piece_at(k + 1);
+    if (index < total) {
+      record = list[index / per];
+      h = index / tiles % d.v_heads, row = index % tiles * kRows;
+    }
     Acc S[2 * C::kSteps];
 #pragma unroll
     for (int n = 0; n < 2 * C::kSteps; ++n) {
@@ -735,10 +797,6 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
         S[n].low = *reinterpret_cast<const float2 *>(seq.state_in + at + 8 * DK + 8 * n);
       }
     }
-    // The 16-token blocks whose x and u this warp forms.  u's block np takes
-    // np + 1 steps: blocks 0 and 3, and 1 and 2, make equal pairs.
-    const int own[2] = {part, 3 - part};
-    const auto owner = [](int np) { return min(np, 3 - np); };
     float m0, m1, i0, i1;
     {
       float a0 = 0.0f, a1 = 0.0f;
@@ -750,8 +808,6 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
       pow2_scale(quad_max(a0), m0, i0);
       pow2_scale(quad_max(a1), m1, i1);
     }
-    if (chunks) bar_sync(bar_w, kGroup);
-    int st = 0;
     for (int c = 0; c < chunks; ++c) {
       const uint32_t kt = ptx::smem_u32(ring_a + st * C::kStageA), tt = kt + kKeyTile;
       const float *vec =
@@ -943,6 +999,19 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
         *reinterpret_cast<float2 *>(seq.state_out + at + 8 * DK + 8 * n) = S[n].low;
       }
     }
+    }
+    // sequences without tokens: their states as they are
+    if (!seq.state_out || seq.state_out == seq.state_in) return;
+    const int empty = static_cast<int>(head[kEmptyWord]) * per;
+    for (int e = blockIdx.x; e < empty; e += grid) {
+      const int slot = list[seq.B - 1 - e / per].z;
+      const int64_t from = ((static_cast<int64_t>(slot) * d.v_heads + e / tiles % d.v_heads) * d.v_dim +
+                            e % tiles * kRows) * DK;
+      for (int i = 4 * tid; i < kRows * DK; i += 4 * 32 * kHalves * kGroups)
+        *reinterpret_cast<float4 *>(seq.state_out + from + i) =
+            seq.state_in ? *reinterpret_cast<const float4 *>(seq.state_in + from + i)
+                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
     return;
   }
 
@@ -952,32 +1021,19 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   const int side = (warp - kHalves * kGroups) & 1;
   const int own[2] = {side, 3 - side};
   const int my_row = lane >> 1;  // of a block, and the half row this lane copies
-  const int64_t row0 = r.start + my_row;
   const uint32_t v_smem = ptx::smem_u32(gs.v[0]), v_to = v_smem + row32_at(my_row, lane & 1);
   const uint32_t v_at = v_smem + row32_at(b_row, b_piece);
-  const moe_bf16 *v_src = in.v + row0 * in.v_ld + h * d.v_dim + dv0 + (lane & 1) * 8;
-  const auto fetch_v = [&](int c) {  // the own blocks of chunk c, zeros past the end
-    if (c < chunks) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const bool live = c * kC + 16 * own[j] + my_row < r.len;
-        cp_async16(v_to + (c % 3) * kC * 32 + own[j] * 16 * 32,
-                   live ? v_src + 16 * own[j] * in.v_ld : in.v, live);
-      }
-      v_src += kC * in.v_ld;
-    }
-    cp_async_commit();
-  };
   // The only wait for a chunk's operands: bar_w passes it on.  One that gave
   // up is not repeated; the loops run to their end on whatever the ring holds,
   // so that all warps pass every barrier.
   bool dead = false;
   const auto wait_full = [&](int stage, uint32_t parity) {
-    if (!dead) dead = !ptx::mbar_wait(&full[stage], parity, abort_flag, budget_ns);
+    if (!dead)
+      dead = __any_sync(kFull, !ptx::mbar_wait(&full[stage], parity, abort_flag, budget_ns));
   };
-  // beta v of chunk c (the last copy but two) and its largest per row
-  const auto values = [&](int c, int stage) {
-    cp_async_wait<2>();
+  // beta v of a chunk (the last copy but one) and its largest per row
+  const auto values = [&](int slot, int stage) {
+    cp_async_wait<1>();
     __syncwarp();
     const float *vec =
         reinterpret_cast<const float *>(ring_a + stage * C::kStageA + kKeyTile + 2 * kTri);
@@ -985,7 +1041,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       uint32_t vv[4];
-      ldsm4_t(vv, v_at + (c % 3) * kC * 32 + own[j] * 16 * 32);
+      ldsm4_t(vv, v_at + slot * kC * 32 + own[j] * 16 * 32);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const float2 be =
@@ -1004,40 +1060,111 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
   static_assert(2 * kGroups == 4, "an output warp for each copy of a chunk");
   const int copy = warp - kHalves * kGroups;
   const bool into_b = copy & 2, of_head = copy & 1;
-  const size_t base = first_slot(r, b);
-  const uint8_t *from = of_head ? ws_head + (base * d.v_heads + h) * kHeadBlob + (into_b ? kPartA : 0)
-                                : ws_key + (base * d.qk_heads + hk) * kKeyBlob<DK> + (into_b ? kKeyTile : 0);
   const size_t from_step = of_head ? static_cast<size_t>(d.v_heads) * kHeadBlob
                                    : static_cast<size_t>(d.qk_heads) * kKeyBlob<DK>;
   const uint32_t copy_bytes = !of_head ? kKeyTile : into_b ? kPartB : kPartA;
   const uint32_t to_step = into_b ? C::kStageB : C::kStageA;
   const uint32_t to = ptx::smem_u32(into_b ? ring_b : ring_a) + (of_head ? kKeyTile : 0);
   int fed = 0;  // chunks under way
-  const auto feed = [&](int stage) {
-    if (lane == 0) {
-      mbar_expect(&full[stage], copy_bytes);
-      bulk_load(to + stage * to_step, from, copy_bytes, &full[stage]);
+  // The next chunk to bring in, two before the one worked on: of piece number
+  // `ahead`, `left` tokens from its first on.  The record of the piece after it
+  // is under way; of those brought in but not yet begun (two at most), their
+  // tokens and where their outputs go wait in line.
+  int ahead = -1, left = 0, index = piece_at(0);
+  int4 record = first;
+  const uint8_t *from = nullptr;
+  const moe_bf16 *v_src = nullptr, *v_now = nullptr;  // v_now, v_left: the chunk brought in last
+  int v_left = 0;
+  moe_bf16 *line_dst[2] = {};
+  int line_len[2] = {};
+  const auto bring_in = [&](int stage, bool alive) {
+    if (left <= 0) {
+      if (index < total) {
+        ++ahead;
+        const int dv = row + group * 16;
+        const bool second = line_len[0] > 0;
+        moe_bf16 *dst = out + (static_cast<int64_t>(record.x) + my_row) * out_ld + h * d.v_dim + dv +
+                        (lane & 1) * 8;
+        (second ? line_dst[1] : line_dst[0]) = dst;
+        (second ? line_len[1] : line_len[0]) = record.y;
+        const size_t base = record.w;
+        left = record.y;
+        from = of_head ? ws_head + (base * d.v_heads + h) * kHeadBlob + (into_b ? kPartA : 0)
+                       : ws_key + (base * d.qk_heads + key_head) * kKeyBlob<DK> + (into_b ? kKeyTile : 0);
+        v_src = in.v + (static_cast<int64_t>(record.x) + my_row) * in.v_ld + h * d.v_dim + dv +
+                (lane & 1) * 8;
+        // the group's state, a line of 128 bytes each, on its way into L2
+        constexpr int kLines = DK / 32;
+        const int line = 32 * side + lane;
+        if (ahead > 0 && seq.state_in && line < 16 * kLines)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(
+              seq.state_in + ((static_cast<int64_t>(record.z) * d.v_heads + h) * d.v_dim + dv +
+                              line / kLines) * DK + line % kLines * 32));
+        index = piece_at(ahead + 1);
+        if (index < total) {
+          record = list[index / per];
+          h = index / tiles % d.v_heads, row = index % tiles * kRows, key_head = h / ratio;
+        }
+      }
     }
-    from += from_step;
-    ++fed;
+    v_now = v_src, v_left = left;
+    if (left > 0) {
+      if (alive) {
+        if (lane == 0) {
+          mbar_expect(&full[stage], copy_bytes);
+          bulk_load(to + stage * to_step, from, copy_bytes, &full[stage]);
+        }
+        ++fed;
+      }
+      v_src += kC * in.v_ld, from += from_step, left -= kC;
+    }
   };
-  int st = 0;
+  // the own blocks of its values, zeros past the end
+  const auto fetch_v = [&](int slot) {
+    if (v_left > 0) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool live = 16 * own[j] + my_row < v_left;
+        cp_async16(v_to + slot * kC * 32 + own[j] * 16 * 32,
+                   live ? v_now + 16 * own[j] * in.v_ld : in.v, live);
+      }
+    }
+    cp_async_commit();
+  };
+  int st = 0;  // stage of the rings, and slot of the values
+  static_assert(kStages == 3, "as many as slots of the values");
   uint32_t parity = 0;
-  if (chunks) {
-    for (int c = 0; c < min(chunks, kStages - 1); ++c) feed(c);
+  // the piece worked on: its number, its tokens from this chunk on
+  int number = -1, now = 0;
+  moe_bf16 *o_dst = nullptr;
+  const bool asks = copy == 0 && lane == 0;
+  int asked = total;  // its answer: piece number + 3
+  if (asks && total > 3 * grid) asked = 3 * grid + atomicAdd(&head[kNextWord], 1u);
+  const auto begin_next = [&] {
+    now = line_len[0], o_dst = line_dst[0];
+    line_len[0] = line_len[1], line_dst[0] = line_dst[1], line_len[1] = 0;
+    ++number;
+    if (asks) {
+      queue[(number + 3) % C::kQueue] = asked;
+      if (asked < total) asked = 3 * grid + atomicAdd(&head[kNextWord], 1u);
+    }
+  };
+  if (piece_at(0) < total) {
+    bring_in(0, true);
     fetch_v(0);
-    fetch_v(1);
+    bring_in(1, true);
+    begin_next();
     wait_full(0, 0);
     bar_sync(bar_w, kGroup);
   }
   const uint32_t o_at = ptx::smem_u32(gs.o) + row32_at(b_row, b_piece);
   const uint8_t *o_from = gs.o + row32_at(my_row, lane & 1);
-  moe_bf16 *o_dst = out + row0 * out_ld + h * d.v_dim + dv0 + (lane & 1) * 8;
-  for (int c = 0; c < chunks; ++c) {
+  for (int n = 0; now > 0; ++n) {
     const uint32_t qt = ptx::smem_u32(ring_b + st * C::kStageB), pt = qt + kKeyTile;
     const float *vec = reinterpret_cast<const float *>(ring_b + st * C::kStageB + kKeyTile + kTri);
-    fetch_v(c + 2);
-    values(c, st);
+    const int next = st + 1 == kStages ? 0 : st + 1;
+    fetch_v(next);
+    values(st, st);
     uint32_t bb[2][2][4];
     const auto load_q = [&](int s) {
 #pragma unroll
@@ -1089,13 +1216,11 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
         O[j][q].top = mul2(mul2(O[j][q].top, both(most.x)), oq);
         O[j][q].low = mul2(mul2(O[j][q].low, both(most.y)), oq);
       }
-    const int next = st + 1 == kStages ? 0 : st + 1;
     const uint32_t next_parity = next ? parity : parity ^ 1;
-    if (c + 1 < chunks) wait_full(next, next_parity);
+    if (fed > n + 1) wait_full(next, next_parity);
     bar_sync(bar_w, kGroup);
-    // chunk c - 1's stage is free (bar_x)
-    if (c + 2 < chunks && !*reinterpret_cast<volatile int *>(abort_flag))
-      feed(st == 0 ? kStages - 1 : st - 1);
+    // the previous chunk's stage is free (bar_x)
+    bring_in(st == 0 ? kStages - 1 : st - 1, !__any_sync(kFull, *reinterpret_cast<volatile int *>(abort_flag)));
     const float2 ui = gs.u_inv[lane];
     Acc I[2][2] = {};
     uint32_t uf[4][4];
@@ -1125,10 +1250,11 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, const u
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      if (c * kC + 16 * own[j] + my_row < r.len)
+      if (16 * own[j] + my_row < now)
         *reinterpret_cast<uint4 *>(o_dst + 16 * own[j] * out_ld) =
             *reinterpret_cast<const uint4 *>(o_from + own[j] * 16 * 32);
-    o_dst += kC * out_ld;
+    o_dst += kC * out_ld, now -= kC;
+    if (now <= 0) begin_next();
     st = next, parity = next_parity;
     __syncwarp();
   }
@@ -1163,24 +1289,27 @@ cudaError_t allow_smem(F kernel, int bytes, std::atomic<uint64_t> &done) {
 
 template <int DK>
 cudaError_t launch_chain(const moe_delta_dims &d, const moe_delta_inputs &in, const DeltaSeqs &seq,
-                         const uint8_t *ws, const uint8_t *ws_key, const uint8_t *ws_head,
+                         uint8_t *ws, const int4 *list, const uint8_t *ws_key, const uint8_t *ws_head,
                          moe_bf16 *out, int64_t out_ld, cudaStream_t s) {
   using C = Chain<DK>;
   static_assert(C::kSmem <= 227 * 1024, "shared memory of one SM");
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(delta_chain_kernel<DK>, C::kSmem, done);
   if (e != cudaSuccess) return e;
-  const int64_t grid = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / kRows);
-  return launch_early(delta_chain_kernel<DK>, dim3(static_cast<unsigned>(grid)),
-                      C::kThreads, C::kSmem, s, d, in, seq, ws, ws_key, ws_head, out, out_ld,
-                      tc_wait_budget_ns());
+  const int pieces = seq.B * d.v_heads * (d.v_dim / kRows), sms = tc_sm_count();
+  return launch_early(delta_chain_kernel<DK>, dim3(pieces < sms ? pieces : sms), C::kThreads, C::kSmem,
+                      s, d, in, seq, ws, list, ws_key, ws_head, out, out_ld, tc_wait_budget_ns());
 }
+
+// The sequences' records, up to a whole 256 bytes.
+size_t list_bytes(int B) { return (static_cast<size_t>(B) * sizeof(int4) + 255) / 256 * 256; }
 
 template <int DK>
 cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const DeltaSeqs &seq,
                    uint8_t *ws, moe_bf16 *out, int64_t out_ld, cudaStream_t s) {
   const size_t slots = static_cast<size_t>(seq.N) / kC + seq.B;
-  uint8_t *ws_key = ws + kHeader;
+  int4 *list = reinterpret_cast<int4 *>(ws + kHeader);
+  uint8_t *ws_key = ws + kHeader + list_bytes(seq.B);
   uint8_t *ws_head = ws_key + slots * d.qk_heads * kKeyBlob<DK>;
   constexpr int kSmem = sizeof(PrepSmem<DK>);
   static std::atomic<uint64_t> done{0};
@@ -1196,11 +1325,11 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
   if (slots * d.qk_heads >= static_cast<size_t>(kPrepCtas * tc_sm_count()))
     for (int n = 2; n <= kPrepHeads; ++n)
       if (ratio % n == 0) heads = n;
-  const dim3 grid(static_cast<unsigned>(slots), d.v_heads / heads);
+  const dim3 grid(static_cast<unsigned>(slots) + 1, d.v_heads / heads);
   e = launch_early(delta_prep_kernel<DK>, grid, kPrepThreads, kSmem, s, d, in, seq, heads, ws,
-                   ws_key, ws_head);
+                   list, ws_key, ws_head);
   if (e != cudaSuccess) return e;
-  return launch_chain<DK>(d, in, seq, ws, ws_key, ws_head, out, out_ld, s);
+  return launch_chain<DK>(d, in, seq, ws, list, ws_key, ws_head, out, out_ld, s);
 }
 
 }  // namespace
@@ -1208,7 +1337,7 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
 size_t delta_chunk_workspace(const moe_delta_dims &d, int N, int B) {
   const size_t slots = static_cast<size_t>(N) / kC + B;
   const size_t key = d.qk_dim == 128 ? kKeyBlob<128> : kKeyBlob<64>;
-  return kHeader + slots * (d.qk_heads * key + static_cast<size_t>(d.v_heads) * kHeadBlob);
+  return kHeader + list_bytes(B) + slots * (d.qk_heads * key + static_cast<size_t>(d.v_heads) * kHeadBlob);
 }
 
 cudaError_t launch_delta_chunk(const moe_delta_dims &d, const moe_delta_inputs &in,
