@@ -292,7 +292,10 @@ moe_status moe_topk_merge(const int32_t *ids, const float *values, int T, int n_
  * g is the natural logarithm of the decay, g <= 0 (below -128, -inf included,
  * it counts as -128: the state is forgotten; growth is served as long as no
  * 64 consecutive g sum to more than 3).  Sums, states and
- * gates are fp32 (or better); out is rounded to bf16 once. */
+ * gates are fp32 (or better); out is rounded to bf16 once.  The prompt form
+ * takes fp32 operands as two fp16 terms: 22 bits of what is above 2^-17 of
+ * the largest value of the same 64 tokens and state row, and 2^-36 of that
+ * largest value below (token by token: fp32 throughout). */
 typedef struct {
   int32_t qk_heads; /* Hk                                                 */
   int32_t v_heads;  /* Hv: a multiple of Hk, <= 256                       */

@@ -29,14 +29,16 @@
 // eighth of the rounding to come).
 //
 // What bounds it (GB300, 32 value heads of 128 x 128 on 16 key heads).  A chunk
-// of the chain takes 1.76 us on whatever SM it runs, so one prompt of 8192
-// tokens takes 225 us there and 84 us in the preparation, of 31 us for the
-// bytes; 13 sequences of 6007 tokens in all, 177 us on 152 SMs, against 170 us
-// if every SM had work to the end.  Measured and slower: four chain warps a group
-// with a quarter of the channels each (393 against 338 us for 8192 tokens then),
-// one output warp a group (369), a ninth warp for the copies (446: 168 registers
-// a thread), and CTAs that stay and take one piece of the work after the other
-// (321 against 313 us, and 263 against 246 for the 13 sequences).
+// of the chain takes 1.73 us on whatever SM it runs, so one prompt of 8192
+// tokens takes 222 us there and 83 us in the preparation, of 31 us for the
+// bytes.  A CTA's pieces of work (32 state rows of one sequence) follow one
+// another, longest sequences first, with the next one's chunks, values and
+// state on their way during the last one's chunks: 240 us for 13 sequences of
+// 6007 tokens in all and 113 us for 32 of 64, against 244 and 137 us with a
+// CTA for each piece.  (Each in a fixed order of pieces was slower, 263 us for
+// the 13.)  Measured and slower: four chain warps a group with a quarter of the
+// channels each (393 against 338 us for 8192 tokens then), one output warp a
+// group (369), and a ninth warp for the copies (446: 168 registers a thread).
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -103,7 +105,9 @@ __device__ __forceinline__ int slot_base(const DeltaSeqs &s, int b) {
   return (s.cu_seqlens ? s.cu_seqlens[b] : b * s.T) / kC + b;
 }
 
-__device__ __forceinline__ int first_slot(const DeltaSeqRange &r, int b) { return r.start / kC + b; }
+__device__ __forceinline__ int first_slot(const DeltaSeqRange &r, int b) {
+  return r.start / kC + b;
+}
 
 // ------------------------------------------------------------------- prep
 
@@ -260,7 +264,8 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
   early_begin();
   if (slot < 0) {  // the first CTAs have no chunk
     if (blockIdx.y == 0)
-      list_sequences(seq, reinterpret_cast<uint32_t *>(ws), list, reinterpret_cast<int *>(smem_raw));
+      list_sequences(seq, reinterpret_cast<uint32_t *>(ws), list,
+                     reinterpret_cast<int *>(smem_raw));
     return;
   }
 
@@ -711,8 +716,8 @@ __device__ __forceinline__ void get4(const uint4 *p, uint32_t (&v)[4]) {
 template <int DK>
 __global__ void __launch_bounds__(Chain<DK>::kThreads, 1)
 delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t *ws,
-                   const int4 *list, const uint8_t *ws_key, const uint8_t *ws_head, moe_bf16 *out, int64_t out_ld,
-                   unsigned long long budget_ns) {
+                   const int4 *list, const uint8_t *ws_key, const uint8_t *ws_head, moe_bf16 *out,
+                   int64_t out_ld, unsigned long long budget_ns) {
   using C = Chain<DK>;
   using Group = typename C::Group;
   constexpr int kKeyTile = kKeyBlob<DK> / 2, kStages = C::kStages;
@@ -743,6 +748,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
   uint32_t *head = reinterpret_cast<uint32_t *>(ws);
   const uint32_t bad = head[kFlagWord];
   const int total = static_cast<int>(head[kCountWord]) * per;
+  const int empty = static_cast<int>(head[kEmptyWord]) * per;
   const int4 first = list[seq_of];  // (meaningless past the total)
   if (bad) return;
   const int grid = static_cast<int>(gridDim.x);
@@ -780,233 +786,233 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
     int4 record = first;
     if (index < total) bar_sync(bar_w, kGroup);  // the first chunk's operands are there
     for (int k = 0; index < total; ++k) {
-    const int chunks = (record.y + kC - 1) / kC;
-    const int64_t at = ((static_cast<int64_t>(record.z) * d.v_heads + h) * d.v_dim + row + group * 16 + g) *
-                           DK + part * C::kCols + 2 * t;
-    index = piece_at(k + 1);
-    if (index < total) {
-      record = list[index / per];
-      h = index / tiles % d.v_heads, row = index % tiles * kRows;
-    }
-    Acc S[2 * C::kSteps];
-#pragma unroll
-    for (int n = 0; n < 2 * C::kSteps; ++n) {
-      S[n].top = S[n].low = both(0.0f);
-      if (seq.state_in) {
-        S[n].top = *reinterpret_cast<const float2 *>(seq.state_in + at + 8 * n);
-        S[n].low = *reinterpret_cast<const float2 *>(seq.state_in + at + 8 * DK + 8 * n);
+      const int chunks = (record.y + kC - 1) / kC;
+      const int64_t line = (static_cast<int64_t>(record.z) * d.v_heads + h) * d.v_dim + row;
+      const int64_t at = (line + group * 16 + g) * DK + part * C::kCols + 2 * t;
+      index = piece_at(k + 1);
+      if (index < total) {
+        record = list[index / per];
+        h = index / tiles % d.v_heads, row = index % tiles * kRows;
       }
-    }
-    float m0, m1, i0, i1;
-    {
-      float a0 = 0.0f, a1 = 0.0f;
+      Acc S[2 * C::kSteps];
 #pragma unroll
       for (int n = 0; n < 2 * C::kSteps; ++n) {
-        a0 = max3_abs(a0, S[n].top.x, S[n].top.y);
-        a1 = max3_abs(a1, S[n].low.x, S[n].low.y);
+        S[n].top = S[n].low = both(0.0f);
+        if (seq.state_in) {
+          S[n].top = *reinterpret_cast<const float2 *>(seq.state_in + at + 8 * n);
+          S[n].low = *reinterpret_cast<const float2 *>(seq.state_in + at + 8 * DK + 8 * n);
+        }
       }
-      pow2_scale(quad_max(a0), m0, i0);
-      pow2_scale(quad_max(a1), m1, i1);
-    }
-    for (int c = 0; c < chunks; ++c) {
-      const uint32_t kt = ptx::smem_u32(ring_a + st * C::kStageA), tt = kt + kKeyTile;
-      const float *vec =
-          reinterpret_cast<const float *>(ring_a + st * C::kStageA + kKeyTile + 2 * kTri);
-      gs.s_inv[part][lane] = make_float2(i0, i1);
-      // this warp's share of X^T = S k^T (16 value channels x 64 tokens)
-      Acc X[8] = {};
+      float m0, m1, i0, i1;
+      {
+        float a0 = 0.0f, a1 = 0.0f;
 #pragma unroll
-      for (int s = 0; s < C::kSteps; ++s) {
-        uint32_t hi[4], lo[4], bb[4][4];
+        for (int n = 0; n < 2 * C::kSteps; ++n) {
+          a0 = max3_abs(a0, S[n].top.x, S[n].top.y);
+          a1 = max3_abs(a1, S[n].low.x, S[n].low.y);
+        }
+        pow2_scale(quad_max(a0), m0, i0);
+        pow2_scale(quad_max(a1), m1, i1);
+      }
+      for (int c = 0; c < chunks; ++c) {
+        const uint32_t kt = ptx::smem_u32(ring_a + st * C::kStageA), tt = kt + kKeyTile;
+        const float *vec =
+            reinterpret_cast<const float *>(ring_a + st * C::kStageA + kKeyTile + 2 * kTri);
+        gs.s_inv[part][lane] = make_float2(i0, i1);
+        // this warp's share of X^T = S k^T (16 value channels x 64 tokens)
+        Acc X[8] = {};
+#pragma unroll
+        for (int s = 0; s < C::kSteps; ++s) {
+          uint32_t hi[4], lo[4], bb[4][4];
+#pragma unroll
+          for (int np = 0; np < 4; ++np)
+            ldsm4(bb[np],
+                  kt + tile_at<DK>(16 * np + b_row, part * (C::kCols / 8) + 2 * s + b_piece));
+          split_frag(S[2 * s], S[2 * s + 1], m0, m1, hi, lo);
+          put4(&gs.s_frag[part * C::kSteps + s][lane], hi);
+#pragma unroll
+          for (int np = 0; np < 4; ++np) {
+            mma16(X[2 * np], hi, bb[np][0], bb[np][1]);
+            mma16(X[2 * np + 1], hi, bb[np][2], bb[np][3]);
+          }
+#pragma unroll
+          for (int np = 0; np < 4; ++np) {
+            mma16(X[2 * np], lo, bb[np][0], bb[np][1]);
+            mma16(X[2 * np + 1], lo, bb[np][2], bb[np][3]);
+          }
+        }
+        Acc mine[2][2];
 #pragma unroll
         for (int np = 0; np < 4; ++np)
-          ldsm4(bb[np], kt + tile_at<DK>(16 * np + b_row, part * (C::kCols / 8) + 2 * s + b_piece));
-        split_frag(S[2 * s], S[2 * s + 1], m0, m1, hi, lo);
-        put4(&gs.s_frag[part * C::kSteps + s][lane], hi);
 #pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          mma16(X[2 * np], hi, bb[np][0], bb[np][1]);
-          mma16(X[2 * np + 1], hi, bb[np][2], bb[np][3]);
-        }
+          for (int q = 0; q < 2; ++q) {
+            Acc &x = X[2 * np + q];
+            x.top = mul2(x.top, both(i0)), x.low = mul2(x.low, both(i1));
+            if (owner(np) != part)
+              gs.x_part[np][q][lane] = make_float4(x.top.x, x.top.y, x.low.x, x.low.y);
 #pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          mma16(X[2 * np], lo, bb[np][0], bb[np][1]);
-          mma16(X[2 * np + 1], lo, bb[np][2], bb[np][3]);
-        }
-      }
-      Acc mine[2][2];
-#pragma unroll
-      for (int np = 0; np < 4; ++np)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          Acc &x = X[2 * np + q];
-          x.top = mul2(x.top, both(i0)), x.low = mul2(x.low, both(i1));
-          if (owner(np) != part)
-            gs.x_part[np][q][lane] = make_float4(x.top.x, x.top.y, x.low.x, x.low.y);
+            for (int j = 0; j < 2; ++j)
+              if (np == own[j]) mine[j][q] = x;
+          }
+        // T's fragments of the own blocks, a step ahead of their use
+        uint32_t th[2][2][4], tl[2][2][4];
+        const auto load_t = [&](int s) {
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            if (np == own[j]) mine[j][q] = x;
-        }
-      // T's fragments of the own blocks, a step ahead of their use
-      uint32_t th[2][2][4], tl[2][2][4];
-      const auto load_t = [&](int s) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (s <= own[j]) {
-            const uint32_t a = tt + block_of(own[j], s) * kBlock + row32_at(b_row, b_piece);
-            ldsm4(th[s & 1][j], a);
-            ldsm4(tl[s & 1][j], a + kTri);
-          }
-      };
-      load_t(0);
-      float2 cc[2][2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          cc[j][q] =
-              *reinterpret_cast<const float2 *>(vec + kVecC * kC + 16 * own[j] + 8 * q + 2 * t);
-      const float4 misc = *reinterpret_cast<const float4 *>(vec + kVecMisc * kC);
-      bar_sync(bar_x, kAll);
-      // x_i = beta_i v_i - c_i (S k_i); vec holds -c_i.  Its scale comes from
-      // norms, so that the warps agree on it without another exchange:
-      // |S k_i| <= |S| |k_i|, where k_i (scaled) stays below 2^15 and each
-      // share of S below 2^15 i0 per element.
-      const float2 si = add2(gs.s_inv[0][lane], gs.s_inv[1][lane]);
-      const float2 va = gs.v_max[0][lane], vb = gs.v_max[1][lane];
-      const float2 vm = make_float2(fmaxf(va.x, vb.x), fmaxf(va.y, vb.y));
-      const float gamma = misc.x, tau = misc.y, back = misc.y * misc.z;
-      const float reach = misc.w * (0x1p30f * (C::kCols == 32 ? 5.66f : 8.0f));  // sqrt
-      float n0, n1, j0, j1;
-      pow2_above(fmaf(reach, si.x, vm.x), j0, n0);
-      pow2_above(fmaf(reach, si.y, vm.y), j1, n1);
-      n0 *= 0x1p15f, n1 *= 0x1p15f, j0 *= 0x1p-15f, j1 *= 0x1p-15f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float4 y[2] = {gs.x_part[own[j]][0][lane], gs.x_part[own[j]][1][lane]};
-        const float4 z[2] = {gs.y[own[j]][0][lane], gs.y[own[j]][1][lane]};
-        Acc x[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          x[q].top = add2(mine[j][q].top, make_float2(y[q].x, y[q].y));
-          x[q].low = add2(mine[j][q].low, make_float2(y[q].z, y[q].w));
-          x[q].top = fma2(cc[j][q], x[q].top, make_float2(z[q].x, z[q].y));
-          x[q].low = fma2(cc[j][q], x[q].low, make_float2(z[q].z, z[q].w));
-        }
-        uint32_t hi[4], lo[4];
-        split_frag(x[0], x[1], n0, n1, hi, lo);
-        put4(&gs.x_frag[own[j]][0][lane], hi);
-        put4(&gs.x_frag[own[j]][1][lane], lo);
-      }
-      float2 ts[2][2], dd[2][2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int col = 16 * own[j] + 8 * q + 2 * t;
-          ts[j][q] = *reinterpret_cast<const float2 *>(vec + kVecT * kC + col);
-          dd[j][q] = *reinterpret_cast<const float2 *>(vec + kVecD * kC + col);
-        }
-      bar_sync(bar_y, 32 * kHalves);
-      // u = T x
-      Acc U[2][2] = {}, V[2][2] = {}, W[2][2] = {};
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (s > own[1]) continue;  // the larger one
-        uint32_t hi[4], lo[4];
-        get4(&gs.x_frag[s][0][lane], hi);
-        get4(&gs.x_frag[s][1][lane], lo);
-        if (s < 3) load_t(s + 1);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (s <= own[j])
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              mma16(U[j][q], hi, th[s & 1][j][2 * q], th[s & 1][j][2 * q + 1]);
-              mma16(V[j][q], hi, tl[s & 1][j][2 * q], tl[s & 1][j][2 * q + 1]);
-              mma16(W[j][q], lo, th[s & 1][j][2 * q], th[s & 1][j][2 * q + 1]);
+            if (s <= own[j]) {
+              const uint32_t a = tt + block_of(own[j], s) * kBlock + row32_at(b_row, b_piece);
+              ldsm4(th[s & 1][j], a);
+              ldsm4(tl[s & 1][j], a + kTri);
             }
-      }
-      // Rescaled by T's row scales and down by a bound of its row sums, u
-      // stays below 2^15 (the scale of x), and so does w_j = Gamma_64,j
-      // kappa_j u_j over the largest such factor.
-      if (part == 0) gs.u_inv[lane] = make_float2(j0 * tau, j1 * tau);
+        };
+        load_t(0);
+        float2 cc[2][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t f[4], hi[4], lo[4];
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float2 top = mul2(add2(U[j][q].top, add2(V[j][q].top, W[j][q].top)), ts[j][q]);
-          const float2 low = mul2(add2(U[j][q].low, add2(V[j][q].low, W[j][q].low)), ts[j][q]);
-          f[2 * q] = h2_bits(__float22half2_rn(top));
-          f[2 * q + 1] = h2_bits(__float22half2_rn(low));
-          split_h2(mul2(top, dd[j][q]), hi[2 * q], lo[2 * q]);
-          split_h2(mul2(low, dd[j][q]), hi[2 * q + 1], lo[2 * q + 1]);
+          for (int q = 0; q < 2; ++q)
+            cc[j][q] =
+                *reinterpret_cast<const float2 *>(vec + kVecC * kC + 16 * own[j] + 8 * q + 2 * t);
+        const float4 misc = *reinterpret_cast<const float4 *>(vec + kVecMisc * kC);
+        bar_sync(bar_x, kAll);
+        // x_i = beta_i v_i - c_i (S k_i); vec holds -c_i.  Its scale comes from
+        // norms, so that the warps agree on it without another exchange:
+        // |S k_i| <= |S| |k_i|, where k_i (scaled) stays below 2^15 and each
+        // share of S below 2^15 i0 per element.
+        const float2 si = add2(gs.s_inv[0][lane], gs.s_inv[1][lane]);
+        const float2 va = gs.v_max[0][lane], vb = gs.v_max[1][lane];
+        const float2 vm = make_float2(fmaxf(va.x, vb.x), fmaxf(va.y, vb.y));
+        const float gamma = misc.x, tau = misc.y, back = misc.y * misc.z;
+        const float reach = misc.w * (0x1p30f * (C::kCols == 32 ? 5.66f : 8.0f));  // sqrt
+        float n0, n1, j0, j1;
+        pow2_above(fmaf(reach, si.x, vm.x), j0, n0);
+        pow2_above(fmaf(reach, si.y, vm.y), j1, n1);
+        n0 *= 0x1p15f, n1 *= 0x1p15f, j0 *= 0x1p-15f, j1 *= 0x1p-15f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float4 y[2] = {gs.x_part[own[j]][0][lane], gs.x_part[own[j]][1][lane]};
+          const float4 z[2] = {gs.y[own[j]][0][lane], gs.y[own[j]][1][lane]};
+          Acc x[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            x[q].top = add2(mine[j][q].top, make_float2(y[q].x, y[q].y));
+            x[q].low = add2(mine[j][q].low, make_float2(y[q].z, y[q].w));
+            x[q].top = fma2(cc[j][q], x[q].top, make_float2(z[q].x, z[q].y));
+            x[q].low = fma2(cc[j][q], x[q].low, make_float2(z[q].z, z[q].w));
+          }
+          uint32_t hi[4], lo[4];
+          split_frag(x[0], x[1], n0, n1, hi, lo);
+          put4(&gs.x_frag[own[j]][0][lane], hi);
+          put4(&gs.x_frag[own[j]][1][lane], lo);
         }
-        put4(&gs.w_frag[own[j]][0][lane], hi);
-        put4(&gs.w_frag[own[j]][1][lane], lo);
-        put4(&gs.u_frag[own[j]][lane], f);
-      }
-      bar_sync(bar_w, kGroup);
-      // S = gamma S + sum_j w_j k_j^T, up to 32 key channels at a time
-      uint32_t wh[4][4], wl[4][4];
+        float2 ts[2][2], dd[2][2];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        get4(&gs.w_frag[s][0][lane], wh[s]);
-        get4(&gs.w_frag[s][1][lane], wl[s]);
-      }
-      const float2 b0 = both(j0 * back), b1 = both(j1 * back);
-      constexpr int kAt = 2;  // 16-channel blocks at a time
-      float a0 = 0.0f, a1 = 0.0f;
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int np = 0; np < C::kSteps; np += kAt) {
-        Acc acc[2 * kAt] = {};
+          for (int q = 0; q < 2; ++q) {
+            const int col = 16 * own[j] + 8 * q + 2 * t;
+            ts[j][q] = *reinterpret_cast<const float2 *>(vec + kVecT * kC + col);
+            dd[j][q] = *reinterpret_cast<const float2 *>(vec + kVecD * kC + col);
+          }
+        bar_sync(bar_y, 32 * kHalves);
+        // u = T x
+        Acc U[2][2] = {}, V[2][2] = {}, W[2][2] = {};
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          uint32_t bb[kAt][4];
+          if (s > own[1]) continue;  // the larger one
+          uint32_t hi[4], lo[4];
+          get4(&gs.x_frag[s][0][lane], hi);
+          get4(&gs.x_frag[s][1][lane], lo);
+          if (s < 3) load_t(s + 1);
 #pragma unroll
-          for (int j = 0; j < kAt; ++j)
-            ldsm4_t(bb[j], kt + tile_at<DK>(16 * s + bt_row,
-                                            part * (C::kCols / 8) + 2 * (np + j) + bt_piece));
+          for (int j = 0; j < 2; ++j)
+            if (s <= own[j])
 #pragma unroll
-          for (int j = 0; j < kAt; ++j) {
-            mma16(acc[2 * j], wh[s], bb[j][0], bb[j][1]);
-            mma16(acc[2 * j + 1], wh[s], bb[j][2], bb[j][3]);
+              for (int q = 0; q < 2; ++q) {
+                mma16(U[j][q], hi, th[s & 1][j][2 * q], th[s & 1][j][2 * q + 1]);
+                mma16(V[j][q], hi, tl[s & 1][j][2 * q], tl[s & 1][j][2 * q + 1]);
+                mma16(W[j][q], lo, th[s & 1][j][2 * q], th[s & 1][j][2 * q + 1]);
+              }
+        }
+        // Rescaled by T's row scales and down by a bound of its row sums, u
+        // stays below 2^15 (the scale of x), and so does w_j = Gamma_64,j
+        // kappa_j u_j over the largest such factor.
+        if (part == 0) gs.u_inv[lane] = make_float2(j0 * tau, j1 * tau);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t f[4], hi[4], lo[4];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float2 top = mul2(add2(U[j][q].top, add2(V[j][q].top, W[j][q].top)), ts[j][q]);
+            const float2 low = mul2(add2(U[j][q].low, add2(V[j][q].low, W[j][q].low)), ts[j][q]);
+            f[2 * q] = h2_bits(__float22half2_rn(top));
+            f[2 * q + 1] = h2_bits(__float22half2_rn(low));
+            split_h2(mul2(top, dd[j][q]), hi[2 * q], lo[2 * q]);
+            split_h2(mul2(low, dd[j][q]), hi[2 * q + 1], lo[2 * q + 1]);
+          }
+          put4(&gs.w_frag[own[j]][0][lane], hi);
+          put4(&gs.w_frag[own[j]][1][lane], lo);
+          put4(&gs.u_frag[own[j]][lane], f);
+        }
+        bar_sync(bar_w, kGroup);
+        // S = gamma S + sum_j w_j k_j^T, up to 32 key channels at a time
+        uint32_t wh[4][4], wl[4][4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          get4(&gs.w_frag[s][0][lane], wh[s]);
+          get4(&gs.w_frag[s][1][lane], wl[s]);
+        }
+        const float2 b0 = both(j0 * back), b1 = both(j1 * back);
+        constexpr int kAt = 2;  // 16-channel blocks at a time
+        float a0 = 0.0f, a1 = 0.0f;
+#pragma unroll
+        for (int np = 0; np < C::kSteps; np += kAt) {
+          Acc acc[2 * kAt] = {};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            uint32_t bb[kAt][4];
+#pragma unroll
+            for (int j = 0; j < kAt; ++j)
+              ldsm4_t(bb[j], kt + tile_at<DK>(16 * s + bt_row,
+                                              part * (C::kCols / 8) + 2 * (np + j) + bt_piece));
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+              mma16(acc[2 * j], wh[s], bb[j][0], bb[j][1]);
+              mma16(acc[2 * j + 1], wh[s], bb[j][2], bb[j][3]);
+            }
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+              mma16(acc[2 * j], wl[s], bb[j][0], bb[j][1]);
+              mma16(acc[2 * j + 1], wl[s], bb[j][2], bb[j][3]);
+            }
           }
 #pragma unroll
-          for (int j = 0; j < kAt; ++j) {
-            mma16(acc[2 * j], wl[s], bb[j][0], bb[j][1]);
-            mma16(acc[2 * j + 1], wl[s], bb[j][2], bb[j][3]);
+          for (int q = 0; q < 2 * kAt; ++q) {
+            Acc &a = S[2 * np + q];
+            a.top = fma2(acc[q].top, b0, mul2(both(gamma), a.top));
+            a.low = fma2(acc[q].low, b1, mul2(both(gamma), a.low));
+            a0 = max3_abs(a0, a.top.x, a.top.y);
+            a1 = max3_abs(a1, a.low.x, a.low.y);
           }
         }
+        if (++st == kStages) st = 0;
+        pow2_scale(quad_max(a0), m0, i0);
+        pow2_scale(quad_max(a1), m1, i1);
+      }
+      if (seq.state_out) {
 #pragma unroll
-        for (int q = 0; q < 2 * kAt; ++q) {
-          Acc &a = S[2 * np + q];
-          a.top = fma2(acc[q].top, b0, mul2(both(gamma), a.top));
-          a.low = fma2(acc[q].low, b1, mul2(both(gamma), a.low));
-          a0 = max3_abs(a0, a.top.x, a.top.y);
-          a1 = max3_abs(a1, a.low.x, a.low.y);
+        for (int n = 0; n < 2 * C::kSteps; ++n) {
+          *reinterpret_cast<float2 *>(seq.state_out + at + 8 * n) = S[n].top;
+          *reinterpret_cast<float2 *>(seq.state_out + at + 8 * DK + 8 * n) = S[n].low;
         }
       }
-      if (++st == kStages) st = 0;
-      pow2_scale(quad_max(a0), m0, i0);
-      pow2_scale(quad_max(a1), m1, i1);
-    }
-    if (seq.state_out) {
-#pragma unroll
-      for (int n = 0; n < 2 * C::kSteps; ++n) {
-        *reinterpret_cast<float2 *>(seq.state_out + at + 8 * n) = S[n].top;
-        *reinterpret_cast<float2 *>(seq.state_out + at + 8 * DK + 8 * n) = S[n].low;
-      }
-    }
     }
     // sequences without tokens: their states as they are
     if (!seq.state_out || seq.state_out == seq.state_in) return;
-    const int empty = static_cast<int>(head[kEmptyWord]) * per;
     for (int e = blockIdx.x; e < empty; e += grid) {
       const int slot = list[seq.B - 1 - e / per].z;
-      const int64_t from = ((static_cast<int64_t>(slot) * d.v_heads + e / tiles % d.v_heads) * d.v_dim +
-                            e % tiles * kRows) * DK;
+      const int64_t state = static_cast<int64_t>(slot) * d.v_heads + e / tiles % d.v_heads;
+      const int64_t from = (state * d.v_dim + e % tiles * kRows) * DK;
       for (int i = 4 * tid; i < kRows * DK; i += 4 * 32 * kHalves * kGroups)
         *reinterpret_cast<float4 *>(seq.state_out + from + i) =
             seq.state_in ? *reinterpret_cast<const float4 *>(seq.state_in + from + i)
@@ -1078,34 +1084,29 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
   moe_bf16 *line_dst[2] = {};
   int line_len[2] = {};
   const auto bring_in = [&](int stage, bool alive) {
-    if (left <= 0) {
-      if (index < total) {
-        ++ahead;
-        const int dv = row + group * 16;
-        const bool second = line_len[0] > 0;
-        moe_bf16 *dst = out + (static_cast<int64_t>(record.x) + my_row) * out_ld + h * d.v_dim + dv +
-                        (lane & 1) * 8;
-        (second ? line_dst[1] : line_dst[0]) = dst;
-        (second ? line_len[1] : line_len[0]) = record.y;
-        const size_t base = record.w;
-        left = record.y;
-        from = of_head ? ws_head + (base * d.v_heads + h) * kHeadBlob + (into_b ? kPartA : 0)
-                       : ws_key + (base * d.qk_heads + key_head) * kKeyBlob<DK> + (into_b ? kKeyTile : 0);
-        v_src = in.v + (static_cast<int64_t>(record.x) + my_row) * in.v_ld + h * d.v_dim + dv +
-                (lane & 1) * 8;
-        // the group's state, a line of 128 bytes each, on its way into L2
-        constexpr int kLines = DK / 32;
-        const int line = 32 * side + lane;
-        if (ahead > 0 && seq.state_in && line < 16 * kLines)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(
-              seq.state_in + ((static_cast<int64_t>(record.z) * d.v_heads + h) * d.v_dim + dv +
-                              line / kLines) * DK + line % kLines * 32));
-        index = piece_at(ahead + 1);
-        if (index < total) {
-          record = list[index / per];
-          h = index / tiles % d.v_heads, row = index % tiles * kRows, key_head = h / ratio;
-        }
-      }
+    const bool begins = left <= 0 && index < total;
+    if (begins) {
+      ++ahead;
+      const int dv = row + group * 16;
+      const bool second = line_len[0] > 0;
+      moe_bf16 *dst = out + (static_cast<int64_t>(record.x) + my_row) * out_ld + h * d.v_dim + dv +
+                      (lane & 1) * 8;
+      (second ? line_dst[1] : line_dst[0]) = dst;
+      (second ? line_len[1] : line_len[0]) = record.y;
+      const size_t base = record.w;
+      left = record.y;
+      from = of_head ? ws_head + (base * d.v_heads + h) * kHeadBlob + (into_b ? kPartA : 0)
+                     : ws_key + (base * d.qk_heads + key_head) * kKeyBlob<DK> +
+                           (into_b ? kKeyTile : 0);
+      v_src = in.v + (static_cast<int64_t>(record.x) + my_row) * in.v_ld + h * d.v_dim + dv +
+              (lane & 1) * 8;
+      // the group's state, a line of 128 bytes each, on its way into L2
+      constexpr int kLines = DK / 32;
+      const int line = 32 * side + lane;
+      if (ahead > 0 && seq.state_in && line < 16 * kLines)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            seq.state_in + ((static_cast<int64_t>(record.z) * d.v_heads + h) * d.v_dim + dv +
+                            line / kLines) * DK + line % kLines * 32));
     }
     v_now = v_src, v_left = left;
     if (left > 0) {
@@ -1117,6 +1118,13 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
         ++fed;
       }
       v_src += kC * in.v_ld, from += from_step, left -= kC;
+    }
+    if (begins) {
+      index = piece_at(ahead + 1);
+      if (index < total) {
+        record = list[index / per];
+        h = index / tiles % d.v_heads, row = index % tiles * kRows, key_head = h / ratio;
+      }
     }
   };
   // the own blocks of its values, zeros past the end
@@ -1220,7 +1228,8 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
     if (fed > n + 1) wait_full(next, next_parity);
     bar_sync(bar_w, kGroup);
     // the previous chunk's stage is free (bar_x)
-    bring_in(st == 0 ? kStages - 1 : st - 1, !__any_sync(kFull, *reinterpret_cast<volatile int *>(abort_flag)));
+    const int given_up = *reinterpret_cast<volatile int *>(abort_flag);
+    bring_in(st == 0 ? kStages - 1 : st - 1, !__any_sync(kFull, given_up));
     const float2 ui = gs.u_inv[lane];
     Acc I[2][2] = {};
     uint32_t uf[4][4];
@@ -1297,8 +1306,9 @@ cudaError_t launch_chain(const moe_delta_dims &d, const moe_delta_inputs &in, co
   cudaError_t e = allow_smem(delta_chain_kernel<DK>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   const int pieces = seq.B * d.v_heads * (d.v_dim / kRows), sms = tc_sm_count();
-  return launch_early(delta_chain_kernel<DK>, dim3(pieces < sms ? pieces : sms), C::kThreads, C::kSmem,
-                      s, d, in, seq, ws, list, ws_key, ws_head, out, out_ld, tc_wait_budget_ns());
+  return launch_early(delta_chain_kernel<DK>, dim3(pieces < sms ? pieces : sms), C::kThreads,
+                      C::kSmem, s, d, in, seq, ws, list, ws_key, ws_head, out, out_ld,
+                      tc_wait_budget_ns());
 }
 
 // The sequences' records, up to a whole 256 bytes.
@@ -1337,7 +1347,8 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
 size_t delta_chunk_workspace(const moe_delta_dims &d, int N, int B) {
   const size_t slots = static_cast<size_t>(N) / kC + B;
   const size_t key = d.qk_dim == 128 ? kKeyBlob<128> : kKeyBlob<64>;
-  return kHeader + list_bytes(B) + slots * (d.qk_heads * key + static_cast<size_t>(d.v_heads) * kHeadBlob);
+  return kHeader + list_bytes(B) +
+         slots * (d.qk_heads * key + static_cast<size_t>(d.v_heads) * kHeadBlob);
 }
 
 cudaError_t launch_delta_chunk(const moe_delta_dims &d, const moe_delta_inputs &in,

@@ -116,6 +116,60 @@ def test_chunk_many_sequences_in_place(env):
     run_chunk(env, make(env, sum(lens), (1, 2), (64, 64)), lens, (1, 2), (64, 64), in_place=True)
 
 
+@pytest.mark.parametrize("lens,heads", [
+    ([int(x) for x in np.random.RandomState(4).randint(0, 140, 40)], (2, 8)),
+    ([int(x) for x in np.random.RandomState(5).randint(0, 4, 290)] + [130, 0, 70] + [1] * 10, (1, 4)),
+    ([1] * 70, (4, 16)), ([64, 0] * 20, (2, 16)), ([0] * 30 + [200] + [0] * 30, (2, 16))])
+def test_chunk_more_work_than_blocks(env, lens, heads):
+    """Several pieces of work for every block of the second kernel; more
+    sequences than are put in order at a time; sequences without tokens.  The
+    order of the batch changes no bit of any sequence."""
+    import torch
+    moe, dev = env
+    dims, n, b = (128, 64), sum(lens), len(lens)
+    s = make(env, n, heads, dims, seed=7)
+    m = mixer(env, heads, dims, n, b)
+    pool = states(env, b, heads, dims)
+    S1 = torch.full_like(pool, 7.0)
+    out = m.chunk(**s, cu_seqlens=cu_of(env, lens), state_in=pool, state_out=S1)
+    assert m.status() == 0 and out.isfinite().all() and S1.isfinite().all()
+    ends = np.cumsum(lens)
+    for i, L in enumerate(lens):
+        assert L or torch.equal(S1[i], pool[i])
+        assert not L or not torch.equal(S1[i], pool[i])
+    rows = torch.tensor([r for e, L in zip(ends[::-1], lens[::-1]) for r in range(e - L, e)],
+                        device=dev)
+    slots = torch.arange(b - 1, -1, -1, dtype=torch.int32, device=dev)
+    again = m.chunk(**{x: t[rows].contiguous() for x, t in s.items()},
+                    cu_seqlens=cu_of(env, lens[::-1]), state_in=pool, state_out=pool, slots=slots)
+    assert m.status() == 0
+    assert torch.equal(again, out[rows]) and torch.equal(pool, S1)
+
+
+def test_chunk_tiny_values_beside_large_ones(env):
+    """A reset, then values far below those of the tokens before it: the
+    prompt form keeps 2^-36 of the largest value of the same 64 tokens and state
+    row (two fp16 terms, their scale from a bound up to 2^4 above it, sums of 64
+    products: 2^-33 in all), and 22 bits of what is above 2^-17 of it."""
+    import torch
+    _, dev = env
+    heads, dims, n = (2, 4), (128, 128), 60
+    s = make(env, n, heads, dims, seed=9)
+    s["g"][50] = -40.0
+    s["v"][50:] *= 2.0 ** -21
+    m = mixer(env, heads, dims, n, 1)
+    S1 = torch.empty((1, 4, 128, 128), device=dev)
+    m.chunk(**s, state_out=S1)
+    c = {x: f64(s[x]) for x in ("q", "k", "v", "g", "beta")}
+    zero = np.zeros((4, 128, 128))
+    _, S, _, A = delta_rule(**c, S0=zero, scale=1.0, qk_norm=True, eps=EPS)
+    _, Sb, _, _ = delta_rule(**{x: t[:50] for x, t in c.items()}, S0=zero, scale=1.0, qk_norm=True,
+                             eps=EPS)
+    most = np.abs(c["v"]).max(0) + np.sqrt((Sb * Sb).sum(-1))  # [Hv][dv]
+    err = np.abs(f64(S1[0]) - S)
+    assert not (err > state_bound(A, 1) + 2.0 ** -33 * most[:, :, None]).any(), err.max()
+
+
 def test_chunk_long(env):
     run_chunk(env, make(env, 1500, (1, 2)), [1500], (1, 2), (128, 128))
 
