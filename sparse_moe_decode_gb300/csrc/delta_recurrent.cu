@@ -10,11 +10,8 @@
 // Bound by memory where there are many sequences: each state is read and
 // written once, 256 sequences of one token (32 heads of 128 x 128, 1.08 GB) in
 // 153.8 us, 7.0 TB/s, 32 in 22.2 us.  One token of one sequence is latency:
-// 4.3 us, and 0.5 us for each further token (a token's products, two shuffle
-// reductions and the update follow one another).  Sixteen rows of the state per
-// warp: eight or four would have less to do in a token's turn, but repeat its
-// k and q, norms and reductions more often, and were slower with many
-// sequences.
+// 2.1 us in a graph, and 0.43 us for each further token (a token's products,
+// two shuffle reductions and the update follow one another).
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -78,25 +75,26 @@ __device__ __forceinline__ float4 pack(const float (&v)[4]) {
 __device__ __forceinline__ float2 pack(const float (&v)[2]) { return make_float2(v[0], v[1]); }
 
 constexpr int kWarps = 4;
-constexpr int kRows = 16;  // state rows per warp
 
-// One warp holds kRows rows of one head's state, lane l columns V l .. V l +
+// One warp holds ROWS rows of one head's state, lane l columns V l .. V l +
 // V - 1 of each (a row is one coalesced access).
-// BLOCKS: blocks of an SM that the registers leave room for.
-template <int DK, int BLOCKS>
+// BLOCKS: blocks of an SM that the registers leave room for.  Three of 16 rows
+// (four: 74.6 against 67.8 us for 64 sequences of 4 tokens, 23.3 against 22.4 for
+// 32 of one), four of 8 (five: 10.6 against 8.8 us for 4 of 8).
+template <int DK, int ROWS, int BLOCKS>
 __global__ void __launch_bounds__(32 * kWarps, BLOCKS)
 delta_recurrent_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, moe_bf16 *out,
                        int64_t out_ld) {
   constexpr int V = DK / 32;
+  constexpr int kPer = 16 / ROWS;  // lanes of a half warp that share a row's sums
   using VF = typename Vec<V>::F;
   using VH = typename Vec<V>::H;
-  const int lane = threadIdx.x & 31;
-  const uint32_t tiles = d.v_dim / kRows;
+  const int lane = threadIdx.x & 31, row = (lane & 15) / kPer;
+  const uint32_t tiles = d.v_dim / ROWS;
   const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int tile = static_cast<int>(unit % tiles);
   const int h = static_cast<int>(unit / tiles % d.v_heads);
   const int b = static_cast<int>(unit / tiles / d.v_heads);
-  if (b >= seq.B) return;
   early_begin();
   if (seq.cu_seqlens) {
     // a call with a bad bound does nothing (launched for few sequences only)
@@ -114,15 +112,15 @@ delta_recurrent_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, moe
   if (!r.ok) return;
   const int hk = h / (d.v_heads / d.qk_heads);
   const int64_t at =
-      ((static_cast<int64_t>(r.slot) * d.v_heads + h) * d.v_dim + tile * kRows) * DK + lane * V;
+      ((static_cast<int64_t>(r.slot) * d.v_heads + h) * d.v_dim + tile * ROWS) * DK + lane * V;
   // A token's values are asked for one token ahead.
   const int64_t row0 = r.start;
   const moe_bf16 *kp = in.k + row0 * in.k_ld + hk * DK + lane * V;
   const moe_bf16 *qp = in.q + row0 * in.q_ld + hk * DK + lane * V;
   const moe_bf16 *vp =
-      in.v + row0 * in.v_ld + h * d.v_dim + tile * kRows + (lane & (kRows - 1));
+      in.v + row0 * in.v_ld + h * d.v_dim + tile * ROWS + row;
   const float *gp = in.g + row0 * in.g_ld + h, *bp = in.beta + row0 * in.beta_ld + h;
-  moe_bf16 *op = out + row0 * out_ld + h * d.v_dim + tile * kRows + lane;
+  moe_bf16 *op = out + row0 * out_ld + h * d.v_dim + tile * ROWS + row;
   VH kw{}, qw{};
   uint16_t vw = 0;
   float gw = 0.0f, bw = 0.0f;
@@ -132,14 +130,14 @@ delta_recurrent_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, moe
     kp += in.k_ld, qp += in.q_ld, vp += in.v_ld, gp += in.g_ld, bp += in.beta_ld;
   };
   if (r.len > 0) fetch();
-  float s[kRows][V];
+  float s[ROWS][V];
   if (seq.state_in) {
     const float *p = seq.state_in + at;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) unpack(*reinterpret_cast<const VF *>(p + i * DK), s[i]);
+    for (int i = 0; i < ROWS; ++i) unpack(*reinterpret_cast<const VF *>(p + i * DK), s[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
+    for (int i = 0; i < ROWS; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) s[i][j] = 0.0f;
   }
@@ -162,9 +160,9 @@ delta_recurrent_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, moe
       kn = rsqrtf(kk + d.qk_eps);
       qn = d.scale * rsqrtf(qq + d.qk_eps);
     }
-    float part[2 * kRows];
+    float part[2 * ROWS];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       float sk = 0.0f, sq = 0.0f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -172,17 +170,17 @@ delta_recurrent_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, moe
         sq = fmaf(s[i][j], q[j], sq);
       }
       part[i] = sk;
-      part[kRows + i] = sq;
+      part[ROWS + i] = sq;
     }
-    // lane i < kRows: row i's S k; lane kRows + i: its S q
+    // lanes below 16: their row's S k; lane 16 + l: S q of lane l's row
     const float sum = reduce_spread(part, lane);
-    const float sq = __shfl_down_sync(kFull, sum, kRows);
-    const float u = beta * (v - a * kn * sum);  // lanes < kRows
-    if (lane < kRows)
+    const float sq = __shfl_down_sync(kFull, sum, 16);
+    const float u = beta * (v - a * kn * sum);  // lanes < 16
+    if (lane < 16 && lane % kPer == 0)
       *op = f32_to_bf16(qn * (a * sq + u * kn * kq));
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const float ui = __shfl_sync(kFull, u, i) * kn;
+    for (int i = 0; i < ROWS; ++i) {
+      const float ui = __shfl_sync(kFull, u, i * kPer) * kn;
 #pragma unroll
       for (int j = 0; j < V; ++j) s[i][j] = fmaf(a, s[i][j], ui * k[j]);
     }
@@ -190,7 +188,7 @@ delta_recurrent_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, moe
   if (seq.state_out) {
     float *p = seq.state_out + at;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) *reinterpret_cast<VF *>(p + i * DK) = pack(s[i]);
+    for (int i = 0; i < ROWS; ++i) *reinterpret_cast<VF *>(p + i * DK) = pack(s[i]);
   }
 }
 
@@ -199,17 +197,18 @@ delta_recurrent_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, moe
 cudaError_t launch_delta_recurrent(const moe_delta_dims &d, const moe_delta_inputs &in,
                                    const DeltaSeqs &seq, moe_bf16 *out, int64_t out_ld,
                                    cudaStream_t s) {
-  const int64_t units = static_cast<int64_t>(seq.B) * d.v_heads * (d.v_dim / kRows);
-  const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
-  // Three blocks an SM keep a token's values in registers ahead of their use:
-  // 22.4 against 23.3 us for 32 sequences of one token (32 heads of 128), 12.3
-  // against 13.2 us for 4 of 8.  More blocks than that at once, with several
-  // tokens each to work on, go faster four to an SM: 8 of 8 tokens in 15.7
-  // against 17.9 us.
-  const bool four = seq.T > 1 && grid > 3u * static_cast<unsigned>(tc_sm_count());
-  const auto kernel = d.qk_dim == 128
-                          ? (four ? delta_recurrent_kernel<128, 4> : delta_recurrent_kernel<128, 3>)
-                          : (four ? delta_recurrent_kernel<64, 4> : delta_recurrent_kernel<64, 3>);
+  const int64_t rows = static_cast<int64_t>(seq.B) * d.v_heads * d.v_dim, sms = tc_sm_count();
+  // Warps of 8 rows have half as much to do in a token's turn but load k and q
+  // and sum their norms twice as often: faster up to 16 warps of 16 rows an SM
+  // (4 sequences of 8 tokens 8.8 against 11.0 us, 8 of one 5.2 against 5.7),
+  // slower beyond (32 of one 16.4 against 15.3 us, states in L2).
+  const bool small = rows <= 16 * 16 * sms;
+  // (a head has a multiple of 64 rows)
+  const unsigned grid = static_cast<unsigned>(rows / (small ? 8 : 16) / kWarps);
+  const bool wide = d.qk_dim == 128;
+  const auto kernel =
+      small ? (wide ? delta_recurrent_kernel<128, 8, 4> : delta_recurrent_kernel<64, 8, 4>)
+            : (wide ? delta_recurrent_kernel<128, 16, 3> : delta_recurrent_kernel<64, 16, 3>);
   return launch_early(kernel, dim3(grid), 32 * kWarps, 0, s, d, in, seq, out, out_ld);
 }
 

@@ -15,18 +15,18 @@ constexpr int kDeltaMaxTokens = 1 << 20;
 constexpr int kDeltaMaxSeqs = 65536;
 constexpr int kDeltaMaxHeads = 256;
 // Calls of few token rows run token by token: one sequence (32 value heads of
-// 128) takes 14.7 us in the chunked form whatever its length up to 64, and 4 to
-// 5 us and 0.5 us for each further token in the recurrent one (11.1 us at 16, 15.5
-// at 24).  Further sequences add 3.4 us each to the chunked form, where 4096
-// state rows take the SMs, and next to nothing to the recurrent one: 4 of 7
-// tokens 10.6 against 25.3 us, 12 of 4 15.2 against 51.5 us.  The lengths are
-// not known here; where one sequence has all of the rows and the others none,
-// the rule loses (28 rows 24.9 against 18.2 us, 48 rows 49.8 against 30.0 us).
+// 128) takes 17.0 us in the chunked form whatever its length up to 64 (8 heads of
+// 64 10.8 us), in a graph, and 1.7 us and 0.43 us for each token in the recurrent
+// one (12.0 and 11.0 us at 24).  Further sequences add 3 us each to the chunked
+// form, where 4096 state rows take the SMs, and next to nothing to the
+// recurrent one: 4 of 7 tokens 8.5 against 23 us, 16 of 3 14.3 against 59 us.  The
+// lengths are not known here; where one sequence has all of the rows and the
+// others none, the rule loses (48 rows of one of 13, 32 against 15 us).
 bool few_rows(const moe_delta_dims &d, int N, int B) {
   constexpr int kMostSeqs = 64;  // each warp looks at all of their bounds
   if (B > kMostSeqs) return false;
   const int more = 4 * (B - 1) * d.v_heads * d.v_dim / 4096;
-  return N <= 16 + (more < 32 ? more : 32);
+  return N <= 24 + (more < 24 ? more : 24);
 }
 constexpr int kNormMaxWidth = 16384;
 constexpr int64_t kNormMaxRows = (int64_t(1) << 31) - 1;
