@@ -298,6 +298,10 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
     const moe_bf16 *src = is_q ? in.q : in.k;
     const int64_t ld = is_q ? in.q_ld : in.k_ld;
     uint8_t *tile = sm.key + (is_q ? kKeyBlob<DK> / 2 : 0);
+    // one CTA of a key head's writes them out, whole lines from registers
+    const bool keeps_key = h0 % ratio == 0;
+    uint8_t *key_out = ws_key + (static_cast<size_t>(slot) * d.qk_heads + hk) * kKeyBlob<DK> +
+                       (is_q ? kKeyBlob<DK> / 2 : 0);
     src += row0 * ld + hk * DK + piece * 8;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
@@ -362,20 +366,16 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           o[j] = h2_bits(__float22half2_rn(mul2(x[e][j], make_float2(mult, mult))));
-        *reinterpret_cast<uint4 *>(tile + tile_at<DK>(i, piece + 8 * e)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
+        const uint4 all = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(tile + tile_at<DK>(i, piece + 8 * e)) = all;
+        if (keeps_key) *reinterpret_cast<uint4 *>(key_out + tile_at<DK>(i, piece + 8 * e)) = all;
       }
       if (d.qk_norm) inv *= rsqrtf(ss + d.qk_eps);
       if (is_q) inv *= d.scale;
       if (piece == 0) (is_q ? sm.rho : sm.kappa)[i] = i < left ? inv : 0.0f;
     }
   }
-  ptx::fence_proxy_async_smem();
   __syncthreads();
-  const bool keeps_key = tid == 0 && h0 % ratio == 0;
-  if (keeps_key)
-    bulk_store(ws_key + (static_cast<size_t>(slot) * d.qk_heads + hk) * kKeyBlob<DK>,
-               ptx::smem_u32(sm.key), kKeyBlob<DK>);
 
   // Rows of k k^T or q k^T, up to the diagonal block; then, once nobody reads k
   // and q any more, into their place.
@@ -402,7 +402,6 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
           mma16(acc[2 * np + 1], a, b[np][2], b[np][3]);
         }
     }
-    if (keeps_key) bulk_store_wait(false);
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < 8; ++n)
