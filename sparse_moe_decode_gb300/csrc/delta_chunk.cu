@@ -30,7 +30,7 @@
 //
 // What bounds it (GB300, 32 value heads of 128 x 128 on 16 key heads).  A chunk
 // of the chain takes 1.73 us on whatever SM it runs, so one prompt of 8192
-// tokens takes 222 us there and 83 us in the preparation, of 31 us for the
+// tokens takes 222 us there and 82 us in the preparation, of 31 us for the
 // bytes.  A CTA's pieces of work (32 state rows of one sequence) follow one
 // another, longest sequences first, with the next one's chunks, values and
 // state on their way during the last one's chunks: 240 us for 13 sequences of
@@ -243,7 +243,7 @@ __device__ void list_sequences(const DeltaSeqs &seq, uint32_t *head, int4 *list,
 // it.  Warps 0..3 take k (k k^T, L, T's diagonal blocks), warps 4..7 take q
 // (q k^T, P), 16 tokens each.
 //
-// Bound by the instructions it issues (0.6 per cycle and scheduler, 84 us for
+// Bound by the instructions it issues (0.6 per cycle and scheduler, 82 us for
 // the 4096 chunks and heads of 8192 tokens, where it moves 1.8 TB/s): the tensor
 // pipe is active for 16 % of the time; the inverse, the decays of the triangles
 // and the conversions are the rest.  80 registers leave three CTAs an SM, which wait for
