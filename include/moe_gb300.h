@@ -333,8 +333,8 @@ size_t moe_delta_workspace_bytes(const moe_delta_dims *dims, int N, int B);
  * <= N, MOE_DEV_BAD_INDEX is set and no out row or state is written.  out row
  * t lies at out + t * out_ld as [Hv][v_dim] bf16 (16-byte aligned, out_ld a
  * multiple of 8) and must not overlap the inputs.  N <= 2^20, B <= 65536.
- * Calls of few rows are worked on token by token, so that a sequence's last
- * digits can depend on the size of the call it is part of.  A value that is not finite makes its head's state,
+ * Sequences of up to 24 tokens are worked on token by token.  No digit of a
+ * sequence depends on the call that it is part of.  A value that is not finite makes its head's state,
  * and that head's outputs within the same run of 64 tokens and after it,
  * not finite; other heads and sequences do not see it. */
 moe_status moe_delta_chunk(const moe_delta_dims *dims, const moe_delta_inputs *in, int N,

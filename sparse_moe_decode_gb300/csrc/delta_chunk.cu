@@ -34,7 +34,7 @@
 // bytes.  A CTA's pieces of work (32 state rows of one sequence) follow one
 // another, longest sequences first, with the next one's chunks, values and
 // state on their way during the last one's chunks: 240 us for 13 sequences of
-// 6007 tokens in all and 113 us for 32 of 64, against 244 and 137 us with a
+// 6007 tokens in all and 116 us for 32 of 64, against 244 and 137 us with a
 // CTA for each piece.  (Each in a fixed order of pieces was slower, 263 us for
 // the 13.)  Measured and slower: four chain warps a group with a quarter of the
 // channels each (393 against 338 us for 8192 tokens then), one output warp a
@@ -70,8 +70,7 @@ constexpr int kHeadBlob = kPartA + kPartB;
 constexpr int kHeader = 256;      // status word, and these words
 enum {
   kFlagWord = 16,  // some bound of the call is bad: it does nothing
-  kCountWord,      // sequences that have tokens, the first records of the list
-  kEmptyWord,      // sequences without, the last ones
+  kCountWord,      // records of the list
   kNextWord,       // pieces of work that the chain's CTAs have asked for
 };
 constexpr int kPrepThreads = 256;
@@ -198,43 +197,38 @@ __device__ __forceinline__ float warp_max_pos(float v) {
 }
 
 // What the second kernel has to do, by one CTA: a record {first row, tokens,
-// state slot, first chunk slot} per sequence, those with tokens from the front
-// (of 256 at a time the longest first), those without from the back.  A call
-// with a bad bound does nothing.
+// state slot, first chunk slot} per sequence that is not short, of 256 at a time
+// the longest first.  A call with a bad bound does nothing.
 __device__ void list_sequences(const DeltaSeqs &seq, uint32_t *head, int4 *list, int *lens) {
   const int tid = threadIdx.x;
-  int count = 0, empty = 0;
+  int count = 0;
   bool bad = false;
   for (int b0 = 0; b0 < seq.B; b0 += kPrepThreads) {
     const int b = b0 + tid;
     DeltaSeqRange r{};
-    int len = -1;
+    int len = 0;
     if (b < seq.B) {
       if (seq.cu_seqlens) {
         const int lo = seq.cu_seqlens[b], hi = seq.cu_seqlens[b + 1];
         bad |= lo < 0 || lo > hi || hi > seq.N;
       }
       r = delta_seq_range(seq, b);
-      if (r.ok) len = r.len;
+      if (r.ok && r.len > kDeltaShort) len = r.len;
     }
     lens[tid] = len;
-    const int full = __syncthreads_count(len > 0), none = __syncthreads_count(len == 0);
-    if (len >= 0) {
+    const int here = __syncthreads_count(len > 0);
+    if (len > 0) {
       int rank = 0;
-      for (int i = 0; i < min(kPrepThreads, seq.B - b0); ++i) {
-        const int other = lens[i];
-        rank += (len > 0 && other > len) || (other == len && i < tid);
-      }
-      list[len > 0 ? count + rank : seq.B - 1 - empty - rank] =
-          make_int4(r.start, len, r.slot, first_slot(r, b));
+      for (int i = 0; i < min(kPrepThreads, seq.B - b0); ++i)
+        rank += lens[i] > len || (lens[i] == len && i < tid);
+      list[count + rank] = make_int4(r.start, len, r.slot, first_slot(r, b));
     }
-    count += full, empty += none;
+    count += here;
     __syncthreads();
   }
   bad = __syncthreads_or(bad);
   if (tid == 0) {
-    head[kFlagWord] = bad, head[kCountWord] = count, head[kEmptyWord] = empty;
-    head[kNextWord] = 0;
+    head[kFlagWord] = bad, head[kCountWord] = count, head[kNextWord] = 0;
     if (bad) set_status(seq.status, MOE_DEV_BAD_INDEX);
   }
 }
@@ -280,7 +274,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
   }
   const DeltaSeqRange r = delta_seq_range(seq, b);
   const int chunk = slot - first_slot(r, b);
-  if (!r.ok || chunk < 0 || chunk >= (r.len + kC - 1) / kC) return;
+  if (!r.ok || r.len <= kDeltaShort || chunk < 0 || chunk >= (r.len + kC - 1) / kC) return;
   const int left = min(kC, r.len - chunk * kC);  // tokens of this chunk
   const int64_t row0 = static_cast<int64_t>(r.start) + chunk * kC;
 
@@ -747,7 +741,6 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
   uint32_t *head = reinterpret_cast<uint32_t *>(ws);
   const uint32_t bad = head[kFlagWord];
   const int total = static_cast<int>(head[kCountWord]) * per;
-  const int empty = static_cast<int>(head[kEmptyWord]) * per;
   const int4 first = list[seq_of];  // (meaningless past the total)
   if (bad) return;
   const int grid = static_cast<int>(gridDim.x);
@@ -1005,17 +998,6 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
           *reinterpret_cast<float2 *>(seq.state_out + at + 8 * DK + 8 * n) = S[n].low;
         }
       }
-    }
-    // sequences without tokens: their states as they are
-    if (!seq.state_out || seq.state_out == seq.state_in) return;
-    for (int e = blockIdx.x; e < empty; e += grid) {
-      const int slot = list[seq.B - 1 - e / per].z;
-      const int64_t state = static_cast<int64_t>(slot) * d.v_heads + e / tiles % d.v_heads;
-      const int64_t from = (state * d.v_dim + e % tiles * kRows) * DK;
-      for (int i = 4 * tid; i < kRows * DK; i += 4 * 32 * kHalves * kGroups)
-        *reinterpret_cast<float4 *>(seq.state_out + from + i) =
-            seq.state_in ? *reinterpret_cast<const float4 *>(seq.state_in + from + i)
-                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     return;
   }
@@ -1347,7 +1329,10 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
   e = launch_early(delta_prep_kernel<DK>, grid, kPrepThreads, kSmem, s, d, in, seq, heads, ws,
                    list, ws_key, ws_head);
   if (e != cudaSuccess) return e;
-  return launch_chain<DK>(d, in, seq, ws, list, ws_key, ws_head, out, out_ld, s);
+  e = launch_chain<DK>(d, in, seq, ws, list, ws_key, ws_head, out, out_ld, s);
+  if (e != cudaSuccess || !seq.cu_seqlens) return e;  // the one sequence is longer
+  return launch_delta_recurrent(d, in, seq, kDeltaShort,
+                                reinterpret_cast<const uint32_t *>(ws) + kFlagWord, out, out_ld, s);
 }
 
 }  // namespace

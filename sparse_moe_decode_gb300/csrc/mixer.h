@@ -21,12 +21,22 @@ struct DeltaSeqs {
   uint32_t *status;
 };
 
-// Token by token, the state in registers (any length).
-cudaError_t launch_delta_recurrent(const moe_delta_dims &d, const moe_delta_inputs &in,
-                                   const DeltaSeqs &seq, moe_bf16 *out, int64_t out_ld,
-                                   cudaStream_t s);
+// A prompt call's sequences of so few tokens run token by token.  One (32 value
+// heads of 128) takes 17.0 us in the chunked form whatever its length up to 64
+// (8 heads of 64 10.8 us), in a graph, and 1.7 us and 0.43 us for each token in
+// the recurrent one (12.0 and 11.0 us at 24); each of many takes 3.1 us in the
+// former, 0.6 us and 0.11 us a token in the latter.
+constexpr int kDeltaShort = 24;
 
-// In chunks of 64 tokens; ws holds delta_chunk_workspace bytes.
+// Token by token, the state in registers: the sequences of up to `most` tokens.
+// `bad`: null, or a word that is not 0 when a bound of the call is bad (without
+// it every warp looks at all bounds).
+cudaError_t launch_delta_recurrent(const moe_delta_dims &d, const moe_delta_inputs &in,
+                                   const DeltaSeqs &seq, int most, const uint32_t *bad,
+                                   moe_bf16 *out, int64_t out_ld, cudaStream_t s);
+
+// In chunks of 64 tokens, the sequences of up to kDeltaShort tokens token by
+// token after the others; ws holds delta_chunk_workspace bytes.
 size_t delta_chunk_workspace(const moe_delta_dims &d, int N, int B);
 cudaError_t launch_delta_chunk(const moe_delta_dims &d, const moe_delta_inputs &in,
                                const DeltaSeqs &seq, void *ws, moe_bf16 *out, int64_t out_ld,

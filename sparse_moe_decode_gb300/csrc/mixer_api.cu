@@ -14,20 +14,8 @@ namespace {
 constexpr int kDeltaMaxTokens = 1 << 20;
 constexpr int kDeltaMaxSeqs = 65536;
 constexpr int kDeltaMaxHeads = 256;
-// Calls of few token rows run token by token: one sequence (32 value heads of
-// 128) takes 17.0 us in the chunked form whatever its length up to 64 (8 heads of
-// 64 10.8 us), in a graph, and 1.7 us and 0.43 us for each token in the recurrent
-// one (12.0 and 11.0 us at 24).  Further sequences add 3 us each to the chunked
-// form, where 4096 state rows take the SMs, and next to nothing to the
-// recurrent one: 4 of 7 tokens 8.5 against 23 us, 16 of 3 14.3 against 59 us.  The
-// lengths are not known here; where one sequence has all of the rows and the
-// others none, the rule loses (48 rows of one of 13, 32 against 15 us).
-bool few_rows(const moe_delta_dims &d, int N, int B) {
-  constexpr int kMostSeqs = 64;  // each warp looks at all of their bounds
-  if (B > kMostSeqs) return false;
-  const int more = 4 * (B - 1) * d.v_heads * d.v_dim / 4096;
-  return N <= 24 + (more < 24 ? more : 24);
-}
+// (each warp of the recurrent kernel looks at all bounds of such a call)
+constexpr int kRecurrentSeqs = 64;
 constexpr int kNormMaxWidth = 16384;
 constexpr int64_t kNormMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxStride = int64_t(1) << 31;  // elements: offsets stay far inside 63 bits
@@ -151,8 +139,9 @@ moe_status moe_delta_chunk(const moe_delta_dims *dims, const moe_delta_inputs *i
   if (B == 0) return MOE_OK;
   const DeltaSeqs seq = delta_seqs(cu_seqlens, N, B, N, slots, n_slots, state_in, state_out,
                                    workspace);
-  if (few_rows(*dims, N, B))
-    return cuda_status(launch_delta_recurrent(*dims, *in, seq, out, out_ld,
+  // no sequence can be longer: one kernel does
+  if (N <= kDeltaShort && B <= kRecurrentSeqs)
+    return cuda_status(launch_delta_recurrent(*dims, *in, seq, N, nullptr, out, out_ld,
                                               static_cast<cudaStream_t>(stream)));
   return cuda_status(launch_delta_chunk(*dims, *in, seq, workspace, out, out_ld,
                                         static_cast<cudaStream_t>(stream)));
@@ -172,7 +161,7 @@ moe_status moe_delta_step(const moe_delta_dims *dims, const moe_delta_inputs *in
   if (B == 0) return MOE_OK;
   const DeltaSeqs seq = delta_seqs(nullptr, B * T, B, T, slots, n_slots, state_in, state_out,
                                    workspace);
-  return cuda_status(launch_delta_recurrent(*dims, *in, seq, out, out_ld,
+  return cuda_status(launch_delta_recurrent(*dims, *in, seq, T, nullptr, out, out_ld,
                                             static_cast<cudaStream_t>(stream)));
 }
 

@@ -146,6 +146,40 @@ def test_chunk_more_work_than_blocks(env, lens, heads):
     assert torch.equal(again, out[rows]) and torch.equal(pool, S1)
 
 
+@pytest.mark.parametrize("heads,dims", [((2, 4), (128, 128)), ((4, 16), (64, 64))])
+def test_chunk_sequence_alone_and_in_a_batch(env, heads, dims):
+    """No bit of a sequence depends on the call it is part of: short ones and
+    long ones, among others of both kinds, some of them not finite."""
+    import torch
+    moe, dev = env
+    lens = [24, 25, 1, 0, 64, 200, 23, 3, 65, 130, 26, 2] + [5, 90] * 20
+    n, b = sum(lens), len(lens)
+    s = make(env, n, heads, dims, seed=11)
+    pool = states(env, b, heads, dims)
+    m = mixer(env, heads, dims, n, b)
+    S1 = torch.full_like(pool, 7.0)
+    out = m.chunk(**s, cu_seqlens=cu_of(env, lens), state_in=pool, state_out=S1)
+    assert m.status() == 0
+    ends = np.cumsum(lens)
+    for i in (0, 1, 2, 3, 4, 5, 6, 8, 10, b - 2, b - 1):
+        r = slice(ends[i] - lens[i], ends[i])
+        S2 = torch.empty_like(pool[:1])
+        o = m.chunk(**{x: t[r] for x, t in s.items()}, cu_seqlens=cu_of(env, [lens[i]]),
+                    state_in=pool[i:i + 1].clone(), state_out=S2)
+        assert torch.equal(o, out[r]) and torch.equal(S2[0], S1[i])
+    bad = {x: t.clone() for x, t in s.items()}
+    for i in (4, 6, b - 3):  # infinities and NaN in a few sequences
+        r = slice(ends[i] - lens[i], ends[i])
+        bad["v"][r] = float("inf")
+        bad["k"][r] = float("nan")
+    S2 = torch.full_like(pool, 7.0)
+    o = m.chunk(**bad, cu_seqlens=cu_of(env, lens), state_in=pool, state_out=S2)
+    for i in range(b):
+        if i not in (4, 6, b - 3):
+            r = slice(ends[i] - lens[i], ends[i])
+            assert torch.equal(o[r], out[r]) and torch.equal(S2[i], S1[i])
+
+
 def test_chunk_tiny_values_beside_large_ones(env):
     """A reset, then values far below those of the tokens before it: the
     prompt form keeps 2^-36 of the largest value of the same 64 tokens and state
