@@ -71,6 +71,7 @@ constexpr int kHeader = 256;      // status word, and these words
 enum {
   kFlagWord = 16,  // some bound of the call is bad: it does nothing
   kCountWord,      // records of the list
+  kGroupsWord,     // groups of 16 state rows that a CTA of the chain works on
   kNextWord,       // pieces of work that the chain's CTAs have asked for
 };
 constexpr int kPrepThreads = 256;
@@ -199,9 +200,11 @@ __device__ __forceinline__ float warp_max_pos(float v) {
 // What the second kernel has to do, by one CTA: a record {first row, tokens,
 // state slot, first chunk slot} per sequence that is not short, of 256 at a time
 // the longest first.  A call with a bad bound does nothing.
-__device__ void list_sequences(const DeltaSeqs &seq, uint32_t *head, int4 *list, int *lens) {
+__device__ void list_sequences(const DeltaSeqs &seq, int rows, int sms, uint32_t *head, int4 *list,
+                               int *lens) {
   const int tid = threadIdx.x;
-  int count = 0;
+  int count = 0, longest = 0;
+  long long chunks = 0;
   bool bad = false;
   for (int b0 = 0; b0 < seq.B; b0 += kPrepThreads) {
     const int b = b0 + tid;
@@ -222,13 +225,26 @@ __device__ void list_sequences(const DeltaSeqs &seq, uint32_t *head, int4 *list,
       for (int i = 0; i < min(kPrepThreads, seq.B - b0); ++i)
         rank += lens[i] > len || (lens[i] == len && i < tid);
       list[count + rank] = make_int4(r.start, len, r.slot, first_slot(r, b));
+      longest = max(longest, len), chunks += (len + kC - 1) / kC;
     }
     count += here;
     __syncthreads();
   }
   bad = __syncthreads_or(bad);
+  // Groups to a CTA.  One alone takes 0.8 of the time for a chunk, but all work
+  // twice as many CTAs: for the better where the longest sequence decides, that
+  // is where its chunks are more than 1.6 times an SM's share of them all with
+  // two groups (2048 tokens of 8 heads of 128 58.8 against 69.4 us).
+  using Wide = unsigned long long;
+  Wide *sum = reinterpret_cast<Wide *>(lens);
+  if (tid == 0) sum[0] = sum[1] = 0;
+  __syncthreads();
+  if (chunks) atomicAdd(&sum[0], static_cast<Wide>(chunks));
+  if (longest) atomicMax(&sum[1], static_cast<Wide>((longest + kC - 1) / kC));
+  __syncthreads();
   if (tid == 0) {
     head[kFlagWord] = bad, head[kCountWord] = count, head[kNextWord] = 0;
+    head[kGroupsWord] = 5 * sum[1] * sms > 8 * sum[0] * (rows / 32) ? 1 : 2;
     if (bad) set_status(seq.status, MOE_DEV_BAD_INDEX);
   }
 }
@@ -246,8 +262,8 @@ __device__ void list_sequences(const DeltaSeqs &seq, uint32_t *head, int4 *list,
 // (2048 tokens 97 against 93 us).
 template <int DK>
 __global__ void __launch_bounds__(kPrepThreads, kPrepCtas)
-delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int heads, uint8_t *ws,
-                  int4 *list, uint8_t *ws_key, uint8_t *ws_head) {
+delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int heads, int sms,
+                  uint8_t *ws, int4 *list, uint8_t *ws_key, uint8_t *ws_head) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   PrepSmem<DK> &sm = *reinterpret_cast<PrepSmem<DK> *>(smem_raw);
   __shared__ float red[kPrepThreads / 32];
@@ -258,7 +274,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
   early_begin();
   if (slot < 0) {  // the first CTAs have no chunk
     if (blockIdx.y == 0)
-      list_sequences(seq, reinterpret_cast<uint32_t *>(ws), list,
+      list_sequences(seq, d.v_heads * d.v_dim, sms, reinterpret_cast<uint32_t *>(ws), list,
                      reinterpret_cast<int *>(smem_raw));
     return;
   }
@@ -632,10 +648,9 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
 // ------------------------------------------------------------------ chain
 
 // How the chain runs: kHalves chain warps and two output warps per group of 16
-// state rows, kGroups groups per CTA, one CTA per SM.
+// state rows, up to kGroups groups per CTA, one CTA per SM.
 constexpr int kHalves = 2;
 constexpr int kGroups = 2;
-constexpr int kRows = 16 * kGroups;  // state rows of a CTA
 
 template <int DK>
 struct Chain {
@@ -727,43 +742,54 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
     for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s], 4);
     ptx::fence_mbar_init();
   }
-  // (all divisions by sizes are done before the wait, or a piece ahead)
-  const int tiles = d.v_dim / kRows, per = d.v_heads * tiles, ratio = d.v_heads / d.qk_heads;
-  const int seq_of = blockIdx.x / per;
-  int h = blockIdx.x / tiles % d.v_heads, row = blockIdx.x % tiles * kRows;
-  int key_head = h / ratio;
+  const int ratio = d.v_heads / d.qk_heads, grid = static_cast<int>(gridDim.x);
+  // pieces per sequence with one group to a CTA
+  const int most = d.v_heads * (d.v_dim / 16), bid = static_cast<int>(blockIdx.x);
+  const int one = bid / most, two = min(2 * bid / most, seq.B - 1);
   early_begin();
-  // The work: kRows state rows of one head of one sequence are a piece, index
-  // (sequence of the list, head, rows).  A CTA's pieces number 0, 1 and 2 are
-  // given; for those after it asks, through output warp 0, which of them is
-  // next.  That warp publishes number k + 3 when it begins number k, so that
-  // all know it after that chunk's bar_x.
+  // The work: the state rows of a CTA, of one head of one sequence, are a piece,
+  // index (sequence of the list, head, rows).  A CTA's pieces number 0, 1 and 2
+  // are given; for those after it asks, through the first output warp, which of
+  // them is next.  That warp publishes number k + 3 when it begins number k, so
+  // that all know it after that chunk's bar_x.
   uint32_t *head = reinterpret_cast<uint32_t *>(ws);
   const uint32_t bad = head[kFlagWord];
-  const int total = static_cast<int>(head[kCountWord]) * per;
-  const int4 first = list[seq_of];  // (meaningless past the total)
+  const int count = static_cast<int>(head[kCountWord]);
+  const int groups_on = static_cast<int>(head[kGroupsWord]);
+  const int4 first_one = list[one], first_two = list[two];  // (meaningless past the count)
   if (bad) return;
-  const int grid = static_cast<int>(gridDim.x);
+  const int4 first = groups_on == 1 ? first_one : first_two;
+  const int rows = 16 * groups_on, per = groups_on == 1 ? most : most / 2, total = count * per;
+  const int tiles = d.v_dim >> (3 + groups_on);  // a power of two
+  struct Place {
+    int b, h, row;
+  };
+  const auto place_of = [&](int index) {
+    const int t = index >> (31 - __clz(tiles)), b = t / d.v_heads;
+    return Place{b, t - b * d.v_heads, (index & (tiles - 1)) * rows};
+  };
   const auto piece_at = [&](int k) {
-    return k < 3 ? static_cast<int>(blockIdx.x) + k * grid : queue[k % C::kQueue];
+    return k < 3 ? bid + k * grid : queue[k % C::kQueue];
   };
   __syncthreads();
 
-  // Chain warps 2 g, 2 g + 1 (half of the key channels each), output warps
-  // kHalves kGroups + 2 g, + 1 (half of the tokens each).  The
-  // warps meet three times per chunk: all of the CTA at bar_x (the shares of S
-  // k^T, the copy of S and beta v are there; nobody reads the previous chunk's
-  // stage any more), a group's chain warps at bar_y (x is there), a group at
-  // bar_w (u is there, and the next chunk's operands).  Every buffer of the
-  // group is written before one of them, read after it, and free again when
-  // its writer comes back to it: x_part, y and v_max x|y, s_frag x|w, x_frag
-  // y|w, w_frag and u_frag w|next x.
+  // Group g's chain warps are 2 g and 2 g + 1 (half of the key channels each), its
+  // output warps 4 + 2 g and 5 + 2 g (half of the tokens each); those of a group
+  // alone are 6 and 7, so that each warp has a scheduler, and the others leave.
+  // The warps meet three times per chunk: all of the CTA
+  // at bar_x (the shares of S k^T, the copy of S and beta v are there; nobody
+  // reads the previous chunk's stage any more), a group's chain warps at bar_y (x
+  // is there), a group at bar_w (u is there, and the next chunk's operands).
+  // Every buffer of the group is written before one of them, read after it, and
+  // free again when its writer comes back to it: x_part, y and v_max x|y, s_frag
+  // x|w, x_frag y|w, w_frag and u_frag w|next x.
   const bool chain = warp < kHalves * kGroups;
-  const int group = chain ? warp / kHalves : (warp - kHalves * kGroups) / 2;
-  const int part = warp % kHalves;
+  const int group = chain || groups_on == 1 ? (warp >> 1) % 3 : (warp >> 1) - 2, part = warp & 1;
+  if (group >= groups_on) return;
   Group &gs = groups[group];
   const int bar_x = 0, bar_y = 1 + 2 * group, bar_w = bar_y + 1, bar_out = 1 + 2 * kGroups;
-  constexpr int kAll = C::kThreads, kGroup = 32 * (kHalves + 2);
+  constexpr int kGroup = 32 * (kHalves + 2);
+  const int all = kGroup * groups_on;
   const int g = lane >> 2, t = lane & 3;
   // B fragments of two n8 tiles from rows (plain) or columns (trans) of a tile
   const int b_row = (lane & 7) + ((lane >> 4) << 3), b_piece = (lane >> 3) & 1;
@@ -776,15 +802,16 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
     const auto owner = [](int np) { return min(np, 3 - np); };
     int st = 0, index = piece_at(0);
     int4 record = first;
+    Place place = place_of(index);
     if (index < total) bar_sync(bar_w, kGroup);  // the first chunk's operands are there
     for (int k = 0; index < total; ++k) {
       const int chunks = (record.y + kC - 1) / kC;
-      const int64_t line = (static_cast<int64_t>(record.z) * d.v_heads + h) * d.v_dim + row;
-      const int64_t at = (line + group * 16 + g) * DK + part * C::kCols + 2 * t;
+      const int64_t state = static_cast<int64_t>(record.z) * d.v_heads + place.h;
+      const int64_t at = (state * d.v_dim + place.row + group * 16 + g) * DK + part * C::kCols + 2 * t;
       index = piece_at(k + 1);
       if (index < total) {
-        record = list[index / per];
-        h = index / tiles % d.v_heads, row = index % tiles * kRows;
+        place = place_of(index);
+        record = list[place.b];
       }
       Acc S[2 * C::kSteps];
 #pragma unroll
@@ -866,7 +893,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
             cc[j][q] =
                 *reinterpret_cast<const float2 *>(vec + kVecC * kC + 16 * own[j] + 8 * q + 2 * t);
         const float4 misc = *reinterpret_cast<const float4 *>(vec + kVecMisc * kC);
-        bar_sync(bar_x, kAll);
+        bar_sync(bar_x, all);
         // x_i = beta_i v_i - c_i (S k_i); vec holds -c_i.  Its scale comes from
         // norms, so that the warps agree on it without another exchange:
         // |S k_i| <= |S| |k_i|, where k_i (scaled) stays below 2^15 and each
@@ -1005,7 +1032,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
   // Output warps: o_i = rho_i gamma_i (S q_i) + sum_j P_ij u_j.  They also bring
   // in the group's values, as beta v in the chain's accumulator layout.  Each
   // has two of the four 16-token blocks, an equal share of P's triangle.
-  const int side = (warp - kHalves * kGroups) & 1;
+  const int side = part;
   const int own[2] = {side, 3 - side};
   const int my_row = lane >> 1;  // of a block, and the half row this lane copies
   const uint32_t v_smem = ptx::smem_u32(gs.v[0]), v_to = v_smem + row32_at(my_row, lane & 1);
@@ -1042,10 +1069,11 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
     }
     gs.v_max[side][lane] = make_float2(quad_max(top), quad_max(low));
   };
-  // This warp's copy of every chunk: k or T's part into ring a, q or P's into
-  // ring b.
-  static_assert(2 * kGroups == 4, "an output warp for each copy of a chunk");
-  const int copy = warp - kHalves * kGroups;
+  // Of every chunk's four copies -- k or T's part into ring a, q or P's into
+  // ring b -- this warp's first lanes have one each.
+  const int mine = 2 / groups_on;
+  const bool copies = lane < mine;
+  const int copy = (2 * group + side) * mine + (copies ? lane : 0);
   const bool into_b = copy & 2, of_head = copy & 1;
   const size_t from_step = of_head ? static_cast<size_t>(d.v_heads) * kHeadBlob
                                    : static_cast<size_t>(d.qk_heads) * kKeyBlob<DK>;
@@ -1059,6 +1087,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
   // tokens and where their outputs go wait in line.
   int ahead = -1, left = 0, index = piece_at(0);
   int4 record = first;
+  Place place = place_of(index);
   const uint8_t *from = nullptr;
   const moe_bf16 *v_src = nullptr, *v_now = nullptr;  // v_now, v_left: the chunk brought in last
   int v_left = 0;
@@ -1068,7 +1097,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
     const bool begins = left <= 0 && index < total;
     if (begins) {
       ++ahead;
-      const int dv = row + group * 16;
+      const int h = place.h, dv = place.row + group * 16;
       const bool second = line_len[0] > 0;
       moe_bf16 *dst = out + (static_cast<int64_t>(record.x) + my_row) * out_ld + h * d.v_dim + dv +
                       (lane & 1) * 8;
@@ -1077,7 +1106,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
       const size_t base = record.w;
       left = record.y;
       from = of_head ? ws_head + (base * d.v_heads + h) * kHeadBlob + (into_b ? kPartA : 0)
-                     : ws_key + (base * d.qk_heads + key_head) * kKeyBlob<DK> +
+                     : ws_key + (base * d.qk_heads + h / ratio) * kKeyBlob<DK> +
                            (into_b ? kKeyTile : 0);
       v_src = in.v + (static_cast<int64_t>(record.x) + my_row) * in.v_ld + h * d.v_dim + dv +
               (lane & 1) * 8;
@@ -1092,7 +1121,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
     v_now = v_src, v_left = left;
     if (left > 0) {
       if (alive) {
-        if (lane == 0) {
+        if (copies) {
           mbar_expect(&full[stage], copy_bytes);
           bulk_load(to + stage * to_step, from, copy_bytes, &full[stage]);
         }
@@ -1103,8 +1132,8 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
     if (begins) {
       index = piece_at(ahead + 1);
       if (index < total) {
-        record = list[index / per];
-        h = index / tiles % d.v_heads, row = index % tiles * kRows, key_head = h / ratio;
+        place = place_of(index);
+        record = list[place.b];
       }
     }
   };
@@ -1126,7 +1155,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
   // the piece worked on: its number, its tokens from this chunk on
   int number = -1, now = 0;
   moe_bf16 *o_dst = nullptr;
-  const bool asks = copy == 0 && lane == 0;
+  const bool asks = group == 0 && side == 0 && lane == 0;
   int asked = total;  // its answer: piece number + 3
   if (asks && total > 3 * grid) asked = 3 * grid + atomicAdd(&head[kNextWord], 1u);
   const auto begin_next = [&] {
@@ -1171,7 +1200,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
         ldsm4(bb[s & 1][j], qt + tile_at<DK>(16 * own[j] + b_row, 2 * s + b_piece));
     };
     load_q(0);
-    bar_sync(bar_x, kAll);
+    bar_sync(bar_x, all);
     // The shares of S have scales of their own: brought to the largest.
     uint32_t a[DK / 16][4];
 #pragma unroll
@@ -1261,11 +1290,11 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
   // Copies in flight land before the CTA's shared memory is given up.  After a
   // wait that gave up, some of the four may have issued one more than the
   // others, whose arrivals its barrier then still waits for.
-  if (lane == 0) fed_by[copy] = fed;
-  bar_sync(bar_out, 4 * 32);
-  if (lane == 0) {
-    const int all = max(max(fed_by[0], fed_by[1]), max(fed_by[2], fed_by[3]));
-    for (; fed < all; ++fed) ptx::mbar_arrive(&full[fed % kStages]);
+  if (copies) fed_by[copy] = fed;
+  bar_sync(bar_out, 64 * groups_on);
+  if (copies) {
+    const int last = max(max(fed_by[0], fed_by[1]), max(fed_by[2], fed_by[3]));
+    for (; fed < last; ++fed) ptx::mbar_arrive(&full[fed % kStages]);
     int ignore = 0;
     for (int c = max(0, fed - kStages); c < fed; ++c)
       ptx::mbar_wait(&full[c % kStages], (c / kStages) & 1, &ignore, ptx::kDrainBudgetNs);
@@ -1295,7 +1324,7 @@ cudaError_t launch_chain(const moe_delta_dims &d, const moe_delta_inputs &in, co
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(delta_chain_kernel<DK>, C::kSmem, done);
   if (e != cudaSuccess) return e;
-  const int pieces = seq.B * d.v_heads * (d.v_dim / kRows), sms = tc_sm_count();
+  const int pieces = seq.B * d.v_heads * (d.v_dim / 16), sms = tc_sm_count();
   return launch_early(delta_chain_kernel<DK>, dim3(pieces < sms ? pieces : sms), C::kThreads,
                       C::kSmem, s, d, in, seq, ws, list, ws_key, ws_head, out, out_ld,
                       tc_wait_budget_ns());
@@ -1326,8 +1355,8 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
     for (int n = 2; n <= kPrepHeads; ++n)
       if (ratio % n == 0) heads = n;
   const dim3 grid(static_cast<unsigned>(slots) + 1, d.v_heads / heads);
-  e = launch_early(delta_prep_kernel<DK>, grid, kPrepThreads, kSmem, s, d, in, seq, heads, ws,
-                   list, ws_key, ws_head);
+  e = launch_early(delta_prep_kernel<DK>, grid, kPrepThreads, kSmem, s, d, in, seq, heads,
+                   tc_sm_count(), ws, list, ws_key, ws_head);
   if (e != cudaSuccess) return e;
   e = launch_chain<DK>(d, in, seq, ws, list, ws_key, ws_head, out, out_ld, s);
   if (e != cudaSuccess || !seq.cu_seqlens) return e;  // the one sequence is longer
