@@ -99,14 +99,27 @@ __device__ __forceinline__ uint32_t tri_at(int i, int piece) {
   return static_cast<uint32_t>(block_of(i >> 4, piece >> 1) * kBlock) + row32_at(i & 15, piece & 1);
 }
 
-// Sequence b's first chunk slot: chunks of different sequences never share
-// one, whatever the lengths.
-__device__ __forceinline__ int slot_base(const DeltaSeqs &s, int b) {
-  return (s.cu_seqlens ? s.cu_seqlens[b] : b * s.T) / kC + b;
+// Where the chunks of a call lie: `count` slots, a sequence's first one at its
+// first row / tokens + each * its number.  Chunks of different sequences never
+// share one, whatever the lengths: with (64, 1), and with (kDeltaShort + 1, 0),
+// since only longer sequences have chunks and no more than a (kDeltaShort + 1)th
+// of their tokens.  Whichever takes fewer.
+struct ChunkSlots {
+  int tokens, each;
+  size_t count;
+};
+ChunkSlots chunk_slots(int N, int B) {
+  const size_t by_seq = static_cast<size_t>(N) / kC + B;
+  const size_t by_row = static_cast<size_t>(N) / (kDeltaShort + 1) + 1;
+  return by_row < by_seq ? ChunkSlots{kDeltaShort + 1, 0, by_row} : ChunkSlots{kC, 1, by_seq};
 }
 
-__device__ __forceinline__ int first_slot(const DeltaSeqRange &r, int b) {
-  return r.start / kC + b;
+__device__ __forceinline__ int slot_base(const DeltaSeqs &s, const ChunkSlots &at, int b) {
+  return (s.cu_seqlens ? s.cu_seqlens[b] : b * s.T) / at.tokens + at.each * b;
+}
+
+__device__ __forceinline__ int first_slot(const DeltaSeqRange &r, const ChunkSlots &at, int b) {
+  return r.start / at.tokens + at.each * b;
 }
 
 // ------------------------------------------------------------------- prep
@@ -200,8 +213,8 @@ __device__ __forceinline__ float warp_max_pos(float v) {
 // What the second kernel has to do, by one CTA: a record {first row, tokens,
 // state slot, first chunk slot} per sequence that is not short, of 256 at a time
 // the longest first.  A call with a bad bound does nothing.
-__device__ void list_sequences(const DeltaSeqs &seq, int rows, int sms, uint32_t *head, int4 *list,
-                               int *lens) {
+__device__ void list_sequences(const DeltaSeqs &seq, const ChunkSlots &at, int rows, int sms,
+                               uint32_t *head, int4 *list, int *lens) {
   const int tid = threadIdx.x;
   int count = 0, longest = 0;
   long long chunks = 0;
@@ -224,7 +237,7 @@ __device__ void list_sequences(const DeltaSeqs &seq, int rows, int sms, uint32_t
       int rank = 0;
       for (int i = 0; i < min(kPrepThreads, seq.B - b0); ++i)
         rank += lens[i] > len || (lens[i] == len && i < tid);
-      list[count + rank] = make_int4(r.start, len, r.slot, first_slot(r, b));
+      list[count + rank] = make_int4(r.start, len, r.slot, first_slot(r, at, b));
       longest = max(longest, len), chunks += (len + kC - 1) / kC;
     }
     count += here;
@@ -262,8 +275,8 @@ __device__ void list_sequences(const DeltaSeqs &seq, int rows, int sms, uint32_t
 // (2048 tokens 97 against 93 us).
 template <int DK>
 __global__ void __launch_bounds__(kPrepThreads, kPrepCtas)
-delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int heads, int sms,
-                  uint8_t *ws, int4 *list, uint8_t *ws_key, uint8_t *ws_head) {
+delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, ChunkSlots slots, int heads,
+                  int sms, uint8_t *ws, int4 *list, uint8_t *ws_key, uint8_t *ws_head) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   PrepSmem<DK> &sm = *reinterpret_cast<PrepSmem<DK> *>(smem_raw);
   __shared__ float red[kPrepThreads / 32];
@@ -274,7 +287,7 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
   early_begin();
   if (slot < 0) {  // the first CTAs have no chunk
     if (blockIdx.y == 0)
-      list_sequences(seq, d.v_heads * d.v_dim, sms, reinterpret_cast<uint32_t *>(ws), list,
+      list_sequences(seq, slots, d.v_heads * d.v_dim, sms, reinterpret_cast<uint32_t *>(ws), list,
                      reinterpret_cast<int *>(smem_raw));
     return;
   }
@@ -284,12 +297,12 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
   int b = 0, hi = seq.B;
   while (hi - b > 1) {
     const int step = (hi - b + 31) >> 5, at = b + lane * step;
-    const bool before = at < hi && slot_base(seq, at) <= slot;
+    const bool before = at < hi && slot_base(seq, slots, at) <= slot;
     b += step * (31 - __clz(__ballot_sync(kFull, before) | 1u));
     hi = min(hi, b + step);
   }
   const DeltaSeqRange r = delta_seq_range(seq, b);
-  const int chunk = slot - first_slot(r, b);
+  const int chunk = slot - first_slot(r, slots, b);
   if (!r.ok || r.len <= kDeltaShort || chunk < 0 || chunk >= (r.len + kC - 1) / kC) return;
   const int left = min(kC, r.len - chunk * kC);  // tokens of this chunk
   const int64_t row0 = static_cast<int64_t>(r.start) + chunk * kC;
@@ -627,7 +640,8 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, int head
         if (p / 2 <= i / 16) {
           uint32_t hw[4], lw[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) split_h2(mul2(v[e][j], make_float2(mult, mult)), hw[j], lw[j]);
+          for (int j = 0; j < 4; ++j)
+            split_h2(mul2(v[e][j], make_float2(mult, mult)), hw[j], lw[j]);
           const uint32_t at = tri_at(i, p);
           *reinterpret_cast<uint4 *>(sm.head + at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
           *reinterpret_cast<uint4 *>(sm.head + kTri + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
@@ -784,7 +798,8 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
   // free again when its writer comes back to it: x_part, y and v_max x|y, s_frag
   // x|w, x_frag y|w, w_frag and u_frag w|next x.
   const bool chain = warp < kHalves * kGroups;
-  const int group = chain || groups_on == 1 ? (warp >> 1) % 3 : (warp >> 1) - 2, part = warp & 1;
+  const int part = warp & 1;
+  const int group = chain || groups_on == 1 ? (warp >> 1) % 3 : (warp >> 1) - 2;
   if (group >= groups_on) return;
   Group &gs = groups[group];
   const int bar_x = 0, bar_y = 1 + 2 * group, bar_w = bar_y + 1, bar_out = 1 + 2 * kGroups;
@@ -807,7 +822,8 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
     for (int k = 0; index < total; ++k) {
       const int chunks = (record.y + kC - 1) / kC;
       const int64_t state = static_cast<int64_t>(record.z) * d.v_heads + place.h;
-      const int64_t at = (state * d.v_dim + place.row + group * 16 + g) * DK + part * C::kCols + 2 * t;
+      const int64_t at =
+          (state * d.v_dim + place.row + group * 16 + g) * DK + part * C::kCols + 2 * t;
       index = piece_at(k + 1);
       if (index < total) {
         place = place_of(index);
@@ -1317,8 +1333,8 @@ cudaError_t allow_smem(F kernel, int bytes, std::atomic<uint64_t> &done) {
 
 template <int DK>
 cudaError_t launch_chain(const moe_delta_dims &d, const moe_delta_inputs &in, const DeltaSeqs &seq,
-                         uint8_t *ws, const int4 *list, const uint8_t *ws_key, const uint8_t *ws_head,
-                         moe_bf16 *out, int64_t out_ld, cudaStream_t s) {
+                         uint8_t *ws, const int4 *list, const uint8_t *ws_key,
+                         const uint8_t *ws_head, moe_bf16 *out, int64_t out_ld, cudaStream_t s) {
   using C = Chain<DK>;
   static_assert(C::kSmem <= 227 * 1024, "shared memory of one SM");
   static std::atomic<uint64_t> done{0};
@@ -1336,10 +1352,10 @@ size_t list_bytes(int B) { return (static_cast<size_t>(B) * sizeof(int4) + 255) 
 template <int DK>
 cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const DeltaSeqs &seq,
                    uint8_t *ws, moe_bf16 *out, int64_t out_ld, cudaStream_t s) {
-  const size_t slots = static_cast<size_t>(seq.N) / kC + seq.B;
+  const ChunkSlots slots = chunk_slots(seq.N, seq.B);
   int4 *list = reinterpret_cast<int4 *>(ws + kHeader);
   uint8_t *ws_key = ws + kHeader + list_bytes(seq.B);
-  uint8_t *ws_head = ws_key + slots * d.qk_heads * kKeyBlob<DK>;
+  uint8_t *ws_head = ws_key + slots.count * d.qk_heads * kKeyBlob<DK>;
   constexpr int kSmem = sizeof(PrepSmem<DK>);
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(delta_prep_kernel<DK>, kSmem, done);
@@ -1351,11 +1367,11 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
   // of 6007 tokens 244 and 259, 2048 tokens 89.5 and 90.3; of 67 tokens,
   // 20.6 and 18.6.
   int heads = 1;
-  if (slots * d.qk_heads >= static_cast<size_t>(kPrepCtas * tc_sm_count()))
+  if (slots.count * d.qk_heads >= static_cast<size_t>(kPrepCtas * tc_sm_count()))
     for (int n = 2; n <= kPrepHeads; ++n)
       if (ratio % n == 0) heads = n;
-  const dim3 grid(static_cast<unsigned>(slots) + 1, d.v_heads / heads);
-  e = launch_early(delta_prep_kernel<DK>, grid, kPrepThreads, kSmem, s, d, in, seq, heads,
+  const dim3 grid(static_cast<unsigned>(slots.count) + 1, d.v_heads / heads);
+  e = launch_early(delta_prep_kernel<DK>, grid, kPrepThreads, kSmem, s, d, in, seq, slots, heads,
                    tc_sm_count(), ws, list, ws_key, ws_head);
   if (e != cudaSuccess) return e;
   e = launch_chain<DK>(d, in, seq, ws, list, ws_key, ws_head, out, out_ld, s);
@@ -1367,7 +1383,7 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
 }  // namespace
 
 size_t delta_chunk_workspace(const moe_delta_dims &d, int N, int B) {
-  const size_t slots = static_cast<size_t>(N) / kC + B;
+  const size_t slots = chunk_slots(N, B).count;
   const size_t key = d.qk_dim == 128 ? kKeyBlob<128> : kKeyBlob<64>;
   return kHeader + list_bytes(B) +
          slots * (d.qk_heads * key + static_cast<size_t>(d.v_heads) * kHeadBlob);
