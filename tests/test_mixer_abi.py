@@ -81,6 +81,19 @@ def test_delta_sizes(moe):
     assert moe.moe_delta_workspace_bytes(d, -1, 1) == 0
 
 
+def test_delta_workspace_grows_with_rows_and_sequences(moe):
+    """More of either never needs less, so that the largest call's workspace
+    serves all; short sequences take none of it each."""
+    d = delta_dims(moe)
+    size = lambda n, b: moe.moe_delta_workspace_bytes(d, n, b)
+    for n in (0, 1, 24, 25, 63, 64, 100, 1000, 4096):
+        for b in (1, 2, 3, 40, 41, 300):
+            assert size(n, b) <= size(n + 1, b) and size(n, b) <= size(n, b + 1)
+    # records of 16 bytes a sequence, and a chunk slot per 25 rows
+    slot = size(64, 1) - size(0, 1)
+    assert size(256, 256) <= size(0, 1) + 256 * 16 + 256 // 25 * slot
+
+
 def norm(moe, **kw):
     base = dict(rows=4, width=128, inner=1, x=FAKE, gamma_post=2 * FAKE, gate=3 * FAKE,
                 resid_in=4 * FAKE, gamma_pre=5 * FAKE, resid_out=6 * FAKE, x_next=7 * FAKE,
