@@ -31,7 +31,7 @@
 // What bounds it (GB300, 32 value heads of 128 x 128 on 16 key heads).  A chunk
 // of the chain takes 1.73 us on whatever SM it runs, so one prompt of 8192
 // tokens takes 222 us there and 82 us in the preparation, of 31 us for the
-// bytes.  A CTA's pieces of work (32 state rows of one sequence) follow one
+// bytes.  A CTA's pieces of work (32 state rows of one sequence, or 16) follow one
 // another, longest sequences first, with the next one's chunks, values and
 // state on their way during the last one's chunks: 240 us for 13 sequences of
 // 6007 tokens in all and 116 us for 32 of 64, against 244 and 137 us with a
