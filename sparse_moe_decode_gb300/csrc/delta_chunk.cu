@@ -919,10 +919,10 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
         const float2 vm = make_float2(fmaxf(va.x, vb.x), fmaxf(va.y, vb.y));
         const float gamma = misc.x, tau = misc.y, back = misc.y * misc.z;
         const float reach = misc.w * (0x1p30f * (C::kCols == 32 ? 5.66f : 8.0f));  // sqrt
+        // (A run that writes nothing has a bound of 0.)
         float n0, n1, j0, j1;
-        pow2_above(fmaf(reach, si.x, vm.x), j0, n0);
-        pow2_above(fmaf(reach, si.y, vm.y), j1, n1);
-        n0 *= 0x1p15f, n1 *= 0x1p15f, j0 *= 0x1p-15f, j1 *= 0x1p-15f;
+        pow2_scale(fmaf(reach, si.x, vm.x), n0, j0);
+        pow2_scale(fmaf(reach, si.y, vm.y), n1, j1);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float4 y[2] = {gs.x_part[own[j]][0][lane], gs.x_part[own[j]][1][lane]};

@@ -505,3 +505,78 @@ def test_state_offsets_beyond_32_bits(env):
         out = getattr(m, api)(**s, state_in=pool, state_out=pool, slots=slots,
                               **({"cu_seqlens": cu_of(env, [n])} if api == "chunk" else {}))
         check_seq(s, slice(0, n), last, out, pool[4199], dims)
+
+
+def _no_writes(s):
+    s["beta"].zero_()
+
+
+def _last_writes_nothing(s):
+    s["beta"][-1] = 0.0
+
+
+def _run_writes_nothing(s):
+    s["beta"][64:128] = 0.0
+
+
+def _zeros(s):
+    for x in "qkv":
+        s[x].zero_()
+
+
+def _padding(rows):
+    def apply(s):
+        for x in "qkv":
+            s[x][:rows] = 0.0
+    return apply
+
+
+def _resets_beside_zero_channels(s):
+    s["g"][0] = -float("inf")
+    s["g"][64] = -1000.0
+    s["v"][:64, :, 3] = 0.0
+    s["v"][64:128, 1] = 0.0
+
+
+def _silent_channels(s):
+    s["v"][:, :, 5] = 0.0
+    s["v"][:64, 1] = 0.0
+    s["beta"].mul_(0.005)
+    s["g"][:] = -0.02
+
+
+def _tiny_values(s):
+    s["v"].mul_(2.0 ** -118)
+
+
+def check_both_forms(env, edit, n, dims, state):
+    """A sequence in chunks and token by token, each as the definition has it."""
+    import torch
+    heads = (2, 4)
+    s = make(env, n, heads, dims, seed=12)
+    edit(s)
+    run_chunk(env, s, [n], heads, dims, state=state)
+    m = mixer(env, heads, dims, n, 1)
+    S0 = states(env, 1, heads, dims) if state else None
+    S1 = torch.empty_like(states(env, 1, heads, dims))
+    out = m.step(**s, state_in=S0, state_out=S1, tokens=n)
+    check_seq(s, slice(0, n), torch.zeros_like(S1[0]) if S0 is None else S0[0], out, S1[0], dims)
+
+
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("dims", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("edit,n", [
+    (_no_writes, 70), (_no_writes, 64), (_last_writes_nothing, 65), (_last_writes_nothing, 129),
+    (_run_writes_nothing, 200), (_zeros, 70), (_padding(64), 130), (_padding(100), 160),
+    (_resets_beside_zero_channels, 150), (_silent_channels, 140)])
+def test_chunk_where_little_or_nothing_is_written(env, edit, n, dims, state):
+    """Runs of 64 tokens whose corrections are zero or nearly so (masked and
+    padded tokens, zero channels), with a carried state and without."""
+    check_both_forms(env, edit, n, dims, state)
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (64, 128), (128, 64), (128, 128)])
+def test_chunk_values_near_the_smallest(env, dims):
+    """(From a zero state: beside a larger one they would be below the prompt
+    form's floor.)"""
+    check_both_forms(env, _tiny_values, 100, dims, False)
