@@ -77,6 +77,12 @@ enum {
 constexpr int kPrepThreads = 256;
 constexpr int kPrepCtas = 3;      // of the first kernel on an SM
 
+// Products with k, q or P under their scales can be 2^17 times their true size:
+// they leave the accumulators 2^16 smaller, and the factors of the tokens, which
+// they meet next, are so much larger.  (The factors first instead: 8192 tokens 315
+// against 312.5 us.)
+constexpr float kUp = 0x1p16f, kDown = 0x1p-16f;
+
 template <int DK>
 constexpr int kKeyBlob = 2 * kC * DK * 2;  // per (chunk, key head): k, then q, as fp16
 
@@ -467,10 +473,10 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, ChunkSlo
       float up, down;
       pow2_above(dmax, up, down);
       *reinterpret_cast<float2 *>(vec + kVecBeta * kC + i) = be;
-      *reinterpret_cast<float2 *>(vec + kVecC * kC + i) = cc;
+      *reinterpret_cast<float2 *>(vec + kVecC * kC + i) = mul2(cc, make_float2(kUp, kUp));
       *reinterpret_cast<float2 *>(vec + kVecD * kC + i) = make_float2(dd.x * down, dd.y * down);
       *reinterpret_cast<float2 *>(vec_b + kVecO * kC + i) =
-          make_float2(rho.x * gamma.x, rho.y * gamma.y);
+          make_float2(rho.x * gamma.x * kUp, rho.y * gamma.y * kUp);
       if (lane == 31) {
         vec[kVecMisc * kC + kGamma] = gamma.y;
         vec[kVecMisc * kC + kDUp] = up;
@@ -501,7 +507,10 @@ delta_prep_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, ChunkSlo
         pow2_above(fabsf(f0) * kmax, up0, s0);
         pow2_above(fabsf(f1) * kmax, up1, s1);
         s0 *= 0x1p-19f, s1 *= 0x1p-19f;
-        if (t == 0) vec_b[kVecP * kC + i0] = up0 * 0x1p19f, vec_b[kVecP * kC + i1] = up1 * 0x1p19f;
+        if (t == 0) {
+          vec_b[kVecP * kC + i0] = up0 * (0x1p19f * kUp);
+          vec_b[kVecP * kC + i1] = up1 * (0x1p19f * kUp);
+        }
       }
       f0 *= s0, f1 *= s1;
       const float a0 = f0 * sm.row[i0], a1 = f1 * sm.row[i1];
@@ -876,13 +885,14 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
             mma16(X[2 * np + 1], lo, bb[np][2], bb[np][3]);
           }
         }
+        const float x0 = i0 * kDown, x1 = i1 * kDown;
         Acc mine[2][2];
 #pragma unroll
         for (int np = 0; np < 4; ++np)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             Acc &x = X[2 * np + q];
-            x.top = mul2(x.top, both(i0)), x.low = mul2(x.low, both(i1));
+            x.top = mul2(x.top, both(x0)), x.low = mul2(x.low, both(x1));
             if (owner(np) != part)
               gs.x_part[np][q][lane] = make_float4(x.top.x, x.top.y, x.low.x, x.low.y);
 #pragma unroll
@@ -910,7 +920,7 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
                 *reinterpret_cast<const float2 *>(vec + kVecC * kC + 16 * own[j] + 8 * q + 2 * t);
         const float4 misc = *reinterpret_cast<const float4 *>(vec + kVecMisc * kC);
         bar_sync(bar_x, all);
-        // x_i = beta_i v_i - c_i (S k_i); vec holds -c_i.  Its scale comes from
+        // x_i = beta_i v_i - c_i (S k_i); vec holds -c_i 2^16.  Its scale comes from
         // norms, so that the warps agree on it without another exchange:
         // |S k_i| <= |S| |k_i|, where k_i (scaled) stays below 2^15 and each
         // share of S below 2^15 i0 per element.
@@ -1257,15 +1267,15 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
         const int col = 16 * own[j] + 8 * q + 2 * t;
         const float2 oq = *reinterpret_cast<const float2 *>(vec + kVecO * kC + col);
         pi[j][q] = *reinterpret_cast<const float2 *>(vec + kVecP * kC + col);
-        O[j][q].top = mul2(mul2(O[j][q].top, both(most.x)), oq);
-        O[j][q].low = mul2(mul2(O[j][q].low, both(most.y)), oq);
+        O[j][q].top = mul2(mul2(O[j][q].top, both(most.x * kDown)), oq);
+        O[j][q].low = mul2(mul2(O[j][q].low, both(most.y * kDown)), oq);
       }
     const uint32_t next_parity = next ? parity : parity ^ 1;
     if constexpr (!kLate) bring_next();
     if (fed > n + 1) wait_full(next, next_parity);
     bar_sync(bar_w, kGroup);
     if constexpr (kLate) bring_next();
-    const float2 ui = gs.u_inv[lane];
+    const float2 ui = mul2(gs.u_inv[lane], both(kDown));
     Acc I[2][2] = {};
     uint32_t uf[4][4];
 #pragma unroll

@@ -580,3 +580,14 @@ def test_chunk_values_near_the_smallest(env, dims):
     """(From a zero state: beside a larger one they would be below the prompt
     form's floor.)"""
     check_both_forms(env, _tiny_values, 100, dims, False)
+
+
+def _large_values(s):
+    s["v"].mul_(2.0 ** 118)
+
+
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("dims", [(64, 64), (64, 128), (128, 64), (128, 128)])
+def test_chunk_values_near_the_largest(env, dims, state):
+    """Finite as long as the states and outputs themselves are."""
+    check_both_forms(env, _large_values, 100, dims, state)
