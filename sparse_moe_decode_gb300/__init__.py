@@ -377,14 +377,13 @@ def _refuse(status, where):
 
 
 _binding = None
-_raw_stream = None
 
 
 def _tensor_calls():
     """The extension module of the tensor-level calls (raises if it is not built)."""
-    global _binding, _raw_stream
+    global _binding
     if _binding is None:
-        import torch
+        import torch  # noqa: F401  (the extension's libraries)
         L = lib()
         if not os.path.exists(os.path.join(_PKG, "_binding.so")):
             raise RuntimeError("_binding.so is not built; run `python -c \"import "
@@ -392,14 +391,13 @@ def _tensor_calls():
         module = importlib.import_module("._binding", __name__)
         module.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
             "moe_delta_chunk", "moe_delta_step", "moe_norm_gate_residual")))
-        _raw_stream = torch._C._cuda_getCurrentRawStream
         _binding = module
     return _binding
 
 
-def _stream_of(stream, device_index):
-    """The given stream, or the current one of the tensors' device."""
-    return _raw_stream(device_index) if stream is None else _s(stream)
+def _given(stream):
+    """A stream's address, or None for the current one of the tensors' device."""
+    return None if stream is None else _s(stream)
 
 
 class GatedDelta:
@@ -410,7 +408,9 @@ class GatedDelta:
     ``g`` (the decay's logarithm) and ``beta`` [N][v_heads] fp32; only their
     first stride is free (slices of one projected row are fine).  States are
     fp32 [n_slots][v_heads][v_dim][qk_dim].  ``state_out`` may be
-    ``state_in``.  The workspace belongs to one stream at a time.
+    ``state_in``.  The workspace belongs to one stream at a time.  With
+    ``stream`` given, results are made in that stream's memory, as under
+    ``torch.cuda.stream``.
     """
 
     def __init__(self, qk_heads, v_heads, qk_dim, v_dim, max_tokens, max_seqs=1, qk_norm=True,
@@ -435,7 +435,7 @@ class GatedDelta:
         """Whole prompts: the rows of len(cu_seqlens) - 1 sequences one after
         another (one sequence without ``cu_seqlens``).  Returns out [N][v_heads][v_dim]."""
         r = self._chunk(self._handle, q, k, v, g, beta, state_in, state_out, slots, out,
-                        cu_seqlens, _stream_of(stream, self._index) if self._index >= 0 else 0)
+                        cu_seqlens, _given(stream))
         return r if type(r) is not int else _refuse(r, "GatedDelta.chunk")
 
     def step(self, q, k, v, g, beta, state_in=None, state_out=None, slots=None, tokens=None,
@@ -444,7 +444,7 @@ class GatedDelta:
         sequence (by default as many as make ``slots``, or else the states,
         one per sequence).  Returns out [rows][v_heads][v_dim]."""
         r = self._step(self._handle, q, k, v, g, beta, state_in, state_out, slots, out, tokens,
-                       _stream_of(stream, self._index) if self._index >= 0 else 0)
+                       _given(stream))
         return r if type(r) is not int else _refuse(r, "GatedDelta.step")
 
     def status(self, stream=None) -> int:
@@ -469,5 +469,5 @@ def norm_gate_residual(x, gamma_post=None, gate=None, gate_act="sigmoid", resid=
         _refuse(MOE_ERR_INVALID_ARG, "norm_gate_residual")
     calls = _binding or _tensor_calls()
     r = calls.norm(x, gamma_post, gate, act, resid, res_scale, gamma_pre, eps, resid_out, x_next,
-                   _stream_of(stream, index))
+                   _given(stream))
     return r if type(r) is not int else _refuse(r, "norm_gate_residual")

@@ -10,6 +10,7 @@ from __future__ import annotations
 import concurrent.futures
 import glob
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -33,6 +34,10 @@ def nvcc() -> str:
         if c and (os.path.sep not in c or os.path.exists(c)):
             return c
     raise RuntimeError("nvcc not found")
+
+
+def cuda_home() -> str:
+    return os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(nvcc()) or nvcc())))
 
 
 def sources():
@@ -75,8 +80,10 @@ def build_binding(force: bool = False) -> str:
            "-I", INCLUDE, "-isystem", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(home, "include"),
            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda_home(), "include"),
            BINDING_SRC, "-o", tmp, "-L", os.path.join(home, "lib"),
-           "-Wl,-rpath," + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+           "-Wl,-rpath," + os.path.join(home, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed on %s:\n%s%s" % (BINDING_SRC, r.stdout, r.stderr))

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -65,6 +66,24 @@ float real(PyObject *o) {
 }
 
 void *address(PyObject *o) { return reinterpret_cast<void *>(static_cast<uintptr_t>(integer(o))); }
+
+// The stream of a call: the one whose address is given, or with None the
+// current one of `device`.  It is current while this lasts, so that memory made
+// for the results comes from its pool and is not still in use by another's work.
+class OnStream {
+ public:
+  OnStream(PyObject *given, int64_t device) {
+    const c10::DeviceIndex d = static_cast<c10::DeviceIndex>(device);
+    const cudaStream_t now = c10::cuda::getCurrentCUDAStream(d).stream();
+    stream_ = given == Py_None ? now : static_cast<cudaStream_t>(address(given));
+    if (stream_ != now) guard_.reset_stream(c10::cuda::getStreamFromExternal(stream_, d));
+  }
+  void *get() const { return stream_; }
+
+ private:
+  cudaStream_t stream_;
+  c10::cuda::OptionalCUDAStreamGuard guard_;
+};
 
 void place(const at::Tensor &x, at::ScalarType type, int64_t device) {
   require(x.scalar_type() == type && x.is_cuda() && x.get_device() == device &&
@@ -223,11 +242,12 @@ PyObject *delta_chunk(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     require(rows <= INT32_MAX && B <= INT32_MAX);
     const DeltaStates s = delta_states(h, a + 6, B);
+    const OnStream stream(a[11], h.device);
     const at::Tensor out = delta_out(h, a[9], rows, ld);
     return delta_result(g_chunk(&h.dims, &in, static_cast<int>(rows), cu, static_cast<int>(B),
                                 s.slots, static_cast<int>(s.n_slots), s.in, s.out,
                                 static_cast<moe_bf16 *>(out.mutable_data_ptr()), ld, h.workspace,
-                                h.ws_bytes, address(a[11])),
+                                h.ws_bytes, stream.get()),
                         out);
   });
 }
@@ -251,11 +271,12 @@ PyObject *delta_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     require(B * tokens == rows && rows <= INT32_MAX);
     const DeltaStates s = delta_states(h, a + 6, B);
+    const OnStream stream(a[11], h.device);
     const at::Tensor out = delta_out(h, a[9], rows, ld);
     return delta_result(g_step(&h.dims, &in, static_cast<int>(B), static_cast<int>(tokens), s.slots,
                                static_cast<int>(s.n_slots), s.in, s.out,
                                static_cast<moe_bf16 *>(out.mutable_data_ptr()), ld, h.workspace,
-                               h.ws_bytes, address(a[11])),
+                               h.ws_bytes, stream.get()),
                         out);
   });
 }
@@ -307,6 +328,7 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     m.gate_act = static_cast<int32_t>(integer(a[3]));
     if (a[4] != Py_None) m.resid_in = ptr(tensor(a[4])), m.resid_in_ld = ld_of(tensor(a[4]));
     m.res_scale = real(a[5]), m.eps = real(a[7]);
+    const OnStream stream(a[10], device);
     const at::Tensor resid = a[8] == Py_None ? fresh(x.sizes(), device) : tensor(a[8]);
     m.resid_out = ptr(resid), m.resid_out_ld = ld_of(resid);
     at::Tensor next;
@@ -316,7 +338,7 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
       next = a[9] == Py_None ? fresh(x.sizes(), device) : tensor(a[9]);
       m.x_next = ptr(next), m.x_next_ld = ld_of(next);
     }
-    const moe_status st = g_norm(&m, address(a[10]));
+    const moe_status st = g_norm(&m, stream.get());
     if (st != MOE_OK) return PyLong_FromLong(st);
     PyObject *both = PyTuple_New(2);
     if (!both) return nullptr;

@@ -591,3 +591,36 @@ def _large_values(s):
 def test_chunk_values_near_the_largest(env, dims, state):
     """Finite as long as the states and outputs themselves are."""
     check_both_forms(env, _large_values, 100, dims, state)
+
+
+def busy_with(env, like):
+    """Work on the current stream that still has to read a block of `like`'s size,
+    which nobody holds any more: (where it lies, what was read, what it holds)."""
+    import torch
+    block = torch.full_like(like, 5.0)
+    read = torch.zeros_like(like)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    read.copy_(block)
+    return block.data_ptr(), read
+
+
+@pytest.mark.parametrize("api", ["chunk", "step"])
+def test_results_on_a_given_stream(env, api):
+    """A result made for a call on another stream is not the memory of work
+    that is still to come on the current one."""
+    import torch
+    heads, dims, n = (2, 4), (128, 128), 3001
+    s = make(env, n, heads, dims)
+    m = mixer(env, heads, dims, n, 1)
+    call = lambda **kw: getattr(m, api)(**s, **kw, **({"tokens": n} if api == "step" else {}))
+    want = call()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    where, read = busy_with(env, want)
+    out = call(stream=side)
+    assert out.data_ptr() != where
+    torch.cuda.synchronize()
+    assert (read == 5.0).all() and torch.equal(out, want)
+    assert torch.equal(call(stream=torch.cuda.current_stream().cuda_stream), want)

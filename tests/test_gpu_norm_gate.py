@@ -189,3 +189,29 @@ def test_offsets_beyond_32_bits(env):
     want = check(env, s)
     got = check(env, dict(s, x=x), resid_out=x)
     assert torch.equal(want[1], got[1])
+
+
+def test_results_on_a_given_stream(env):
+    """Results made for a call on another stream are not the memory of work
+    that is still to come on the current one."""
+    import torch
+    s = make(env, 3001, 2048)
+    want = check(env, s)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    blocks = [torch.full_like(w, 5.0) for w in want]
+    where = [b.data_ptr() for b in blocks]
+    reads = [torch.zeros_like(w) for w in want]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    for r, b in zip(reads, blocks):
+        r.copy_(b)
+    del blocks, b
+    moe, _ = env
+    got = moe.norm_gate_residual(s["x"], gamma_post=s["post"], gate=s["gate"], resid=s["resid"],
+                                 res_scale=0.5, gamma_pre=s["pre"], eps=EPS, stream=side)
+    assert not {g.data_ptr() for g in got} & set(where)
+    torch.cuda.synchronize()
+    assert all((r == 5.0).all() for r in reads)
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
