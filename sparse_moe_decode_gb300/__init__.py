@@ -395,6 +395,20 @@ def _tensor_calls():
     return _binding
 
 
+_OTHER_DEVICE = -1  # a call's answer where its tensors' device is not the current one
+
+
+def _not_done(r, where, index, call, *args):
+    """A call's answer in place of tensors: its refusal, unless another device
+    than the tensors' was current.  Then it is made again with theirs (its stream
+    and the kernels are of the current one)."""
+    if r != _OTHER_DEVICE:
+        _refuse(r, where)
+    import torch
+    with torch.cuda.device(index):
+        return call(*args)
+
+
 def _given(stream):
     """A stream's address, or None for the current one of the tensors' device."""
     return None if stream is None else _s(stream)
@@ -436,7 +450,9 @@ class GatedDelta:
         another (one sequence without ``cu_seqlens``).  Returns out [N][v_heads][v_dim]."""
         r = self._chunk(self._handle, q, k, v, g, beta, state_in, state_out, slots, out,
                         cu_seqlens, _given(stream))
-        return r if type(r) is not int else _refuse(r, "GatedDelta.chunk")
+        return r if type(r) is not int else _not_done(
+            r, "GatedDelta.chunk", self._index, self.chunk, q, k, v, g, beta, cu_seqlens,
+            state_in, state_out, slots, out, stream)
 
     def step(self, q, k, v, g, beta, state_in=None, state_out=None, slots=None, tokens=None,
              out=None, stream=None):
@@ -445,13 +461,19 @@ class GatedDelta:
         one per sequence).  Returns out [rows][v_heads][v_dim]."""
         r = self._step(self._handle, q, k, v, g, beta, state_in, state_out, slots, out, tokens,
                        _given(stream))
-        return r if type(r) is not int else _refuse(r, "GatedDelta.step")
+        return r if type(r) is not int else _not_done(
+            r, "GatedDelta.step", self._index, self.step, q, k, v, g, beta, state_in, state_out,
+            slots, tokens, out, stream)
 
     def status(self, stream=None) -> int:
-        return moe_read_status(self.workspace, stream)
+        import torch
+        with torch.cuda.device(self._index):
+            return moe_read_status(self.workspace, stream)
 
     def clear_status(self, stream=None):
-        moe_clear_status(self.workspace, stream)
+        import torch
+        with torch.cuda.device(self._index):
+            moe_clear_status(self.workspace, stream)
 
 
 def norm_gate_residual(x, gamma_post=None, gate=None, gate_act="sigmoid", resid=None,
@@ -470,4 +492,6 @@ def norm_gate_residual(x, gamma_post=None, gate=None, gate_act="sigmoid", resid=
     calls = _binding or _tensor_calls()
     r = calls.norm(x, gamma_post, gate, act, resid, res_scale, gamma_pre, eps, resid_out, x_next,
                    _given(stream))
-    return r if type(r) is not int else _refuse(r, "norm_gate_residual")
+    return r if type(r) is not int else _not_done(
+        r, "norm_gate_residual", index, norm_gate_residual, x, gamma_post, gate, gate_act, resid,
+        res_scale, gamma_pre, eps, resid_out, x_next, stream)

@@ -4,7 +4,8 @@
 // interpreter's cost per attribute.  A CPython extension module; the library's
 // functions come in through `init`, so that it links against torch alone.
 //
-// Every call returns its tensors, or the moe_status it was refused with.
+// Every call returns its tensors, or the moe_status it was refused with, or
+// kOtherDevice, nothing done, where another device than its tensors' is current.
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
@@ -24,6 +25,8 @@ decltype(&moe_norm_gate_residual) g_norm;
 struct Refused {
   int status;
 };
+
+constexpr int kOtherDevice = -1;
 
 void require(bool ok) {
   if (!ok) throw Refused{MOE_ERR_INVALID_ARG};
@@ -74,6 +77,7 @@ class OnStream {
  public:
   OnStream(PyObject *given, int64_t device) {
     const c10::DeviceIndex d = static_cast<c10::DeviceIndex>(device);
+    if (c10::cuda::current_device() != d) throw Refused{kOtherDevice};
     const cudaStream_t now = c10::cuda::getCurrentCUDAStream(d).stream();
     stream_ = given == Py_None ? now : static_cast<cudaStream_t>(address(given));
     if (stream_ != now) guard_.reset_stream(c10::cuda::getStreamFromExternal(stream_, d));

@@ -140,3 +140,54 @@ def test_python_entries_check_their_tensors(moe):
         m.chunk(q, q, v, g, g)
     with pytest.raises(moe.MoEError):
         m.step(q[0], q, v, g, g)
+
+
+def test_calls_run_on_their_tensors_device(moe, monkeypatch):
+    """With another device current than the tensors', every call makes theirs
+    current for its time (their stream and the kernels are of the current one)."""
+    import contextlib
+    import types
+    torch = pytest.importorskip("torch")
+    now = [0]
+
+    @contextlib.contextmanager
+    def device(index):
+        before, now[0] = now[0], index
+        try:
+            yield
+        finally:
+            now[0] = before
+
+    m = moe.GatedDelta(2, 4, 128, 128, max_tokens=8, device="cpu")
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda *a: types.SimpleNamespace(cuda_stream=100 + now[0]))
+    where, status = [], [0]
+
+    def call(*args):  # as the extension: nothing is done on another device
+        where.append(now[0])
+        return -1 if now[0] != index else status[0] or "result"
+
+    m._chunk = m._step = call
+    fake = types.SimpleNamespace(moe_read_status=lambda *a: where.append(a[1]) or 0,
+                                 moe_clear_status=lambda *a: where.append(a[1]) or 0,
+                                 moe_status_string=moe.lib().moe_status_string)
+    monkeypatch.setattr(moe, "lib", lambda: fake)
+    monkeypatch.setattr(moe, "_binding", types.SimpleNamespace(norm=call))
+    for index, tries in ((0, [0]), (1, [0, 1])):
+        m._index = index
+        x = types.SimpleNamespace(get_device=lambda: index)
+        calls = (lambda: m.chunk(*[None] * 5), lambda: m.step(*[None] * 5),
+                 lambda: moe.norm_gate_residual(x))
+        del where[:]
+        assert [f() for f in calls] == ["result"] * 3 and where == tries * 3
+        del where[:]
+        m.status()
+        m.clear_status()
+        assert where == [100 + index] * 2 and now == [0]
+        status[0] = moe.MOE_ERR_WORKSPACE  # refusals come through
+        for f in calls:
+            with pytest.raises(moe.MoEError) as e:
+                f()
+            assert e.value.status == moe.MOE_ERR_WORKSPACE and now == [0]
+        status[0] = 0
