@@ -424,7 +424,8 @@ class GatedDelta:
     fp32 [n_slots][v_heads][v_dim][qk_dim].  ``state_out`` may be
     ``state_in``.  The workspace belongs to one stream at a time.  With
     ``stream`` given, results are made in that stream's memory, as under
-    ``torch.cuda.stream``.
+    ``torch.cuda.stream``.  For inference: results carry no gradient, whether
+    an input requires one or not.
     """
 
     def __init__(self, qk_heads, v_heads, qk_dim, v_dim, max_tokens, max_seqs=1, qk_norm=True,
@@ -485,7 +486,8 @@ def norm_gate_residual(x, gamma_post=None, gate=None, gate_act="sigmoid", resid=
     [tokens][heads][width] (one norm per head); ``gate`` is [width] (per
     channel), shaped like ``x``, or [.., 1] (per row).  Returns (resid_out,
     x_next), x_next None without ``gamma_pre``; x is not changed unless it is
-    given as an output."""
+    given as an output.  For inference: the results carry no gradient, whether
+    an input requires one or not."""
     act, index = GATE_ACTS.get(gate_act), x.get_device()
     if act is None or index < 0:
         _refuse(MOE_ERR_INVALID_ARG, "norm_gate_residual")

@@ -112,6 +112,14 @@ int64_t row_stride(const at::Tensor &x, at::ScalarType type, int64_t device, int
   return rows > 1 ? x.stride(0) : whole;
 }
 
+// A caller's tensor that a kernel was told to write: autograd sees that what it
+// may have kept of it is no longer there.
+void written(PyObject *o) {
+  if (o == Py_None) return;
+  const at::Tensor &x = THPVariable_Unpack(o);
+  if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
+}
+
 at::Tensor fresh(at::IntArrayRef sizes, int64_t device) {
   return at::empty(sizes, at::TensorOptions()
                               .dtype(at::kBFloat16)
@@ -225,8 +233,11 @@ at::Tensor delta_out(const Delta &h, PyObject *o, int64_t rows, int64_t &ld) {
   return out;
 }
 
-PyObject *delta_result(moe_status st, const at::Tensor &out) {
-  return st == MOE_OK ? THPVariable_Wrap(out) : PyLong_FromLong(st);
+// a: state_in, state_out, slots, out as they were given
+PyObject *delta_result(moe_status st, const at::Tensor &out, PyObject *const *a) {
+  if (st != MOE_OK) return PyLong_FromLong(st);
+  written(a[1]), written(a[3]);
+  return THPVariable_Wrap(out);
 }
 
 // chunk(handle, q, k, v, g, beta, state_in, state_out, slots, out, cu_seqlens, stream)
@@ -252,7 +263,7 @@ PyObject *delta_chunk(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                 s.slots, static_cast<int>(s.n_slots), s.in, s.out,
                                 static_cast<moe_bf16 *>(out.mutable_data_ptr()), ld, h.workspace,
                                 h.ws_bytes, stream.get()),
-                        out);
+                        out, a + 6);
   });
 }
 
@@ -281,7 +292,7 @@ PyObject *delta_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                static_cast<int>(s.n_slots), s.in, s.out,
                                static_cast<moe_bf16 *>(out.mutable_data_ptr()), ld, h.workspace,
                                h.ws_bytes, stream.get()),
-                        out);
+                        out, a + 6);
   });
 }
 
@@ -344,6 +355,7 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     const moe_status st = g_norm(&m, stream.get());
     if (st != MOE_OK) return PyLong_FromLong(st);
+    written(a[8]), written(a[9]);
     PyObject *both = PyTuple_New(2);
     if (!both) return nullptr;
     PyObject *r = THPVariable_Wrap(resid), *x2 = Py_None;

@@ -624,3 +624,30 @@ def test_results_on_a_given_stream(env, api):
     torch.cuda.synchronize()
     assert (read == 5.0).all() and torch.equal(out, want)
     assert torch.equal(call(stream=torch.cuda.current_stream().cuda_stream), want)
+
+
+@pytest.mark.parametrize("api", ["chunk", "step"])
+def test_written_tensors_count_a_version(env, api):
+    """Autograd learns that a kept tensor has been overwritten; without
+    gradients (inference mode) nothing is counted, and nothing else changes."""
+    import torch
+    heads, dims, n = (2, 4), (64, 64), 40
+    s = make(env, n, heads, dims)
+    m = mixer(env, heads, dims, n, 1)
+    S0 = states(env, 1, heads, dims)
+    S1, out = torch.empty_like(S0), torch.empty(n, 4, 64, dtype=torch.bfloat16, device=env[1])
+    call = lambda **kw: getattr(m, api)(**s, **kw, **({"tokens": n} if api == "step" else {}))
+    read = list(s.values()) + [S0]
+    before = [t._version for t in read + [S1, out]]
+    call(state_in=S0, state_out=S1, out=out)
+    after = [t._version for t in read + [S1, out]]
+    assert after == before[:-2] + [before[-2] + 1, before[-1] + 1]
+    x = torch.randn(n, 4, 64, dtype=torch.bfloat16, device=env[1], requires_grad=True)
+    kept = x.detach()
+    y = (x * kept).sum()
+    call(out=kept)
+    with pytest.raises(RuntimeError):
+        y.backward()
+    with torch.inference_mode():
+        again = torch.empty_like(out)
+        assert torch.equal(call(state_in=S0, out=again), out)

@@ -215,3 +215,17 @@ def test_results_on_a_given_stream(env):
     torch.cuda.synchronize()
     assert all((r == 5.0).all() for r in reads)
     assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_written_tensors_count_a_version(env):
+    import torch
+    moe, _ = env
+    s = make(env, 9, 128)
+    r, n = torch.empty_like(s["x"]), torch.empty_like(s["x"])
+    read = [s["x"], s["resid"], s["pre"]]
+    before = [t._version for t in read + [r, n]]
+    moe.norm_gate_residual(s["x"], resid=s["resid"], gamma_pre=s["pre"], resid_out=r, x_next=n)
+    assert [t._version for t in read + [r, n]] == before[:3] + [before[3] + 1, before[4] + 1]
+    with torch.inference_mode():
+        again, _ = moe.norm_gate_residual(s["x"], resid=s["resid"], resid_out=torch.empty_like(r))
+        assert torch.equal(again, r)
