@@ -386,8 +386,9 @@ def _tensor_calls():
         import torch  # noqa: F401  (the extension's libraries)
         L = lib()
         if not os.path.exists(os.path.join(_PKG, "_binding.so")):
-            raise RuntimeError("_binding.so is not built; run `python -c \"import "
-                               "__graft_entry__ as g; g.build()\"`")
+            raise RuntimeError("_binding.so is not built (it needs torch's, Python's and CUDA's "
+                               "headers and g++); run `python -c \"import __graft_entry__ as g; "
+                               "g.build()\"`")
         module = importlib.import_module("._binding", __name__)
         module.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
             "moe_delta_chunk", "moe_delta_step", "moe_norm_gate_residual")))

@@ -3,12 +3,16 @@
 Each .cu is compiled to an object in parallel, then linked into a shared
 library next to this file; beside it the extension module ``_binding`` (the
 tensor-level calls) is compiled with g++ against the installed torch.  Each is
-rebuilt only when a source or header is newer.
+rebuilt only when a source or header is newer, the extension also when it was
+built for another torch or Python.  The library needs neither: where the
+extension's headers or its compiler are missing, it is left out with a note, and
+the tensor-level calls say so when they are made.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -23,6 +27,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_STAMP = os.path.join(BUILD, "binding.txt")  # what it was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Werror=implicit-fallthrough", "-Xcompiler", "-Wall",
@@ -66,14 +71,51 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     return LIB
 
 
-def build_binding(force: bool = False) -> str:
-    """The extension module of the tensor-level calls, against this torch."""
+def _torch_home():
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def binding_lacks():
+    """What the extension cannot be built without and this machine lacks, or None."""
+    home = _torch_home()
+    if home is None:
+        return "torch"
+    for path in (os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+                 os.path.join(home, "include", "c10", "cuda", "CUDAGuard.h"),
+                 os.path.join(cuda_home(), "include", "cuda_runtime_api.h")):
+        if not os.path.exists(path):
+            return path
+    cxx = os.environ.get("CXX", "g++")
+    return None if shutil.which(cxx) else cxx
+
+
+def binding_target() -> str:
+    """The torch and the Python that the extension is built for."""
+    home = _torch_home()
+    with open(os.path.join(home, "version.py")) as f:
+        return "%s\n%s\n%s" % (sysconfig.get_config_var("SOABI"), home, f.read())
+
+
+def build_binding(force: bool = False):
+    """The extension module of the tensor-level calls, against this torch; None
+    where something that it needs is missing."""
+    lacks = binding_lacks()
+    if lacks:
+        sys.stderr.write("sparse_moe_decode_gb300: no %s, so the tensor-level calls of the gated "
+                         "delta rule and the norms are not built\n" % lacks)
+        return None
     deps = [BINDING_SRC, os.path.join(INCLUDE, "moe_gb300.h"), os.path.abspath(__file__)]
-    if (not force and os.path.exists(BINDING) and
+    target = binding_target()
+    built_for = None
+    if os.path.exists(BINDING_STAMP):
+        with open(BINDING_STAMP) as f:
+            built_for = f.read()
+    if (not force and os.path.exists(BINDING) and built_for == target and
             all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps)):
         return BINDING
     import torch
-    home = os.path.dirname(os.path.abspath(torch.__file__))
+    home = _torch_home()
     tmp = BINDING + ".%d.tmp" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
@@ -88,6 +130,9 @@ def build_binding(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("g++ failed on %s:\n%s%s" % (BINDING_SRC, r.stdout, r.stderr))
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(BINDING_STAMP), exist_ok=True)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(target)
     return BINDING
 
 
