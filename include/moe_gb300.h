@@ -291,11 +291,17 @@ moe_status moe_topk_merge(const int32_t *ids, const float *values, int T, int n_
  * With qk_norm != 0, q and k are first divided by sqrt(sum x^2 + qk_eps).
  * g is the natural logarithm of the decay, g <= 0 (below -128, -inf included,
  * it counts as -128: the state is forgotten; growth is served as long as no
- * 64 consecutive g sum to more than 3).  Sums, states and
- * gates are fp32 (or better); out is rounded to bf16 once.  The prompt form
- * takes fp32 operands as two fp16 terms: 22 bits of what is above 2^-17 of
- * the largest value of the same 64 tokens and state row, and 2^-36 of that
- * largest value below (token by token: fp32 throughout). */
+ * 64 consecutive g sum to more than 3).  The 2-norms of q's and k's rows must
+ * stay below 2^63, and above 2^-60 where qk_eps is 0 (their squares are summed
+ * in fp32).
+ * States, gates and sums are fp32 (or better) and out is rounded to bf16 once.
+ * Token by token that is all.  The prompt form rounds the operands of its
+ * products.  For the states, fp32 operands enter as two fp16 terms: 22 bits of
+ * what is above 2^-17 of the largest value of the same 64 tokens and state
+ * row, and 2^-36 of that largest value below.  For out, S, u and the products
+ * of q and k enter as ONE fp16 term each, 11 bits: out is off by up to 2^-10
+ * of the sum of its terms' absolute values, beside its rounding to bf16 (more
+ * than that rounding where the terms cancel to a quarter or less). */
 typedef struct {
   int32_t qk_heads; /* Hk                                                 */
   int32_t v_heads;  /* Hv: a multiple of Hk, <= 256                       */

@@ -25,8 +25,9 @@
 // bits; products accumulate in fp32 and the state is summed in fp32 registers.
 // The scales are of the largest value where one warp holds a row (S) and of a
 // bound from norms where two would have to agree (x, u).  The outputs, which
-// are rounded to bf16 once, take P, S and u as single fp16 terms (2^-11, an
-// eighth of the rounding to come).
+// are rounded to bf16 once, take P, S and u as single fp16 terms: off by up to
+// 2^-10 of the sum of their terms' absolute values, a quarter of the rounding to
+// come where the terms do not cancel.
 //
 // What bounds it (GB300, 32 value heads of 128 x 128 on 16 key heads).  A chunk
 // of the chain takes 1.73 us on whatever SM it runs, so one prompt of 8192
