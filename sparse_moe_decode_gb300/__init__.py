@@ -451,7 +451,10 @@ class GatedDelta:
     def chunk(self, q, k, v, g, beta, cu_seqlens=None, state_in=None, state_out=None, slots=None,
               out=None, stream=None):
         """Whole prompts: the rows of len(cu_seqlens) - 1 sequences one after
-        another (one sequence without ``cu_seqlens``).  Returns out [N][v_heads][v_dim]."""
+        another (one sequence without ``cu_seqlens``).  Returns out [N][v_heads][v_dim].
+        Rows of no sequence, and of one that is skipped (a negative slot; a slot or
+        bound out of range, which ``status`` tells), are left as they were: in a
+        result that the call makes they are undefined."""
         r = self._chunk(self._handle, q, k, v, g, beta, state_in, state_out, slots, out,
                         cu_seqlens, _given(stream))
         return r if type(r) is not int else _not_done(
@@ -462,7 +465,12 @@ class GatedDelta:
              out=None, stream=None):
         """Decode and verification: ``tokens`` consecutive rows for each
         sequence (by default as many as make ``slots``, or else the states,
-        one per sequence).  Returns out [rows][v_heads][v_dim]."""
+        one per sequence).  Returns out [rows][v_heads][v_dim]; skipped sequences'
+        rows as in ``chunk``.
+
+        After a draft that was accepted in part, a second call keeps the states:
+        verify without ``state_out``, then ``chunk`` over the same rows with each
+        sequence cut after its accepted tokens and the rest in a slot of -1."""
         r = self._step(self._handle, q, k, v, g, beta, state_in, state_out, slots, out, tokens,
                        _given(stream))
         return r if type(r) is not int else _not_done(

@@ -651,3 +651,30 @@ def test_written_tensors_count_a_version(env, api):
     with torch.inference_mode():
         again = torch.empty_like(out)
         assert torch.equal(call(state_in=S0, out=again), out)
+
+
+@pytest.mark.parametrize("T", [8, 30])
+def test_verification_keeps_the_accepted_state(env, T):
+    """A verified draft's outputs, then the states after the accepted tokens of
+    each sequence: a call over the same rows, the rejected ones in a slot of -1."""
+    import torch
+    _, dev = env
+    heads, dims = (2, 4), (128, 128)
+    accepted = torch.tensor([1, T, 0, T - 3, 4], dtype=torch.int32, device=dev)
+    B = len(accepted)
+    s = make(env, B * T, heads, dims, seed=3)
+    m = mixer(env, heads, dims, B * T, 2 * B)
+    S = states(env, B + 1, heads, dims)
+    given = S.clone()
+    slots = torch.arange(B, 0, -1, dtype=torch.int32, device=dev)
+    out = m.step(**s, state_in=S, slots=slots)
+    assert torch.equal(S, given)
+    start = T * torch.arange(B, dtype=torch.int32, device=dev)
+    cut = torch.stack([start, start + accepted], 1).flatten()
+    rest = slots.new_full((B,), -1)
+    m.chunk(**s, cu_seqlens=torch.cat([cut, cut.new_tensor([B * T])]), state_in=S, state_out=S,
+            slots=torch.stack([slots, rest], 1).flatten())
+    assert m.status() == 0 and torch.equal(S[0], given[0])
+    for i, n in enumerate(accepted.tolist()):
+        c = slice(i * T, i * T + n)
+        check_seq(s, c, given[slots[i]], out, S[slots[i]], dims)
