@@ -15,9 +15,11 @@
 // chain, each with half of the key channels: S k^T, T x and u k^T follow one
 // another there, and the two exchange shares through shared memory.  The other
 // two form the outputs from copies of the operands, a phase behind, and bring in
-// the next chunks.  mma.sync rather than tcgen05: the chain is bound by the
-// latency of its dependent steps, and a round trip of each through tensor
-// memory costs more than its few products.
+// the next chunks.  mma.sync: the chain is bound by the latency of its dependent
+// steps, each of few products whose results the next one needs in registers.  A
+// form with tcgen05, where each would pass through tensor memory, has not been
+// built or measured; where there are several pieces of work for every SM it may
+// be the better one.
 //
 // Precision.  k and q are bf16: scaled by a power of two per token they are
 // exact in fp16 down to 2^-25 of the token's norm.  S, x, u and T are fp32 and
@@ -35,8 +37,8 @@
 // bytes.  A CTA's pieces of work (32 state rows of one sequence, or 16) follow one
 // another, longest sequences first, with the next one's chunks, values and
 // state on their way during the last one's chunks: 240 us for 13 sequences of
-// 6007 tokens in all and 116 us for 32 of 64, against 244 and 137 us with a
-// CTA for each piece.  (Each in a fixed order of pieces was slower, 263 us for
+// 6007 tokens in all and 115 us for 32 of 64 (244 and 137 us with a CTA for each
+// piece, when that was changed).  (Each in a fixed order of pieces was slower, 263 us for
 // the 13.)  Measured and slower: four chain warps a group with a quarter of the
 // channels each (393 against 338 us for 8192 tokens then), one output warp a
 // group (369), and a ninth warp for the copies (446: 168 registers a thread).
@@ -205,7 +207,7 @@ __device__ __forceinline__ void product(float (&acc)[4], uint32_t a, uint32_t a_
 }
 
 // (hi, lo) += (h, l), pairs whose sum is the value: no digit of the larger
-// terms is lost.
+// terms is lost (Knuth's two-sum).
 __device__ __forceinline__ void add_exact(float &hi, float &lo, float h, float l) {
   const float s = __fadd_rn(hi, h), t = __fsub_rn(s, hi);
   const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(h, t));
@@ -1207,8 +1209,8 @@ delta_chain_kernel(moe_delta_dims d, moe_delta_inputs in, DeltaSeqs seq, uint8_t
   // The next chunk can be brought in any time after bar_x, when the stage of the
   // one before is free.  Issuing its copy takes 500 cycles; where S q^T has half
   // as many products the chain waits for them less before bar_w, else after it:
-  // 8 prompts (8 heads of 64) 132.2 against 136.3 us, 8192 tokens (32 heads of
-  // 128) 322.6 against 308.2 us.
+  // 8 prompts (8 heads of 64) 111 us before it and 120 after, 8192 tokens (32 heads
+  // of 128) 320.7 before it and 312.5 after.
   constexpr bool kLate = DK == 128;
   const auto bring_next = [&] {
     const int given_up = *reinterpret_cast<volatile int *>(abort_flag);
@@ -1374,9 +1376,10 @@ cudaError_t launch(const moe_delta_dims &d, const moe_delta_inputs &in, const De
   const int ratio = d.v_heads / d.qk_heads;
   // A CTA serves several of the value heads of its key head (and forms k k^T
   // and q k^T once for them) when there are enough to fill the SMs so: 8192
-  // tokens take 314 us with two heads of 32 to a CTA, 330 with one, 13 sequences
-  // of 6007 tokens 244 and 259, 2048 tokens 89.5 and 90.3; of 67 tokens,
-  // 20.6 and 18.6.
+  // tokens take 312.5 us with two heads of 32 to a CTA, 328.7 with one, 13
+  // sequences of 6007 tokens 240.5 and 253.6, 2048 tokens 89.6 and 90.5; where
+  // there are not, 67 tokens take 20.0 and 16.4, 512 beside 32 of one 66.7 and
+  // 61.4.
   int heads = 1;
   if (slots.count * d.qk_heads >= static_cast<size_t>(kPrepCtas * tc_sm_count()))
     for (int n = 2; n <= kPrepHeads; ++n)

@@ -10,7 +10,7 @@
 //
 // Bound by memory where there are many sequences: each state is read and
 // written once, 256 sequences of one token (32 heads of 128 x 128, 1.08 GB) in
-// 153.8 us, 7.0 TB/s, 32 in 22.2 us.  One token of one sequence is latency:
+// 154.5 us, 7.0 TB/s, 32 in 22.6 us.  One token of one sequence is latency:
 // 2.1 us in a graph, and 0.43 us for each further token (a token's products,
 // two shuffle reductions and the update follow one another).
 #include <cuda_runtime.h>

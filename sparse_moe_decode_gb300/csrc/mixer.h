@@ -25,7 +25,10 @@ struct DeltaSeqs {
 // heads of 128) takes 17.0 us in the chunked form whatever its length up to 64
 // (8 heads of 64 10.8 us), in a graph, and 1.7 us and 0.43 us for each token in
 // the recurrent one (12.0 and 11.0 us at 24); each of many takes 3.1 us in the
-// former, 0.6 us and 0.11 us a token in the latter.
+// former, 0.6 us and 0.11 us a token in the latter.  With fewer heads both sides
+// are nearer to one another: 25 tokens of 1 to 8 heads take 10.3 to 11.8 us in
+// chunks and 11.7 to 12.8 us token by token, of 16 heads 14.3 and 12.8 us, of 32
+// heads 16.9 and 12.9 us.
 constexpr int kDeltaShort = 24;
 
 // Token by token, the state in registers: the sequences of up to `most` tokens.

@@ -3,9 +3,12 @@
 //   y = a act(gate) rms(x) g_post + resid,  r = bf16(y),  n = bf16(rms(r) g_pre).
 // Bound by memory: x, resid and an element gate are read once and r and n
 // written once; a row's values stay in registers between the two norms.
-// Measured: 16384 rows of 2048 with an element gate (336 MB) 55.8 us, 6.0 TB/s;
-// 65536 rows of 128 (one per head, gated by silu(z), 50 MB) 11.5 us; one row
-// takes 6 us, the launch included.
+// Measured: 16384 rows of 2048 with an element gate (336 MB) 56.2 us, 6.0 TB/s;
+// rows of 8 to 128 of the same bytes 54 to 55 us; 65536 rows of 128 (one per
+// head, gated by silu(z), 50 MB) 11.6 us; a call of one row 6.4 us of the host's
+// time.  Widths or strides that are no multiple of 8 go by groups of two values
+// or one: 336 MB take 126 us at width 2046, 290 us at 2047, 226 to 253 us at 15 to
+// 1023.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -61,7 +64,8 @@ __device__ __forceinline__ void pack(const float2 (&v)[4], uint4 &w) { w = pack(
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // exp's argument is rounded once: a relative error of the sigmoid of 2^-21 up
-// to |z| = 8 and of |z| 2^-24 beyond, far below the one rounding to bf16.
+// to |z| = 8 and of |z| 2^-24 beyond, far below the one rounding to bf16; 0
+// where it is below 2^-126 (z < -87).
 __device__ __forceinline__ float sigmoid(float z) {
   return __fdividef(1.0f, 1.0f + __expf(-z));
 }
