@@ -80,7 +80,7 @@ typedef enum {
 #define MOE_DEV_NONFINITE 0x1u  /* a token's logits held NaN/inf (A2)       */
 #define MOE_DEV_BAD_EXPERT 0x2u /* an expert id >= num_experts was given    */
 #define MOE_DEV_TIMEOUT 0x4u    /* a bounded device-side wait gave up       */
-#define MOE_DEV_BAD_INDEX 0x8u  /* a sequence bound or state slot out of range */
+#define MOE_DEV_BAD_INDEX 0x8u  /* a sequence bound, state slot, page or token out of range */
 
 typedef struct {
   int32_t hidden;       /* H                                              */
@@ -391,6 +391,134 @@ typedef struct {
 } moe_norm_args;
 
 moe_status moe_norm_gate_residual(const moe_norm_args *args, void *stream);
+
+/* ---- The full-attention layers of a hybrid decoder: a paged cache of keys
+ * and values, quantised as it is written, and the attention of new tokens
+ * over it.
+ *
+ * The cache holds pages of page_size positions: k and v are
+ * [pages][kv_heads][page_size][head_dim] of the cache's type, and with the
+ * 8-bit types k_scale and v_scale [pages][kv_heads][page_size] fp32 (NULL
+ * with bf16).  Position p of a sequence lies in page table[p / page_size] at
+ * p % page_size.  A row x (one token and head of k or v) is kept as
+ *   BF16: itself;
+ *   INT8: codes c = x / s rounded to nearest, ties to even (the exact
+ *         quotient is rounded), s = max(fp32(max|x| / 127), 2^-126);
+ *   E4M3: codes c = e4m3(x / s), s the power of two with max|x| / s in
+ *         (224, 448], at least 2^-126 (a floating code's relative step does
+ *         not depend on s, and x / s is exact);
+ * and stands for c * s.  A row that holds a value that is not finite gets
+ * codes 0 and the scale NaN in the 8-bit types, so that all of it reads as
+ * NaN. */
+#define MOE_KV_BF16 0
+#define MOE_KV_INT8 1
+#define MOE_KV_E4M3 2
+
+typedef struct {
+  int32_t q_heads;   /* a multiple of kv_heads, at most 64 times as many; <= 1024 */
+  int32_t kv_heads;  /* query head h reads key/value head h / (q_heads / kv_heads) */
+  int32_t head_dim;  /* 64, 128 or 256                                       */
+  int32_t page_size; /* 16, 32, 64, 128 or 256                               */
+  int32_t kv_type;   /* MOE_KV_*                                             */
+  int32_t window;    /* 0: a token sees all positions up to its own; W > 0: the
+                        last W of them                                       */
+  float scale;       /* of the products of q and k; finite                   */
+} moe_attn_dims;
+
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int64_t pages; /* >= 1; pages * kv_heads * page_size < 2^31              */
+} moe_kv_cache;
+
+/* The new tokens of a call and where they belong: N rows hold B sequences one
+ * after another, sequence b rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1
+ * (device, int32 [B + 1]; NULL: N / B rows each).  seq_lens[b] (device, int32)
+ * is the number of positions that the sequence has with them: row i of its n
+ * rows is position seq_lens[b] - n + i.  page_table row b, at page_table +
+ * b * table_ld (device, int32), holds the pages of its positions;
+ * table_cols columns may be read.
+ * A sequence without rows or with seq_lens[b] <= 0 is skipped (a padded
+ * batch): its rows are left as they were.  So is one whose bounds are not
+ * 0 <= start <= end <= N, or with fewer positions than rows or more than
+ * table_cols * page_size, and that sets MOE_DEV_BAD_INDEX.  Entries of the
+ * table behind a sequence's last position are not read. */
+typedef struct {
+  int32_t N, B; /* N <= 2^20, B <= 65536                                    */
+  const int32_t *cu_seqlens;
+  const int32_t *seq_lens;
+  const int32_t *page_table;
+  int64_t table_ld;
+  int32_t table_cols;
+} moe_kv_batch;
+
+/* Writes the rows of k and v into the cache.  Token t's k lies at k + t * k_ld
+ * as [kv_heads][head_dim] bf16 (16-byte aligned, strides multiples of 8).  A
+ * token whose page is not 0 <= page < pages is not written, and sets
+ * MOE_DEV_BAD_INDEX.  Two tokens of a call must not have the same place.  The
+ * workspace holds only the status word (ws_bytes >= 256). */
+moe_status moe_kv_write(const moe_attn_dims *dims, const moe_kv_cache *cache,
+                        const moe_kv_batch *batch, const moe_bf16 *k, int64_t k_ld,
+                        const moe_bf16 *v, int64_t v_ld, void *workspace, size_t ws_bytes,
+                        void *stream);
+
+/* Reads the positions of the rows back as bf16 (c * s rounded once): out rows
+ * laid out like moe_kv_write's.  Either output may be NULL.  A row whose page
+ * is out of range is left as it was, and sets MOE_DEV_BAD_INDEX. */
+moe_status moe_kv_read(const moe_attn_dims *dims, const moe_kv_cache *cache,
+                       const moe_kv_batch *batch, moe_bf16 *k, int64_t k_ld, moe_bf16 *v,
+                       int64_t v_ld, void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace moe_paged_attention needs, whatever the batch (0 on bad
+ * dims). */
+size_t moe_attn_workspace_bytes(const moe_attn_dims *dims);
+
+/* Attention of the rows over their sequences' positions, which are in the
+ * cache already (moe_kv_write first):
+ *   out[t][h] = sum_j w_j v_j,   w = softmax over j of scale * q[t][h] . k_j,
+ * j over the positions that token t's position sees.  q at q + t * q_ld as
+ * [q_heads][head_dim] bf16, out alike (16-byte aligned, strides multiples of
+ * 8; out must not overlap q or the cache).  Any mix of single tokens, drafts
+ * and whole prompts.  The products run on tensor cores with fp32 sums, the
+ * softmax in fp32; the weights enter the second product as bf16 (as fp16 with
+ * an 8-bit cache, whose codes are exact in fp16), out is rounded to bf16 once.
+ * Weights below 2^-126 of a row's largest are 0; with an 8-bit cache the
+ * products of a weight and its v_scale keep 11 bits, but no less than 2^-38 of
+ * the row's largest product.
+ * What lies in the cache behind a sequence's last position is not looked at.
+ * A value that is not finite in k, or in an 8-bit cache's rows, reaches the
+ * rows that see its position; one in a bf16 cache's v may also reach rows of
+ * its sequence that do not see it but see or share a key tile of 128
+ * positions with it.  A page out of range sets MOE_DEV_BAD_INDEX, and its
+ * sequence's rows are then of no use. */
+moe_status moe_paged_attention(const moe_attn_dims *dims, const moe_kv_cache *cache,
+                               const moe_kv_batch *batch, const moe_bf16 *q, int64_t q_ld,
+                               moe_bf16 *out, int64_t out_ld, void *workspace, size_t ws_bytes,
+                               void *stream);
+
+/* Which tokens of a draft stand: B sequences with up to T drafted tokens
+ * d_i and the target's probabilities p_0 .. p_T (p_i after i of them), the
+ * drafter's q_i, and numbers u_i and r = u_T, uniform in [0, 1).
+ *   accepted = the first i with d_i < 0 (the draft ends there) or not
+ *              u_i * q_i(d_i) < p_i(d_i), else T;
+ *   tokens   = d_0 .. d_(accepted - 1), one more, then -1;
+ * the one more is the least j with C_j > r * C_V-1, C the running sums of
+ * max(p - q, 0) at a rejected token's place, and of p where the draft ended
+ * or where p never exceeds q.  Products and differences are exact, sums kept
+ * to 48 bits or more.  Without draft probabilities (draft NULL) q_i is 1 at
+ * d_i and 0 elsewhere.  Rows of p and q need not sum to 1.
+ * target row (b, i) at target + b * target_seq_ld + i * target_ld, draft
+ * alike; [V] fp32, 4-byte aligned.  draft_tokens [B][T], uniform [B][T + 1],
+ * tokens [B][T + 1], accepted [B], all whole.  T <= 1024, V <= 2^24.
+ * A drafted token >= V sets MOE_DEV_BAD_INDEX; a value that is negative or
+ * not finite in the rows that the last token is taken from, or one of them
+ * without a positive value, sets MOE_DEV_NONFINITE; either leaves tokens -1
+ * and accepted 0.  The workspace holds only the status word. */
+moe_status moe_verify_draft(int B, int T, int V, const float *target, int64_t target_seq_ld,
+                            int64_t target_ld, const float *draft, int64_t draft_seq_ld,
+                            int64_t draft_ld, const int32_t *draft_tokens, const float *uniform,
+                            int32_t *tokens, int32_t *accepted, void *workspace, size_t ws_bytes,
+                            void *stream);
 
 /* Copy the device status word to *bits (synchronises the stream). */
 moe_status moe_read_status(const void *workspace, void *stream, uint32_t *bits);

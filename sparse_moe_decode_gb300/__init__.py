@@ -11,7 +11,10 @@ The entry points keep the C names: ``moe_router_logits``,
 ``moe_workspace_bytes``, ``moe_read_status``, ``moe_clear_status``; the other
 half of a hybrid decoder layer in ``moe_delta_chunk``, ``moe_delta_step``
 (the gated delta rule; ``GatedDelta`` holds its workspace) and
-``moe_norm_gate_residual`` (``norm_gate_residual`` takes tensors).  Array
+``moe_norm_gate_residual`` (``norm_gate_residual`` takes tensors); the
+full-attention layers in ``moe_kv_write``, ``moe_kv_read``,
+``moe_paged_attention`` (``PagedAttention``), and the verification of drafted
+tokens in ``moe_verify_draft`` (``DraftVerifier``).  Array
 arguments may be torch tensors (their ``data_ptr()`` is passed), raw integer
 addresses, or None where the C argument is nullable.
 
@@ -23,6 +26,7 @@ import ctypes
 import importlib
 import os
 import threading
+from typing import Any, NamedTuple
 
 __all__ = [
     "MoEError", "lib", "Dims", "weights_struct", "moe_router_logits",
@@ -35,6 +39,8 @@ __all__ = [
     "moe_topk_merge", "moe_block_forward_residual",
     "DeltaDims", "moe_delta_workspace_bytes", "moe_delta_chunk", "moe_delta_step",
     "moe_norm_gate_residual", "GatedDelta", "norm_gate_residual", "DEV_BAD_INDEX",
+    "AttnDims", "KVCacheArgs", "KVBatch", "moe_attn_workspace_bytes", "moe_kv_write", "moe_kv_read",
+    "moe_paged_attention", "moe_verify_draft", "KVCache", "PagedAttention", "DraftVerifier",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -44,6 +50,7 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUD
 DEV_NONFINITE, DEV_BAD_EXPERT, DEV_TIMEOUT, DEV_BAD_INDEX = 0x1, 0x2, 0x4, 0x8
 GATE_NONE, GATE_CHANNEL, GATE_ELEMENT, GATE_ROW = range(4)
 GATE_ACTS = {"identity": 0, "sigmoid": 1, "silu": 2}
+KV_TYPES = {"bf16": 0, "int8": 1, "e4m3": 2}
 
 # every symbol include/moe_gb300.h declares
 EXPORTS = (
@@ -55,6 +62,8 @@ EXPORTS = (
     "moe_block_forward_noalloc", "moe_topk_workspace_bytes", "moe_topk_candidates",
     "moe_topk_merge", "moe_block_forward_residual",
     "moe_delta_workspace_bytes", "moe_delta_chunk", "moe_delta_step", "moe_norm_gate_residual",
+    "moe_attn_workspace_bytes", "moe_kv_write", "moe_kv_read", "moe_paged_attention",
+    "moe_verify_draft",
 )
 
 
@@ -103,6 +112,23 @@ class NormArgs(ctypes.Structure):
                  ("res_scale", ctypes.c_float), ("eps", ctypes.c_float)])
 
 
+class AttnDims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("q_heads", "kv_heads", "head_dim", "page_size",
+                                               "kv_type", "window")] +
+                [("scale", ctypes.c_float)])
+
+
+class KVCacheArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] +
+                [("pages", ctypes.c_int64)])
+
+
+class KVBatch(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("B", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_ld", ctypes.c_int64), ("table_cols", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -122,6 +148,7 @@ def lib() -> ctypes.CDLL:
             WP = ctypes.POINTER(Weights)
             DDP, DIP = ctypes.POINTER(DeltaDims), ctypes.POINTER(DeltaInputs)
             L64 = ctypes.c_int64
+            ADP, KCP, KBP = (ctypes.POINTER(t) for t in (AttnDims, KVCacheArgs, KVBatch))
             sig = {
                 "moe_workspace_bytes": (Z, [DP, I]),
                 "moe_router_logits": (I, [DP, WP, P, I, P, P, P]),
@@ -149,6 +176,11 @@ def lib() -> ctypes.CDLL:
                 "moe_delta_chunk": (I, [DDP, DIP, I, P, I, P, I, P, P, P, L64, P, Z, P]),
                 "moe_delta_step": (I, [DDP, DIP, I, I, P, I, P, P, P, L64, P, Z, P]),
                 "moe_norm_gate_residual": (I, [ctypes.POINTER(NormArgs), P]),
+                "moe_attn_workspace_bytes": (Z, [ADP]),
+                "moe_kv_write": (I, [ADP, KCP, KBP, P, L64, P, L64, P, Z, P]),
+                "moe_kv_read": (I, [ADP, KCP, KBP, P, L64, P, L64, P, Z, P]),
+                "moe_paged_attention": (I, [ADP, KCP, KBP, P, L64, P, L64, P, Z, P]),
+                "moe_verify_draft": (I, [I, I, I, P, L64, L64, P, L64, L64, P, P, P, P, P, Z, P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -323,6 +355,39 @@ def moe_norm_gate_residual(args: NormArgs, stream=None):
            "moe_norm_gate_residual")
 
 
+def moe_attn_workspace_bytes(dims: AttnDims) -> int:
+    return int(lib().moe_attn_workspace_bytes(ctypes.byref(dims)))
+
+
+def moe_kv_write(dims: AttnDims, cache: KVCacheArgs, batch: KVBatch, k, k_ld, v, v_ld, workspace,
+                 ws_bytes, stream=None):
+    _check(lib().moe_kv_write(ctypes.byref(dims), ctypes.byref(cache), ctypes.byref(batch), _a(k),
+                              int(k_ld), _a(v), int(v_ld), _a(workspace), int(ws_bytes),
+                              _s(stream)), "moe_kv_write")
+
+
+def moe_kv_read(dims: AttnDims, cache: KVCacheArgs, batch: KVBatch, k, k_ld, v, v_ld, workspace,
+                ws_bytes, stream=None):
+    _check(lib().moe_kv_read(ctypes.byref(dims), ctypes.byref(cache), ctypes.byref(batch), _a(k),
+                             int(k_ld), _a(v), int(v_ld), _a(workspace), int(ws_bytes),
+                             _s(stream)), "moe_kv_read")
+
+
+def moe_paged_attention(dims: AttnDims, cache: KVCacheArgs, batch: KVBatch, q, q_ld, out, out_ld,
+                        workspace, ws_bytes, stream=None):
+    _check(lib().moe_paged_attention(ctypes.byref(dims), ctypes.byref(cache), ctypes.byref(batch),
+                                     _a(q), int(q_ld), _a(out), int(out_ld), _a(workspace),
+                                     int(ws_bytes), _s(stream)), "moe_paged_attention")
+
+
+def moe_verify_draft(B, T, V, target, target_seq_ld, target_ld, draft, draft_seq_ld, draft_ld,
+                     draft_tokens, uniform, tokens, accepted, workspace, ws_bytes, stream=None):
+    _check(lib().moe_verify_draft(int(B), int(T), int(V), _a(target), int(target_seq_ld),
+                                  int(target_ld), _a(draft), int(draft_seq_ld), int(draft_ld),
+                                  _a(draft_tokens), _a(uniform), _a(tokens), _a(accepted),
+                                  _a(workspace), int(ws_bytes), _s(stream)), "moe_verify_draft")
+
+
 def moe_read_status(workspace, stream=None) -> int:
     bits = ctypes.c_uint32(0)
     _check(lib().moe_read_status(_a(workspace), _s(stream), ctypes.byref(bits)), "moe_read_status")
@@ -391,7 +456,8 @@ def _tensor_calls():
                                "g.build()\"`")
         module = importlib.import_module("._binding", __name__)
         module.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
-            "moe_delta_chunk", "moe_delta_step", "moe_norm_gate_residual")))
+            "moe_delta_chunk", "moe_delta_step", "moe_norm_gate_residual", "moe_kv_write",
+            "moe_kv_read", "moe_paged_attention", "moe_verify_draft")))
         _binding = module
     return _binding
 
@@ -508,3 +574,151 @@ def norm_gate_residual(x, gamma_post=None, gate=None, gate_act="sigmoid", resid=
     return r if type(r) is not int else _not_done(
         r, "norm_gate_residual", index, norm_gate_residual, x, gamma_post, gate, gate_act, resid,
         res_scale, gamma_pre, eps, resid_out, x_next, stream)
+
+
+class KVCache(NamedTuple):
+    """The pages of one layer: k, v [pages][kv_heads][page_size][head_dim] (bf16,
+    int8 or float8_e4m3fn) and, with 8-bit types, the scales [pages][kv_heads]
+    [page_size] fp32 that their rows are multiplied by (None with bf16)."""
+    k: Any
+    v: Any
+    k_scale: Any = None
+    v_scale: Any = None
+
+
+class PagedAttention:
+    """Attention of new tokens over a paged cache, with its workspace.
+
+    A call's rows are sequences one after another: as many each, or by
+    ``cu_seqlens`` (int32 [B + 1]).  ``seq_lens`` (int32 [B]) are the positions
+    that the sequences have with these rows, which are their last; position p
+    lies in page ``page_table[b][p // page_size]`` (int32 [B][pages of the
+    longest], -1 or anything behind a sequence's end) at ``p % page_size``.
+    Single tokens, drafts and whole prompts may be mixed.  A sequence without
+    rows or with ``seq_lens`` of 0 is skipped, its rows left as they were (in a
+    result that the call makes they are undefined); bounds, lengths and pages
+    out of range are not followed, and ``status`` tells.
+
+    ``kv_type`` is "bf16", or "int8" or "e4m3" with a scale for each token and
+    head, quantised as it is written (see ``moe_gb300.h``).  ``window`` W > 0
+    lets a token see only the last W positions up to its own.  One object serves
+    all layers of its shape; its workspace belongs to one stream at a time.
+    With ``stream`` given, results are made in that stream's memory.  For
+    inference: results carry no gradient, whether an input requires one or not.
+    """
+
+    def __init__(self, q_heads, kv_heads, head_dim, page_size=64, kv_type="bf16", window=0,
+                 scale=None, device="cuda"):
+        import torch
+        if kv_type not in KV_TYPES:
+            _refuse(MOE_ERR_INVALID_ARG, "PagedAttention")
+        self.kv_type = kv_type
+        self.dims = AttnDims(q_heads, kv_heads, head_dim, page_size, KV_TYPES[kv_type], window,
+                             head_dim ** -0.5 if scale is None else scale)
+        self.ws_bytes = moe_attn_workspace_bytes(self.dims)
+        if self.ws_bytes == 0:
+            raise MoEError(MOE_ERR_UNSUPPORTED, "moe_attn_workspace_bytes")
+        # only the status word must start at zero
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.workspace[:256].zero_()
+        self._index = self.workspace.get_device()
+        calls = _tensor_calls()
+        self._write, self._read, self._attend = calls.kv_write, calls.kv_read, calls.attend
+        self._handle = calls.attn(ctypes.addressof(self.dims), self.workspace.data_ptr(),
+                                  self.ws_bytes, self._index)
+
+    def new_cache(self, pages) -> KVCache:
+        """An empty cache of that many pages for one layer."""
+        import torch
+        d = self.dims
+        kind = {"bf16": torch.bfloat16, "int8": torch.int8,
+                "e4m3": torch.float8_e4m3fn}[self.kv_type]
+        shape = (pages, d.kv_heads, d.page_size, d.head_dim)
+        k, v = (torch.zeros(shape, dtype=kind, device=self.workspace.device) for _ in range(2))
+        if self.kv_type == "bf16":
+            return KVCache(k, v)
+        return KVCache(k, v, *(torch.zeros(shape[:3], device=k.device) for _ in range(2)))
+
+    def write(self, cache, k, v, page_table, seq_lens, cu_seqlens=None, stream=None):
+        """Puts the rows' k and v [rows][kv_heads][head_dim] (bf16, only the first
+        stride free) into ``cache`` at the sequences' last positions."""
+        r = self._write(self._handle, *cache, page_table, seq_lens, cu_seqlens, k, v,
+                        _given(stream))
+        if r != MOE_OK:
+            _not_done(r, "PagedAttention.write", self._index, self.write, cache, k, v, page_table,
+                      seq_lens, cu_seqlens, stream)
+
+    def read(self, cache, page_table, seq_lens, cu_seqlens=None, rows=None, k=None, v=None,
+             stream=None):
+        """The sequences' last positions back in bf16, ``rows`` of them in all (by
+        default those of ``k`` or ``v``, where they are given to be written).
+        Returns (k, v) [rows][kv_heads][head_dim]."""
+        if rows is None:
+            given = k if k is not None else v
+            if given is None:
+                _refuse(MOE_ERR_INVALID_ARG, "PagedAttention.read")
+            rows = given.shape[0]
+        r = self._read(self._handle, *cache, page_table, seq_lens, cu_seqlens, rows, k, v,
+                       _given(stream))
+        return r if type(r) is not int else _not_done(
+            r, "PagedAttention.read", self._index, self.read, cache, page_table, seq_lens,
+            cu_seqlens, rows, k, v, stream)
+
+    def attend(self, cache, q, page_table, seq_lens, cu_seqlens=None, out=None, stream=None):
+        """softmax(scale * q k^T) v for the rows of q [rows][q_heads][head_dim] (bf16,
+        only the first stride free), each over the positions up to its own, which
+        ``write`` has put into ``cache`` before.  Returns out, shaped like q."""
+        r = self._attend(self._handle, *cache, page_table, seq_lens, cu_seqlens, q, out,
+                         _given(stream))
+        return r if type(r) is not int else _not_done(
+            r, "PagedAttention.attend", self._index, self.attend, cache, q, page_table, seq_lens,
+            cu_seqlens, out, stream)
+
+    def status(self, stream=None) -> int:
+        import torch
+        with torch.cuda.device(self._index):
+            return moe_read_status(self.workspace, stream)
+
+    def clear_status(self, stream=None):
+        import torch
+        with torch.cuda.device(self._index):
+            moe_clear_status(self.workspace, stream)
+
+
+class DraftVerifier:
+    """Which drafted tokens stand against the target's probabilities, and the
+    token after them (``moe_verify_draft``).
+
+    ``target`` [B][T + 1][V] fp32 are the target's probabilities after 0 .. T of
+    the drafted tokens, ``draft`` [B][T][V] the drafter's (None: it was certain
+    of each token), ``draft_tokens`` int32 [B][T] (a negative one ends a shorter
+    draft), ``uniform`` fp32 [B][T + 1] numbers in [0, 1): one for each drafted
+    token, the last for the token after them.  T may be 0: a sample of each row.
+    """
+
+    def __init__(self, device="cuda"):
+        import torch
+        self.workspace = torch.zeros(256, dtype=torch.uint8, device=device)
+        self._index = self.workspace.get_device()
+        self._address = self.workspace.data_ptr()
+        self._verify = _tensor_calls().verify
+
+    def verify(self, target, draft_tokens, uniform, draft=None, tokens=None, accepted=None,
+               stream=None):
+        """Returns tokens int32 [B][T + 1] (those that stand, one more, then -1) and
+        accepted int32 [B] (how many stand)."""
+        r = self._verify(self._address, 256, self._index, target, draft, draft_tokens, uniform,
+                         tokens, accepted, _given(stream))
+        return r if type(r) is not int else _not_done(
+            r, "DraftVerifier.verify", self._index, self.verify, target, draft_tokens, uniform,
+            draft, tokens, accepted, stream)
+
+    def status(self, stream=None) -> int:
+        import torch
+        with torch.cuda.device(self._index):
+            return moe_read_status(self.workspace, stream)
+
+    def clear_status(self, stream=None):
+        import torch
+        with torch.cuda.device(self._index):
+            moe_clear_status(self.workspace, stream)

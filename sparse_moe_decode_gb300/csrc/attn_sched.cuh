@@ -1,0 +1,249 @@
+// attn_sched.cuh -- how the attention kernels share out a batch, from lengths
+// that only the device knows.
+//
+// A tile is R consecutive rows of one sequence and key/value head, a row being
+// a (token, head of the group) pair; its work is the KT-wide key tiles that
+// any of its rows sees.  All tiles' key tiles, one after another (sequence,
+// head, tile, key tile), are cut into equal shares, one for each block; a
+// share's pieces are segments of one tile each.  A tile that lies in one share
+// is finished there; otherwise its segments leave unnormalised sums (and the
+// softmax's maximum and total) for attn_combine.cu.  Every block finds its
+// share by itself: a scan over the sequences, whose key tiles have a closed
+// form.
+#pragma once
+
+#include "attn.h"
+#include "common.cuh"
+
+namespace moe {
+
+struct AttnSeq {
+  int start, n, len;  // rows start .. start + n - 1, len positions; n == 0: skipped
+};
+
+// One thread of the grid says so for each sequence that is out of range.
+__device__ __forceinline__ AttnSeq attn_seq(const AttnBatch &a, int b, bool report) {
+  AttnSeq s;
+  int end;
+  if (a.cu) {
+    s.start = a.cu[b], end = a.cu[b + 1];
+  } else {
+    s.start = b * a.T, end = s.start + a.T;
+  }
+  s.len = a.lens[b];
+  const bool bounds = s.start >= 0 && s.start <= end && end <= a.N;
+  s.n = bounds ? end - s.start : 0;
+  const bool bad = !bounds || (s.n > 0 && s.len > 0 &&
+                               (s.len < s.n || s.len > (static_cast<int64_t>(a.cols) << a.page_shift)));
+  if (bad && report) set_status(a.status, MOE_DEV_BAD_INDEX);
+  if (bad || s.len <= 0) s.n = 0;
+  return s;
+}
+
+// sum over i < n of floor((a i + b) / m), all >= 0, m > 0 (Euclid's steps).
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t sum = 0;
+  while (n > 0) {
+    sum += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
+    a %= m, b %= m;
+    const int64_t top = a * n + b;
+    if (top < m) break;
+    n = top / m, b = top % m;
+    const int64_t t = a;
+    a = m, m = t;
+  }
+  return sum;
+}
+
+// The tiles of one sequence and head.  A tile's keys end behind its last
+// row's position and begin, under a window, with its first row's first key.
+template <int R, int KT>
+struct AttnTiles {
+  int ctx, len, group, window, count;
+  int64_t rows;
+
+  __device__ __forceinline__ AttnTiles() {}
+  __device__ __forceinline__ AttnTiles(const AttnSeq &s, int group_, int window_)
+      : ctx(s.len - s.n), len(s.len), group(group_), window(window_) {
+    rows = static_cast<int64_t>(s.n) * group;
+    count = static_cast<int>((rows + R - 1) / R);
+  }
+  // (ctx + row / group) / KT = (ctx * group + row) / (KT * group), both floors
+  __device__ __forceinline__ int hi(int t) const {
+    if (t + 1 >= count) return (len - 1) / KT + 1;
+    return static_cast<int>((static_cast<int64_t>(ctx) * group + (t + 1LL) * R - 1) /
+                            (static_cast<int64_t>(KT) * group)) + 1;
+  }
+  __device__ __forceinline__ int lo(int t) const {
+    if (!window) return 0;
+    const int64_t x = (static_cast<int64_t>(ctx) - window + 1) * group + static_cast<int64_t>(t) * R;
+    return x <= 0 ? 0 : static_cast<int>(x / (static_cast<int64_t>(KT) * group));
+  }
+  // key tiles of the tiles before t
+  __device__ __forceinline__ int64_t before(int t) const {
+    if (t == 0) return 0;
+    if (count == 1) return hi(0) - lo(0);
+    const int64_t m = static_cast<int64_t>(KT) * group;
+    const int n = t < count ? t : count - 1;
+    int64_t sum = floor_sum(n, m, R, static_cast<int64_t>(ctx) * group + R - 1) + n;
+    if (t == count) sum += hi(count - 1);
+    if (window) {
+      const int64_t x0 = (static_cast<int64_t>(ctx) - window + 1) * group;
+      const int64_t i0 = x0 >= 0 ? 0 : (-x0 + R - 1) / R;
+      if (t > i0) sum -= floor_sum(t - i0, m, R, x0 + i0 * R);
+    }
+    return sum;
+  }
+};
+
+// What a block leaves for attn_combine.cu about the tile that it began and
+// did not finish.
+struct AttnOpen {
+  int32_t last;            // the block that finishes it; -1: there is none
+  int32_t rows;            // of the tile
+  int32_t start, row0;     // the sequence's first token row, the tile's first row
+  int32_t head, pad[3];
+};
+
+struct AttnShare {  // in shared memory
+  int64_t at, per, total, offset;  // first key tile, a share's, all, within the sequence
+  int64_t scan[32];
+  int32_t seq;
+};
+
+// Sequences whose rows are in (least, most] take part.
+struct AttnRange {
+  int32_t least, most;
+};
+
+template <int R, int KT>
+__device__ __forceinline__ int64_t attn_units(const AttnBatch &a, const AttnRange &r, int b,
+                                              bool report) {
+  const AttnSeq s = attn_seq(a, b, report);
+  const int64_t rows = static_cast<int64_t>(s.n) * a.group;
+  if (s.n == 0 || rows <= r.least || rows > r.most) return 0;
+  const AttnTiles<R, KT> t(s, a.group, a.window);
+  return t.before(t.count) * a.kv_heads;
+}
+
+// All threads of the block (a multiple of 32, at most 1024): this block's
+// share.  seq = -1: nothing to do.
+template <int R, int KT>
+__device__ __forceinline__ void attn_share(const AttnBatch &a, const AttnRange &r, int least_share,
+                                           AttnShare *sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+  const bool one = a.B <= nt;
+  int64_t mine = 0, sum = 0;
+  for (int b = tid; b < a.B; b += nt) {
+    mine = attn_units<R, KT>(a, r, b, blockIdx.x == 0);
+    sum += mine;
+  }
+  // an inclusive scan over the threads of v; the total through sh->scan
+  const auto scan = [&](int64_t v, int64_t &total) {
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t n = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += n;
+    }
+    __syncthreads();
+    if (lane == 31) sh->scan[warp] = v;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < nt / 32; ++w) {
+      if (w == warp) v += total;
+      total += sh->scan[w];
+    }
+    return v;
+  };
+  int64_t total, incl = scan(sum, total);
+  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < least_share) per = least_share;
+  const int64_t at = per * blockIdx.x;
+  if (tid == 0) {
+    sh->at = at, sh->per = per, sh->total = total;
+    sh->seq = -1;
+  }
+  __syncthreads();
+  if (at >= total) return;
+  if (one) {
+    if (at >= incl - mine && at < incl) sh->seq = tid, sh->offset = at - (incl - mine);
+  } else {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < a.B && base <= at; b0 += nt) {
+      const int b = b0 + tid;
+      const int64_t u = b < a.B ? attn_units<R, KT>(a, r, b, false) : 0;
+      int64_t round;
+      incl = base + scan(u, round);
+      if (at >= incl - u && at < incl) sh->seq = b, sh->offset = at - (incl - u);
+      base += round;
+    }
+  }
+  __syncthreads();
+}
+
+// A block's way through its share, segment by segment.  Every warp walks it
+// by itself and sees the same.
+template <int R, int KT>
+struct AttnWalk {
+  int b, head, tile, at, left_in_tile;
+  int64_t left, next_unit;  // key tiles left of the share; of all, before the next segment
+  AttnSeq s;
+  AttnTiles<R, KT> t;
+
+  // the current segment (of sequence b and head)
+  int cur;            // its tile
+  int k0, k1;         // key tiles
+  bool begins, ends;  // the tile's first, last
+  int64_t tile_end;   // of all key tiles
+
+  __device__ __forceinline__ void init(const AttnBatch &a, const AttnShare &sh) {
+    b = sh.seq;
+    left = 0;
+    if (b < 0) return;
+    left = sh.total - sh.at < sh.per ? sh.total - sh.at : sh.per;
+    next_unit = sh.at;
+    s = attn_seq(a, b, false);
+    t = AttnTiles<R, KT>(s, a.group, a.window);
+    int64_t rem = sh.offset;
+    const int64_t each = t.before(t.count);
+    head = static_cast<int>(rem / each);
+    rem -= each * head;
+    int low = 0, high = t.count;  // before(low) <= rem < before(high)
+    while (high - low > 1) {
+      const int mid = (low + high) / 2;
+      if (t.before(mid) <= rem) low = mid;
+      else high = mid;
+    }
+    tile = low;
+    at = static_cast<int>(rem - t.before(low));
+  }
+  __device__ __forceinline__ bool next(const AttnBatch &a, const AttnRange &r) {
+    if (left <= 0) return false;
+    if (tile == t.count) {
+      tile = 0;
+      if (++head == a.kv_heads) {
+        head = 0;
+        do {
+          if (++b >= a.B) {
+            left = 0;
+            return false;
+          }
+          s = attn_seq(a, b, false);
+        } while (s.n == 0 || static_cast<int64_t>(s.n) * a.group <= r.least ||
+                 static_cast<int64_t>(s.n) * a.group > r.most);
+        t = AttnTiles<R, KT>(s, a.group, a.window);
+      }
+    }
+    const int lo = t.lo(tile), whole = t.hi(tile) - lo;
+    const int n = whole - at < left ? whole - at : static_cast<int>(left);
+    k0 = lo + at, k1 = k0 + n;
+    begins = at == 0, ends = at + n == whole;
+    tile_end = next_unit + whole - at;
+    cur = tile;
+    left -= n, next_unit += n;
+    if (ends) at = 0, ++tile;
+    else at += n;
+    return true;
+  }
+};
+
+}  // namespace moe

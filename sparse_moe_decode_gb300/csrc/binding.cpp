@@ -1,5 +1,6 @@
 // binding.cpp -- the tensor-level calls of the Python package whose kernels
-// take a few microseconds (the gated delta rule, the norms around a block):
+// take a few microseconds (the gated delta rule, the norms around a block,
+// paged attention and its cache, the verification of drafts):
 // argument checks, output allocation and the call of the C ABI without the
 // interpreter's cost per attribute.  A CPython extension module; the library's
 // functions come in through `init`, so that it links against torch alone.
@@ -21,6 +22,10 @@ namespace {
 decltype(&moe_delta_chunk) g_chunk;
 decltype(&moe_delta_step) g_step;
 decltype(&moe_norm_gate_residual) g_norm;
+decltype(&moe_kv_write) g_kv_write;
+decltype(&moe_kv_read) g_kv_read;
+decltype(&moe_paged_attention) g_attention;
+decltype(&moe_verify_draft) g_draft;
 
 struct Refused {
   int status;
@@ -120,9 +125,9 @@ void written(PyObject *o) {
   if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
 }
 
-at::Tensor fresh(at::IntArrayRef sizes, int64_t device) {
+at::Tensor fresh(at::IntArrayRef sizes, int64_t device, at::ScalarType type = at::kBFloat16) {
   return at::empty(sizes, at::TensorOptions()
-                              .dtype(at::kBFloat16)
+                              .dtype(type)
                               .device(at::kCUDA, static_cast<c10::DeviceIndex>(device)));
 }
 
@@ -367,13 +372,246 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-// init(moe_delta_chunk, moe_delta_step, moe_norm_gate_residual): addresses
+// -------------------------------------------------------- paged attention
+
+struct Attn {
+  moe_attn_dims dims;
+  void *workspace;
+  size_t ws_bytes;
+  int64_t device;
+};
+
+constexpr const char *kAttn = "sparse_moe_decode_gb300.attn";
+
+void attn_free(PyObject *capsule) {
+  delete static_cast<Attn *>(PyCapsule_GetPointer(capsule, kAttn));
+}
+
+// attn(address of a moe_attn_dims, workspace, ws_bytes, device) -> handle
+PyObject *attn_handle(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    require(n == 4);
+    Attn *h = new Attn{*static_cast<const moe_attn_dims *>(address(a[0])), address(a[1]),
+                       static_cast<size_t>(integer(a[2])), integer(a[3])};
+    return PyCapsule_New(h, kAttn, attn_free);
+  });
+}
+
+const Attn &attn_of(PyObject *o) {
+  const void *p = PyCapsule_GetPointer(o, kAttn);
+  if (!p) {
+    PyErr_Clear();
+    require(false);
+  }
+  const Attn &h = *static_cast<const Attn *>(p);
+  require(h.device >= 0);  // CUDA memory only
+  return h;
+}
+
+// The cache's tensors k, v, k_scale, v_scale at a[0..3].
+moe_kv_cache attn_cache(const Attn &h, PyObject *const *a) {
+  const moe_attn_dims &d = h.dims;
+  const at::ScalarType type = d.kv_type == MOE_KV_BF16   ? at::kBFloat16
+                              : d.kv_type == MOE_KV_INT8 ? at::kChar
+                                                         : at::kFloat8_e4m3fn;
+  moe_kv_cache c = {};
+  for (int i = 0; i < 2; ++i) {
+    const at::Tensor &x = tensor(a[i]);
+    place(x, type, h.device);
+    require(x.dim() == 4 && x.size(1) == d.kv_heads && x.size(2) == d.page_size &&
+            x.size(3) == d.head_dim && x.is_contiguous());
+    require(i == 0 || x.size(0) == c.pages);
+    c.pages = x.size(0);
+    (i ? c.v : c.k) = x.mutable_data_ptr();
+    if (d.kv_type == MOE_KV_BF16) {
+      require(a[2 + i] == Py_None);
+      continue;
+    }
+    const at::Tensor &s = tensor(a[2 + i]);
+    place(s, at::kFloat, h.device);
+    require(s.dim() == 3 && s.size(0) == c.pages && s.size(1) == d.kv_heads &&
+            s.size(2) == d.page_size && s.is_contiguous());
+    (i ? c.v_scale : c.k_scale) = static_cast<float *>(s.mutable_data_ptr());
+  }
+  return c;
+}
+
+// page_table, seq_lens and cu_seqlens (or None) at a[0..2]
+moe_kv_batch attn_batch(const Attn &h, PyObject *const *a, int64_t rows) {
+  const at::Tensor &table = tensor(a[0]), &lens = tensor(a[1]);
+  place(table, at::kInt, h.device), place(lens, at::kInt, h.device);
+  require(lens.dim() == 1 && lens.is_contiguous());
+  const int64_t B = lens.size(0);
+  require(table.dim() == 2 && table.size(0) == B &&
+          (table.size(1) <= 1 || table.stride(1) == 1));
+  require(rows <= INT32_MAX && B <= INT32_MAX && table.size(1) <= INT32_MAX);
+  moe_kv_batch b = {};
+  b.N = static_cast<int32_t>(rows), b.B = static_cast<int32_t>(B);
+  if (a[2] != Py_None) {
+    const at::Tensor &cu = tensor(a[2]);
+    place(cu, at::kInt, h.device);
+    require(cu.dim() == 1 && cu.size(0) == B + 1 && cu.is_contiguous());
+    b.cu_seqlens = static_cast<const int32_t *>(cu.const_data_ptr());
+  }
+  b.seq_lens = static_cast<const int32_t *>(lens.const_data_ptr());
+  b.page_table = static_cast<const int32_t *>(table.const_data_ptr());
+  b.table_cols = static_cast<int32_t>(table.size(1));
+  b.table_ld = B > 1 ? table.stride(0) : b.table_cols;
+  return b;
+}
+
+// write(handle, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_seqlens, k, v,
+// stream) -> 0
+PyObject *kv_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    require(n == 11);
+    const Attn &h = attn_of(a[0]);
+    const at::Tensor &k = tensor(a[8]), &v = tensor(a[9]);
+    require(k.dim() == 3);
+    const int64_t row[2] = {h.dims.kv_heads, h.dims.head_dim};
+    const int64_t k_ld = row_stride(k, at::kBFloat16, h.device, k.size(0), row);
+    const int64_t v_ld = row_stride(v, at::kBFloat16, h.device, k.size(0), row);
+    const moe_kv_cache c = attn_cache(h, a + 1);
+    const moe_kv_batch b = attn_batch(h, a + 5, k.size(0));
+    const OnStream stream(a[10], h.device);
+    const moe_status st = g_kv_write(&h.dims, &c, &b,
+                                     static_cast<const moe_bf16 *>(k.const_data_ptr()), k_ld,
+                                     static_cast<const moe_bf16 *>(v.const_data_ptr()), v_ld,
+                                     h.workspace, h.ws_bytes, stream.get());
+    if (st == MOE_OK)
+      for (int i = 1; i <= 4; ++i) written(a[i]);
+    return PyLong_FromLong(st);
+  });
+}
+
+at::Tensor attn_out(const Attn &h, PyObject *o, int64_t rows, int64_t heads, int64_t &ld) {
+  const int64_t row[2] = {heads, h.dims.head_dim};
+  if (o == Py_None) {
+    ld = row[0] * row[1];
+    return fresh({rows, row[0], row[1]}, h.device);
+  }
+  at::Tensor out = tensor(o);
+  ld = row_stride(out, at::kBFloat16, h.device, rows, row);
+  return out;
+}
+
+// read(handle, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_seqlens, rows, k, v,
+// stream) -> (k, v)
+PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    require(n == 12);
+    const Attn &h = attn_of(a[0]);
+    const int64_t rows = integer(a[8]);
+    require(rows >= 0 && rows <= INT32_MAX);
+    const moe_kv_cache c = attn_cache(h, a + 1);
+    const moe_kv_batch b = attn_batch(h, a + 5, rows);
+    const OnStream stream(a[11], h.device);
+    int64_t k_ld, v_ld;
+    const at::Tensor k = attn_out(h, a[9], rows, h.dims.kv_heads, k_ld);
+    const at::Tensor v = attn_out(h, a[10], rows, h.dims.kv_heads, v_ld);
+    const moe_status st =
+        g_kv_read(&h.dims, &c, &b, static_cast<moe_bf16 *>(k.mutable_data_ptr()), k_ld,
+                  static_cast<moe_bf16 *>(v.mutable_data_ptr()), v_ld, h.workspace, h.ws_bytes,
+                  stream.get());
+    if (st != MOE_OK) return PyLong_FromLong(st);
+    written(a[9]), written(a[10]);
+    PyObject *both = PyTuple_New(2);
+    if (!both) return nullptr;
+    PyTuple_SET_ITEM(both, 0, THPVariable_Wrap(k));
+    PyTuple_SET_ITEM(both, 1, THPVariable_Wrap(v));
+    return both;
+  });
+}
+
+// attend(handle, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_seqlens, q, out,
+// stream) -> out
+PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    require(n == 11);
+    const Attn &h = attn_of(a[0]);
+    const at::Tensor &q = tensor(a[8]);
+    require(q.dim() == 3);
+    const int64_t rows = q.size(0), row[2] = {h.dims.q_heads, h.dims.head_dim};
+    const int64_t q_ld = row_stride(q, at::kBFloat16, h.device, rows, row);
+    const moe_kv_cache c = attn_cache(h, a + 1);
+    const moe_kv_batch b = attn_batch(h, a + 5, rows);
+    const OnStream stream(a[10], h.device);
+    int64_t ld;
+    const at::Tensor out = attn_out(h, a[9], rows, h.dims.q_heads, ld);
+    const moe_status st =
+        g_attention(&h.dims, &c, &b, static_cast<const moe_bf16 *>(q.const_data_ptr()), q_ld,
+                    static_cast<moe_bf16 *>(out.mutable_data_ptr()), ld, h.workspace, h.ws_bytes,
+                    stream.get());
+    if (st != MOE_OK) return PyLong_FromLong(st);
+    written(a[9]);
+    return THPVariable_Wrap(out);
+  });
+}
+
+// ------------------------------------------------------------------ drafts
+
+// verify(workspace, ws_bytes, device, target, draft, draft_tokens, uniform, tokens, accepted,
+// stream) -> (tokens, accepted)
+PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    require(n == 10);
+    const int64_t device = integer(a[2]);
+    require(device >= 0);
+    const at::Tensor &p = tensor(a[3]), &d = tensor(a[5]), &u = tensor(a[6]);
+    place(p, at::kFloat, device), place(d, at::kInt, device), place(u, at::kFloat, device);
+    require(p.dim() == 3 && d.dim() == 2 && p.size(1) >= 1);
+    const int64_t B = p.size(0), T = p.size(1) - 1, V = p.size(2);
+    require(B <= INT32_MAX && T <= INT32_MAX && V >= 1 && V <= INT32_MAX);
+    require((V == 1 || p.stride(2) == 1) && d.size(0) == B && d.size(1) == T && d.is_contiguous());
+    require(u.dim() == 2 && u.size(0) == B && u.size(1) == T + 1 && u.is_contiguous());
+    const float *q = nullptr;
+    int64_t q_seq = 0, q_ld = 0;
+    if (a[4] != Py_None) {
+      const at::Tensor &x = tensor(a[4]);
+      place(x, at::kFloat, device);
+      require(x.dim() == 3 && x.size(0) == B && x.size(1) == T && x.size(2) == V &&
+              (V == 1 || x.stride(2) == 1));
+      if (T > 0) q = static_cast<const float *>(x.const_data_ptr());
+      q_seq = x.stride(0), q_ld = x.stride(1);
+    }
+    const auto whole = [&](PyObject *o, at::IntArrayRef sizes) {
+      if (o == Py_None) return fresh(sizes, device, at::kInt);
+      at::Tensor x = tensor(o);
+      place(x, at::kInt, device);
+      require(x.sizes() == sizes && x.is_contiguous());
+      return x;
+    };
+    const OnStream stream(a[9], device);
+    const at::Tensor tokens = whole(a[7], {B, T + 1}), accepted = whole(a[8], {B});
+    const moe_status st = g_draft(
+        static_cast<int>(B), static_cast<int>(T), static_cast<int>(V),
+        static_cast<const float *>(p.const_data_ptr()), p.stride(0), p.stride(1), q, q_seq, q_ld,
+        static_cast<const int32_t *>(d.const_data_ptr()),
+        static_cast<const float *>(u.const_data_ptr()),
+        static_cast<int32_t *>(tokens.mutable_data_ptr()),
+        static_cast<int32_t *>(accepted.mutable_data_ptr()), address(a[0]),
+        static_cast<size_t>(integer(a[1])), stream.get());
+    if (st != MOE_OK) return PyLong_FromLong(st);
+    written(a[7]), written(a[8]);
+    PyObject *both = PyTuple_New(2);
+    if (!both) return nullptr;
+    PyTuple_SET_ITEM(both, 0, THPVariable_Wrap(tokens));
+    PyTuple_SET_ITEM(both, 1, THPVariable_Wrap(accepted));
+    return both;
+  });
+}
+
+// init(the addresses of the library's functions, in the order below)
 PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
-    require(n == 3);
+    require(n == 7);
     g_chunk = reinterpret_cast<decltype(g_chunk)>(address(a[0]));
     g_step = reinterpret_cast<decltype(g_step)>(address(a[1]));
     g_norm = reinterpret_cast<decltype(g_norm)>(address(a[2]));
+    g_kv_write = reinterpret_cast<decltype(g_kv_write)>(address(a[3]));
+    g_kv_read = reinterpret_cast<decltype(g_kv_read)>(address(a[4]));
+    g_attention = reinterpret_cast<decltype(g_attention)>(address(a[5]));
+    g_draft = reinterpret_cast<decltype(g_draft)>(address(a[6]));
     Py_RETURN_NONE;
   });
 }
@@ -386,6 +624,11 @@ PyMethodDef kMethods[] = {METHOD("init", init),
                           METHOD("delta_chunk", delta_chunk),
                           METHOD("delta_step", delta_step),
                           METHOD("norm", norm),
+                          METHOD("attn", attn_handle),
+                          METHOD("kv_write", kv_write),
+                          METHOD("kv_read", kv_read),
+                          METHOD("attend", attend),
+                          METHOD("verify", verify),
                           {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods,

@@ -1,0 +1,275 @@
+// kv_cache.cu -- the paged cache's rows written (and quantised) and read back.
+//
+// A row is one token's D values of one head of k or v; D / 8 lanes take it, 16
+// bytes of bf16 each, and find its scale by shuffles.  Bound by memory: a row
+// is read and written once.
+//
+// int8: c = x / s with the exact quotient rounded.  With f = floor(x * (1 / s)),
+// off by one at most where x / s is next to a whole number, the sign of
+// x - (f + 1/2) s, which one fused multiply-add gives exactly, says which of
+// f and f + 1 is nearest, or that x / s lies between them.
+// e4m3: s is a power of two, so x / s is exact and the conversion rounds once.
+#include "attn.h"
+#include "attn_sched.cuh"
+#include "early.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct KvSide {  // of k or v
+  const moe_bf16 *in;
+  moe_bf16 *out;
+  int64_t ld;
+  void *store;
+  float *scale;
+};
+
+// Where token t's row of `head` lies in the cache; -1: nowhere.
+__device__ __forceinline__ int64_t kv_place(const AttnBatch &a, int t, int head, AttnSeq &s,
+                                            int &b) {
+  if (b < 0 || t < s.start || t >= s.start + s.n) {
+    if (a.cu) {
+      int low = 0, high = a.B;  // cu[low] <= t < cu[high]
+      while (high - low > 1) {
+        const int mid = (low + high) / 2;
+        if (a.cu[mid] <= t) low = mid;
+        else high = mid;
+      }
+      b = low;
+    } else {
+      b = t / a.T;
+    }
+    s = attn_seq(a, b, false);
+    if (t < s.start || t >= s.start + s.n) {
+      b = -1;
+      return -1;
+    }
+  }
+  const int pos = s.len - s.n + (t - s.start);
+  const int page = a.table[b * a.table_ld + (pos >> a.page_shift)];
+  if (page < 0 || page >= a.pages) {
+    set_status(a.status, MOE_DEV_BAD_INDEX);
+    return -1;
+  }
+  return ((static_cast<int64_t>(page) * a.kv_heads + head) << a.page_shift) +
+         (pos & ((1 << a.page_shift) - 1));
+}
+
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The scale of a row whose largest magnitude is `top`, and its inverse.
+template <int KV>
+__device__ __forceinline__ void kv_scale(float top, float &s, float &inv) {
+  if (KV == MOE_KV_INT8) {
+    s = fmaxf(__fdiv_rn(top, 127.0f), 0x1p-126f);
+    inv = __frcp_rn(s);
+  } else {
+    // top = m 2^e, 448 = 1.75 * 2^8: s = 2^(e - 8), twice that where m > 1.75
+    const int e = static_cast<int>((__float_as_uint(top) + 0x1FFFFFu) >> 23) - 8;
+    const uint32_t f = static_cast<uint32_t>(max(e, 1));
+    s = __uint_as_float(f << 23);
+    inv = __uint_as_float((254u - f) << 23);
+  }
+}
+
+__device__ __forceinline__ uint32_t int8_code(float x, float s, float inv) {
+  const float v = fabsf(x), f = floorf(v * inv);
+  const float d = fmaf(-(f + 0.5f), s, v);
+  float c = d > 0.0f ? f + 1.0f : f;
+  // in the middle: the even one (f is below 2^23: half of it is exact)
+  if (d == 0.0f) c = f + 2.0f * (0.5f * f - floorf(0.5f * f));
+  // 1.5 * 2^23 + c: the low byte is c in two's complement
+  return __float_as_uint(copysignf(c, x) + 12582912.0f);
+}
+
+template <int KV>
+__device__ __forceinline__ uint2 kv_codes(const float (&x)[8], float s, float inv) {
+  uint32_t r[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (KV == MOE_KV_INT8) {
+      uint32_t c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] = int8_code(x[4 * i + j], s, inv);
+      r[i] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    } else {
+      uint16_t lo, hi;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+          : "=h"(lo)
+          : "f"(x[4 * i + 1] * inv), "f"(x[4 * i] * inv));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+          : "=h"(hi)
+          : "f"(x[4 * i + 3] * inv), "f"(x[4 * i + 2] * inv));
+      r[i] = lo | (static_cast<uint32_t>(hi) << 16);
+    }
+  }
+  return make_uint2(r[0], r[1]);
+}
+
+template <int KV>
+__device__ __forceinline__ void kv_values(uint2 c, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t v = i ? c.y : c.x;
+    if (KV == MOE_KV_INT8) {
+      const f4 f = i8x4_to_f32(v);
+      x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v >> (16 * j))));
+        asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\t"
+            "cvt.f32.f16 %1, u;\n\t}"
+            : "=f"(x[4 * i + 2 * j]), "=f"(x[4 * i + 2 * j + 1])
+            : "r"(h));
+      }
+    }
+  }
+}
+
+// Row i of `rows`: token i / (2 heads), k's heads and then v's.
+template <int D, int KV, bool WRITE, int EACH>
+__global__ void __launch_bounds__(kThreads)
+kv_rows_kernel(const AttnBatch a, const KvSide k, const KvSide v, uint32_t rows) {
+  constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
+  early_begin();
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < a.B; b += kThreads) attn_seq(a, b, true);
+  const int l = threadIdx.x % kLanes;
+  const uint32_t first = blockIdx.x * (kRows * EACH) + threadIdx.x / kLanes;
+  const uint32_t heads2 = 2 * a.kv_heads;
+  // (chosen by selects: an index would put the arguments into local memory)
+#define OF(e, field) (kv[e] ? v.field : k.field)
+  int64_t place[EACH];
+  uint32_t token[EACH];
+  int kv[EACH], head[EACH];
+  uint4 data[EACH];
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    const uint32_t i = first + e * kRows;
+    token[e] = i / heads2;
+    const int h = i % heads2;
+    kv[e] = h >= a.kv_heads;
+    head[e] = kv[e] ? h - a.kv_heads : h;
+    if (WRITE && i < rows)
+      data[e] = ld_nc(OF(e, in) + token[e] * OF(e, ld) + head[e] * D + l * 8);
+  }
+  AttnSeq s;
+  int b = -1;
+#pragma unroll
+  for (int e = 0; e < EACH; ++e)
+    place[e] = first + e * kRows < rows ? kv_place(a, token[e], head[e], s, b) : -1;
+  if (WRITE) {
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+      if (KV == MOE_KV_BF16) {
+        if (place[e] >= 0)
+          *reinterpret_cast<uint4 *>(static_cast<moe_bf16 *>(OF(e, store)) + place[e] * D + l * 8) =
+              data[e];
+        continue;
+      }
+      const uint32_t w[4] = {data[e].x, data[e].y, data[e].z, data[e].w};
+      float x[8];
+      uint32_t most = 0;  // magnitudes order like their bits, inf and NaN above all
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[2 * j] = bf16_lo(w[j]), x[2 * j + 1] = bf16_hi(w[j]);
+        most = max(most, max((w[j] << 16) & 0x7FFF0000u, w[j] & 0x7FFF0000u));
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1)
+        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+      float scale, inv;
+      kv_scale<KV>(__uint_as_float(most), scale, inv);
+      uint2 c = kv_codes<KV>(x, scale, inv);
+      if (most >= 0x7F800000u) c = make_uint2(0, 0), scale = __uint_as_float(0x7FC00000u);
+      if (place[e] >= 0) {
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(OF(e, store)) + place[e] * D + l * 8) = c;
+        if (l == 0) OF(e, scale)[place[e]] = scale;
+      }
+    }
+  } else {
+    float scale[EACH];
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+      if (!OF(e, out)) place[e] = -1;
+      if (place[e] < 0) continue;
+      const uint8_t *from = static_cast<const uint8_t *>(OF(e, store));
+      if (KV == MOE_KV_BF16) {
+        data[e] = *reinterpret_cast<const uint4 *>(from + (place[e] * D + l * 8) * 2);
+      } else {
+        const uint2 c = *reinterpret_cast<const uint2 *>(from + place[e] * D + l * 8);
+        data[e].x = c.x, data[e].y = c.y;
+        scale[e] = OF(e, scale)[place[e]];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+      if (place[e] < 0) continue;
+      if (KV != MOE_KV_BF16) {
+        float x[8];
+        kv_values<KV>(make_uint2(data[e].x, data[e].y), x);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = bf16x2_of(x[2 * j] * scale[e], x[2 * j + 1] * scale[e]);
+        data[e] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      *reinterpret_cast<uint4 *>(OF(e, out) + token[e] * OF(e, ld) + head[e] * D + l * 8) =
+          data[e];
+    }
+  }
+#undef OF
+}
+
+template <int D, int KV, bool WRITE>
+cudaError_t launch_rows(const AttnBatch &a, const KvSide (&io)[2], cudaStream_t s) {
+  constexpr int kRows = kThreads / (D / 8);
+  const uint32_t rows = 2u * a.N * a.kv_heads;
+  const auto go = [&](auto kernel, int each) {
+    const uint32_t per = kRows * each;
+    return launch_early(kernel, dim3((rows + per - 1) / per), kThreads, 0, s, a, io[0], io[1], rows);
+  };
+  if (rows <= 8u * kRows * 152) return go(kv_rows_kernel<D, KV, WRITE, 1>, 1);
+  return go(kv_rows_kernel<D, KV, WRITE, 4>, 4);
+}
+
+template <int D, bool WRITE>
+cudaError_t launch_rows_kv(int kv, const AttnBatch &a, const KvSide (&io)[2], cudaStream_t s) {
+  if (kv == MOE_KV_BF16) return launch_rows<D, MOE_KV_BF16, WRITE>(a, io, s);
+  if (kv == MOE_KV_INT8) return launch_rows<D, MOE_KV_INT8, WRITE>(a, io, s);
+  return launch_rows<D, MOE_KV_E4M3, WRITE>(a, io, s);
+}
+
+template <bool WRITE>
+cudaError_t launch_rows_any(const moe_attn_dims &d, const AttnBatch &a, const KvSide (&io)[2],
+                            cudaStream_t s) {
+  if (d.head_dim == 64) return launch_rows_kv<64, WRITE>(d.kv_type, a, io, s);
+  if (d.head_dim == 128) return launch_rows_kv<128, WRITE>(d.kv_type, a, io, s);
+  return launch_rows_kv<256, WRITE>(d.kv_type, a, io, s);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write(const moe_attn_dims &d, const moe_kv_cache &c, const AttnBatch &a,
+                            const moe_bf16 *k, int64_t k_ld, const moe_bf16 *v, int64_t v_ld,
+                            cudaStream_t s) {
+  const KvSide io[2] = {{k, nullptr, k_ld, c.k, c.k_scale}, {v, nullptr, v_ld, c.v, c.v_scale}};
+  return launch_rows_any<true>(d, a, io, s);
+}
+
+cudaError_t launch_kv_read(const moe_attn_dims &d, const moe_kv_cache &c, const AttnBatch &a,
+                           moe_bf16 *k, int64_t k_ld, moe_bf16 *v, int64_t v_ld, cudaStream_t s) {
+  const KvSide io[2] = {{nullptr, k, k_ld, c.k, c.k_scale}, {nullptr, v, v_ld, c.v, c.v_scale}};
+  return launch_rows_any<false>(d, a, io, s);
+}
+
+}  // namespace moe
