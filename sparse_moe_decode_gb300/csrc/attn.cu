@@ -61,7 +61,7 @@ attn_combine_kernel(const AttnBatch a, const AttnArgs p, int D, int blocks) {
       const float2 ml = p.parts.ml[at];
       const float w = ml.x == -INFINITY ? 0.0f : attn_exp2(ml.x - top);
       l += w * ml.y;
-      if (d < D) {
+      if (d < D && ml.x != -INFINITY) {  // (a part that saw no key has no sums)
         const float4 x = *reinterpret_cast<const float4 *>(p.parts.sums + at * D + d);
         v.x += w * x.x, v.y += w * x.y, v.z += w * x.z, v.w += w * x.w;
       }
@@ -97,11 +97,15 @@ struct Layout {
 };
 
 Layout layout(const moe_attn_dims &d) {
+  // both kernels' parts: 2 a block
+  const size_t tc = 2 * kTcMaxCtas * (d.head_dim == 256 ? 128 : 256);
+  size_t rows = 2 * kStreamMaxCtas * kStreamMaxRows;
+  if (tc > rows) rows = tc;
   Layout l;
   l.open = 256;
   l.ml = l.open + align256(kStreamMaxCtas * sizeof(AttnOpen));
-  l.sums = l.ml + align256(2 * kStreamMaxCtas * kStreamMaxRows * sizeof(float2));
-  l.total = l.sums + static_cast<size_t>(2 * kStreamMaxCtas) * kStreamMaxRows * d.head_dim * 4;
+  l.sums = l.ml + align256(rows * sizeof(float2));
+  l.total = l.sums + rows * d.head_dim * 4;
   return l;
 }
 
@@ -122,6 +126,15 @@ bool attn_map(CUtensorMap *m, const void *base, int d, int size, int64_t rows, i
   const uint32_t bx[3] = {static_cast<uint32_t>(inner), static_cast<uint32_t>(box),
                           static_cast<uint32_t>(cols)};
   return tc_make_map3(m, base, dt, size, dims, strides, bx);
+}
+
+bool attn_tc_map(CUtensorMap *m, const void *base, int d, int size, int64_t rows, int box, int cols) {
+  const uint64_t dims[3] = {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(d) / 64};
+  const uint64_t strides[2] = {static_cast<uint64_t>(d) * size, static_cast<uint64_t>(64) * size};
+  const uint32_t bx[3] = {64, static_cast<uint32_t>(box), static_cast<uint32_t>(cols)};
+  if (size == 2)
+    return tc_make_map3(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dims, strides, bx);
+  return tc_make_map_nd(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dims, strides, bx);
 }
 
 cudaError_t launch_attn_combine(const AttnBatch &a, const AttnArgs &p, int d, int blocks,
@@ -152,14 +165,29 @@ cudaError_t launch_attention(const moe_attn_dims &d, const moe_kv_cache &c, cons
   x.args.parts.rows = 0;
   x.args.scale_log2 = d.scale * 1.44269504088896340736f;
   x.args.budget = tc_wait_budget_ns();
-  x.args.least_share = 2;
-  x.range.least = 0, x.range.most = INT32_MAX;
-  const int64_t rows = a.cu ? a.N : static_cast<int64_t>(a.T) * a.group;
-  const int wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   const auto stream = d.kv_type == MOE_KV_BF16   ? launch_stream_bf16
                       : d.kv_type == MOE_KV_INT8 ? launch_stream_int8
                                                  : launch_stream_e4m3;
-  return stream(x, d.head_dim, wr);
+  const auto tc = d.kv_type == MOE_KV_BF16   ? launch_tc_bf16
+                  : d.kv_type == MOE_KV_INT8 ? launch_tc_int8
+                                             : launch_tc_e4m3;
+  // Sequences of up to `few` rows stream; the others go to the tensor cores'
+  // kernel.  Lengths that only the device knows: both kernels look.
+  const int64_t most = static_cast<int64_t>(a.cu ? a.N : a.T) * a.group;
+  const int few = a.cu ? (a.group <= 16 ? 16 : a.group <= 32 ? 32 : 64) : 64;
+  cudaError_t e = cudaSuccess;
+  if (a.cu || most <= few) {
+    const int rows = static_cast<int>(most < few ? most : few);
+    x.range.least = 0, x.range.most = few;
+    x.args.least_share = 2;
+    e = stream(x, d.head_dim, rows <= 16 ? 1 : rows <= 32 ? 2 : 4);
+  }
+  if (e == cudaSuccess && most > few) {
+    x.range.least = few, x.range.most = INT32_MAX;
+    x.args.least_share = 1;
+    e = tc(x, d.head_dim);
+  }
+  return e;
 }
 
 }  // namespace moe

@@ -22,6 +22,14 @@ struct AttnLaunch {
 // is `box` positions of one page and head, all their columns.
 bool attn_map(CUtensorMap *m, const void *base, int d, int size, int64_t rows, int box);
 
+// The same rows as columns of 64 elements (128 bytes with the swizzle, or 64
+// of codes as they lie): a box is `box` positions by `cols` of them.
+bool attn_tc_map(CUtensorMap *m, const void *base, int d, int size, int64_t rows, int box, int cols);
+
+cudaError_t launch_tc_bf16(const AttnLaunch &x, int d);
+cudaError_t launch_tc_int8(const AttnLaunch &x, int d);
+cudaError_t launch_tc_e4m3(const AttnLaunch &x, int d);
+
 cudaError_t launch_stream_bf16(const AttnLaunch &x, int d, int wr);
 cudaError_t launch_stream_int8(const AttnLaunch &x, int d, int wr);
 cudaError_t launch_stream_e4m3(const AttnLaunch &x, int d, int wr);

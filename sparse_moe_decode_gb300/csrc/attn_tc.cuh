@@ -1,0 +1,714 @@
+// attn_tc.cuh -- attention of many rows (prompts, chunks, long drafts): both
+// products on the 5th-generation tensor cores.
+//
+// A tile is R = 128 NQ rows (token, head of the group) of one sequence and
+// key/value head: NQ = 2 query tiles of 128 rows where their sums fit tensor
+// memory (head_dim <= 128), else one.  Key tiles are 128 keys.  Per key tile
+// and query tile
+//   S = q k^T       128 x 128, both operands in shared memory,
+//   p = 2^(s - m)   by the 128 threads that hold a row of S each,
+//   O += p v        p in tensor memory (over S, bf16 or fp16 pairs), v in
+//                   shared memory, O in tensor memory (fp32),
+// with the running maximum m.  O is brought to a new maximum only when a
+// row's grows by more than 2^8 (its exponentials stay far inside fp32 and
+// bf16), and the thread that holds the row does it.  While one query tile's
+// softmax runs, the other's products do (NQ = 2: the tensor cores have 2048
+// cycles of work a key tile and the exponentials half of that); with NQ = 1
+// two key tiles' S alternate.
+//
+// K and V come through a ring of 16 KB units: K 128 keys by 64 columns
+// (K-major operand), V as many keys as fill one by all columns (MN-major
+// operand: a key's values lie along N).  8-bit codes come through a ring of
+// their own and four warps make fp16 of them, exactly; scales multiply the
+// columns of S, and the weights of the values (see attn_stream.cuh, whose
+// power of two a row this kernel has too).
+//
+// Warps: 4 NQ softmax, 4 that convert (8-bit), one that fetches, one that
+// issues the products.  Every wait is bounded; after one that gave up, all
+// later ones do at once, copies and products in flight are waited for, and
+// MOE_DEV_TIMEOUT is set.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include "attn_args.cuh"
+#include "delta_mma.cuh"
+#include "early.cuh"
+#include "pair.cuh"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+
+template <int D, int KV>
+struct TcShape {
+  static constexpr bool kBytes = KV != MOE_KV_BF16;
+  static constexpr int kNQ = D == 256 ? 1 : 2, kR = 128 * kNQ, kKT = 128;
+  static constexpr int kChunks = D / 64;        // 128-byte columns: units of K a tile, and of V
+  static constexpr int kVKeys = 128 / kChunks;  // keys of a unit of V
+  static constexpr int kUnit = 16384, kRaw = kUnit / 2;
+  static constexpr int kQ = kNQ * 128 * D * 2;
+  static constexpr int kScaleSlots = 4;
+  static constexpr int kScales = kBytes ? kScaleSlots * 256 * 4 : 0;
+  static constexpr int kFixed = kQ + kScales + 2048 + kNQ * 512;  // + barriers, row factors
+  static constexpr int kRoom = 232448 - kFixed;
+  static constexpr int kUnits = kBytes ? kRoom / (kUnit + kRaw) : kRoom / kUnit;
+  static constexpr int kRaws = kBytes ? (kRoom - kUnits * kUnit) / kRaw : 0;
+  static constexpr int kSmem = kFixed + kUnits * kUnit + kRaws * kRaw;
+  static constexpr int kSoftWarps = 4 * kNQ;
+  static constexpr int kFetchWarp = kSoftWarps + (kBytes ? 4 : 0), kMmaWarp = kFetchWarp + 1;
+  static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  static constexpr uint32_t kS = 0, kO = 256;  // columns of tensor memory
+  // a key tile's K and the V before it are there together (NQ = 2)
+  static_assert(kUnits <= 12 && kRaws <= 12 && kUnits >= (kNQ == 2 ? 2 * kChunks : 5), "ring");
+};
+
+struct TcSmem {
+  uint64_t full[12], empty[12], raw_full[12], raw_empty[12];
+  uint64_t scale_full[4], scale_empty[4];
+  uint64_t q_full[2], s_full[2], p_full[2], o_done[2], done;
+  AttnShare share;
+  uint32_t tmem_holder;
+  int abort;
+};
+static_assert(sizeof(TcSmem) <= 2048, "shared memory");
+
+// V as operand B with its N along a row: rows (keys) of 64 values in the
+// 128-byte swizzle, groups of 8 keys 1024 bytes apart, the next 64 columns
+// `next` bytes on.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t next) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(next >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+constexpr uint32_t kIdescTransB = 1u << 16;
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// The key tiles of a segment that query tile i of its tile has to do with.
+struct TcSpan {
+  int k0, k1;
+  __device__ __forceinline__ bool has(int kt) const { return kt >= k0 && kt < k1; }
+};
+template <class Walk>
+__device__ __forceinline__ TcSpan tc_span(const Walk &w, const AttnBatch &a, int R, int i) {
+  const int64_t first = static_cast<int64_t>(w.cur) * R + 128 * i;
+  int64_t last = first + 127;
+  if (last >= w.t.rows) last = w.t.rows - 1;
+  TcSpan s;
+  if (first >= w.t.rows) {
+    s.k0 = s.k1 = 0;
+    return s;
+  }
+  const int p0 = w.t.ctx + static_cast<int>(first / a.group);
+  const int p1 = w.t.ctx + static_cast<int>(last / a.group);
+  const int lo = a.window && p0 >= a.window ? (p0 - a.window + 1) / 128 : 0;
+  s.k0 = max(w.k0, lo);
+  s.k1 = min(w.k1, p1 / 128 + 1);
+  return s;
+}
+
+template <int D, int KV>
+__global__ void __launch_bounds__((TcShape<D, KV>::kThreads), 1)
+attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+               const AttnBatch a, const AttnRange range, const AttnArgs p) {
+  using S = TcShape<D, KV>;
+  constexpr bool kBytes = S::kBytes;
+  constexpr int NQ = S::kNQ, R = S::kR, kChunks = S::kChunks, kUnits = S::kUnits;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *q_area = smem;
+  uint8_t *ring = q_area + S::kQ;
+  uint8_t *raw = ring + kUnits * S::kUnit;
+  float *scales = reinterpret_cast<float *>(raw + S::kRaws * S::kRaw);
+  float *q_factor = scales + S::kScales / 4;
+  TcSmem *sh = reinterpret_cast<TcSmem *>(q_factor + NQ * 128);
+  volatile int *abort = &sh->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 12; ++i) {
+      ptx::mbar_init(&sh->full[i], kBytes ? 4 : 1);
+      ptx::mbar_init(&sh->empty[i], 1);
+      ptx::mbar_init(&sh->raw_full[i], 1);
+      ptx::mbar_init(&sh->raw_empty[i], 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      ptx::mbar_init(&sh->scale_full[i], 1);
+      ptx::mbar_init(&sh->scale_empty[i], S::kSoftWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sh->q_full[i], 4);
+      ptx::mbar_init(&sh->s_full[i], 1);
+      ptx::mbar_init(&sh->p_full[i], 4);
+      ptx::mbar_init(&sh->o_done[i], 1);
+    }
+    ptx::mbar_init(&sh->done, 1);
+    sh->abort = 0;
+    ptx::fence_mbar_init();
+    ptx::tma_prefetch_desc(&tm_k);
+    ptx::tma_prefetch_desc(&tm_v);
+  }
+  early_begin();
+  if (threadIdx.x == 0) p.parts.open[blockIdx.x].last = -1;
+  attn_share<R, 128>(a, range, p.least_share, &sh->share);
+  if (sh->share.seq < 0) return;
+  if (warp == S::kMmaWarp) {
+    ptx::tmem_alloc(&sh->tmem_holder, 512);
+    ptx::tmem_relinquish();
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sh->tmem_holder;
+  AttnWalk<R, 128> w;
+  w.init(a, sh->share);
+  const int page = 1 << a.page_shift;
+  const int k_box = page < 128 ? page : 128, v_box = page < S::kVKeys ? page : S::kVKeys;
+
+  if (warp == S::kFetchWarp) {  // ------------------------------------ fetch
+    const uint64_t pol = ptx::policy_evict_last();
+    uint32_t n = 0, tiles = 0;
+    constexpr int kSlots = kBytes ? S::kRaws : kUnits;
+    constexpr int kSlotBytes = kBytes ? S::kRaw : S::kUnit;
+    uint8_t *slots = kBytes ? raw : ring;
+    uint64_t *full = kBytes ? sh->raw_full : sh->full, *empty = kBytes ? sh->raw_empty : sh->empty;
+    bool ok = true;
+    while (ok && w.next(a, range)) {
+      const int32_t *table = a.table + w.b * a.table_ld;
+      const int len = w.s.len;
+      // lane i: the page of position kt * 128 + i * page
+      const auto pages_of = [&](int kt) {
+        const int64_t pos = static_cast<int64_t>(kt) * 128 + static_cast<int64_t>(lane) * page;
+        int id = 0;
+        if (kt < w.k1 && lane * k_box < 128 && pos < len) {
+          id = table[pos >> a.page_shift];
+          if (id < 0 || id >= a.pages) {
+            set_status(a.status, MOE_DEV_BAD_INDEX);
+            id = 0;
+          }
+        }
+        return id;
+      };
+      // the cache's row of a position of the tile whose pages `ids` are
+      const auto row_of = [&](int ids, int kt, int in_tile) {
+        const int id = __shfl_sync(0xFFFFFFFFu, ids, (in_tile >> a.page_shift) & 31);
+        return static_cast<int>(
+            ((static_cast<int64_t>(id) * a.kv_heads + w.head) << a.page_shift) +
+            ((kt * 128 + in_tile) & (page - 1)));
+      };
+      const auto unit = [&](const CUtensorMap *tm, int ids, int kt, int at, int keys, int box,
+                            int bytes, int col) {
+        // `keys` keys from `at` of the tile, in boxes of `box`; `bytes` each
+        const uint32_t slot = n % kSlots;
+        if (!(ok = ptx::mbar_wait(&empty[slot], ((n / kSlots) & 1) ^ 1, abort, p.budget))) return;
+        const int there = len - kt * 128 - at;
+        const int have = there <= 0 ? 0 : min(keys / box, (there + box - 1) / box);
+        if (lane == 0) ptx::mbar_expect_tx(&full[slot], have * box * bytes);
+        __syncwarp();
+        const int row = row_of(ids, kt, (at + lane * box) & 127);
+        if (lane < have)
+          ptx::tma_load_3d(slots + slot * kSlotBytes + lane * box * bytes, tm, 0, row, col,
+                           &full[slot], pol);
+        ++n;
+      };
+      const auto k_units = [&](int ids, int kt) {
+        for (int c = 0; c < kChunks && ok; ++c)
+          unit(&tm_k, ids, kt, 0, 128, k_box, kBytes ? 64 : 128, c);
+      };
+      const auto v_units = [&](int ids, int kt) {
+        for (int u = 0; u < kChunks && ok; ++u)
+          unit(&tm_v, ids, kt, u * S::kVKeys, S::kVKeys, v_box, D * (kBytes ? 1 : 2), 0);
+      };
+      int before = 0, ids = pages_of(w.k0);
+      for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
+        const int next = kt < w.k1 ? pages_of(kt + 1) : 0;
+        if (NQ == 2 && kt > w.k0) v_units(before, kt - 1);
+        if (kt < w.k1) {
+          if (kBytes && ok) {
+            const uint32_t slot = tiles % S::kScaleSlots;
+            ok = ptx::mbar_wait(&sh->scale_empty[slot], ((tiles / S::kScaleSlots) & 1) ^ 1, abort,
+                                p.budget);
+            if (!ok) break;
+            const int there = len - kt * 128;
+            const int have = min(128 / k_box, (there + k_box - 1) / k_box);
+            if (lane == 0) ptx::mbar_expect_tx(&sh->scale_full[slot], 2 * have * k_box * 4);
+            __syncwarp();
+            const int row = row_of(ids, kt, (lane * k_box) & 127);
+            if (lane < have) {
+              float *dst = scales + slot * 256 + lane * k_box;
+              bulk_load(ptx::smem_u32(dst), p.k_scale + row, k_box * 4, &sh->scale_full[slot]);
+              bulk_load(ptx::smem_u32(dst + 128), p.v_scale + row, k_box * 4, &sh->scale_full[slot]);
+            }
+            ++tiles;
+          }
+          if (ok) k_units(ids, kt);
+        }
+        if (NQ == 1 && kt > w.k0 && ok) v_units(before, kt - 1);
+        before = ids, ids = next;
+      }
+    }
+    if (*abort) {  // let the copies in flight land before exiting
+      if (lane == 0) {
+        set_status(a.status, MOE_DEV_TIMEOUT);
+        int never = 0;
+        for (uint32_t k = 0; k < kSlots && k < n; ++k) {
+          const uint32_t j = n - 1 - k;
+          ptx::mbar_wait(&full[j % kSlots], (j / kSlots) & 1, &never, ptx::kDrainBudgetNs);
+        }
+        for (uint32_t k = 0; k < S::kScaleSlots && k < tiles; ++k) {
+          const uint32_t j = tiles - 1 - k;
+          ptx::mbar_wait(&sh->scale_full[j % S::kScaleSlots], (j / S::kScaleSlots) & 1, &never,
+                         ptx::kDrainBudgetNs);
+        }
+      }
+      __syncwarp();
+    }
+  } else if (kBytes && warp >= S::kSoftWarps && warp < S::kFetchWarp) {  // -- convert
+    const int t = threadIdx.x - 32 * S::kSoftWarps;
+    constexpr uint32_t kRaws = S::kRaws > 0 ? S::kRaws : 1;
+    uint32_t n = 0;
+    bool ok = true;
+    // 128 rows of 64 codes, 16 of a row at a time, to rows of 128 bytes; rows
+    // whose key is `dead` or later become 0 (v only)
+    const auto unit = [&](bool is_v, int dead) {
+      const uint32_t rs = n % kRaws, us = n % kUnits;
+      ok = ptx::mbar_wait(&sh->raw_full[rs], (n / kRaws) & 1, abort, p.budget) &&
+           ptx::mbar_wait(&sh->empty[us], ((n / kUnits) & 1) ^ 1, abort, p.budget);
+      if (!ok) return;
+      const uint4 *src = reinterpret_cast<const uint4 *>(raw + rs * S::kRaw);
+      uint8_t *dst = ring + us * S::kUnit;
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = src[i * 128 + t];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = i * 32 + t / 4, c = 2 * (t & 3);
+        if (is_v) {
+          const int key = row / (v_box * kChunks) * v_box + row % v_box;
+          if (key >= dead) v[i] = make_uint4(0, 0, 0, 0);
+        }
+        uint32_t h[8];
+        codes_to_f16x2<KV>(v[i].x, h[0], h[1]);
+        codes_to_f16x2<KV>(v[i].y, h[2], h[3]);
+        codes_to_f16x2<KV>(v[i].z, h[4], h[5]);
+        codes_to_f16x2<KV>(v[i].w, h[6], h[7]);
+        *reinterpret_cast<uint4 *>(dst + row * 128 + ((c ^ (row & 7)) << 4)) =
+            make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) =
+            make_uint4(h[4], h[5], h[6], h[7]);
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(&sh->raw_empty[rs]);
+        ptx::mbar_arrive(&sh->full[us]);
+      }
+      ++n;
+    };
+    while (ok && w.next(a, range)) {
+      const auto v_units = [&](int kt) {
+        for (int u = 0; u < kChunks && ok; ++u) unit(true, w.s.len - kt * 128 - u * S::kVKeys);
+      };
+      for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
+        if (NQ == 2 && kt > w.k0) v_units(kt - 1);
+        if (kt < w.k1)
+          for (int c = 0; c < kChunks && ok; ++c) unit(false, 0);
+        if (NQ == 1 && kt > w.k0) v_units(kt - 1);
+      }
+    }
+  } else if (warp == S::kMmaWarp) {  // --------------------------- products
+    const uint32_t type = kBytes ? ptx::idesc_f16_f32(128, 128) : ptx::idesc_bf16_f32(128, 128);
+    const uint32_t type_v = (kBytes ? ptx::idesc_f16_f32(128, D) : ptx::idesc_bf16_f32(128, D)) |
+                            kIdescTransB;
+    const uint32_t q_at = ptx::smem_u32(q_area), ring_at = ptx::smem_u32(ring);
+    uint32_t n = 0;                 // units used
+    uint32_t segs[2] = {0, 0};      // segments of each query tile
+    uint32_t items[2] = {0, 0};     // NQ == 2: of each query tile; NQ == 1: items[0]
+    bool ok = true;
+    while (ok && w.next(a, range)) {
+      TcSpan span[2];
+      bool q_waited[2] = {false, false}, o_begun[2] = {false, false};
+      for (int i = 0; i < NQ; ++i) span[i] = tc_span(w, a, R, i);
+      const auto s_buffer = [&](int i, uint32_t item) { return NQ == 2 ? i : static_cast<int>(item & 1); };
+      const auto s_parity = [&](uint32_t item) { return NQ == 2 ? item & 1 : (item >> 1) & 1; };
+      // A unit's products by one query tile: the first to use it waits for it,
+      // the last gives it back when its products are complete.
+      const auto arrived = [&](uint32_t u) {
+        ok = ok && ptx::mbar_wait(&sh->full[u % kUnits], (u / kUnits) & 1, abort, p.budget);
+        ptx::tc_fence_after();
+        return ok;
+      };
+      const auto give_back = [&](uint32_t u) {
+        if (lane == 0) ptx::mma_commit(&sh->empty[u % kUnits]);
+      };
+      // Values behind the sequence's end: 0 (the slot holds what was there).
+      const auto clear_tail = [&](uint8_t *at, int left) {
+        for (int i = lane; i < 1024; i += 32) {  // 16 bytes each
+          const int row = i / 8, key = row / (v_box * kChunks) * v_box + row % v_box;
+          if (key >= left) reinterpret_cast<uint4 *>(at)[i] = make_uint4(0, 0, 0, 0);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+      };
+      // S of query tile i from the units n0 .. of a key tile
+      const auto qk = [&](int i, uint32_t n0, bool first, bool last) {
+        if (!q_waited[i]) {
+          q_waited[i] = true;
+          ok = ptx::mbar_wait(&sh->q_full[i], segs[i]++ & 1, abort, p.budget);
+          if (!ok) return;
+        }
+        const int sb = s_buffer(i, items[i]);
+        for (int c = 0; c < kChunks; ++c) {
+          if (first && !arrived(n0 + c)) return;
+          ptx::tc_fence_after();
+          if (lane == 0) {
+            const uint32_t k_at = ring_at + (n0 + c) % kUnits * S::kUnit;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              ptx::mma_bf16(tmem + S::kS + sb * 128,
+                            ptx::sw128_desc(q_at + (i * kChunks + c) * 16384 + kk * 32),
+                            ptx::sw128_desc(k_at + kk * 32), type, c > 0 || kk > 0);
+          }
+          if (last) give_back(n0 + c);
+        }
+        if (lane == 0) ptx::mma_commit(&sh->s_full[sb]);
+        __syncwarp();
+        ++items[i];
+      };
+      // O of query tile i += p v, p of its item before the newest `ahead`;
+      // `left` keys of the tile are the sequence's
+      const auto pv = [&](int i, uint32_t n0, int ahead, int left, bool first, bool last) {
+        const uint32_t item = items[i] - 1 - ahead;
+        const int sb = s_buffer(i, item);
+        ok = ptx::mbar_wait(&sh->p_full[sb], s_parity(item), abort, p.budget);
+        if (!ok) return;
+        for (int u = 0; u < kChunks; ++u) {
+          if (first && !arrived(n0 + u)) return;
+          const uint32_t slot = (n0 + u) % kUnits;
+          if (!kBytes && first && left < (u + 1) * S::kVKeys)
+            clear_tail(ring + slot * S::kUnit, left - u * S::kVKeys);
+          ptx::tc_fence_after();
+          if (lane == 0) {
+            const uint32_t v_at = ring_at + slot * S::kUnit;
+#pragma unroll
+            for (int k = 0; k < S::kVKeys / 16; ++k) {
+              const int key = k * 16;
+              const uint32_t at = v_at + key / v_box * (v_box * D * 2) + key % v_box * 128;
+              ptx::mma_tmem_a(tmem + S::kO + i * D,
+                              tmem + S::kS + sb * 128 + (u * S::kVKeys + key) / 2,
+                              sw128_mn_desc(at, v_box * 128), type_v, o_begun[i] || u > 0 || k > 0);
+            }
+          }
+          if (last) give_back(n0 + u);
+        }
+        if (lane == 0) ptx::mma_commit(&sh->o_done[i]);
+        __syncwarp();
+        o_begun[i] = true;
+      };
+      for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
+        const bool has_k = kt < w.k1, has_v = kt > w.k0;
+        const int left = w.s.len - (kt - 1) * 128;
+        if (NQ == 1) {
+          if (has_k) qk(0, n, true, true), n += kChunks;
+          if (has_v && ok) pv(0, n, has_k ? 1 : 0, left, true, true), n += kChunks;
+          continue;
+        }
+        uint32_t nv = 0, nk = 0;
+        if (has_v) nv = n, n += kChunks;
+        if (has_k) nk = n, n += kChunks;
+        const bool v0 = has_v && span[0].has(kt - 1), v1 = has_v && span[1].has(kt - 1);
+        const bool k0 = has_k && span[0].has(kt), k1 = has_k && span[1].has(kt);
+        if (v0) pv(0, nv, 0, left, true, !v1);
+        if (k0 && ok) qk(0, nk, true, !k1);
+        if (v1 && ok) pv(1, nv, 0, left, !v0, true);
+        if (k1 && ok) qk(1, nk, !k0, true);
+        for (int u = 0; u < kChunks; ++u) {  // (a tile that neither needs)
+          if (has_v && !v0 && !v1 && arrived(nv + u)) give_back(nv + u);
+          if (has_k && !k0 && !k1 && arrived(nk + u)) give_back(nk + u);
+        }
+      }
+    }
+    // all products are complete before tensor memory is given back
+    if (lane == 0) {
+      int never = 0;
+      ptx::mma_commit(&sh->done);
+      ptx::mbar_wait(&sh->done, 0, &never, ptx::kDrainBudgetNs);
+      if (*abort) set_status(a.status, MOE_DEV_TIMEOUT);
+    }
+    __syncwarp();
+  } else {  // ------------------------------------------------------ softmax
+    const int qi = warp / 4, wq = warp % 4;
+    const uint32_t lanes = static_cast<uint32_t>(wq) << 21;  // TMEM lane 32 wq
+    const uint32_t o_at = tmem + lanes + S::kO + qi * D;
+    const float sign = p.scale_log2 < 0.0f ? -1.0f : 1.0f;
+    const float c_all = fabsf(p.scale_log2);
+    uint32_t items = 0, tiles = 0;
+    bool ok = true;
+    while (w.next(a, range)) {
+      if (!ok) break;
+      const int64_t row0 = static_cast<int64_t>(w.cur) * R;
+      const int rows = static_cast<int>(w.t.rows - row0 < R ? w.t.rows - row0 : R);
+      const TcSpan span = tc_span(w, a, R, qi);
+      const int r = qi * 128 + wq * 32 + lane;  // this thread's row of the tile
+      const bool live = r < rows;
+      const int64_t my_row = row0 + (live ? r : rows - 1);
+      const int token = static_cast<int>(my_row / a.group);
+      const int pos = w.t.ctx + token;
+      const int64_t q_off = (w.s.start + token) * p.q_ld +
+                            (w.head * a.group + static_cast<int>(my_row % a.group)) * D;
+      float factor = c_all;
+      if (span.k0 < span.k1) {  // ---- this warp's 32 rows of q
+        constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 8;
+        const int l16 = lane % kLanes;
+        uint8_t *q_dst = q_area + qi * kChunks * 16384 + (l16 >> 3) * 16384;
+#pragma unroll 1
+        for (int b0 = 0; b0 < 32; b0 += kBatch * kRows) {
+          uint4 x[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int rr = b0 + i * kRows + lane / kLanes;
+            const int64_t off = __shfl_sync(0xFFFFFFFFu, q_off, rr);
+            const bool has = qi * 128 + wq * 32 + rr < rows;
+            x[i] = has ? ld_nc(p.q + off + l16 * 8) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int rr = b0 + i * kRows + lane / kLanes;
+            uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            if (c_all == 0.0f) v[0] = v[1] = v[2] = v[3] = 0u;  // all scores are 0
+            if (kBytes) {
+              float top = 0.0f;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) top = max3_abs(top, bf16_lo(v[j]), bf16_hi(v[j]));
+#pragma unroll
+              for (int o = kLanes / 2; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+              float mult, inv;
+              pow2_scale(top, mult, inv);
+              if (l16 == 0) q_factor[qi * 128 + wq * 32 + rr] = inv;
+              mult *= sign;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                v[j] = h2_bits(__floats2half2_rn(bf16_lo(v[j]) * mult, bf16_hi(v[j]) * mult));
+            } else if (sign < 0.0f) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[j] ^= 0x80008000u;
+            }
+            const int row = wq * 32 + rr;
+            *reinterpret_cast<uint4 *>(q_dst + row * 128 + (((l16 & 7) ^ (row & 7)) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh->q_full[qi]);
+        if (kBytes) factor *= q_factor[qi * 128 + wq * 32 + lane];
+      }
+      if (c_all == 0.0f) factor = 1.0f;
+      float m = -INFINITY, l = 0.0f;
+      float ref = 0x1p-110f;  // (8-bit) O's sums times ref / 2^13
+      bool begun = false, several = false;
+      for (int kt = w.k0; kt < w.k1 && ok; ++kt) {
+        const uint32_t slot = tiles % S::kScaleSlots;
+        if (kBytes) {
+          ok = ptx::mbar_wait(&sh->scale_full[slot], (tiles / S::kScaleSlots) & 1, abort, p.budget);
+          if (!ok) break;
+          ++tiles;
+        }
+        if (span.has(kt)) {
+          const int sb = NQ == 2 ? qi : static_cast<int>(items & 1);
+          const uint32_t s_at = tmem + lanes + S::kS + sb * 128;
+          ok = ptx::mbar_wait(&sh->s_full[sb], NQ == 2 ? items & 1 : (items >> 1) & 1, abort,
+                              p.budget);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          float s[128];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            ptx::tmem_ld32(s_at + 32 * i, *reinterpret_cast<float(*)[32]>(s + 32 * i));
+          ptx::tmem_wait_ld();
+          const float *sc = scales + slot * 256;
+          if (kBytes) {
+#pragma unroll
+            for (int i = 0; i < 128; i += 4) {
+              const float4 f = *reinterpret_cast<const float4 *>(sc + i);
+              s[i] *= f.x, s[i + 1] *= f.y, s[i + 2] *= f.z, s[i + 3] *= f.w;
+            }
+          }
+          const int key0 = kt * 128;
+          // some row of the warp does not see all of the tile
+          const int hi = pos - key0, lo = a.window ? pos - a.window - key0 : -1;
+          if (__any_sync(0xFFFFFFFFu, hi < 127 || lo >= 0)) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i > hi || i <= lo) s[i] = -INFINITY;
+          }
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 128; i += 8)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top[j] = max3(top[j], s[i + 2 * j], s[i + 2 * j + 1]);
+          const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
+          // The first maximum; later ones that are more than 2^8 above it,
+          // by a whole power of two (so that O's factor is exact).
+          float alpha = 1.0f;
+          if (!begun) {
+            m = mt;
+          } else if (mt > m + 8.0f) {
+            const float up = m == -INFINITY ? mt : m + ceilf(mt - m);
+            alpha = attn_exp2(m - up);
+            m = up;
+          }
+          const float base = m == -INFINITY ? 0.0f : m;
+          l *= alpha;
+          float f16 = 0.0f;  // (8-bit) the factor of the weights
+          const float2 f2 = make_float2(factor, factor), b2 = make_float2(-base, -base);
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+          float most = 0.0f;
+          float o_factor = alpha;
+          const auto rescale = [&]() {
+            // O's products so far are complete
+            if (!__any_sync(0xFFFFFFFFu, o_factor != 1.0f) || !begun) return;
+            ok = ptx::mbar_wait(&sh->o_done[qi], (items - 1) & 1, abort, p.budget);
+            if (!ok) return;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < D; i += 16) {
+              float o[16];
+              uint32_t u[16];
+              ptx::tmem_ld16(o_at + i, o);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[j] * o_factor);
+              tmem_st16(o_at + i, u);
+            }
+          };
+          if (!kBytes) rescale();
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int at = h * 32 + 2 * i;
+              float2 x = fma2(make_float2(s[at], s[at + 1]), f2, b2);
+              x.x = attn_exp2(x.x), x.y = attn_exp2(x.y);
+              sum[i & 1] = fma2(x, make_float2(1.0f, 1.0f), sum[i & 1]);
+              if (kBytes) {
+                const float2 v = *reinterpret_cast<const float2 *>(sc + 128 + at);
+                // a hidden key's weight is 0 whatever its scale
+                s[at] = x.x == 0.0f ? 0.0f : x.x * v.x;
+                s[at + 1] = x.y == 0.0f ? 0.0f : x.y * v.y;
+                most = max3(most, s[at], s[at + 1]);
+              } else {
+                pk[i] = pack_bf16(x.x, x.y);
+              }
+            }
+            if (!kBytes) tmem_st16(s_at + 16 * h, pk);
+          }
+          if (kBytes) {
+            const float now = ref * alpha;  // (powers of two)
+            float up = now;
+            if (!begun || most >= 4.0f * now) up = pow2_floor(most);
+            up = fmaxf(up, 0x1p-110f);
+            const float inv = pow2_inverse(up);
+            o_factor = now * inv;
+            ref = up;
+            f16 = inv * 0x1p13f;
+            rescale();
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                pk[i] = h2_bits(__floats2half2_rn(s[h * 32 + 2 * i] * f16, s[h * 32 + 2 * i + 1] * f16));
+              tmem_st16(s_at + 16 * h, pk);
+            }
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          if (!ok) break;
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh->p_full[sb]);
+          several = begun, begun = true;
+          ++items;
+        }
+        if (kBytes) {
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh->scale_empty[slot]);
+        }
+      }
+      if (!ok) break;
+      // ----------------------------------------------- the segment's end
+      const bool whole = w.begins && w.ends;
+      const int part = 2 * blockIdx.x + (w.begins ? 1 : 0);
+      if (!whole && w.begins && threadIdx.x == 0) {
+        AttnOpen d;
+        d.last = static_cast<int>((w.tile_end - 1) / sh->share.per);
+        d.rows = rows, d.start = w.s.start, d.row0 = static_cast<int>(row0), d.head = w.head;
+        p.parts.open[blockIdx.x] = d;
+      }
+      const int64_t at = static_cast<int64_t>(part) * p.parts.rows + r;
+      if (!whole && live) p.parts.ml[at] = make_float2(m, l);
+      if (begun) {
+        // (a barrier tells its last phase only: with two key tiles in flight the
+        // products before the last ones may not be complete yet)
+        if (NQ == 1 && several)
+          ok = ptx::mbar_wait(&sh->o_done[qi], items & 1, abort, p.budget);
+        ok = ok && ptx::mbar_wait(&sh->o_done[qi], (items - 1) & 1, abort, p.budget);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        float f = whole ? 1.0f / l : 1.0f;
+        if (kBytes) f *= ref * 0x1p-13f;
+        moe_bf16 *dst = p.out + (w.s.start + token) * p.out_ld +
+                        (w.head * a.group + static_cast<int>(my_row % a.group)) * D;
+        float *sums = p.parts.sums + at * D;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          float o[32];
+          ptx::tmem_ld32(o_at + i, o);
+          ptx::tmem_wait_ld();
+          if (!live) continue;
+          if (whole) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+              *reinterpret_cast<uint4 *>(dst + i + j) =
+                  make_uint4(pack_bf16(o[j] * f, o[j + 1] * f), pack_bf16(o[j + 2] * f, o[j + 3] * f),
+                             pack_bf16(o[j + 4] * f, o[j + 5] * f),
+                             pack_bf16(o[j + 6] * f, o[j + 7] * f));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4 *>(sums + i + j) =
+                  make_float4(o[j] * f, o[j + 1] * f, o[j + 2] * f, o[j + 3] * f);
+          }
+        }
+        ptx::tc_fence_before();
+      }
+    }
+    if (!ok && lane == 0) set_status(a.status, MOE_DEV_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == S::kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace moe

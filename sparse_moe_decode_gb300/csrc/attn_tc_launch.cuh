@@ -1,0 +1,44 @@
+// attn_tc_launch.cuh -- the launch of attn_tc_kernel for one cache type.
+#pragma once
+
+#include "attn_launch.h"
+#include "attn_tc.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+template <int D, int KV>
+cudaError_t launch_tc(const AttnLaunch &x) {
+  using S = TcShape<D, KV>;
+  const auto kernel = attn_tc_kernel<D, KV>;
+  static bool attr[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr[dev] = true;
+  }
+  CUtensorMap tk, tv;
+  const int size = S::kBytes ? 1 : 2;
+  const int kb = x.page < 128 ? x.page : 128, vb = x.page < S::kVKeys ? x.page : S::kVKeys;
+  if (!attn_tc_map(&tk, x.k, D, size, x.cache_rows, kb, 1) ||
+      !attn_tc_map(&tv, x.v, D, size, x.cache_rows, vb, S::kChunks))
+    return cudaErrorInvalidValue;
+  AttnArgs p = x.args;
+  p.parts.rows = S::kR;
+  int grid = tc_sm_count();
+  if (grid > kTcMaxCtas) grid = kTcMaxCtas;
+  const cudaError_t e =
+      launch_early(kernel, dim3(grid), S::kThreads, S::kSmem, x.stream, tk, tv, x.batch, x.range, p);
+  if (e != cudaSuccess) return e;
+  return launch_attn_combine(x.batch, p, D, grid, x.stream);
+}
+
+template <int KV>
+cudaError_t launch_tc_kv(const AttnLaunch &x, int d) {
+  return d == 64 ? launch_tc<64, KV>(x) : d == 128 ? launch_tc<128, KV>(x) : launch_tc<256, KV>(x);
+}
+
+}  // namespace moe
