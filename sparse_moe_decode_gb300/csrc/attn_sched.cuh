@@ -40,19 +40,32 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnBatch &a, int b, bool repo
   return s;
 }
 
-// sum over i < n of floor((a i + b) / m), all >= 0, m > 0 (Euclid's steps).
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  int64_t sum = 0;
-  while (n > 0) {
-    sum += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
-    a %= m, b %= m;
-    const int64_t top = a * n + b;
-    if (top < m) break;
-    n = top / m, b = top % m;
-    const int64_t t = a;
-    a = m, m = t;
+// x / m and x % m; divisions of 64 bits take several times as long.
+__device__ __forceinline__ uint64_t div_mod(uint64_t x, uint32_t m, uint32_t &rest) {
+  if ((x >> 32) == 0) {
+    const uint32_t d = static_cast<uint32_t>(x) / m;
+    rest = static_cast<uint32_t>(x) - d * m;
+    return d;
   }
-  return sum;
+  const uint64_t d = x / m;
+  rest = static_cast<uint32_t>(x - d * m);
+  return d;
+}
+
+// sum over i < n of floor((a i + b) / m), m > 0 (Euclid's steps).
+__device__ __forceinline__ int64_t floor_sum(uint64_t n, uint32_t m, uint64_t a, uint64_t b) {
+  uint64_t sum = 0;
+  while (n > 0) {
+    uint32_t ra, rb;
+    const uint64_t da = div_mod(a, m, ra), db = div_mod(b, m, rb);
+    sum += da * (n * (n - 1) / 2) + db * n;
+    const uint64_t top = ra * n + rb;
+    if (top < m) break;
+    n = div_mod(top, m, rb);
+    b = rb;
+    a = m, m = ra;
+  }
+  return static_cast<int64_t>(sum);
 }
 
 // The tiles of one sequence and head.  A tile's keys end behind its last
@@ -71,19 +84,21 @@ struct AttnTiles {
   // (ctx + row / group) / KT = (ctx * group + row) / (KT * group), both floors
   __device__ __forceinline__ int hi(int t) const {
     if (t + 1 >= count) return (len - 1) / KT + 1;
-    return static_cast<int>((static_cast<int64_t>(ctx) * group + (t + 1LL) * R - 1) /
-                            (static_cast<int64_t>(KT) * group)) + 1;
+    uint32_t rest;
+    return static_cast<int>(div_mod(static_cast<int64_t>(ctx) * group + (t + 1LL) * R - 1,
+                                    KT * group, rest)) + 1;
   }
   __device__ __forceinline__ int lo(int t) const {
     if (!window) return 0;
     const int64_t x = (static_cast<int64_t>(ctx) - window + 1) * group + static_cast<int64_t>(t) * R;
-    return x <= 0 ? 0 : static_cast<int>(x / (static_cast<int64_t>(KT) * group));
+    uint32_t rest;
+    return x <= 0 ? 0 : static_cast<int>(div_mod(x, KT * group, rest));
   }
   // key tiles of the tiles before t
   __device__ __forceinline__ int64_t before(int t) const {
     if (t == 0) return 0;
     if (count == 1) return hi(0) - lo(0);
-    const int64_t m = static_cast<int64_t>(KT) * group;
+    const uint32_t m = KT * group;
     const int n = t < count ? t : count - 1;
     int64_t sum = floor_sum(n, m, R, static_cast<int64_t>(ctx) * group + R - 1) + n;
     if (t == count) sum += hi(count - 1);
@@ -205,13 +220,20 @@ struct AttnWalk {
     t = AttnTiles<R, KT>(s, a.group, a.window);
     int64_t rem = sh.offset;
     const int64_t each = t.before(t.count);
-    head = static_cast<int>(rem / each);
+    if ((each | rem) >> 32) {
+      head = static_cast<int>(rem / each);
+    } else {
+      head = static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(each));
+    }
     rem -= each * head;
-    int low = 0, high = t.count;  // before(low) <= rem < before(high)
+    // before(low) <= rem < before(high): the lanes try 32 places at a time
+    int low = 0, high = t.count;
+    const int lane = threadIdx.x & 31;
     while (high - low > 1) {
-      const int mid = (low + high) / 2;
-      if (t.before(mid) <= rem) low = mid;
-      else high = mid;
+      const int step = (high - low + 31) / 32, mid = low + step * lane;
+      const unsigned fits = __ballot_sync(0xFFFFFFFFu, mid < high && t.before(mid) <= rem);
+      low += step * (31 - __clz(fits));  // (lane 0's does)
+      high = min(high, low + step);
     }
     tile = low;
     at = static_cast<int>(rem - t.before(low));

@@ -56,8 +56,16 @@ struct TcShape {
   static constexpr int kRaws = kBytes ? (kRoom - kUnits * kUnit) / kRaw : 0;
   static constexpr int kSmem = kFixed + kUnits * kUnit + kRaws * kRaw;
   static constexpr int kSoftWarps = 4 * kNQ;
+  // (whole groups of four warps)
   static constexpr int kFetchWarp = kSoftWarps + (kBytes ? 4 : 0), kMmaWarp = kFetchWarp + 1;
-  static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  static constexpr int kThreads = 32 * (kFetchWarp + 4);
+  // Registers a thread at launch, and what the softmax's warps and the rest
+  // have of them (0: no more than a thread can have anyway).
+  static constexpr int kRegs = kThreads == 512 ? 128 : 168;
+  static constexpr int kSoftRegs = kThreads == 256 ? 0 : kNQ == 1 ? 232 : kBytes ? 192 : 216;
+  static constexpr int kRestRegs = kNQ == 1 ? 136 : kBytes ? 64 : 72;
+  static_assert(kSoftRegs * kSoftWarps + kRestRegs * (kThreads / 32 - kSoftWarps) <=
+                    kRegs * (kThreads / 32) || kSoftRegs == 0, "registers");
   static constexpr uint32_t kS = 0, kO = 256;  // columns of tensor memory
   // a key tile's K and the V before it are there together (NQ = 2)
   static_assert(kUnits <= 12 && kRaws <= 12 && kUnits >= (kNQ == 2 ? 2 * kChunks : 5), "ring");
@@ -66,25 +74,76 @@ struct TcShape {
 struct TcSmem {
   uint64_t full[12], empty[12], raw_full[12], raw_empty[12];
   uint64_t scale_full[4], scale_empty[4];
-  uint64_t q_full[2], s_full[2], p_full[2], o_done[2], done;
+  uint64_t q_full[2], s_full[2], p_full[2], o_done[2], o_last[2], done;
   AttnShare share;
   uint32_t tmem_holder;
   int abort;
 };
 static_assert(sizeof(TcSmem) <= 2048, "shared memory");
 
-// V as operand B with its N along a row: rows (keys) of 64 values in the
-// 128-byte swizzle, groups of 8 keys 1024 bytes apart, the next 64 columns
-// `next` bytes on.
-__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t next) {
-  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(next >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
+// Operand descriptors in two words (128-byte swizzle, groups of 8 rows 1024
+// bytes apart): the upper is the same for all; the lower is the address / 16
+// and, for V, how far on its next 64 columns are.  q and k lie along K; V has
+// its N along a row (rows are keys).
+constexpr uint32_t kDescUpper = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lower(uint32_t saddr, uint32_t next) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((next >> 4) << 16);
 }
 constexpr uint32_t kIdescTransB = 1u << 16;
+
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// Four products of K = 16 after one another (one thread).  Issued one by one,
+// each with descriptors of its own, they took some 120 cycles each, twice what
+// they take to run.
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                        bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t"
+      "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\t"
+      "mov.b64 da, {x, %3};\n\tmov.b64 db, {y, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, t;\n\t"
+      "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\t"
+      "mov.b64 da, {x, %3};\n\tmov.b64 db, {y, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, t;\n\t"
+      "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\t"
+      "mov.b64 da, {x, %3};\n\tmov.b64 db, {y, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, t;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kDescUpper), "r"(idesc), "r"(accumulate ? 1 : 0)
+      : "memory");
+}
+// Two, A in tensor memory: b and b + 2048 bytes.
+__device__ __forceinline__ void mma_ts2(uint32_t d, uint32_t a, uint32_t b, uint32_t b2,
+                                        uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 db;\n\t.reg .b32 x;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "mov.b64 db, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %5, p;\n\t"
+      "add.u32 x, %1, 8;\n\tmov.b64 db, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %5, t;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(b2), "r"(kDescUpper), "r"(idesc), "r"(accumulate ? 1 : 0)
+      : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N > 0 ? N : 24));
+}
+template <int N>
+__device__ __forceinline__ void leave_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -144,7 +203,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   if (threadIdx.x == 0) {
     for (int i = 0; i < 12; ++i) {
       ptx::mbar_init(&sh->full[i], kBytes ? 4 : 1);
-      ptx::mbar_init(&sh->empty[i], 1);
+      ptx::mbar_init(&sh->empty[i], NQ);
       ptx::mbar_init(&sh->raw_full[i], 1);
       ptx::mbar_init(&sh->raw_empty[i], 4);
     }
@@ -157,8 +216,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       ptx::mbar_init(&sh->s_full[i], 1);
       ptx::mbar_init(&sh->p_full[i], 4);
       ptx::mbar_init(&sh->o_done[i], 1);
+      ptx::mbar_init(&sh->o_last[i], 1);
     }
-    ptx::mbar_init(&sh->done, 1);
+    ptx::mbar_init(&sh->done, NQ);
     sh->abort = 0;
     ptx::fence_mbar_init();
     ptx::tma_prefetch_desc(&tm_k);
@@ -181,284 +241,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   const int page = 1 << a.page_shift;
   const int k_box = page < 128 ? page : 128, v_box = page < S::kVKeys ? page : S::kVKeys;
 
-  if (warp == S::kFetchWarp) {  // ------------------------------------ fetch
-    const uint64_t pol = ptx::policy_evict_last();
-    uint32_t n = 0, tiles = 0;
-    constexpr int kSlots = kBytes ? S::kRaws : kUnits;
-    constexpr int kSlotBytes = kBytes ? S::kRaw : S::kUnit;
-    uint8_t *slots = kBytes ? raw : ring;
-    uint64_t *full = kBytes ? sh->raw_full : sh->full, *empty = kBytes ? sh->raw_empty : sh->empty;
-    bool ok = true;
-    while (ok && w.next(a, range)) {
-      const int32_t *table = a.table + w.b * a.table_ld;
-      const int len = w.s.len;
-      // lane i: the page of position kt * 128 + i * page
-      const auto pages_of = [&](int kt) {
-        const int64_t pos = static_cast<int64_t>(kt) * 128 + static_cast<int64_t>(lane) * page;
-        int id = 0;
-        if (kt < w.k1 && lane * k_box < 128 && pos < len) {
-          id = table[pos >> a.page_shift];
-          if (id < 0 || id >= a.pages) {
-            set_status(a.status, MOE_DEV_BAD_INDEX);
-            id = 0;
-          }
-        }
-        return id;
-      };
-      // the cache's row of a position of the tile whose pages `ids` are
-      const auto row_of = [&](int ids, int kt, int in_tile) {
-        const int id = __shfl_sync(0xFFFFFFFFu, ids, (in_tile >> a.page_shift) & 31);
-        return static_cast<int>(
-            ((static_cast<int64_t>(id) * a.kv_heads + w.head) << a.page_shift) +
-            ((kt * 128 + in_tile) & (page - 1)));
-      };
-      const auto unit = [&](const CUtensorMap *tm, int ids, int kt, int at, int keys, int box,
-                            int bytes, int col) {
-        // `keys` keys from `at` of the tile, in boxes of `box`; `bytes` each
-        const uint32_t slot = n % kSlots;
-        if (!(ok = ptx::mbar_wait(&empty[slot], ((n / kSlots) & 1) ^ 1, abort, p.budget))) return;
-        const int there = len - kt * 128 - at;
-        const int have = there <= 0 ? 0 : min(keys / box, (there + box - 1) / box);
-        if (lane == 0) ptx::mbar_expect_tx(&full[slot], have * box * bytes);
-        __syncwarp();
-        const int row = row_of(ids, kt, (at + lane * box) & 127);
-        if (lane < have)
-          ptx::tma_load_3d(slots + slot * kSlotBytes + lane * box * bytes, tm, 0, row, col,
-                           &full[slot], pol);
-        ++n;
-      };
-      const auto k_units = [&](int ids, int kt) {
-        for (int c = 0; c < kChunks && ok; ++c)
-          unit(&tm_k, ids, kt, 0, 128, k_box, kBytes ? 64 : 128, c);
-      };
-      const auto v_units = [&](int ids, int kt) {
-        for (int u = 0; u < kChunks && ok; ++u)
-          unit(&tm_v, ids, kt, u * S::kVKeys, S::kVKeys, v_box, D * (kBytes ? 1 : 2), 0);
-      };
-      int before = 0, ids = pages_of(w.k0);
-      for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
-        const int next = kt < w.k1 ? pages_of(kt + 1) : 0;
-        if (NQ == 2 && kt > w.k0) v_units(before, kt - 1);
-        if (kt < w.k1) {
-          if (kBytes && ok) {
-            const uint32_t slot = tiles % S::kScaleSlots;
-            ok = ptx::mbar_wait(&sh->scale_empty[slot], ((tiles / S::kScaleSlots) & 1) ^ 1, abort,
-                                p.budget);
-            if (!ok) break;
-            const int there = len - kt * 128;
-            const int have = min(128 / k_box, (there + k_box - 1) / k_box);
-            if (lane == 0) ptx::mbar_expect_tx(&sh->scale_full[slot], 2 * have * k_box * 4);
-            __syncwarp();
-            const int row = row_of(ids, kt, (lane * k_box) & 127);
-            if (lane < have) {
-              float *dst = scales + slot * 256 + lane * k_box;
-              bulk_load(ptx::smem_u32(dst), p.k_scale + row, k_box * 4, &sh->scale_full[slot]);
-              bulk_load(ptx::smem_u32(dst + 128), p.v_scale + row, k_box * 4, &sh->scale_full[slot]);
-            }
-            ++tiles;
-          }
-          if (ok) k_units(ids, kt);
-        }
-        if (NQ == 1 && kt > w.k0 && ok) v_units(before, kt - 1);
-        before = ids, ids = next;
-      }
-    }
-    if (*abort) {  // let the copies in flight land before exiting
-      if (lane == 0) {
-        set_status(a.status, MOE_DEV_TIMEOUT);
-        int never = 0;
-        for (uint32_t k = 0; k < kSlots && k < n; ++k) {
-          const uint32_t j = n - 1 - k;
-          ptx::mbar_wait(&full[j % kSlots], (j / kSlots) & 1, &never, ptx::kDrainBudgetNs);
-        }
-        for (uint32_t k = 0; k < S::kScaleSlots && k < tiles; ++k) {
-          const uint32_t j = tiles - 1 - k;
-          ptx::mbar_wait(&sh->scale_full[j % S::kScaleSlots], (j / S::kScaleSlots) & 1, &never,
-                         ptx::kDrainBudgetNs);
-        }
-      }
-      __syncwarp();
-    }
-  } else if (kBytes && warp >= S::kSoftWarps && warp < S::kFetchWarp) {  // -- convert
-    const int t = threadIdx.x - 32 * S::kSoftWarps;
-    constexpr uint32_t kRaws = S::kRaws > 0 ? S::kRaws : 1;
-    uint32_t n = 0;
-    bool ok = true;
-    // 128 rows of 64 codes, 16 of a row at a time, to rows of 128 bytes; rows
-    // whose key is `dead` or later become 0 (v only)
-    const auto unit = [&](bool is_v, int dead) {
-      const uint32_t rs = n % kRaws, us = n % kUnits;
-      ok = ptx::mbar_wait(&sh->raw_full[rs], (n / kRaws) & 1, abort, p.budget) &&
-           ptx::mbar_wait(&sh->empty[us], ((n / kUnits) & 1) ^ 1, abort, p.budget);
-      if (!ok) return;
-      const uint4 *src = reinterpret_cast<const uint4 *>(raw + rs * S::kRaw);
-      uint8_t *dst = ring + us * S::kUnit;
-      uint4 v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = src[i * 128 + t];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = i * 32 + t / 4, c = 2 * (t & 3);
-        if (is_v) {
-          const int key = row / (v_box * kChunks) * v_box + row % v_box;
-          if (key >= dead) v[i] = make_uint4(0, 0, 0, 0);
-        }
-        uint32_t h[8];
-        codes_to_f16x2<KV>(v[i].x, h[0], h[1]);
-        codes_to_f16x2<KV>(v[i].y, h[2], h[3]);
-        codes_to_f16x2<KV>(v[i].z, h[4], h[5]);
-        codes_to_f16x2<KV>(v[i].w, h[6], h[7]);
-        *reinterpret_cast<uint4 *>(dst + row * 128 + ((c ^ (row & 7)) << 4)) =
-            make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4 *>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) =
-            make_uint4(h[4], h[5], h[6], h[7]);
-      }
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        ptx::mbar_arrive(&sh->raw_empty[rs]);
-        ptx::mbar_arrive(&sh->full[us]);
-      }
-      ++n;
-    };
-    while (ok && w.next(a, range)) {
-      const auto v_units = [&](int kt) {
-        for (int u = 0; u < kChunks && ok; ++u) unit(true, w.s.len - kt * 128 - u * S::kVKeys);
-      };
-      for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
-        if (NQ == 2 && kt > w.k0) v_units(kt - 1);
-        if (kt < w.k1)
-          for (int c = 0; c < kChunks && ok; ++c) unit(false, 0);
-        if (NQ == 1 && kt > w.k0) v_units(kt - 1);
-      }
-    }
-  } else if (warp == S::kMmaWarp) {  // --------------------------- products
-    const uint32_t type = kBytes ? ptx::idesc_f16_f32(128, 128) : ptx::idesc_bf16_f32(128, 128);
-    const uint32_t type_v = (kBytes ? ptx::idesc_f16_f32(128, D) : ptx::idesc_bf16_f32(128, D)) |
-                            kIdescTransB;
-    const uint32_t q_at = ptx::smem_u32(q_area), ring_at = ptx::smem_u32(ring);
-    uint32_t n = 0;                 // units used
-    uint32_t segs[2] = {0, 0};      // segments of each query tile
-    uint32_t items[2] = {0, 0};     // NQ == 2: of each query tile; NQ == 1: items[0]
-    bool ok = true;
-    while (ok && w.next(a, range)) {
-      TcSpan span[2];
-      bool q_waited[2] = {false, false}, o_begun[2] = {false, false};
-      for (int i = 0; i < NQ; ++i) span[i] = tc_span(w, a, R, i);
-      const auto s_buffer = [&](int i, uint32_t item) { return NQ == 2 ? i : static_cast<int>(item & 1); };
-      const auto s_parity = [&](uint32_t item) { return NQ == 2 ? item & 1 : (item >> 1) & 1; };
-      // A unit's products by one query tile: the first to use it waits for it,
-      // the last gives it back when its products are complete.
-      const auto arrived = [&](uint32_t u) {
-        ok = ok && ptx::mbar_wait(&sh->full[u % kUnits], (u / kUnits) & 1, abort, p.budget);
-        ptx::tc_fence_after();
-        return ok;
-      };
-      const auto give_back = [&](uint32_t u) {
-        if (lane == 0) ptx::mma_commit(&sh->empty[u % kUnits]);
-      };
-      // Values behind the sequence's end: 0 (the slot holds what was there).
-      const auto clear_tail = [&](uint8_t *at, int left) {
-        for (int i = lane; i < 1024; i += 32) {  // 16 bytes each
-          const int row = i / 8, key = row / (v_box * kChunks) * v_box + row % v_box;
-          if (key >= left) reinterpret_cast<uint4 *>(at)[i] = make_uint4(0, 0, 0, 0);
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-      };
-      // S of query tile i from the units n0 .. of a key tile
-      const auto qk = [&](int i, uint32_t n0, bool first, bool last) {
-        if (!q_waited[i]) {
-          q_waited[i] = true;
-          ok = ptx::mbar_wait(&sh->q_full[i], segs[i]++ & 1, abort, p.budget);
-          if (!ok) return;
-        }
-        const int sb = s_buffer(i, items[i]);
-        for (int c = 0; c < kChunks; ++c) {
-          if (first && !arrived(n0 + c)) return;
-          ptx::tc_fence_after();
-          if (lane == 0) {
-            const uint32_t k_at = ring_at + (n0 + c) % kUnits * S::kUnit;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              ptx::mma_bf16(tmem + S::kS + sb * 128,
-                            ptx::sw128_desc(q_at + (i * kChunks + c) * 16384 + kk * 32),
-                            ptx::sw128_desc(k_at + kk * 32), type, c > 0 || kk > 0);
-          }
-          if (last) give_back(n0 + c);
-        }
-        if (lane == 0) ptx::mma_commit(&sh->s_full[sb]);
-        __syncwarp();
-        ++items[i];
-      };
-      // O of query tile i += p v, p of its item before the newest `ahead`;
-      // `left` keys of the tile are the sequence's
-      const auto pv = [&](int i, uint32_t n0, int ahead, int left, bool first, bool last) {
-        const uint32_t item = items[i] - 1 - ahead;
-        const int sb = s_buffer(i, item);
-        ok = ptx::mbar_wait(&sh->p_full[sb], s_parity(item), abort, p.budget);
-        if (!ok) return;
-        for (int u = 0; u < kChunks; ++u) {
-          if (first && !arrived(n0 + u)) return;
-          const uint32_t slot = (n0 + u) % kUnits;
-          if (!kBytes && first && left < (u + 1) * S::kVKeys)
-            clear_tail(ring + slot * S::kUnit, left - u * S::kVKeys);
-          ptx::tc_fence_after();
-          if (lane == 0) {
-            const uint32_t v_at = ring_at + slot * S::kUnit;
-#pragma unroll
-            for (int k = 0; k < S::kVKeys / 16; ++k) {
-              const int key = k * 16;
-              const uint32_t at = v_at + key / v_box * (v_box * D * 2) + key % v_box * 128;
-              ptx::mma_tmem_a(tmem + S::kO + i * D,
-                              tmem + S::kS + sb * 128 + (u * S::kVKeys + key) / 2,
-                              sw128_mn_desc(at, v_box * 128), type_v, o_begun[i] || u > 0 || k > 0);
-            }
-          }
-          if (last) give_back(n0 + u);
-        }
-        if (lane == 0) ptx::mma_commit(&sh->o_done[i]);
-        __syncwarp();
-        o_begun[i] = true;
-      };
-      for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
-        const bool has_k = kt < w.k1, has_v = kt > w.k0;
-        const int left = w.s.len - (kt - 1) * 128;
-        if (NQ == 1) {
-          if (has_k) qk(0, n, true, true), n += kChunks;
-          if (has_v && ok) pv(0, n, has_k ? 1 : 0, left, true, true), n += kChunks;
-          continue;
-        }
-        uint32_t nv = 0, nk = 0;
-        if (has_v) nv = n, n += kChunks;
-        if (has_k) nk = n, n += kChunks;
-        const bool v0 = has_v && span[0].has(kt - 1), v1 = has_v && span[1].has(kt - 1);
-        const bool k0 = has_k && span[0].has(kt), k1 = has_k && span[1].has(kt);
-        if (v0) pv(0, nv, 0, left, true, !v1);
-        if (k0 && ok) qk(0, nk, true, !k1);
-        if (v1 && ok) pv(1, nv, 0, left, !v0, true);
-        if (k1 && ok) qk(1, nk, !k0, true);
-        for (int u = 0; u < kChunks; ++u) {  // (a tile that neither needs)
-          if (has_v && !v0 && !v1 && arrived(nv + u)) give_back(nv + u);
-          if (has_k && !k0 && !k1 && arrived(nk + u)) give_back(nk + u);
-        }
-      }
-    }
-    // all products are complete before tensor memory is given back
-    if (lane == 0) {
-      int never = 0;
-      ptx::mma_commit(&sh->done);
-      ptx::mbar_wait(&sh->done, 0, &never, ptx::kDrainBudgetNs);
-      if (*abort) set_status(a.status, MOE_DEV_TIMEOUT);
-    }
-    __syncwarp();
-  } else {  // ------------------------------------------------------ softmax
+  if (warp < S::kSoftWarps) {  // ------------------------------------ softmax
+    if (S::kSoftRegs) take_registers<S::kSoftRegs>();
     const int qi = warp / 4, wq = warp % 4;
     const uint32_t lanes = static_cast<uint32_t>(wq) << 21;  // TMEM lane 32 wq
     const uint32_t o_at = tmem + lanes + S::kO + qi * D;
     const float sign = p.scale_log2 < 0.0f ? -1.0f : 1.0f;
     const float c_all = fabsf(p.scale_log2);
-    uint32_t items = 0, tiles = 0;
+    uint32_t items = 0, tiles = 0, segs = 0;
     bool ok = true;
     while (w.next(a, range)) {
       if (!ok) break;
@@ -474,7 +264,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                             (w.head * a.group + static_cast<int>(my_row % a.group)) * D;
       float factor = c_all;
       if (span.k0 < span.k1) {  // ---- this warp's 32 rows of q
-        constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 8;
+        constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = D == 64 ? 8 : 16;
         const int l16 = lane % kLanes;
         uint8_t *q_dst = q_area + qi * kChunks * 16384 + (l16 >> 3) * 16384;
 #pragma unroll 1
@@ -523,7 +313,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       if (c_all == 0.0f) factor = 1.0f;
       float m = -INFINITY, l = 0.0f;
       float ref = 0x1p-110f;  // (8-bit) O's sums times ref / 2^13
-      bool begun = false, several = false;
+      bool begun = false;
       for (int kt = w.k0; kt < w.k1 && ok; ++kt) {
         const uint32_t slot = tiles % S::kScaleSlots;
         if (kBytes) {
@@ -559,94 +349,101 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             for (int i = 0; i < 128; ++i)
               if (i > hi || i <= lo) s[i] = -INFINITY;
           }
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 128; i += 8)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top[j] = max3(top[j], s[i + 2 * j], s[i + 2 * j + 1]);
-          const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
-          // The first maximum; later ones that are more than 2^8 above it,
-          // by a whole power of two (so that O's factor is exact).
-          float alpha = 1.0f;
-          if (!begun) {
-            m = mt;
-          } else if (mt > m + 8.0f) {
-            const float up = m == -INFINITY ? mt : m + ceilf(mt - m);
-            alpha = attn_exp2(m - up);
-            m = up;
-          }
-          const float base = m == -INFINITY ? 0.0f : m;
-          l *= alpha;
-          float f16 = 0.0f;  // (8-bit) the factor of the weights
-          const float2 f2 = make_float2(factor, factor), b2 = make_float2(-base, -base);
-          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-          float most = 0.0f;
-          float o_factor = alpha;
-          const auto rescale = [&]() {
-            // O's products so far are complete
-            if (!__any_sync(0xFFFFFFFFu, o_factor != 1.0f) || !begun) return;
-            ok = ptx::mbar_wait(&sh->o_done[qi], (items - 1) & 1, abort, p.budget);
-            if (!ok) return;
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int i = 0; i < D; i += 16) {
-              float o[16];
-              uint32_t u[16];
-              ptx::tmem_ld16(o_at + i, o);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[j] * o_factor);
-              tmem_st16(o_at + i, u);
-            }
-          };
-          if (!kBytes) rescale();
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int at = h * 32 + 2 * i;
-              float2 x = fma2(make_float2(s[at], s[at + 1]), f2, b2);
-              x.x = attn_exp2(x.x), x.y = attn_exp2(x.y);
-              sum[i & 1] = fma2(x, make_float2(1.0f, 1.0f), sum[i & 1]);
-              if (kBytes) {
-                const float2 v = *reinterpret_cast<const float2 *>(sc + 128 + at);
-                // a hidden key's weight is 0 whatever its scale
-                s[at] = x.x == 0.0f ? 0.0f : x.x * v.x;
-                s[at + 1] = x.y == 0.0f ? 0.0f : x.y * v.y;
-                most = max3(most, s[at], s[at + 1]);
-              } else {
-                pk[i] = pack_bf16(x.x, x.y);
-              }
-            }
-            if (!kBytes) tmem_st16(s_at + 16 * h, pk);
-          }
-          if (kBytes) {
-            const float now = ref * alpha;  // (powers of two)
-            float up = now;
-            if (!begun || most >= 4.0f * now) up = pow2_floor(most);
-            up = fmaxf(up, 0x1p-110f);
-            const float inv = pow2_inverse(up);
-            o_factor = now * inv;
-            ref = up;
-            f16 = inv * 0x1p13f;
-            rescale();
+          float2 sum[2];
+          float most = 0.0f, mt = 0.0f;
+          // p = 2^(s - m) (with 8-bit caches times the value's scale) into S's
+          // place; the tile's maximum on the way
+          const auto weights = [&](float base, float f16) {
+            const float2 f2 = make_float2(factor, factor), b2 = make_float2(-base, -base);
+            sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+            most = 0.0f;
+            float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               uint32_t pk[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                pk[i] = h2_bits(__floats2half2_rn(s[h * 32 + 2 * i] * f16, s[h * 32 + 2 * i + 1] * f16));
+              for (int i = 0; i < 16; ++i) {
+                const int at = h * 32 + 2 * i;
+                float2 x = fma2(make_float2(s[at], s[at + 1]), f2, b2);
+                x.x = attn_exp2(x.x), x.y = attn_exp2(x.y);
+                sum[i & 1] = add2(x, sum[i & 1]);
+                top[i & 1] = max3(top[i & 1], s[at], s[at + 1]);
+                if (kBytes) {
+                  const float2 v = *reinterpret_cast<const float2 *>(sc + 128 + at);
+                  // a hidden key's weight is 0 whatever its scale
+                  x.x = x.x == 0.0f ? 0.0f : x.x * v.x;
+                  x.y = x.y == 0.0f ? 0.0f : x.y * v.y;
+                  most = max3(most, x.x, x.y);
+                  pk[i] = h2_bits(__floats2half2_rn(x.x * f16, x.y * f16));
+                } else {
+                  pk[i] = pack_bf16(x.x, x.y);
+                }
+              }
               tmem_st16(s_at + 16 * h, pk);
+            }
+            mt = fmaxf(top[0], top[1]) * factor;
+          };
+          // The tiles before have left a maximum that nearly always does: p is
+          // formed under it at once.  Only where a score lies more than 2^8 above
+          // it (or a weight above its power of two) is the tile done again.
+          bool again = !begun;
+          if (begun) {
+            weights(m == -INFINITY ? 0.0f : m, pow2_inverse(ref) * 0x1p13f);
+            again = mt > m + 8.0f || (kBytes && most >= 4.0f * ref);
+          }
+          if (__any_sync(0xFFFFFFFFu, again)) {
+            if (!begun) {
+              float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int i = 0; i < 128; i += 8)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top[j] = max3(top[j], s[i + 2 * j], s[i + 2 * j + 1]);
+              mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
+            }
+            // by a whole power of two, so that O's factor is exact
+            float alpha = 1.0f;
+            if (!begun) {
+              m = mt;
+            } else if (mt > m + 8.0f) {
+              const float up = m == -INFINITY ? mt : m + ceilf(mt - m);
+              alpha = attn_exp2(m - up);
+              m = up;
+            }
+            l *= alpha;
+            const float base = m == -INFINITY ? 0.0f : m;
+            float o_factor = alpha;
+            if (kBytes) {
+              weights(base, 0.0f);  // the largest weight
+              const float now = ref * alpha;  // (powers of two)
+              const float up = begun && most < 4.0f * now ? now : pow2_floor(most);
+              ref = fmaxf(up, 0x1p-110f);
+              o_factor = now * pow2_inverse(ref);
+            }
+            weights(base, pow2_inverse(ref) * 0x1p13f);
+            if (begun && __any_sync(0xFFFFFFFFu, o_factor != 1.0f)) {
+              // O's products so far are complete.  (Those before the last are: the
+              // scores just read were issued after them.)
+              ok = ptx::mbar_wait(&sh->o_done[qi], (items - 1) & 1, abort, p.budget);
+              if (!ok) break;
+              ptx::tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < D; i += 16) {
+                float o[16];
+                uint32_t u[16];
+                ptx::tmem_ld16(o_at + i, o);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[j] * o_factor);
+                tmem_st16(o_at + i, u);
+              }
             }
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          if (!ok) break;
           ptx::tmem_wait_st();
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sh->p_full[sb]);
-          several = begun, begun = true;
+          begun = true;
           ++items;
         }
         if (kBytes) {
@@ -667,11 +464,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const int64_t at = static_cast<int64_t>(part) * p.parts.rows + r;
       if (!whole && live) p.parts.ml[at] = make_float2(m, l);
       if (begun) {
-        // (a barrier tells its last phase only: with two key tiles in flight the
-        // products before the last ones may not be complete yet)
-        if (NQ == 1 && several)
-          ok = ptx::mbar_wait(&sh->o_done[qi], items & 1, abort, p.budget);
-        ok = ok && ptx::mbar_wait(&sh->o_done[qi], (items - 1) & 1, abort, p.budget);
+        ok = ptx::mbar_wait(&sh->o_last[qi], segs++ & 1, abort, p.budget);
         if (!ok) break;
         ptx::tc_fence_after();
         float f = whole ? 1.0f / l : 1.0f;
@@ -703,6 +496,274 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       }
     }
     if (!ok && lane == 0) set_status(a.status, MOE_DEV_TIMEOUT);
+  } else {
+    if (S::kSoftRegs) leave_registers<S::kRestRegs>();
+    if (warp == S::kFetchWarp) {  // ------------------------------------ fetch
+      const uint64_t pol = ptx::policy_evict_last();
+      uint32_t n = 0, tiles = 0;
+      constexpr int kSlots = kBytes ? S::kRaws : kUnits;
+      constexpr int kSlotBytes = kBytes ? S::kRaw : S::kUnit;
+      uint8_t *slots = kBytes ? raw : ring;
+      uint64_t *full = kBytes ? sh->raw_full : sh->full, *empty = kBytes ? sh->raw_empty : sh->empty;
+      bool ok = true;
+      while (ok && w.next(a, range)) {
+        const int32_t *table = a.table + w.b * a.table_ld;
+        const int len = w.s.len;
+        // lane i: the page of position kt * 128 + i * page
+        const auto pages_of = [&](int kt) {
+          const int64_t pos = static_cast<int64_t>(kt) * 128 + static_cast<int64_t>(lane) * page;
+          int id = 0;
+          if (kt < w.k1 && lane * k_box < 128 && pos < len) {
+            id = table[pos >> a.page_shift];
+            if (id < 0 || id >= a.pages) {
+              set_status(a.status, MOE_DEV_BAD_INDEX);
+              id = 0;
+            }
+          }
+          return id;
+        };
+        // the cache's row of a position of the tile whose pages `ids` are
+        const auto row_of = [&](int ids, int kt, int in_tile) {
+          const int id = __shfl_sync(0xFFFFFFFFu, ids, (in_tile >> a.page_shift) & 31);
+          return static_cast<int>(
+              ((static_cast<int64_t>(id) * a.kv_heads + w.head) << a.page_shift) +
+              ((kt * 128 + in_tile) & (page - 1)));
+        };
+        const auto unit = [&](const CUtensorMap *tm, int ids, int kt, int at, int keys, int box,
+                              int bytes, int col) {
+          // `keys` keys from `at` of the tile, in boxes of `box`; `bytes` each
+          const uint32_t slot = n % kSlots;
+          if (!(ok = ptx::mbar_wait(&empty[slot], ((n / kSlots) & 1) ^ 1, abort, p.budget))) return;
+          const int there = len - kt * 128 - at;
+          const int have = there <= 0 ? 0 : min(keys / box, (there + box - 1) / box);
+          if (lane == 0) ptx::mbar_expect_tx(&full[slot], have * box * bytes);
+          __syncwarp();
+          const int row = row_of(ids, kt, (at + lane * box) & 127);
+          if (lane < have)
+            ptx::tma_load_3d(slots + slot * kSlotBytes + lane * box * bytes, tm, 0, row, col,
+                             &full[slot], pol);
+          ++n;
+        };
+        const auto k_units = [&](int ids, int kt) {
+          for (int c = 0; c < kChunks && ok; ++c)
+            unit(&tm_k, ids, kt, 0, 128, k_box, kBytes ? 64 : 128, c);
+        };
+        const auto v_units = [&](int ids, int kt) {
+          for (int u = 0; u < kChunks && ok; ++u)
+            unit(&tm_v, ids, kt, u * S::kVKeys, S::kVKeys, v_box, D * (kBytes ? 1 : 2), 0);
+        };
+        int before = 0, ids = pages_of(w.k0);
+        for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
+          const int next = kt < w.k1 ? pages_of(kt + 1) : 0;
+          if (NQ == 2 && kt > w.k0) v_units(before, kt - 1);
+          if (kt < w.k1) {
+            if (kBytes && ok) {
+              const uint32_t slot = tiles % S::kScaleSlots;
+              ok = ptx::mbar_wait(&sh->scale_empty[slot], ((tiles / S::kScaleSlots) & 1) ^ 1, abort,
+                                  p.budget);
+              if (!ok) break;
+              const int there = len - kt * 128;
+              const int have = min(128 / k_box, (there + k_box - 1) / k_box);
+              if (lane == 0) ptx::mbar_expect_tx(&sh->scale_full[slot], 2 * have * k_box * 4);
+              __syncwarp();
+              const int row = row_of(ids, kt, (lane * k_box) & 127);
+              if (lane < have) {
+                float *dst = scales + slot * 256 + lane * k_box;
+                bulk_load(ptx::smem_u32(dst), p.k_scale + row, k_box * 4, &sh->scale_full[slot]);
+                bulk_load(ptx::smem_u32(dst + 128), p.v_scale + row, k_box * 4, &sh->scale_full[slot]);
+              }
+              ++tiles;
+            }
+            if (ok) k_units(ids, kt);
+          }
+          if (NQ == 1 && kt > w.k0 && ok) v_units(before, kt - 1);
+          before = ids, ids = next;
+        }
+      }
+      if (*abort) {  // let the copies in flight land before exiting
+        if (lane == 0) {
+          set_status(a.status, MOE_DEV_TIMEOUT);
+          int never = 0;
+          for (uint32_t k = 0; k < kSlots && k < n; ++k) {
+            const uint32_t j = n - 1 - k;
+            ptx::mbar_wait(&full[j % kSlots], (j / kSlots) & 1, &never, ptx::kDrainBudgetNs);
+          }
+          for (uint32_t k = 0; k < S::kScaleSlots && k < tiles; ++k) {
+            const uint32_t j = tiles - 1 - k;
+            ptx::mbar_wait(&sh->scale_full[j % S::kScaleSlots], (j / S::kScaleSlots) & 1, &never,
+                           ptx::kDrainBudgetNs);
+          }
+        }
+        __syncwarp();
+      }
+    } else if (kBytes && warp >= S::kSoftWarps && warp < S::kFetchWarp) {  // -- convert
+      const int t = threadIdx.x - 32 * S::kSoftWarps;
+      constexpr uint32_t kRaws = S::kRaws > 0 ? S::kRaws : 1;
+      uint32_t n = 0;
+      bool ok = true;
+      // 128 rows of 64 codes, 16 of a row at a time, to rows of 128 bytes; rows
+      // whose key is `dead` or later become 0 (v only)
+      const auto unit = [&](bool is_v, int dead) {
+        const uint32_t rs = n % kRaws, us = n % kUnits;
+        ok = ptx::mbar_wait(&sh->raw_full[rs], (n / kRaws) & 1, abort, p.budget) &&
+             ptx::mbar_wait(&sh->empty[us], ((n / kUnits) & 1) ^ 1, abort, p.budget);
+        if (!ok) return;
+        const uint4 *src = reinterpret_cast<const uint4 *>(raw + rs * S::kRaw);
+        uint8_t *dst = ring + us * S::kUnit;
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = src[i * 128 + t];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = i * 32 + t / 4, c = 2 * (t & 3);
+          if (is_v) {
+            const int key = row / (v_box * kChunks) * v_box + row % v_box;
+            if (key >= dead) v[i] = make_uint4(0, 0, 0, 0);
+          }
+          uint32_t h[8];
+          codes_to_f16x2<KV>(v[i].x, h[0], h[1]);
+          codes_to_f16x2<KV>(v[i].y, h[2], h[3]);
+          codes_to_f16x2<KV>(v[i].z, h[4], h[5]);
+          codes_to_f16x2<KV>(v[i].w, h[6], h[7]);
+          *reinterpret_cast<uint4 *>(dst + row * 128 + ((c ^ (row & 7)) << 4)) =
+              make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4 *>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) =
+              make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(&sh->raw_empty[rs]);
+          ptx::mbar_arrive(&sh->full[us]);
+        }
+        ++n;
+      };
+      while (ok && w.next(a, range)) {
+        const auto v_units = [&](int kt) {
+          for (int u = 0; u < kChunks && ok; ++u) unit(true, w.s.len - kt * 128 - u * S::kVKeys);
+        };
+        for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
+          if (NQ == 2 && kt > w.k0) v_units(kt - 1);
+          if (kt < w.k1)
+            for (int c = 0; c < kChunks && ok; ++c) unit(false, 0);
+          if (NQ == 1 && kt > w.k0) v_units(kt - 1);
+        }
+      }
+    } else if (warp >= S::kMmaWarp && warp < S::kMmaWarp + NQ) {  // --- products
+      // One warp a query tile: while one waits, the other's products run.
+      const int qi = warp - S::kMmaWarp;
+      const uint32_t type = kBytes ? ptx::idesc_f16_f32(128, 128) : ptx::idesc_bf16_f32(128, 128);
+      const uint32_t type_v = (kBytes ? ptx::idesc_f16_f32(128, D) : ptx::idesc_bf16_f32(128, D)) |
+                              kIdescTransB;
+      const uint32_t q_at = ptx::smem_u32(q_area) + qi * kChunks * 16384;
+      const uint32_t ring_at = ptx::smem_u32(ring);
+      constexpr int kVSteps = S::kVKeys / 16;
+      uint32_t v_step[kVSteps];  // where 16 keys' values begin in a unit, / 16
+#pragma unroll
+      for (int k = 0; k < kVSteps; ++k)
+        v_step[k] = (16 * k / v_box * (v_box * D * 2) + 16 * k % v_box * 128) >> 4;
+      uint32_t n = 0, segs = 0, items = 0;  // units, segments and key tiles so far
+      bool ok = true;
+      while (ok && w.next(a, range)) {
+        const TcSpan span = tc_span(w, a, R, qi);
+        bool q_here = false, o_begun = false;
+        const auto buffer = [&](uint32_t item) { return NQ == 2 ? qi : static_cast<int>(item & 1); };
+        const auto parity = [&](uint32_t item) { return NQ == 2 ? item & 1 : (item >> 1) & 1; };
+        const auto arrived = [&](uint32_t u) {
+          ok = ok && ptx::mbar_wait(&sh->full[u % kUnits], (u / kUnits) & 1, abort, p.budget);
+          return ok;
+        };
+        // (free when the products that read it, and all before, are complete)
+        const auto give_back = [&](uint32_t u) {
+          if (elect_one()) ptx::mma_commit(&sh->empty[u % kUnits]);
+        };
+        // Values behind the sequence's end: 0 (the slot holds what was there; with
+        // two query tiles both warps do so).
+        const auto clear_tail = [&](uint8_t *at, int left) {
+          for (int i = lane; i < 1024; i += 32) {  // 16 bytes each
+            const int row = i / 8, key = row / (v_box * kChunks) * v_box + row % v_box;
+            if (key >= left) reinterpret_cast<uint4 *>(at)[i] = make_uint4(0, 0, 0, 0);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+        };
+        // S from the units n0 .. of a key tile
+        const auto qk = [&](uint32_t n0) {
+          if (!q_here) {
+            q_here = true;
+            ok = ptx::mbar_wait(&sh->q_full[qi], segs++ & 1, abort, p.budget);
+            if (!ok) return;
+          }
+          const uint32_t s_at = tmem + S::kS + buffer(items) * 128;
+          for (int c = 0; c < kChunks; ++c) {
+            if (!arrived(n0 + c)) return;
+            ptx::tc_fence_after();
+            if (elect_one())
+              mma_ss4(s_at, desc_lower(q_at + c * 16384, 16),
+                      desc_lower(ring_at + (n0 + c) % kUnits * S::kUnit, 16), type, c > 0);
+            give_back(n0 + c);
+          }
+          if (elect_one()) ptx::mma_commit(&sh->s_full[buffer(items)]);
+          ++items;
+        };
+        // O += p v, p of the key tile before the newest `ahead`; `left` keys of it
+        // are the sequence's.  `ends`: the segment's last (a barrier of its own:
+        // o_done's phases before may go by unseen)
+        const auto pv = [&](uint32_t n0, int ahead, int left, bool ends) {
+          const uint32_t item = items - 1 - ahead;
+          const uint32_t p_at = tmem + S::kS + buffer(item) * 128;
+          ok = ptx::mbar_wait(&sh->p_full[buffer(item)], parity(item), abort, p.budget);
+          if (!ok) return;
+          for (int u = 0; u < kChunks; ++u) {
+            if (!arrived(n0 + u)) return;
+            const uint32_t slot = (n0 + u) % kUnits;
+            if (!kBytes && left < (u + 1) * S::kVKeys)
+              clear_tail(ring + slot * S::kUnit, left - u * S::kVKeys);
+            ptx::tc_fence_after();
+            if (elect_one()) {
+              const uint32_t v_at = desc_lower(ring_at + slot * S::kUnit, v_box * 128);
+#pragma unroll
+              for (int k = 0; k < kVSteps; k += 2)
+                mma_ts2(tmem + S::kO + qi * D, p_at + u * (S::kVKeys / 2) + 8 * k,
+                        v_at + v_step[k], v_at + v_step[k + 1], type_v, o_begun || u > 0 || k > 0);
+            }
+            give_back(n0 + u);
+          }
+          if (elect_one()) {
+            ptx::mma_commit(&sh->o_done[qi]);
+            if (ends) ptx::mma_commit(&sh->o_last[qi]);
+          }
+          o_begun = true;
+        };
+        const auto pass = [&](uint32_t n0) {  // a key tile of no row of this query tile
+          for (int u = 0; u < kChunks; ++u)
+            if (arrived(n0 + u)) give_back(n0 + u);
+        };
+        for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
+          const bool has_k = kt < w.k1, has_v = kt > w.k0;
+          const int left = w.s.len - (kt - 1) * 128;
+          if (NQ == 1 && has_k) qk(n), n += kChunks;
+          if (has_v && ok) {
+            if (span.has(kt - 1)) pv(n, NQ == 1 && has_k ? 1 : 0, left, kt == span.k1);
+            else pass(n);
+            n += kChunks;
+          }
+          if (NQ == 2 && has_k && ok) {
+            if (span.has(kt)) qk(n);
+            else pass(n);
+            n += kChunks;
+          }
+        }
+      }
+      // all products are complete before tensor memory is given back
+      if (elect_one()) {
+        int never = 0;
+        ptx::mma_commit(&sh->done);
+        ptx::mbar_wait(&sh->done, 0, &never, ptx::kDrainBudgetNs);
+        if (*abort) set_status(a.status, MOE_DEV_TIMEOUT);
+      }
+      __syncwarp();
+    }
   }
   __syncthreads();
   if (warp == S::kMmaWarp) {

@@ -18,6 +18,11 @@ cudaError_t launch_tc(const AttnLaunch &x) {
     const cudaError_t e = cudaFuncSetAttribute(
         kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
+    // the registers that its warps pass to one another are there at launch
+    cudaFuncAttributes have;
+    const cudaError_t f = cudaFuncGetAttributes(&have, kernel);
+    if (f != cudaSuccess) return f;
+    if (S::kSoftRegs && have.numRegs < S::kRegs) return cudaErrorLaunchOutOfResources;
     if (dev >= 0 && dev < 64) attr[dev] = true;
   }
   CUtensorMap tk, tv;
