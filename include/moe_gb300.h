@@ -483,7 +483,7 @@ size_t moe_attn_workspace_bytes(const moe_attn_dims *dims);
  * softmax in fp32; the weights enter the second product as bf16 (as fp16 with
  * an 8-bit cache, whose codes are exact in fp16), out is rounded to bf16 once.
  * Weights below 2^-126 of a row's largest are 0; with an 8-bit cache the
- * products of a weight and its v_scale keep 11 bits, but no less than 2^-38 of
+ * products of a weight and its v_scale keep 11 bits, but no less than 2^-32 of
  * the row's largest product.
  * What lies in the cache behind a sequence's last position is not looked at.
  * A value that is not finite in k, or in an 8-bit cache's rows, reaches the

@@ -10,84 +10,115 @@ namespace {
 
 constexpr int kCombineThreads = 256, kCombineWarps = kCombineThreads / 32;
 
-// A tile's row in 128 columns (a lane has four): sum_i w_i o_i / sum_i w_i l_i
-// with w_i = 2^(m_i - max m) over the blocks that worked on it.  A warp does
-// it, or where tiles are few and blocks per tile many, the warps of a block
-// share the blocks out.
+// Up to 32 of a tile's rows in 4 Q columns for each of the rest of the lanes:
+// sum_i w_i o_i / sum_i w_i l_i with w_i = 2^(m_i - max m) over the blocks that
+// worked on it.  A warp does it (Q = 8); where tiles are few and blocks per tile
+// many, the warps of a block share the blocks out (Q = 2).
+template <int Q, bool TOGETHER>
+__device__ __forceinline__ void combine(const AttnBatch &a, const AttnArgs &p, int D, int count,
+                                        const int *list, float4 (*part)[32], float2 *part_ml) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int R = p.parts.rows, side = R < 32 ? R : 32, subs = 32 / side;
+  const int cols = 4 * Q * subs, row_tasks = R / side, tasks = row_tasks * (D / cols);
+  const int total = count * tasks;
+  for (int t = TOGETHER ? blockIdx.x : blockIdx.x + warp * gridDim.x; t < total;
+       t += TOGETHER ? gridDim.x : gridDim.x * kCombineWarps) {
+    const int b0 = list[t / tasks], in = t % tasks;
+    const AttnOpen o = p.parts.open[b0];
+    const int r = in % row_tasks * side + lane % side;
+    const int d = in / row_tasks * cols + lane / side * (4 * Q);
+    const int n = o.last - b0 + 1;
+    float m = -INFINITY, l = 0.0f;
+    float4 v[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const auto add = [&](float2 ml, const float4 (&x)[Q]) {
+      if (ml.x == -INFINITY) return;  // a part that saw no key has no sums
+      const float top = fmaxf(m, ml.x);
+      const float f = attn_exp2(m - top), g = attn_exp2(ml.x - top);
+      m = top;
+      l = l * f + ml.y * g;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        v[q].x = v[q].x * f + x[q].x * g, v[q].y = v[q].y * f + x[q].y * g;
+        v[q].z = v[q].z * f + x[q].z * g, v[q].w = v[q].w * f + x[q].w * g;
+      }
+    };
+    if (r < o.rows) {
+      constexpr int kAhead = TOGETHER ? 4 : 2;
+      for (int i0 = TOGETHER ? warp : 0; i0 < n; i0 += kAhead * (TOGETHER ? kCombineWarps : 1)) {
+        float2 ml[kAhead];
+        float4 x[kAhead][Q];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int i = i0 + k * (TOGETHER ? kCombineWarps : 1);
+          ml[k] = make_float2(-INFINITY, 0.0f);
+          if (i < n) {
+            const int64_t slot = i == 0 ? 2 * b0 + 1 : 2 * (b0 + i);
+            ml[k] = p.parts.ml[slot * R + r];
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+              x[k][q] = *reinterpret_cast<const float4 *>(p.parts.at(slot, D, d + 4 * q, r));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) add(ml[k], x[k]);
+      }
+    }
+    if (TOGETHER) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) part[warp * Q + q][lane] = v[q];
+      part_ml[warp * 32 + lane] = make_float2(m, l);
+      __syncthreads();
+      if (warp == 0)
+        for (int k = 1; k < kCombineWarps; ++k) {
+          float4 x[Q];
+#pragma unroll
+          for (int q = 0; q < Q; ++q) x[q] = part[k * Q + q][lane];
+          add(part_ml[k * 32 + lane], x);
+        }
+    }
+    if ((!TOGETHER || warp == 0) && r < o.rows) {
+      const int token = (o.row0 + r) / a.group, h = (o.row0 + r) % a.group;
+      moe_bf16 *dst = p.out + (o.start + token) * p.out_ld + (o.head * a.group + h) * D + d;
+      const float f = 1.0f / l;
+#pragma unroll
+      for (int q = 0; q < Q; q += 2)
+        *reinterpret_cast<uint4 *>(dst + 4 * q) =
+            make_uint4(bf16x2(v[q].x * f, v[q].y * f), bf16x2(v[q].z * f, v[q].w * f),
+                       bf16x2(v[q + 1].x * f, v[q + 1].y * f),
+                       bf16x2(v[q + 1].z * f, v[q + 1].w * f));
+    }
+    if (TOGETHER) __syncthreads();
+  }
+}
+
 __global__ void __launch_bounds__(kCombineThreads)
 attn_combine_kernel(const AttnBatch a, const AttnArgs p, int D, int blocks) {
   __shared__ int list[kStreamMaxCtas];
   __shared__ int count;
-  __shared__ float4 part[kCombineWarps][32];
-  __shared__ float part_l[kCombineWarps];
+  __shared__ float4 part[kCombineWarps * 2][32];
+  __shared__ float2 part_ml[kCombineWarps * 32];
   early_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
+    bool has[kStreamMaxCtas / 32];
+#pragma unroll
+    for (int i = 0; i < kStreamMaxCtas / 32; ++i)
+      has[i] = 32 * i + lane < blocks && p.parts.open[32 * i + lane].last >= 0;
     int n = 0;
-    for (int i0 = 0; i0 < blocks; i0 += 32) {
-      const bool has = i0 + lane < blocks && p.parts.open[i0 + lane].last >= 0;
-      const unsigned mask = __ballot_sync(0xFFFFFFFFu, has);
-      if (has) list[n + __popc(mask & ((1u << lane) - 1))] = i0 + lane;
+#pragma unroll
+    for (int i = 0; i < kStreamMaxCtas / 32; ++i) {
+      const unsigned mask = __ballot_sync(0xFFFFFFFFu, has[i]);
+      if (has[i]) list[n + __popc(mask & ((1u << lane) - 1))] = 32 * i + lane;
       n += __popc(mask);
     }
     if (lane == 0) count = n;
   }
   __syncthreads();
   if (count == 0) return;
-  const int R = p.parts.rows, chunks = D > 128 ? D / 128 : 1;
-  const bool together = blocks > 6 * count;
-  const int64_t tasks = static_cast<int64_t>(count) * R * chunks;
-  const int64_t step = together ? gridDim.x : static_cast<int64_t>(gridDim.x) * kCombineWarps;
-  // (neighbouring tasks in different blocks)
-  for (int64_t t = blockIdx.x + (together ? 0 : static_cast<int64_t>(warp) * gridDim.x); t < tasks;
-       t += step) {
-    const int b0 = list[t / (R * chunks)];
-    const AttnOpen o = p.parts.open[b0];
-    const int r = static_cast<int>(t % (R * chunks)) / chunks, d = static_cast<int>(t % chunks) * 128 + 4 * lane;
-    if (r >= o.rows) continue;  // (the same for all warps that share a task)
-    const int n = o.last - b0 + 1;
-    const auto slot = [&](int i) {
-      return static_cast<int64_t>(i == 0 ? 2 * b0 + 1 : 2 * (b0 + i)) * R + r;
-    };
-    float top = -INFINITY;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, p.parts.ml[slot(i)].x);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
-#pragma unroll 4
-    for (int i = together ? warp : 0; i < n; i += together ? kCombineWarps : 1) {
-      const int64_t at = slot(i);
-      const float2 ml = p.parts.ml[at];
-      const float w = ml.x == -INFINITY ? 0.0f : attn_exp2(ml.x - top);
-      l += w * ml.y;
-      if (d < D && ml.x != -INFINITY) {  // (a part that saw no key has no sums)
-        const float4 x = *reinterpret_cast<const float4 *>(p.parts.sums + at * D + d);
-        v.x += w * x.x, v.y += w * x.y, v.z += w * x.z, v.w += w * x.w;
-      }
-    }
-    if (together) {
-      part[warp][lane] = v;
-      if (lane == 0) part_l[warp] = l;
-      __syncthreads();
-      if (warp == 0) {
-        for (int k = 1; k < kCombineWarps; ++k) {
-          const float4 x = part[k][lane];
-          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-          l += part_l[k];
-        }
-      }
-    }
-    if ((!together || warp == 0) && d < D) {
-      const int64_t at = static_cast<int64_t>(o.row0) + r;
-      moe_bf16 *dst = p.out + (o.start + at / a.group) * p.out_ld +
-                      (o.head * a.group + at % a.group) * D + d;
-      const float f = 1.0f / l;
-      *reinterpret_cast<uint2 *>(dst) =
-          make_uint2(bf16x2(v.x * f, v.y * f), bf16x2(v.z * f, v.w * f));
-    }
-    if (together) __syncthreads();
-  }
+  if (blocks > 6 * count) combine<2, true>(a, p, D, count, list, part, part_ml);
+  else combine<8, false>(a, p, D, count, list, part, part_ml);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -139,7 +170,7 @@ bool attn_tc_map(CUtensorMap *m, const void *base, int d, int size, int64_t rows
 
 cudaError_t launch_attn_combine(const AttnBatch &a, const AttnArgs &p, int d, int blocks,
                                 cudaStream_t s) {
-  return launch_early(attn_combine_kernel, dim3(2 * tc_sm_count()), kCombineThreads, 0, s, a, p, d,
+  return launch_early(attn_combine_kernel, dim3(4 * tc_sm_count()), kCombineThreads, 0, s, a, p, d,
                       blocks);
 }
 

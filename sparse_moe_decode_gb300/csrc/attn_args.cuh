@@ -14,8 +14,12 @@ namespace moe {
 struct AttnParts {
   AttnOpen *open;  // [blocks]
   float2 *ml;      // [2 blocks][rows]: maximum (in powers of two) and total
-  float *sums;     // [2 blocks][rows][head_dim]
+  float *sums;     // [2 blocks][head_dim / 4][rows][4]: rows lie side by side
   int rows;        // of a tile
+  // four columns from d on of a part's row
+  __device__ __forceinline__ float *at(int64_t part, int head_dim, int d, int row) const {
+    return sums + ((part * (head_dim / 4) + d / 4) * rows + row) * 4;
+  }
 };
 
 struct AttnArgs {
@@ -26,6 +30,7 @@ struct AttnArgs {
   AttnParts parts;
   float scale_log2;  // scale * log2(e)
   int least_share;
+  int q_copy;  // q's tiles come by TMA
   unsigned long long budget;
 };
 

@@ -5,7 +5,8 @@
 // a (token, head of the group) pair; its work is the KT-wide key tiles that
 // any of its rows sees.  All tiles' key tiles, one after another (sequence,
 // head, tile, key tile), are cut into equal shares, one for each block; a
-// share's pieces are segments of one tile each.  A tile that lies in one share
+// share's pieces are segments of one tile each.  A tile counts C key tiles more
+// than it has, for what beginning and ending it costs.  A tile that lies in one share
 // is finished there; otherwise its segments leave unnormalised sums (and the
 // softmax's maximum and total) for attn_combine.cu.  Every block finds its
 // share by itself: a scan over the sequences, whose key tiles have a closed
@@ -70,16 +71,16 @@ __device__ __forceinline__ int64_t floor_sum(uint64_t n, uint32_t m, uint64_t a,
 
 // The tiles of one sequence and head.  A tile's keys end behind its last
 // row's position and begin, under a window, with its first row's first key.
-template <int R, int KT>
+template <int R, int KT, int C>
 struct AttnTiles {
   int ctx, len, group, window, count;
-  int64_t rows;
+  int rows;  // at most 2^20 tokens of 64 heads
 
   __device__ __forceinline__ AttnTiles() {}
   __device__ __forceinline__ AttnTiles(const AttnSeq &s, int group_, int window_)
       : ctx(s.len - s.n), len(s.len), group(group_), window(window_) {
-    rows = static_cast<int64_t>(s.n) * group;
-    count = static_cast<int>((rows + R - 1) / R);
+    rows = s.n * group;
+    count = (rows + R - 1) / R;
   }
   // (ctx + row / group) / KT = (ctx * group + row) / (KT * group), both floors
   __device__ __forceinline__ int hi(int t) const {
@@ -94,13 +95,14 @@ struct AttnTiles {
     uint32_t rest;
     return x <= 0 ? 0 : static_cast<int>(div_mod(x, KT * group, rest));
   }
-  // key tiles of the tiles before t
+  // units (key tiles, and C a tile) of the tiles before t
   __device__ __forceinline__ int64_t before(int t) const {
     if (t == 0) return 0;
-    if (count == 1) return hi(0) - lo(0);
+    if (count == 1) return hi(0) - lo(0) + C;
     const uint32_t m = KT * group;
     const int n = t < count ? t : count - 1;
-    int64_t sum = floor_sum(n, m, R, static_cast<int64_t>(ctx) * group + R - 1) + n;
+    int64_t sum = floor_sum(n, m, R, static_cast<int64_t>(ctx) * group + R - 1) + n +
+                  static_cast<int64_t>(C) * t;
     if (t == count) sum += hi(count - 1);
     if (window) {
       const int64_t x0 = (static_cast<int64_t>(ctx) - window + 1) * group;
@@ -121,7 +123,7 @@ struct AttnOpen {
 };
 
 struct AttnShare {  // in shared memory
-  int64_t at, per, total, offset;  // first key tile, a share's, all, within the sequence
+  int64_t at, per, total, offset;  // first unit, a share's, all, within the sequence
   int64_t scan[32];
   int32_t seq;
 };
@@ -131,26 +133,26 @@ struct AttnRange {
   int32_t least, most;
 };
 
-template <int R, int KT>
+template <int R, int KT, int C>
 __device__ __forceinline__ int64_t attn_units(const AttnBatch &a, const AttnRange &r, int b,
                                               bool report) {
   const AttnSeq s = attn_seq(a, b, report);
-  const int64_t rows = static_cast<int64_t>(s.n) * a.group;
+  const int rows = s.n * a.group;
   if (s.n == 0 || rows <= r.least || rows > r.most) return 0;
-  const AttnTiles<R, KT> t(s, a.group, a.window);
+  const AttnTiles<R, KT, C> t(s, a.group, a.window);
   return t.before(t.count) * a.kv_heads;
 }
 
 // All threads of the block (a multiple of 32, at most 1024): this block's
 // share.  seq = -1: nothing to do.
-template <int R, int KT>
+template <int R, int KT, int C>
 __device__ __forceinline__ void attn_share(const AttnBatch &a, const AttnRange &r, int least_share,
                                            AttnShare *sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
   const bool one = a.B <= nt;
   int64_t mine = 0, sum = 0;
   for (int b = tid; b < a.B; b += nt) {
-    mine = attn_units<R, KT>(a, r, b, blockIdx.x == 0);
+    mine = attn_units<R, KT, C>(a, r, b, blockIdx.x == 0);
     sum += mine;
   }
   // an inclusive scan over the threads of v; the total through sh->scan
@@ -185,7 +187,7 @@ __device__ __forceinline__ void attn_share(const AttnBatch &a, const AttnRange &
     int64_t base = 0;
     for (int b0 = 0; b0 < a.B && base <= at; b0 += nt) {
       const int b = b0 + tid;
-      const int64_t u = b < a.B ? attn_units<R, KT>(a, r, b, false) : 0;
+      const int64_t u = b < a.B ? attn_units<R, KT, C>(a, r, b, false) : 0;
       int64_t round;
       incl = base + scan(u, round);
       if (at >= incl - u && at < incl) sh->seq = b, sh->offset = at - (incl - u);
@@ -197,18 +199,18 @@ __device__ __forceinline__ void attn_share(const AttnBatch &a, const AttnRange &
 
 // A block's way through its share, segment by segment.  Every warp walks it
 // by itself and sees the same.
-template <int R, int KT>
+template <int R, int KT, int C>
 struct AttnWalk {
   int b, head, tile, at, left_in_tile;
-  int64_t left, next_unit;  // key tiles left of the share; of all, before the next segment
+  int64_t left, next_unit;  // units left of the share; of all, before the next segment
   AttnSeq s;
-  AttnTiles<R, KT> t;
+  AttnTiles<R, KT, C> t;
 
   // the current segment (of sequence b and head)
   int cur;            // its tile
   int k0, k1;         // key tiles
   bool begins, ends;  // the tile's first, last
-  int64_t tile_end;   // of all key tiles
+  int64_t tile_end;   // of all units
 
   __device__ __forceinline__ void init(const AttnBatch &a, const AttnShare &sh) {
     b = sh.seq;
@@ -217,7 +219,7 @@ struct AttnWalk {
     left = sh.total - sh.at < sh.per ? sh.total - sh.at : sh.per;
     next_unit = sh.at;
     s = attn_seq(a, b, false);
-    t = AttnTiles<R, KT>(s, a.group, a.window);
+    t = AttnTiles<R, KT, C>(s, a.group, a.window);
     int64_t rem = sh.offset;
     const int64_t each = t.before(t.count);
     if ((each | rem) >> 32) {
@@ -250,16 +252,20 @@ struct AttnWalk {
             return false;
           }
           s = attn_seq(a, b, false);
-        } while (s.n == 0 || static_cast<int64_t>(s.n) * a.group <= r.least ||
-                 static_cast<int64_t>(s.n) * a.group > r.most);
-        t = AttnTiles<R, KT>(s, a.group, a.window);
+        } while (s.n == 0 || s.n * a.group <= r.least || s.n * a.group > r.most);
+        t = AttnTiles<R, KT, C>(s, a.group, a.window);
       }
     }
-    const int lo = t.lo(tile), whole = t.hi(tile) - lo;
-    const int n = whole - at < left ? whole - at : static_cast<int>(left);
-    k0 = lo + at, k1 = k0 + n;
-    begins = at == 0, ends = at + n == whole;
-    tile_end = next_unit + whole - at;
+    if (at < C) {  // the C units come first
+      const int skip = C - at < left ? C - at : static_cast<int>(left);
+      at += skip, left -= skip, next_unit += skip;
+      if (left == 0) return false;
+    }
+    const int lo = t.lo(tile), whole = t.hi(tile) - lo, done = at - C;
+    const int n = whole - done < left ? whole - done : static_cast<int>(left);
+    k0 = lo + done, k1 = k0 + n;
+    begins = done == 0, ends = done + n == whole;
+    tile_end = next_unit + whole - done;
     cur = tile;
     left -= n, next_unit += n;
     if (ends) at = 0, ++tile;

@@ -28,6 +28,8 @@
 
 namespace moe {
 
+constexpr int kStreamTileCost = 1;  // beginning and ending a tile, in key tiles
+
 template <int D, int KV, int WR>
 struct StreamShape {
   static constexpr int kWK = 4 / WR, kR = 16 * WR, kKT = 64, kNK = kKT / kWK;
@@ -119,9 +121,9 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
   early_begin();
   if (threadIdx.x == 0) p.parts.open[blockIdx.x].last = -1;
-  attn_share<R, 64>(a, range, p.least_share, &sh->share);
+  attn_share<R, 64, kStreamTileCost>(a, range, p.least_share, &sh->share);
   if (sh->share.seq < 0) return;
-  AttnWalk<R, 64> w;
+  AttnWalk<R, 64, kStreamTileCost> w;
   w.init(a, sh->share);
   const int page = 1 << a.page_shift;
   const int box = page < 64 ? page : 64;  // positions
@@ -206,8 +208,8 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int row_v = (lane & 7) + ((lane >> 3) & 1) * 8, col_v = lane >> 4;
 
   while (w.next(a, range)) {
-    const int64_t row0 = static_cast<int64_t>(w.cur) * R;
-    const int rows = static_cast<int>(w.t.rows - row0 < R ? w.t.rows - row0 : R);
+    const int row0 = w.cur * R;
+    const int rows = min(w.t.rows - row0, R);
     const int ctx = w.t.ctx;
     // this thread's two rows
     int pos[2];
@@ -219,8 +221,8 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
       for (int i = 0; i < 2; ++i) {
         const int r = wr * 16 + g + 8 * i;
         live[i] = r < rows;
-        const int64_t at = row0 + (live[i] ? r : rows - 1);
-        const int token = static_cast<int>(at / a.group), h = static_cast<int>(at % a.group);
+        const int at = row0 + (live[i] ? r : rows - 1);
+        const int token = at / a.group, h = at % a.group;
         pos[i] = ctx + token;
         src[i] = p.q + (w.s.start + token) * p.q_ld + (w.head * a.group + h) * D;
         factor[i] = p.scale_log2;
@@ -283,8 +285,8 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
       for (int j = 0; j < kMine; ++j) qf[(j * kWK + wk) * 32 + lane] = f[j];
       ptx::named_barrier(1, 128);
     }
-    const int first_pos = ctx + static_cast<int>(row0 / a.group);
-    const int last_pos = ctx + static_cast<int>((row0 + rows - 1) / a.group);
+    const int first_pos = ctx + row0 / a.group;
+    const int last_pos = ctx + (row0 + rows - 1) / a.group;
 
     float o[D / 8][4];
 #pragma unroll
@@ -497,15 +499,14 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (!whole && w.begins && threadIdx.x == 0) {
       AttnOpen d;
       d.last = static_cast<int>((w.tile_end - 1) / sh->share.per);
-      d.rows = rows, d.start = w.s.start, d.row0 = static_cast<int>(row0), d.head = w.head;
+      d.rows = rows, d.start = w.s.start, d.row0 = row0, d.head = w.head;
       p.parts.open[blockIdx.x] = d;
     }
     const auto out_at = [&](int r) {  // row r of the tile
-      const int64_t at = row0 + r;
-      const int64_t token = at / a.group, h = at % a.group;
+      const int token = (row0 + r) / a.group, h = (row0 + r) % a.group;
       return p.out + (w.s.start + token) * p.out_ld + (w.head * a.group + h) * D;
     };
-    float *part_o = p.parts.sums + static_cast<int64_t>(part) * p.parts.rows * D;
+    const auto part_at = [&](int r, int d) { return p.parts.at(part, D, d, r); };
     float2 *part_ml = p.parts.ml + static_cast<int64_t>(part) * p.parts.rows;
     if (kWK == 1) {
 #pragma unroll
@@ -524,12 +525,12 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
             if (whole)
               *reinterpret_cast<uint2 *>(dst + d) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
             else
-              *reinterpret_cast<float4 *>(part_o + r * D + d) = v;
+              *reinterpret_cast<float4 *>(part_at(r, d)) = v;
           } else {
             const int d = 8 * j + 2 * c;
             const float x = o[j][2 * i] * f, y = o[j][2 * i + 1] * f;
             if (whole) *reinterpret_cast<uint32_t *>(dst + d) = bf16x2(x, y);
-            else *reinterpret_cast<float2 *>(part_o + r * D + d) = make_float2(x, y);
+            else *reinterpret_cast<float2 *>(part_at(r, d) + (d & 2)) = make_float2(x, y);
           }
         }
       }
@@ -596,7 +597,7 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
               *reinterpret_cast<uint2 *>(dst + d + d0 + e) =
                   make_uint2(bf16x2(v.x * f, v.y * f), bf16x2(v.z * f, v.w * f));
             else
-              *reinterpret_cast<float4 *>(part_o + r * D + d + d0 + e) = v;
+              *reinterpret_cast<float4 *>(part_at(r, d + d0 + e)) = v;
           }
         }
         if (d + kCols < D) ptx::named_barrier(1, 128);

@@ -40,6 +40,8 @@
 
 namespace moe {
 
+constexpr int kTcTileCost = 2;  // beginning and ending a tile, in key tiles
+
 template <int D, int KV>
 struct TcShape {
   static constexpr bool kBytes = KV != MOE_KV_BF16;
@@ -74,7 +76,7 @@ struct TcShape {
 struct TcSmem {
   uint64_t full[12], empty[12], raw_full[12], raw_empty[12];
   uint64_t scale_full[4], scale_empty[4];
-  uint64_t q_full[2], s_full[2], p_full[2], o_done[2], o_last[2], done;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_last[2], turn[2], done;
   AttnShare share;
   uint32_t tmem_holder;
   int abort;
@@ -167,16 +169,13 @@ struct TcSpan {
 };
 template <class Walk>
 __device__ __forceinline__ TcSpan tc_span(const Walk &w, const AttnBatch &a, int R, int i) {
-  const int64_t first = static_cast<int64_t>(w.cur) * R + 128 * i;
-  int64_t last = first + 127;
-  if (last >= w.t.rows) last = w.t.rows - 1;
+  const int first = w.cur * R + 128 * i, last = min(first + 127, w.t.rows - 1);
   TcSpan s;
   if (first >= w.t.rows) {
     s.k0 = s.k1 = 0;
     return s;
   }
-  const int p0 = w.t.ctx + static_cast<int>(first / a.group);
-  const int p1 = w.t.ctx + static_cast<int>(last / a.group);
+  const int p0 = w.t.ctx + first / a.group, p1 = w.t.ctx + last / a.group;
   const int lo = a.window && p0 >= a.window ? (p0 - a.window + 1) / 128 : 0;
   s.k0 = max(w.k0, lo);
   s.k1 = min(w.k1, p1 / 128 + 1);
@@ -186,7 +185,7 @@ __device__ __forceinline__ TcSpan tc_span(const Walk &w, const AttnBatch &a, int
 template <int D, int KV>
 __global__ void __launch_bounds__((TcShape<D, KV>::kThreads), 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-               const AttnBatch a, const AttnRange range, const AttnArgs p) {
+               const __grid_constant__ CUtensorMap tm_q, const AttnBatch a, const AttnRange range, const AttnArgs p) {
   using S = TcShape<D, KV>;
   constexpr bool kBytes = S::kBytes;
   constexpr int NQ = S::kNQ, R = S::kR, kChunks = S::kChunks, kUnits = S::kUnits;
@@ -212,7 +211,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       ptx::mbar_init(&sh->scale_empty[i], S::kSoftWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sh->q_full[i], 4);
+      ptx::mbar_init(&sh->q_full[i], p.q_copy ? 1 : 4);
+      ptx::mbar_init(&sh->q_empty[i], 1);
+      ptx::mbar_init(&sh->turn[i], 1);
       ptx::mbar_init(&sh->s_full[i], 1);
       ptx::mbar_init(&sh->p_full[i], 4);
       ptx::mbar_init(&sh->o_done[i], 1);
@@ -226,7 +227,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   }
   early_begin();
   if (threadIdx.x == 0) p.parts.open[blockIdx.x].last = -1;
-  attn_share<R, 128>(a, range, p.least_share, &sh->share);
+  attn_share<R, 128, kTcTileCost>(a, range, p.least_share, &sh->share);
   if (sh->share.seq < 0) return;
   if (warp == S::kMmaWarp) {
     ptx::tmem_alloc(&sh->tmem_holder, 512);
@@ -236,7 +237,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = sh->tmem_holder;
-  AttnWalk<R, 128> w;
+  AttnWalk<R, 128, kTcTileCost> w;
   w.init(a, sh->share);
   const int page = 1 << a.page_shift;
   const int k_box = page < 128 ? page : 128, v_box = page < S::kVKeys ? page : S::kVKeys;
@@ -252,18 +253,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     bool ok = true;
     while (w.next(a, range)) {
       if (!ok) break;
-      const int64_t row0 = static_cast<int64_t>(w.cur) * R;
-      const int rows = static_cast<int>(w.t.rows - row0 < R ? w.t.rows - row0 : R);
+      const int row0 = w.cur * R;
+      const int rows = min(w.t.rows - row0, R);
       const TcSpan span = tc_span(w, a, R, qi);
       const int r = qi * 128 + wq * 32 + lane;  // this thread's row of the tile
       const bool live = r < rows;
-      const int64_t my_row = row0 + (live ? r : rows - 1);
-      const int token = static_cast<int>(my_row / a.group);
+      const int my_row = row0 + (live ? r : rows - 1);
+      const int token = my_row / a.group, head = w.head * a.group + my_row % a.group;
       const int pos = w.t.ctx + token;
-      const int64_t q_off = (w.s.start + token) * p.q_ld +
-                            (w.head * a.group + static_cast<int>(my_row % a.group)) * D;
+      const int64_t q_off = (w.s.start + token) * p.q_ld + head * D;
       float factor = c_all;
-      if (span.k0 < span.k1) {  // ---- this warp's 32 rows of q
+      if (!p.q_copy && span.k0 < span.k1) {  // ---- this warp's 32 rows of q
         constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = D == 64 ? 8 : 16;
         const int l16 = lane % kLanes;
         uint8_t *q_dst = q_area + qi * kChunks * 16384 + (l16 >> 3) * 16384;
@@ -312,7 +312,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       }
       if (c_all == 0.0f) factor = 1.0f;
       float m = -INFINITY, l = 0.0f;
-      float ref = 0x1p-110f;  // (8-bit) O's sums times ref / 2^13
+      float ref = 0x1p-110f;  // (8-bit) O's sums times ref / 2^7
       bool begun = false;
       for (int kt = w.k0; kt < w.k1 && ok; ++kt) {
         const uint32_t slot = tiles % S::kScaleSlots;
@@ -388,8 +388,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           // it (or a weight above its power of two) is the tile done again.
           bool again = !begun;
           if (begun) {
-            weights(m == -INFINITY ? 0.0f : m, pow2_inverse(ref) * 0x1p13f);
-            again = mt > m + 8.0f || (kBytes && most >= 4.0f * ref);
+            weights(m == -INFINITY ? 0.0f : m, pow2_inverse(ref) * 0x1p7f);
+            again = mt > m + 8.0f || (kBytes && most >= 256.0f * ref);
           }
           if (__any_sync(0xFFFFFFFFu, again)) {
             if (!begun) {
@@ -415,11 +415,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             if (kBytes) {
               weights(base, 0.0f);  // the largest weight
               const float now = ref * alpha;  // (powers of two)
-              const float up = begun && most < 4.0f * now ? now : pow2_floor(most);
+              const float up = begun && most < 256.0f * now ? now : pow2_floor(most);
               ref = fmaxf(up, 0x1p-110f);
               o_factor = now * pow2_inverse(ref);
             }
-            weights(base, pow2_inverse(ref) * 0x1p13f);
+            weights(base, pow2_inverse(ref) * 0x1p7f);
             if (begun && __any_sync(0xFFFFFFFFu, o_factor != 1.0f)) {
               // O's products so far are complete.  (Those before the last are: the
               // scores just read were issued after them.)
@@ -458,7 +458,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       if (!whole && w.begins && threadIdx.x == 0) {
         AttnOpen d;
         d.last = static_cast<int>((w.tile_end - 1) / sh->share.per);
-        d.rows = rows, d.start = w.s.start, d.row0 = static_cast<int>(row0), d.head = w.head;
+        d.rows = rows, d.start = w.s.start, d.row0 = row0, d.head = w.head;
         p.parts.open[blockIdx.x] = d;
       }
       const int64_t at = static_cast<int64_t>(part) * p.parts.rows + r;
@@ -468,10 +468,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         if (!ok) break;
         ptx::tc_fence_after();
         float f = whole ? 1.0f / l : 1.0f;
-        if (kBytes) f *= ref * 0x1p-13f;
-        moe_bf16 *dst = p.out + (w.s.start + token) * p.out_ld +
-                        (w.head * a.group + static_cast<int>(my_row % a.group)) * D;
-        float *sums = p.parts.sums + at * D;
+        if (kBytes) f *= ref * 0x1p-7f;
+        moe_bf16 *dst = p.out + (w.s.start + token) * p.out_ld + head * D;
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {
           float o[32];
@@ -488,7 +486,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           } else {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<float4 *>(sums + i + j) =
+              *reinterpret_cast<float4 *>(p.parts.at(part, D, i + j, r)) =
                   make_float4(o[j] * f, o[j + 1] * f, o[j + 2] * f, o[j + 3] * f);
           }
         }
@@ -500,7 +498,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (S::kSoftRegs) leave_registers<S::kRestRegs>();
     if (warp == S::kFetchWarp) {  // ------------------------------------ fetch
       const uint64_t pol = ptx::policy_evict_last();
-      uint32_t n = 0, tiles = 0;
+      uint32_t n = 0, tiles = 0, q_tiles[2] = {0, 0};
       constexpr int kSlots = kBytes ? S::kRaws : kUnits;
       constexpr int kSlotBytes = kBytes ? S::kRaw : S::kUnit;
       uint8_t *slots = kBytes ? raw : ring;
@@ -552,6 +550,22 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           for (int u = 0; u < kChunks && ok; ++u)
             unit(&tm_v, ids, kt, u * S::kVKeys, S::kVKeys, v_box, D * (kBytes ? 1 : 2), 0);
         };
+        if (p.q_copy) {
+          // (rows behind the sequence's last are of no use and do no harm)
+          for (int i = 0; i < NQ && ok; ++i) {
+            const TcSpan span = tc_span(w, a, R, i);
+            if (span.k0 >= span.k1) continue;
+            ok = ptx::mbar_wait(&sh->q_empty[i], (q_tiles[i] & 1) ^ 1, abort, p.budget);
+            if (!ok) break;
+            ++q_tiles[i];
+            if (lane == 0) ptx::mbar_expect_tx(&sh->q_full[i], kChunks * 16384);
+            __syncwarp();
+            if (lane < kChunks)
+              ptx::tma_load_3d(q_area + (i * kChunks + lane) * 16384, &tm_q, lane * 64,
+                               w.head * a.group, w.s.start + (w.cur * R + 128 * i) / a.group,
+                               &sh->q_full[i], pol);
+          }
+        }
         int before = 0, ids = pages_of(w.k0);
         for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
           const int next = kt < w.k1 ? pages_of(kt + 1) : 0;
@@ -588,6 +602,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const uint32_t j = n - 1 - k;
             ptx::mbar_wait(&full[j % kSlots], (j / kSlots) & 1, &never, ptx::kDrainBudgetNs);
           }
+          for (int i = 0; i < NQ; ++i)
+            if (q_tiles[i] > 0)
+              ptx::mbar_wait(&sh->q_full[i], (q_tiles[i] - 1) & 1, &never, ptx::kDrainBudgetNs);
           for (uint32_t k = 0; k < S::kScaleSlots && k < tiles; ++k) {
             const uint32_t j = tiles - 1 - k;
             ptx::mbar_wait(&sh->scale_full[j % S::kScaleSlots], (j / S::kScaleSlots) & 1, &never,
@@ -662,7 +679,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll
       for (int k = 0; k < kVSteps; ++k)
         v_step[k] = (16 * k / v_box * (v_box * D * 2) + 16 * k % v_box * 128) >> 4;
-      uint32_t n = 0, segs = 0, items = 0;  // units, segments and key tiles so far
+      uint32_t n = 0, segs = 0, items = 0, turns = 0;  // units, segments, key tiles so far
       bool ok = true;
       while (ok && w.next(a, range)) {
         const TcSpan span = tc_span(w, a, R, qi);
@@ -688,7 +705,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           __syncwarp();
         };
         // S from the units n0 .. of a key tile
-        const auto qk = [&](uint32_t n0) {
+        const auto qk = [&](uint32_t n0, bool ends) {
           if (!q_here) {
             q_here = true;
             ok = ptx::mbar_wait(&sh->q_full[qi], segs++ & 1, abort, p.budget);
@@ -703,7 +720,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                       desc_lower(ring_at + (n0 + c) % kUnits * S::kUnit, 16), type, c > 0);
             give_back(n0 + c);
           }
-          if (elect_one()) ptx::mma_commit(&sh->s_full[buffer(items)]);
+          if (elect_one()) {
+            ptx::mma_commit(&sh->s_full[buffer(items)]);
+            if (ends) ptx::mma_commit(&sh->q_empty[qi]);
+          }
           ++items;
         };
         // O += p v, p of the key tile before the newest `ahead`; `left` keys of it
@@ -742,17 +762,22 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
           const bool has_k = kt < w.k1, has_v = kt > w.k0;
           const int left = w.s.len - (kt - 1) * 128;
-          if (NQ == 1 && has_k) qk(n), n += kChunks;
+          if (NQ == 1 && has_k) qk(n, kt + 1 == w.k1), n += kChunks;
+          // The query tiles take turns: each one's softmax then falls into the
+          // other's products, not into the other's softmax.
+          if (NQ == 2 && ok)
+            ok = ptx::mbar_wait(&sh->turn[qi], (turns++ & 1) ^ (qi == 0 ? 1 : 0), abort, p.budget);
           if (has_v && ok) {
             if (span.has(kt - 1)) pv(n, NQ == 1 && has_k ? 1 : 0, left, kt == span.k1);
             else pass(n);
             n += kChunks;
           }
           if (NQ == 2 && has_k && ok) {
-            if (span.has(kt)) qk(n);
+            if (span.has(kt)) qk(n, kt + 1 == span.k1);
             else pass(n);
             n += kChunks;
           }
+          if (NQ == 2 && elect_one()) ptx::mbar_arrive(&sh->turn[1 - qi]);
         }
       }
       // all products are complete before tensor memory is given back

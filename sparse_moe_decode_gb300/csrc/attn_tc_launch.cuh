@@ -25,7 +25,7 @@ cudaError_t launch_tc(const AttnLaunch &x) {
     if (S::kSoftRegs && have.numRegs < S::kRegs) return cudaErrorLaunchOutOfResources;
     if (dev >= 0 && dev < 64) attr[dev] = true;
   }
-  CUtensorMap tk, tv;
+  CUtensorMap tk, tv, tq;
   const int size = S::kBytes ? 1 : 2;
   const int kb = x.page < 128 ? x.page : 128, vb = x.page < S::kVKeys ? x.page : S::kVKeys;
   if (!attn_tc_map(&tk, x.k, D, size, x.cache_rows, kb, 1) ||
@@ -33,10 +33,24 @@ cudaError_t launch_tc(const AttnLaunch &x) {
     return cudaErrorInvalidValue;
   AttnArgs p = x.args;
   p.parts.rows = S::kR;
+  // A query tile as whole tokens' groups of heads: one box.  Not where q is made
+  // fp16, or its sign or zero enters.
+  const int group = x.batch.group;
+  p.q_copy = !S::kBytes && (group & (group - 1)) == 0 && p.scale_log2 > 0.0f;
+  if (p.q_copy) {
+    const uint64_t dims[3] = {D, static_cast<uint64_t>(group) * x.batch.kv_heads,
+                              static_cast<uint64_t>(x.batch.N)};
+    const uint64_t strides[2] = {D * 2, static_cast<uint64_t>(p.q_ld) * 2};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(group), 128u / group};
+    if (!tc_make_map3(&tq, p.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dims, strides, box))
+      return cudaErrorInvalidValue;
+  } else {
+    tq = tk;  // (not used)
+  }
   int grid = tc_sm_count();
   if (grid > kTcMaxCtas) grid = kTcMaxCtas;
   const cudaError_t e =
-      launch_early(kernel, dim3(grid), S::kThreads, S::kSmem, x.stream, tk, tv, x.batch, x.range, p);
+      launch_early(kernel, dim3(grid), S::kThreads, S::kSmem, x.stream, tk, tv, tq, x.batch, x.range, p);
   if (e != cudaSuccess) return e;
   return launch_attn_combine(x.batch, p, D, grid, x.stream);
 }

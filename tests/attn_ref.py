@@ -54,7 +54,7 @@ def attention(q, k, v, length, scale, window, v_scale=None):
         slip[:, h] = np.where(seen, np.abs(q[:, h]) @ np.abs(kk).T, 0.0).max(1) * abs(scale)
         if v_scale is not None:
             sv = v_scale[:, h // g].astype(np.float64)
-            floor[:, h] = 2.0 ** -38 * (w * sv).max(1, keepdims=True) * (seen @ np.abs(vv / sv[:, None]))
+            floor[:, h] = 2.0 ** -32 * (w * sv).max(1, keepdims=True) * (seen @ np.abs(vv / sv[:, None]))
         floor[:, h] += 3 * 2.0 ** -126 * (seen @ np.abs(vv))
     return out, mass, slip, floor
 
@@ -65,9 +65,9 @@ def attention_bound(out, mass, slip, floor, kv):
     any order, the products by the scales and by log2 e, the difference to the
     maximum), which moves a weight and the weights' total by that factor each;
     exp2 and the sums over the keys are off by 2^-18 at most.  With an 8-bit
-    cache a product t of a weight and a scale enters as fp16 of t 2^13 / r, r the
-    power of two at or below the row's largest t: fp16 has steps of 2^-24 below
-    2^-14, so that each t is off by at most 2^-25 / 2^13 r <= 2^-38 of the
+    cache a product t of a weight and a scale enters as fp16 of at least t 2^7 / r,
+    r a power of two at or below the row's largest t: fp16 has steps of 2^-24
+    below 2^-14, so that each t is off by at most 2^-25 / 2^7 r <= 2^-32 of the
     largest, whatever its size, and each term by that times its code.  Weights
     are fp32 beside the largest one's 1: below 2^-126 they count as 0, and so do
     the factors that bring a part's sums (of terms of at most |v| each) to
