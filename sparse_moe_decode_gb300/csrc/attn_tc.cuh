@@ -75,7 +75,7 @@ struct TcShape {
 
 struct TcSmem {
   uint64_t full[12], empty[12], raw_full[12], raw_empty[12];
-  uint64_t scale_full[4], scale_empty[4];
+  uint64_t scale_raw[4], scale_full[4], scale_empty[4];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_last[2], turn[2], done;
   AttnShare share;
   uint32_t tmem_holder;
@@ -207,7 +207,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       ptx::mbar_init(&sh->raw_empty[i], 4);
     }
     for (int i = 0; i < 4; ++i) {
-      ptx::mbar_init(&sh->scale_full[i], 1);
+      ptx::mbar_init(&sh->scale_raw[i], 1);
+      ptx::mbar_init(&sh->scale_full[i], 4);
       ptx::mbar_init(&sh->scale_empty[i], S::kSoftWarps);
     }
     for (int i = 0; i < 2; ++i) {
@@ -261,6 +262,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const int my_row = row0 + (live ? r : rows - 1);
       const int token = my_row / a.group, head = w.head * a.group + my_row % a.group;
       const int pos = w.t.ctx + token;
+      const int warp_pos = __shfl_sync(0xFFFFFFFFu, pos, 0);  // the warp's first and last
+      const int warp_last = __shfl_sync(0xFFFFFFFFu, pos, 31);
       const int64_t q_off = (w.s.start + token) * p.q_ld + head * D;
       float factor = c_all;
       if (!p.q_copy && span.k0 < span.k1) {  // ---- this warp's 32 rows of q
@@ -333,112 +336,119 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           for (int i = 0; i < 4; ++i)
             ptx::tmem_ld32(s_at + 32 * i, *reinterpret_cast<float(*)[32]>(s + 32 * i));
           ptx::tmem_wait_ld();
-          const float *sc = scales + slot * 256;
+          const float4 *sc = reinterpret_cast<const float4 *>(scales + slot * 256);
           if (kBytes) {
 #pragma unroll
             for (int i = 0; i < 128; i += 4) {
-              const float4 f = *reinterpret_cast<const float4 *>(sc + i);
-              s[i] *= f.x, s[i + 1] *= f.y, s[i + 2] *= f.z, s[i + 3] *= f.w;
+              const float4 f = sc[i / 4];
+              const float2 x = mul2(make_float2(s[i], s[i + 1]), make_float2(f.x, f.y));
+              const float2 y = mul2(make_float2(s[i + 2], s[i + 3]), make_float2(f.z, f.w));
+              s[i] = x.x, s[i + 1] = x.y, s[i + 2] = y.x, s[i + 3] = y.y;
             }
           }
-          const int key0 = kt * 128;
-          // some row of the warp does not see all of the tile
-          const int hi = pos - key0, lo = a.window ? pos - a.window - key0 : -1;
-          if (__any_sync(0xFFFFFFFFu, hi < 127 || lo >= 0)) {
+          const int key0 = kt * 128, hi = pos - key0;
+          if (key0 + 127 > warp_pos) {  // some row of the warp does not see all of the tile
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i > hi || i <= lo) s[i] = -INFINITY;
+            for (int i = 0; i < 128; ++i) s[i] = i > hi ? -INFINITY : s[i];
           }
-          float2 sum[2];
-          float most = 0.0f, mt = 0.0f;
-          // p = 2^(s - m) (with 8-bit caches times the value's scale) into S's
-          // place; the tile's maximum on the way
-          const auto weights = [&](float base, float f16) {
+          if (a.window && key0 + a.window <= warp_last) {
+            const int lo = hi - a.window;
+#pragma unroll
+            for (int i = 0; i < 128; ++i) s[i] = i <= lo ? -INFINITY : s[i];
+          }
+          const auto largest = [&]() {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 128; i += 8)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) top[j] = max3(top[j], s[i + 2 * j], s[i + 2 * j + 1]);
+            return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
+          };
+          // p = 2^(s - m), with 8-bit caches times the value's scale, into S's
+          // place.  m is the maximum of the tiles before, which nearly always
+          // does: only where the tile's total (or a weight above its power of two)
+          // says that m is far too small is it found anew, and the tile done again.
+          float o_factor = 1.0f, total, most;
+          if (!begun) m = largest();
+          while (true) {
+            const float base = m == -INFINITY ? 0.0f : m;
             const float2 f2 = make_float2(factor, factor), b2 = make_float2(-base, -base);
-            sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+            const float f = pow2_inverse(ref) * 0x1p7f;
+            const float2 w2 = make_float2(f, f);
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
             most = 0.0f;
-            float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               uint32_t pk[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
+              for (int i = 0; i < 16; i += 2) {
                 const int at = h * 32 + 2 * i;
                 float2 x = fma2(make_float2(s[at], s[at + 1]), f2, b2);
+                float2 y = fma2(make_float2(s[at + 2], s[at + 3]), f2, b2);
                 x.x = attn_exp2(x.x), x.y = attn_exp2(x.y);
-                sum[i & 1] = add2(x, sum[i & 1]);
-                top[i & 1] = max3(top[i & 1], s[at], s[at + 1]);
+                y.x = attn_exp2(y.x), y.y = attn_exp2(y.y);
+                sum[0] = add2(x, sum[0]), sum[1] = add2(y, sum[1]);
                 if (kBytes) {
-                  const float2 v = *reinterpret_cast<const float2 *>(sc + 128 + at);
-                  // a hidden key's weight is 0 whatever its scale
-                  x.x = x.x == 0.0f ? 0.0f : x.x * v.x;
-                  x.y = x.y == 0.0f ? 0.0f : x.y * v.y;
-                  most = max3(most, x.x, x.y);
-                  pk[i] = h2_bits(__floats2half2_rn(x.x * f16, x.y * f16));
+                  const float4 v = sc[32 + at / 4];
+                  x = mul2(x, make_float2(v.x, v.y)), y = mul2(y, make_float2(v.z, v.w));
+                  most = max3(max3(most, x.x, x.y), y.x, y.y);
+                  x = mul2(x, w2), y = mul2(y, w2);
+                  pk[i] = h2_bits(__float22half2_rn(x)), pk[i + 1] = h2_bits(__float22half2_rn(y));
                 } else {
-                  pk[i] = pack_bf16(x.x, x.y);
+                  pk[i] = pack_bf16(x.x, x.y), pk[i + 1] = pack_bf16(y.x, y.y);
                 }
               }
               tmem_st16(s_at + 16 * h, pk);
             }
-            mt = fmaxf(top[0], top[1]) * factor;
-          };
-          // The tiles before have left a maximum that nearly always does: p is
-          // formed under it at once.  Only where a score lies more than 2^8 above
-          // it (or a weight above its power of two) is the tile done again.
-          bool again = !begun;
-          if (begun) {
-            weights(m == -INFINITY ? 0.0f : m, pow2_inverse(ref) * 0x1p7f);
-            again = mt > m + 8.0f || (kBytes && most >= 256.0f * ref);
-          }
-          if (__any_sync(0xFFFFFFFFu, again)) {
-            if (!begun) {
-              float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-              for (int i = 0; i < 128; i += 8)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) top[j] = max3(top[j], s[i + 2 * j], s[i + 2 * j + 1]);
-              mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
+            const float2 both = add2(sum[0], sum[1]);
+            total = both.x + both.y;
+            const bool far = total > 0x1p15f || m == -INFINITY;
+            const bool over = kBytes && most >= 256.0f * ref && ref < 0x1p126f;
+            if (!__any_sync(0xFFFFFFFFu, far || over)) break;
+            float up = m;
+            if (far) {
+              const float mt = largest();
+              // (by a whole power of two, so that O's factor is exact)
+              if (m == -INFINITY) up = mt;
+              else if (mt > m) up = m + ceilf(mt - m);
             }
-            // by a whole power of two, so that O's factor is exact
-            float alpha = 1.0f;
-            if (!begun) {
-              m = mt;
-            } else if (mt > m + 8.0f) {
-              const float up = m == -INFINITY ? mt : m + ceilf(mt - m);
-              alpha = attn_exp2(m - up);
+            float factor_o = 1.0f;
+            if (up != m) {
+              factor_o = attn_exp2(m - up);
+              l *= factor_o;
               m = up;
-            }
-            l *= alpha;
-            const float base = m == -INFINITY ? 0.0f : m;
-            float o_factor = alpha;
-            if (kBytes) {
-              weights(base, 0.0f);  // the largest weight
-              const float now = ref * alpha;  // (powers of two)
-              const float up = begun && most < 256.0f * now ? now : pow2_floor(most);
-              ref = fmaxf(up, 0x1p-110f);
-              o_factor = now * pow2_inverse(ref);
-            }
-            weights(base, pow2_inverse(ref) * 0x1p7f);
-            if (begun && __any_sync(0xFFFFFFFFu, o_factor != 1.0f)) {
-              // O's products so far are complete.  (Those before the last are: the
-              // scores just read were issued after them.)
-              ok = ptx::mbar_wait(&sh->o_done[qi], (items - 1) & 1, abort, p.budget);
-              if (!ok) break;
-              ptx::tc_fence_after();
-#pragma unroll 1
-              for (int i = 0; i < D; i += 16) {
-                float o[16];
-                uint32_t u[16];
-                ptx::tmem_ld16(o_at + i, o);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[j] * o_factor);
-                tmem_st16(o_at + i, u);
+              if (kBytes) {
+                const float now = ref * factor_o;
+                ref = fmaxf(now, 0x1p-110f);
+                factor_o = now * pow2_inverse(ref);
               }
+            } else if (over) {
+              const float now = ref;
+              ref = pow2_floor(most);
+              factor_o = now * pow2_inverse(ref);
+            }
+            o_factor *= factor_o;
+            // (nothing left to change: rows that see none of the tile)
+            if (!__any_sync(0xFFFFFFFFu, factor_o != 1.0f)) break;
+          }
+          if (begun && __any_sync(0xFFFFFFFFu, o_factor != 1.0f)) {
+            // O's products so far are complete.  (Those before the last are: the
+            // scores just read were issued after them.)
+            ok = ptx::mbar_wait(&sh->o_done[qi], (items - 1) & 1, abort, p.budget);
+            if (!ok) break;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < D; i += 16) {
+              float o[16];
+              uint32_t u[16];
+              ptx::tmem_ld16(o_at + i, o);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[j] * o_factor);
+              tmem_st16(o_at + i, u);
             }
           }
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          l += total;
           ptx::tmem_wait_st();
           ptx::tc_fence_before();
           __syncwarp();
@@ -578,13 +588,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
               if (!ok) break;
               const int there = len - kt * 128;
               const int have = min(128 / k_box, (there + k_box - 1) / k_box);
-              if (lane == 0) ptx::mbar_expect_tx(&sh->scale_full[slot], 2 * have * k_box * 4);
+              if (lane == 0) ptx::mbar_expect_tx(&sh->scale_raw[slot], 2 * have * k_box * 4);
               __syncwarp();
               const int row = row_of(ids, kt, (lane * k_box) & 127);
               if (lane < have) {
                 float *dst = scales + slot * 256 + lane * k_box;
-                bulk_load(ptx::smem_u32(dst), p.k_scale + row, k_box * 4, &sh->scale_full[slot]);
-                bulk_load(ptx::smem_u32(dst + 128), p.v_scale + row, k_box * 4, &sh->scale_full[slot]);
+                bulk_load(ptx::smem_u32(dst), p.k_scale + row, k_box * 4, &sh->scale_raw[slot]);
+                bulk_load(ptx::smem_u32(dst + 128), p.v_scale + row, k_box * 4, &sh->scale_raw[slot]);
               }
               ++tiles;
             }
@@ -607,7 +617,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
               ptx::mbar_wait(&sh->q_full[i], (q_tiles[i] - 1) & 1, &never, ptx::kDrainBudgetNs);
           for (uint32_t k = 0; k < S::kScaleSlots && k < tiles; ++k) {
             const uint32_t j = tiles - 1 - k;
-            ptx::mbar_wait(&sh->scale_full[j % S::kScaleSlots], (j / S::kScaleSlots) & 1, &never,
+            ptx::mbar_wait(&sh->scale_raw[j % S::kScaleSlots], (j / S::kScaleSlots) & 1, &never,
                            ptx::kDrainBudgetNs);
           }
         }
@@ -655,12 +665,29 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         ++n;
       };
+      uint32_t tiles = 0;
+      // A value's scale that is not finite moves to its key's, so that the row that
+      // sees it is NaN, and 0 times it is not NaN where it is hidden.
+      const auto tile_scales = [&]() {
+        const uint32_t slot = tiles % S::kScaleSlots;
+        ok = ptx::mbar_wait(&sh->scale_raw[slot], (tiles / S::kScaleSlots) & 1, abort, p.budget);
+        if (!ok) return;
+        float *sc = scales + slot * 256 + t;
+        if (!(fabsf(sc[128]) < INFINITY)) {
+          sc[0] = sc[128] - sc[128], sc[128] = 0.0f;
+          ptx::fence_proxy_async_smem();  // (the slot's next copy)
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh->scale_full[slot]);
+        ++tiles;
+      };
       while (ok && w.next(a, range)) {
         const auto v_units = [&](int kt) {
           for (int u = 0; u < kChunks && ok; ++u) unit(true, w.s.len - kt * 128 - u * S::kVKeys);
         };
         for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
           if (NQ == 2 && kt > w.k0) v_units(kt - 1);
+          if (kt < w.k1 && ok) tile_scales();
           if (kt < w.k1)
             for (int c = 0; c < kChunks && ok; ++c) unit(false, 0);
           if (NQ == 1 && kt > w.k0) v_units(kt - 1);
@@ -690,94 +717,115 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           ok = ok && ptx::mbar_wait(&sh->full[u % kUnits], (u / kUnits) & 1, abort, p.budget);
           return ok;
         };
-        // (free when the products that read it, and all before, are complete)
-        const auto give_back = [&](uint32_t u) {
-          if (elect_one()) ptx::mma_commit(&sh->empty[u % kUnits]);
-        };
-        // Values behind the sequence's end: 0 (the slot holds what was there; with
+        // Values behind the sequence's end: 0 (the slots hold what was there; with
         // two query tiles both warps do so).
-        const auto clear_tail = [&](uint8_t *at, int left) {
-          for (int i = lane; i < 1024; i += 32) {  // 16 bytes each
-            const int row = i / 8, key = row / (v_box * kChunks) * v_box + row % v_box;
-            if (key >= left) reinterpret_cast<uint4 *>(at)[i] = make_uint4(0, 0, 0, 0);
+        const auto clear_tail = [&](uint32_t n0, int left) {
+          for (int u = 0; u < kChunks; ++u) {
+            uint4 *at = reinterpret_cast<uint4 *>(ring + (n0 + u) % kUnits * S::kUnit);
+            for (int i = lane; i < 1024; i += 32) {  // 16 bytes each
+              const int row = i / 8;
+              const int key = u * S::kVKeys + row / (v_box * kChunks) * v_box + row % v_box;
+              if (key >= left) at[i] = make_uint4(0, 0, 0, 0);
+            }
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
         };
-        // S from the units n0 .. of a key tile
+        const auto here = [&](uint32_t n0) {
+          for (int u = 0; u < kChunks; ++u)
+            if (!arrived(n0 + u)) return;
+        };
+        // S from the units n0 .. of a key tile, which are here
         const auto qk = [&](uint32_t n0, bool ends) {
-          if (!q_here) {
-            q_here = true;
-            ok = ptx::mbar_wait(&sh->q_full[qi], segs++ & 1, abort, p.budget);
-            if (!ok) return;
-          }
           const uint32_t s_at = tmem + S::kS + buffer(items) * 128;
-          for (int c = 0; c < kChunks; ++c) {
-            if (!arrived(n0 + c)) return;
-            ptx::tc_fence_after();
-            if (elect_one())
+          if (elect_one()) {
+            for (int c = 0; c < kChunks; ++c)
               mma_ss4(s_at, desc_lower(q_at + c * 16384, 16),
                       desc_lower(ring_at + (n0 + c) % kUnits * S::kUnit, 16), type, c > 0);
-            give_back(n0 + c);
-          }
-          if (elect_one()) {
+            if (NQ == 2) ptx::mbar_arrive(&sh->turn[1 - qi]);
             ptx::mma_commit(&sh->s_full[buffer(items)]);
+            for (int c = 0; c < kChunks; ++c) ptx::mma_commit(&sh->empty[(n0 + c) % kUnits]);
             if (ends) ptx::mma_commit(&sh->q_empty[qi]);
           }
+          __syncwarp();
           ++items;
         };
-        // O += p v, p of the key tile before the newest `ahead`; `left` keys of it
-        // are the sequence's.  `ends`: the segment's last (a barrier of its own:
-        // o_done's phases before may go by unseen)
-        const auto pv = [&](uint32_t n0, int ahead, int left, bool ends) {
+        // The p of the key tile before the newest `ahead`.
+        const auto weights = [&](int ahead) {
           const uint32_t item = items - 1 - ahead;
-          const uint32_t p_at = tmem + S::kS + buffer(item) * 128;
-          ok = ptx::mbar_wait(&sh->p_full[buffer(item)], parity(item), abort, p.budget);
-          if (!ok) return;
-          for (int u = 0; u < kChunks; ++u) {
-            if (!arrived(n0 + u)) return;
-            const uint32_t slot = (n0 + u) % kUnits;
-            if (!kBytes && left < (u + 1) * S::kVKeys)
-              clear_tail(ring + slot * S::kUnit, left - u * S::kVKeys);
-            ptx::tc_fence_after();
-            if (elect_one()) {
-              const uint32_t v_at = desc_lower(ring_at + slot * S::kUnit, v_box * 128);
+          ok = ok && ptx::mbar_wait(&sh->p_full[buffer(item)], parity(item), abort, p.budget);
+        };
+        // O += p v.  `ends`: the segment's last (a barrier of its own: o_done's
+        // phases before may go by unseen)
+        const auto pv = [&](uint32_t n0, int ahead, bool ends) {
+          const uint32_t p_at = tmem + S::kS + buffer(items - 1 - ahead) * 128;
+          if (elect_one()) {
+            for (int u = 0; u < kChunks; ++u) {
+              const uint32_t v_at =
+                  desc_lower(ring_at + (n0 + u) % kUnits * S::kUnit, v_box * 128);
 #pragma unroll
               for (int k = 0; k < kVSteps; k += 2)
                 mma_ts2(tmem + S::kO + qi * D, p_at + u * (S::kVKeys / 2) + 8 * k,
                         v_at + v_step[k], v_at + v_step[k + 1], type_v, o_begun || u > 0 || k > 0);
             }
-            give_back(n0 + u);
-          }
-          if (elect_one()) {
             ptx::mma_commit(&sh->o_done[qi]);
             if (ends) ptx::mma_commit(&sh->o_last[qi]);
+            for (int u = 0; u < kChunks; ++u) ptx::mma_commit(&sh->empty[(n0 + u) % kUnits]);
           }
+          __syncwarp();
           o_begun = true;
         };
         const auto pass = [&](uint32_t n0) {  // a key tile of no row of this query tile
-          for (int u = 0; u < kChunks; ++u)
-            if (arrived(n0 + u)) give_back(n0 + u);
+          if (elect_one())
+            for (int u = 0; u < kChunks; ++u) ptx::mma_commit(&sh->empty[(n0 + u) % kUnits]);
+          __syncwarp();
         };
-        for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
+        for (int kt = w.k0; kt <= w.k1; ++kt) {
           const bool has_k = kt < w.k1, has_v = kt > w.k0;
+          const bool do_k = has_k && span.has(kt), do_v = has_v && span.has(kt - 1);
           const int left = w.s.len - (kt - 1) * 128;
-          if (NQ == 1 && has_k) qk(n, kt + 1 == w.k1), n += kChunks;
+          // All that the products need is waited for before the first of them: the
+          // tensor cores have room for few, and stand still during a wait.
+          if (do_k && !q_here) {
+            q_here = true;
+            ok = ok && ptx::mbar_wait(&sh->q_full[qi], segs++ & 1, abort, p.budget);
+          }
+          if (NQ == 1) {
+            if (has_k) {
+              here(n);
+              if (!ok) break;
+              ptx::tc_fence_after();
+              qk(n, kt + 1 == w.k1), n += kChunks;
+            }
+            if (has_v) {
+              here(n);
+              if (ok && !kBytes && left < 128) clear_tail(n, left);
+              weights(has_k ? 1 : 0);
+              if (!ok) break;
+              ptx::tc_fence_after();
+              pv(n, has_k ? 1 : 0, kt == w.k1), n += kChunks;
+            }
+            continue;
+          }
+          uint32_t nv = n;
+          if (has_v) here(n), n += kChunks;
+          if (has_k) here(n);
+          if (ok && do_v && !kBytes && left < 128) clear_tail(nv, left);
+          if (do_v) weights(0);
           // The query tiles take turns: each one's softmax then falls into the
           // other's products, not into the other's softmax.
-          if (NQ == 2 && ok)
-            ok = ptx::mbar_wait(&sh->turn[qi], (turns++ & 1) ^ (qi == 0 ? 1 : 0), abort, p.budget);
-          if (has_v && ok) {
-            if (span.has(kt - 1)) pv(n, NQ == 1 && has_k ? 1 : 0, left, kt == span.k1);
-            else pass(n);
-            n += kChunks;
+          ok = ok && ptx::mbar_wait(&sh->turn[qi], (turns++ & 1) ^ (qi == 0 ? 1 : 0), abort, p.budget);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          if (do_v) pv(nv, 0, kt == span.k1);
+          else if (has_v) pass(nv);
+          if (do_k) {
+            qk(n, kt + 1 == span.k1);
+          } else {
+            if (elect_one()) ptx::mbar_arrive(&sh->turn[1 - qi]);
+            if (has_k) pass(n);
           }
-          if (NQ == 2 && has_k && ok) {
-            if (span.has(kt)) qk(n, kt + 1 == span.k1);
-            else pass(n);
-            n += kChunks;
-          }
-          if (NQ == 2 && elect_one()) ptx::mbar_arrive(&sh->turn[1 - qi]);
+          if (has_k) n += kChunks;
         }
       }
       // all products are complete before tensor memory is given back
