@@ -2,13 +2,16 @@
 //
 // A cluster of 8 blocks takes a sequence.  Each finds the first token that is
 // not accepted (u q < p as exact products in 64 bits); then the blocks share
-// out the row of V weights max(p - q, 0): their sums by segments of 1024, the
+// out the row of V weights max(p - q, 0): their sums by segments of 512, the
 // total over the cluster, and the block whose segments hold r * total looks
 // for the place in that one segment again.  Bound by memory for many
 // sequences (one row of p and q each, read once), by the chain of loads for
-// few.  Sums of the weights are pairs of fp32 (48 bits, exact differences),
-// added up in 64 bits: the place that r falls into does not depend on the
-// order, but for ties within 2^-48 of the total.
+// few.
+//
+// Weights and sums are pairs of fp32 (differences exact, 48 bits kept): the
+// place that r falls into does not depend on the order of the sums, but for
+// borders within some 2^-45 of the total.  Adding in 64 bits took longer than
+// the loads: a warp's addition occupies the SM for 16 cycles.
 #include <cooperative_groups.h>
 
 #include "attn.h"
@@ -23,85 +26,128 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCluster = 8;
-constexpr int kSegment = 1024;
-// of one block's share
-constexpr int kMaxSegments = (1 << 24) / kSegment / kCluster;
+constexpr int kSegment = 512;
 
-struct DraftShared {
-  double seg[kMaxSegments];
-  double warp_sum[kWarps];
-  double total;  // of the block
-  int stop, token, bad;
-  int positive;  // last place with a positive weight in a segment
+// hi + lo, |lo| at most half a step of hi.
+struct Pair {
+  float hi, lo;
 };
 
 // x - y = hi + lo, exactly (Moller, Knuth).
-__device__ __forceinline__ void exact_diff(float x, float y, float &hi, float &lo) {
-  hi = x - y;
-  const float t = hi - x;
-  lo = (x - (hi - t)) - (y + t);
+__device__ __forceinline__ Pair exact_diff(float x, float y) {
+  Pair r;
+  r.hi = x - y;
+  const float t = r.hi - x;
+  r.lo = (x - (r.hi - t)) - (y + t);
+  return r;
 }
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo);
+  Pair r;
+  r.hi = s + e;
+  r.lo = e - (r.hi - s);
+  return r;
+}
+__device__ __forceinline__ Pair times(Pair a, float f) {
+  const float p = a.hi * f, e = fmaf(a.hi, f, -p) + a.lo * f;
+  Pair r;
+  r.hi = p + e;
+  r.lo = e - (r.hi - p);
+  return r;
+}
+__device__ __forceinline__ bool above(Pair a, Pair b) {
+  return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
+}
+__device__ __forceinline__ Pair shuffle_xor(Pair a, int o) {
+  return Pair{__shfl_xor_sync(0xFFFFFFFFu, a.hi, o), __shfl_xor_sync(0xFFFFFFFFu, a.lo, o)};
+}
+// The sum over the lanes up to this one, and over all.
+__device__ __forceinline__ Pair scan(Pair a, int lane, Pair &all) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair b{__shfl_up_sync(0xFFFFFFFFu, a.hi, o), __shfl_up_sync(0xFFFFFFFFu, a.lo, o)};
+    if (lane >= o) a = add(b, a);
+  }
+  all = Pair{__shfl_sync(0xFFFFFFFFu, a.hi, 31), __shfl_sync(0xFFFFFFFFu, a.lo, 31)};
+  return a;
+}
+
+struct DraftShared {
+  Pair totals[kCluster];  // of all blocks of the cluster
+  uint32_t worst[kCluster];
+  uint32_t warp_worst[kWarps];
+  Pair warp_sum[kWarps];
+  Pair start;  // the sum before the segment of the aim
+  int stop, token, found, hit, last;
+  // the segments' sums follow
+};
 
 struct DraftRow {
   const float *p, *q;  // q nullable
   int one;             // the place whose q is 1 where q is null; -1: none
-  bool aligned;        // both rows start on 16 bytes
 
-  __device__ __forceinline__ float less(int j) const {
+  __device__ __forceinline__ float less(int64_t j) const {
     return q ? q[j] : j == one ? 1.0f : 0.0f;
-  }
-  __device__ __forceinline__ double weight(int j) const {
-    const double w = static_cast<double>(p[j]) - static_cast<double>(less(j));
-    return w > 0.0 ? w : 0.0;
   }
 };
 
-__device__ __forceinline__ bool usable(float x) { return x >= 0.0f && x < INFINITY; }
+__device__ __forceinline__ Pair weight(float p, float q) {
+  Pair d = exact_diff(p, q);
+  if (!(d.hi > 0.0f)) d.hi = d.lo = 0.0f;  // (a difference that rounds to 0 is 0)
+  return d;
+}
 
-// Sum of the weights at j0 .. j0 + kSegment - 1 (those below V), one warp.
-__device__ __forceinline__ double segment_sum(const DraftRow &row, int64_t j0, int V, int lane,
-                                              bool &bad) {
-  float hi = 0.0f, lo = 0.0f;
-  const auto add = [&](float p, float q) {
-    bad |= !usable(p) | !usable(q);
-    float d, e;
-    exact_diff(p, q, d, e);
-    if (!(d > 0.0f)) d = e = 0.0f;  // (a difference that rounds to 0 is 0)
-    const float s = hi + d, t = s - hi;
-    lo += ((hi - (s - t)) + (d - t)) + e;
-    hi = s;
-  };
-  if (row.aligned && j0 + kSegment <= V) {
-    float4 p[kSegment / 128], q[kSegment / 128];
+// A block's values of one segment, 16 a lane.
+struct Segment {
+  float4 p[kSegment / 128], q[kSegment / 128];
+
+  __device__ __forceinline__ void load(const DraftRow &row, int64_t j0, int V, int lane,
+                                       bool aligned) {
 #pragma unroll
     for (int i = 0; i < kSegment / 128; ++i) {
       const int64_t j = j0 + i * 128 + lane * 4;
-      p[i] = __ldg(reinterpret_cast<const float4 *>(row.p + j));
-      if (row.q) q[i] = __ldg(reinterpret_cast<const float4 *>(row.q + j));
-      else
-        q[i] = make_float4(row.less(j), row.less(j + 1), row.less(j + 2), row.less(j + 3));
-    }
+      if (aligned && j + 4 <= V) {
+        p[i] = __ldg(reinterpret_cast<const float4 *>(row.p + j));
+        q[i] = row.q ? __ldg(reinterpret_cast<const float4 *>(row.q + j))
+                     : make_float4(row.less(j), row.less(j + 1), row.less(j + 2), row.less(j + 3));
+      } else {
+        float a[4], b[4];
 #pragma unroll
-    for (int i = 0; i < kSegment / 128; ++i) {
-      add(p[i].x, q[i].x), add(p[i].y, q[i].y), add(p[i].z, q[i].z), add(p[i].w, q[i].w);
-    }
-  } else {
-#pragma unroll 8
-    for (int i = 0; i < kSegment / 32; ++i) {
-      const int64_t j = j0 + i * 32 + lane;
-      if (j < V) add(row.p[j], row.less(static_cast<int>(j)));
+        for (int k = 0; k < 4; ++k) {
+          a[k] = j + k < V ? __ldg(row.p + j + k) : 0.0f;
+          b[k] = j + k < V ? row.less(j + k) : 0.0f;
+        }
+        p[i] = make_float4(a[0], a[1], a[2], a[3]);
+        q[i] = make_float4(b[0], b[1], b[2], b[3]);
+      }
     }
   }
-  double s = static_cast<double>(hi) + static_cast<double>(lo);
+  // The lane's weights' sum; `worst`: the largest bits of a value, above all
+  // finite positive ones' where one is negative, infinite or NaN.
+  __device__ __forceinline__ Pair sum(uint32_t &worst) const {
+    Pair s{0.0f, 0.0f};
+    const auto one = [&](float x, float y) {
+      // (-0 + 0 = 0)
+      worst = max(worst, max(__float_as_uint(x + 0.0f), __float_as_uint(y + 0.0f)));
+      const Pair d = weight(x, y);
+      const float t = s.hi + d.hi, u = t - s.hi;
+      s.lo += ((s.hi - (t - u)) + (d.hi - u)) + d.lo;
+      s.hi = t;
+    };
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  return s;
-}
+    for (int i = 0; i < kSegment / 128; ++i) {
+      one(p[i].x, q[i].x), one(p[i].y, q[i].y), one(p[i].z, q[i].z), one(p[i].w, q[i].w);
+    }
+    return add(Pair{s.hi, 0.0f}, Pair{s.lo, 0.0f});
+  }
+};
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 3)
 verify_draft_kernel(const DraftArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   DraftShared *sh = reinterpret_cast<DraftShared *>(smem);
+  Pair *seg = reinterpret_cast<Pair *>(sh + 1);
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
   const int b = blockIdx.x / kCluster;
@@ -109,6 +155,7 @@ verify_draft_kernel(const DraftArgs a) {
   early_begin();
   const int32_t *drafted = a.draft_tokens + static_cast<int64_t>(b) * a.T;
   const float *u = a.uniform + static_cast<int64_t>(b) * (a.T + 1);
+  const float r = u[a.T];
   if (warp == 0) {
     int stop = a.T, token = -1;
     for (int i0 = 0; i0 < a.T; i0 += 32) {
@@ -117,11 +164,12 @@ verify_draft_kernel(const DraftArgs a) {
       bool stands = true;
       if (i < a.T) {
         d = drafted[i];
+        const float ui = u[i];
         stands = false;
         if (d >= 0 && d < a.V) {
           const float p = a.target[b * a.target_seq_ld + i * a.target_ld + d];
           const float q = a.draft ? a.draft[b * a.draft_seq_ld + i * a.draft_ld + d] : 1.0f;
-          stands = static_cast<double>(u[i]) * static_cast<double>(q) < static_cast<double>(p);
+          stands = static_cast<double>(ui) * static_cast<double>(q) < static_cast<double>(p);
         }
       }
       const unsigned fell = __ballot_sync(0xFFFFFFFFu, !stands);
@@ -132,20 +180,22 @@ verify_draft_kernel(const DraftArgs a) {
         break;
       }
     }
-    if (lane == 0) sh->stop = stop, sh->token = token, sh->bad = 0;
+    if (lane == 0) sh->stop = stop, sh->token = token, sh->found = -1;
   }
   __syncthreads();
   const int stop = sh->stop, token = sh->token;
-  const bool outside = token >= a.V;  // not a token
   int32_t *out = a.tokens + static_cast<int64_t>(b) * (a.T + 1);
-  if (outside) {  // (all blocks of the cluster)
+  const auto refuse = [&](uint32_t bits) {
     if (rank == 0) {
       for (int i = tid; i <= a.T; i += kThreads) out[i] = -1;
       if (tid == 0) {
         a.accepted[b] = 0;
-        set_status(a.status, MOE_DEV_BAD_INDEX);
+        set_status(a.status, bits);
       }
     }
+  };
+  if (token >= a.V) {  // not a token (all blocks of the cluster)
+    refuse(MOE_DEV_BAD_INDEX);
     return;
   }
   DraftRow row;
@@ -157,49 +207,59 @@ verify_draft_kernel(const DraftArgs a) {
   }
   const int all = static_cast<int>((static_cast<int64_t>(a.V) + kSegment - 1) / kSegment);
   const int per = (all + kCluster - 1) / kCluster;
-  const int seg0 = rank * per, segs = min(per, all - seg0);  // may be below 0
-  double total = 0.0, before = 0.0;
-  bool any_bad = false;
+  const int seg0 = rank * per, segs = max(0, min(per, all - seg0));
+  Pair total, before, mine;
+  uint32_t worst = 0;
   int last_rank = 0;  // that has any weight
   for (int round = 0; round < 2; ++round) {
-    row.aligned = (reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) % 16 == 0;
-    bool bad = false;
+    const bool aligned =
+        (reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) % 16 == 0;
+    uint32_t bits = 0;
+    Pair part{0.0f, 0.0f};  // of this warp's segments
+    Segment now, next;
+    if (warp < segs) now.load(row, static_cast<int64_t>(seg0 + warp) * kSegment, a.V, lane, aligned);
     for (int s = warp; s < segs; s += kWarps) {
-      const double v =
-          segment_sum(row, static_cast<int64_t>(seg0 + s) * kSegment, a.V, lane, bad);
-      if (lane == 0) sh->seg[s] = v;
-    }
-    if (bad) sh->bad = 1;
-    __syncthreads();
-    if (warp == 0) {
-      double sum = 0.0;
-      for (int s = lane; s < segs; s += 32) sum += sh->seg[s];
+      if (s + kWarps < segs)
+        next.load(row, static_cast<int64_t>(seg0 + s + kWarps) * kSegment, a.V, lane, aligned);
+      Pair v = now.sum(bits);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      if (lane == 0) sh->total = sum;
+      for (int o = 16; o > 0; o >>= 1) v = add(v, shuffle_xor(v, o));
+      if (lane == 0) seg[s] = v;
+      part = add(part, v);
+      now = next;
+    }
+    bits = __reduce_max_sync(0xFFFFFFFFu, bits);
+    if (lane == 0) sh->warp_worst[warp] = bits, sh->warp_sum[warp] = part;
+    __syncthreads();
+    if (tid < kCluster) {  // every block hears of every other's
+      Pair t = sh->warp_sum[0];
+      uint32_t x = sh->warp_worst[0];
+      for (int k = 1; k < kWarps; ++k) {
+        t = add(t, sh->warp_sum[k]);
+        x = max(x, sh->warp_worst[k]);
+      }
+      DraftShared *other = cluster.map_shared_rank(sh, tid);
+      other->totals[rank] = t;
+      other->worst[rank] = x;
     }
     cluster.sync();
-    total = before = 0.0;
+    total = before = Pair{0.0f, 0.0f};
     for (int k = 0; k < kCluster; ++k) {
-      const DraftShared *other = cluster.map_shared_rank(sh, k);
+      const Pair t = sh->totals[k];
       if (k == rank) before = total;
-      total += other->total;
-      if (other->total > 0.0) last_rank = k;
-      any_bad |= other->bad != 0;
+      total = add(total, t);
+      worst = max(worst, sh->worst[k]);
+      if (t.hi > 0.0f) last_rank = k;
     }
-    cluster.sync();  // nobody's sums change or end before all have read them
+    mine = add(before, sh->totals[rank]);
     // p never exceeds q: p itself
-    if (any_bad || total > 0.0 || (!row.q && row.one < 0)) break;
+    if (worst >= 0x7F800000u || total.hi > 0.0f || (!row.q && row.one < 0)) break;
+    cluster.sync();  // all have read
     row.q = nullptr, row.one = -1;
   }
-  if (any_bad || !(total > 0.0)) {
-    if (rank == 0) {
-      for (int i = tid; i <= a.T; i += kThreads) out[i] = -1;
-      if (tid == 0) {
-        a.accepted[b] = 0;
-        set_status(a.status, MOE_DEV_NONFINITE);
-      }
-    }
+  // (a block may end: its last remote store was before the barrier)
+  if (worst >= 0x7F800000u || !(total.hi > 0.0f && total.hi < INFINITY)) {
+    refuse(MOE_DEV_NONFINITE);
     return;
   }
   if (rank == 0) {
@@ -209,63 +269,69 @@ verify_draft_kernel(const DraftArgs a) {
   }
   // The block whose weights hold the aim, or (the aim rounded up to the total)
   // the last one that has any.
-  const double aim = static_cast<double>(u[a.T]) * total, mine = sh->total;
-  if (aim < total ? aim < before || !(aim < before + mine) : rank != last_rank) return;
-  // The segment: the first whose running sum passes the aim, else the last
-  // with any weight (all threads do the same).
-  double run = before, start = before;
-  int found = -1;
-  for (int s = 0; s < segs; ++s) {
-    const double v = sh->seg[s];
-    if (v > 0.0) {
-      found = s, start = run;
-      run += v;
-      if (run > aim) break;
+  const Pair aim = times(total, r);
+  if (above(total, aim) ? above(before, aim) || !above(mine, aim) : rank != last_rank) return;
+  // The segment: the first whose running sum is above the aim, else the last
+  // with any weight.
+  if (warp == 0) {
+    Pair run = before, start = before;
+    int found = -1;
+    for (int s0 = 0; s0 < segs; s0 += 32) {
+      const Pair v = s0 + lane < segs ? seg[s0 + lane] : Pair{0.0f, 0.0f};
+      Pair sum;
+      const Pair to = add(run, scan(v, lane, sum));
+      const unsigned some = __ballot_sync(0xFFFFFFFFu, v.hi > 0.0f);
+      const unsigned over = __ballot_sync(0xFFFFFFFFu, v.hi > 0.0f && above(to, aim));
+      if (some) {
+        const int l = over ? __ffs(over) - 1 : 31 - __clz(some);
+        found = s0 + l;
+        // the sum before it: up to the lane before
+        const Pair prev{__shfl_sync(0xFFFFFFFFu, to.hi, max(l - 1, 0)),
+                        __shfl_sync(0xFFFFFFFFu, to.lo, max(l - 1, 0))};
+        start = l > 0 ? prev : run;
+      }
+      if (over) break;
+      run = add(run, sum);
     }
+    if (lane == 0) sh->found = found, sh->start = start, sh->hit = INT32_MAX, sh->last = -1;
   }
-  if (found < 0) return;
-  // Its weights in order: four to a thread.
-  const int64_t j0 = static_cast<int64_t>(seg0 + found) * kSegment + tid * 4;
-  double w[4], sum = 0.0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = j0 + i < a.V ? row.weight(static_cast<int>(j0 + i)) : 0.0;
-    sum += w[i];
-  }
-  double incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double n = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-    if (lane >= o) incl += n;
-  }
-  if (lane == 31) sh->warp_sum[warp] = incl;
-  if (tid == 0) sh->stop = INT32_MAX, sh->positive = -1;
   __syncthreads();
-  double c = start;
-  for (int k = 0; k < warp; ++k) c += sh->warp_sum[k];
-  c += incl - sum;
-  int hit = INT32_MAX, last = -1;
+  if (sh->found < 0) return;
+  // Its weights in order: two to a thread.
+  const int64_t j0 = static_cast<int64_t>(seg0 + sh->found) * kSegment + tid * 2;
+  Pair w[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    c += w[i];
-    if (w[i] > 0.0) {
-      last = static_cast<int>(j0) + i;
-      if (c > aim && hit == INT32_MAX) hit = last;
+  for (int i = 0; i < 2; ++i)
+    w[i] = j0 + i < a.V ? weight(row.p[j0 + i], row.less(j0 + i)) : Pair{0.0f, 0.0f};
+  Pair sum;
+  const Pair both = add(w[0], w[1]);
+  Pair c = scan(both, lane, sum);
+  if (lane == 31) sh->warp_sum[warp] = c;
+  c = Pair{__shfl_up_sync(0xFFFFFFFFu, c.hi, 1), __shfl_up_sync(0xFFFFFFFFu, c.lo, 1)};
+  if (lane == 0) c = Pair{0.0f, 0.0f};
+  __syncthreads();
+  Pair base = sh->start;
+  for (int k = 0; k < warp; ++k) base = add(base, sh->warp_sum[k]);
+  c = add(base, c);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    c = add(c, w[i]);
+    if (w[i].hi > 0.0f) {
+      atomicMax(&sh->last, static_cast<int>(j0) + i);
+      if (above(c, aim)) atomicMin(&sh->hit, static_cast<int>(j0) + i);
     }
   }
-  if (hit != INT32_MAX) atomicMin(&sh->stop, hit);
-  if (last >= 0) atomicMax(&sh->positive, last);
   __syncthreads();
   // (sums in another order may end a rounding short of the aim)
-  if (tid == 0) out[stop] = sh->stop != INT32_MAX ? sh->stop : sh->positive;
+  if (tid == 0) out[stop] = sh->hit != INT32_MAX ? sh->hit : sh->last;
 }
 
 }  // namespace
 
 cudaError_t launch_verify_draft(const DraftArgs &a, cudaStream_t s) {
-  // (the segments' sums come first: no more of them than the rows have)
-  return launch_early(verify_draft_kernel, dim3(a.B * kCluster), kThreads, sizeof(DraftShared), s,
-                      a);
+  const int all = (a.V - 1) / kSegment + 1, per = (all + kCluster - 1) / kCluster;
+  return launch_early(verify_draft_kernel, dim3(a.B * kCluster), kThreads,
+                      sizeof(DraftShared) + per * sizeof(Pair), s, a);
 }
 
 }  // namespace moe
