@@ -1,6 +1,6 @@
 // draft.cu -- which tokens of a draft stand, and the one more after them.
 //
-// A cluster of 8 blocks takes a sequence.  Each finds the first token that is
+// A cluster of up to 8 blocks takes a sequence.  Each finds the first token that is
 // not accepted (u q < p as exact products in 64 bits); then the blocks share
 // out the row of V weights max(p - q, 0): their sums by segments of 512, the
 // total over the cluster, and the block whose segments hold r * total looks
@@ -17,6 +17,7 @@
 #include "attn.h"
 #include "common.cuh"
 #include "early.cuh"
+#include "kernels.h"
 
 namespace moe {
 
@@ -25,8 +26,9 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kCluster = 8;
+constexpr int kCluster = 8;  // at most
 constexpr int kSegment = 512;
+constexpr int kBlocks = 4;  // an SM
 
 // hi + lo, |lo| at most half a step of hi.
 struct Pair {
@@ -143,14 +145,15 @@ struct Segment {
   }
 };
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kBlocks)
 verify_draft_kernel(const DraftArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   DraftShared *sh = reinterpret_cast<DraftShared *>(smem);
   Pair *seg = reinterpret_cast<Pair *>(sh + 1);
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
-  const int b = blockIdx.x / kCluster;
+  const int cluster_size = static_cast<int>(cluster.num_blocks());
+  const int b = blockIdx.x / cluster_size;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   early_begin();
   const int32_t *drafted = a.draft_tokens + static_cast<int64_t>(b) * a.T;
@@ -206,7 +209,7 @@ verify_draft_kernel(const DraftArgs a) {
     else row.one = token;
   }
   const int all = static_cast<int>((static_cast<int64_t>(a.V) + kSegment - 1) / kSegment);
-  const int per = (all + kCluster - 1) / kCluster;
+  const int per = (all + cluster_size - 1) / cluster_size;
   const int seg0 = rank * per, segs = max(0, min(per, all - seg0));
   Pair total, before, mine;
   uint32_t worst = 0;
@@ -216,22 +219,19 @@ verify_draft_kernel(const DraftArgs a) {
         (reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) % 16 == 0;
     uint32_t bits = 0;
     Pair part{0.0f, 0.0f};  // of this warp's segments
-    Segment now, next;
-    if (warp < segs) now.load(row, static_cast<int64_t>(seg0 + warp) * kSegment, a.V, lane, aligned);
     for (int s = warp; s < segs; s += kWarps) {
-      if (s + kWarps < segs)
-        next.load(row, static_cast<int64_t>(seg0 + s + kWarps) * kSegment, a.V, lane, aligned);
+      Segment now;
+      now.load(row, static_cast<int64_t>(seg0 + s) * kSegment, a.V, lane, aligned);
       Pair v = now.sum(bits);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v = add(v, shuffle_xor(v, o));
       if (lane == 0) seg[s] = v;
       part = add(part, v);
-      now = next;
     }
     bits = __reduce_max_sync(0xFFFFFFFFu, bits);
     if (lane == 0) sh->warp_worst[warp] = bits, sh->warp_sum[warp] = part;
     __syncthreads();
-    if (tid < kCluster) {  // every block hears of every other's
+    if (tid < cluster_size) {  // every block hears of every other's
       Pair t = sh->warp_sum[0];
       uint32_t x = sh->warp_worst[0];
       for (int k = 1; k < kWarps; ++k) {
@@ -244,7 +244,7 @@ verify_draft_kernel(const DraftArgs a) {
     }
     cluster.sync();
     total = before = Pair{0.0f, 0.0f};
-    for (int k = 0; k < kCluster; ++k) {
+    for (int k = 0; k < cluster_size; ++k) {
       const Pair t = sh->totals[k];
       if (k == rank) before = total;
       total = add(total, t);
@@ -329,9 +329,30 @@ verify_draft_kernel(const DraftArgs a) {
 }  // namespace
 
 cudaError_t launch_verify_draft(const DraftArgs &a, cudaStream_t s) {
-  const int all = (a.V - 1) / kSegment + 1, per = (all + kCluster - 1) / kCluster;
-  return launch_early(verify_draft_kernel, dim3(a.B * kCluster), kThreads,
-                      sizeof(DraftShared) + per * sizeof(Pair), s, a);
+  // As many blocks a sequence as all run at once (128 sequences in clusters of 4
+  // take 36.6 us, of 8 in two rounds 38.1), as far as a block has room for its
+  // segments' sums.
+  const int64_t room = static_cast<int64_t>(tc_sm_count()) * kBlocks;
+  const int all = (a.V - 1) / kSegment + 1;
+  const auto smem_of = [&](int c) { return sizeof(DraftShared) + (all + c - 1) / c * sizeof(Pair); };
+  int cluster = kCluster;
+  while (cluster > 1 && a.B * static_cast<int64_t>(cluster) > room &&
+         smem_of(cluster / 2) <= 48 * 1024)
+    cluster /= 2;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_of(cluster);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, verify_draft_kernel, a);
 }
 
 }  // namespace moe

@@ -65,6 +65,19 @@ def test_random(env, v, t):
     check(env, p, None, d, u)
 
 
+@pytest.mark.parametrize("b", [77, 150, 301, 700])
+def test_many_sequences(env, b):
+    """As many blocks a sequence as the GPU has room for, down to one."""
+    p, q, d, u = distributions(env, b, 2, 5000, b)
+    check(env, p, q, d, u)
+    check(env, p, None, d, u)
+
+
+def test_the_widest_row(env):
+    p, q, d, u = distributions(env, 1, 1, 1 << 24, 3)
+    check(env, p, q, d, u)
+
+
 def test_long_drafts(env):
     p, q, d, u = distributions(env, 6, 90, 300, 5, noise=0.05)
     u *= 0.6
