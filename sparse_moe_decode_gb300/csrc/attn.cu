@@ -130,7 +130,7 @@ struct Layout {
 Layout layout(const moe_attn_dims &d) {
   // both kernels' parts: 2 a block
   const size_t tc = 2 * kTcMaxCtas * (d.head_dim == 256 ? 128 : 256);
-  size_t rows = 2 * kStreamMaxCtas * kStreamMaxRows;
+  size_t rows = 2 * kStreamMaxCtas * kStreamRows;
   if (tc > rows) rows = tc;
   Layout l;
   l.open = 256;
@@ -202,19 +202,18 @@ cudaError_t launch_attention(const moe_attn_dims &d, const moe_kv_cache &c, cons
   const auto tc = d.kv_type == MOE_KV_BF16   ? launch_tc_bf16
                   : d.kv_type == MOE_KV_INT8 ? launch_tc_int8
                                              : launch_tc_e4m3;
-  // Sequences of up to `few` rows stream; the others go to the tensor cores'
-  // kernel.  Lengths that only the device knows: both kernels look.
+  // Sequences of up to 16 rows stream; the others go to the tensor cores' kernel
+  // (8 sequences of 4 tokens, 32 rows each, take MEASUREDTC us there and 37 us
+  // streaming).  Lengths that only the device knows: both kernels look.
   const int64_t most = static_cast<int64_t>(a.cu ? a.N : a.T) * a.group;
-  const int few = a.cu ? (a.group <= 16 ? 16 : a.group <= 32 ? 32 : 64) : 64;
   cudaError_t e = cudaSuccess;
-  if (a.cu || most <= few) {
-    const int rows = static_cast<int>(most < few ? most : few);
-    x.range.least = 0, x.range.most = few;
+  if ((a.cu && a.group <= kStreamRows) || most <= kStreamRows) {
+    x.range.least = 0, x.range.most = kStreamRows;
     x.args.least_share = 2;
-    e = stream(x, d.head_dim, rows <= 16 ? 1 : rows <= 32 ? 2 : 4);
+    e = stream(x, d.head_dim);
   }
-  if (e == cudaSuccess && most > few) {
-    x.range.least = few, x.range.most = INT32_MAX;
+  if (e == cudaSuccess && most > kStreamRows) {
+    x.range.least = kStreamRows, x.range.most = INT32_MAX;
     x.args.least_share = 1;
     e = tc(x, d.head_dim);
   }

@@ -11,8 +11,8 @@ namespace moe {
 
 constexpr int kAttnMaxGroup = 64;  // query heads of a key/value head
 // Blocks of an attention kernel: what the workspace has room for.
-constexpr int kStreamMaxCtas = 320;
-constexpr int kStreamMaxRows = 64;  // rows (token, head of a group) of a block
+constexpr int kStreamMaxCtas = 480;
+constexpr int kStreamRows = 16;  // rows (token, head of a group) of a tile
 constexpr int kTcMaxCtas = 160;     // one an SM; 256 rows, 128 with a head_dim of 256
 
 // A batch as the kernels take it.

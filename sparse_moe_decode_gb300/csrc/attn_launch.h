@@ -30,9 +30,9 @@ cudaError_t launch_tc_bf16(const AttnLaunch &x, int d);
 cudaError_t launch_tc_int8(const AttnLaunch &x, int d);
 cudaError_t launch_tc_e4m3(const AttnLaunch &x, int d);
 
-cudaError_t launch_stream_bf16(const AttnLaunch &x, int d, int wr);
-cudaError_t launch_stream_int8(const AttnLaunch &x, int d, int wr);
-cudaError_t launch_stream_e4m3(const AttnLaunch &x, int d, int wr);
+cudaError_t launch_stream_bf16(const AttnLaunch &x, int d);
+cudaError_t launch_stream_int8(const AttnLaunch &x, int d);
+cudaError_t launch_stream_e4m3(const AttnLaunch &x, int d);
 
 // Joins the tiles that the `blocks` blocks of the kernel before it left apart.
 cudaError_t launch_attn_combine(const AttnBatch &a, const AttnArgs &p, int d, int blocks,

@@ -1,21 +1,26 @@
-// attn_stream.cuh -- attention of few rows (single tokens, drafts) over long
-// contexts: the cache streams through, bound by its bytes.
+// attn_stream.cuh -- attention of few rows (single tokens, short drafts) over
+// long contexts: the cache streams through, bound by its bytes.
 //
-// out = softmax(scale q k^T) v for a tile of R = 16 WR rows, in one pass over
-// the keys with the running maximum m and total l of the softmax.  A block has
-// four warps that compute, and one that fetches: WR of them take 16 rows each,
-// WK = 4 / WR share out the 64 keys of a key tile among themselves (so that
-// with up to 16 rows no key is read twice from shared memory).  Each keeps its
-// own m, l and sums; they are joined when the segment ends.  K and V tiles
-// come through a ring of shared-memory slots (TMA, 128-byte swizzle, one box a
-// page); products are mma.sync m16n8k16 with fp32 sums.
+// out = softmax(scale q k^T) v for a tile of 16 rows, in one pass over the keys
+// with the running maximum m and total l of the softmax.  A block has four
+// warps that compute, and one that fetches.  Of the 64 keys of a key tile each
+// warp takes 16 for the scores, and then a quarter of the columns for the
+// values; the weights pass between them as operand fragments in shared memory,
+// one barrier a tile.  No key is read twice, and a warp's sums are 16 rows of
+// head_dim / 4 columns in registers, finished where they are (with the keys
+// shared out for the values as well, four times the registers, and joining the
+// warps' sums took 1.2 to 3.1 us a segment).  K and V tiles come through a ring
+// of shared-memory slots (TMA, 128-byte swizzle, one box a page); products are
+// mma.sync m16n8k16 with fp32 sums.
+//
+// m is that of the tiles before, which nearly always does; only where a weight
+// comes out above 2^13 or so do the warps find the maximum anew.
 //
 // 8-bit codes are made fp16 in registers, exactly; q then takes a power of two
 // a row (fp16 keeps all of bf16's digits within 2^-28 of the row's largest).
 // A key's scale multiplies its column of q k^T; a value's scale multiplies its
 // weight, and the products t = p s_v enter as fp16 under a power of two a row
-// that follows their running maximum, so that they keep 11 digits whatever the
-// scales are.
+// that follows the largest, so that they keep 11 digits whatever the scales are.
 #pragma once
 
 #include <cuda.h>
@@ -30,34 +35,27 @@ namespace moe {
 
 constexpr int kStreamTileCost = 1;  // beginning and ending a tile, in key tiles
 
-template <int D, int KV, int WR>
+template <int D, int KV>
 struct StreamShape {
-  static constexpr int kWK = 4 / WR, kR = 16 * WR, kKT = 64, kNK = kKT / kWK;
+  static constexpr int kR = kStreamRows, kKT = 64, kWarps = 4;
   static constexpr bool kBytes = KV != MOE_KV_BF16;  // 8-bit codes
   static constexpr int kRow = D * (kBytes ? 1 : 2);  // bytes of a cached row
-  static constexpr int kTile = kKT * kRow;
+  static constexpr int kTile = kKT * kRow, kSlot = kTile + (kBytes ? 256 : 0);
   static constexpr int kSteps = D / 16;
   static constexpr int kThreads = 160;
-  // the rows' fragments of q; reused when the warps' sums are joined
-  static constexpr int kQ = kR * D * 2;
-  static constexpr int kJoinCols = kQ >= 64 * 64 * 4 ? 64 : 32;  // at a time
-  static constexpr int kJoin = kWK == 1 ? 0 : 64 * kJoinCols * 4;
-  static constexpr int kQArea = kQ > kJoin ? kQ : kJoin;
-  // two blocks an SM where that leaves three slots, else one
-  static constexpr int kFixed = kQArea + 2048;  // + barriers, m and l, the share
-  static constexpr int kHalf = (233472 / 2 - 1024 - kFixed) / (kTile + 256);
-  static constexpr int kWhole = (232448 - kFixed) / (kTile + 256);
-  static constexpr int kBlocks = kHalf >= 3 ? 2 : 1;
-  static constexpr int kFit = kBlocks == 2 ? kHalf : kWhole;
+  static constexpr int kQ = kR * D * 2, kP = 2 * kWarps * 512;  // fragments of q, of the weights
+  static constexpr int kFixed = kQ + kP + 2048;                 // + barriers, maxima, the share
+  static constexpr int kBlocks = kTile > 16384 ? 2 : 3;         // an SM
+  static constexpr int kFit = (233472 / kBlocks - 1024 - kFixed) / kSlot;
   static constexpr int kSlots = kFit > 12 ? 12 : kFit;
-  static constexpr int kSmem = kFixed + kSlots * (kTile + 256);
+  static constexpr int kSmem = kFixed + kSlots * kSlot;
   static_assert(kSlots >= 3, "ring");
 };
 
-struct StreamSmem {  // behind the slots, their scales and the q area
+struct StreamSmem {  // behind the slots, their scales, q and the weights
   uint64_t full[12], empty[12];
   AttnShare share;
-  float m[64], l[64], qmax[64];
+  float top[4][kStreamRows], most[4][kStreamRows], l[4][kStreamRows];
   int abort;
 };
 static_assert(sizeof(StreamSmem) <= 2048, "shared memory");
@@ -94,18 +92,31 @@ __device__ __forceinline__ void attn_mma(float (&c)[4], const uint32_t (&a)[4], 
     mma16(c, a, b0, b1);
 }
 
-template <int D, int KV, int WR>
-__global__ void __launch_bounds__(160, (StreamShape<D, KV, WR>::kBlocks))
+// All compute warps meet; whether any thread says so.
+__device__ __forceinline__ bool meet_any(bool mine) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(mine ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+template <int D, int KV>
+__global__ void __launch_bounds__(160, (StreamShape<D, KV>::kBlocks))
 attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const AttnBatch a, const AttnRange range,
                    const AttnArgs p) {
-  using S = StreamShape<D, KV, WR>;
-  constexpr int kSlots = S::kSlots, kWK = S::kWK, R = S::kR, kNK = S::kNK, kSteps = S::kSteps;
+  using S = StreamShape<D, KV>;
+  constexpr int kSlots = S::kSlots, R = S::kR, kSteps = S::kSteps;
   constexpr bool kBytes = S::kBytes;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *q_area = smem + kSlots * S::kTile;
-  float *scales = reinterpret_cast<float *>(q_area + S::kQArea);
-  StreamSmem *sh = reinterpret_cast<StreamSmem *>(scales + kSlots * 64);
+  uint4 *qf = reinterpret_cast<uint4 *>(smem + kSlots * S::kTile);
+  uint4 *weights = qf + S::kQ / 16;  // [2][4 warps' keys][32 lanes]
+  float *scales = reinterpret_cast<float *>(weights + S::kP / 16);
+  StreamSmem *sh = reinterpret_cast<StreamSmem *>(scales + (kBytes ? kSlots * 64 : 0));
   volatile int *abort = &sh->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -196,42 +207,38 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
 
   // ------------------------------------------------------------- compute
-  const int wr = warp / kWK, wk = warp % kWK;
+  constexpr int kCols = D / 4;                   // of this warp
   const int g = lane >> 2, c = lane & 3;
-  uint4 *qf = reinterpret_cast<uint4 *>(q_area) + wr * kSteps * 32;
-  float *join = reinterpret_cast<float *>(q_area);
   uint32_t n = 0;
   const uint32_t smem_at = ptx::smem_u32(smem);
   // ldmatrix rows: lane l gives row l % 8 of block l / 8
   const int row_k = (lane & 7) + (kBytes ? ((lane >> 3) & 1) : (lane >> 4)) * 8;
   const int col_k = kBytes ? lane >> 4 : (lane >> 3) & 1;
-  const int row_v = (lane & 7) + ((lane >> 3) & 1) * 8, col_v = lane >> 4;
+  const int row_v = (lane & 7) + ((lane >> 3) & 1) * 8;
 
   while (w.next(a, range)) {
     const int row0 = w.cur * R;
     const int rows = min(w.t.rows - row0, R);
     const int ctx = w.t.ctx;
     // this thread's two rows
-    int pos[2];
+    int pos[2], out_row[2];
     float factor[2];
-    bool live[2];
     {
       const moe_bf16 *src[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = wr * 16 + g + 8 * i;
-        live[i] = r < rows;
-        const int at = row0 + (live[i] ? r : rows - 1);
-        const int token = at / a.group, h = at % a.group;
+        const int at = row0 + min(g + 8 * i, rows - 1);
+        const int token = at / a.group, h = w.head * a.group + at % a.group;
         pos[i] = ctx + token;
-        src[i] = p.q + (w.s.start + token) * p.q_ld + (w.head * a.group + h) * D;
+        src[i] = p.q + (w.s.start + token) * p.q_ld + h * D;
+        out_row[i] = h;
         factor[i] = p.scale_log2;
       }
-      constexpr int kMine = (kSteps + kWK - 1) / kWK;
+      constexpr int kMine = kSteps / 4;
       uint4 f[kMine];
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
-        const int ks = j * kWK + wk;
+        const int ks = j * 4 + warp;
         if (kBytes) {
           const uint2 x = *reinterpret_cast<const uint2 *>(src[0] + ks * 16 + 4 * c);
           const uint2 y = *reinterpret_cast<const uint2 *>(src[1] + ks * 16 + 4 * c);
@@ -243,7 +250,6 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
           f[j] = make_uint4(ld(0, 0), ld(1, 0), ld(0, 8), ld(1, 8));
         }
       }
-      ptx::named_barrier(1, 128);  // the q area and the maxima are free
       if (kBytes) {
         float top[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -257,18 +263,13 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
         for (int i = 0; i < 2; ++i) {
           top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
           top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
-          if (c == 0) sh->qmax[wk * R + wr * 16 + g + 8 * i] = top[i];
+          if (c == 0) sh->top[warp][g + 8 * i] = top[i];
         }
-        if (kWK > 1) {
-          ptx::named_barrier(1, 128);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            for (int k = 0; k < kWK; ++k)
-              top[i] = fmaxf(top[i], sh->qmax[k * R + wr * 16 + g + 8 * i]);
-        }
+        ptx::named_barrier(1, 128);
         float mult[2], inv;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          for (int k = 0; k < 4; ++k) top[i] = fmaxf(top[i], sh->top[k][g + 8 * i]);
           pow2_scale(top[i], mult[i], inv);
           factor[i] *= inv;
         }
@@ -281,218 +282,261 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
                             half(f[j].w, mult[1]));
         }
       }
+      // (the fragments of the segment before have been read: the warps have met
+      // since)
 #pragma unroll
-      for (int j = 0; j < kMine; ++j) qf[(j * kWK + wk) * 32 + lane] = f[j];
+      for (int j = 0; j < kMine; ++j) qf[(j * 4 + warp) * 32 + lane] = f[j];
       ptx::named_barrier(1, 128);
     }
     const int first_pos = ctx + row0 / a.group;
     const int last_pos = ctx + (row0 + rows - 1) / a.group;
 
-    float o[D / 8][4];
+    float o[kCols / 8][4];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    for (int i = 0; i < kCols / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    float ref[2] = {0x1p-110f, 0x1p-110f};  // (8-bit) powers of two: o's sums times ref / 2^13
+    float ref[2] = {0x1p-110f, 0x1p-110f};  // (8-bit) powers of two: o's sums times ref / 2^7
 
     bool ok = true;
     for (int kt = w.k0; kt < w.k1; ++kt, n += 2) {
-      const int key0 = kt * 64 + wk * kNK;
-      const bool active = key0 <= last_pos &&
-                          (!a.window || key0 + kNK > first_pos - a.window + 1);
-      float s[kNK / 8][4];
-      {
-        const uint32_t slot = n % kSlots;
-        if (!(ok = ptx::mbar_wait(&sh->full[slot], (n / kSlots) & 1, abort, p.budget))) break;
-        if (active) {
-          const uint32_t tile = smem_at + slot * S::kTile;
+      const int key0 = kt * 64 + warp * 16;
+      const uint32_t k_slot = n % kSlots, v_slot = (n + 1) % kSlots;
+      // (after a wait that gave up, every wait does so at once: the warps go on
+      // meeting at their barriers to the end)
+      ok = ptx::mbar_wait(&sh->full[k_slot], (n / kSlots) & 1, abort, p.budget) && ok;
+      float s[2][4];
 #pragma unroll
-          for (int i = 0; i < kNK / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+      for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = -INFINITY;
+      if (key0 <= last_pos && (!a.window || key0 + 16 > first_pos - a.window + 1)) {
+        const uint32_t tile = smem_at + k_slot * S::kTile;
+        const TileRows<S::kRow> rows16(warp * 16, box);
+        // two sums each, so that a product does not wait for the one before it
+        float t[2][4];
 #pragma unroll
-          for (int k16 = 0; k16 < kNK / 16; ++k16) {
-            const TileRows<S::kRow> rows16(wk * kNK + k16 * 16, box);
-#pragma unroll
-            for (int ks = 0; ks < kSteps; ks += kBytes ? 2 : 1) {
-              uint32_t b[4];
-              if (kBytes) {
-                ldsm4(b, tile + rows16.at(row_k, ks + col_k));
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint4 qv = qf[(ks + h) * 32 + lane];
-                  const uint32_t av[4] = {qv.x, qv.y, qv.z, qv.w};
-#pragma unroll
-                  for (int i = 0; i < 2; ++i) {
-                    uint32_t lo, hi;
-                    codes_to_f16x2<KV>(b[2 * h + i], lo, hi);
-                    attn_mma<KV>(s[2 * k16 + i], av, lo, hi);
-                  }
-                }
-              } else {
-                ldsm4(b, tile + rows16.at(row_k, 2 * ks + col_k));
-                const uint4 qv = qf[ks * 32 + lane];
-                const uint32_t av[4] = {qv.x, qv.y, qv.z, qv.w};
-                attn_mma<KV>(s[2 * k16], av, b[0], b[1]);
-                attn_mma<KV>(s[2 * k16 + 1], av, b[2], b[3]);
-              }
-            }
-          }
-          if (kBytes) {
-            const float *ksc = scales + slot * 64 + wk * kNK + 2 * c;
-#pragma unroll
-            for (int i = 0; i < kNK / 8; ++i) {
-              const float2 f = *reinterpret_cast<const float2 *>(ksc + 8 * i);
-              s[i][0] *= factor[0] * f.x, s[i][1] *= factor[0] * f.y;
-              s[i][2] *= factor[1] * f.x, s[i][3] *= factor[1] * f.y;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < kNK / 8; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) s[i][j] *= factor[0];
-          }
+        for (int i = 0; i < 2; ++i) {
+          s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+          t[i][0] = t[i][1] = t[i][2] = t[i][3] = 0.0f;
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh->empty[slot]);
-      }
-      const bool edge = key0 + kNK > first_pos + 1 ||
-                        (a.window && key0 <= last_pos - a.window);
-      const uint32_t slot = (n + 1) % kSlots;
-      uint32_t pf[kNK / 16][4];
-      if (active) {
-        if (edge) {
 #pragma unroll
-          for (int i = 0; i < kNK / 8; ++i)
+        for (int ks = 0; ks < kSteps; ks += 2) {
+          uint32_t b[8];
+          if (kBytes) {
+            uint32_t x[4];
+            ldsm4(x, tile + rows16.at(row_k, ks + col_k));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) codes_to_f16x2<KV>(x[i], b[2 * i], b[2 * i + 1]);
+          } else {
+            uint32_t x[4], y[4];
+            ldsm4(x, tile + rows16.at(row_k, 2 * ks + col_k));
+            ldsm4(y, tile + rows16.at(row_k, 2 * ks + 2 + col_k));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = x[i], b[4 + i] = y[i];
+          }
+          const uint4 q0 = qf[ks * 32 + lane], q1 = qf[(ks + 1) * 32 + lane];
+          const uint32_t a0[4] = {q0.x, q0.y, q0.z, q0.w}, a1[4] = {q1.x, q1.y, q1.z, q1.w};
+          attn_mma<KV>(s[0], a0, b[0], b[1]);
+          attn_mma<KV>(s[1], a0, b[2], b[3]);
+          attn_mma<KV>(t[0], a1, b[4], b[5]);
+          attn_mma<KV>(t[1], a1, b[6], b[7]);
+        }
+        const float *ksc = scales + k_slot * 64 + warp * 16 + 2 * c;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 f = kBytes ? *reinterpret_cast<const float2 *>(ksc + 8 * i)
+                                  : make_float2(1.0f, 1.0f);
+          s[i][0] = (s[i][0] + t[i][0]) * (factor[0] * f.x);
+          s[i][1] = (s[i][1] + t[i][1]) * (factor[0] * f.y);
+          s[i][2] = (s[i][2] + t[i][2]) * (factor[1] * f.x);
+          s[i][3] = (s[i][3] + t[i][3]) * (factor[1] * f.y);
+        }
+        if (key0 + 16 > first_pos + 1 || (a.window && key0 <= last_pos - a.window)) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int key = key0 + 8 * i + 2 * c + (j & 1), ps = pos[j >> 1];
               if (key > ps || (a.window && key <= ps - a.window)) s[i][j] = -INFINITY;
             }
         }
-        float top[2] = {-INFINITY, -INFINITY}, alpha[2], base[2];
-#pragma unroll
-        for (int i = 0; i < kNK / 8; ++i) {
-          top[0] = fmaxf(top[0], fmaxf(s[i][0], s[i][1]));
-          top[1] = fmaxf(top[1], fmaxf(s[i][2], s[i][3]));
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
-          top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
-          top[i] = fmaxf(top[i], m[i]);
-          base[i] = top[i] == -INFINITY ? 0.0f : top[i];
-          alpha[i] = attn_exp2(m[i] - base[i]);
-          m[i] = top[i];
-          l[i] *= alpha[i];
-        }
-#pragma unroll
-        for (int i = 0; i < kNK / 8; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[i][j] = attn_exp2(s[i][j] - base[j >> 1]);
-            l[j >> 1] += s[i][j];
-          }
-        if (!kBytes) {
-#pragma unroll
-          for (int i = 0; i < kNK / 16; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              pf[i][j] = bf16x2(s[2 * i + (j >> 1)][2 * (j & 1)], s[2 * i + (j >> 1)][2 * (j & 1) + 1]);
-        }
-        if (!(ok = ptx::mbar_wait(&sh->full[slot], ((n + 1) / kSlots) & 1, abort, p.budget))) break;
-        if (kBytes) {
-          const float *vsc = scales + slot * 64 + wk * kNK + 2 * c;
-          float most[2] = {0.0f, 0.0f};
-#pragma unroll
-          for (int i = 0; i < kNK / 8; ++i) {
-            const float2 f = *reinterpret_cast<const float2 *>(vsc + 8 * i);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              // a hidden key's weight is 0 whatever its scale
-              s[i][j] = s[i][j] == 0.0f ? 0.0f : s[i][j] * ((j & 1) ? f.y : f.x);
-              most[j >> 1] = fmaxf(most[j >> 1], s[i][j]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            most[i] = fmaxf(most[i], __shfl_xor_sync(0xFFFFFFFFu, most[i], 1));
-            most[i] = fmaxf(most[i], __shfl_xor_sync(0xFFFFFFFFu, most[i], 2));
-            const float up = pow2_floor(fmaxf(ref[i] * alpha[i], most[i]));
-            const float inv = pow2_inverse(up);
-            alpha[i] = alpha[i] * ref[i] * inv;  // (in this order: at most 2)
-            ref[i] = up;
-            base[i] = inv * 0x1p13f;
-          }
-#pragma unroll
-          for (int i = 0; i < kNK / 16; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float f = base[j & 1];
-              pf[i][j] = h2_bits(__floats2half2_rn(s[2 * i + (j >> 1)][2 * (j & 1)] * f,
-                                                   s[2 * i + (j >> 1)][2 * (j & 1) + 1] * f));
-            }
-        }
-        if (__any_sync(0xFFFFFFFFu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[i][0] *= alpha[0], o[i][1] *= alpha[0];
-            o[i][2] *= alpha[1], o[i][3] *= alpha[1];
-          }
-        }
-        // Behind the last position the slot holds what was there before: 0 in
-        // place of values that may not be finite.
-        const bool tail = KV != MOE_KV_INT8 && key0 + kNK > w.s.len;
-        const uint32_t tile = smem_at + slot * S::kTile;
-#pragma unroll
-        for (int k16 = 0; k16 < kNK / 16; ++k16) {
-          const TileRows<S::kRow> rows16(wk * kNK + k16 * 16, box);
-          uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // of keys 2c, 2c + 1; 8 on
-          if (tail) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int over = w.s.len - (key0 + k16 * 16 + 8 * h + 2 * c);  // keys there
-              keep[h] = over >= 2 ? 0xFFFFFFFFu : over == 1 ? 0x0000FFFFu : 0u;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < D / (kBytes ? 32 : 16); ++j) {
-            uint32_t b[4];
-            ldsm4_t(b, tile + rows16.at(row_v, 2 * j + col_v));
-            if (tail) b[0] &= keep[0], b[1] &= keep[1], b[2] &= keep[0], b[3] &= keep[1];
-            if (kBytes) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                // b[2h]: keys 2c, 2c + 1 of columns 2g, 2g + 1
-                uint32_t e0, o0, e1, o1;
-                codes_to_f16x2_apart<KV>(b[2 * h], e0, o0);
-                codes_to_f16x2_apart<KV>(b[2 * h + 1], e1, o1);
-                attn_mma<KV>(o[4 * j + 2 * h], pf[k16], e0, e1);
-                attn_mma<KV>(o[4 * j + 2 * h + 1], pf[k16], o0, o1);
-              }
-            } else {
-              attn_mma<KV>(o[2 * j], pf[k16], b[0], b[1]);
-              attn_mma<KV>(o[2 * j + 1], pf[k16], b[2], b[3]);
-            }
-          }
-        }
-      } else {
-        if (!(ok = ptx::mbar_wait(&sh->full[slot], ((n + 1) / kSlots) & 1, abort, p.budget))) break;
       }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh->empty[slot]);
+      if (lane == 0) ptx::mbar_arrive(&sh->empty[k_slot]);
+      float2 vs[2];
+      if (kBytes) {
+        ok = ptx::mbar_wait(&sh->full[v_slot], ((n + 1) / kSlots) & 1, abort, p.budget) && ok;
+        const float *vsc = scales + v_slot * 64 + warp * 16 + 2 * c;
+        vs[0] = *reinterpret_cast<const float2 *>(vsc);
+        vs[1] = *reinterpret_cast<const float2 *>(vsc + 8);
+      }
+
+      float e[2][4], sum[2], most[2];  // the weights
+      // under m and ref; `most`: the largest with their scales (8-bit)
+      const auto form = [&]() {
+        sum[0] = sum[1] = most[0] = most[1] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            e[i][j] = attn_exp2(s[i][j] - (m[j >> 1] == -INFINITY ? 0.0f : m[j >> 1]));
+            sum[j >> 1] += e[i][j];
+            if (kBytes) {
+              // a hidden key's weight is 0 whatever its scale
+              e[i][j] = e[i][j] == 0.0f ? 0.0f : e[i][j] * ((j & 1) ? vs[i].y : vs[i].x);
+              most[j >> 1] = fmaxf(most[j >> 1], e[i][j]);
+            }
+          }
+      };
+      const auto hand_over = [&]() {
+        uint4 f;
+        if (kBytes) {
+          const float f0 = pow2_inverse(ref[0]) * 0x1p7f, f1 = pow2_inverse(ref[1]) * 0x1p7f;
+          f.x = h2_bits(__floats2half2_rn(e[0][0] * f0, e[0][1] * f0));
+          f.y = h2_bits(__floats2half2_rn(e[0][2] * f1, e[0][3] * f1));
+          f.z = h2_bits(__floats2half2_rn(e[1][0] * f0, e[1][1] * f0));
+          f.w = h2_bits(__floats2half2_rn(e[1][2] * f1, e[1][3] * f1));
+        } else {
+          f = make_uint4(bf16x2(e[0][0], e[0][1]), bf16x2(e[0][2], e[0][3]),
+                         bf16x2(e[1][0], e[1][1]), bf16x2(e[1][2], e[1][3]));
+        }
+        weights[((kt & 1) * 4 + warp) * 32 + lane] = f;
+      };
+      // The largest of the four warps' (and the four lanes' of a row) values.
+      const auto over_warps = [&](float (&x)[2], float (*shared)[kStreamRows]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          x[i] = fmaxf(x[i], __shfl_xor_sync(0xFFFFFFFFu, x[i], 1));
+          x[i] = fmaxf(x[i], __shfl_xor_sync(0xFFFFFFFFu, x[i], 2));
+          if (c == 0) shared[warp][g + 8 * i] = x[i];
+        }
+        ptx::named_barrier(1, 128);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          for (int k = 0; k < 4; ++k) x[i] = fmaxf(x[i], shared[k][g + 8 * i]);
+      };
+      bool again = true;
+      if (kt > w.k0) {
+        form();
+        hand_over();
+        bool far = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          far |= sum[i] > 0x1p15f;
+          if (kBytes) far |= most[i] >= 256.0f * ref[i] && ref[i] < 0x1p126f;
+          // (nothing seen so far)
+          far |= m[i] == -INFINITY && fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]),
+                                            fmaxf(s[1][2 * i], s[1][2 * i + 1])) > -INFINITY;
+        }
+        again = meet_any(far);
+      }
+      if (again) {  // (all warps)
+        float top[2], alpha[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          top[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+        over_warps(top, sh->top);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          alpha[i] = 1.0f;
+          if (top[i] > m[i]) {
+            // (by a whole power of two: o's factor is exact)
+            const float up = m[i] == -INFINITY ? top[i] : m[i] + ceilf(top[i] - m[i]);
+            alpha[i] = attn_exp2(m[i] - up);
+            m[i] = up;
+          }
+          l[i] *= alpha[i];
+        }
+        form();
+        if (kBytes) {
+          float all[2] = {most[0], most[1]};
+          over_warps(all, sh->most);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float now = ref[i] * alpha[i];
+            ref[i] = all[i] >= 256.0f * now || kt == w.k0 ? pow2_floor(all[i]) : fmaxf(now, 0x1p-110f);
+            alpha[i] = now * pow2_inverse(ref[i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kCols / 8; ++i) {
+          o[i][0] *= alpha[0], o[i][1] *= alpha[0];
+          o[i][2] *= alpha[1], o[i][3] *= alpha[1];
+        }
+        hand_over();
+        ptx::named_barrier(1, 128);
+      }
+      l[0] += sum[0], l[1] += sum[1];
+      if (!kBytes)
+        ok = ptx::mbar_wait(&sh->full[v_slot], ((n + 1) / kSlots) & 1, abort, p.budget) && ok;
+      // Behind the last position the slot holds what was there before: 0 in place
+      // of values that may not be finite.
+      const bool tail = KV != MOE_KV_INT8 && kt * 64 + 64 > w.s.len;
+      const uint32_t tile = smem_at + v_slot * S::kTile;
+      const auto keep_of = [&](int key) {  // of keys key + 2c, + 1
+        const int over = w.s.len - (key + 2 * c);
+        return over >= 2 ? 0xFFFFFFFFu : over == 1 ? 0x0000FFFFu : 0u;
+      };
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {  // 32 keys
+        uint32_t wf[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 x = weights[((kt & 1) * 4 + k + h) * 32 + lane];
+          wf[h][0] = x.x, wf[h][1] = x.y, wf[h][2] = x.z, wf[h][3] = x.w;
+        }
+        if (kBytes) {
+          const TileRows<S::kRow> rows16(16 * k + (lane >> 4) * 16, box);
+#pragma unroll
+          for (int j = 0; j < kCols / 16; ++j) {
+            uint32_t b[4];  // keys 0-7, 8-15, 16-23, 24-31
+            ldsm4_t(b, tile + rows16.at(row_v, warp * (kCols / 16) + j));
+            if (tail) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) b[i] &= keep_of(kt * 64 + 16 * k + 8 * i);
+            }
+            uint32_t ev[4], od[4];  // of columns 2g, 2g + 1
+#pragma unroll
+            for (int i = 0; i < 4; ++i) codes_to_f16x2_apart<KV>(b[i], ev[i], od[i]);
+            attn_mma<KV>(o[2 * j], wf[0], ev[0], ev[1]);
+            attn_mma<KV>(o[2 * j + 1], wf[0], od[0], od[1]);
+            attn_mma<KV>(o[2 * j], wf[1], ev[2], ev[3]);
+            attn_mma<KV>(o[2 * j + 1], wf[1], od[2], od[3]);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const TileRows<S::kRow> rows16(16 * (k + h), box);
+#pragma unroll
+            for (int j = 0; j < kCols / 16; ++j) {
+              uint32_t b[4];
+              ldsm4_t(b, tile + rows16.at(row_v, warp * (kCols / 8) + 2 * j + (lane >> 4)));
+              if (tail) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i] &= keep_of(kt * 64 + 16 * (k + h) + 8 * (i & 1));
+              }
+              attn_mma<KV>(o[2 * j], wf[h], b[0], b[1]);
+              attn_mma<KV>(o[2 * j + 1], wf[h], b[2], b[3]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh->empty[v_slot]);
     }
-    // (a wait that gave up: every wait from here on does so at once, and the
-    // block still meets at its barriers)
     if (!ok && lane == 0) set_status(a.status, MOE_DEV_TIMEOUT);
 
     // ------------------------------------------------- the segment's end
+    float total[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
       l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-      if (kBytes) {
-        const float f = ref[i] * 0x1p-13f;
+      if (c == 0) sh->l[warp][g + 8 * i] = l[i];
+    }
+    ptx::named_barrier(1, 128);
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) o[j][2 * i] *= f, o[j][2 * i + 1] *= f;
-      }
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i;
+      total[i] = (sh->l[0][r] + sh->l[1][r]) + (sh->l[2][r] + sh->l[3][r]);
     }
     const bool whole = w.begins && w.ends;
     const int part = 2 * blockIdx.x + (w.begins ? 1 : 0);
@@ -502,105 +546,32 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
       d.rows = rows, d.start = w.s.start, d.row0 = row0, d.head = w.head;
       p.parts.open[blockIdx.x] = d;
     }
-    const auto out_at = [&](int r) {  // row r of the tile
-      const int token = (row0 + r) / a.group, h = (row0 + r) % a.group;
-      return p.out + (w.s.start + token) * p.out_ld + (w.head * a.group + h) * D;
-    };
-    const auto part_at = [&](int r, int d) { return p.parts.at(part, D, d, r); };
-    float2 *part_ml = p.parts.ml + static_cast<int64_t>(part) * p.parts.rows;
-    if (kWK == 1) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = wr * 16 + g + 8 * i;
-        if (!live[i]) continue;
-        const float f = whole ? 1.0f / l[i] : 1.0f;
-        moe_bf16 *dst = out_at(r);
-        if (!whole && c == 0) part_ml[r] = make_float2(m[i], l[i]);
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i;
+      if (r >= rows) continue;
+      if (!whole && warp == 0 && c == 0)
+        p.parts.ml[static_cast<int64_t>(part) * R + r] = make_float2(m[i], total[i]);
+      float f = whole ? 1.0f / total[i] : 1.0f;
+      if (kBytes) f *= ref[i] * 0x1p-7f;
+      moe_bf16 *dst = p.out + (w.s.start + pos[i] - ctx) * p.out_ld + out_row[i] * D;
 #pragma unroll
-        for (int j = 0; j < D / (kBytes ? 16 : 8); ++j) {
-          if (kBytes) {
-            const float4 v = make_float4(o[2 * j][2 * i] * f, o[2 * j + 1][2 * i] * f,
-                                         o[2 * j][2 * i + 1] * f, o[2 * j + 1][2 * i + 1] * f);
-            const int d = 16 * j + 4 * c;
-            if (whole)
-              *reinterpret_cast<uint2 *>(dst + d) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
-            else
-              *reinterpret_cast<float4 *>(part_at(r, d)) = v;
-          } else {
-            const int d = 8 * j + 2 * c;
-            const float x = o[j][2 * i] * f, y = o[j][2 * i + 1] * f;
-            if (whole) *reinterpret_cast<uint32_t *>(dst + d) = bf16x2(x, y);
-            else *reinterpret_cast<float2 *>(part_at(r, d) + (d & 2)) = make_float2(x, y);
-          }
+      for (int j = 0; j < kCols / (kBytes ? 16 : 8); ++j) {
+        if (kBytes) {
+          const int d = warp * kCols + 16 * j + 4 * c;
+          const float4 v = make_float4(o[2 * j][2 * i] * f, o[2 * j + 1][2 * i] * f,
+                                       o[2 * j][2 * i + 1] * f, o[2 * j + 1][2 * i + 1] * f);
+          if (whole)
+            *reinterpret_cast<uint2 *>(dst + d) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+          else
+            *reinterpret_cast<float4 *>(p.parts.at(part, D, d, r)) = v;
+        } else {
+          const int d = warp * kCols + 8 * j + 2 * c;
+          const float x = o[j][2 * i] * f, y = o[j][2 * i + 1] * f;
+          if (whole) *reinterpret_cast<uint32_t *>(dst + d) = bf16x2(x, y);
+          else
+            *reinterpret_cast<float2 *>(p.parts.at(part, D, d, r) + (d & 2)) = make_float2(x, y);
         }
-      }
-    } else {
-      constexpr int kCols = S::kJoinCols;
-      if (c == 0)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          sh->m[wk * R + wr * 16 + g + 8 * i] = m[i];
-          sh->l[wk * R + wr * 16 + g + 8 * i] = l[i];
-        }
-      ptx::named_barrier(1, 128);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = wr * 16 + g + 8 * i;
-        float top = -INFINITY;
-        for (int k = 0; k < kWK; ++k) top = fmaxf(top, sh->m[k * R + r]);
-        const float f = top == -INFINITY ? 0.0f : attn_exp2(m[i] - top);
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) o[j][2 * i] *= f, o[j][2 * i + 1] *= f;
-      }
-      // each thread joins 16 WR kCols / 128 columns of one row at a time
-      constexpr int kEach = R * kCols / 128;
-      const int r = threadIdx.x * kEach / kCols, d0 = threadIdx.x * kEach % kCols;
-      float top = -INFINITY, total = 0.0f;
-      for (int k = 0; k < kWK; ++k) top = fmaxf(top, sh->m[k * R + r]);
-      for (int k = 0; k < kWK; ++k)
-        total += sh->l[k * R + r] * (top == -INFINITY ? 0.0f : attn_exp2(sh->m[k * R + r] - top));
-      if (!whole && d0 == 0 && r < rows) part_ml[r] = make_float2(top, total);
-      const float f = whole ? 1.0f / total : 1.0f;
-      moe_bf16 *dst = r < rows ? out_at(r) : nullptr;
-#pragma unroll
-      for (int d = 0; d < D; d += kCols) {
-        float *mine = join + (wk * R + wr * 16) * kCols;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int j = 0; j < kCols / (kBytes ? 16 : 8); ++j) {
-            const int at = (g + 8 * i) * kCols;
-            if (kBytes) {
-              const int jj = d / 16 + j;
-              *reinterpret_cast<float4 *>(mine + at + 16 * j + 4 * c) =
-                  make_float4(o[2 * jj][2 * i], o[2 * jj + 1][2 * i], o[2 * jj][2 * i + 1],
-                              o[2 * jj + 1][2 * i + 1]);
-            } else {
-              const int jj = d / 8 + j;
-              *reinterpret_cast<float2 *>(mine + at + 8 * j + 2 * c) =
-                  make_float2(o[jj][2 * i], o[jj][2 * i + 1]);
-            }
-          }
-        }
-        ptx::named_barrier(1, 128);
-        if (r < rows) {
-#pragma unroll
-          for (int e = 0; e < kEach; e += 4) {
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int k = 0; k < kWK; ++k) {
-              const float4 x =
-                  *reinterpret_cast<const float4 *>(join + (k * R + r) * kCols + d0 + e);
-              v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-            }
-            if (whole)
-              *reinterpret_cast<uint2 *>(dst + d + d0 + e) =
-                  make_uint2(bf16x2(v.x * f, v.y * f), bf16x2(v.z * f, v.w * f));
-            else
-              *reinterpret_cast<float4 *>(part_at(r, d + d0 + e)) = v;
-          }
-        }
-        if (d + kCols < D) ptx::named_barrier(1, 128);
       }
     }
   }

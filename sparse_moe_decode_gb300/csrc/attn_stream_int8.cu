@@ -3,8 +3,8 @@
 
 namespace moe {
 
-cudaError_t launch_stream_int8(const AttnLaunch &x, int d, int wr) {
-  return launch_stream_kv<MOE_KV_INT8>(x, d, wr);
+cudaError_t launch_stream_int8(const AttnLaunch &x, int d) {
+  return launch_stream_kv<MOE_KV_INT8>(x, d);
 }
 
 }  // namespace moe

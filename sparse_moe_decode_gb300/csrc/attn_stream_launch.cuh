@@ -7,10 +7,10 @@
 
 namespace moe {
 
-template <int D, int KV, int WR>
+template <int D, int KV>
 cudaError_t launch_stream(const AttnLaunch &x) {
-  using S = StreamShape<D, KV, WR>;
-  const auto kernel = attn_stream_kernel<D, KV, WR>;
+  using S = StreamShape<D, KV>;
+  const auto kernel = attn_stream_kernel<D, KV>;
   static bool attr[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -35,21 +35,10 @@ cudaError_t launch_stream(const AttnLaunch &x) {
 }
 
 template <int KV>
-cudaError_t launch_stream_kv(const AttnLaunch &x, int d, int wr) {
-  switch (d) {
-    case 64:
-      return wr == 1   ? launch_stream<64, KV, 1>(x)
-             : wr == 2 ? launch_stream<64, KV, 2>(x)
-                       : launch_stream<64, KV, 4>(x);
-    case 128:
-      return wr == 1   ? launch_stream<128, KV, 1>(x)
-             : wr == 2 ? launch_stream<128, KV, 2>(x)
-                       : launch_stream<128, KV, 4>(x);
-    default:
-      return wr == 1   ? launch_stream<256, KV, 1>(x)
-             : wr == 2 ? launch_stream<256, KV, 2>(x)
-                       : launch_stream<256, KV, 4>(x);
-  }
+cudaError_t launch_stream_kv(const AttnLaunch &x, int d) {
+  return d == 64    ? launch_stream<64, KV>(x)
+         : d == 128 ? launch_stream<128, KV>(x)
+                    : launch_stream<256, KV>(x);
 }
 
 }  // namespace moe

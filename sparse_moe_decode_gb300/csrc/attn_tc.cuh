@@ -330,6 +330,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           ok = ptx::mbar_wait(&sh->s_full[sb], NQ == 2 ? items & 1 : (items >> 1) & 1, abort,
                               p.budget);
           if (!ok) break;
+          if (qi * 128 + wq * 32 >= rows) {  // none of the warp's rows is the tile's
+            if (lane == 0) {
+              ptx::mbar_arrive(&sh->p_full[sb]);
+              if (kBytes) ptx::mbar_arrive(&sh->scale_empty[slot]);
+            }
+            ++items;
+            begun = true;
+            continue;
+          }
           ptx::tc_fence_after();
           float s[128];
 #pragma unroll
