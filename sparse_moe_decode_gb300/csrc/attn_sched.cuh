@@ -41,6 +41,9 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnBatch &a, int b, bool repo
   return s;
 }
 
+// (Out of line: code that runs once costs its way through the instruction caches.)
+static __device__ __noinline__ uint64_t div_wide(uint64_t x, uint64_t m) { return x / m; }
+
 // x / m and x % m; divisions of 64 bits take several times as long.
 __device__ __forceinline__ uint64_t div_mod(uint64_t x, uint32_t m, uint32_t &rest) {
   if ((x >> 32) == 0) {
@@ -48,13 +51,13 @@ __device__ __forceinline__ uint64_t div_mod(uint64_t x, uint32_t m, uint32_t &re
     rest = static_cast<uint32_t>(x) - d * m;
     return d;
   }
-  const uint64_t d = x / m;
+  const uint64_t d = div_wide(x, m);
   rest = static_cast<uint32_t>(x - d * m);
   return d;
 }
 
 // sum over i < n of floor((a i + b) / m), m > 0 (Euclid's steps).
-__device__ __forceinline__ int64_t floor_sum(uint64_t n, uint32_t m, uint64_t a, uint64_t b) {
+static __device__ __noinline__ int64_t floor_sum(uint64_t n, uint32_t m, uint64_t a, uint64_t b) {
   uint64_t sum = 0;
   while (n > 0) {
     uint32_t ra, rb;
@@ -172,7 +175,8 @@ __device__ __forceinline__ void attn_share(const AttnBatch &a, const AttnRange &
     return v;
   };
   int64_t total, incl = scan(sum, total);
-  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  uint32_t rest;
+  int64_t per = div_mod(total + gridDim.x - 1, gridDim.x, rest);
   if (per < least_share) per = least_share;
   const int64_t at = per * blockIdx.x;
   if (tid == 0) {
@@ -223,7 +227,7 @@ struct AttnWalk {
     int64_t rem = sh.offset;
     const int64_t each = t.before(t.count);
     if ((each | rem) >> 32) {
-      head = static_cast<int>(rem / each);
+      head = static_cast<int>(div_wide(rem, each));
     } else {
       head = static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(each));
     }

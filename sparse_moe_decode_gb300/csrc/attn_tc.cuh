@@ -60,6 +60,8 @@ struct TcShape {
   static constexpr int kSoftWarps = 4 * kNQ;
   // (whole groups of four warps)
   static constexpr int kFetchWarp = kSoftWarps + (kBytes ? 4 : 0), kMmaWarp = kFetchWarp + 1;
+  static constexpr int kPlanWarp = kMmaWarp + kNQ;
+  static constexpr int kReaders = kSoftWarps + (kBytes ? 4 : 0) + 1 + kNQ;  // of the plan
   static constexpr int kThreads = 32 * (kFetchWarp + 4);
   // Registers a thread at launch, and what the softmax's warps and the rest
   // have of them (0: no more than a thread can have anyway).
@@ -73,10 +75,27 @@ struct TcShape {
   static_assert(kUnits <= 12 && kRaws <= 12 && kUnits >= (kNQ == 2 ? 2 * kChunks : 5), "ring");
 };
 
+// A segment of a tile, as the planning warp hands it to the others.
+struct __align__(16) TcSegment {
+  int32_t there;           // 0: there is no more
+  int32_t b, start, len;   // the sequence, its first row, its positions
+  int32_t head, row0, rows, ctx;  // the tile: its first row and rows; positions before the rows'
+  int32_t k0, k1;          // key tiles
+  int32_t q0[2], q1[2];    // those that query tile i has to do with: q0[i] .. q1[i] - 1
+  int32_t begins, last;    // the tile's first segment; the block with its last one, -1: this
+  // (selects: an index would put the segment into local memory)
+  __device__ __forceinline__ int first(int i) const { return i ? q0[1] : q0[0]; }
+  __device__ __forceinline__ int end(int i) const { return i ? q1[1] : q1[0]; }
+  __device__ __forceinline__ bool has(int i, int kt) const { return kt >= first(i) && kt < end(i); }
+};
+static_assert(sizeof(TcSegment) == 64, "segment");
+
 struct TcSmem {
+  TcSegment plan[4];
+  uint64_t plan_full[4], plan_empty[4];
   uint64_t full[12], empty[12], raw_full[12], raw_empty[12];
   uint64_t scale_raw[4], scale_full[4], scale_empty[4];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_last[2], turn[2], done;
+  uint64_t q_raw[2], q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_last[2], turn[2], done;
   AttnShare share;
   uint32_t tmem_holder;
   int abort;
@@ -162,26 +181,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 
-// The key tiles of a segment that query tile i of its tile has to do with.
-struct TcSpan {
-  int k0, k1;
-  __device__ __forceinline__ bool has(int kt) const { return kt >= k0 && kt < k1; }
-};
-template <class Walk>
-__device__ __forceinline__ TcSpan tc_span(const Walk &w, const AttnBatch &a, int R, int i) {
-  const int first = w.cur * R + 128 * i, last = min(first + 127, w.t.rows - 1);
-  TcSpan s;
-  if (first >= w.t.rows) {
-    s.k0 = s.k1 = 0;
-    return s;
-  }
-  const int p0 = w.t.ctx + first / a.group, p1 = w.t.ctx + last / a.group;
-  const int lo = a.window && p0 >= a.window ? (p0 - a.window + 1) / 128 : 0;
-  s.k0 = max(w.k0, lo);
-  s.k1 = min(w.k1, p1 / 128 + 1);
-  return s;
-}
-
 template <int D, int KV>
 __global__ void __launch_bounds__((TcShape<D, KV>::kThreads), 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -207,12 +206,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       ptx::mbar_init(&sh->raw_empty[i], 4);
     }
     for (int i = 0; i < 4; ++i) {
+      ptx::mbar_init(&sh->plan_full[i], 1);
+      ptx::mbar_init(&sh->plan_empty[i], S::kReaders);
       ptx::mbar_init(&sh->scale_raw[i], 1);
       ptx::mbar_init(&sh->scale_full[i], 4);
       ptx::mbar_init(&sh->scale_empty[i], S::kSoftWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sh->q_full[i], p.q_copy ? 1 : 4);
+      ptx::mbar_init(&sh->q_raw[i], 1);
+      ptx::mbar_init(&sh->q_full[i], p.q_copy && !kBytes ? 1 : 4);
       ptx::mbar_init(&sh->q_empty[i], 1);
       ptx::mbar_init(&sh->turn[i], 1);
       ptx::mbar_init(&sh->s_full[i], 1);
@@ -238,8 +240,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = sh->tmem_holder;
-  AttnWalk<R, 128, kTcTileCost> w;
-  w.init(a, sh->share);
+  uint32_t seg_n = 0;
+  bool ok = true;
+  const auto next_segment = [&]() {
+    const uint32_t slot = seg_n % 4;
+    TcSegment s;
+    s.there = 0;
+    ok = ok && ptx::mbar_wait(&sh->plan_full[slot], (seg_n / 4) & 1, abort, p.budget);
+    if (ok) s = sh->plan[slot];
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&sh->plan_empty[slot]);
+    ++seg_n;
+    return s;
+  };
   const int page = 1 << a.page_shift;
   const int k_box = page < 128 ? page : 128, v_box = page < S::kVKeys ? page : S::kVKeys;
 
@@ -250,24 +263,57 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     const uint32_t o_at = tmem + lanes + S::kO + qi * D;
     const float sign = p.scale_log2 < 0.0f ? -1.0f : 1.0f;
     const float c_all = fabsf(p.scale_log2);
-    uint32_t items = 0, tiles = 0, segs = 0;
-    bool ok = true;
-    while (w.next(a, range)) {
-      if (!ok) break;
-      const int row0 = w.cur * R;
-      const int rows = min(w.t.rows - row0, R);
-      const TcSpan span = tc_span(w, a, R, qi);
+    uint32_t items = 0, tiles = 0, segs = 0, q_tiles = 0;
+    for (TcSegment w = next_segment(); w.there; w = next_segment()) {
+      const int rows = w.rows;
       const int r = qi * 128 + wq * 32 + lane;  // this thread's row of the tile
       const bool live = r < rows;
-      const int my_row = row0 + (live ? r : rows - 1);
+      const int my_row = w.row0 + (live ? r : rows - 1);
       const int token = my_row / a.group, head = w.head * a.group + my_row % a.group;
-      const int pos = w.t.ctx + token;
+      const int pos = w.ctx + token;
       const int warp_pos = __shfl_sync(0xFFFFFFFFu, pos, 0);  // the warp's first and last
       const int warp_last = __shfl_sync(0xFFFFFFFFu, pos, 31);
-      const int64_t q_off = (w.s.start + token) * p.q_ld + head * D;
+      const bool idle = qi * 128 + wq * 32 >= rows;  // none of the warp's rows is the tile's
+      const bool mine = w.first(qi) < w.end(qi);
       float factor = c_all;
-      if (!p.q_copy && span.k0 < span.k1) {  // ---- this warp's 32 rows of q
-        constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = D == 64 ? 8 : 16;
+      if (kBytes && p.q_copy && mine) {
+        // ---- this thread's row of q as it lies in its place, made fp16
+        ok = ptx::mbar_wait(&sh->q_raw[qi], q_tiles++ & 1, abort, p.budget);
+        if (!ok) break;
+        if (!idle) {
+          const int row = wq * 32 + lane;
+          uint8_t *at = q_area + qi * kChunks * 16384 + row * 128;
+          float top = 0.0f;
+#pragma unroll 1
+          for (int ch = 0; ch < kChunks; ++ch)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 x = *reinterpret_cast<const uint4 *>(at + ch * 16384 + ((i ^ (row & 7)) << 4));
+              top = max3_abs(max3_abs(top, bf16_lo(x.x), bf16_hi(x.x)), bf16_lo(x.y), bf16_hi(x.y));
+              top = max3_abs(max3_abs(top, bf16_lo(x.z), bf16_hi(x.z)), bf16_lo(x.w), bf16_hi(x.w));
+            }
+          float mult, inv;
+          pow2_scale(top, mult, inv);
+          factor *= inv;
+          mult = c_all == 0.0f ? 0.0f : mult * sign;
+          const auto half = [&](uint32_t v) {
+            if (c_all == 0.0f) return 0u;  // all scores are 0
+            return h2_bits(__floats2half2_rn(bf16_lo(v) * mult, bf16_hi(v) * mult));
+          };
+#pragma unroll 1
+          for (int ch = 0; ch < kChunks; ++ch)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint4 *x = reinterpret_cast<uint4 *>(at + ch * 16384 + ((i ^ (row & 7)) << 4));
+              *x = make_uint4(half(x->x), half(x->y), half(x->z), half(x->w));
+            }
+          ptx::fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh->q_full[qi]);
+      } else if (!p.q_copy && mine) {  // ---- this warp's 32 rows of q
+        const int64_t q_off = (w.start + token) * p.q_ld + head * D;
+        constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 4;
         const int l16 = lane % kLanes;
         uint8_t *q_dst = q_area + qi * kChunks * 16384 + (l16 >> 3) * 16384;
 #pragma unroll 1
@@ -324,13 +370,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           if (!ok) break;
           ++tiles;
         }
-        if (span.has(kt)) {
+        if (w.has(qi, kt)) {
           const int sb = NQ == 2 ? qi : static_cast<int>(items & 1);
           const uint32_t s_at = tmem + lanes + S::kS + sb * 128;
           ok = ptx::mbar_wait(&sh->s_full[sb], NQ == 2 ? items & 1 : (items >> 1) & 1, abort,
                               p.budget);
           if (!ok) break;
-          if (qi * 128 + wq * 32 >= rows) {  // none of the warp's rows is the tile's
+          if (idle) {
             if (lane == 0) {
               ptx::mbar_arrive(&sh->p_full[sb]);
               if (kBytes) ptx::mbar_arrive(&sh->scale_empty[slot]);
@@ -472,12 +518,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       }
       if (!ok) break;
       // ----------------------------------------------- the segment's end
-      const bool whole = w.begins && w.ends;
+      const bool whole = w.begins && w.last < 0;
       const int part = 2 * blockIdx.x + (w.begins ? 1 : 0);
       if (!whole && w.begins && threadIdx.x == 0) {
         AttnOpen d;
-        d.last = static_cast<int>((w.tile_end - 1) / sh->share.per);
-        d.rows = rows, d.start = w.s.start, d.row0 = row0, d.head = w.head;
+        d.last = w.last;
+        d.rows = rows, d.start = w.start, d.row0 = w.row0, d.head = w.head;
         p.parts.open[blockIdx.x] = d;
       }
       const int64_t at = static_cast<int64_t>(part) * p.parts.rows + r;
@@ -488,7 +534,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         ptx::tc_fence_after();
         float f = whole ? 1.0f / l : 1.0f;
         if (kBytes) f *= ref * 0x1p-7f;
-        moe_bf16 *dst = p.out + (w.s.start + token) * p.out_ld + head * D;
+        moe_bf16 *dst = p.out + (w.start + token) * p.out_ld + head * D;
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {
           float o[32];
@@ -522,10 +568,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       constexpr int kSlotBytes = kBytes ? S::kRaw : S::kUnit;
       uint8_t *slots = kBytes ? raw : ring;
       uint64_t *full = kBytes ? sh->raw_full : sh->full, *empty = kBytes ? sh->raw_empty : sh->empty;
-      bool ok = true;
-      while (ok && w.next(a, range)) {
+      for (TcSegment w = next_segment(); w.there && ok; w = next_segment()) {
         const int32_t *table = a.table + w.b * a.table_ld;
-        const int len = w.s.len;
+        const int len = w.len;
         // lane i: the page of position kt * 128 + i * page
         const auto pages_of = [&](int kt) {
           const int64_t pos = static_cast<int64_t>(kt) * 128 + static_cast<int64_t>(lane) * page;
@@ -572,17 +617,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         if (p.q_copy) {
           // (rows behind the sequence's last are of no use and do no harm)
           for (int i = 0; i < NQ && ok; ++i) {
-            const TcSpan span = tc_span(w, a, R, i);
-            if (span.k0 >= span.k1) continue;
+            if (w.first(i) >= w.end(i)) continue;
+            uint64_t *here = kBytes ? &sh->q_raw[i] : &sh->q_full[i];
             ok = ptx::mbar_wait(&sh->q_empty[i], (q_tiles[i] & 1) ^ 1, abort, p.budget);
             if (!ok) break;
             ++q_tiles[i];
-            if (lane == 0) ptx::mbar_expect_tx(&sh->q_full[i], kChunks * 16384);
+            if (lane == 0) ptx::mbar_expect_tx(here, kChunks * 16384);
             __syncwarp();
             if (lane < kChunks)
               ptx::tma_load_3d(q_area + (i * kChunks + lane) * 16384, &tm_q, lane * 64,
-                               w.head * a.group, w.s.start + (w.cur * R + 128 * i) / a.group,
-                               &sh->q_full[i], pol);
+                               w.head * a.group, w.start + (w.row0 + 128 * i) / a.group, here, pol);
           }
         }
         int before = 0, ids = pages_of(w.k0);
@@ -623,7 +667,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           }
           for (int i = 0; i < NQ; ++i)
             if (q_tiles[i] > 0)
-              ptx::mbar_wait(&sh->q_full[i], (q_tiles[i] - 1) & 1, &never, ptx::kDrainBudgetNs);
+              ptx::mbar_wait(kBytes ? &sh->q_raw[i] : &sh->q_full[i], (q_tiles[i] - 1) & 1, &never,
+                             ptx::kDrainBudgetNs);
           for (uint32_t k = 0; k < S::kScaleSlots && k < tiles; ++k) {
             const uint32_t j = tiles - 1 - k;
             ptx::mbar_wait(&sh->scale_raw[j % S::kScaleSlots], (j / S::kScaleSlots) & 1, &never,
@@ -636,7 +681,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const int t = threadIdx.x - 32 * S::kSoftWarps;
       constexpr uint32_t kRaws = S::kRaws > 0 ? S::kRaws : 1;
       uint32_t n = 0;
-      bool ok = true;
       // 128 rows of 64 codes, 16 of a row at a time, to rows of 128 bytes; rows
       // whose key is `dead` or later become 0 (v only)
       const auto unit = [&](bool is_v, int dead) {
@@ -690,9 +734,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         if (lane == 0) ptx::mbar_arrive(&sh->scale_full[slot]);
         ++tiles;
       };
-      while (ok && w.next(a, range)) {
+      for (TcSegment w = next_segment(); w.there && ok; w = next_segment()) {
         const auto v_units = [&](int kt) {
-          for (int u = 0; u < kChunks && ok; ++u) unit(true, w.s.len - kt * 128 - u * S::kVKeys);
+          for (int u = 0; u < kChunks && ok; ++u) unit(true, w.len - kt * 128 - u * S::kVKeys);
         };
         for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
           if (NQ == 2 && kt > w.k0) v_units(kt - 1);
@@ -701,6 +745,37 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             for (int c = 0; c < kChunks && ok; ++c) unit(false, 0);
           if (NQ == 1 && kt > w.k0) v_units(kt - 1);
         }
+      }
+    } else if (warp == S::kPlanWarp) {  // --------------------------------- plan
+      AttnWalk<R, 128, kTcTileCost> w;
+      w.init(a, sh->share);
+      for (bool more = true; more; ++seg_n) {
+        more = w.next(a, range);
+        if (!ptx::mbar_wait(&sh->plan_empty[seg_n % 4], ((seg_n / 4) & 1) ^ 1, abort, p.budget)) break;
+        if (lane == 0) {
+          TcSegment s;
+          s.there = more;
+          if (more) {
+            s.b = w.b, s.start = w.s.start, s.len = w.s.len, s.head = w.head, s.ctx = w.t.ctx;
+            s.row0 = w.cur * R, s.rows = min(w.t.rows - s.row0, R);
+            s.k0 = w.k0, s.k1 = w.k1;
+            s.begins = w.begins;
+            s.last = w.ends ? -1 : static_cast<int>((w.tile_end - 1) / sh->share.per);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              s.q0[i] = s.q1[i] = 0;
+              if (i < NQ && 128 * i < s.rows) {
+                const int first = s.ctx + (s.row0 + 128 * i) / a.group;
+                const int last = s.ctx + (s.row0 + min(128 * i + 127, s.rows - 1)) / a.group;
+                s.q0[i] = max(w.k0, a.window && first >= a.window ? (first - a.window + 1) / 128 : 0);
+                s.q1[i] = max(s.q0[i], min(w.k1, last / 128 + 1));
+              }
+            }
+          }
+          sh->plan[seg_n % 4] = s;
+          ptx::mbar_arrive(&sh->plan_full[seg_n % 4]);
+        }
+        __syncwarp();
       }
     } else if (warp >= S::kMmaWarp && warp < S::kMmaWarp + NQ) {  // --- products
       // One warp a query tile: while one waits, the other's products run.
@@ -716,9 +791,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       for (int k = 0; k < kVSteps; ++k)
         v_step[k] = (16 * k / v_box * (v_box * D * 2) + 16 * k % v_box * 128) >> 4;
       uint32_t n = 0, segs = 0, items = 0, turns = 0;  // units, segments, key tiles so far
-      bool ok = true;
-      while (ok && w.next(a, range)) {
-        const TcSpan span = tc_span(w, a, R, qi);
+      for (TcSegment w = next_segment(); w.there && ok; w = next_segment()) {
         bool q_here = false, o_begun = false;
         const auto buffer = [&](uint32_t item) { return NQ == 2 ? qi : static_cast<int>(item & 1); };
         const auto parity = [&](uint32_t item) { return NQ == 2 ? item & 1 : (item >> 1) & 1; };
@@ -791,8 +864,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         };
         for (int kt = w.k0; kt <= w.k1; ++kt) {
           const bool has_k = kt < w.k1, has_v = kt > w.k0;
-          const bool do_k = has_k && span.has(kt), do_v = has_v && span.has(kt - 1);
-          const int left = w.s.len - (kt - 1) * 128;
+          const bool do_k = has_k && w.has(qi, kt), do_v = has_v && w.has(qi, kt - 1);
+          const int left = w.len - (kt - 1) * 128;
           // All that the products need is waited for before the first of them: the
           // tensor cores have room for few, and stand still during a wait.
           if (do_k && !q_here) {
@@ -826,10 +899,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           ok = ok && ptx::mbar_wait(&sh->turn[qi], (turns++ & 1) ^ (qi == 0 ? 1 : 0), abort, p.budget);
           if (!ok) break;
           ptx::tc_fence_after();
-          if (do_v) pv(nv, 0, kt == span.k1);
+          if (do_v) pv(nv, 0, kt == w.end(qi));
           else if (has_v) pass(nv);
           if (do_k) {
-            qk(n, kt + 1 == span.k1);
+            qk(n, kt + 1 == w.end(qi));
           } else {
             if (elect_one()) ptx::mbar_arrive(&sh->turn[1 - qi]);
             if (has_k) pass(n);

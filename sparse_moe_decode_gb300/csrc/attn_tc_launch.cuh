@@ -33,10 +33,10 @@ cudaError_t launch_tc(const AttnLaunch &x) {
     return cudaErrorInvalidValue;
   AttnArgs p = x.args;
   p.parts.rows = S::kR;
-  // A query tile as whole tokens' groups of heads: one box.  Not where q is made
-  // fp16, or its sign or zero enters.
+  // A query tile as whole tokens' groups of heads: one box.  (A negative or zero
+  // scale enters through q: with a bf16 cache that has to pass through registers.)
   const int group = x.batch.group;
-  p.q_copy = !S::kBytes && (group & (group - 1)) == 0 && p.scale_log2 > 0.0f;
+  p.q_copy = (group & (group - 1)) == 0 && (S::kBytes || p.scale_log2 > 0.0f);
   if (p.q_copy) {
     const uint64_t dims[3] = {D, static_cast<uint64_t>(group) * x.batch.kv_heads,
                               static_cast<uint64_t>(x.batch.N)};
