@@ -480,11 +480,15 @@ size_t moe_attn_workspace_bytes(const moe_attn_dims *dims);
  * [q_heads][head_dim] bf16, out alike (16-byte aligned, strides multiples of
  * 8; out must not overlap q or the cache).  Any mix of single tokens, drafts
  * and whole prompts.  The products run on tensor cores with fp32 sums, the
- * softmax in fp32; the weights enter the second product as bf16 (as fp16 with
- * an 8-bit cache, whose codes are exact in fp16), out is rounded to bf16 once.
- * Weights below 2^-126 of a row's largest are 0; with an 8-bit cache the
- * products of a weight and its v_scale keep 11 bits, but no less than 2^-32 of
- * the row's largest product.
+ * softmax in fp32; weights below 2^-126 of a row's largest are 0; out is
+ * rounded to bf16 once.  With a bf16 cache the weights enter the second
+ * product as bf16.  With an 8-bit cache, for sequences of up to 16 rows (tokens
+ * times q_heads / kv_heads), codes and scales are exact, and the products of a
+ * weight and its v_scale enter as fp16: 11 bits, but no less than 2^-32 of the
+ * row's largest.  For sequences of more rows the weights and the cache's values
+ * code * scale enter as fp16, 11 bits each (of the values: down to 2^-20 of the
+ * largest scale of the sequence's keys of that head; of the weights: to 2^-21 of
+ * the largest).
  * What lies in the cache behind a sequence's last position is not looked at.
  * A value that is not finite in k, or in an 8-bit cache's rows, reaches the
  * rows that see its position; one in a bf16 cache's v may also reach rows of

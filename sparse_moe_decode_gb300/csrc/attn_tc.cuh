@@ -94,7 +94,9 @@ struct TcSmem {
   TcSegment plan[4];
   uint64_t plan_full[4], plan_empty[4];
   uint64_t full[12], empty[12], raw_full[12], raw_empty[12];
-  uint64_t scale_raw[4], scale_full[4], scale_empty[4];
+  uint64_t scale_raw[4], scale_full[4], scale_empty[4], meet;
+  float k_unit[4], v_unit[4];  // what 1 stands for in a key tile's fp16 keys, values
+  uint32_t top[4][2];
   uint64_t q_raw[2], q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_last[2], turn[2], done;
   AttnShare share;
   uint32_t tmem_holder;
@@ -157,6 +159,10 @@ __device__ __forceinline__ void mma_ts2(uint32_t d, uint32_t a, uint32_t b, uint
       : "memory");
 }
 
+__device__ __forceinline__ __half2 bits_h2(uint32_t v) {
+  return *reinterpret_cast<const __half2 *>(&v);
+}
+
 template <int N>
 __device__ __forceinline__ void take_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N > 0 ? N : 24));
@@ -200,17 +206,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 12; ++i) {
-      ptx::mbar_init(&sh->full[i], kBytes ? 4 : 1);
+      ptx::mbar_init(&sh->full[i], 1);
       ptx::mbar_init(&sh->empty[i], NQ);
       ptx::mbar_init(&sh->raw_full[i], 1);
-      ptx::mbar_init(&sh->raw_empty[i], 4);
+      ptx::mbar_init(&sh->raw_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(&sh->plan_full[i], 1);
       ptx::mbar_init(&sh->plan_empty[i], S::kReaders);
       ptx::mbar_init(&sh->scale_raw[i], 1);
       ptx::mbar_init(&sh->scale_full[i], 4);
-      ptx::mbar_init(&sh->scale_empty[i], S::kSoftWarps);
+      ptx::mbar_init(&sh->scale_empty[i], S::kSoftWarps + 4);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sh->q_raw[i], 1);
@@ -223,6 +229,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       ptx::mbar_init(&sh->o_last[i], 1);
     }
     ptx::mbar_init(&sh->done, NQ);
+    ptx::mbar_init(&sh->meet, 4);
     sh->abort = 0;
     ptx::fence_mbar_init();
     ptx::tma_prefetch_desc(&tm_k);
@@ -263,6 +270,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     const uint32_t o_at = tmem + lanes + S::kO + qi * D;
     const float sign = p.scale_log2 < 0.0f ? -1.0f : 1.0f;
     const float c_all = fabsf(p.scale_log2);
+    // 8-bit: weights enter as fp16 of 2^7 times them, 11 bits down to 2^-21
+    constexpr float kPower = kBytes ? 7.0f : 0.0f;
     uint32_t items = 0, tiles = 0, segs = 0, q_tiles = 0;
     for (TcSegment w = next_segment(); w.there; w = next_segment()) {
       const int rows = w.rows;
@@ -361,7 +370,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       }
       if (c_all == 0.0f) factor = 1.0f;
       float m = -INFINITY, l = 0.0f;
-      float ref = 0x1p-110f;  // (8-bit) O's sums times ref / 2^7
+      float unit = 1.0f;  // (8-bit) what 1 of O stands for
       bool begun = false;
       for (int kt = w.k0; kt < w.k1 && ok; ++kt) {
         const uint32_t slot = tiles % S::kScaleSlots;
@@ -391,15 +400,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           for (int i = 0; i < 4; ++i)
             ptx::tmem_ld32(s_at + 32 * i, *reinterpret_cast<float(*)[32]>(s + 32 * i));
           ptx::tmem_wait_ld();
-          const float4 *sc = reinterpret_cast<const float4 *>(scales + slot * 256);
-          if (kBytes) {
-#pragma unroll
-            for (int i = 0; i < 128; i += 4) {
-              const float4 f = sc[i / 4];
-              const float2 x = mul2(make_float2(s[i], s[i + 1]), make_float2(f.x, f.y));
-              const float2 y = mul2(make_float2(s[i + 2], s[i + 3]), make_float2(f.z, f.w));
-              s[i] = x.x, s[i + 1] = x.y, s[i + 2] = y.x, s[i + 3] = y.y;
-            }
+          const float f_tile = kBytes ? factor * sh->k_unit[slot] : factor;
+          float o_factor = 1.0f;
+          if (kBytes) {  // (powers of two, growing)
+            const float now = sh->v_unit[slot];
+            if (begun) o_factor = unit * pow2_inverse(now);
+            unit = now;
           }
           const int key0 = kt * 128, hi = pos - key0;
           if (key0 + 127 > warp_pos) {  // some row of the warp does not see all of the tile
@@ -417,49 +423,41 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             for (int i = 0; i < 128; i += 8)
 #pragma unroll
               for (int j = 0; j < 4; ++j) top[j] = max3(top[j], s[i + 2 * j], s[i + 2 * j + 1]);
-            return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
+            return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f_tile;
           };
-          // p = 2^(s - m), with 8-bit caches times the value's scale, into S's
-          // place.  m is the maximum of the tiles before, which nearly always
-          // does: only where the tile's total (or a weight above its power of two)
+          // p = 2^(s - m) (2^7 of that as fp16) into S's place.  m is the maximum of
+          // the tiles before, which nearly always does: only where the tile's total
           // says that m is far too small is it found anew, and the tile done again.
-          float o_factor = 1.0f, total, most;
+          float total;
           if (!begun) m = largest();
           while (true) {
-            const float base = m == -INFINITY ? 0.0f : m;
-            const float2 f2 = make_float2(factor, factor), b2 = make_float2(-base, -base);
-            const float f = pow2_inverse(ref) * 0x1p7f;
-            const float2 w2 = make_float2(f, f);
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-            most = 0.0f;
+            const float b = kPower - (m == -INFINITY ? 0.0f : m);
+            const float2 f2 = make_float2(f_tile, f_tile), b2 = make_float2(b, b);
+            float2 sum[4];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              uint32_t pk[16];
+            for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.0f, 0.0f);
+            uint32_t pk[16];
+            // in steps, so that the exponentials of 16 keys are on their way together
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const int at = h * 32 + 2 * i;
-                float2 x = fma2(make_float2(s[at], s[at + 1]), f2, b2);
-                float2 y = fma2(make_float2(s[at + 2], s[at + 3]), f2, b2);
-                x.x = attn_exp2(x.x), x.y = attn_exp2(x.y);
-                y.x = attn_exp2(y.x), y.y = attn_exp2(y.y);
-                sum[0] = add2(x, sum[0]), sum[1] = add2(y, sum[1]);
-                if (kBytes) {
-                  const float4 v = sc[32 + at / 4];
-                  x = mul2(x, make_float2(v.x, v.y)), y = mul2(y, make_float2(v.z, v.w));
-                  most = max3(max3(most, x.x, x.y), y.x, y.y);
-                  x = mul2(x, w2), y = mul2(y, w2);
-                  pk[i] = h2_bits(__float22half2_rn(x)), pk[i + 1] = h2_bits(__float22half2_rn(y));
-                } else {
-                  pk[i] = pack_bf16(x.x, x.y), pk[i + 1] = pack_bf16(y.x, y.y);
-                }
+            for (int h = 0; h < 8; ++h) {
+              float2 x[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                x[i] = fma2(make_float2(s[16 * h + 2 * i], s[16 * h + 2 * i + 1]), f2, b2);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i].x = attn_exp2(x[i].x), x[i].y = attn_exp2(x[i].y);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                sum[i & 3] = add2(x[i], sum[i & 3]);
+                pk[8 * (h & 1) + i] = kBytes ? h2_bits(__float22half2_rn(x[i]))
+                                             : pack_bf16(x[i].x, x[i].y);
               }
-              tmem_st16(s_at + 16 * h, pk);
+              if (h & 1) tmem_st16(s_at + 8 * (h - 1), pk);
             }
-            const float2 both = add2(sum[0], sum[1]);
+            const float2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
             total = both.x + both.y;
             const bool far = total > 0x1p15f || m == -INFINITY;
-            const bool over = kBytes && most >= 256.0f * ref && ref < 0x1p126f;
-            if (!__any_sync(0xFFFFFFFFu, far || over)) break;
+            if (!__any_sync(0xFFFFFFFFu, far)) break;
             float up = m;
             if (far) {
               const float mt = largest();
@@ -467,24 +465,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
               if (m == -INFINITY) up = mt;
               else if (mt > m) up = m + ceilf(mt - m);
             }
-            float factor_o = 1.0f;
+            // (nothing to change: rows that see none of the tile)
+            if (!__any_sync(0xFFFFFFFFu, up != m)) break;
             if (up != m) {
-              factor_o = attn_exp2(m - up);
-              l *= factor_o;
+              const float f = attn_exp2(m - up);
+              l *= f, o_factor *= f;
               m = up;
-              if (kBytes) {
-                const float now = ref * factor_o;
-                ref = fmaxf(now, 0x1p-110f);
-                factor_o = now * pow2_inverse(ref);
-              }
-            } else if (over) {
-              const float now = ref;
-              ref = pow2_floor(most);
-              factor_o = now * pow2_inverse(ref);
             }
-            o_factor *= factor_o;
-            // (nothing left to change: rows that see none of the tile)
-            if (!__any_sync(0xFFFFFFFFu, factor_o != 1.0f)) break;
           }
           if (begun && __any_sync(0xFFFFFFFFu, o_factor != 1.0f)) {
             // O's products so far are complete.  (Those before the last are: the
@@ -527,13 +514,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         p.parts.open[blockIdx.x] = d;
       }
       const int64_t at = static_cast<int64_t>(part) * p.parts.rows + r;
-      if (!whole && live) p.parts.ml[at] = make_float2(m, l);
+      if (!whole && live) p.parts.ml[at] = make_float2(m - kPower, l);
       if (begun) {
         ok = ptx::mbar_wait(&sh->o_last[qi], segs++ & 1, abort, p.budget);
         if (!ok) break;
         ptx::tc_fence_after();
         float f = whole ? 1.0f / l : 1.0f;
-        if (kBytes) f *= ref * 0x1p-7f;
+        if (kBytes) f *= unit;
         moe_bf16 *dst = p.out + (w.start + token) * p.out_ld + head * D;
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {
@@ -680,70 +667,128 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     } else if (kBytes && warp >= S::kSoftWarps && warp < S::kFetchWarp) {  // -- convert
       const int t = threadIdx.x - 32 * S::kSoftWarps;
       constexpr uint32_t kRaws = S::kRaws > 0 ? S::kRaws : 1;
+      constexpr int kChunkBits = kChunks == 4 ? 2 : kChunks - 1;
       uint32_t n = 0;
-      // 128 rows of 64 codes, 16 of a row at a time, to rows of 128 bytes; rows
-      // whose key is `dead` or later become 0 (v only)
-      const auto unit = [&](bool is_v, int dead) {
+      // A unit is one warp's: 128 rows of 64 codes, 16 of a row at a time, become
+      // rows of 64 fp16 code * scale, rounded once (the scale as two fp16 terms, 22
+      // bits); rows whose key is `dead` or later become 0 (v only).
+      const int v_shift = 31 - __clz(v_box);
+      const auto unit = [&](const uint32_t *sc, bool is_v, int dead) {
         const uint32_t rs = n % kRaws, us = n % kUnits;
-        ok = ptx::mbar_wait(&sh->raw_full[rs], (n / kRaws) & 1, abort, p.budget) &&
-             ptx::mbar_wait(&sh->empty[us], ((n / kUnits) & 1) ^ 1, abort, p.budget);
-        if (!ok) return;
-        const uint4 *src = reinterpret_cast<const uint4 *>(raw + rs * S::kRaw);
-        uint8_t *dst = ring + us * S::kUnit;
-        uint4 v[4];
+        if ((n & 3) == static_cast<uint32_t>(t >> 5)) {
+          ok = ok && ptx::mbar_wait(&sh->raw_full[rs], (n / kRaws) & 1, abort, p.budget) &&
+               ptx::mbar_wait(&sh->empty[us], ((n / kUnits) & 1) ^ 1, abort, p.budget);
+          if (!ok) return;
+          const uint4 *src = reinterpret_cast<const uint4 *>(raw + rs * S::kRaw) + lane;
+          uint8_t *dst = ring + us * S::kUnit;
+          const int c = 2 * (lane & 3);
+#pragma unroll 1
+          for (int i0 = 0; i0 < 16; i0 += 4) {
+            uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = src[i * 128 + t];
+            for (int i = 0; i < 4; ++i) v[i] = src[(i0 + i) * 32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = i * 32 + t / 4, c = 2 * (t & 3);
-          if (is_v) {
-            const int key = row / (v_box * kChunks) * v_box + row % v_box;
-            if (key >= dead) v[i] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 4; ++i) {
+              const int row = (i0 + i) * 8 + lane / 4;
+              int key = row;
+              if (is_v) {
+                key = (row >> (v_shift + kChunkBits) << v_shift) + (row & (v_box - 1));
+                if (key >= dead) v[i] = make_uint4(0, 0, 0, 0);
+              }
+              const uint32_t scale = sc[key];
+              const __half2 hi = bits_h2(__byte_perm(scale, 0, 0x1010));
+              const __half2 lo = bits_h2(__byte_perm(scale, 0, 0x3232));
+              const auto scaled = [&](uint32_t codes, uint32_t &a, uint32_t &b) {
+                codes_to_f16x2<KV>(codes, a, b);
+                a = h2_bits(__hfma2(bits_h2(a), hi, __hmul2(bits_h2(a), lo)));
+                b = h2_bits(__hfma2(bits_h2(b), hi, __hmul2(bits_h2(b), lo)));
+              };
+              uint32_t h[8];
+              scaled(v[i].x, h[0], h[1]), scaled(v[i].y, h[2], h[3]);
+              scaled(v[i].z, h[4], h[5]), scaled(v[i].w, h[6], h[7]);
+              *reinterpret_cast<uint4 *>(dst + row * 128 + ((c ^ (row & 7)) << 4)) =
+                  make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4 *>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) =
+                  make_uint4(h[4], h[5], h[6], h[7]);
+            }
           }
-          uint32_t h[8];
-          codes_to_f16x2<KV>(v[i].x, h[0], h[1]);
-          codes_to_f16x2<KV>(v[i].y, h[2], h[3]);
-          codes_to_f16x2<KV>(v[i].z, h[4], h[5]);
-          codes_to_f16x2<KV>(v[i].w, h[6], h[7]);
-          *reinterpret_cast<uint4 *>(dst + row * 128 + ((c ^ (row & 7)) << 4)) =
-              make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4 *>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) =
-              make_uint4(h[4], h[5], h[6], h[7]);
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(&sh->raw_empty[rs]);
-          ptx::mbar_arrive(&sh->full[us]);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            ptx::mbar_arrive(&sh->raw_empty[rs]);
+            ptx::mbar_arrive(&sh->full[us]);
+          }
         }
         ++n;
       };
-      uint32_t tiles = 0;
-      // A value's scale that is not finite moves to its key's, so that the row that
-      // sees it is NaN, and 0 times it is not NaN where it is hidden.
-      const auto tile_scales = [&]() {
-        const uint32_t slot = tiles % S::kScaleSlots;
-        ok = ptx::mbar_wait(&sh->scale_raw[slot], (tiles / S::kScaleSlots) & 1, abort, p.budget);
+      uint32_t tiles = 0, v_tiles = 0, meetings = 0;
+      const auto meet = [&]() {  // of the four warps
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh->meet);
+        ok = ok && ptx::mbar_wait(&sh->meet, meetings++ & 1, abort, p.budget);
+      };
+      float v_top = 0.0f;  // the largest scale of the segment's values so far
+      // A thread has a key: its scales, under powers of two that bring the tile's
+      // largest (of the values, the segment's so far) into [2^5, 2^6), as two terms.
+      // A value's scale that is not finite makes its key NaN and itself 0: the rows
+      // that see it are NaN, and 0 times it is not NaN where it is hidden.
+      const auto tile_scales = [&](int left) {
+        const uint32_t slot = tiles++ % S::kScaleSlots;
+        ok = ok && ptx::mbar_wait(&sh->scale_raw[slot], ((tiles - 1) / S::kScaleSlots) & 1, abort,
+                                  p.budget);
         if (!ok) return;
         float *sc = scales + slot * 256 + t;
-        if (!(fabsf(sc[128]) < INFINITY)) {
-          sc[0] = sc[128] - sc[128], sc[128] = 0.0f;
-          ptx::fence_proxy_async_smem();  // (the slot's next copy)
+        float k = sc[0], v = sc[128];
+        if (t >= left) k = v = 0.0f;
+        if (!(fabsf(v) < INFINITY)) k = v - v, v = 0.0f;
+        const auto magnitude = [](float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.0f; };
+        const uint32_t k_most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(magnitude(k)));
+        const uint32_t v_most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(magnitude(v)));
+        if (lane == 0) sh->top[t >> 5][0] = k_most, sh->top[t >> 5][1] = v_most;
+        meet();
+        if (!ok) return;
+        float k_top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          k_top = fmaxf(k_top, __uint_as_float(sh->top[i][0]));
+          v_top = fmaxf(v_top, __uint_as_float(sh->top[i][1]));
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh->scale_full[slot]);
-        ++tiles;
+        const auto power = [](float top) {  // brings it into [2^5, 2^6)
+          const int e = static_cast<int>(__float_as_uint(top) >> 23);
+          return __uint_as_float(static_cast<uint32_t>(min(259 - e, 253)) << 23);
+        };
+        const float k_up = power(k_top), v_up = power(v_top);
+        const auto two_terms = [](float x) {
+          const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
+          return static_cast<uint32_t>(__half_as_ushort(hi)) |
+                 (static_cast<uint32_t>(__half_as_ushort(lo)) << 16);
+        };
+        sc[0] = __uint_as_float(two_terms(k * k_up));
+        sc[128] = __uint_as_float(two_terms(v * v_up));
+        if (t == 0) sh->k_unit[slot] = pow2_inverse(k_up), sh->v_unit[slot] = pow2_inverse(v_up);
+        ptx::fence_proxy_async_smem();  // (before the slot's next copy)
+        meet();
+        if (ok && lane == 0) ptx::mbar_arrive(&sh->scale_full[slot]);
       };
       for (TcSegment w = next_segment(); w.there && ok; w = next_segment()) {
         const auto v_units = [&](int kt) {
-          for (int u = 0; u < kChunks && ok; ++u) unit(true, w.len - kt * 128 - u * S::kVKeys);
+          const uint32_t slot = v_tiles++ % S::kScaleSlots;
+          const uint32_t *sc = reinterpret_cast<const uint32_t *>(scales + slot * 256 + 128);
+          for (int u = 0; u < kChunks && ok; ++u)
+            unit(sc + u * S::kVKeys, true, w.len - kt * 128 - u * S::kVKeys);
+          __syncwarp();
+          if (ok && lane == 0) ptx::mbar_arrive(&sh->scale_empty[slot]);
         };
+        v_top = 0.0f;
         for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
           if (NQ == 2 && kt > w.k0) v_units(kt - 1);
-          if (kt < w.k1 && ok) tile_scales();
-          if (kt < w.k1)
-            for (int c = 0; c < kChunks && ok; ++c) unit(false, 0);
-          if (NQ == 1 && kt > w.k0) v_units(kt - 1);
+          if (kt < w.k1 && ok) {
+            tile_scales(w.len - kt * 128);
+            const uint32_t *sc = reinterpret_cast<const uint32_t *>(
+                scales + (tiles - 1) % S::kScaleSlots * 256);
+            for (int c = 0; c < kChunks && ok; ++c) unit(sc, false, 0);
+          }
+          if (NQ == 1 && kt > w.k0 && ok) v_units(kt - 1);
         }
       }
     } else if (warp == S::kPlanWarp) {  // --------------------------------- plan

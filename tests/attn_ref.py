@@ -34,47 +34,59 @@ def codes(x, s, kv):
     return np.where(np.isfinite(s)[..., None], c, 0.0)
 
 
-def attention(q, k, v, length, scale, window, v_scale=None):
+def attention(q, k, v, length, scale, window, k_scale=None, v_scale=None):
     """One sequence: q [n][Hq][D] at its last positions, k, v [length][Hkv][D],
-    for an 8-bit cache the scales of v [length][Hkv].  Returns out, the sums of
-    absolute terms, the largest sum of absolute terms of a score per row
-    [n][Hq], and what is lost of tiny weights."""
+    for an 8-bit cache their scales [length][Hkv].  Returns out and, per output,
+    how far off it may be."""
     q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
     n, g = q.shape[0], q.shape[1] // k.shape[1]
     at, key = length - n + np.arange(n)[:, None], np.arange(length)[None]
     seen = (key <= at) & (key > at - window if window else True)
-    out, mass = np.zeros(q.shape), np.zeros(q.shape)
-    slip, floor = np.zeros(q.shape[:2]), np.zeros(q.shape)
+    codes_wide = v_scale is not None and n * g > 16  # the tensor cores' kernel
+    out, bound = np.zeros(q.shape), np.zeros(q.shape)
     for h in range(q.shape[1]):
         kk, vv = k[:, h // g], v[:, h // g]
         s = np.where(seen, q[:, h] @ kk.T * scale, -np.inf)
         w = np.exp(s - s.max(1, keepdims=True))
         w /= w.sum(1, keepdims=True)
-        out[:, h], mass[:, h] = w @ vv, w @ np.abs(vv)
-        slip[:, h] = np.where(seen, np.abs(q[:, h]) @ np.abs(kk).T, 0.0).max(1) * abs(scale)
+        o, mass = w @ vv, w @ np.abs(vv)
+        terms = np.where(seen, np.abs(q[:, h]) @ np.abs(kk).T, 0.0).max(1, keepdims=True) * abs(scale)
+        # A score in fp32 is off by 2^-21 of its terms' sum (sums in any order, the
+        # products by the scales and by log2 e, the difference to the maximum).
+        slip = 2.0 ** -21 * terms
+        weight = BF16 if v_scale is None else FP16
+        floor = 3 * 2.0 ** -126 * (seen @ np.abs(vv))
         if v_scale is not None:
-            sv = v_scale[:, h // g].astype(np.float64)
-            floor[:, h] = 2.0 ** -32 * (w * sv).max(1, keepdims=True) * (seen @ np.abs(vv / sv[:, None]))
-        floor[:, h] += 3 * 2.0 ** -126 * (seen @ np.abs(vv))
-    return out, mass, slip, floor
-
-
-def attention_bound(out, mass, slip, floor, kv):
-    """One rounding of out to bf16 and one of each weight (to bf16, to fp16 with
-    8-bit caches).  A score in fp32 is off by 2^-21 of its terms' sum (sums in
-    any order, the products by the scales and by log2 e, the difference to the
-    maximum), which moves a weight and the weights' total by that factor each;
-    exp2 and the sums over the keys are off by 2^-18 at most.  With an 8-bit
-    cache a product t of a weight and a scale enters as fp16 of at least t 2^7 / r,
-    r a power of two at or below the row's largest t: fp16 has steps of 2^-24
-    below 2^-14, so that each t is off by at most 2^-25 / 2^7 r <= 2^-32 of the
-    largest, whatever its size, and each term by that times its code.  Weights
-    are fp32 beside the largest one's 1: below 2^-126 they count as 0, and so do
-    the factors that bring a part's sums (of terms of at most |v| each) to
-    another maximum, within the keys, between warps and between blocks: 3 2^-126
-    of the sum of |v|."""
-    weight = BF16 if kv == "bf16" else FP16
-    return BF16 * np.abs(out) + (weight + 2.0 ** -18 + 2 * 2.0 ** -21 * slip[..., None]) * mass + floor + 1e-37
+            kt, vt = (np.abs(x[:, h // g].astype(np.float64)) for x in (k_scale, v_scale))
+            if codes_wide:
+                # Each value of k is one fp16 rounding off: the sum of D independent
+                # ones lies within 8 standard deviations, of 2^-11 / sqrt(3) of the
+                # root of the terms' squares.  Scales under a power of two that brings
+                # the key tile's largest to 2^5 or more are two fp16 terms, off by
+                # 2^-26: a code of at most 448 by 2^-22 of the largest scale.
+                square = np.where(seen, (q[:, h] ** 2) @ (kk ** 2).T, 0.0).max(1, keepdims=True)
+                slip = slip + 8 * FP16 / 3 ** 0.5 * np.sqrt(square) * abs(scale)
+                slip = slip + 2.0 ** -22 * np.abs(q[:, h]).sum(1, keepdims=True) * kt.max() * abs(scale)
+                # A value of v is one fp16 rounding off too, and 2^-22 of the largest
+                # scale so far; a weight's fp16 is of 2^7 times it: off by 2^-32 at most.
+                weight = 2 * FP16
+                floor = floor + 2.0 ** -22 * vt.max() + 2.0 ** -32 * (seen @ np.abs(vv))
+            else:
+                # A product t of a weight and a scale enters as fp16 of t 2^7 / r, r a
+                # power of two at or below the row's largest t: fp16 has steps of 2^-24
+                # below 2^-14, so that each t is off by at most 2^-25 / 2^7 r <= 2^-32 of
+                # the largest, whatever its size, and each term by that times its code.
+                floor = floor + 2.0 ** -32 * (w * vt).max(1, keepdims=True) * (
+                    seen @ np.abs(vv / vt[:, None]))
+        # Two factors of 2^slip (a weight and the weights' total); the exponentials
+        # and the sums over the keys are off by 2^-18 at most.  Weights are fp32
+        # beside the largest one's 1: below 2^-126 they count as 0, and so do the
+        # factors that bring a part's sums (of terms of at most |v| each) to another
+        # maximum, within the keys, between warps and between blocks.
+        slip = np.expm1(2 * slip)
+        out[:, h] = o
+        bound[:, h] = BF16 * np.abs(o) + (weight + 2.0 ** -18 + slip) * mass + floor + 1e-37
+    return out, bound
 
 
 def verify(target, draft, drafted, uniform):

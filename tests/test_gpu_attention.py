@@ -3,7 +3,7 @@ definition; the bounds stand in attn_ref."""
 import numpy as np
 import pytest
 
-from attn_ref import attention, attention_bound
+from attn_ref import attention
 from util import gpu_env
 
 pytestmark = pytest.mark.gpu
@@ -79,19 +79,20 @@ class Batch:
         return self.attn.attend(self.cache, self.q, self.table, self.lens, self.cu, **kw)
 
     def values(self):
-        """What the cache stands for, per sequence (k, v), and the scales of v."""
+        """What the cache stands for, per sequence (k, v), and the scales."""
         out = []
         for i, length in enumerate(self.length):
             pos = np.arange(length)
             pg = self.table[i].cpu().numpy()[pos // self.page] if length else pos
-            both, scale = [], None
+            both, both_scales = [], []
             for x, s in zip(self.cache[:2], self.cache[2:]):
                 y = x.float().double().cpu().numpy()[pg, :, pos % self.page]
                 if s is not None:
                     scale = s.double().cpu().numpy()[pg, :, pos % self.page]
                     y = y * scale[..., None]
+                    both_scales.append(scale)
                 both.append(y)
-            out.append((*both, scale))
+            out.append((*both, *both_scales))
         return out
 
     def check(self, out, skip=()):
@@ -99,12 +100,11 @@ class Batch:
         q = self.q.double().cpu().numpy()
         start = 0
         worst = 0.0
-        for i, (n, (k, v, vs)) in enumerate(zip(self.new, self.values())):
+        for i, (n, (k, v, *scales)) in enumerate(zip(self.new, self.values())):
             if n and i not in skip:
-                want, mass, slip, floor = attention(q[start:start + n], k, v, self.length[i],
-                                                    self.attn.dims.scale, self.window, vs)
+                want, bound = attention(q[start:start + n], k, v, self.length[i],
+                                        self.attn.dims.scale, self.window, *scales)
                 err = np.abs(got[start:start + n] - want)
-                bound = attention_bound(want, mass, slip, floor, self.kv)
                 ok = bool((err <= bound).all())  # (NaN is not)
                 assert ok, (i, np.nanmax(err / bound), np.argwhere(~(err <= bound))[:4])
                 worst = max(worst, (err / bound).max())
