@@ -58,16 +58,17 @@ struct TcShape {
   static constexpr int kRaws = kBytes ? (kRoom - kUnits * kUnit) / kRaw : 0;
   static constexpr int kSmem = kFixed + kUnits * kUnit + kRaws * kRaw;
   static constexpr int kSoftWarps = 4 * kNQ;
-  // (whole groups of four warps)
-  static constexpr int kFetchWarp = kSoftWarps + (kBytes ? 4 : 0), kMmaWarp = kFetchWarp + 1;
+  // (with one query tile each key tile's conversion serves half as many products)
+  static constexpr int kConvWarps = !kBytes ? 0 : kNQ == 1 ? 8 : 4;
+  static constexpr int kFetchWarp = kSoftWarps + kConvWarps, kMmaWarp = kFetchWarp + 1;
   static constexpr int kPlanWarp = kMmaWarp + kNQ;
-  static constexpr int kReaders = kSoftWarps + (kBytes ? 4 : 0) + 1 + kNQ;  // of the plan
-  static constexpr int kThreads = 32 * (kFetchWarp + 4);
+  static constexpr int kThreads = 128 * ((kPlanWarp + 4) / 4);  // whole groups of four warps
+  static constexpr int kReaders = kSoftWarps + kConvWarps + 1 + kNQ;  // of the plan
   // Registers a thread at launch, and what the softmax's warps and the rest
   // have of them (0: no more than a thread can have anyway).
   static constexpr int kRegs = kThreads == 512 ? 128 : 168;
-  static constexpr int kSoftRegs = kThreads == 256 ? 0 : kNQ == 1 ? 232 : kBytes ? 192 : 216;
-  static constexpr int kRestRegs = kNQ == 1 ? 136 : kBytes ? 64 : 72;
+  static constexpr int kSoftRegs = kThreads == 256 ? 0 : kBytes ? 192 : 216;
+  static constexpr int kRestRegs = kNQ == 1 ? 104 : kBytes ? 64 : 72;
   static_assert(kSoftRegs * kSoftWarps + kRestRegs * (kThreads / 32 - kSoftWarps) <=
                     kRegs * (kThreads / 32) || kSoftRegs == 0, "registers");
   static constexpr uint32_t kS = 0, kO = 256;  // columns of tensor memory
@@ -94,9 +95,8 @@ struct TcSmem {
   TcSegment plan[4];
   uint64_t plan_full[4], plan_empty[4];
   uint64_t full[12], empty[12], raw_full[12], raw_empty[12];
-  uint64_t scale_raw[4], scale_full[4], scale_empty[4], meet;
+  uint64_t scale_raw[4], scale_full[4], scale_empty[4];
   float k_unit[4], v_unit[4];  // what 1 stands for in a key tile's fp16 keys, values
-  uint32_t top[4][2];
   uint64_t q_raw[2], q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_last[2], turn[2], done;
   AttnShare share;
   uint32_t tmem_holder;
@@ -206,17 +206,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 12; ++i) {
-      ptx::mbar_init(&sh->full[i], 1);
+      ptx::mbar_init(&sh->full[i], kBytes ? S::kConvWarps : 1);
       ptx::mbar_init(&sh->empty[i], NQ);
       ptx::mbar_init(&sh->raw_full[i], 1);
-      ptx::mbar_init(&sh->raw_empty[i], 1);
+      ptx::mbar_init(&sh->raw_empty[i], S::kConvWarps + (kBytes ? 0 : 1));
     }
     for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(&sh->plan_full[i], 1);
       ptx::mbar_init(&sh->plan_empty[i], S::kReaders);
       ptx::mbar_init(&sh->scale_raw[i], 1);
-      ptx::mbar_init(&sh->scale_full[i], 4);
-      ptx::mbar_init(&sh->scale_empty[i], S::kSoftWarps + 4);
+      ptx::mbar_init(&sh->scale_full[i], 1);
+      ptx::mbar_init(&sh->scale_empty[i], S::kSoftWarps + S::kConvWarps);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sh->q_raw[i], 1);
@@ -229,7 +229,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       ptx::mbar_init(&sh->o_last[i], 1);
     }
     ptx::mbar_init(&sh->done, NQ);
-    ptx::mbar_init(&sh->meet, 4);
     sh->abort = 0;
     ptx::fence_mbar_init();
     ptx::tma_prefetch_desc(&tm_k);
@@ -665,111 +664,65 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         __syncwarp();
       }
     } else if (kBytes && warp >= S::kSoftWarps && warp < S::kFetchWarp) {  // -- convert
-      const int t = threadIdx.x - 32 * S::kSoftWarps;
+      constexpr uint32_t kConvWarps = S::kConvWarps > 0 ? S::kConvWarps : 1;
       constexpr uint32_t kRaws = S::kRaws > 0 ? S::kRaws : 1;
       constexpr int kChunkBits = kChunks == 4 ? 2 : kChunks - 1;
       uint32_t n = 0;
-      // A unit is one warp's: 128 rows of 64 codes, 16 of a row at a time, become
-      // rows of 64 fp16 code * scale, rounded once (the scale as two fp16 terms, 22
-      // bits); rows whose key is `dead` or later become 0 (v only).
+      // 128 rows of 64 codes, 16 of a row at a time, become rows of 64 fp16 code *
+      // scale, rounded once (the scale as two fp16 terms, 22 bits); rows whose key is
+      // `dead` or later become 0 (v only).  (A warp for each unit took longer: the
+      // ring is short, and a unit by itself takes some 2400 cycles.)
+      const int t = threadIdx.x - 32 * S::kSoftWarps;
       const int v_shift = 31 - __clz(v_box);
       const auto unit = [&](const uint32_t *sc, bool is_v, int dead) {
         const uint32_t rs = n % kRaws, us = n % kUnits;
-        if ((n & 3) == static_cast<uint32_t>(t >> 5)) {
-          ok = ok && ptx::mbar_wait(&sh->raw_full[rs], (n / kRaws) & 1, abort, p.budget) &&
-               ptx::mbar_wait(&sh->empty[us], ((n / kUnits) & 1) ^ 1, abort, p.budget);
-          if (!ok) return;
-          const uint4 *src = reinterpret_cast<const uint4 *>(raw + rs * S::kRaw) + lane;
-          uint8_t *dst = ring + us * S::kUnit;
-          const int c = 2 * (lane & 3);
-#pragma unroll 1
-          for (int i0 = 0; i0 < 16; i0 += 4) {
-            uint4 v[4];
+        constexpr int kEach = 512 / (32 * kConvWarps);
+        ok = ok && ptx::mbar_wait(&sh->raw_full[rs], (n / kRaws) & 1, abort, p.budget);
+        if (!ok) return;
+        const uint4 *src = reinterpret_cast<const uint4 *>(raw + rs * S::kRaw) + t;
+        uint4 v[kEach];
+        uint32_t scale[kEach];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = src[(i0 + i) * 32];
+        for (int i = 0; i < kEach; ++i) {
+          const int row = i * (8 * kConvWarps) + t / 4;
+          v[i] = src[i * (32 * kConvWarps)];
+          int key = row;
+          if (is_v) {
+            key = (row >> (v_shift + kChunkBits) << v_shift) + (row & (v_box - 1));
+            if (key >= dead) v[i] = make_uint4(0, 0, 0, 0);
+          }
+          scale[i] = sc[key];
+        }
+        ok = ptx::mbar_wait(&sh->empty[us], ((n / kUnits) & 1) ^ 1, abort, p.budget);
+        if (!ok) return;
+        uint8_t *dst = ring + us * S::kUnit;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = (i0 + i) * 8 + lane / 4;
-              int key = row;
-              if (is_v) {
-                key = (row >> (v_shift + kChunkBits) << v_shift) + (row & (v_box - 1));
-                if (key >= dead) v[i] = make_uint4(0, 0, 0, 0);
-              }
-              const uint32_t scale = sc[key];
-              const __half2 hi = bits_h2(__byte_perm(scale, 0, 0x1010));
-              const __half2 lo = bits_h2(__byte_perm(scale, 0, 0x3232));
-              const auto scaled = [&](uint32_t codes, uint32_t &a, uint32_t &b) {
-                codes_to_f16x2<KV>(codes, a, b);
-                a = h2_bits(__hfma2(bits_h2(a), hi, __hmul2(bits_h2(a), lo)));
-                b = h2_bits(__hfma2(bits_h2(b), hi, __hmul2(bits_h2(b), lo)));
-              };
-              uint32_t h[8];
-              scaled(v[i].x, h[0], h[1]), scaled(v[i].y, h[2], h[3]);
-              scaled(v[i].z, h[4], h[5]), scaled(v[i].w, h[6], h[7]);
-              *reinterpret_cast<uint4 *>(dst + row * 128 + ((c ^ (row & 7)) << 4)) =
-                  make_uint4(h[0], h[1], h[2], h[3]);
-              *reinterpret_cast<uint4 *>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) =
-                  make_uint4(h[4], h[5], h[6], h[7]);
-            }
-          }
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            ptx::mbar_arrive(&sh->raw_empty[rs]);
-            ptx::mbar_arrive(&sh->full[us]);
-          }
+        for (int i = 0; i < kEach; ++i) {
+          const int row = i * (8 * kConvWarps) + t / 4, c = 2 * (t & 3);
+          const __half2 hi = bits_h2(__byte_perm(scale[i], 0, 0x1010));
+          const __half2 lo = bits_h2(__byte_perm(scale[i], 0, 0x3232));
+          const auto scaled = [&](uint32_t codes, uint32_t &a, uint32_t &b) {
+            codes_to_f16x2<KV>(codes, a, b);
+            a = h2_bits(__hfma2(bits_h2(a), hi, __hmul2(bits_h2(a), lo)));
+            b = h2_bits(__hfma2(bits_h2(b), hi, __hmul2(bits_h2(b), lo)));
+          };
+          uint32_t h[8];
+          scaled(v[i].x, h[0], h[1]), scaled(v[i].y, h[2], h[3]);
+          scaled(v[i].z, h[4], h[5]), scaled(v[i].w, h[6], h[7]);
+          *reinterpret_cast<uint4 *>(dst + row * 128 + ((c ^ (row & 7)) << 4)) =
+              make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4 *>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) =
+              make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(&sh->raw_empty[rs]);
+          ptx::mbar_arrive(&sh->full[us]);
         }
         ++n;
       };
-      uint32_t tiles = 0, v_tiles = 0, meetings = 0;
-      const auto meet = [&]() {  // of the four warps
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh->meet);
-        ok = ok && ptx::mbar_wait(&sh->meet, meetings++ & 1, abort, p.budget);
-      };
-      float v_top = 0.0f;  // the largest scale of the segment's values so far
-      // A thread has a key: its scales, under powers of two that bring the tile's
-      // largest (of the values, the segment's so far) into [2^5, 2^6), as two terms.
-      // A value's scale that is not finite makes its key NaN and itself 0: the rows
-      // that see it are NaN, and 0 times it is not NaN where it is hidden.
-      const auto tile_scales = [&](int left) {
-        const uint32_t slot = tiles++ % S::kScaleSlots;
-        ok = ok && ptx::mbar_wait(&sh->scale_raw[slot], ((tiles - 1) / S::kScaleSlots) & 1, abort,
-                                  p.budget);
-        if (!ok) return;
-        float *sc = scales + slot * 256 + t;
-        float k = sc[0], v = sc[128];
-        if (t >= left) k = v = 0.0f;
-        if (!(fabsf(v) < INFINITY)) k = v - v, v = 0.0f;
-        const auto magnitude = [](float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.0f; };
-        const uint32_t k_most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(magnitude(k)));
-        const uint32_t v_most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(magnitude(v)));
-        if (lane == 0) sh->top[t >> 5][0] = k_most, sh->top[t >> 5][1] = v_most;
-        meet();
-        if (!ok) return;
-        float k_top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          k_top = fmaxf(k_top, __uint_as_float(sh->top[i][0]));
-          v_top = fmaxf(v_top, __uint_as_float(sh->top[i][1]));
-        }
-        const auto power = [](float top) {  // brings it into [2^5, 2^6)
-          const int e = static_cast<int>(__float_as_uint(top) >> 23);
-          return __uint_as_float(static_cast<uint32_t>(min(259 - e, 253)) << 23);
-        };
-        const float k_up = power(k_top), v_up = power(v_top);
-        const auto two_terms = [](float x) {
-          const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
-          return static_cast<uint32_t>(__half_as_ushort(hi)) |
-                 (static_cast<uint32_t>(__half_as_ushort(lo)) << 16);
-        };
-        sc[0] = __uint_as_float(two_terms(k * k_up));
-        sc[128] = __uint_as_float(two_terms(v * v_up));
-        if (t == 0) sh->k_unit[slot] = pow2_inverse(k_up), sh->v_unit[slot] = pow2_inverse(v_up);
-        ptx::fence_proxy_async_smem();  // (before the slot's next copy)
-        meet();
-        if (ok && lane == 0) ptx::mbar_arrive(&sh->scale_full[slot]);
-      };
+      uint32_t tiles = 0, v_tiles = 0;
       for (TcSegment w = next_segment(); w.there && ok; w = next_segment()) {
         const auto v_units = [&](int kt) {
           const uint32_t slot = v_tiles++ % S::kScaleSlots;
@@ -779,13 +732,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           __syncwarp();
           if (ok && lane == 0) ptx::mbar_arrive(&sh->scale_empty[slot]);
         };
-        v_top = 0.0f;
         for (int kt = w.k0; kt <= w.k1 && ok; ++kt) {
           if (NQ == 2 && kt > w.k0) v_units(kt - 1);
           if (kt < w.k1 && ok) {
-            tile_scales(w.len - kt * 128);
-            const uint32_t *sc = reinterpret_cast<const uint32_t *>(
-                scales + (tiles - 1) % S::kScaleSlots * 256);
+            const uint32_t slot = tiles % S::kScaleSlots;
+            ok = ptx::mbar_wait(&sh->scale_full[slot], (tiles++ / S::kScaleSlots) & 1, abort, p.budget);
+            const uint32_t *sc = reinterpret_cast<const uint32_t *>(scales + slot * 256);
             for (int c = 0; c < kChunks && ok; ++c) unit(sc, false, 0);
           }
           if (NQ == 1 && kt > w.k0 && ok) v_units(kt - 1);
@@ -794,10 +746,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     } else if (warp == S::kPlanWarp) {  // --------------------------------- plan
       AttnWalk<R, 128, kTcTileCost> w;
       w.init(a, sh->share);
-      for (bool more = true; more; ++seg_n) {
-        more = w.next(a, range);
-        if (!ptx::mbar_wait(&sh->plan_empty[seg_n % 4], ((seg_n / 4) & 1) ^ 1, abort, p.budget)) break;
-        if (lane == 0) {
+      // The next segment; whether there is one.
+      const auto plan = [&]() {
+        const bool more = w.next(a, range);
+        ok = ok && ptx::mbar_wait(&sh->plan_empty[seg_n % 4], ((seg_n / 4) & 1) ^ 1, abort, p.budget);
+        if (ok && lane == 0) {
           TcSegment s;
           s.there = more;
           if (more) {
@@ -821,6 +774,64 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           ptx::mbar_arrive(&sh->plan_full[seg_n % 4]);
         }
         __syncwarp();
+        ++seg_n;
+        return more && ok;
+      };
+      if (!kBytes) {
+        while (plan()) {}
+      } else {
+        // ... and the scales of its key tiles, four keys a lane: under powers of two
+        // that bring the largest (of the tile's keys, of the segment's values so far)
+        // into [2^5, 2^6), as two fp16 terms.  A value's scale that is not finite
+        // makes its key NaN and itself 0: the rows that see it are NaN, and 0 times it
+        // is not NaN where it is hidden.
+        const auto magnitude = [](float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.0f; };
+        const auto largest = [&](const float (&x)[4]) {
+          const float top = fmaxf(fmaxf(magnitude(x[0]), magnitude(x[1])),
+                                  fmaxf(magnitude(x[2]), magnitude(x[3])));
+          return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
+        };
+        const auto power = [](float top) {
+          const int e = static_cast<int>(__float_as_uint(top) >> 23);
+          return __uint_as_float(static_cast<uint32_t>(min(259 - e, 253)) << 23);
+        };
+        const auto two_terms = [](float x) {
+          const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
+          return static_cast<uint32_t>(__half_as_ushort(hi)) |
+                 (static_cast<uint32_t>(__half_as_ushort(lo)) << 16);
+        };
+        uint32_t tiles = 0;
+        bool more = plan();
+        while (more) {
+          const int k0 = w.k0, k1 = w.k1, len = w.s.len;
+          more = plan();  // (one ahead)
+          float v_top = 0.0f;
+          for (int kt = k0; kt < k1 && ok; ++kt, ++tiles) {
+            const uint32_t slot = tiles % S::kScaleSlots;
+            ok = ptx::mbar_wait(&sh->scale_raw[slot], (tiles / S::kScaleSlots) & 1, abort, p.budget);
+            if (!ok) break;
+            float4 *ks = reinterpret_cast<float4 *>(scales + slot * 256) + lane, *vs = ks + 32;
+            const float4 kx = *ks, vx = *vs;
+            float k[4] = {kx.x, kx.y, kx.z, kx.w}, v[4] = {vx.x, vx.y, vx.z, vx.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (kt * 128 + 4 * lane + i >= len) k[i] = v[i] = 0.0f;
+              if (!(fabsf(v[i]) < INFINITY)) k[i] = v[i] - v[i], v[i] = 0.0f;
+            }
+            const float k_up = power(largest(k));
+            v_top = fmaxf(v_top, largest(v));
+            const float v_up = power(v_top);
+            *reinterpret_cast<uint4 *>(ks) = make_uint4(two_terms(k[0] * k_up), two_terms(k[1] * k_up),
+                                                        two_terms(k[2] * k_up), two_terms(k[3] * k_up));
+            *reinterpret_cast<uint4 *>(vs) = make_uint4(two_terms(v[0] * v_up), two_terms(v[1] * v_up),
+                                                        two_terms(v[2] * v_up), two_terms(v[3] * v_up));
+            if (lane == 0)
+              sh->k_unit[slot] = pow2_inverse(k_up), sh->v_unit[slot] = pow2_inverse(v_up);
+            ptx::fence_proxy_async_smem();  // (before the slot's next copy)
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh->scale_full[slot]);
+          }
+        }
       }
     } else if (warp >= S::kMmaWarp && warp < S::kMmaWarp + NQ) {  // --- products
       // One warp a query tile: while one waits, the other's products run.
