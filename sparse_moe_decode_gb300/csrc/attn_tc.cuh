@@ -669,17 +669,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       constexpr int kChunkBits = kChunks == 4 ? 2 : kChunks - 1;
       uint32_t n = 0;
       // 128 rows of 64 codes, 16 of a row at a time, become rows of 64 fp16 code *
-      // scale, rounded once (the scale as two fp16 terms, 22 bits); rows whose key is
-      // `dead` or later become 0 (v only).  (A warp for each unit took longer: the
-      // ring is short, and a unit by itself takes some 2400 cycles.)
+      // scale, rounded once: a key's scale is two fp16 terms (22 bits, since it moves
+      // all of a score), a value's one (it moves a weight by as much as the weight's
+      // own rounding).  Values whose key is `dead` or later become 0.  (A warp for
+      // each unit, or two units at a time, took longer: the ring is short.)
       const int t = threadIdx.x - 32 * S::kSoftWarps;
       const int v_shift = 31 - __clz(v_box);
+      constexpr int kEach = 512 / (32 * kConvWarps);
       const auto unit = [&](const uint32_t *sc, bool is_v, int dead) {
         const uint32_t rs = n % kRaws, us = n % kUnits;
-        constexpr int kEach = 512 / (32 * kConvWarps);
         ok = ok && ptx::mbar_wait(&sh->raw_full[rs], (n / kRaws) & 1, abort, p.budget);
         if (!ok) return;
         const uint4 *src = reinterpret_cast<const uint4 *>(raw + rs * S::kRaw) + t;
+        uint8_t *dst = ring + us * S::kUnit;
         uint4 v[kEach];
         uint32_t scale[kEach];
 #pragma unroll
@@ -695,20 +697,22 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         ok = ptx::mbar_wait(&sh->empty[us], ((n / kUnits) & 1) ^ 1, abort, p.budget);
         if (!ok) return;
-        uint8_t *dst = ring + us * S::kUnit;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
           const int row = i * (8 * kConvWarps) + t / 4, c = 2 * (t & 3);
           const __half2 hi = bits_h2(__byte_perm(scale[i], 0, 0x1010));
           const __half2 lo = bits_h2(__byte_perm(scale[i], 0, 0x3232));
-          const auto scaled = [&](uint32_t codes, uint32_t &a, uint32_t &b) {
-            codes_to_f16x2<KV>(codes, a, b);
-            a = h2_bits(__hfma2(bits_h2(a), hi, __hmul2(bits_h2(a), lo)));
-            b = h2_bits(__hfma2(bits_h2(b), hi, __hmul2(bits_h2(b), lo)));
-          };
           uint32_t h[8];
-          scaled(v[i].x, h[0], h[1]), scaled(v[i].y, h[2], h[3]);
-          scaled(v[i].z, h[4], h[5]), scaled(v[i].w, h[6], h[7]);
+          codes_to_f16x2<KV>(v[i].x, h[0], h[1]), codes_to_f16x2<KV>(v[i].y, h[2], h[3]);
+          codes_to_f16x2<KV>(v[i].z, h[4], h[5]), codes_to_f16x2<KV>(v[i].w, h[6], h[7]);
+          if (is_v) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[k] = h2_bits(__hmul2(bits_h2(h[k]), hi));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              h[k] = h2_bits(__hfma2(bits_h2(h[k]), hi, __hmul2(bits_h2(h[k]), lo)));
+          }
           *reinterpret_cast<uint4 *>(dst + row * 128 + ((c ^ (row & 7)) << 4)) =
               make_uint4(h[0], h[1], h[2], h[3]);
           *reinterpret_cast<uint4 *>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) =
@@ -717,8 +721,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          ptx::mbar_arrive(&sh->raw_empty[rs]);
           ptx::mbar_arrive(&sh->full[us]);
+          ptx::mbar_arrive(&sh->raw_empty[rs]);
         }
         ++n;
       };

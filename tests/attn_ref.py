@@ -67,10 +67,11 @@ def attention(q, k, v, length, scale, window, k_scale=None, v_scale=None):
                 square = np.where(seen, (q[:, h] ** 2) @ (kk ** 2).T, 0.0).max(1, keepdims=True)
                 slip = slip + 8 * FP16 / 3 ** 0.5 * np.sqrt(square) * abs(scale)
                 slip = slip + 2.0 ** -22 * np.abs(q[:, h]).sum(1, keepdims=True) * kt.max() * abs(scale)
-                # A value of v is one fp16 rounding off too, and 2^-22 of the largest
-                # scale so far; a weight's fp16 is of 2^7 times it: off by 2^-32 at most.
-                weight = 2 * FP16
-                floor = floor + 2.0 ** -22 * vt.max() + 2.0 ** -32 * (seen @ np.abs(vv))
+                # A value of v is two fp16 roundings off (its scale's and its own), and
+                # 2^-21 of the largest scale so far (a scale's step at 2^-14 below 2^5, times
+                # 448); a weight's fp16 is of 2^7 times it: off by 2^-32 at most.
+                weight = 3 * FP16
+                floor = floor + 2.0 ** -21 * vt.max() + 2.0 ** -32 * (seen @ np.abs(vv))
             else:
                 # A product t of a weight and a scale enters as fp16 of t 2^7 / r, r a
                 # power of two at or below the row's largest t: fp16 has steps of 2^-24
