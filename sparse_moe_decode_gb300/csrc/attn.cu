@@ -25,8 +25,11 @@ __device__ __forceinline__ void combine(const AttnBatch &a, const AttnArgs &p, i
        t += TOGETHER ? gridDim.x : gridDim.x * kCombineWarps) {
     const int b0 = list[t / tasks], in = t % tasks;
     const AttnOpen o = p.parts.open[b0];
-    const int r = in % row_tasks * side + lane % side;
-    const int d = in / row_tasks * cols + lane / side * (4 * Q);
+    // (neighbouring tasks are columns of the same rows: a tile need not have them all)
+    const int row0 = in / (D / cols) * side;
+    if (row0 >= o.rows) continue;
+    const int r = row0 + lane % side;
+    const int d = in % (D / cols) * cols + lane / side * (4 * Q);
     const int n = o.last - b0 + 1;
     float m = -INFINITY, l = 0.0f;
     float4 v[Q];
@@ -79,7 +82,7 @@ __device__ __forceinline__ void combine(const AttnBatch &a, const AttnArgs &p, i
         }
     }
     if ((!TOGETHER || warp == 0) && r < o.rows) {
-      const int token = (o.row0 + r) / a.group, h = (o.row0 + r) % a.group;
+      const int token = attn_token(a, o.row0 + r), h = o.row0 + r - token * a.group;
       moe_bf16 *dst = p.out + (o.start + token) * p.out_ld + (o.head * a.group + h) * D + d;
       const float f = 1.0f / l;
 #pragma unroll

@@ -24,6 +24,7 @@ struct AttnBatch {
   int32_t cols, N, B, T;
   int32_t group, kv_heads, page_shift, window;
   int32_t pages;
+  uint64_t group_inverse;  // of rows below 2^26: row / group = row * this >> 32
   uint32_t *status;
 };
 
@@ -39,6 +40,7 @@ inline AttnBatch attn_batch(const moe_attn_dims &d, const moe_kv_cache &c, const
   while ((1 << a.page_shift) < d.page_size) ++a.page_shift;
   a.window = d.window;
   a.pages = static_cast<int32_t>(c.pages);
+  a.group_inverse = (uint64_t(1) << 32) / a.group + 1;
   a.status = static_cast<uint32_t *>(ws);
   return a;
 }

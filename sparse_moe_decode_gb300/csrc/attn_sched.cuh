@@ -125,9 +125,16 @@ struct AttnOpen {
   int32_t head, pad[3];
 };
 
+// Token of a tile row and head within its group.
+__device__ __forceinline__ int attn_token(const AttnBatch &a, int row) {
+  return static_cast<int>((static_cast<uint64_t>(row) * a.group_inverse) >> 32);
+}
+
 struct AttnShare {  // in shared memory
   int64_t at, per, total, offset;  // first unit, a share's, all, within the sequence
   int64_t scan[32];
+  int64_t each;  // units of one head of the sequence
+  AttnSeq s;
   int32_t seq;
 };
 
@@ -136,14 +143,15 @@ struct AttnRange {
   int32_t least, most;
 };
 
+// Units of one head of sequence b, which is given back too.
 template <int R, int KT, int C>
 __device__ __forceinline__ int64_t attn_units(const AttnBatch &a, const AttnRange &r, int b,
-                                              bool report) {
-  const AttnSeq s = attn_seq(a, b, report);
+                                              bool report, AttnSeq &s) {
+  s = attn_seq(a, b, report);
   const int rows = s.n * a.group;
   if (s.n == 0 || rows <= r.least || rows > r.most) return 0;
   const AttnTiles<R, KT, C> t(s, a.group, a.window);
-  return t.before(t.count) * a.kv_heads;
+  return t.before(t.count);
 }
 
 // All threads of the block (a multiple of 32, at most 1024): this block's
@@ -152,18 +160,48 @@ template <int R, int KT, int C>
 __device__ __forceinline__ void attn_share(const AttnBatch &a, const AttnRange &r, int least_share,
                                            AttnShare *sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
-  const bool one = a.B <= nt;
-  int64_t mine = 0, sum = 0;
-  for (int b = tid; b < a.B; b += nt) {
-    mine = attn_units<R, KT, C>(a, r, b, blockIdx.x == 0);
-    sum += mine;
-  }
-  // an inclusive scan over the threads of v; the total through sh->scan
-  const auto scan = [&](int64_t v, int64_t &total) {
+  AttnSeq s;
+  const auto find = [&](int64_t at, int64_t total, int64_t per, int64_t each, int64_t incl, int b) {
+    const int64_t first = incl - each * a.kv_heads;
+    if (at >= first && at < incl) sh->seq = b, sh->offset = at - first, sh->each = each, sh->s = s;
+  };
+  const auto share_of = [&](int64_t total) {
+    uint32_t rest;
+    const int64_t per = div_mod(total + gridDim.x - 1, gridDim.x, rest);
+    return per < least_share ? static_cast<int64_t>(least_share) : per;
+  };
+  // an inclusive scan over the warp
+  const auto warp_scan = [&](int64_t v) {
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t n = __shfl_up_sync(0xFFFFFFFFu, v, o);
       if (lane >= o) v += n;
     }
+    return v;
+  };
+  if (tid == 0) sh->seq = -1;
+  if (a.B <= 32) {  // one warp does it
+    if (warp == 0) {
+      __syncwarp();
+      const int64_t each =
+          lane < a.B ? attn_units<R, KT, C>(a, r, lane, blockIdx.x == 0, s) : 0;
+      const int64_t incl = a.B == 1 ? each * a.kv_heads : warp_scan(each * a.kv_heads);
+      const int64_t total = __shfl_sync(0xFFFFFFFFu, incl, a.B - 1);
+      const int64_t per = share_of(total), at = per * blockIdx.x;
+      if (lane == 0) sh->at = at, sh->per = per, sh->total = total;
+      if (lane < a.B && at < total) find(at, total, per, each, incl, lane);
+    }
+    __syncthreads();
+    return;
+  }
+  const bool one = a.B <= nt;
+  int64_t mine = 0, sum = 0;
+  for (int b = tid; b < a.B; b += nt) {
+    mine = attn_units<R, KT, C>(a, r, b, blockIdx.x == 0, s);
+    sum += mine;
+  }
+  // over the threads; the total through sh->scan
+  const auto scan = [&](int64_t v, int64_t &total) {
+    v = warp_scan(v);
     __syncthreads();
     if (lane == 31) sh->scan[warp] = v;
     __syncthreads();
@@ -174,27 +212,21 @@ __device__ __forceinline__ void attn_share(const AttnBatch &a, const AttnRange &
     }
     return v;
   };
-  int64_t total, incl = scan(sum, total);
-  uint32_t rest;
-  int64_t per = div_mod(total + gridDim.x - 1, gridDim.x, rest);
-  if (per < least_share) per = least_share;
-  const int64_t at = per * blockIdx.x;
-  if (tid == 0) {
-    sh->at = at, sh->per = per, sh->total = total;
-    sh->seq = -1;
-  }
+  int64_t total, incl = scan(sum * a.kv_heads, total);
+  const int64_t per = share_of(total), at = per * blockIdx.x;
+  if (tid == 0) sh->at = at, sh->per = per, sh->total = total;
   __syncthreads();
   if (at >= total) return;
   if (one) {
-    if (at >= incl - mine && at < incl) sh->seq = tid, sh->offset = at - (incl - mine);
+    if (tid < a.B) find(at, total, per, mine, incl, tid);
   } else {
     int64_t base = 0;
     for (int b0 = 0; b0 < a.B && base <= at; b0 += nt) {
       const int b = b0 + tid;
-      const int64_t u = b < a.B ? attn_units<R, KT, C>(a, r, b, false) : 0;
+      const int64_t each = b < a.B ? attn_units<R, KT, C>(a, r, b, false, s) : 0;
       int64_t round;
-      incl = base + scan(u, round);
-      if (at >= incl - u && at < incl) sh->seq = b, sh->offset = at - (incl - u);
+      incl = base + scan(each * a.kv_heads, round);
+      if (b < a.B) find(at, total, per, each, incl, b);
       base += round;
     }
   }
@@ -222,27 +254,30 @@ struct AttnWalk {
     if (b < 0) return;
     left = sh.total - sh.at < sh.per ? sh.total - sh.at : sh.per;
     next_unit = sh.at;
-    s = attn_seq(a, b, false);
+    s = sh.s;
     t = AttnTiles<R, KT, C>(s, a.group, a.window);
     int64_t rem = sh.offset;
-    const int64_t each = t.before(t.count);
-    if ((each | rem) >> 32) {
-      head = static_cast<int>(div_wide(rem, each));
-    } else {
-      head = static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(each));
+    head = 0;
+    if (rem >= sh.each) {
+      if ((sh.each | rem) >> 32) head = static_cast<int>(div_wide(rem, sh.each));
+      else head = static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(sh.each));
+      rem -= sh.each * head;
     }
-    rem -= each * head;
     // before(low) <= rem < before(high): the lanes try 32 places at a time
     int low = 0, high = t.count;
+    int64_t first = 0;  // before(low)
     const int lane = threadIdx.x & 31;
     while (high - low > 1) {
       const int step = (high - low + 31) / 32, mid = low + step * lane;
-      const unsigned fits = __ballot_sync(0xFFFFFFFFu, mid < high && t.before(mid) <= rem);
-      low += step * (31 - __clz(fits));  // (lane 0's does)
+      const int64_t there = mid < high ? t.before(mid) : 0;
+      const unsigned fits = __ballot_sync(0xFFFFFFFFu, mid < high && there <= rem);
+      const int last = 31 - __clz(fits);  // (lane 0's does)
+      first = __shfl_sync(0xFFFFFFFFu, there, last);
+      low += step * last;
       high = min(high, low + step);
     }
     tile = low;
-    at = static_cast<int>(rem - t.before(low));
+    at = static_cast<int>(rem - first);
   }
   __device__ __forceinline__ bool next(const AttnBatch &a, const AttnRange &r) {
     if (left <= 0) return false;

@@ -228,7 +228,7 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int at = row0 + min(g + 8 * i, rows - 1);
-        const int token = at / a.group, h = w.head * a.group + at % a.group;
+        const int token = attn_token(a, at), h = w.head * a.group + at - token * a.group;
         pos[i] = ctx + token;
         src[i] = p.q + (w.s.start + token) * p.q_ld + h * D;
         out_row[i] = h;
@@ -288,8 +288,8 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
       for (int j = 0; j < kMine; ++j) qf[(j * 4 + warp) * 32 + lane] = f[j];
       ptx::named_barrier(1, 128);
     }
-    const int first_pos = ctx + row0 / a.group;
-    const int last_pos = ctx + (row0 + rows - 1) / a.group;
+    const int first_pos = ctx + attn_token(a, row0);
+    const int last_pos = ctx + attn_token(a, row0 + rows - 1);
 
     float o[kCols / 8][4];
 #pragma unroll

@@ -54,7 +54,9 @@ struct TcShape {
   static constexpr int kScales = kBytes ? kScaleSlots * 256 * 4 : 0;
   static constexpr int kFixed = kQ + kScales + 2048 + kNQ * 512;  // + barriers, row factors
   static constexpr int kRoom = 232448 - kFixed;
-  static constexpr int kUnits = kBytes ? kRoom / (kUnit + kRaw) : kRoom / kUnit;
+  // (With two query tiles room for converted units pays more than for raw ones: 16
+  // heads of 128, 4096 over 16384, 8 and 3 slots 543 us, 6 and 7 590; one tile: 5 % less)
+  static constexpr int kUnits = kBytes ? kRoom / (kUnit + kRaw) + (kNQ == 2 ? 2 : 0) : kRoom / kUnit;
   static constexpr int kRaws = kBytes ? (kRoom - kUnits * kUnit) / kRaw : 0;
   static constexpr int kSmem = kFixed + kUnits * kUnit + kRaws * kRaw;
   static constexpr int kSoftWarps = 4 * kNQ;
@@ -277,7 +279,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const int r = qi * 128 + wq * 32 + lane;  // this thread's row of the tile
       const bool live = r < rows;
       const int my_row = w.row0 + (live ? r : rows - 1);
-      const int token = my_row / a.group, head = w.head * a.group + my_row % a.group;
+      const int token = attn_token(a, my_row), head = w.head * a.group + my_row - token * a.group;
       const int pos = w.ctx + token;
       const int warp_pos = __shfl_sync(0xFFFFFFFFu, pos, 0);  // the warp's first and last
       const int warp_last = __shfl_sync(0xFFFFFFFFu, pos, 31);
@@ -612,7 +614,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             __syncwarp();
             if (lane < kChunks)
               ptx::tma_load_3d(q_area + (i * kChunks + lane) * 16384, &tm_q, lane * 64,
-                               w.head * a.group, w.start + (w.row0 + 128 * i) / a.group, here, pol);
+                               w.head * a.group, w.start + attn_token(a, w.row0 + 128 * i), here, pol);
           }
         }
         int before = 0, ids = pages_of(w.k0);
@@ -767,8 +769,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             for (int i = 0; i < 2; ++i) {
               s.q0[i] = s.q1[i] = 0;
               if (i < NQ && 128 * i < s.rows) {
-                const int first = s.ctx + (s.row0 + 128 * i) / a.group;
-                const int last = s.ctx + (s.row0 + min(128 * i + 127, s.rows - 1)) / a.group;
+                const int first = s.ctx + attn_token(a, s.row0 + 128 * i);
+                const int last = s.ctx + attn_token(a, s.row0 + min(128 * i + 127, s.rows - 1));
                 s.q0[i] = max(w.k0, a.window && first >= a.window ? (first - a.window + 1) / 128 : 0);
                 s.q1[i] = max(s.q0[i], min(w.k1, last / 128 + 1));
               }
