@@ -32,6 +32,8 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "attn_args.cuh"
 #include "delta_mma.cuh"
 #include "early.cuh"
@@ -552,7 +554,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (warp == S::kFetchWarp) {  // ------------------------------------ fetch
       const uint64_t pol = ptx::policy_evict_last();
       uint32_t n = 0, tiles = 0, q_tiles[2] = {0, 0};
-      constexpr int kSlots = kBytes ? S::kRaws : kUnits;
+      // Slots are waited for, and boxes issued, for a key tile's units together: a box
+      // by itself takes some 65 cycles, more than its bytes where pages are short.
+      // (Codes: one by one, as the conversion leaves them.)
+      constexpr uint32_t kSlots = kBytes ? S::kRaws : kUnits, kGroup = kBytes ? 1 : kChunks;
+      uint32_t slot = 0, phase = 1;
+      const int k_shift = 31 - __clz(k_box), v_shift = 31 - __clz(v_box);
       constexpr int kSlotBytes = kBytes ? S::kRaw : S::kUnit;
       uint8_t *slots = kBytes ? raw : ring;
       uint64_t *full = kBytes ? sh->raw_full : sh->full, *empty = kBytes ? sh->raw_empty : sh->empty;
@@ -572,35 +579,68 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           }
           return id;
         };
-        // the cache's row of a position of the tile whose pages `ids` are
-        const auto row_of = [&](int ids, int kt, int in_tile) {
-          const int id = __shfl_sync(0xFFFFFFFFu, ids, (in_tile >> a.page_shift) & 31);
+        // lane i: the cache's row of position i << shift of the tile whose pages `ids` are
+        const auto rows_of = [&](int ids, int kt, int shift) {
+          const int at = (lane << shift) & 127;
+          const int id = __shfl_sync(0xFFFFFFFFu, ids, at >> a.page_shift);
           return static_cast<int>(
               ((static_cast<int64_t>(id) * a.kv_heads + w.head) << a.page_shift) +
-              ((kt * 128 + in_tile) & (page - 1)));
+              ((kt * 128 + at) & (page - 1)));
         };
-        const auto unit = [&](const CUtensorMap *tm, int ids, int kt, int at, int keys, int box,
-                              int bytes, int col) {
-          // `keys` keys from `at` of the tile, in boxes of `box`; `bytes` each
-          const uint32_t slot = n % kSlots;
-          if (!(ok = ptx::mbar_wait(&empty[slot], ((n / kSlots) & 1) ^ 1, abort, p.budget))) return;
-          const int there = len - kt * 128 - at;
-          const int have = there <= 0 ? 0 : min(keys / box, (there + box - 1) / box);
-          if (lane == 0) ptx::mbar_expect_tx(&full[slot], have * box * bytes);
+        // Units of K or V from the tile's `first`, kGroup of them; box i of the tile
+        // comes from row `rows` of lane i, and positions there are `there`.
+        const auto units = [&](const CUtensorMap *tm, int rows, auto which, int first, int there) {
+          constexpr bool is_v = which.value;
+          uint32_t mine = slot + lane % kGroup, parity = phase;
+          if (mine >= kSlots) mine -= kSlots, parity ^= 1;
+          ok = ptx::mbar_wait(&empty[mine], parity, abort, p.budget);
+          if (kGroup > 1) ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) return;
+          // a unit's boxes; a unit of K has the tile's, one of V its share of them
+          constexpr int kKeys = is_v ? S::kVKeys : 128, kRow = (is_v ? D : 64) * (kBytes ? 1 : 2);
+          constexpr int kKeyBits = kKeys == 128 ? 7 : kKeys == 64 ? 6 : 5;
+          const int shift = is_v ? v_shift : k_shift, per_shift = kKeyBits - shift;
+          const int bytes = kRow << shift, b0 = is_v ? first << per_shift : 0;
+          const int all = min((is_v ? kGroup : 1) << per_shift, ((there - 1) >> shift) + 1 - b0);
+          if (lane < kGroup) {
+            const int have = is_v ? min(max(all - (lane << per_shift), 0), 1 << per_shift) : all;
+            ptx::mbar_expect_tx(&full[mine], have * bytes);
+          }
+          const auto box = [&](int i, int row) {
+            const int at = (is_v ? i & ((1 << per_shift) - 1) : i) * bytes;
+#pragma unroll
+            for (int c = 0; c < (is_v ? 1 : kGroup); ++c) {
+              uint32_t to = slot + (is_v ? i >> per_shift : c);
+              if (to >= kSlots) to -= kSlots;
+              ptx::tma_load_3d(slots + to * kSlotBytes + at, tm, 0, row, is_v ? 0 : first + c,
+                               &full[to], pol);
+            }
+          };
+          if (kGroup == 1) {
+            const int row = __shfl_sync(0xFFFFFFFFu, rows, b0 + lane);
+            if (lane < all) box(lane, row);
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < all; i += 2) {
+              const int r0 = __shfl_sync(0xFFFFFFFFu, rows, b0 + i);
+              const int r1 = __shfl_sync(0xFFFFFFFFu, rows, b0 + i + 1);
+              if (elect_one()) {
+                box(i, r0);
+                if (i + 1 < all) box(i + 1, r1);
+              }
+            }
+          }
           __syncwarp();
-          const int row = row_of(ids, kt, (at + lane * box) & 127);
-          if (lane < have)
-            ptx::tma_load_3d(slots + slot * kSlotBytes + lane * box * bytes, tm, 0, row, col,
-                             &full[slot], pol);
-          ++n;
+          n += kGroup, slot += kGroup;
+          if (slot >= kSlots) slot -= kSlots, phase ^= 1;
         };
-        const auto k_units = [&](int ids, int kt) {
-          for (int c = 0; c < kChunks && ok; ++c)
-            unit(&tm_k, ids, kt, 0, 128, k_box, kBytes ? 64 : 128, c);
+        const auto k_units = [&](int rows, int kt) {
+          for (int c = 0; c < kChunks && ok; c += kGroup)
+            units(&tm_k, rows, std::false_type(), c, len - kt * 128);
         };
         const auto v_units = [&](int ids, int kt) {
-          for (int u = 0; u < kChunks && ok; ++u)
-            unit(&tm_v, ids, kt, u * S::kVKeys, S::kVKeys, v_box, D * (kBytes ? 1 : 2), 0);
+          const int rows = rows_of(ids, kt, v_shift);
+          for (int u = 0; u < kChunks && ok; u += kGroup) units(&tm_v, rows, std::true_type(), u, len - kt * 128);
         };
         if (p.q_copy) {
           // (rows behind the sequence's last are of no use and do no harm)
@@ -622,24 +662,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           const int next = kt < w.k1 ? pages_of(kt + 1) : 0;
           if (NQ == 2 && kt > w.k0) v_units(before, kt - 1);
           if (kt < w.k1) {
+            const int rows = rows_of(ids, kt, k_shift);
             if (kBytes && ok) {
               const uint32_t slot = tiles % S::kScaleSlots;
               ok = ptx::mbar_wait(&sh->scale_empty[slot], ((tiles / S::kScaleSlots) & 1) ^ 1, abort,
                                   p.budget);
               if (!ok) break;
-              const int there = len - kt * 128;
-              const int have = min(128 / k_box, (there + k_box - 1) / k_box);
-              if (lane == 0) ptx::mbar_expect_tx(&sh->scale_raw[slot], 2 * have * k_box * 4);
+              const int have = min(128 >> k_shift, ((len - kt * 128 - 1) >> k_shift) + 1);
+              if (elect_one()) ptx::mbar_expect_tx(&sh->scale_raw[slot], 2 * have * k_box * 4);
               __syncwarp();
-              const int row = row_of(ids, kt, (lane * k_box) & 127);
               if (lane < have) {
-                float *dst = scales + slot * 256 + lane * k_box;
-                bulk_load(ptx::smem_u32(dst), p.k_scale + row, k_box * 4, &sh->scale_raw[slot]);
-                bulk_load(ptx::smem_u32(dst + 128), p.v_scale + row, k_box * 4, &sh->scale_raw[slot]);
+                const uint32_t dst = ptx::smem_u32(scales + slot * 256 + lane * k_box);
+                bulk_load(dst, p.k_scale + rows, k_box * 4, &sh->scale_raw[slot]);
+                bulk_load(dst + 512, p.v_scale + rows, k_box * 4, &sh->scale_raw[slot]);
               }
               ++tiles;
             }
-            if (ok) k_units(ids, kt);
+            if (ok) k_units(rows, kt);
           }
           if (NQ == 1 && kt > w.k0 && ok) v_units(before, kt - 1);
           before = ids, ids = next;
