@@ -554,10 +554,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (warp == S::kFetchWarp) {  // ------------------------------------ fetch
       const uint64_t pol = ptx::policy_evict_last();
       uint32_t n = 0, tiles = 0, q_tiles[2] = {0, 0};
-      // Slots are waited for, and boxes issued, for a key tile's units together: a box
-      // by itself takes some 65 cycles, more than its bytes where pages are short.
-      // (Codes: one by one, as the conversion leaves them.)
-      constexpr uint32_t kSlots = kBytes ? S::kRaws : kUnits, kGroup = kBytes ? 1 : kChunks;
+      // With 8 units a key tile (16 heads of 256, bf16) this warp would be what bounds
+      // the kernel: there one lane issues a key tile's copies, some 25 cycles each, with
+      // all their slots waited for together (pages of 64: 1130 -> 1350 TFLOP/s, of 16:
+      // 820 -> 1265).  With 4 units, or where the conversion leaves slots one by one,
+      // lanes with a copy each, some 65 cycles, take 1 to 10 % less than that.
+      constexpr uint32_t kSlots = kBytes ? S::kRaws : kUnits, kGroup = !kBytes && NQ == 1 ? kChunks : 1;
       uint32_t slot = 0, phase = 1;
       const int k_shift = 31 - __clz(k_box), v_shift = 31 - __clz(v_box);
       constexpr int kSlotBytes = kBytes ? S::kRaw : S::kUnit;
