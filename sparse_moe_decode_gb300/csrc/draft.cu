@@ -156,6 +156,9 @@ verify_draft_kernel(const DraftArgs a) {
   const int b = blockIdx.x / cluster_size;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   early_begin();
+  // (no block writes to another's shared memory before that one is there)
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  const auto all_here = [] { asm volatile("barrier.cluster.wait;" ::: "memory"); };
   const int32_t *drafted = a.draft_tokens + static_cast<int64_t>(b) * a.T;
   const float *u = a.uniform + static_cast<int64_t>(b) * (a.T + 1);
   const float r = u[a.T];
@@ -198,6 +201,7 @@ verify_draft_kernel(const DraftArgs a) {
     }
   };
   if (token >= a.V) {  // not a token (all blocks of the cluster)
+    all_here();
     refuse(MOE_DEV_BAD_INDEX);
     return;
   }
@@ -231,6 +235,7 @@ verify_draft_kernel(const DraftArgs a) {
     bits = __reduce_max_sync(0xFFFFFFFFu, bits);
     if (lane == 0) sh->warp_worst[warp] = bits, sh->warp_sum[warp] = part;
     __syncthreads();
+    if (round == 0) all_here();
     if (tid < cluster_size) {  // every block hears of every other's
       Pair t = sh->warp_sum[0];
       uint32_t x = sh->warp_worst[0];

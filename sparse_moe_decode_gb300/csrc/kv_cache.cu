@@ -2,12 +2,19 @@
 //
 // A row is one token's D values of one head of k or v; D / 8 lanes take it, 16
 // bytes of bf16 each, and find its scale by shuffles.  Bound by memory: a row
-// is read and written once.
+// is read and written once.  Two rows a thread, their loads on the way together
+// (8192 tokens of 8 heads of 128, e4m3, written and read back: one 32.2 us, two
+// and four 25.8, eight 30.6; for a few tokens no difference).  That is 3.9 TB/s:
+// of a call's 12.9 us some 4 are a launch's start and end, and loads of lengths and
+// pages before the first row moves.
 //
-// int8: c = x / s with the exact quotient rounded.  With f = floor(x * (1 / s)),
-// off by one at most where x / s is next to a whole number, the sign of
-// x - (f + 1/2) s, which one fused multiply-add gives exactly, says which of
-// f and f + 1 is nearest, or that x / s lies between them.
+// int8: c is x / s, the exact quotient, rounded to the nearest.  c1, x times the
+// rounded inverse, rounded, is off by one at most, and d = x - c1 s is exact: it is
+// a multiple of s's last place and no larger than s, or c1 is 0.  So c = c1 where
+// |d| <= s / 2, else its neighbour towards d.  Where x / s lies in the middle c has
+// to be even, and c1 is: (c + 1/2) s with s of 24 digits has the 8 of x only where s
+// is a power of two (s = max / 127 rounded is one, or has no end within 24 digits),
+// and then its inverse is exact.
 // e4m3: s is a power of two, so x / s is exact and the conversion rounds once.
 #include "attn.h"
 #include "attn_sched.cuh"
@@ -18,6 +25,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kEach = 2;  // rows a thread
 
 struct KvSide {  // of k or v
   const moe_bf16 *in;
@@ -80,13 +88,10 @@ __device__ __forceinline__ void kv_scale(float top, float &s, float &inv) {
 }
 
 __device__ __forceinline__ uint32_t int8_code(float x, float s, float inv) {
-  const float v = fabsf(x), f = floorf(v * inv);
-  const float d = fmaf(-(f + 0.5f), s, v);
-  float c = d > 0.0f ? f + 1.0f : f;
-  // in the middle: the even one (f is below 2^23: half of it is exact)
-  if (d == 0.0f) c = f + 2.0f * (0.5f * f - floorf(0.5f * f));
   // 1.5 * 2^23 + c: the low byte is c in two's complement
-  return __float_as_uint(copysignf(c, x) + 12582912.0f);
+  constexpr float kPlace = 12582912.0f;
+  const float c = fmaf(x, inv, kPlace), d = fmaf(kPlace - c, s, x);
+  return __float_as_uint(fabsf(d) > 0.5f * s ? c + copysignf(1.0f, d) : c);
 }
 
 template <int KV>
@@ -136,7 +141,7 @@ __device__ __forceinline__ void kv_values(uint2 c, float (&x)[8]) {
 }
 
 // Row i of `rows`: token i / (2 heads), k's heads and then v's.
-template <int D, int KV, bool WRITE, int EACH>
+template <int D, int KV, bool WRITE>
 __global__ void __launch_bounds__(kThreads)
 kv_rows_kernel(const AttnBatch a, const KvSide k, const KvSide v, uint32_t rows) {
   constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
@@ -144,16 +149,16 @@ kv_rows_kernel(const AttnBatch a, const KvSide k, const KvSide v, uint32_t rows)
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.B; b += kThreads) attn_seq(a, b, true);
   const int l = threadIdx.x % kLanes;
-  const uint32_t first = blockIdx.x * (kRows * EACH) + threadIdx.x / kLanes;
+  const uint32_t first = blockIdx.x * (kRows * kEach) + threadIdx.x / kLanes;
   const uint32_t heads2 = 2 * a.kv_heads;
   // (chosen by selects: an index would put the arguments into local memory)
 #define OF(e, field) (kv[e] ? v.field : k.field)
-  int64_t place[EACH];
-  uint32_t token[EACH];
-  int kv[EACH], head[EACH];
-  uint4 data[EACH];
+  int64_t place[kEach];
+  uint32_t token[kEach];
+  int kv[kEach], head[kEach];
+  uint4 data[kEach];
 #pragma unroll
-  for (int e = 0; e < EACH; ++e) {
+  for (int e = 0; e < kEach; ++e) {
     const uint32_t i = first + e * kRows;
     token[e] = i / heads2;
     const int h = i % heads2;
@@ -165,11 +170,11 @@ kv_rows_kernel(const AttnBatch a, const KvSide k, const KvSide v, uint32_t rows)
   AttnSeq s;
   int b = -1;
 #pragma unroll
-  for (int e = 0; e < EACH; ++e)
+  for (int e = 0; e < kEach; ++e)
     place[e] = first + e * kRows < rows ? kv_place(a, token[e], head[e], s, b) : -1;
   if (WRITE) {
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) {
+    for (int e = 0; e < kEach; ++e) {
       if (KV == MOE_KV_BF16) {
         if (place[e] >= 0)
           *reinterpret_cast<uint4 *>(static_cast<moe_bf16 *>(OF(e, store)) + place[e] * D + l * 8) =
@@ -197,9 +202,9 @@ kv_rows_kernel(const AttnBatch a, const KvSide k, const KvSide v, uint32_t rows)
       }
     }
   } else {
-    float scale[EACH];
+    float scale[kEach];
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) {
+    for (int e = 0; e < kEach; ++e) {
       if (!OF(e, out)) place[e] = -1;
       if (place[e] < 0) continue;
       const uint8_t *from = static_cast<const uint8_t *>(OF(e, store));
@@ -212,7 +217,7 @@ kv_rows_kernel(const AttnBatch a, const KvSide k, const KvSide v, uint32_t rows)
       }
     }
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) {
+    for (int e = 0; e < kEach; ++e) {
       if (place[e] < 0) continue;
       if (KV != MOE_KV_BF16) {
         float x[8];
@@ -234,12 +239,9 @@ template <int D, int KV, bool WRITE>
 cudaError_t launch_rows(const AttnBatch &a, const KvSide (&io)[2], cudaStream_t s) {
   constexpr int kRows = kThreads / (D / 8);
   const uint32_t rows = 2u * a.N * a.kv_heads;
-  const auto go = [&](auto kernel, int each) {
-    const uint32_t per = kRows * each;
-    return launch_early(kernel, dim3((rows + per - 1) / per), kThreads, 0, s, a, io[0], io[1], rows);
-  };
-  if (rows <= 8u * kRows * 152) return go(kv_rows_kernel<D, KV, WRITE, 1>, 1);
-  return go(kv_rows_kernel<D, KV, WRITE, 4>, 4);
+  const uint32_t per = kRows * kEach;
+  return launch_early(kv_rows_kernel<D, KV, WRITE>, dim3((rows + per - 1) / per), kThreads, 0, s, a,
+                      io[0], io[1], rows);
 }
 
 template <int D, bool WRITE>
