@@ -19,14 +19,31 @@
 // K and V come through a ring of 16 KB units: K 128 keys by 64 columns
 // (K-major operand), V as many keys as fill one by all columns (MN-major
 // operand: a key's values lie along N).  8-bit codes come through a ring of
-// their own and four warps make fp16 of them, exactly; scales multiply the
-// columns of S, and the weights of the values (see attn_stream.cuh, whose
-// power of two a row this kernel has too).
+// their own and become fp16 code * scale (rounded once) under a power of two a
+// key tile, for the values one that only grows within a segment; O follows it.
+// Weights are then fp16 under 2^7.  Exact codes, with the scales on S's columns
+// and on the weights as the streaming kernel has them, cost the softmax's
+// threads more than the conversion: 1370 us for what takes 963 now.
 //
-// Warps: 4 NQ softmax, 4 that convert (8-bit), one that fetches, one that
-// issues the products.  Every wait is bounded; after one that gave up, all
-// later ones do at once, copies and products in flight are waited for, and
-// MOE_DEV_TIMEOUT is set.
+// Warps: 4 NQ softmax; 4 (NQ = 2) or 8 that convert; one that fetches; NQ that
+// issue products, a query tile each and by turns, so that while one waits for
+// its weights the other's products run; one that plans the segments one ahead
+// (every warp for itself: 61 us for a prompt of 2048, 52 now) and prepares the scales.
+// Registers move from the others to the softmax.  Every wait is bounded; after
+// one that gave up, all later ones do at once, copies and products in flight
+// are waited for, and MOE_DEV_TIMEOUT is set.
+//
+// Measured, 4096 tokens over 16384, 16 heads on 4, pages of 64 (TFLOP/s of the
+// products below the diagonal; 1910 measured for a plain bf16 product):
+//   head_dim       64    128    256
+//   bf16          895   1550   1350
+//   int8          570    968    780
+//   e4m3          570    960    790
+// 64: the exponentials, one for each 4 * 64 operations.  128: tensor cores,
+// less the turns' gaps.  256 (one query tile): each K and V is read by 128
+// rows, 128 KB a key tile from the L2.  8-bit: the conversion, its
+// reads and writes of shared memory beside the products' own.  Short prompts:
+// some 8 us from launch to the first product, and the join.
 #pragma once
 
 #include <cuda.h>

@@ -91,7 +91,8 @@ __device__ __forceinline__ uint32_t int8_code(float x, float s, float inv) {
   // 1.5 * 2^23 + c: the low byte is c in two's complement
   constexpr float kPlace = 12582912.0f;
   const float c = fmaf(x, inv, kPlace), d = fmaf(kPlace - c, s, x);
-  return __float_as_uint(fabsf(d) > 0.5f * s ? c + copysignf(1.0f, d) : c);
+  // (half of a scale next to 2^-126 may have no last place: d does not reach between)
+  return __float_as_uint(fabsf(d) > __fmul_rz(0.5f, s) ? c + copysignf(1.0f, d) : c);
 }
 
 template <int KV>
