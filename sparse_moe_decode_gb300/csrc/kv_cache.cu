@@ -1,12 +1,11 @@
 // kv_cache.cu -- the paged cache's rows written (and quantised) and read back.
 //
 // A row is one token's D values of one head of k or v; D / 8 lanes take it, 16
-// bytes of bf16 each, and find its scale by shuffles.  Bound by memory: a row
-// is read and written once.  Two rows a thread, their loads on the way together
-// (8192 tokens of 8 heads of 128, e4m3, written and read back: one 32.2 us, two
-// and four 25.8, eight 30.6; for a few tokens no difference).  That is 3.9 TB/s:
-// of a call's 12.9 us some 4 are a launch's start and end, and loads of lengths and
-// pages before the first row moves.
+// bytes of bf16 each, and find its scale by shuffles; the same lanes take k and v,
+// whose place in the cache they look up once, and a block one head's rows of some
+// tokens.  A row is read and written once: 8192 tokens of 8 heads of 128 in e4m3,
+// written and read back, 19.8 us, 5.1 TB/s.  (Rows of all heads and of k and v one
+// after another, each with its own look-up, were bound by their instructions: 25.8.)
 //
 // int8: c is x / s, the exact quotient, rounded to the nearest.  c1, x times the
 // rounded inverse, rounded, is off by one at most, and d = x - c1 s is exact: it is
@@ -19,13 +18,13 @@
 #include "attn.h"
 #include "attn_sched.cuh"
 #include "early.cuh"
+#include "kernels.h"
 
 namespace moe {
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kEach = 2;  // rows a thread
 
 struct KvSide {  // of k or v
   const moe_bf16 *in;
@@ -141,108 +140,112 @@ __device__ __forceinline__ void kv_values(uint2 c, float (&x)[8]) {
   }
 }
 
-// Row i of `rows`: token i / (2 heads), k's heads and then v's.
-template <int D, int KV, bool WRITE>
+// Block (x, y): kRows * EACH tokens' rows of k and v of head y.
+template <int D, int KV, bool WRITE, int EACH>
 __global__ void __launch_bounds__(kThreads)
-kv_rows_kernel(const AttnBatch a, const KvSide k, const KvSide v, uint32_t rows) {
+kv_rows_kernel(const AttnBatch a, const KvSide k, const KvSide v) {
   constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
   early_begin();
-  if (blockIdx.x == 0)
+  if (blockIdx.x + blockIdx.y == 0)
     for (int b = threadIdx.x; b < a.B; b += kThreads) attn_seq(a, b, true);
-  const int l = threadIdx.x % kLanes;
-  const uint32_t first = blockIdx.x * (kRows * kEach) + threadIdx.x / kLanes;
-  const uint32_t heads2 = 2 * a.kv_heads;
-  // (chosen by selects: an index would put the arguments into local memory)
-#define OF(e, field) (kv[e] ? v.field : k.field)
-  int64_t place[kEach];
-  uint32_t token[kEach];
-  int kv[kEach], head[kEach];
-  uint4 data[kEach];
+  const int l = threadIdx.x % kLanes, head = blockIdx.y;
+  const int first = blockIdx.x * (kRows * EACH) + threadIdx.x / kLanes;
+  // (places and sides by constants: an index would put them into local memory)
+  const auto side = [&](int i) -> const KvSide & { return i % 2 ? v : k; };
+  uint4 data[2 * EACH];
+  if (WRITE) {
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    const uint32_t i = first + e * kRows;
-    token[e] = i / heads2;
-    const int h = i % heads2;
-    kv[e] = h >= a.kv_heads;
-    head[e] = kv[e] ? h - a.kv_heads : h;
-    if (WRITE && i < rows)
-      data[e] = ld_nc(OF(e, in) + token[e] * OF(e, ld) + head[e] * D + l * 8);
+    for (int i = 0; i < 2 * EACH; ++i) {
+      const int t = first + i / 2 * kRows;
+      if (t < a.N) data[i] = ld_nc(side(i).in + t * side(i).ld + head * D + l * 8);
+    }
   }
+  int64_t place[EACH];
   AttnSeq s;
   int b = -1;
 #pragma unroll
-  for (int e = 0; e < kEach; ++e)
-    place[e] = first + e * kRows < rows ? kv_place(a, token[e], head[e], s, b) : -1;
+  for (int e = 0; e < EACH; ++e) {
+    const int t = first + e * kRows;
+    place[e] = t < a.N ? kv_place(a, t, head, s, b) : -1;
+  }
   if (WRITE) {
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
+    for (int i = 0; i < 2 * EACH; ++i) {
+      const int64_t at = place[i / 2];
       if (KV == MOE_KV_BF16) {
-        if (place[e] >= 0)
-          *reinterpret_cast<uint4 *>(static_cast<moe_bf16 *>(OF(e, store)) + place[e] * D + l * 8) =
-              data[e];
+        if (at >= 0)
+          *reinterpret_cast<uint4 *>(static_cast<moe_bf16 *>(side(i).store) + at * D + l * 8) =
+              data[i];
         continue;
       }
-      const uint32_t w[4] = {data[e].x, data[e].y, data[e].z, data[e].w};
+      const uint32_t w[4] = {data[i].x, data[i].y, data[i].z, data[i].w};
       float x[8];
-      uint32_t most = 0;  // magnitudes order like their bits, inf and NaN above all
+      // magnitudes order like their bits, inf and NaN above all; two at a time
+      uint32_t both = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         x[2 * j] = bf16_lo(w[j]), x[2 * j + 1] = bf16_hi(w[j]);
-        most = max(most, max((w[j] << 16) & 0x7FFF0000u, w[j] & 0x7FFF0000u));
+        both = __vmaxu2(both, w[j] & 0x7FFF7FFFu);
       }
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1)
-        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+        both = __vmaxu2(both, __shfl_xor_sync(0xFFFFFFFFu, both, o));
+      const uint32_t most = max(both << 16, both & 0xFFFF0000u);
       float scale, inv;
       kv_scale<KV>(__uint_as_float(most), scale, inv);
       uint2 c = kv_codes<KV>(x, scale, inv);
       if (most >= 0x7F800000u) c = make_uint2(0, 0), scale = __uint_as_float(0x7FC00000u);
-      if (place[e] >= 0) {
-        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(OF(e, store)) + place[e] * D + l * 8) = c;
-        if (l == 0) OF(e, scale)[place[e]] = scale;
+      if (at >= 0) {
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(side(i).store) + at * D + l * 8) = c;
+        if (l == 0) side(i).scale[at] = scale;
       }
     }
   } else {
-    float scale[kEach];
+    float scale[2 * EACH];
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      if (!OF(e, out)) place[e] = -1;
-      if (place[e] < 0) continue;
-      const uint8_t *from = static_cast<const uint8_t *>(OF(e, store));
+    for (int i = 0; i < 2 * EACH; ++i) {
+      const int64_t at = place[i / 2];
+      if (at < 0 || !side(i).out) continue;
+      const uint8_t *from = static_cast<const uint8_t *>(side(i).store);
       if (KV == MOE_KV_BF16) {
-        data[e] = *reinterpret_cast<const uint4 *>(from + (place[e] * D + l * 8) * 2);
+        data[i] = *reinterpret_cast<const uint4 *>(from + (at * D + l * 8) * 2);
       } else {
-        const uint2 c = *reinterpret_cast<const uint2 *>(from + place[e] * D + l * 8);
-        data[e].x = c.x, data[e].y = c.y;
-        scale[e] = OF(e, scale)[place[e]];
+        const uint2 c = *reinterpret_cast<const uint2 *>(from + at * D + l * 8);
+        data[i].x = c.x, data[i].y = c.y;
+        scale[i] = side(i).scale[at];
       }
     }
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      if (place[e] < 0) continue;
+    for (int i = 0; i < 2 * EACH; ++i) {
+      if (place[i / 2] < 0 || !side(i).out) continue;
       if (KV != MOE_KV_BF16) {
         float x[8];
-        kv_values<KV>(make_uint2(data[e].x, data[e].y), x);
+        kv_values<KV>(make_uint2(data[i].x, data[i].y), x);
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          w[j] = bf16x2_of(x[2 * j] * scale[e], x[2 * j + 1] * scale[e]);
-        data[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          w[j] = bf16x2_of(x[2 * j] * scale[i], x[2 * j + 1] * scale[i]);
+        data[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      *reinterpret_cast<uint4 *>(OF(e, out) + token[e] * OF(e, ld) + head[e] * D + l * 8) =
-          data[e];
+      const int t = first + i / 2 * kRows;
+      *reinterpret_cast<uint4 *>(side(i).out + t * side(i).ld + head * D + l * 8) = data[i];
     }
   }
-#undef OF
 }
 
 template <int D, int KV, bool WRITE>
 cudaError_t launch_rows(const AttnBatch &a, const KvSide (&io)[2], cudaStream_t s) {
-  constexpr int kRows = kThreads / (D / 8);
-  const uint32_t rows = 2u * a.N * a.kv_heads;
-  const uint32_t per = kRows * kEach;
-  return launch_early(kv_rows_kernel<D, KV, WRITE>, dim3((rows + per - 1) / per), kThreads, 0, s, a,
-                      io[0], io[1], rows);
+  const auto go = [&](auto kernel, int tokens) {
+    return launch_early(kernel, dim3((a.N + tokens - 1) / tokens, a.kv_heads), kThreads, 0, s, a,
+                        io[0], io[1]);
+  };
+  // Two tokens a thread from 12 blocks an SM of one each (8 run at once): 4096 tokens of
+  // 8 heads of 128 in e4m3 10.7 and 10.1 us, 16384 38.3 and 33.7; 1536 blocks 8.8 and
+  // 9.3, 256 4.2 and 4.7.  (Four: 21.3 us where two take 19.8.)
+  constexpr int kTokens = kThreads / (D / 8);
+  if ((a.N + kTokens - 1) / kTokens * static_cast<int64_t>(a.kv_heads) < 12 * tc_sm_count())
+    return go(kv_rows_kernel<D, KV, WRITE, 1>, kTokens);
+  return go(kv_rows_kernel<D, KV, WRITE, 2>, 2 * kTokens);
 }
 
 template <int D, bool WRITE>
