@@ -600,9 +600,10 @@ class PagedAttention:
     out of range are not followed, and ``status`` tells.
 
     ``kv_type`` is "bf16", or "int8" or "e4m3" with a scale for each token and
-    head, quantised as it is written (see ``moe_gb300.h``).  ``window`` W > 0
-    lets a token see only the last W positions up to its own.  One object serves
-    all layers of its shape; its workspace belongs to one stream at a time.
+    head, quantised as it is written (see ``moe_gb300.h``, which also says how
+    far each product is rounded).  ``window`` W > 0 lets a token see only the last W
+    positions up to its own.  One object serves all layers of its shape; its
+    workspace belongs to one stream at a time.
     With ``stream`` given, results are made in that stream's memory.  For
     inference: results carry no gradient, whether an input requires one or not.
     """

@@ -38,7 +38,7 @@
 //   head_dim       64    128    256
 //   bf16          895   1550   1350
 //   int8          570    968    780
-//   e4m3          570    960    790
+//   e4m3          575    950    840
 // 64: the exponentials, one for each 4 * 64 operations.  128: tensor cores,
 // less the turns' gaps.  256 (one query tile): each K and V is read by 128
 // rows, 128 KB a key tile from the L2.  8-bit: the conversion, its
