@@ -502,7 +502,8 @@ moe_status moe_paged_attention(const moe_attn_dims *dims, const moe_kv_cache *ca
 
 /* Which tokens of a draft stand: B sequences with up to T drafted tokens
  * d_i and the target's probabilities p_0 .. p_T (p_i after i of them), the
- * drafter's q_i, and numbers u_i and r = u_T, uniform in [0, 1).
+ * drafter's q_i, and numbers u_i and r = u_T, uniform in [0, 1) (an r below 0
+ * or NaN counts as 0, one of 1 or more takes the last token with any weight).
  *   accepted = the first i with d_i < 0 (the draft ends there) or not
  *              u_i * q_i(d_i) < p_i(d_i), else T;
  *   tokens   = d_0 .. d_(accepted - 1), one more, then -1;

@@ -9,6 +9,7 @@
 
 namespace moe {
 
+constexpr int64_t kMaxPositions = int64_t(1) << 30;  // of a sequence
 constexpr int kAttnMaxGroup = 64;  // query heads of a key/value head
 // Blocks of an attention kernel: what the workspace has room for.
 constexpr int kStreamMaxCtas = 480;
@@ -38,7 +39,7 @@ inline AttnBatch attn_batch(const moe_attn_dims &d, const moe_kv_cache &c, const
   a.group = d.q_heads / d.kv_heads, a.kv_heads = d.kv_heads;
   a.page_shift = 0;
   while ((1 << a.page_shift) < d.page_size) ++a.page_shift;
-  a.window = d.window;
+  a.window = d.window < kMaxPositions ? d.window : 0;  // (places plus it stay in 32 bits)
   a.pages = static_cast<int32_t>(c.pages);
   a.group_inverse = (uint64_t(1) << 32) / a.group + 1;
   a.status = static_cast<uint32_t *>(ws);

@@ -14,7 +14,6 @@ namespace {
 
 constexpr int kMaxTokens = 1 << 20, kMaxSeqs = 65536, kMaxHeads = 1024;
 constexpr int64_t kMaxRows = int64_t(1) << 31;       // of a cache (coordinates of a copy)
-constexpr int64_t kMaxPositions = int64_t(1) << 30;  // of a sequence
 constexpr int kMaxDraft = 1024, kMaxVocab = 1 << 24;
 
 moe_status check_dims(const moe_attn_dims *d) {

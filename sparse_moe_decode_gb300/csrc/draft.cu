@@ -161,7 +161,7 @@ verify_draft_kernel(const DraftArgs a) {
   const auto all_here = [] { asm volatile("barrier.cluster.wait;" ::: "memory"); };
   const int32_t *drafted = a.draft_tokens + static_cast<int64_t>(b) * a.T;
   const float *u = a.uniform + static_cast<int64_t>(b) * (a.T + 1);
-  const float r = u[a.T];
+  const float r = fmaxf(u[a.T], 0.0f);  // (a NaN is 0; from 1 on the last weight is taken)
   if (warp == 0) {
     int stop = a.T, token = -1;
     for (int i0 = 0; i0 < a.T; i0 += 32) {

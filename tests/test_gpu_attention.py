@@ -214,6 +214,17 @@ def test_negative_scale(env):
         b.check(b.attend())
 
 
+@pytest.mark.parametrize("new", [1, 60])
+def test_windows_longer_than_any_sequence(env, new):
+    import torch
+    b = Batch(env, [new] * 2, [700, 400], (8, 2), 64, 16, "bf16", uniform=True).fill()
+    want = b.attend()
+    for window in (700, 1 << 30, 2 ** 31 - 1):
+        b.attn = env[0].PagedAttention(8, 2, 64, 16, "bf16", window, device=env[1])
+        assert torch.equal(b.attend(), want)
+    b.check(want)
+
+
 @pytest.mark.parametrize("kv", KV)
 @pytest.mark.parametrize("new", [[1, 1, 1], [3, 140, 1], [200, 300, 150]])
 def test_values_that_are_not_finite_stay_in_their_sequence(env, kv, new):

@@ -184,6 +184,20 @@ def test_refused_values(env):
     assert accepted.item() == 2 and v.status() == 0
 
 
+def test_numbers_out_of_range(env):
+    """Below 0 and NaN as 0, from 1 on the last weight."""
+    import torch
+    moe, dev = env
+    p = torch.zeros((6, 1, 3000), device=dev)
+    p[:, 0, 1000], p[:, 0, 2000] = 0.25, 0.75
+    none = torch.empty((6, 0), dtype=torch.int32, device=dev)
+    u = torch.tensor([-1.0, float("nan"), -float("inf"), 1.0, 7.0, float("inf")], device=dev)
+    v = moe.DraftVerifier(device=dev)
+    tokens, accepted = v.verify(p, none, u[:, None])
+    assert tokens[:, 0].tolist() == [1000] * 3 + [2000] * 3
+    assert (accepted == 0).all() and v.status() == 0
+
+
 def test_outputs_capture_and_checks(env):
     import torch
     moe, dev = env
