@@ -23,7 +23,7 @@
 // key tile, for the values one that only grows within a segment; O follows it.
 // Weights are then fp16 under 2^7.  Exact codes, with the scales on S's columns
 // and on the weights as the streaming kernel has them, cost the softmax's
-// threads more than the conversion: 1370 us for what takes 963 now.
+// threads more than the conversion: 1370 us for what takes 892 now.
 //
 // Warps: 4 NQ softmax; 4 (NQ = 2) or 8 that convert; one that fetches; NQ that
 // issue products, a query tile each and by turns, so that while one waits for
@@ -36,9 +36,9 @@
 // Measured, 4096 tokens over 16384, 16 heads on 4, pages of 64 (TFLOP/s of the
 // products below the diagonal; 1910 measured for a plain bf16 product):
 //   head_dim       64    128    256
-//   bf16          895   1550   1350
-//   int8          570    968    780
-//   e4m3          575    950    840
+//   bf16          875   1540   1380
+//   int8          698   1045    780
+//   e4m3          670   1065    865
 // 64: the exponentials, one for each 4 * 64 operations.  128: tensor cores,
 // less the turns' gaps.  256 (one query tile): each K and V is read by 128
 // rows, 128 KB a key tile from the L2.  8-bit: the conversion, its
@@ -427,15 +427,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             if (begun) o_factor = unit * pow2_inverse(now);
             unit = now;
           }
-          const int key0 = kt * 128, hi = pos - key0;
-          if (key0 + 127 > warp_pos) {  // some row of the warp does not see all of the tile
+          const int key0 = kt * 128, hi = pos - key0;  // (the row's own position)
+          if (key0 + 127 > warp_pos || (a.window && key0 + a.window <= warp_last)) {
+            // some row of the warp does not see all of the tile: bits for what it sees
+            const int lo = a.window ? hi - a.window + 1 : 0;
 #pragma unroll
-            for (int i = 0; i < 128; ++i) s[i] = i > hi ? -INFINITY : s[i];
-          }
-          if (a.window && key0 + a.window <= warp_last) {
-            const int lo = hi - a.window;
+            for (int j = 0; j < 4; ++j) {
+              const int h = hi - 32 * j, l = lo - 32 * j;
+              const uint32_t upto = h >= 31 ? 0xFFFFFFFFu : h < 0 ? 0u : (2u << h) - 1u;
+              const uint32_t from = l <= 0 ? 0xFFFFFFFFu : l >= 32 ? 0u : 0xFFFFFFFFu << l;
+              const uint32_t sees = upto & from;
 #pragma unroll
-            for (int i = 0; i < 128; ++i) s[i] = i <= lo ? -INFINITY : s[i];
+              for (int i = 0; i < 32; ++i)
+                s[32 * j + i] = sees & (1u << i) ? s[32 * j + i] : -INFINITY;
+            }
           }
           const auto largest = [&]() {
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -449,8 +454,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           // the tiles before, which nearly always does: only where the tile's total
           // says that m is far too small is it found anew, and the tile done again.
           float total;
-          if (!begun) m = largest();
-          while (true) {
+          const auto form = [&]() {
             const float b = kPower - (m == -INFINITY ? 0.0f : m);
             const float2 f2 = make_float2(f_tile, f_tile), b2 = make_float2(b, b);
             float2 sum[4];
@@ -476,21 +480,44 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             }
             const float2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
             total = both.x + both.y;
-            const bool far = total > 0x1p15f || m == -INFINITY;
-            if (!__any_sync(0xFFFFFFFFu, far)) break;
-            float up = m;
-            if (far) {
-              const float mt = largest();
-              // (by a whole power of two, so that O's factor is exact)
-              if (m == -INFINITY) up = mt;
-              else if (mt > m) up = m + ceilf(mt - m);
-            }
-            // (nothing to change: rows that see none of the tile)
-            if (!__any_sync(0xFFFFFFFFu, up != m)) break;
+            return total > 0x1p15f || m == -INFINITY;
+          };
+          const auto higher = [&]() {
+            const float mt = largest();
+            // (by a whole power of two, so that O's factor is exact)
+            return m == -INFINITY ? mt : mt > m ? m + ceilf(mt - m) : m;
+          };
+          const auto raise = [&](float up) {
             if (up != m) {
               const float f = attn_exp2(m - up);
               l *= f, o_factor *= f;
               m = up;
+            }
+          };
+          // With 8-bit caches one place in the code finds the first maximum and later ones,
+          // since the kernel does not fit the instruction caches (4096 over 16384, 16 heads
+          // of 128, 485 us with two, 459 with one; with bf16 313 with two, 331 with one).
+          // Where no row's has changed there is no more to do: rows that see nothing.
+          if (kBytes) {
+            bool far = !begun, again = far;
+            for (bool first = true;; first = false) {
+              if (again) {
+                const float up = far ? higher() : m;
+                if (!first && !__any_sync(0xFFFFFFFFu, up != m)) break;
+                raise(up);
+              }
+              far = form();
+              again = __any_sync(0xFFFFFFFFu, far);
+              if (!again) break;
+            }
+          } else {
+            if (!begun) m = largest();
+            while (true) {
+              const bool far = form();
+              if (!__any_sync(0xFFFFFFFFu, far)) break;
+              const float up = far ? higher() : m;
+              if (!__any_sync(0xFFFFFFFFu, up != m)) break;
+              raise(up);
             }
           }
           if (begun && __any_sync(0xFFFFFFFFu, o_factor != 1.0f)) {
