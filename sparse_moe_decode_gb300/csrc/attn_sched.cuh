@@ -8,7 +8,7 @@
 // share's pieces are segments of one tile each.  A tile counts C key tiles more
 // than it has, for what beginning and ending it costs.  A tile that lies in one share
 // is finished there; otherwise its segments leave unnormalised sums (and the
-// softmax's maximum and total) for attn_combine.cu.  Every block finds its
+// softmax's maximum and total) for attn_combine_kernel.  Every block finds its
 // share by itself: a scan over the sequences, whose key tiles have a closed
 // form.
 #pragma once
@@ -116,7 +116,7 @@ struct AttnTiles {
   }
 };
 
-// What a block leaves for attn_combine.cu about the tile that it began and
+// What a block leaves for attn_combine_kernel about the tile that it began and
 // did not finish.
 struct AttnOpen {
   int32_t last;            // the block that finishes it; -1: there is none
