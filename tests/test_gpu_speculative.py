@@ -102,6 +102,30 @@ def test_graphs_share_a_workspace(env):
         assert torch.equal(outs[i], want[i])
 
 
+def test_two_streams_at_once(env):
+    """Objects of their own on streams of their own, their calls overlapping."""
+    import torch
+    moe, dev = env
+    batches = [Batch(env, [300, 2, 90], [700, 44, 90], (8, 2), 128, 64, "int8").fill(),
+               Batch(env, [1000], [3000], (8, 2), 256, 16, "bf16", seed=1).fill(),
+               Batch(env, [1] * 5, [40, 3000, 1, 700, 64], (8, 2), 64, 64, "e4m3").fill()]
+    p = torch.softmax(torch.randn((40, 3, 20000), device=dev) * 3, -1)
+    drafted, u = p[:, :2].argmax(-1).int(), torch.rand((40, 3), device=dev)
+    verifier = moe.DraftVerifier(dev)
+    calls = [b.attend for b in batches] + [lambda **kw: verifier.verify(p, drafted, u, **kw)[0]]
+    want = [f().clone() for f in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[] for _ in calls]
+    for _ in range(10):
+        for f, s, r in zip(calls, streams, got):
+            r.append(f(stream=s))
+    torch.cuda.synchronize()
+    for w, r in zip(want, got):
+        assert all(torch.equal(x, w) for x in r)
+    assert not any(b.attn.status() for b in batches) and verifier.status() == 0
+
+
 @pytest.mark.parametrize("new", [1, 40])
 def test_sequences_share_pages(env, new):
     """A prefix in pages that several sequences name."""
