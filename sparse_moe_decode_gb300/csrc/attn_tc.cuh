@@ -487,8 +487,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             // (by a whole power of two, so that O's factor is exact)
             return m == -INFINITY ? mt : mt > m ? m + ceilf(mt - m) : m;
           };
+          // (A comparison that NaN fails: a row whose maximum is NaN raises nothing, and the
+          // searches below end however many rows of the warp see nothing.)
           const auto raise = [&](float up) {
-            if (up != m) {
+            if (up > m) {
               const float f = attn_exp2(m - up);
               l *= f, o_factor *= f;
               m = up;
@@ -503,7 +505,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             for (bool first = true;; first = false) {
               if (again) {
                 const float up = far ? higher() : m;
-                if (!first && !__any_sync(0xFFFFFFFFu, up != m)) break;
+                if (!first && !__any_sync(0xFFFFFFFFu, up > m)) break;
                 raise(up);
               }
               far = form();
@@ -516,7 +518,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
               const bool far = form();
               if (!__any_sync(0xFFFFFFFFu, far)) break;
               const float up = far ? higher() : m;
-              if (!__any_sync(0xFFFFFFFFu, up != m)) break;
+              if (!__any_sync(0xFFFFFFFFu, up > m)) break;
               raise(up);
             }
           }
