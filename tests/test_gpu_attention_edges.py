@@ -4,7 +4,7 @@ left behind.  The definition and its bounds stand in attn_ref."""
 import numpy as np
 import pytest
 
-from attn_ref import attention
+from attn_ref import BF16, FP16, attention
 from test_gpu_attention import Batch
 from util import gpu_env
 
@@ -44,3 +44,62 @@ def test_zero_queries_beside_others_under_a_window(env, kv, d, heads):
     torch.cuda.synchronize()
     assert b.attn.status() == 0
     check_heads(b, out, slice(1, None))
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads", [(4, 2), (6, 2)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_scores_of_zero(env, kv, d, heads, window):
+    """Zero or tiny queries and keys: the mean of the values that a row sees."""
+    for q_size, k_size in ((0, 0), (2.0 ** -13, 0), (1, 0), (0, 2.0 ** -10), (0, 1),
+                           (2.0 ** -60, 2.0 ** -60), (0, 2.0 ** -120)):
+        b = Batch(env, [150, 2, 40], [333, 50, 40], heads, d, 16, kv, window, k_std=k_size).fill()
+        b.q *= q_size
+        b.check(b.attend())
+        assert b.attn.status() == 0
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [[2, 1], [100, 300]])
+def test_key_tiles_of_zeros(env, kv, d, new):
+    """A key tile of zero keys among others, under queries of different sizes."""
+    b = Batch(env, new, [700, 500], (4, 2), d, 64, kv)
+    b.k[256:384] = 0
+    b.k[700 + 384:] = 0
+    b.q[::3] *= 2.0 ** -14
+    b.q[1::3, 0] = 0
+    b.fill()
+    b.check(b.attend())
+
+
+@pytest.mark.parametrize("kv", ["int8", "e4m3"])
+@pytest.mark.parametrize("new", [[1, 1], [30, 100]])
+def test_pages_never_written(env, kv, new):
+    """Scales of 0, as a new cache has them: keys and values of 0."""
+    b = Batch(env, new, [200, 130], (4, 2), 128, 64, kv)
+    b.cache = b.attn.new_cache(b.cache.k.shape[0])
+    assert (b.attend() == 0).all()
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("power", [40, 80, 100])
+def test_huge_queries_beside_huge_hidden_keys(env, kv, power):
+    """The product of a row's and a key tile's powers of two is beyond fp32: rows that do not
+    see the huge key, with scores of 0, give the mean of their values."""
+    b = Batch(env, [140], [260], (4, 2), 128, 64, kv)
+    b.q *= 2.0 ** power
+    b.k[250] *= 2.0 ** power
+    b.k[:250, :, 1:] = 0  # scores of one product each
+    b.q[:130, :, 0] = 0   # ... of 0
+    b.fill()
+    out = b.attend()[:130].double().cpu().numpy()
+    assert b.attn.status() == 0
+    v = b.values()[0][1]
+    for i in range(130):
+        seen = v[:121 + i].repeat(2, 1)  # each query head's
+        want, size = seen.mean(0), np.abs(seen).mean(0)
+        # attn_ref's bound of a weight and a value, without its term for scores
+        bound = BF16 * np.abs(want) + (3 * FP16 + 2.0 ** -18) * size + 2.0 ** -21
+        assert (np.abs(out[i] - want) <= bound).all(), i
