@@ -41,7 +41,8 @@ __device__ __forceinline__ void combine(const AttnBatch &a, const AttnArgs &p, i
 #pragma unroll
     for (int q = 0; q < Q; ++q) v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const auto add = [&](float2 ml, const float4 (&x)[Q]) {
-      if (ml.x == -INFINITY) return;  // a part that saw no key has no sums
+      // a part that saw no key has no sums (one that saw keys of NaN alone has NaN of them)
+      if (ml.x == -INFINITY && ml.y == 0.0f) return;
       const float top = fmaxf(m, ml.x);
       const float f = attn_exp2(m - top), g = attn_exp2(ml.x - top);
       m = top;

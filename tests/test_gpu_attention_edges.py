@@ -103,3 +103,20 @@ def test_huge_queries_beside_huge_hidden_keys(env, kv, power):
         # attn_ref's bound of a weight and a value, without its term for scores
         bound = BF16 * np.abs(want) + (3 * FP16 + 2.0 ** -18) * size + 2.0 ** -21
         assert (np.abs(out[i] - want) <= bound).all(), i
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("heads,d", [((4, 2), 128), ((8, 1), 64), ((4, 2), 256)])
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_a_key_that_is_nan_alone_in_its_tile(env, kv, heads, d, new):
+    """A row that sees of one block's keys only a NaN one is NaN, whatever the others hold."""
+    import torch
+    for at in (64, 128, 512, 1024):  # the first position of a key tile
+        b = Batch(env, [new, new], [at + new, at + 30], heads, d, 64, kv)
+        b.k[at, 0, 3] = float("nan")
+        b.fill()
+        out = b.attend()
+        group = heads[0] // heads[1]
+        assert torch.isnan(out[:new, :group].float()).all()
+        assert torch.isfinite(out[:new, group:].float()).all()
+        b.check(out, skip=(0,))
