@@ -77,7 +77,7 @@ typedef enum {
 } moe_status;
 
 /* Device status bits, OR-ed into the status word at workspace + 0. */
-#define MOE_DEV_NONFINITE 0x1u  /* a token's logits held NaN/inf (A2)       */
+#define MOE_DEV_NONFINITE 0x1u  /* logits, probabilities or scores out of range (A2) */
 #define MOE_DEV_BAD_EXPERT 0x2u /* an expert id >= num_experts was given    */
 #define MOE_DEV_TIMEOUT 0x4u    /* a bounded device-side wait gave up       */
 #define MOE_DEV_BAD_INDEX 0x8u  /* a sequence bound, state slot, page or token out of range */
@@ -489,6 +489,10 @@ size_t moe_attn_workspace_bytes(const moe_attn_dims *dims);
  * code * scale enter as fp16, 11 bits each (of the values: down to 2^-20 of the
  * largest scale of the sequence's keys of that head; of the weights: to 2^-21 of
  * the largest).
+ * Scores count in fp32, times log2(e): in a sequence of more than 16 rows a row
+ * whose largest one is above 2^26 or below -2^26 sets MOE_DEV_NONFINITE and may
+ * be of no use, since the weights may leave their range; no score may leave
+ * fp32's.
  * What lies in the cache behind a sequence's last position is not looked at.
  * A value that is not finite in k, or in an 8-bit cache's rows, reaches the
  * rows that see its position; one in a bf16 cache's v may also reach rows of

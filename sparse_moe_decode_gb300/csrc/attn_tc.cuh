@@ -566,6 +566,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         d.rows = rows, d.start = w.start, d.row0 = w.row0, d.head = w.head;
         p.parts.open[blockIdx.x] = d;
       }
+      // Beside scores of this size m's rounding is an exponent of its own: 2^(s f - m) of the
+      // largest may leave fp16 or bf16.  (s f rounded by itself, as m is, took 3 to 9 %
+      // more with bf16, and as long with 8-bit caches only where all rows do so.)
+      if (live && fabsf(m) > 0x1p26f && m != -INFINITY) set_status(a.status, MOE_DEV_NONFINITE);
       const int64_t at = static_cast<int64_t>(part) * p.parts.rows + r;
       if (!whole && live) p.parts.ml[at] = make_float2(m - kPower, l);
       if (begun) {

@@ -30,6 +30,16 @@ def check_heads(b, out, heads):
         start += n
 
 
+def near_mean(got, values, kv):
+    """Whether `got` is the mean over the values' first axis, as near as weights and values that
+    enter rounded allow: attn_ref's bound without its term for scores (with a bf16 cache one
+    rounding of a weight to bf16, with the others a weight's and a value's two to fp16)."""
+    want, size = values.mean(0), np.abs(values).mean(0)
+    entering = BF16 if kv == "bf16" else 3 * FP16
+    bound = BF16 * np.abs(want) + (entering + 2.0 ** -18) * size + 2.0 ** -21
+    return bool((np.abs(got - want) <= bound).all())  # (NaN is not)
+
+
 @pytest.mark.parametrize("kv", KV)
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("heads", [(4, 2), (6, 2)])
@@ -95,14 +105,10 @@ def test_huge_queries_beside_huge_hidden_keys(env, kv, power):
     b.q[:130, :, 0] = 0   # ... of 0
     b.fill()
     out = b.attend()[:130].double().cpu().numpy()
-    assert b.attn.status() == 0
     v = b.values()[0][1]
     for i in range(130):
         seen = v[:121 + i].repeat(2, 1)  # each query head's
-        want, size = seen.mean(0), np.abs(seen).mean(0)
-        # attn_ref's bound of a weight and a value, without its term for scores
-        bound = BF16 * np.abs(want) + (3 * FP16 + 2.0 ** -18) * size + 2.0 ** -21
-        assert (np.abs(out[i] - want) <= bound).all(), i
+        assert near_mean(out[i], seen, kv), i
 
 
 @pytest.mark.parametrize("kv", KV)
@@ -120,3 +126,30 @@ def test_a_key_that_is_nan_alone_in_its_tile(env, kv, heads, d, new):
         assert torch.isnan(out[:new, :group].float()).all()
         assert torch.isfinite(out[:new, group:].float()).all()
         b.check(out, skip=(0,))
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [3, 150])
+def test_scores_beyond_the_digits_of_fp32(env, kv, d, new):
+    """Scores of 2^20 to 2^100, some 2^-8 of themselves apart: the largest one's value, up to
+    2^26 in sequences of many rows; those say so from there on."""
+    moe, _ = env
+    for power in (20, 23, 34, 60, 100):
+        for sign in (1, -1):
+            b = Batch(env, [new], [400], (4, 2), d, 64, kv, scale=1.0)
+            b.q[:, :, 1:] = 0
+            b.q[:, :, 0] = sign * 2.0 ** power
+            b.k[:, :, 1:] = 0
+            b.fill()
+            out = b.attend().double().cpu().numpy()
+            if new > 8 and power > 26:
+                assert b.attn.status() == moe.DEV_NONFINITE
+                continue
+            assert b.attn.status() == 0
+            k, v = b.values()[0][:2]
+            for i in range(new):
+                for h in range(4):
+                    s = k[:401 - new + i, h // 2, 0] * sign
+                    vv = v[:401 - new + i, h // 2][s == s.max()]
+                    assert near_mean(out[i, h], vv, kv), (power, sign, i, h)
