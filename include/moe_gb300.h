@@ -422,7 +422,7 @@ typedef struct {
   int32_t kv_type;   /* MOE_KV_*                                             */
   int32_t window;    /* 0: a token sees all positions up to its own; W > 0: the
                         last W of them                                       */
-  float scale;       /* of the products of q and k; finite                   */
+  float scale;       /* of the products of q and k; finite, times log2(e) too */
 } moe_attn_dims;
 
 typedef struct {

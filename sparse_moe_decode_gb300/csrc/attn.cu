@@ -203,7 +203,7 @@ cudaError_t launch_attention(const moe_attn_dims &d, const moe_kv_cache &c, cons
   x.args.parts.ml = reinterpret_cast<float2 *>(base + l.ml);
   x.args.parts.sums = reinterpret_cast<float *>(base + l.sums);
   x.args.parts.rows = 0;
-  x.args.scale_log2 = d.scale * 1.44269504088896340736f;
+  x.args.scale_log2 = attn_scale_log2(d);
   x.args.budget = tc_wait_budget_ns();
   const auto stream = d.kv_type == MOE_KV_BF16   ? launch_stream_bf16
                       : d.kv_type == MOE_KV_INT8 ? launch_stream_int8

@@ -16,6 +16,9 @@ constexpr int kStreamMaxCtas = 480;
 constexpr int kStreamRows = 16;  // rows (token, head of a group) of a tile
 constexpr int kTcMaxCtas = 160;     // one an SM; 256 rows, 128 with a head_dim of 256
 
+// What the kernels multiply the products of q and k by: weights are powers of two.
+inline float attn_scale_log2(const moe_attn_dims &d) { return d.scale * 1.44269504088896340736f; }
+
 // A batch as the kernels take it.
 struct AttnBatch {
   const int32_t *cu;    // [B + 1] or nullptr: T rows each

@@ -25,7 +25,7 @@ moe_status check_dims(const moe_attn_dims *d) {
   if (d->page_size < 16 || d->page_size > 256 || (d->page_size & (d->page_size - 1)))
     return MOE_ERR_UNSUPPORTED;
   if (d->kv_type < MOE_KV_BF16 || d->kv_type > MOE_KV_E4M3) return MOE_ERR_UNSUPPORTED;
-  if (d->window < 0 || !isfinite(d->scale)) return MOE_ERR_INVALID_ARG;
+  if (d->window < 0 || !isfinite(attn_scale_log2(*d))) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
