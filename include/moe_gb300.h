@@ -494,6 +494,8 @@ size_t moe_attn_workspace_bytes(const moe_attn_dims *dims);
  * be of no use, since the weights may leave their range; no score may leave
  * fp32's.
  * What lies in the cache behind a sequence's last position is not looked at.
+ * Under a window neither are the table's entries, nor their pages, that lie wholly
+ * before the first position that the sequence's first row sees.
  * A value that is not finite in k, or in an 8-bit cache's rows, reaches the
  * rows that see its position; one in a bf16 cache's v may also reach rows of
  * its sequence that do not see it but see or share a key tile of 128

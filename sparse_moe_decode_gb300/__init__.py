@@ -602,7 +602,8 @@ class PagedAttention:
     ``kv_type`` is "bf16", or "int8" or "e4m3" with a scale for each token and
     head, quantised as it is written (see ``moe_gb300.h``, which also says how
     far each product is rounded).  ``window`` W > 0 lets a token see only the last W
-    positions up to its own.  One object serves all layers of its shape; its
+    positions up to its own; ``attend`` does not look at pages (or at their entries) that
+    lie wholly before what a sequence's first row sees.  One object serves all layers of its shape; its
     workspace belongs to one stream at a time.
     With ``stream`` given, results are made in that stream's memory.  For
     inference: results carry no gradient, whether an input requires one or not.

@@ -130,6 +130,15 @@ __device__ __forceinline__ int attn_token(const AttnBatch &a, int row) {
   return static_cast<int>((static_cast<uint64_t>(row) * a.group_inverse) >> 32);
 }
 
+// The first position whose page the tile with first row `row0` reads: pages that lie
+// wholly before its first row's window may have been given back.  In their place come
+// zeros: page number a.pages is behind the cache's last row, where a tiled copy fills.
+__device__ __forceinline__ int attn_first_read(const AttnBatch &a, int ctx, int row0) {
+  if (!a.window) return 0;
+  const int first = ctx + attn_token(a, row0) - a.window + 1;
+  return first <= 0 ? 0 : first >> a.page_shift << a.page_shift;
+}
+
 struct AttnShare {  // in shared memory
   int64_t at, per, total, offset;  // first unit, a share's, all, within the sequence
   int64_t scan[32];

@@ -154,13 +154,16 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int32_t *table = a.table + w.b * a.table_ld;
       const int tiles = w.k1 - w.k0;
       const int boxes = (w.s.len + box - 1) / box;  // that the sequence has
+      const int first_read = attn_first_read(a, w.t.ctx, w.cur * R);
       int page_of = 0;                              // lane i's box of the 32 fetched next
       for (int i = 0; i < tiles && !stop; ++i) {
         const int b0 = (w.k0 + i) * per_tile;
         if ((i * per_tile) % 32 == 0) {
           const int bx = b0 + lane;
           page_of = 0;
-          if (bx < boxes && bx < w.k1 * per_tile) {
+          if (bx * box < first_read) {
+            page_of = a.pages;
+          } else if (bx < boxes && bx < w.k1 * per_tile) {
             page_of = table[(static_cast<int64_t>(bx) * box) >> a.page_shift];
             if (page_of < 0 || page_of >= a.pages) {
               set_status(a.status, MOE_DEV_BAD_INDEX);
@@ -193,7 +196,8 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
                              &sh->full[slot], pol);
             if (kBytes)
               bulk_load(ptx::smem_u32(scales + slot * 64 + lane * box),
-                        (kv ? p.v_scale : p.k_scale) + row, box * 4, &sh->full[slot]);
+                        (kv ? p.v_scale : p.k_scale) + (id < a.pages ? row : 0), box * 4,
+                        &sh->full[slot]);
           }
         }
       }

@@ -621,12 +621,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       uint64_t *full = kBytes ? sh->raw_full : sh->full, *empty = kBytes ? sh->raw_empty : sh->empty;
       for (TcSegment w = next_segment(); w.there && ok; w = next_segment()) {
         const int32_t *table = a.table + w.b * a.table_ld;
-        const int len = w.len;
+        const int len = w.len, first_read = attn_first_read(a, w.ctx, w.row0);
         // lane i: the page of position kt * 128 + i * page
         const auto pages_of = [&](int kt) {
           const int64_t pos = static_cast<int64_t>(kt) * 128 + static_cast<int64_t>(lane) * page;
           int id = 0;
-          if (kt < w.k1 && lane * k_box < 128 && pos < len) {
+          if (pos < first_read) {
+            id = a.pages;
+          } else if (kt < w.k1 && lane * k_box < 128 && pos < len) {
             id = table[pos >> a.page_shift];
             if (id < 0 || id >= a.pages) {
               set_status(a.status, MOE_DEV_BAD_INDEX);
@@ -729,8 +731,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
               __syncwarp();
               if (lane < have) {
                 const uint32_t dst = ptx::smem_u32(scales + slot * 256 + lane * k_box);
-                bulk_load(dst, p.k_scale + rows, k_box * 4, &sh->scale_raw[slot]);
-                bulk_load(dst + 512, p.v_scale + rows, k_box * 4, &sh->scale_raw[slot]);
+                // (scales before first_read are not looked at)
+                const int from = kt * 128 + (lane << k_shift) < first_read ? 0 : rows;
+                bulk_load(dst, p.k_scale + from, k_box * 4, &sh->scale_raw[slot]);
+                bulk_load(dst + 512, p.v_scale + from, k_box * 4, &sh->scale_raw[slot]);
               }
               ++tiles;
             }
@@ -905,6 +909,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         bool more = plan();
         while (more) {
           const int k0 = w.k0, k1 = w.k1, len = w.s.len;
+          const int first_read = attn_first_read(a, w.t.ctx, w.cur * R);
           more = plan();  // (one ahead)
           float v_top = 0.0f;
           for (int kt = k0; kt < k1 && ok; ++kt, ++tiles) {
@@ -916,7 +921,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             float k[4] = {kx.x, kx.y, kx.z, kx.w}, v[4] = {vx.x, vx.y, vx.z, vx.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if (kt * 128 + 4 * lane + i >= len) k[i] = v[i] = 0.0f;
+              const int key = kt * 128 + 4 * lane + i;
+              if (key >= len || key < first_read) k[i] = v[i] = 0.0f;
               if (!(fabsf(v[i]) < INFINITY)) k[i] = v[i] - v[i], v[i] = 0.0f;
             }
             const float k_up = power(largest(k));

@@ -153,3 +153,64 @@ def test_scores_beyond_the_digits_of_fp32(env, kv, d, new):
                     s = k[:401 - new + i, h // 2, 0] * sign
                     vv = v[:401 - new + i, h // 2][s == s.max()]
                     assert near_mean(out[i, h], vv, kv), (power, sign, i, h)
+
+
+def give_back(b, keep):
+    """The pages that lie wholly before position `keep[i]` of sequence i are no longer in its
+    table; they and page 0, which no sequence has, hold what is not finite.  Returns the table
+    as it was."""
+    import torch
+    whole = b.table.clone()
+    for x in b.cache:  # page 0's rows to a page that nobody has
+        if x is not None:
+            used = set(whole.flatten().tolist())
+            spare = max(set(range(x.shape[0])) - used)
+            x.view(torch.uint8)[spare] = x.view(torch.uint8)[0]
+    b.table[b.table == 0] = spare
+    whole[whole == 0] = spare
+    for i, first in enumerate(keep):
+        gone = max(0, first) // b.page
+        b.poison([0] + b.table[i, :gone].tolist())
+        b.table[i, :gone] = -1 if i % 2 else 1 << 30
+    return whole
+
+
+def finite(b):
+    """What was poisoned made finite, for the definition, which multiplies it by 0."""
+    for x, least in zip(b.cache, (0.0, 0.0, 2.0 ** -126, 2.0 ** -126)):
+        if x is not None and x.is_floating_point():
+            x.copy_(x.float().nan_to_num(least).to(x.dtype))
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page,window", [(16, 100), (32, 33), (64, 200), (16, 1), (128, 500),
+                                         (256, 260)])
+@pytest.mark.parametrize("new,heads", [([1, 2, 1], (4, 2)), ([1, 40, 150], (6, 2))])
+def test_pages_before_the_window_are_not_read(env, kv, d, page, window, new, heads):
+    """A layer with a window that gives its old pages back."""
+    b = Batch(env, new, [700, 333, 1111], heads, d, page, kv, window).fill()
+    table = give_back(b, [x - n - window + 1 for x, n in zip(b.length, new)])
+    out = b.attend()
+    assert b.attn.status() == 0
+    b.table = table
+    finite(b)
+    b.check(out)
+
+
+@pytest.mark.parametrize("kv", KV)
+def test_prompts_whose_first_pages_are_gone(env, kv):
+    """A chunk of a long prompt behind a window, page 0 of another's rows that are not finite;
+    a page inside the window that is missing is still told."""
+    moe, _ = env
+    b = Batch(env, [600], [5000], (8, 2), 128, 16, kv, window=777).fill()
+    table = give_back(b, [5000 - 600 - 776])
+    out = b.attend()
+    assert b.attn.status() == 0
+    gone, b.table = b.table, table
+    finite(b)
+    b.check(out)
+    gone[0, (5000 - 600 - 776) // 16] = -1
+    b.table = gone
+    b.attend()
+    assert b.attn.status() == moe.DEV_BAD_INDEX
