@@ -576,8 +576,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         ok = ptx::mbar_wait(&sh->o_last[qi], segs++ & 1, abort, p.budget);
         if (!ok) break;
         ptx::tc_fence_after();
-        float f = whole ? 1.0f / l : 1.0f;
-        if (kBytes) f *= unit;
+        const float inv_l = whole ? 1.0f / l : 1.0f, f = kBytes ? 1.0f : inv_l;
         moe_bf16 *dst = p.out + (w.start + token) * p.out_ld + head * D;
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {
@@ -585,6 +584,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           ptx::tmem_ld32(o_at + i, o);
           ptx::tmem_wait_ld();
           if (!live) continue;
+          if (kBytes) {  // (the product of both factors may be below fp32's normal numbers)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = o[j] * inv_l * unit;
+          }
           if (whole) {
 #pragma unroll
             for (int j = 0; j < 32; j += 8)

@@ -214,3 +214,15 @@ def test_prompts_whose_first_pages_are_gone(env, kv):
     b.table = gone
     b.attend()
     assert b.attn.status() == moe.DEV_BAD_INDEX
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("new", [2, 20])
+def test_values_next_to_the_smallest(env, kv, new):
+    """Values of 2^-116 and many equal weights, tiles that one block begins and ends: outputs
+    keep their digits (the definition's bound has 1e-37 for what fp32 cannot hold)."""
+    b = Batch(env, [new] * 40, [4000] * 40, (8, 8), 64, 256, kv, uniform=True)
+    b.q[:] = 0
+    b.v.copy_(2.0 ** -116 * (1 + 0.5 * b.v.float().abs()))
+    b.fill()
+    b.check(b.attend())
