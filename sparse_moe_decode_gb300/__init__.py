@@ -612,7 +612,10 @@ class PagedAttention:
     def __init__(self, q_heads, kv_heads, head_dim, page_size=64, kv_type="bf16", window=0,
                  scale=None, device="cuda"):
         import torch
-        if kv_type not in KV_TYPES:
+        # (ctypes keeps the lower 32 bits of a larger number)
+        if kv_type not in KV_TYPES or head_dim < 1 or any(
+                not -2 ** 31 <= x < 2 ** 31
+                for x in (q_heads, kv_heads, head_dim, page_size, window)):
             _refuse(MOE_ERR_INVALID_ARG, "PagedAttention")
         self.kv_type = kv_type
         self.dims = AttnDims(q_heads, kv_heads, head_dim, page_size, KV_TYPES[kv_type], window,
