@@ -517,14 +517,15 @@ moe_status moe_paged_attention(const moe_attn_dims *dims, const moe_kv_cache *ca
  * max(p - q, 0) at a rejected token's place, and of p where the draft ended
  * or where p never exceeds q.  Products and differences are exact, sums kept
  * to 48 bits or more.  Without draft probabilities (draft NULL) q_i is 1 at
- * d_i and 0 elsewhere.  Rows of p and q need not sum to 1.
+ * d_i and 0 elsewhere.  Rows of p and q need not sum to 1, but the sum has to be
+ * finite in fp32 (one below 2^-100 keeps fewer bits).
  * target row (b, i) at target + b * target_seq_ld + i * target_ld, draft
  * alike; [V] fp32, 4-byte aligned.  draft_tokens [B][T], uniform [B][T + 1],
  * tokens [B][T + 1], accepted [B], all whole.  T <= 1024, V <= 2^24.
  * A drafted token >= V sets MOE_DEV_BAD_INDEX; a value that is negative or
- * not finite in the rows that the last token is taken from, or one of them
- * without a positive value, sets MOE_DEV_NONFINITE; either leaves tokens -1
- * and accepted 0.  The workspace holds only the status word. */
+ * not finite in the rows that the last token is taken from, one of them
+ * without a positive value, or a sum beyond fp32, sets MOE_DEV_NONFINITE; either
+ * leaves tokens -1 and accepted 0.  The workspace holds only the status word. */
 moe_status moe_verify_draft(int B, int T, int V, const float *target, int64_t target_seq_ld,
                             int64_t target_ld, const float *draft, int64_t draft_seq_ld,
                             int64_t draft_ld, const int32_t *draft_tokens, const float *uniform,
