@@ -775,8 +775,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       // 128 rows of 64 codes, 16 of a row at a time, become rows of 64 fp16 code *
       // scale, rounded once: a key's scale is two fp16 terms (22 bits, since it moves
       // all of a score), a value's one (it moves a weight by as much as the weight's
-      // own rounding).  Values whose key is `dead` or later become 0.  (A warp for
-      // each unit, or two units at a time, took longer: the ring is short.)
+      // own rounding; two terms there too: 942 us for 902).  Values whose key is `dead`
+      // or later become 0.  (A warp for each unit, or two units at a time, took longer:
+      // the ring is short.)
       const int t = threadIdx.x - 32 * S::kSoftWarps;
       const int v_shift = 31 - __clz(v_box);
       constexpr int kEach = 512 / (32 * kConvWarps);
@@ -924,8 +925,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             float k[4] = {kx.x, kx.y, kx.z, kx.w}, v[4] = {vx.x, vx.y, vx.z, vx.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int key = kt * 128 + 4 * lane + i;
-              if (key >= len || key < first_read) k[i] = v[i] = 0.0f;
+              if (kt * 128 + 4 * lane + i >= len || kt * 128 + 4 * lane < first_read)
+                k[i] = v[i] = 0.0f;  // (pages begin at multiples of 16)
               if (!(fabsf(v[i]) < INFINITY)) k[i] = v[i] - v[i], v[i] = 0.0f;
             }
             const float k_up = power(largest(k));
