@@ -175,7 +175,8 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
         for (int kv = 0; kv < 2 && !stop; ++kv, ++n) {
           const uint32_t slot = n % kSlots;
-          if (!ptx::mbar_wait(&sh->empty[slot], ((n / kSlots) & 1) ^ 1, abort, p.budget)) {
+          const bool free = ptx::mbar_wait(&sh->empty[slot], ((n / kSlots) & 1) ^ 1, abort, p.budget);
+          if (!__all_sync(0xFFFFFFFFu, free)) {  // (lanes issue and account for copies together)
             stop = true;
             break;
           }
@@ -202,16 +203,15 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
       }
     }
-    if (*abort) {  // let the copies in flight land before exiting
-      if (lane == 0) {
-        set_status(a.status, MOE_DEV_TIMEOUT);
-        int never = 0;
-        for (uint32_t k = 0; k < kSlots && k < n; ++k) {
-          const uint32_t j = n - 1 - k;
-          ptx::mbar_wait(&sh->full[j % kSlots], (j / kSlots) & 1, &never, ptx::kDrainBudgetNs);
-        }
+    // The block does not end before its copies have landed, whoever gives up waiting for
+    // them, and when.
+    if (lane == 0) {
+      int never = 0;
+      for (uint32_t k = 0; k < kSlots && k < n; ++k) {
+        const uint32_t j = n - 1 - k;
+        ptx::mbar_wait(&sh->full[j % kSlots], (j / kSlots) & 1, &never, ptx::kDrainBudgetNs);
       }
-      __syncwarp();
+      if (*abort) set_status(a.status, MOE_DEV_TIMEOUT);
     }
     return;
   }
