@@ -212,7 +212,7 @@ gateup_split_kernel(const __grid_constant__ XMaps maps, const XParams p) {
           ++nb;
         }
       }
-      if (*abort) {  // let the copies in flight land before exiting
+      {  // the copies in flight land before the block ends, whoever gives up and when
         int never = 0;
         for (uint32_t k = 0; k < kXQS && k < nq; ++k) {
           const uint32_t j = nq - 1 - k;
@@ -530,7 +530,7 @@ down_split_kernel(const __grid_constant__ XMaps maps, const XParams p) {
           ++nb;
         }
       }
-      if (*abort) {  // let the copies in flight land before exiting
+      {  // the copies in flight land before the block ends, whoever gives up and when
         int never = 0;
         for (uint32_t k = 0; k < kXQS && k < nq; ++k) {
           const uint32_t j = nq - 1 - k;

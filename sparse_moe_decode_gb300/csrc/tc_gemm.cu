@@ -103,7 +103,7 @@ router_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
           ptx::tma_load_2d(dst + kRABytes, &tmX, k * 64, t0, &bars->full[s], pol);
         }
       }
-      if (*abort) {  // let the copies in flight land before exiting
+      {  // the copies in flight land before the block ends, whoever gives up and when
         int never = 0;
         for (uint32_t k = 0; k < kRStages && k < n; ++k) {
           const uint32_t j = n - 1 - k;
