@@ -102,8 +102,8 @@ def build_binding(force: bool = False):
     where something that it needs is missing."""
     lacks = binding_lacks()
     if lacks:
-        sys.stderr.write("sparse_moe_decode_gb300: no %s, so the tensor-level calls of the gated "
-                         "delta rule and the norms are not built\n" % lacks)
+        sys.stderr.write("sparse_moe_decode_gb300: no %s, so the tensor-level calls (delta rule, "
+                         "norms, attention and its cache, drafts) are not built\n" % lacks)
         return None
     deps = [BINDING_SRC, os.path.join(INCLUDE, "moe_gb300.h"), os.path.abspath(__file__)]
     target = binding_target()

@@ -94,9 +94,9 @@ __device__ __forceinline__ void combine(const AttnBatch &a, const AttnArgs &p, i
 #pragma unroll
       for (int q = 0; q < Q; q += 2)
         *reinterpret_cast<uint4 *>(dst + 4 * q) =
-            make_uint4(bf16x2(v[q].x * f, v[q].y * f), bf16x2(v[q].z * f, v[q].w * f),
-                       bf16x2(v[q + 1].x * f, v[q + 1].y * f),
-                       bf16x2(v[q + 1].z * f, v[q + 1].w * f));
+            make_uint4(pack_bf16(v[q].x * f, v[q].y * f), pack_bf16(v[q].z * f, v[q].w * f),
+                       pack_bf16(v[q + 1].x * f, v[q + 1].y * f),
+                       pack_bf16(v[q + 1].z * f, v[q + 1].w * f));
     }
     if (TOGETHER) __syncthreads();
   }

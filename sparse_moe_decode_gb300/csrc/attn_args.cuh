@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_sched.cuh"
+#include "pair.cuh"
 
 namespace moe {
 
@@ -38,12 +39,6 @@ __device__ __forceinline__ float attn_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // The power of two at or below x, in [2^-110, 2^126], and its inverse.

@@ -170,7 +170,7 @@ __device__ __forceinline__ void attn_share(const AttnBatch &a, const AttnRange &
                                            AttnShare *sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
   AttnSeq s;
-  const auto find = [&](int64_t at, int64_t total, int64_t per, int64_t each, int64_t incl, int b) {
+  const auto find = [&](int64_t at, int64_t each, int64_t incl, int b) {
     const int64_t first = incl - each * a.kv_heads;
     if (at >= first && at < incl) sh->seq = b, sh->offset = at - first, sh->each = each, sh->s = s;
   };
@@ -197,7 +197,7 @@ __device__ __forceinline__ void attn_share(const AttnBatch &a, const AttnRange &
       const int64_t total = __shfl_sync(0xFFFFFFFFu, incl, a.B - 1);
       const int64_t per = share_of(total), at = per * blockIdx.x;
       if (lane == 0) sh->at = at, sh->per = per, sh->total = total;
-      if (lane < a.B && at < total) find(at, total, per, each, incl, lane);
+      if (lane < a.B && at < total) find(at, each, incl, lane);
     }
     __syncthreads();
     return;
@@ -227,7 +227,7 @@ __device__ __forceinline__ void attn_share(const AttnBatch &a, const AttnRange &
   __syncthreads();
   if (at >= total) return;
   if (one) {
-    if (tid < a.B) find(at, total, per, mine, incl, tid);
+    if (tid < a.B) find(at, mine, incl, tid);
   } else {
     int64_t base = 0;
     for (int b0 = 0; b0 < a.B && base <= at; b0 += nt) {
@@ -235,7 +235,7 @@ __device__ __forceinline__ void attn_share(const AttnBatch &a, const AttnRange &
       const int64_t each = b < a.B ? attn_units<R, KT, C>(a, r, b, false, s) : 0;
       int64_t round;
       incl = base + scan(each * a.kv_heads, round);
-      if (b < a.B) find(at, total, per, each, incl, b);
+      if (b < a.B) find(at, each, incl, b);
       base += round;
     }
   }

@@ -405,8 +405,8 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
           f.z = h2_bits(__floats2half2_rn(e[1][0] * f0, e[1][1] * f0));
           f.w = h2_bits(__floats2half2_rn(e[1][2] * f1, e[1][3] * f1));
         } else {
-          f = make_uint4(bf16x2(e[0][0], e[0][1]), bf16x2(e[0][2], e[0][3]),
-                         bf16x2(e[1][0], e[1][1]), bf16x2(e[1][2], e[1][3]));
+          f = make_uint4(pack_bf16(e[0][0], e[0][1]), pack_bf16(e[0][2], e[0][3]),
+                         pack_bf16(e[1][0], e[1][1]), pack_bf16(e[1][2], e[1][3]));
         }
         weights[((kt & 1) * 4 + warp) * 32 + lane] = f;
       };
@@ -572,13 +572,13 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
           const float4 v = make_float4(o[2 * j][2 * i] * f, o[2 * j + 1][2 * i] * f,
                                        o[2 * j][2 * i + 1] * f, o[2 * j + 1][2 * i + 1] * f);
           if (whole)
-            *reinterpret_cast<uint2 *>(dst + d) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+            *reinterpret_cast<uint2 *>(dst + d) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
           else
             *reinterpret_cast<float4 *>(p.parts.at(part, D, d, r)) = v;
         } else {
           const int d = warp * kCols + 8 * j + 2 * c;
           const float x = o[j][2 * i] * f, y = o[j][2 * i + 1] * f;
-          if (whole) *reinterpret_cast<uint32_t *>(dst + d) = bf16x2(x, y);
+          if (whole) *reinterpret_cast<uint32_t *>(dst + d) = pack_bf16(x, y);
           else
             *reinterpret_cast<float2 *>(p.parts.at(part, D, d, r) + (d & 2)) = make_float2(x, y);
         }

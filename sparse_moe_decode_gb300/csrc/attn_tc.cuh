@@ -55,7 +55,6 @@
 #include "attn_args.cuh"
 #include "delta_mma.cuh"
 #include "early.cuh"
-#include "pair.cuh"
 #include "sm100_ptx.cuh"
 
 namespace moe {

@@ -19,6 +19,7 @@
 #include "attn_sched.cuh"
 #include "early.cuh"
 #include "kernels.h"
+#include "pair.cuh"
 
 namespace moe {
 
@@ -63,12 +64,6 @@ __device__ __forceinline__ int64_t kv_place(const AttnBatch &a, int t, int head,
   }
   return ((static_cast<int64_t>(page) * a.kv_heads + head) << a.page_shift) +
          (pos & ((1 << a.page_shift) - 1));
-}
-
-__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // The scale of a row whose largest magnitude is `top`, and its inverse.
@@ -224,7 +219,7 @@ kv_rows_kernel(const AttnBatch a, const KvSide k, const KvSide v) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          w[j] = bf16x2_of(x[2 * j] * scale[i], x[2 * j + 1] * scale[i]);
+          w[j] = pack_bf16(x[2 * j] * scale[i], x[2 * j + 1] * scale[i]);
         data[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
       const int t = first + i / 2 * kRows;
