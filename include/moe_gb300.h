@@ -488,7 +488,8 @@ size_t moe_attn_workspace_bytes(const moe_attn_dims *dims);
  * row's largest.  For sequences of more rows the weights and the cache's values
  * code * scale enter as fp16, 11 bits each (of the values: down to 2^-20 of the
  * largest scale of the sequence's keys of that head; of the weights: to 2^-21 of
- * the largest).
+ * the largest), so that a token's result differs by that between calls with few
+ * and with more rows of its sequence.
  * Scores count in fp32, times log2(e): in a sequence of more than 16 rows a row
  * whose largest one is above 2^26 or below -2^26 sets MOE_DEV_NONFINITE and may
  * be of no use, since the weights may leave their range; no score may leave

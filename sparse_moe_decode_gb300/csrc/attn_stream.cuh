@@ -24,8 +24,8 @@
 //
 // Measured: 128 sequences of 1 .. 16384 positions, 32 heads on 8 of 128, bf16
 // 640 us, 6.75 TB/s, the rate of a copy.  int8 halves the bytes and the time
-// is then that of the conversions and products (32 sequences of up to 8192: 66
-// us, 4.6 TB/s; issue slots 57 % used, ALU 46 %).  One sequence of 4099: 11.3 us,
+// is then that of the conversions and products (32 sequences of up to 8192: 67
+// us, 4.5 TB/s; issue slots 57 % used, ALU 46 %; e4m3 64.5 us).  One sequence of 4099: 11.3 us,
 // launches, page table, one round trip and the join.
 #pragma once
 

@@ -23,7 +23,7 @@
 // key tile, for the values one that only grows within a segment; O follows it.
 // Weights are then fp16 under 2^7.  Exact codes, with the scales on S's columns
 // and on the weights as the streaming kernel has them, cost the softmax's
-// threads more than the conversion: 1370 us for what takes 892 now.
+// threads more than the conversion: 1370 us for what takes 888 now.
 //
 // Warps: 4 NQ softmax; 4 (NQ = 2) or 8 that convert; one that fetches; NQ that
 // issue products, a query tile each and by turns, so that while one waits for
@@ -37,9 +37,9 @@
 // Measured, 4096 tokens over 16384, 16 heads on 4, pages of 64 (TFLOP/s of the
 // products below the diagonal; 1910 measured for a plain bf16 product):
 //   head_dim       64    128    256
-//   bf16          875   1540   1380
-//   int8          698   1045    780
-//   e4m3          670   1065    865
+//   bf16          895   1520   1355
+//   int8          695   1045    780
+//   e4m3          710   1085    855
 // 64: the exponentials, one for each 4 * 64 operations.  128: tensor cores,
 // less the turns' gaps.  256 (one query tile): each K and V is read by 128
 // rows, 128 KB a key tile from the L2.  8-bit: the conversion, its
@@ -74,7 +74,7 @@ struct TcShape {
   static constexpr int kFixed = kQ + kScales + 2048 + kNQ * 512;  // + barriers, row factors
   static constexpr int kRoom = 232448 - kFixed;
   // (With two query tiles room for converted units pays more than for raw ones: 16
-  // heads of 128, 4096 over 16384, 8 and 3 slots 543 us, 6 and 7 590; one tile: 5 % less)
+  // heads of 128, 4096 over 16384, 8 and 3 slots 461 us, 6 and 7 472; one tile: as long)
   static constexpr int kUnits = kBytes ? kRoom / (kUnit + kRaw) + (kNQ == 2 ? 2 : 0) : kRoom / kUnit;
   static constexpr int kRaws = kBytes ? (kRoom - kUnits * kUnit) / kRaw : 0;
   static constexpr int kSmem = kFixed + kUnits * kUnit + kRaws * kRaw;
@@ -502,7 +502,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           };
           // With 8-bit caches one place in the code finds the first maximum and later ones,
           // since the kernel does not fit the instruction caches (4096 over 16384, 16 heads
-          // of 128, 485 us with two, 459 with one; with bf16 313 with two, 331 with one).
+          // of 128, 485 us with two, 461 with one; with bf16 313 with two, 331 with one).
           // Where no row's has changed there is no more to do: rows that see nothing.
           if (kBytes) {
             bool far = !begun, again = far;
@@ -752,6 +752,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       // for them, and when.
       if (lane == 0) {
         int never = 0;
+#pragma unroll 1
         for (uint32_t k = 0; k < kSlots && k < n; ++k) {
           const uint32_t j = n - 1 - k;
           ptx::mbar_wait(&full[j % kSlots], (j / kSlots) & 1, &never, ptx::kDrainBudgetNs);
@@ -760,6 +761,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           if (q_tiles[i] > 0)
             ptx::mbar_wait(kBytes ? &sh->q_raw[i] : &sh->q_full[i], (q_tiles[i] - 1) & 1, &never,
                            ptx::kDrainBudgetNs);
+#pragma unroll 1
         for (uint32_t k = 0; k < S::kScaleSlots && k < tiles; ++k) {
           const uint32_t j = tiles - 1 - k;
           ptx::mbar_wait(&sh->scale_raw[j % S::kScaleSlots], (j / S::kScaleSlots) & 1, &never,
