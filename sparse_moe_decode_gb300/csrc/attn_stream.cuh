@@ -312,7 +312,8 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int key0 = kt * 64 + warp * 16;
       const uint32_t k_slot = n % kSlots, v_slot = (n + 1) % kSlots;
       // (after a wait that gave up, every wait does so at once: the warps go on
-      // meeting at their barriers to the end)
+      // meeting at their barriers to the end, but give no slot back, since copies into
+      // it may be on their way)
       ok = ptx::mbar_wait(&sh->full[k_slot], (n / kSlots) & 1, abort, p.budget) && ok;
       float s[2][4];
 #pragma unroll
@@ -370,7 +371,7 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
       }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh->empty[k_slot]);
+      if (lane == 0 && ok) ptx::mbar_arrive(&sh->empty[k_slot]);
       float2 vs[2];
       if (kBytes) {
         ok = ptx::mbar_wait(&sh->full[v_slot], ((n + 1) / kSlots) & 1, abort, p.budget) && ok;
@@ -530,7 +531,7 @@ attn_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
       }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh->empty[v_slot]);
+      if (lane == 0 && ok) ptx::mbar_arrive(&sh->empty[v_slot]);
     }
     if (!ok && lane == 0) set_status(a.status, MOE_DEV_TIMEOUT);
 
